@@ -133,8 +133,9 @@ shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             int it = 0;
             for (int p = 0; p < passes && !flags[0]; ++p) {
                 const int d0 = p * spp, dn = min(spp, D - d0);
-                const int rows = dn * GR, rows_pad = (rows + 15) / 16 * 16;
-                const uint32_t bytes = kShrXBytes + rows_pad * kShrBK * 2;
+                // With an odd number of 8-row blocks the MMA's N is 8 rows wider than the loaded
+                // rows; those accumulator columns belong to no token and are not read.
+                const uint32_t bytes = kShrXBytes + dn * GR * kShrBK * 2;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     const int s = it % kShrStages;
                     if (it >= kShrStages && !mbar_wait(&empty[s], ((it / kShrStages) & 1) ^ 1, flags)) break;
@@ -147,11 +148,6 @@ shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
                             tma_load_2d(st + kShrXBytes + (d * G + q) * R * 128, mA, &full[s], kb * kShrBK,
                                         dlist[d0 + d] * R);
                         }
-                    if (rows_pad > rows) {  // r_max = 8 and an odd row-block count: repeat the last block
-                        const int q = G - 1;
-                        const CUtensorMap* mA = q == 0 ? &tmA0 : q == 1 ? &tmA1 : q == 2 ? &tmA2 : &tmA3;
-                        tma_load_2d(st + kShrXBytes + rows * 128, mA, &full[s], kb * kShrBK, dlist[d0 + dn - 1] * R);
-                    }
                 }
             }
             if (flags[0]) {
