@@ -39,6 +39,8 @@ EXPORTED = (
     "lora_cache_slot_of", "lora_cache_stats", "lora_wait_selftest", "lora_set_kernel_stamps", "lora_set_aux_stamps",
     "lora_loader_create", "lora_loader_destroy", "lora_loader_mount", "lora_loader_acquire", "lora_loader_release",
     "lora_loader_stats",
+    "lora_fp4_bytes", "lora_fp4_quantize", "lora_fp4_dequantize", "lora_fp4_matmul",
+    "lora_fp4_linear_workspace_bytes", "lora_fp4_linear_fwd",
 )
 
 
@@ -51,6 +53,11 @@ class LoraError(RuntimeError):
 class lora_pool_desc(ctypes.Structure):
     _fields_ = [("h_in", ctypes.c_int32), ("h_out", ctypes.c_int32), ("r_max", ctypes.c_int32),
                 ("n_slots", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class lora_fp4_matrix(ctypes.Structure):
+    _fields_ = [("codes_dev", ctypes.c_void_p), ("scales_dev", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32)]
 
 
 class lora_segments(ctypes.Structure):
@@ -101,6 +108,12 @@ def _load() -> ctypes.CDLL:
         "lora_loader_acquire": [vp, i32, P(i32), vp],
         "lora_loader_release": [vp, i32, P(i32), vp],
         "lora_loader_stats": [vp, P(ctypes.c_uint64), P(ctypes.c_uint64)],
+        "lora_fp4_bytes": [i32, i32, P(sz), P(sz)],
+        "lora_fp4_quantize": [vp, i32, ctypes.c_int64, P(lora_fp4_matrix), vp],
+        "lora_fp4_dequantize": [P(lora_fp4_matrix), vp, i32, ctypes.c_int64, vp],
+        "lora_fp4_matmul": [P(lora_fp4_matrix), P(lora_fp4_matrix), vp, i32, ctypes.c_int64, vp],
+        "lora_fp4_linear_workspace_bytes": [vp, i32, P(sz)],
+        "lora_fp4_linear_fwd": [vp, P(lora_fp4_matrix), vp, P(lora_fp4_matrix), vp, P(lora_segments), vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -537,6 +550,86 @@ class LoraLoader:
             pass
 
 
+# ---- microscaled 4-bit base weights ----------------------------------------------------------
+
+def lora_fp4_bytes(rows: int, cols: int):
+    """(codes bytes, scales bytes) of a stored 4-bit matrix [rows, cols]."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib.lora_fp4_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+class Fp4Matrix:
+    """A stored microscaled 4-bit matrix [rows, cols] (layout in include/lora.h) in device buffers
+    this object owns: ``codes`` and ``scales``, uint8.  Its contents are what ``lora_fp4_quantize``
+    writes; before that they are undefined."""
+
+    def __init__(self, rows: int, cols: int, device="cuda"):
+        nc, ns = lora_fp4_bytes(rows, cols)
+        self.rows, self.cols = int(rows), int(cols)
+        self.codes = torch.empty(max(nc, 256), dtype=torch.uint8, device=device)
+        self.scales = torch.empty(max(ns, 256), dtype=torch.uint8, device=device)
+        self.struct = lora_fp4_matrix(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _fp4_rows(t: torch.Tensor, rows: int, cols: int, name: str):
+    """dtype code and row stride of a CUDA tensor [rows, cols] whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in TORCH_TO_LORA:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must have shape [{rows}, {cols}]")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return TORCH_TO_LORA[t.dtype], ld
+
+
+def lora_fp4_quantize(x: torch.Tensor, out: Fp4Matrix, stream=None) -> Fp4Matrix:
+    """Quantise x [rows, cols] (contiguous rows, any row stride) into out."""
+    dt, ld = _fp4_rows(x, out.rows, out.cols, "x")
+    _check(_lib.lora_fp4_quantize(_ptr(x), dt, ld, ctypes.byref(out.struct), _stream(stream)))
+    return out
+
+
+def lora_fp4_dequantize(q: Fp4Matrix, out: torch.Tensor, stream=None) -> torch.Tensor:
+    """Read q back into out [rows, cols] (contiguous rows, any row stride)."""
+    dt, ld = _fp4_rows(out, q.rows, q.cols, "out")
+    _check(_lib.lora_fp4_dequantize(ctypes.byref(q.struct), _ptr(out), dt, ld, _stream(stream)))
+    return out
+
+
+def lora_fp4_matmul(x: Fp4Matrix, w: Fp4Matrix, y: torch.Tensor, stream=None) -> torch.Tensor:
+    """y [x.rows, w.rows] = x w^T of two stored matrices (y: contiguous rows, any row stride)."""
+    dt, ld = _fp4_rows(y, x.rows, w.rows, "y")
+    _check(_lib.lora_fp4_matmul(ctypes.byref(x.struct), ctypes.byref(w.struct), _ptr(y), dt, ld, _stream(stream)))
+    return y
+
+
+def lora_fp4_linear_workspace_bytes(pool_handle, n_tokens: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_fp4_linear_workspace_bytes(pool_handle, n_tokens, ctypes.byref(out)))
+    return out.value
+
+
+def lora_fp4_linear_fwd(pool_handle, w: Fp4Matrix, x: torch.Tensor, y: torch.Tensor, seg: lora_segments,
+                        ws: torch.Tensor, xq: Optional[Fp4Matrix] = None, stream=None) -> torch.Tensor:
+    """lora_linear_fwd over a 4-bit base weight; xq: the stored form of x, where another projection
+    of the same x has made it already (it is made in the workspace otherwise)."""
+    _check(_lib.lora_fp4_linear_fwd(pool_handle, ctypes.byref(w.struct), _ptr(_dev(x, "x")),
+                                    None if xq is None else ctypes.byref(xq.struct), _ptr(_dev(y, "y")),
+                                    ctypes.byref(seg), _ptr(_dev(ws, "ws")), ws.numel() * ws.element_size(),
+                                    _stream(stream)))
+    return y
+
+
 def segment_arrays(seg: lora_segments) -> dict:
     """Views (int32 device tensors) of the segment outputs inside the workspace ``seg._ws``."""
     ws = seg._ws
@@ -605,6 +698,22 @@ class LoraPool:
                 self._ws[key] = self.linear_workspace(n, x.device)
             ws = self._ws[key]
         return lora_linear_fwd(self.handle, W, x, y, seg, ws, variant, stream)
+
+    def fp4_linear_workspace(self, n_tokens: int, device="cuda") -> torch.Tensor:
+        return _device_bytes(lora_fp4_linear_workspace_bytes(self.handle, n_tokens), device)
+
+    def fp4_linear(self, w: Fp4Matrix, x: torch.Tensor, seg, xq: Optional[Fp4Matrix] = None,
+                   y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """``linear`` over a 4-bit base weight."""
+        n = int(seg.n_tokens)
+        if y is None:
+            y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
+        if ws is None:
+            key = ("fp4", n, x.device)
+            if key not in self._ws:
+                self._ws[key] = self.fp4_linear_workspace(n, x.device)
+            ws = self._ws[key]
+        return lora_fp4_linear_fwd(self.handle, w, x, y, seg, ws, xq, stream)
 
     def close(self) -> None:
         if self.handle is not None:

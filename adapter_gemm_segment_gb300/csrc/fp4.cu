@@ -1,0 +1,372 @@
+// Microscaled 4-bit matrices (MXFP4): quantisation, reading back, and the entry points of the
+// linear over a 4-bit base weight.
+//
+// Stored form (lora.h): rows of 4-bit codes (e2m1: sign, two exponent bits, one mantissa bit) and,
+// per block of 32 elements, one power-of-two scale byte, the scale bytes in tiles of 128 rows x 4
+// blocks.  With E the biased float32 exponent of the block's largest |x|, the scale byte is
+// max(E - 2, 0): the largest element then lies in [4, 8) times the scale, of which [6, 8) saturates
+// at 6.  The factor 2^(127 - byte) and the product with it are exact in float32, so the rounding to
+// e2m1 is the only one.
+//
+// Both kernels move every byte once and are bound by memory.  A warp takes 256 columns of the four
+// rows r, r + 32, r + 64, r + 96 of a 128-row tile: a lane holds 8 consecutive elements of each row
+// (16-byte loads of 16-bit data, a warp's lanes side by side), four lanes share a block (two
+// shuffles give its maximum), and the 4 x 4 scale bytes of those rows' four blocks are 16
+// consecutive bytes of a scale tile, written by one lane.
+#include <cstring>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace lora {
+
+constexpr int kFp4Threads = 256;  // 8 warps: 8 of the 32 row quadruples of a row tile
+constexpr int kFp4Cols = 256;     // columns per warp
+
+// 8 elements starting at column c of a row (zeros past cols).  VEC: rows are 16-byte aligned, so
+// whole groups of 8 take vector loads.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* __restrict__ row, int c, int cols, float (&f)[8]) {
+    if (VEC && c + 8 <= cols) {
+        if constexpr (sizeof(T) == 2) {
+            unpack8<T>(__ldg(reinterpret_cast<const uint4*>(row + c)), f);
+        } else {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(row + c));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(row + c + 4));
+            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = c + e < cols ? to_f32(row[c + e]) : 0.f;
+}
+
+// Two float32 values to a byte of two e2m1 codes (lo in the low half), round to nearest even,
+// saturating.
+__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
+    uint16_t r;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
+        "cvt.u16.u8 %0, t;\n\t}"
+        : "=h"(r)
+        : "f"(lo), "f"(hi));
+    return r;
+}
+
+// The codes of a lane's 8 elements and the scale byte of its block (shared by 4 lanes).
+__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], uint32_t& scale) {
+    // |x| as an integer orders like |x|, with infinities and NaNs on top
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t E = m >> 23;
+    if (E == 255) {
+        scale = 255;
+        return 0;
+    }
+    scale = E > 2 ? E - 2 : 0;
+    const float k = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale): 2^-125 .. 2^127
+    uint32_t c = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c |= cvt_e2m1x2(f[2 * e] * k, f[2 * e + 1] * k) << (8 * e);
+    return c;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kFp4Threads)
+fp4_quantize_kernel(const T* __restrict__ x, long long ld, Fp4View q) {
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r32 = blockIdx.y * 8 + warp;  // row within each 32-row quarter
+    const int r0 = blockIdx.z * 128 + r32;
+    const int c = blockIdx.x * kFp4Cols + lane * 8;
+    float f[4][8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = r0 + 32 * j;
+        if (r < q.rows) {
+            load8<T, VEC>(x + (long long)r * ld, c, q.cols, f[j]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[j][e] = 0.f;
+        }
+    }
+    uint32_t sw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t scale;
+        const uint32_t codes = quantise8(f[j], scale);
+        const int r = r0 + 32 * j;
+        // c / 32 < blocks: the last block's codes past cols are written (as zeros) too
+        if (r < q.rows && c / 32 < q.blocks)
+            *reinterpret_cast<uint32_t*>(q.codes + (size_t)r * q.pitch + c / 2) = codes;
+        // the four scale bytes of this half-warp's 128 columns, in every lane of it
+        uint32_t w = __shfl_sync(0xffffffffu, scale, (lane & 16));
+        w |= __shfl_sync(0xffffffffu, scale, (lane & 16) + 4) << 8;
+        w |= __shfl_sync(0xffffffffu, scale, (lane & 16) + 8) << 16;
+        w |= __shfl_sync(0xffffffffu, scale, (lane & 16) + 12) << 24;
+        sw[j] = w;
+    }
+    if ((lane & 15) == 0) {
+        const size_t tile = (size_t)blockIdx.z * q.ktiles + blockIdx.x * 2 + (lane >> 4);
+        *reinterpret_cast<uint4*>(q.scales + tile * 512 + r32 * 16) = make_uint4(sw[0], sw[1], sw[2], sw[3]);
+    }
+}
+
+// Two e2m1 codes of a byte to float32 values times s.
+__device__ __forceinline__ float2 decode_e2m1x2(uint32_t byte, float s) {
+    uint32_t h2;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.u8.u32 t, %1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+        : "=r"(h2)
+        : "r"(byte));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    return make_float2(v.x * s, v.y * s);
+}
+
+// 2^(byte - 127); 2^-127 is a subnormal float32, byte 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7fc00000u)
+                                                                  : __uint_as_float(byte << 23);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kFp4Threads)
+fp4_dequantize_kernel(Fp4View q, T* __restrict__ out, long long ld) {
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r32 = blockIdx.y * 8 + warp;
+    const int r0 = blockIdx.z * 128 + r32;
+    const int c = blockIdx.x * kFp4Cols + lane * 8;
+    if (c >= q.cols) return;
+    const size_t tile = (size_t)blockIdx.z * q.ktiles + blockIdx.x * 2 + (lane >> 4);
+    const uint4 sv = __ldg(reinterpret_cast<const uint4*>(q.scales + tile * 512 + r32 * 16));
+    const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+    uint32_t codes[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = r0 + 32 * j;
+        codes[j] = r < q.rows ? __ldg(reinterpret_cast<const uint32_t*>(q.codes + (size_t)r * q.pitch + c / 2)) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = r0 + 32 * j;
+        if (r >= q.rows) break;
+        const float s = scale_value((sw[j] >> (8 * ((lane >> 2) & 3))) & 255u);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = decode_e2m1x2((codes[j] >> (8 * e)) & 255u, s);
+            f[2 * e] = v.x;
+            f[2 * e + 1] = v.y;
+        }
+        T* o = out + (long long)r * ld + c;
+        if (VEC && c + 8 <= q.cols) {
+            alignas(16) T v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(f[e]);
+#pragma unroll
+            for (int e = 0; e < (int)(8 * sizeof(T) / 16); ++e)
+                reinterpret_cast<uint4*>(o)[e] = reinterpret_cast<const uint4*>(v)[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < q.cols) o[e] = from_f32<T>(f[e]);
+        }
+    }
+}
+
+static dim3 fp4_grid(const Fp4View& q) {
+    return dim3(q.ktiles / 2, 4, (q.rows + 127) / 128);
+}
+
+template <typename T>
+static int quantize_t(const void* x, long long ld, const Fp4View& q, cudaStream_t st) {
+    // vector loads need every row on a 16-byte boundary; otherwise elements are loaded singly
+    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * (long long)sizeof(T)) % 16 == 0;
+    const T* xp = static_cast<const T*>(x);
+    void* args[] = {(void*)&xp, (void*)&ld, (void*)&q};
+    const void* fn = vec ? (const void*)fp4_quantize_kernel<T, true> : (const void*)fp4_quantize_kernel<T, false>;
+    LORA_CUDA_TRY(launch_pdl(fn, fp4_grid(q), dim3(kFp4Threads), 0, st, args));
+    return LORA_OK;
+}
+
+int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q, cudaStream_t st) {
+    if (q.rows == 0) return LORA_OK;
+    switch (dtype) {
+        case LORA_F32: return quantize_t<float>(x, ld, q, st);
+        case LORA_F16: return quantize_t<__half>(x, ld, q, st);
+        default: return quantize_t<__nv_bfloat16>(x, ld, q, st);
+    }
+}
+
+template <typename T>
+static int dequantize_t(const Fp4View& q, void* out, long long ld, cudaStream_t st) {
+    const bool vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && (ld * (long long)sizeof(T)) % 16 == 0;
+    T* op = static_cast<T*>(out);
+    void* args[] = {(void*)&q, (void*)&op, (void*)&ld};
+    const void* fn = vec ? (const void*)fp4_dequantize_kernel<T, true> : (const void*)fp4_dequantize_kernel<T, false>;
+    LORA_CUDA_TRY(launch_pdl(fn, fp4_grid(q), dim3(kFp4Threads), 0, st, args));
+    return LORA_OK;
+}
+
+// grid.z counts 128-row tiles
+constexpr int kFp4MaxRows = 65535 * 128;
+
+static int check_shape(int rows, int cols) {
+    if (rows < 0 || cols < 1) return set_error(LORA_EINVAL, "4-bit matrix of %d x %d", rows, cols);
+    if (rows > kFp4MaxRows || cols > (1 << 30))
+        return set_error(LORA_EUNSUP, "4-bit matrix of %d x %d is too large", rows, cols);
+    return LORA_OK;
+}
+
+static int check_matrix(const lora_fp4_matrix* m, const char* what) {
+    if (!m) return set_error(LORA_EINVAL, "%s is NULL", what);
+    const int rc = check_shape(m->rows, m->cols);
+    if (rc) return rc;
+    if (m->rows == 0) return LORA_OK;
+    if (!m->codes_dev || !m->scales_dev) return set_error(LORA_EINVAL, "%s has no codes or scales", what);
+    if ((reinterpret_cast<uintptr_t>(m->codes_dev) | reinterpret_cast<uintptr_t>(m->scales_dev)) % 256)
+        return set_error(LORA_EINVAL, "%s: codes and scales must be 256-byte aligned", what);
+    return LORA_OK;
+}
+
+// A strided [rows, cols] array of dtype (what the 4-bit form is made from or read into).
+static int check_rows(const void* p, int dtype, int64_t ld, int rows, int cols, const char* what) {
+    if (dtype != LORA_F32 && dtype != LORA_F16 && dtype != LORA_BF16) return set_error(LORA_EINVAL, "bad dtype %d", dtype);
+    if (ld < cols) return set_error(LORA_EINVAL, "%s: row stride %lld below %d columns", what, (long long)ld, cols);
+    if (rows == 0) return LORA_OK;
+    if (!p) return set_error(LORA_EINVAL, "%s is NULL", what);
+    if (reinterpret_cast<uintptr_t>(p) % dtype_size(dtype)) return set_error(LORA_EINVAL, "%s is misaligned", what);
+    return LORA_OK;
+}
+
+static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev, m->scales_dev, m->rows, m->cols); }
+
+// Workspace of lora_fp4_linear_fwd: the shrink output, then the stored form of x.
+struct Fp4WsLayout {
+    size_t s_bytes, codes_off, scales_off, total;
+};
+static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
+    const int rc = lora_linear_workspace_bytes(pool, n, &L->s_bytes);
+    if (rc) return rc;
+    const int h_in = pool->desc.h_in;
+    L->codes_off = align256(L->s_bytes);
+    L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
+    L->total = L->scales_off + align256(fp4_scales_bytes(n, h_in));
+    return LORA_OK;
+}
+
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+int lora_fp4_bytes(int rows, int cols, size_t* codes_bytes, size_t* scales_bytes) {
+    if (!codes_bytes || !scales_bytes) return set_error(LORA_EINVAL, "codes_bytes/scales_bytes is NULL");
+    const int rc = check_shape(rows, cols);
+    if (rc) return rc;
+    *codes_bytes = fp4_codes_bytes(rows, cols);
+    *scales_bytes = fp4_scales_bytes(rows, cols);
+    return LORA_OK;
+}
+
+int lora_fp4_quantize(const void* x_dev, int dtype, int64_t ld, const lora_fp4_matrix* out, void* stream) {
+    int rc = check_matrix(out, "out");
+    if (rc) return rc;
+    rc = check_rows(x_dev, dtype, ld, out->rows, out->cols, "x");
+    if (rc) return rc;
+    return launch_fp4_quantize(x_dev, dtype, ld, view_of(out), static_cast<cudaStream_t>(stream));
+}
+
+int lora_fp4_dequantize(const lora_fp4_matrix* q, void* out_dev, int dtype, int64_t ld, void* stream) {
+    int rc = check_matrix(q, "q");
+    if (rc) return rc;
+    rc = check_rows(out_dev, dtype, ld, q->rows, q->cols, "out");
+    if (rc || q->rows == 0) return rc;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (dtype) {
+        case LORA_F32: return dequantize_t<float>(view_of(q), out_dev, ld, st);
+        case LORA_F16: return dequantize_t<__half>(view_of(q), out_dev, ld, st);
+        default: return dequantize_t<__nv_bfloat16>(view_of(q), out_dev, ld, st);
+    }
+}
+
+int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_dev, int dtype, int64_t ldy,
+                    void* stream) {
+    int rc = check_matrix(x, "x");
+    if (!rc) rc = check_matrix(w, "w");
+    if (rc) return rc;
+    if (x->cols != w->cols) return set_error(LORA_EINVAL, "x has %d columns, w %d", x->cols, w->cols);
+    rc = check_rows(y_dev, dtype, ldy, w->rows ? x->rows : 0, w->rows, "y");
+    if (rc || x->rows == 0 || w->rows == 0) return rc;
+    return launch_fp4_gemm(view_of(x), view_of(w), y_dev, dtype, ldy, nullptr, /*early_w=*/false,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes) {
+    if (!pool || !bytes) return set_error(LORA_EINVAL, "pool/bytes is NULL");
+    Fp4WsLayout L;
+    const int rc = fp4_ws_layout(pool, n_tokens, &L);
+    if (rc) return rc;
+    *bytes = L.total;
+    return LORA_OK;
+}
+
+int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* x_dev, const lora_fp4_matrix* xq,
+                        void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream) {
+    if (!pool || !seg) return set_error(LORA_EINVAL, "pool/seg is NULL");
+    const PoolView pv = pool_view(pool);
+    const int n = seg->n_tokens;
+    if (seg->n_slots != pv.S)
+        return set_error(LORA_EINVAL, "segments were built for %d slots, pool has %d", seg->n_slots, pv.S);
+    int rc = check_matrix(w, "w");
+    if (rc) return rc;
+    if (w->rows != pv.h_out || w->cols != pv.h_in)
+        return set_error(LORA_EINVAL, "w is %d x %d, the pool's linear %d x %d", w->rows, w->cols, pv.h_out, pv.h_in);
+    if (xq) {
+        rc = check_matrix(xq, "xq");
+        if (rc) return rc;
+        if (xq->rows != n || xq->cols != pv.h_in)
+            return set_error(LORA_EINVAL, "xq is %d x %d, x %d x %d", xq->rows, xq->cols, n, pv.h_in);
+    }
+    if (n == 0) return LORA_OK;
+    if (!x_dev || !y_dev || !ws_dev) return set_error(LORA_EINVAL, "x/y/ws is NULL");
+    const size_t align = pv.dtype == LORA_F32 ? 4 : 16;
+    if ((reinterpret_cast<uintptr_t>(x_dev) | reinterpret_cast<uintptr_t>(y_dev)) % align)
+        return set_error(LORA_EINVAL, "x/y must be %zu-byte aligned", align);
+    if (reinterpret_cast<uintptr_t>(ws_dev) % 256) return set_error(LORA_EINVAL, "ws must be 256-byte aligned");
+    Fp4WsLayout L;
+    rc = fp4_ws_layout(pool, n, &L);
+    if (rc) return rc;
+    if (ws_bytes < L.total)
+        return set_error(LORA_ENOSPACE, "4-bit linear workspace needs %zu bytes, got %zu", L.total, ws_bytes);
+    char* ws = static_cast<char*>(ws_dev);
+    float* s_buf = reinterpret_cast<float*>(ws);
+    const Fp4View q = xq ? view_of(xq) : fp4_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
+    const SegView sv = seg_view(seg);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+    if (!xq) {
+        rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
+        if (rc) return rc;
+    }
+    int s_parts = 1;
+    if (n > 256 && shrink_tc_supported(pv))
+        rc = launch_shrink_tc(pv, sv, x_dev, s_buf, st);
+    else
+        rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
+    if (rc) return rc;
+    rc = launch_fp4_gemm(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
+    if (rc) return rc;
+    return launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
+}
+
+}  // extern "C"

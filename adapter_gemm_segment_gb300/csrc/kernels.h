@@ -76,6 +76,36 @@ int shrink_tc_group_supported(const PoolView& pv, int count);
 int launch_shrink_tc_group(const PoolView& pv, const GroupView& grp, const SegView& sv, const void* x, float* s_out,
                            cudaStream_t st);
 
+// A stored 4-bit matrix as the kernels see it (layout in lora.h).
+struct Fp4View {
+    uint8_t* codes;
+    uint8_t* scales;
+    int rows, cols;
+    int blocks;     // blocks of 32 per row
+    int ktiles;     // scale tiles per 128 rows (KT)
+    size_t pitch;   // bytes per row of codes
+};
+inline Fp4View fp4_view(void* codes, void* scales, int rows, int cols) {
+    Fp4View v;
+    v.codes = static_cast<uint8_t*>(codes);
+    v.scales = static_cast<uint8_t*>(scales);
+    v.rows = rows;
+    v.cols = cols;
+    v.blocks = (cols - 1) / 32 + 1;
+    v.ktiles = 2 * ((cols - 1) / 256 + 1);
+    v.pitch = (size_t)v.blocks * 16;
+    return v;
+}
+inline size_t fp4_codes_bytes(int rows, int cols) { return (size_t)rows * ((cols - 1) / 32 + 1) * 16; }
+inline size_t fp4_scales_bytes(int rows, int cols) {
+    return (size_t)((rows + 127) / 128) * (2 * ((cols - 1) / 256 + 1)) * 512;
+}
+int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q, cudaStream_t st);
+// y = x w^T (dtype, row stride ldy).  status: nullable device word; y stays untouched unless it is
+// LORA_OK.  early_w: every kernel that could have written w has completed when this grid starts.
+int launch_fp4_gemm(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, const int32_t* status,
+                    bool early_w, cudaStream_t st);
+
 int num_sms();
 
 }  // namespace lora

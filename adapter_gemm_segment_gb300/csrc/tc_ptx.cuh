@@ -238,6 +238,37 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Instruction descriptor of kind::mxf4 (block-scaled 4-bit operands, float32 accumulation): e2m1
+// operands, both K-major, e8m0 scales, dense K = 64.  sf_id (0 or 2): which half of the four scale
+// bytes of a row the instruction's two blocks of 32 take.
+//   bits 4-5 / 29-30 scale id of B / A   bits 7-9 / 10-11 A / B format (1 = e2m1)
+//   bits 17-22 N >> 3   bit 23 scale format (1 = e8m0)   bits 27-28 M >> 7
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int sf_id) {
+    return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (1u << 23) | (static_cast<uint32_t>(M >> 7) << 27) | (static_cast<uint32_t>(sf_id) << 29);
+}
+// D[tmem] (+)= A[smem] * B[smem]^T with the block scales of A and B in tensor memory (32 lanes x 4
+// columns per 128 rows, the same in every group of 32 lanes), issued by one thread.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+// Copy one scale tile (32 rows x 16 bytes, contiguous) from shared memory into tensor memory: 4
+// columns of 32 lanes, repeated for the four groups of 32 lanes.  Ordered before later MMAs of
+// this thread.  Descriptor: no swizzle, 8-row groups of 128 bytes.
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128 >> 4) << 16) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
 // Arrive (once) on `bar` when every tcgen05.mma issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))

@@ -94,5 +94,21 @@ inline int make_map_bchunks(CUtensorMap* m, const void* base, int bf16, uint64_t
     return LORA_OK;
 }
 
+// Codes of a stored 4-bit matrix: [rows, pitch] bytes, box {128 bytes (256 elements), box_rows},
+// 128-byte swizzle; bytes past the matrix read as zero codes.
+inline int make_map_fp4(CUtensorMap* m, const void* codes, uint64_t pitch, uint64_t rows, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return set_error(LORA_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+    const cuuint64_t dims[2] = {pitch, rows};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {128u, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(LORA_ECUDA, "cuTensorMapEncodeTiled (4-bit codes) failed (%d)", (int)r);
+    return LORA_OK;
+}
+
 }  // namespace tc
 }  // namespace lora

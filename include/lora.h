@@ -352,6 +352,62 @@ int lora_loader_acquire(lora_loader_t loader, int count, const int* slots, void*
 int lora_loader_release(lora_loader_t loader, int count, const int* slots, void* stream);
 int lora_loader_stats(lora_loader_t loader, uint64_t* mounts, uint64_t* drained_fences);
 
+/* ---- microscaled 4-bit base weights (MXFP4) -----------------------------------------------
+ *
+ * A frozen base weight under 16-bit adapters may be held in microscaled 4-bit floating point:
+ * 32 consecutive elements of a row (a block) share one scale 2^e, and each element is one of
+ * +-{0, 0.5, 1, 1.5, 2, 3, 4, 6} times that scale -- 4.25 bits an element.  The tensor cores
+ * multiply two such matrices directly, applying the scales themselves.  The multi-LoRA pages
+ * have no counterpart to these entry points.
+ *
+ * A stored matrix [rows, cols] is two device buffers (sizes from lora_fp4_bytes, contents
+ * written by lora_fp4_quantize, or by the caller in the same layout):
+ *   codes   row r at r * pitch, pitch = 16 * ceil(cols / 32) bytes; element k is the low (k even)
+ *           or high (k odd) half of byte k / 2: bit 3 the sign, bits 0-2 the index into the eight
+ *           magnitudes.  Codes past cols are 0.
+ *   scales  byte of row r, block b (= k / 32) at
+ *             ((r / 128) * KT + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4
+ *           with KT = 2 * ceil(cols / 256): tiles of 128 rows x 4 blocks, the order in which the
+ *           tensor cores take them.  Byte e + 127; 255 is NaN and makes its whole block NaN.
+ *           Bytes of rows past `rows` and blocks past the last are 0.
+ * Both 256-byte aligned, owned by the caller.  rows >= 0, cols >= 1. */
+typedef struct {
+    void* codes_dev;
+    void* scales_dev;
+    int32_t rows;
+    int32_t cols;
+} lora_fp4_matrix;
+
+/* Bytes of the two buffers of a [rows, cols] matrix.  LORA_EINVAL on a bad shape. */
+int lora_fp4_bytes(int rows, int cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Quantise x_dev [rows, cols] (dtype a lora_dtype, consecutive rows ld elements apart, ld >= cols;
+ * aligned to its element) into out.  Block scale: e = max(floor(log2 max|x|) - 2, -127); element:
+ * x / 2^e rounded to the nearest magnitude, ties to the even code, at most 6.  Everything is exact
+ * up to that one rounding, so equal inputs give equal bytes for every dtype.  A block that holds an
+ * infinity or a NaN gets the NaN scale and codes 0.  One kernel on `stream`. */
+int lora_fp4_quantize(const void* x_dev, int dtype, int64_t ld, const lora_fp4_matrix* out, void* stream);
+
+/* Read a stored matrix back: out_dev [rows, cols] (dtype, row stride ld >= cols), each value rounded
+ * once to dtype.  One kernel on `stream`. */
+int lora_fp4_dequantize(const lora_fp4_matrix* q, void* out_dev, int dtype, int64_t ld, void* stream);
+
+/* y_dev [x.rows, w.rows] = x w^T of two stored matrices with the same cols (float32 accumulation,
+ * one rounding to dtype, row stride ldy >= w.rows elements, aligned to its element).  A NaN scale
+ * makes the outputs of its row NaN and no others. */
+int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_dev, int dtype, int64_t ldy,
+                    void* stream);
+
+/* lora_linear_fwd over a 4-bit base weight:
+ *     y[t,:] = Q(x)[t,:] w^T + (alpha_s / r_s) (x[t,:] A_s^T) B_s^T
+ * w: stored [h_out, h_in].  The base term takes x quantised as lora_fp4_quantize does (into the
+ * workspace; or, when xq is not NULL, takes xq as the stored form of x, which projections that read
+ * the same x share); the LoRA term takes x as it is, in the pool's dtype.  x_dev, y_dev, seg,
+ * errors and the device status word as in lora_linear_fwd. */
+int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes);
+int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* x_dev, const lora_fp4_matrix* xq,
+                        void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);
+
 /* Message of the last failed call on this host thread ("" if none). */
 const char* lora_last_error(void);
 
