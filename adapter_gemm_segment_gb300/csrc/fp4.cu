@@ -16,6 +16,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "fp4_device.cuh"
 #include "kernels.h"
 
 namespace lora {
@@ -40,39 +41,6 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int c, int cols
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = c + e < cols ? to_f32(row[c + e]) : 0.f;
-}
-
-// Two float32 values to a byte of two e2m1 codes (lo in the low half), round to nearest even,
-// saturating.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
-    uint16_t r;
-    asm("{\n\t.reg .b8 t;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-        "cvt.u16.u8 %0, t;\n\t}"
-        : "=h"(r)
-        : "f"(lo), "f"(hi));
-    return r;
-}
-
-// The codes of a lane's 8 elements and the scale byte of its block (shared by 4 lanes).
-__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], uint32_t& scale) {
-    // |x| as an integer orders like |x|, with infinities and NaNs on top
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t E = m >> 23;
-    if (E == 255) {
-        scale = 255;
-        return 0;
-    }
-    scale = E > 2 ? E - 2 : 0;
-    const float k = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale): 2^-125 .. 2^127
-    uint32_t c = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c |= cvt_e2m1x2(f[2 * e] * k, f[2 * e + 1] * k) << (8 * e);
-    return c;
 }
 
 template <typename T, bool VEC>
@@ -104,12 +72,7 @@ fp4_quantize_kernel(const T* __restrict__ x, long long ld, Fp4View q) {
         // c / 32 < blocks: the last block's codes past cols are written (as zeros) too
         if (r < q.rows && c / 32 < q.blocks)
             *reinterpret_cast<uint32_t*>(q.codes + (size_t)r * q.pitch + c / 2) = codes;
-        // the four scale bytes of this half-warp's 128 columns, in every lane of it
-        uint32_t w = __shfl_sync(0xffffffffu, scale, (lane & 16));
-        w |= __shfl_sync(0xffffffffu, scale, (lane & 16) + 4) << 8;
-        w |= __shfl_sync(0xffffffffu, scale, (lane & 16) + 8) << 16;
-        w |= __shfl_sync(0xffffffffu, scale, (lane & 16) + 12) << 24;
-        sw[j] = w;
+        sw[j] = scale_word(scale, lane);
     }
     if ((lane & 15) == 0) {
         const size_t tile = (size_t)blockIdx.z * q.ktiles + blockIdx.x * 2 + (lane >> 4);
@@ -251,13 +214,14 @@ static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev,
 
 // Workspace of lora_fp4_linear_fwd: the shrink output, then the stored form of x.
 struct Fp4WsLayout {
-    size_t s_bytes, codes_off, scales_off, total;
+    size_t codes_off, scales_off, total;
 };
 static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
-    const int rc = lora_linear_workspace_bytes(pool, n, &L->s_bytes);
+    size_t s_bytes;
+    const int rc = lora_linear_workspace_bytes(pool, n, &s_bytes);
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
-    L->codes_off = align256(L->s_bytes);
+    L->codes_off = align256(s_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
     L->total = L->scales_off + align256(fp4_scales_bytes(n, h_in));
     return LORA_OK;
@@ -354,15 +318,19 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
     const SegView sv = seg_view(seg);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
 
+    if (n > 256 && pv.dtype != LORA_F32) {
+        const Fp4View own = fp4_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
+        rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, st);
+        if (rc) return rc;
+        const Fp4Lora lora = {sv.perm, sv.idx, s_buf, pv.B, pv.R, pv.S};
+        return launch_fp4_pair(own, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
+    }
     if (!xq) {
         rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (rc) return rc;
     }
     int s_parts = 1;
-    if (n > 256 && shrink_tc_supported(pv))
-        rc = launch_shrink_tc(pv, sv, x_dev, s_buf, st);
-    else
-        rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
+    rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
     if (rc) return rc;
     rc = launch_fp4_gemm(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
     if (rc) return rc;

@@ -1,0 +1,839 @@
+// Large batches (more than 256 tokens) over a 4-bit base weight: the product on CTA pairs, and the
+// kernel before it that quantises x and computes the LoRA shrink in one read of x.
+//
+// The linear's tokens are taken in the order of the segments (sorted by adapter), so a tile of
+// tokens meets few adapters whatever the batch's order; y rows go back to their own places.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "fp4_device.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+#include "tma_host.h"
+
+namespace lora {
+namespace tc {
+
+using namespace ptx;
+
+// ============================================================================================
+// product: 256 x 256 tiles on CTA pairs (tcgen05 cta_group::2)
+// ============================================================================================
+// At 4 bits an operand byte carries 4 multiply-adds per output row, so a 128 x 256 tile per CTA
+// would take operands in faster (about 100 bytes a clock and SM at the tensor cores' rate) than an
+// SM receives them.  A pair of CTAs shares a 256 x 256 tile: CTA r stages token rows 128r.. and
+// weight rows 128r.. (32 KB of codes a step of 256 along K instead of 48 KB), the even CTA issues
+// M = 256 x N = 256 MMAs that read both halves, and each CTA's tensor memory receives its 128
+// tokens x 256 features.
+//
+// Tensor memory (512 columns): two accumulators of 256 columns that share 48 of them ([0, 256) and
+// [208, 464)), and two sets of 24 scale columns.  The main loop of the next tile may start once the
+// epilogue has taken those 48 columns, which it takes first.  A set of scale columns is rewritten
+// (tcgen05.cp) only after the MMAs of the step two before have completed.
+//
+// The LoRA term is more K blocks of the same accumulator: for the distinct adapters d of the pair's
+// 256 tokens, columns d * r_max + j hold s[t, j] on the token side (zero unless t uses d; s is
+// rounded to the 16-bit type by the kernel before) and B_d[o, j] on the feature side, kind::f16, 32
+// columns a block, two block buffers.  Because those products reach every token of the tile, an
+// infinity or NaN in one tenant's B would reach the other tenants' rows as 0 * inf: such elements
+// are replaced by zeros here and the epilogue adds them to their own tokens alone.
+//
+// Warps: 0 loads, 1 issues MMAs (even CTA), 2-5 drain the accumulator, 6-9 build the LoRA blocks.
+constexpr int kPM = 128;         // token rows per CTA
+constexpr int kPN = 256;         // features per pair tile
+constexpr int kPThreads = 320;
+constexpr int kPStages = 5;
+constexpr uint32_t kPXBytes = kPM * 128, kPWBytes = (kPN / 2) * 128;
+constexpr uint32_t kPSxBytes = 1024, kPSwBytes = 2048;
+constexpr uint32_t kPStageBytes = kPXBytes + kPWBytes + kPSxBytes + kPSwBytes;
+constexpr int kPAcc1 = 208;                         // first column of the second accumulator
+constexpr int kPScaleCol = 464;                     // first column of the scale sets (24 each)
+constexpr int kPLoraChunk = kPM * 16;               // 8 columns of 128 rows, 16 bytes a row
+constexpr int kPLoraBytes = 2 * 4 * kPLoraChunk;    // one block: 4 chunks on each side
+constexpr int kPStageOut = 4 * 32 * 64 * 2;         // y staging: 32 rows x 64 16-bit columns a warp
+constexpr int kPScratch = 64 * 4 + 64 * 4 + 256 * 4 + 1024;
+constexpr size_t kPSmem = (size_t)kPStages * kPStageBytes + 2 * kPLoraBytes + kPStageOut + kPScratch + 256 + 1024;
+static_assert(kPSmem <= 227 * 1024, "shared memory of the pair kernel");
+static_assert(kPStageBytes % 1024 == 0, "swizzle atoms stay aligned");
+
+struct PairArgs {
+    void* y;
+    int32_t* status;         // nullable
+    const int32_t* perm;     // row of y of each token row (nullptr: the same)
+    const int32_t* idx;      // fuse: adapter slot by original token
+    const void* s16;         // fuse: [n][R] shrink output in token-row order, 16-bit
+    const void* B;           // fuse: pool's B slab
+    long long ldy;
+    int n, h_out, m_tiles, n_tiles, nkb, kt;
+    int R, S, fuse, bf16, early_w, vec;
+};
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                const __grid_constant__ CUtensorMap tmSx, const __grid_constant__ CUtensorMap tmSw, const PairArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_align(smem_raw, 1024);
+    uint8_t* lora_sm = smem + kPStages * kPStageBytes;      // [2] blocks {token side, feature side}
+    uint8_t* yst = lora_sm + 2 * kPLoraBytes;               // [4 warps][32 rows][64] (f32: spills into lora_sm's room)
+    uint32_t* seen = reinterpret_cast<uint32_t*>(yst + kPStageOut);  // [64] slots the tile's tokens name
+    int* before = reinterpret_cast<int*>(seen + 64);        // [64] named slots below each word
+    int* dlist = before + 64;                               // [256] the tile's slots in order
+    uint32_t* badmap = reinterpret_cast<uint32_t*>(dlist + 256);  // [256] LoRA chunks with a non-finite B
+    uint64_t* full = reinterpret_cast<uint64_t*>(badmap + 256);   // even CTA: both halves of a stage
+    uint64_t* empty = full + kPStages;       // the even CTA's commits (multicast)
+    uint64_t* acc_full = empty + kPStages;   // [2] (multicast)
+    uint64_t* ov_free = acc_full + 2;        // even CTA: the shared columns are drained (8 warps)
+    uint64_t* lora_full = ov_free + 1;       // [2] even CTA: a LoRA block is written (8 warps)
+    uint64_t* lora_empty = lora_full + 2;    // [2] (multicast)
+    uint64_t* linfo = lora_empty + 2;        // even CTA: the tile's number of LoRA blocks is known
+    uint64_t* epi_done = linfo + 1;          // the epilogue is through with a tile (4 warps)
+    uint64_t* lora_done = epi_done + 1;      // the tile's LoRA scratch is complete (4 warps)
+    uint64_t* drained = lora_done + 1;       // even CTA: every MMA has completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort, LoRA blocks, any bad chunk
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int total = a.m_tiles * a.n_tiles;
+    const int nkb = a.nkb;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&lora_full[b], 8);
+            mbar_init(&lora_empty[b], 1);
+        }
+        mbar_init(ov_free, 8);
+        mbar_init(linfo, 1);
+        mbar_init(epi_done, 4);
+        mbar_init(lora_done, 4);
+        mbar_init(drained, 1);
+        flags[0] = flags[1] = flags[2] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmX);
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmSx);
+        prefetch_tmap(&tmSw);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before either arrives on the other's
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+            auto load = [&](int s, const CUtensorMap* m, uint32_t off, int c0, int c1) {
+                tma_load_2d_pair(smem + s * kPStageBytes + off, m, full0 + static_cast<uint32_t>(s) * 8u, c0, c1);
+            };
+            auto load_w = [&](int s, int kb, int n0) {
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPStageBytes);
+                load(s, &tmW, kPXBytes, kb * 128, n0 + static_cast<int>(rank) * (kPN / 2));
+                const int rt = n0 / 128;
+                load(s, &tmSw, kPXBytes + kPWBytes + kPSxBytes, 0, rt * a.kt + 2 * kb);
+                load(s, &tmSw, kPXBytes + kPWBytes + kPSxBytes + 1024, 0, (rt + 1) * a.kt + 2 * kb);
+            };
+            auto load_x = [&](int s, int kb, int m0) {
+                const int row = m0 + static_cast<int>(rank) * kPM;
+                load(s, &tmX, 0, kb * 128, row);
+                load(s, &tmSx, kPXBytes + kPWBytes, 0, row / 128 * a.kt + 2 * kb);
+            };
+            // the first tile's weight boxes go out before the kernels ahead have finished
+            int pre = 0;
+            if (a.early_w && pair < total) {
+                pre = min(kPStages, nkb);
+                for (int i = 0; i < pre; ++i) load_w(i, i, pair % a.n_tiles * kPN);
+            }
+            pdl_wait();
+            int it = 0;
+            for (int tile = pair; tile < total && !flags[0]; tile += npairs) {
+                const int m0 = tile / a.n_tiles * 2 * kPM, n0 = tile % a.n_tiles * kPN;
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = it % kPStages;
+                    if (it >= kPStages && !mbar_wait(&empty[s], ((it / kPStages) & 1) ^ 1, flags)) break;
+                    if (it >= pre) load_w(s, kb, n0);
+                    load_x(s, kb, m0);
+                }
+            }
+            // aborted: the even CTA lets every copy in flight (counted on its barriers) land
+            if (flags[0]) {
+                if (a.status) report_timeout_status(a.status);
+                if (rank == 0)
+                    for (int i = max(0, it - kPStages); i < it; ++i) {
+                        const unsigned long long t0 = globaltimer();
+                        while (!mbar_try_wait(&full[i % kPStages], (i / kPStages) & 1) &&
+                               globaltimer() - t0 < kWaitLimitNs) {
+                        }
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc_lora = idesc_f16(2 * kPM, kPN, a.bf16 != 0);
+            int it = 0, local = 0, lb = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok; tile += npairs, ++local) {
+                const int buf = local & 1;
+                const uint32_t acc = tmem + buf * kPAcc1;
+                // the tile before has left the columns both accumulators share (and, the epilogue
+                // taking tiles in order, the one before that has left this accumulator)
+                if (local > 0 && !mbar_wait_cluster(ov_free, (local - 1) & 1, flags)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int s = it % kPStages;
+                    if (!mbar_wait(&full[s], (it / kPStages) & 1, flags) ||
+                        // the scale columns' last readers
+                        (it >= 2 && !mbar_wait(&empty[(it - 2) % kPStages], ((it - 2) / kPStages) & 1, flags))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xa = smem_u32(smem + s * kPStageBytes), wa = xa + kPXBytes, sc = wa + kPWBytes;
+                    const uint32_t sfa = tmem + kPScaleCol + (it & 1) * 24, sfb = sfa + 8;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        tmem_cp_scales_pair(sfa + 4 * j, sdesc_scales(sc + 512 * j));
+                        tmem_cp_scales_pair(sfb + 8 * j, sdesc_scales(sc + kPSxBytes + 512 * j));
+                        tmem_cp_scales_pair(sfb + 8 * j + 4, sdesc_scales(sc + kPSxBytes + 1024 + 512 * j));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_pair_mxf4(acc, sdesc_sw128(xa + k * 32), sdesc_sw128(wa + k * 32),
+                                       idesc_mxf4(2 * kPM, kPN, (k & 1) * 2), sfa + 4 * (k >> 1), sfb + 8 * (k >> 1),
+                                       (kb > 0 || k > 0) ? 1u : 0u);
+                    umma_pair_commit(&empty[s], 0x3);
+                }
+                if (!ok) break;
+                if (a.fuse) {
+                    if (!mbar_wait(linfo, local & 1, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    const int blocks = flags[1];
+                    for (int b = 0; b < blocks; ++b, ++lb) {
+                        const int lbuf = lb & 1;
+                        if (!mbar_wait_cluster(&lora_full[lbuf], (lb >> 1) & 1, flags)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(lora_sm + lbuf * kPLoraBytes), ba = sa + 4 * kPLoraChunk;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            umma_pair_f16(acc, sdesc_chunks(sa + 2 * k * kPLoraChunk, kPLoraChunk),
+                                          sdesc_chunks(ba + 2 * k * kPLoraChunk, kPLoraChunk), idesc_lora, 1u);
+                        umma_pair_commit(&lora_empty[lbuf], 0x3);
+                    }
+                    if (!ok) break;
+                }
+                umma_pair_commit(&acc_full[buf], 0x3);
+            }
+            if (!ok && a.status) report_timeout_status(a.status);
+            // every MMA issued above has completed before the pair may tear down
+            umma_pair_commit(drained, 0x1);
+            const unsigned long long t0 = globaltimer();
+            while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kWaitLimitNs) {
+            }
+        }
+    } else if (warp < 6) {
+        // ---- epilogue: thread <-> token row (TMEM lane) of this CTA's half, 64 features a round ----
+        const int q = warp & 3;
+        constexpr int kCh = 64 * sizeof(T) / 16;  // 16-byte pieces of a staged row
+        uint8_t* ys = sizeof(T) == 2 ? yst + q * (32 * 64 * 2) : lora_sm + q * (32 * 64 * 4);  // f32 never fuses
+        const uint32_t ov_free0 = mapa_shared(smem_u32(ov_free), 0);
+        pdl_wait();
+        const int status = a.status ? __ldcg(a.status) : LORA_OK;
+        T* y = static_cast<T*>(a.y);
+        int local = 0;
+        for (int tile = pair; tile < total; tile += npairs, ++local) {
+            const int buf = local & 1;
+            const int m0 = tile / a.n_tiles * 2 * kPM + static_cast<int>(rank) * kPM, n0 = tile % a.n_tiles * kPN;
+            const int row = m0 + q * 32 + lane;
+            const int yrow = row < a.n ? (a.perm ? __ldcg(a.perm + row) : row) : -1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, flags) &&
+                                             (!a.fuse || mbar_wait(lora_done, local & 1, flags))))
+                break;
+            tc_fence_after();
+            const bool any_bad = a.fuse && flags[2] != 0;
+            const int slot = any_bad && yrow >= 0 && status == LORA_OK ? __ldcg(a.idx + yrow) : -1;
+            const uint32_t taddr = tmem + buf * kPAcc1 + (static_cast<uint32_t>(q * 32) << 16);
+            for (int u = 0; u < 4; ++u) {
+                const int c0 = (buf == 0 ? 3 - u : u) * 64;  // the shared columns first
+                uint32_t r[64];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_ld16(taddr + c0 + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * i]));
+                tmem_ld_wait();
+                if (u == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(ov_free0);
+                }
+                if (n0 + c0 >= a.h_out || status != LORA_OK) continue;
+                if constexpr (sizeof(T) == 2) {
+                    if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
+                        const int w = slot >> 5;
+                        const int d = before[w] + __popc(seen[w] & ((1u << (slot & 31)) - 1u));
+                        const int chunks = a.R / 8;
+                        for (int c = 0; c < chunks; ++c) {
+                            const int p = d * chunks + c;
+                            if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
+                            const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
+                                                                                   (size_t)row * a.R + c * 8));
+                            const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + n0 + c0) * a.R + c * 8;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (n0 + c0 + i < a.h_out)
+                                    r[i] = __float_as_uint(
+                                        nonfinite_dot8<T>(__ldg(reinterpret_cast<const uint4*>(Bs + (size_t)i * a.R)), sv,
+                                                          __uint_as_float(r[i])));
+                        }
+                    }
+                }
+                // through shared memory (16-byte pieces permuted by row), so that eight lanes write
+                // 128 consecutive bytes of a row of y
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < kCh; ++c) {
+                    constexpr int per = 16 / sizeof(T);
+                    alignas(16) T v[per];
+#pragma unroll
+                    for (int e = 0; e < per; ++e) v[e] = from_f32<T>(__uint_as_float(r[c * per + e]));
+                    *reinterpret_cast<uint4*>(ys + (lane * kCh + (c ^ (lane & 7))) * 16) = *reinterpret_cast<const uint4*>(v);
+                }
+                __syncwarp();
+                constexpr int kRows = 32 / kCh;  // rows a warp writes at once
+                const int c = lane % kCh;
+                const int col = n0 + c0 + c * (16 / (int)sizeof(T));
+#pragma unroll
+                for (int i = 0; i < kCh; ++i) {
+                    const int rr = i * kRows + lane / kCh;
+                    const int yr = __shfl_sync(0xffffffffu, yrow, rr);
+                    const uint4 v = *reinterpret_cast<const uint4*>(ys + (rr * kCh + (c ^ (rr & 7))) * 16);
+                    if (yr < 0) continue;
+                    T* yp = y + (long long)yr * a.ldy + col;
+                    if (a.vec && col + (int)(16 / sizeof(T)) <= a.h_out) {
+                        *reinterpret_cast<uint4*>(yp) = v;
+                    } else {
+                        alignas(16) T e8[16 / sizeof(T)];
+                        *reinterpret_cast<uint4*>(e8) = v;
+#pragma unroll
+                        for (int e = 0; e < (int)(16 / sizeof(T)); ++e)
+                            if (col + e < a.h_out) yp[e] = e8[e];
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(epi_done);
+        }
+    } else if (a.fuse) {
+        // ---- LoRA blocks ----
+        const int lt = threadIdx.x - 192;  // 0..127: a token row and a feature of this CTA's half
+        if constexpr (sizeof(T) == 2) {
+            pdl_wait();
+            const int status = a.status ? __ldcg(a.status) : LORA_OK;
+            const uint32_t lora_full0 = mapa_shared(smem_u32(lora_full), 0);
+            const int chunks = a.R / 8;
+            int local = 0, lb = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total; tile += npairs, ++local) {
+                const int m0 = tile / a.n_tiles * 2 * kPM, n0 = tile % a.n_tiles * kPN;
+                // the slots of the pair's 256 tokens: this CTA's row lt, then the other CTA's
+                int slot[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = m0 + static_cast<int>(rank ^ h) * kPM + lt;
+                    slot[h] = -1;
+                    if (row < a.n && status == LORA_OK) slot[h] = __ldcg(a.idx + __ldcg(a.perm + row));
+                }
+                // the epilogue reads this scratch for the tile before
+                if (local > 0 && !mbar_wait(epi_done, (local - 1) & 1, flags)) ok = false;
+                if (!named_bar_and(2, 128, ok)) break;  // all four warps leave together
+                if (lt < 64) seen[lt] = 0;
+                for (int i = lt; i < 256; i += 128) badmap[i] = 0;
+                if (lt == 0) flags[2] = 0;
+                named_bar_sync(2, 128);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (slot[h] >= 0) atomicOr(&seen[slot[h] >> 5], 1u << (slot[h] & 31));
+                named_bar_sync(2, 128);
+                if (lt < 32) {  // words 2 lane and 2 lane + 1
+                    const int p0 = __popc(seen[2 * lt]), p1 = __popc(seen[2 * lt + 1]);
+                    int v = p0 + p1;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, v, d);
+                        if (lt >= d) v += o;
+                    }
+                    before[2 * lt] = v - p0 - p1;
+                    before[2 * lt + 1] = v - p1;
+                }
+                named_bar_sync(2, 128);
+                if (lt < 64) {
+                    int at = before[lt];
+                    for (uint32_t m = seen[lt]; m; m &= m - 1) dlist[at++] = lt * 32 + __ffs(m) - 1;
+                }
+                named_bar_sync(2, 128);
+                const int D = before[63] + __popc(seen[63]);
+                const int P = D * chunks;            // 8-column chunks of the tile's adapters
+                const int blocks = (P + 3) / 4;
+                if (rank == 0 && lt == 0) {
+                    flags[1] = blocks;
+                    mbar_arrive(linfo);
+                }
+                const int o_own = n0 + static_cast<int>(rank) * (kPN / 2) + lt;
+                const int o_other = n0 + static_cast<int>(rank ^ 1) * (kPN / 2) + lt;
+                const T* srow = static_cast<const T*>(a.s16) + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
+                for (int b = 0; b < blocks; ++b, ++lb) {
+                    const int lbuf = lb & 1;
+                    uint4 sv[4], bv[4], bo[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int p = 4 * b + j;
+                        sv[j] = bv[j] = bo[j] = make_uint4(0, 0, 0, 0);
+                        if (p < P) {
+                            const int d = p / chunks, c = p - d * chunks;
+                            const int sl = dlist[d];
+                            if (sl == slot[0]) sv[j] = __ldcg(reinterpret_cast<const uint4*>(srow + c * 8));
+                            const T* Bs = static_cast<const T*>(a.B) + (size_t)sl * a.h_out * a.R + c * 8;
+                            if (o_own < a.h_out) bv[j] = __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)o_own * a.R));
+                            if (o_other < a.h_out) bo[j] = __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)o_other * a.R));
+                        }
+                    }
+                    if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((lb >> 1) & 1) ^ 1, flags))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* blk = lora_sm + lbuf * kPLoraBytes;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (nonfinite8<T>(bv[j]) || nonfinite8<T>(bo[j])) {  // both CTAs see both halves
+                            const int p = 4 * b + j;
+                            atomicOr(&badmap[p >> 5], 1u << (p & 31));
+                            flags[2] = 1;
+                            bv[j] = finite8<T>(bv[j]);
+                        }
+                        *reinterpret_cast<uint4*>(blk + j * kPLoraChunk + lt * 16) = sv[j];
+                        *reinterpret_cast<uint4*>(blk + (4 + j) * kPLoraChunk + lt * 16) = bv[j];
+                    }
+                    fence_proxy_async_smem();  // read by the tensor cores
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(lora_full0 + static_cast<uint32_t>(lbuf) * 8u);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(lora_done);
+            }
+            if (!ok && a.status) report_timeout_status(a.status);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves (or frees tensor memory) while its pair may still use it
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// Pairs the GPU holds at once (an SM left over in a group of SMs cannot host a pair).
+template <typename T>
+static int max_pairs() {
+    static int pairs = 0;
+    if (!pairs) {
+        cudaLaunchConfig_t q;
+        memset(&q, 0, sizeof(q));
+        q.gridDim = dim3(2 * (num_sms() / 2));
+        q.blockDim = dim3(kPThreads);
+        q.dynamicSmemBytes = kPSmem;
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = 2;
+        qa[0].val.clusterDim.y = 1;
+        qa[0].val.clusterDim.z = 1;
+        q.attrs = qa;
+        q.numAttrs = 1;
+        int c = 0;
+        if (cudaOccupancyMaxActiveClusters(&c, (const void*)fp4_pair_kernel<T>, &q) != cudaSuccess || c < 1) {
+            (void)cudaGetLastError();
+            c = num_sms() / 2;
+        }
+        pairs = std::min(c, num_sms() / 2);
+    }
+    return pairs;
+}
+
+template <typename T>
+static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, bool early_w,
+                         const Fp4Lora* lora, cudaStream_t st) {
+    PairArgs a;
+    memset(&a, 0, sizeof(a));
+    a.y = y;
+    a.status = status;
+    a.ldy = ldy;
+    a.n = x.rows;
+    a.h_out = w.rows;
+    a.m_tiles = (x.rows + 2 * kPM - 1) / (2 * kPM);
+    a.n_tiles = (w.rows + kPN - 1) / kPN;
+    a.nkb = x.ktiles / 2;
+    a.kt = x.ktiles;
+    a.early_w = early_w;
+    // rows of y are written 16 bytes at a time when every row starts on a 16-byte boundary
+    a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
+    if (lora) {
+        a.fuse = 1;
+        a.perm = lora->perm;
+        a.idx = lora->idx;
+        a.s16 = lora->s16;
+        a.B = lora->B;
+        a.R = lora->R;
+        a.S = lora->S;
+        a.bf16 = std::is_same<T, __nv_bfloat16>::value;
+    }
+    CUtensorMap mX, mW, mSx, mSw;
+    int rc = make_map_fp4(&mX, x.codes, x.pitch, x.rows, kPM);
+    if (!rc) rc = make_map_fp4(&mW, w.codes, w.pitch, w.rows, kPN / 2);
+    if (!rc) rc = make_map_fp4_scales(&mSx, x.scales, (uint64_t)((x.rows + 127) / 128) * x.ktiles);
+    if (!rc) rc = make_map_fp4_scales(&mSw, w.scales, (uint64_t)((w.rows + 127) / 128) * w.ktiles);
+    if (rc) return rc;
+    static bool attr = false;
+    if (!attr) {
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmem));
+        attr = true;
+    }
+    const int pairs = (int)std::min<long long>((long long)a.m_tiles * a.n_tiles, max_pairs<T>());
+    void* args[] = {(void*)&mX, (void*)&mW, (void*)&mSx, (void*)&mSw, (void*)&a};
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_pair_kernel<T>, dim3(2 * pairs), dim3(kPThreads), kPSmem, st, args));
+    return LORA_OK;
+}
+
+// ============================================================================================
+// before the product: x quantised and the LoRA shrink, one read of x
+// ============================================================================================
+// One CTA per 128 tokens in segment order.  Eight worker warps load the tokens' rows of x, 128
+// columns a step, quantise them from registers (as the quantise kernel does) and write the 16-bit
+// values to shared memory, where the tensor cores multiply them with the A rows of the tile's
+// adapters (TMA): s[t, :] = (alpha / r) x[t] A^T, kept in float32 until the one rounding to the
+// pool's 16-bit type on the way out.  Tiles whose adapters need more than 256 accumulator columns
+// take several passes over K.  With x already stored in 4 bits, the codes and scales are copied
+// instead.  Bound by the read of x; one kernel instead of two reads it once.
+constexpr int kQThreads = 320;  // warp 0: A rows, warp 1: MMAs, warps 2-9: workers
+constexpr uint32_t kQXBytes = 128 * 256, kQABytes = 256 * 256;  // two 64-column swizzled halves each
+constexpr uint32_t kQStageBytes = kQXBytes + kQABytes;
+constexpr size_t kQSmem = 2 * (size_t)kQStageBytes + 1024 + 128 * 4 * 2 + 64 * 8 + 256 * 4 + 256;
+
+struct PrepArgs {
+    PoolView pool;
+    SegView seg;
+    const void* x;
+    Fp4View q;                 // out: rows in segment order
+    const uint8_t* xq_codes;   // x already stored, rows in token order (nullable)
+    const uint8_t* xq_scales;
+    void* s16;                 // out: [n][R]
+    int bf16;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kQThreads, 1)
+fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_align(smem_raw, 1024);
+    int* src_sm = reinterpret_cast<int*>(smem + 2 * kQStageBytes);  // [128] token of each row (-1: none)
+    int* slot_sm = src_sm + 128;                                    // [128]
+    uint32_t* seen = reinterpret_cast<uint32_t*>(slot_sm + 128);    // [64]
+    int* before = reinterpret_cast<int*>(seen + 64);                // [64]
+    int* dlist = before + 64;                                       // [128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(dlist + 256);      // [2] 8 worker warps and the A rows
+    uint64_t* empty = full + 2;                                     // [2]
+    uint64_t* acc_full = empty + 2;
+    uint64_t* acc_free = acc_full + 1;                              // 4 worker warps
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    const int m0 = blockIdx.x * 128;
+    const int R = a.pool.R, h = a.pool.h_in;
+    pdl_wait();
+    pdl_trigger();
+    if (__ldcg(a.seg.status) != LORA_OK) return;  // the product leaves y alone
+
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&full[s], 9);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_free, 4);
+        flags[0] = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tmA);
+    }
+    if (tid < 128) {
+        const int src = m0 + tid < a.seg.n ? __ldcg(a.seg.perm + m0 + tid) : -1;
+        src_sm[tid] = src;
+        slot_sm[tid] = src >= 0 ? __ldcg(a.seg.idx + src) : -1;
+    } else if (tid < 192) {
+        seen[tid - 128] = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 256);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (tid < 128 && slot_sm[tid] >= 0) atomicOr(&seen[slot_sm[tid] >> 5], 1u << (slot_sm[tid] & 31));
+    __syncthreads();
+    if (tid < 64) {
+        int v = 0;
+        for (int w = 0; w < tid; ++w) v += __popc(seen[w]);
+        before[tid] = v;
+        for (uint32_t m = seen[tid]; m; m &= m - 1) dlist[v++] = tid * 32 + __ffs(m) - 1;
+    }
+    __syncthreads();
+    const int D = before[63] + __popc(seen[63]);
+    const int spp = 256 / R;                       // adapters per pass
+    const int passes = (D + spp - 1) / spp;        // 0: no token of the tile has an adapter
+    const int nch = a.q.ktiles;                    // steps of 128 columns
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int p = 0; p < passes && !flags[0]; ++p) {
+                const int d0 = p * spp, dn = min(spp, D - d0);
+                for (int ch = 0; ch < nch; ++ch, ++it) {
+                    const int s = it & 1;
+                    if (it >= 2 && !mbar_wait(&empty[s], ((it >> 1) & 1) ^ 1, flags)) break;
+                    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(dn * R * 256));
+                    uint8_t* As = smem + s * kQStageBytes + kQXBytes;
+                    for (int d = 0; d < dn; ++d)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf)
+                            tma_load_2d_cta(As + hf * (kQABytes / 2) + d * R * 128, &tmA, &full[s], ch * 128 + hf * 64,
+                                            dlist[d0 + d] * R);
+                }
+            }
+            if (flags[0]) {
+                report_timeout_status(a.seg.status);
+                for (int i = max(0, it - 2); i < it; ++i) {
+                    const unsigned long long t0 = globaltimer();
+                    while (!mbar_try_wait(&full[i & 1], (i >> 1) & 1) && globaltimer() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int p = 0; p < passes && ok; ++p) {
+                const int cols = (min(spp, D - p * spp) * R + 15) / 16 * 16;  // 8 more than loaded: not read
+                const uint32_t idesc = idesc_f16(128, cols, a.bf16 != 0);
+                if (p > 0 && !mbar_wait(acc_free, (p - 1) & 1, flags)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int ch = 0; ch < nch; ++ch, ++it) {
+                    const int s = it & 1;
+                    if (!mbar_wait(&full[s], (it >> 1) & 1, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xa = smem_u32(smem + s * kQStageBytes), aa = xa + kQXBytes;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        umma_f16(tmem, sdesc_sw128(xa + (k >> 2) * (kQXBytes / 2) + (k & 3) * 32),
+                                 sdesc_sw128(aa + (k >> 2) * (kQABytes / 2) + (k & 3) * 32), idesc,
+                                 (ch > 0 || k > 0) ? 1u : 0u);
+                    umma_commit(&empty[s]);
+                }
+                umma_commit(acc_full);
+            }
+            if (!ok) {
+                report_timeout_status(a.seg.status);
+                umma_commit(acc_full);
+            }
+        }
+    } else {
+        const int ww = warp - 2, l16 = lane & 15;
+        // this thread's rows: r32 + 32 j2 for two r32 (j & 1) and the four quarters (j >> 1)
+        const int r0 = ww * 4 + (lane >> 4);
+        int src[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) src[j] = src_sm[r0 + 2 * (j & 1) + 32 * (j >> 1)];
+        const T* x = static_cast<const T*>(a.x);
+        auto load = [&](int ch, uint4 (&v)[8]) {
+            const int c = ch * 128 + l16 * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (src[j] >= 0 && c < h) v[j] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src[j] * h + c));
+            }
+        };
+        auto quantise = [&](int ch, const uint4 (&v)[8]) {
+            const int c = ch * 128 + l16 * 8;
+            uint32_t sw[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = r0 + 2 * (j & 1) + 32 * (j >> 1);
+                uint32_t codes, scale;
+                if (a.xq_codes) {
+                    codes = 0;
+                    sw[j] = 0;
+                    if (src[j] >= 0) {
+                        if (c / 32 < a.q.blocks)
+                            codes = __ldg(reinterpret_cast<const uint32_t*>(a.xq_codes + (size_t)src[j] * a.q.pitch + c / 2));
+                        sw[j] = __ldg(reinterpret_cast<const uint32_t*>(
+                            a.xq_scales + ((size_t)(src[j] / 128) * a.q.ktiles + ch) * 512 + (src[j] % 32) * 16 +
+                            (src[j] % 128) / 32 * 4));
+                    }
+                } else {
+                    float f[8];
+                    unpack8<T>(v[j], f);
+                    codes = quantise8(f, scale);
+                    sw[j] = scale_word(scale, lane);
+                }
+                if (m0 + r < a.q.rows && c / 32 < a.q.blocks)
+                    *reinterpret_cast<uint32_t*>(a.q.codes + (size_t)(m0 + r) * a.q.pitch + c / 2) = codes;
+            }
+            if (l16 == 0) {
+                uint8_t* tile = a.q.scales + ((size_t)blockIdx.x * a.q.ktiles + ch) * 512;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4*>(tile + (r0 + 2 * i) * 16) = make_uint4(sw[i], sw[2 + i], sw[4 + i], sw[6 + i]);
+            }
+        };
+        const int rounds = max(passes, 1);  // the first round quantises
+        const int row = (warp & 3) * 32 + lane;
+        const int slot = slot_sm[row];
+        const int dl = slot >= 0 ? before[slot >> 5] + __popc(seen[slot >> 5] & ((1u << (slot & 31)) - 1u)) : -1;
+        const float scale = slot >= 0 ? a.pool.table[slot].scale : 0.f;
+        int it = 0;
+        bool ok = true;
+        for (int p = 0; p < rounds && ok; ++p) {
+            uint4 cur[8], nxt[8];
+            load(0, cur);
+            for (int ch = 0; ch < nch; ++ch, ++it) {
+                if (ch + 1 < nch) load(ch + 1, nxt);
+                if (passes > 0) {
+                    const int s = it & 1;
+                    if (it >= 2 && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((it >> 1) & 1) ^ 1, flags))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* xs = smem + s * kQStageBytes + (l16 >> 3) * (kQXBytes / 2);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = r0 + 2 * (j & 1) + 32 * (j >> 1);
+                        *reinterpret_cast<uint4*>(xs + r * 128 + (((l16 & 7) ^ (r & 7)) << 4)) = cur[j];
+                    }
+                    fence_proxy_async_smem();  // read by the tensor cores
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
+                }
+                if (p == 0) quantise(ch, cur);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
+            }
+            if (passes == 0 || warp >= 6) continue;
+            // ---- the pass's shrink output: thread <-> token row, the columns of its own adapter ----
+            const bool got = __all_sync(0xffffffffu, ok && mbar_wait(acc_full, p & 1, flags));
+            if (!got) break;
+            tc_fence_after();
+            const int d0 = p * spp, dn = min(spp, D - d0);
+            const bool mine = dl >= d0 && dl < d0 + dn;
+            const int col0 = (dl - d0) * R;
+            const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            T* out = static_cast<T*>(a.s16) + (size_t)(m0 + row) * R;
+            for (int c0 = 0; c0 < dn * R; c0 += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_ld16(taddr + c0, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int j = c0 + 8 * hf - col0;
+                    if (mine && j >= 0 && j < R) {
+                        alignas(16) T v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(scale * __uint_as_float(r[8 * hf + e]));
+                        *reinterpret_cast<uint4*>(out + j) = *reinterpret_cast<const uint4*>(v);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free);
+        }
+        if (!ok) report_timeout_status(a.seg.status);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 256);
+}
+
+template <typename T>
+static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
+                            void* s16, cudaStream_t st) {
+    PrepArgs a;
+    a.pool = pv;
+    a.seg = sv;
+    a.x = x;
+    a.q = q;
+    a.xq_codes = xq ? xq->codes : nullptr;
+    a.xq_scales = xq ? xq->scales : nullptr;
+    a.s16 = s16;
+    a.bf16 = std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap mA;
+    const int rc = make_map(&mA, pv.A, a.bf16, pv.h_in, (uint64_t)pv.S * pv.R, pv.R);
+    if (rc) return rc;
+    static bool attr = false;
+    if (!attr) {
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_prepare_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQSmem));
+        attr = true;
+    }
+    void* args[] = {(void*)&mA, (void*)&a};
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_prepare_kernel<T>, dim3((sv.n + 127) / 128), dim3(kQThreads), kQSmem, st,
+                             args));
+    return LORA_OK;
+}
+
+}  // namespace tc
+
+int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
+                       void* s16, cudaStream_t st) {
+    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, s16, st);
+    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, s16, st);
+}
+
+int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
+                    const Fp4Lora* lora, cudaStream_t st) {
+    switch (dtype) {
+        case LORA_F32: return tc::launch_pair_t<float>(x, w, y, ldy, status, early_w, nullptr, st);
+        case LORA_F16: return tc::launch_pair_t<__half>(x, w, y, ldy, status, early_w, lora, st);
+        default: return tc::launch_pair_t<__nv_bfloat16>(x, w, y, ldy, status, early_w, lora, st);
+    }
+}
+
+}  // namespace lora

@@ -29,7 +29,7 @@ struct Fp4GemmArgs {
     const uint8_t* sx;  // scale tiles of x and w
     const uint8_t* sw;
     void* y;
-    const int32_t* status;
+    int32_t* status;
     long long ldy;
     int n, h_out, nkb, ktiles;
     int early_w;
@@ -148,7 +148,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
 }
 
 template <typename T>
-static int launch_fp4_gemm_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, const int32_t* status,
+static int launch_fp4_gemm_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status,
                              bool early_w, cudaStream_t st) {
     Fp4GemmArgs a;
     a.sx = x.scales;
@@ -180,8 +180,9 @@ static int launch_fp4_gemm_t(const Fp4View& x, const Fp4View& w, void* y, long l
 
 }  // namespace tc
 
-int launch_fp4_gemm(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, const int32_t* status,
+int launch_fp4_gemm(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                     bool early_w, cudaStream_t st) {
+    if (x.rows > 256) return launch_fp4_pair(x, w, y, dtype, ldy, status, early_w, nullptr, st);
     switch (dtype) {
         case LORA_F32: return tc::launch_fp4_gemm_t<float>(x, w, y, ldy, status, early_w, st);
         case LORA_F16: return tc::launch_fp4_gemm_t<__half>(x, w, y, ldy, status, early_w, st);
