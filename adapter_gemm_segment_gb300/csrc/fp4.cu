@@ -179,6 +179,12 @@ static int dequantize_t(const Fp4View& q, void* out, long long ld, cudaStream_t 
     return LORA_OK;
 }
 
+static int launch_fp4_product(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
+                              bool early_w, cudaStream_t st) {
+    return x.rows <= 256 ? launch_fp4_decode(x, w, y, dtype, ldy, status, early_w, nullptr, st)
+                         : launch_fp4_pair(x, w, y, dtype, ldy, status, early_w, nullptr, st);
+}
+
 // grid.z counts 128-row tiles
 constexpr int kFp4MaxRows = 65535 * 128;
 
@@ -271,8 +277,8 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
     if (x->cols != w->cols) return set_error(LORA_EINVAL, "x has %d columns, w %d", x->cols, w->cols);
     rc = check_rows(y_dev, dtype, ldy, w->rows ? x->rows : 0, w->rows, "y");
     if (rc || x->rows == 0 || w->rows == 0) return rc;
-    return launch_fp4_gemm(view_of(x), view_of(w), y_dev, dtype, ldy, nullptr, /*early_w=*/false,
-                           static_cast<cudaStream_t>(stream));
+    return launch_fp4_product(view_of(x), view_of(w), y_dev, dtype, ldy, nullptr, /*early_w=*/false,
+                              static_cast<cudaStream_t>(stream));
 }
 
 int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes) {
@@ -332,7 +338,12 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
     int s_parts = 1;
     rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
     if (rc) return rc;
-    rc = launch_fp4_gemm(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
+    if (pv.dtype != LORA_F32) {
+        const Fp4DecodeLora lora = {&pv, sv.idx, s_buf, s_parts};
+        return launch_fp4_decode(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
+    }
+    // float32 pools: the LoRA term in float32, by the expand kernel
+    rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
     if (rc) return rc;
     return launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
 }

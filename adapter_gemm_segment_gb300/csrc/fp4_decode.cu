@@ -1,0 +1,498 @@
+// Batches of up to 256 tokens over a 4-bit base weight.
+//
+// The weight is the MMA's M side (128 features a tile) and the tokens its N side, so the weight
+// streams through once; K is split over the CTAs of a thread-block cluster until the grid fills the
+// GPU.  At 4 bits a 4096 x 4096 weight is 8.9 MB, 1.3 us of HBM time: the call is bound by latency
+// (launch, the first loads, the reduction), so every CTA has its share of the weight in flight
+// before it waits for anything, and the split sums meet in shared memory.
+//
+// The LoRA term is more K blocks of the same accumulator, divided over the cluster's CTAs: for the
+// batch's distinct adapters d, columns d * r_max + j hold B_d[o, j] on the feature side (TMA boxes
+// of 128 rows x 8 columns, which land as the tensor cores take them) and s[t, j] on the token side
+// (zero unless token t uses d; rounded to the pool's 16-bit type here).  An adapter's B rows are
+// thus read once per feature tile, however many tokens use it.  Infinities and NaNs in B are
+// replaced by zeros in the block -- 0 * inf would reach every token -- and added afterwards to the
+// tokens of that adapter alone.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "common.cuh"
+#include "fp4_device.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+#include "tma_host.h"
+
+namespace lora {
+namespace tc {
+
+using namespace ptx;
+
+constexpr int kDM = 128;         // features per tile
+constexpr int kDThreads = 320;   // warp 0 loads, 1 MMAs, 2-5 accumulator, 6-9 LoRA blocks
+constexpr uint32_t kDWBytes = kDM * 128, kDSwBytes = 1024;
+constexpr int kDChunks = 4;      // 8-column chunks per LoRA block
+constexpr int kDScratch = 64 * 4 + 64 * 4 + 256 * 4 + 256 * 4 + 1024;
+constexpr int kDBars = 512;
+
+struct Fp4DecodeArgs {
+    const uint8_t* sx;
+    const uint8_t* sw;
+    void* y;
+    int32_t* status;      // nullable
+    long long ldy;
+    int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, tmem_cols, kt, early_w;
+    // the LoRA term (fuse)
+    int fuse, R, s_parts, bf16;
+    const float* s_in;    // [s_parts][n][R]
+    const int32_t* idx;
+    const void* B;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kDThreads, 1)
+fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                  const __grid_constant__ CUtensorMap tmB, const Fp4DecodeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_align(smem_raw, 1024);
+    const int stages = a.stages, n = a.n, n_pad = a.n_pad;
+    const int xt = n_pad > 128 ? 2 : 1;  // scale tiles of x
+    const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 128;
+    const uint32_t stage_bytes = kDWBytes + kDSwBytes + x_bytes + 1024u * xt;
+    const uint32_t schunk = static_cast<uint32_t>(n_pad) * 16;                 // token side of a chunk
+    const uint32_t lora_bytes = a.fuse ? kDChunks * (2048 + schunk) : 0;
+    uint8_t* lora_sm = smem + (size_t)stages * stage_bytes;                    // [2] {features, tokens}
+    uint32_t* seen = reinterpret_cast<uint32_t*>(lora_sm + 2 * lora_bytes);    // [64]
+    int* before = reinterpret_cast<int*>(seen + 64);                           // [64]
+    int* dlist = before + 64;                                                  // [256]
+    int* slot_sm = dlist + 256;                                                // [256]
+    uint32_t* badmap = reinterpret_cast<uint32_t*>(slot_sm + 256);             // [256]
+    uint64_t* full = reinterpret_cast<uint64_t*>(badmap + 256);
+    uint64_t* empty = full + stages;
+    uint64_t* acc_full = empty + stages;
+    uint64_t* lora_tma = acc_full + 1;    // [2] feature side landed
+    uint64_t* lora_full = lora_tma + 2;   // [2] block complete (4 warps)
+    uint64_t* lora_empty = lora_full + 2; // [2]
+    uint64_t* linfo = lora_empty + 2;     // number of LoRA blocks known
+    uint64_t* lora_done = linfo + 1;      // slots, bad chunks: complete (4 warps)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lora_done + 1);
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort, LoRA blocks, any bad chunk
+    float* P = reinterpret_cast<float*>(smem);  // after the main loop: [n_pad][128] partial sums
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m_tile = blockIdx.x, split = blockIdx.y;
+    const int kb0 = split * a.kb_per_split;
+    const int nkb = min(a.kb_total, kb0 + a.kb_per_split) - kb0;
+    T* y = static_cast<T*>(a.y);
+
+    auto issue_w = [&](int i) {
+        const int s = i % stages;
+        uint8_t* st = smem + (size_t)s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        tma_load_2d_cta(st, &tmW, &full[s], (kb0 + i) * 128, m_tile * kDM);
+        bulk_g2s(st + kDWBytes, a.sw + ((size_t)m_tile * a.kt + 2 * (kb0 + i)) * 512, 1024, &full[s]);
+    };
+    auto issue_x = [&](int i) {
+        const int s = i % stages;
+        uint8_t* st = smem + (size_t)s * stage_bytes + kDWBytes + kDSwBytes;
+        tma_load_2d_cta(st, &tmX, &full[s], (kb0 + i) * 128, 0);
+        for (int h = 0; h < xt; ++h)
+            bulk_g2s(st + x_bytes + h * 1024, a.sx + ((size_t)h * a.kt + 2 * (kb0 + i)) * 512, 1024, &full[s]);
+    };
+    const int pre = min(stages, nkb);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&lora_tma[b], 1);
+            mbar_init(&lora_full[b], 4);
+            mbar_init(&lora_empty[b], 1);
+        }
+        mbar_init(linfo, 1);
+        mbar_init(lora_done, 4);
+        flags[0] = flags[1] = flags[2] = 0;
+        fence_barrier_init();
+        prefetch_tmap(&tmW);
+        prefetch_tmap(&tmX);
+        // the weight is complete when this grid starts behind a kernel that waited for it
+        if (a.early_w)
+            for (int i = 0; i < pre; ++i) issue_w(i);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, a.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();
+            int issued = 0;
+            for (int i = 0; i < nkb; ++i) {
+                const int s = i % stages;
+                if (i >= stages && !mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)) break;
+                if (!a.early_w || i >= pre) issue_w(i);
+                issue_x(i);
+                ++issued;
+            }
+            if (flags[0]) {
+                if (a.status) report_timeout_status(a.status);
+                for (int i = max(0, issued - stages); i < issued; ++i) {
+                    const unsigned long long t0 = globaltimer();
+                    while (!mbar_try_wait(&full[i % stages], (i / stages) & 1) && globaltimer() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            const uint32_t id0 = idesc_mxf4(kDM, n_pad, 0), id2 = idesc_mxf4(kDM, n_pad, 2);
+            for (int i = 0; i < nkb; ++i) {
+                const int s = i % stages;
+                if (!mbar_wait(&full[s], (i / stages) & 1, flags)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t wa = smem_u32(smem + (size_t)s * stage_bytes), sw = wa + kDWBytes;
+                const uint32_t xa = sw + kDSwBytes, sx = xa + x_bytes;
+                // each stage has its own scale columns: w's two tiles (4 each), x's two (8 each)
+                const uint32_t sfw = tmem + static_cast<uint32_t>(n_pad + s * 24), sfx = sfw + 8;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    tmem_cp_scales(sfw + 4 * j, sdesc_scales(sw + 512 * j));
+                    tmem_cp_scales(sfx + 8 * j, sdesc_scales(sx + 512 * j));
+                    if (xt == 2) tmem_cp_scales(sfx + 8 * j + 4, sdesc_scales(sx + 1024 + 512 * j));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_mxf4(tmem, sdesc_sw128(wa + k * 32), sdesc_sw128(xa + k * 32), (k & 1) ? id2 : id0,
+                              sfw + 4 * (k >> 1), sfx + 8 * (k >> 1), (i > 0 || k > 0) ? 1u : 0u);
+                umma_commit(&empty[s]);
+            }
+            if (ok && a.fuse) {
+                ok = mbar_wait(linfo, 0, flags);
+                const int blocks = ok ? flags[1] : 0;
+                const uint32_t idesc_lora = idesc_f16(kDM, n_pad, a.bf16 != 0);
+                for (int b = 0; b < blocks; ++b) {
+                    const int lbuf = b & 1;
+                    if (!mbar_wait(&lora_full[lbuf], (b >> 1) & 1, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t ba = smem_u32(lora_sm + lbuf * lora_bytes), sa = ba + kDChunks * 2048;
+#pragma unroll
+                    for (int k = 0; k < kDChunks / 2; ++k)
+                        umma_f16(tmem, sdesc_chunks(ba + 2 * k * 2048, 2048), sdesc_chunks(sa + 2 * k * schunk, schunk),
+                                 idesc_lora, 1u);
+                    umma_commit(&lora_empty[lbuf]);
+                }
+            }
+            if (!ok && a.status) report_timeout_status(a.status);
+            umma_commit(acc_full);  // also on abort: fires once the issued MMAs have finished
+        }
+    } else if (warp >= 6 && a.fuse) {
+        // ---- LoRA blocks: this CTA's share of the batch's (adapter, 8 columns) chunks ----
+        if constexpr (sizeof(T) == 2) {
+            const int lt = threadIdx.x - 192;
+            const int chunks = a.R / 8;
+            const bool st_ok = __ldcg(a.status) == LORA_OK;  // the segments are older than the kernel ahead
+            if (lt < 64) seen[lt] = 0;
+            for (int i = lt; i < 256; i += 128) {
+                badmap[i] = 0;
+                slot_sm[i] = st_ok && i < n ? __ldcg(a.idx + i) : -1;
+            }
+            named_bar_sync(2, 128);
+            for (int i = lt; i < 256; i += 128)
+                if (slot_sm[i] >= 0) atomicOr(&seen[slot_sm[i] >> 5], 1u << (slot_sm[i] & 31));
+            named_bar_sync(2, 128);
+            if (lt < 32) {
+                const int p0 = __popc(seen[2 * lt]), p1 = __popc(seen[2 * lt + 1]);
+                int v = p0 + p1;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, v, d);
+                    if (lt >= d) v += o;
+                }
+                before[2 * lt] = v - p0 - p1;
+                before[2 * lt + 1] = v - p1;
+            }
+            named_bar_sync(2, 128);
+            if (lt < 64) {
+                int at = before[lt];
+                for (uint32_t m = seen[lt]; m; m &= m - 1) dlist[at++] = lt * 32 + __ffs(m) - 1;
+            }
+            named_bar_sync(2, 128);
+            const int P_all = (before[63] + __popc(seen[63])) * chunks;
+            const int blocks_all = (P_all + kDChunks - 1) / kDChunks;
+            const int blocks = blocks_all > split ? (blocks_all - split - 1) / a.splits + 1 : 0;
+            auto issue_b = [&](int b) {  // the feature side of this CTA's block b
+                const int p0 = (split + b * a.splits) * kDChunks, cnt = min(kDChunks, P_all - p0);
+                uint64_t* bar = &lora_tma[b & 1];
+                mbar_arrive_expect_tx(bar, static_cast<uint32_t>(cnt) * 2048);
+                for (int j = 0; j < cnt; ++j) {
+                    const int d = (p0 + j) / chunks, c = (p0 + j) - d * chunks;
+                    tma_load_3d_cta(lora_sm + (b & 1) * lora_bytes + j * 2048, &tmB, bar, 0, c,
+                                    dlist[d] * a.h_out + m_tile * kDM);
+                }
+            };
+            if (lt == 0) {
+                flags[1] = blocks;
+                mbar_arrive(linfo);
+                for (int b = 0; b < min(blocks, 2); ++b) issue_b(b);
+            }
+            pdl_wait();  // s
+            bool ok = true;
+            for (int b = 0; b < blocks; ++b) {
+                const int lbuf = b & 1, p0 = (split + b * a.splits) * kDChunks;
+                uint8_t* blk = lora_sm + lbuf * lora_bytes;
+                if (b >= 2) {
+                    // the block two before is consumed; its feature side may be overwritten
+                    ok = __all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((b >> 1) & 1) ^ 1, flags));
+                    if (ok && lt == 0) issue_b(b);
+                }
+                // token side: 16 bytes a token and chunk
+                if (ok)
+                    for (int t = lt; t < n_pad; t += 128) {
+                        const int slot = slot_sm[t];
+#pragma unroll
+                        for (int j = 0; j < kDChunks; ++j) {
+                            const int d = (p0 + j) / chunks, c = (p0 + j) - d * chunks;
+                            uint4 v = make_uint4(0, 0, 0, 0);
+                            if (p0 + j < P_all && slot == dlist[d]) {
+                                float s8[8] = {};
+                                for (int k = 0; k < a.s_parts; ++k) {
+                                    const float4* sp = reinterpret_cast<const float4*>(
+                                        a.s_in + ((size_t)k * n + t) * a.R + c * 8);
+                                    const float4 u0 = __ldcg(sp), u1 = __ldcg(sp + 1);
+                                    s8[0] += u0.x, s8[1] += u0.y, s8[2] += u0.z, s8[3] += u0.w;
+                                    s8[4] += u1.x, s8[5] += u1.y, s8[6] += u1.z, s8[7] += u1.w;
+                                }
+                                alignas(16) T h8[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) h8[e] = from_f32<T>(s8[e]);
+                                v = *reinterpret_cast<const uint4*>(h8);
+                            }
+                            *reinterpret_cast<uint4*>(blk + kDChunks * 2048 + j * schunk + t * 16) = v;
+                        }
+                    }
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&lora_tma[lbuf], (b >> 1) & 1, flags));
+                if (!ok) break;
+#pragma unroll
+                for (int j = 0; j < kDChunks; ++j) {
+                    uint4* bp = reinterpret_cast<uint4*>(blk + j * 2048 + lt * 16);
+                    if (p0 + j >= P_all) {
+                        *bp = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint4 v = *bp;
+                        if (nonfinite8<T>(v)) {
+                            *bp = finite8<T>(v);
+                            atomicOr(&badmap[(p0 + j) >> 5], 1u << ((p0 + j) & 31));
+                            flags[2] = 1;
+                        }
+                    }
+                }
+                fence_proxy_async_smem();  // read by the tensor cores
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&lora_full[lbuf]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(lora_done);
+            if (!ok) {
+                if (a.status) report_timeout_status(a.status);
+                // boxes in flight land before the CTA leaves
+                if (lt == 0)
+                    for (int b = 0; b < 2; ++b) {
+                        const unsigned long long t0 = globaltimer();
+                        while (!mbar_try_wait(&lora_tma[b], 0) && globaltimer() - t0 < kWaitLimitNs) {
+                        }
+                    }
+            }
+        }
+    }
+
+    bool store = false;
+    if (warp >= 2) {
+        pdl_wait();
+        store = !a.status || __ldcg(a.status) == LORA_OK;
+    }
+    if (warp >= 2 && warp < 6) {
+        const int row = (warp & 3) * 32 + lane, o = m_tile * kDM + row;
+        const bool got = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, flags) && (!a.fuse || mbar_wait(lora_done, 0, flags)));
+        if (got) {
+            tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            for (int c0 = 0; c0 < n_pad; c0 += 16) {
+                uint32_t r[16];
+                __syncwarp();
+                tmem_ld16(taddr + c0, r);
+                tmem_ld_wait();
+                if constexpr (sizeof(T) == 2) {
+                    if (a.fuse && flags[2] && o < a.h_out) {  // elements of B left out of the blocks
+                        const int chunks = a.R / 8;
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const int t = c0 + c, slot = t < n ? slot_sm[t] : -1;
+                            if (slot < 0) continue;
+                            const int w = slot >> 5;
+                            const int d = before[w] + __popc(seen[w] & ((1u << (slot & 31)) - 1u));
+                            for (int k8 = 0; k8 < chunks; ++k8) {
+                                const int p = d * chunks + k8;
+                                if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
+                                alignas(16) T h8[8];
+                                for (int e = 0; e < 8; ++e) {
+                                    float v = 0.f;
+                                    for (int k = 0; k < a.s_parts; ++k)
+                                        v += __ldcg(a.s_in + ((size_t)k * n + t) * a.R + k8 * 8 + e);
+                                    h8[e] = from_f32<T>(v);
+                                }
+                                const uint4 bv = __ldg(reinterpret_cast<const uint4*>(
+                                    static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + o) * a.R + k8 * 8));
+                                r[c] = __float_as_uint(nonfinite_dot8<T>(bv, *reinterpret_cast<const uint4*>(h8),
+                                                                         __uint_as_float(r[c])));
+                            }
+                        }
+                    }
+                }
+                if (a.splits == 1) {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (store && c0 + c < n && o < a.h_out)
+                            y[(long long)(c0 + c) * a.ldy + o] = from_f32<T>(__uint_as_float(r[c]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
+                }
+            }
+        } else if (lane == 0) {
+            flags[0] = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (a.splits > 1) {
+        // each CTA adds up the partial sums of its share of the tokens, in split order
+        const bool good = flags[0] == 0;
+        cluster_sync();
+        if (warp >= 2 && good && store) {
+            const int rt = threadIdx.x - 64, row = rt & 127, o = m_tile * kDM + row;
+            const int per = (n + a.splits - 1) / a.splits;
+            const int t_end = min(n, (split + 1) * per);
+            for (int t0 = split * per + (rt >> 7); t0 < t_end; t0 += 16) {
+                float v[8] = {};
+                for (int c = 0; c < a.splits; ++c) {
+                    const uint32_t base = mapa_shared(smem_u32(P + row), static_cast<uint32_t>(c));
+                    float u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = t0 + 2 * i < t_end ? ld_dsmem_f32(base + (t0 + 2 * i) * (kDM * 4)) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] += u[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (t0 + 2 * i < t_end && o < a.h_out) y[(long long)(t0 + 2 * i) * a.ldy + o] = from_f32<T>(v[i]);
+            }
+        }
+        cluster_sync();  // no CTA leaves while its partial sums may still be read
+    }
+    if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
+}
+
+template <typename T>
+static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, bool early_w,
+                               const Fp4DecodeLora* lora, cudaStream_t st) {
+    Fp4DecodeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.sx = x.scales;
+    a.sw = w.scales;
+    a.y = y;
+    a.status = status;
+    a.ldy = ldy;
+    a.n = x.rows;
+    a.n_pad = (x.rows + 15) / 16 * 16;
+    a.h_out = w.rows;
+    a.kt = x.ktiles;
+    a.kb_total = x.ktiles / 2;
+    a.early_w = early_w;
+    const int m_tiles = (w.rows + kDM - 1) / kDM;
+    int splits = std::max(1, num_sms() / m_tiles);
+    splits = std::min({splits, 8, a.kb_total});
+    a.kb_per_split = (a.kb_total + splits - 1) / splits;
+    a.splits = (a.kb_total + a.kb_per_split - 1) / a.kb_per_split;
+    PoolView pv;
+    if (lora) {
+        pv = *lora->pool;
+        a.fuse = 1;
+        a.R = pv.R;
+        a.s_parts = lora->s_parts;
+        a.bf16 = pv.dtype == LORA_BF16;
+        a.s_in = lora->s_in;
+        a.idx = lora->idx;
+        a.B = pv.B;
+    }
+    const size_t stage_bytes = kDWBytes + kDSwBytes + (size_t)a.n_pad * 128 + (a.n_pad > 128 ? 2048 : 1024);
+    const size_t fixed = (lora ? 2 * (size_t)kDChunks * (2048 + a.n_pad * 16) : 0) + kDScratch + kDBars + 1024;
+    const size_t park = a.splits > 1 ? (size_t)a.n_pad * kDM * 4 : 0;
+    int stages = (int)((227 * 1024 - fixed) / stage_bytes);
+    stages = std::min({stages, 8, a.kb_per_split});
+    while ((size_t)stages * stage_bytes < park) ++stages;  // (park is at most 128 KB, 2.5 stages of its size)
+    a.stages = stages;
+    int cols = 32;
+    while (cols < a.n_pad + 24 * stages) cols <<= 1;
+    a.tmem_cols = cols;
+    const size_t smem = (size_t)stages * stage_bytes + fixed;
+    if (smem > 227 * 1024 || cols > 512) return set_error(LORA_EUNSUP, "internal: 4-bit decode plan");
+    CUtensorMap mX, mW, mB;
+    int rc = make_map_fp4(&mX, x.codes, x.pitch, x.rows, a.n_pad);
+    if (!rc) rc = make_map_fp4(&mW, w.codes, w.pitch, w.rows, kDM);
+    if (!rc && lora) rc = make_map_bchunks(&mB, pv.B, a.bf16, pv.R, (uint64_t)pv.S * pv.h_out);
+    if (rc) return rc;
+    if (!lora) mB = mW;  // not used
+    static bool attr_set = false;
+    if (!attr_set) {
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+        attr_set = true;
+    }
+    void* args[] = {(void*)&mW, (void*)&mX, (void*)&mB, (void*)&a};
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(m_tiles, a.splits);
+    cfg.blockDim = dim3(kDThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = a.splits;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    LORA_CUDA_TRY(cudaLaunchKernelExC(&cfg, (const void*)fp4_decode_kernel<T>, args));
+    count_launch();
+    return LORA_OK;
+}
+
+}  // namespace tc
+
+int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
+                      bool early_w, const Fp4DecodeLora* lora, cudaStream_t st) {
+    switch (dtype) {
+        case LORA_F32: return tc::launch_fp4_decode_t<float>(x, w, y, ldy, status, early_w, nullptr, st);
+        case LORA_F16: return tc::launch_fp4_decode_t<__half>(x, w, y, ldy, status, early_w, lora, st);
+        default: return tc::launch_fp4_decode_t<__nv_bfloat16>(x, w, y, ldy, status, early_w, lora, st);
+    }
+}
+
+}  // namespace lora

@@ -103,7 +103,7 @@ inline size_t fp4_scales_bytes(int rows, int cols) {
 int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q, cudaStream_t st);
 // y = x w^T (dtype, row stride ldy).  status: nullable device word; y stays untouched unless it is
 // LORA_OK.  early_w: every kernel that could have written w has completed when this grid starts.
-// lora (nullable, 16-bit y): the LoRA term, with x's rows in the order of perm.
+// lora (nullable, 16-bit y): the LoRA term, for launch_fp4_pair with x's rows in the order of perm.
 struct Fp4Lora {
     const int32_t* perm;  // token of each row of x
     const int32_t* idx;   // slot of each token
@@ -111,8 +111,16 @@ struct Fp4Lora {
     const void* B;
     int R, S;
 };
-int launch_fp4_gemm(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
-                    bool early_w, cudaStream_t st);
+// Up to 256 tokens.  lora: the pool, the slot of each token and the shrink output in K parts.
+struct Fp4DecodeLora {
+    const PoolView* pool;
+    const int32_t* idx;
+    const float* s_in;
+    int s_parts;
+};
+int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
+                      bool early_w, const Fp4DecodeLora* lora, cudaStream_t st);
+// More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
 // Quantises x (or copies xq) into q and writes the shrink output to s16 [n][R] (16-bit), rows of
