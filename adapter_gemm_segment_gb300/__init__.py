@@ -202,8 +202,16 @@ def _check(rc: int) -> None:
         raise LoraError(rc, lora_last_error())
 
 
+# torch.cuda.current_stream() builds a Stream object, 3 us of host time a call; its handle alone is
+# what the library takes.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _raw_stream is not None and _cur_device is not None and torch.cuda.is_initialized():
+            return ctypes.c_void_p(_raw_stream(_cur_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -578,38 +586,43 @@ class Fp4Matrix:
 
 def _fp4_rows(t: torch.Tensor, rows: int, cols: int, name: str):
     """dtype code and row stride of a CUDA tensor [rows, cols] whose rows are contiguous."""
+    dt = TORCH_TO_LORA.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in TORCH_TO_LORA:
-        raise ValueError(f"{name} must be float32, float16 or bfloat16")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape [{rows}, {cols}]")
-    if cols > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return dt, cols
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if rows <= 1:
+        return dt, cols
     if ld < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return TORCH_TO_LORA[t.dtype], ld
+    return dt, ld
 
 
 def lora_fp4_quantize(x: torch.Tensor, out: Fp4Matrix, stream=None) -> Fp4Matrix:
     """Quantise x [rows, cols] (contiguous rows, any row stride) into out."""
     dt, ld = _fp4_rows(x, out.rows, out.cols, "x")
-    _check(_lib.lora_fp4_quantize(_ptr(x), dt, ld, ctypes.byref(out.struct), _stream(stream)))
+    _check(_lib.lora_fp4_quantize(x.data_ptr(), dt, ld, ctypes.byref(out.struct), _stream(stream)))
     return out
 
 
 def lora_fp4_dequantize(q: Fp4Matrix, out: torch.Tensor, stream=None) -> torch.Tensor:
     """Read q back into out [rows, cols] (contiguous rows, any row stride)."""
     dt, ld = _fp4_rows(out, q.rows, q.cols, "out")
-    _check(_lib.lora_fp4_dequantize(ctypes.byref(q.struct), _ptr(out), dt, ld, _stream(stream)))
+    _check(_lib.lora_fp4_dequantize(ctypes.byref(q.struct), out.data_ptr(), dt, ld, _stream(stream)))
     return out
 
 
 def lora_fp4_matmul(x: Fp4Matrix, w: Fp4Matrix, y: torch.Tensor, stream=None) -> torch.Tensor:
     """y [x.rows, w.rows] = x w^T of two stored matrices (y: contiguous rows, any row stride)."""
     dt, ld = _fp4_rows(y, x.rows, w.rows, "y")
-    _check(_lib.lora_fp4_matmul(ctypes.byref(x.struct), ctypes.byref(w.struct), _ptr(y), dt, ld, _stream(stream)))
+    _check(_lib.lora_fp4_matmul(ctypes.byref(x.struct), ctypes.byref(w.struct), y.data_ptr(), dt, ld, _stream(stream)))
     return y
 
 
@@ -623,9 +636,9 @@ def lora_fp4_linear_fwd(pool_handle, w: Fp4Matrix, x: torch.Tensor, y: torch.Ten
                         ws: torch.Tensor, xq: Optional[Fp4Matrix] = None, stream=None) -> torch.Tensor:
     """lora_linear_fwd over a 4-bit base weight; xq: the stored form of x, where another projection
     of the same x has made it already (it is made in the workspace otherwise)."""
-    _check(_lib.lora_fp4_linear_fwd(pool_handle, ctypes.byref(w.struct), _ptr(_dev(x, "x")),
-                                    None if xq is None else ctypes.byref(xq.struct), _ptr(_dev(y, "y")),
-                                    ctypes.byref(seg), _ptr(_dev(ws, "ws")), ws.numel() * ws.element_size(),
+    _check(_lib.lora_fp4_linear_fwd(pool_handle, ctypes.byref(w.struct), _dev(x, "x").data_ptr(),
+                                    None if xq is None else ctypes.byref(xq.struct), _dev(y, "y").data_ptr(),
+                                    ctypes.byref(seg), _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size(),
                                     _stream(stream)))
     return y
 

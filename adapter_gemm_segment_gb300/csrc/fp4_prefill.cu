@@ -29,10 +29,14 @@ using namespace ptx;
 // M = 256 x N = 256 MMAs that read both halves, and each CTA's tensor memory receives its 128
 // tokens x 256 features.
 //
-// Tensor memory (512 columns): two accumulators of 256 columns that share 48 of them ([0, 256) and
-// [208, 464)), and two sets of 24 scale columns.  The main loop of the next tile may start once the
-// epilogue has taken those 48 columns, which it takes first.  A set of scale columns is rewritten
-// (tcgen05.cp) only after the MMAs of the step two before have completed.
+// Block scales reach tensor memory through registers: four warps read a step's 3 KB from shared
+// memory and store it to their 32 lanes (tcgen05.st).  Copying it there by tcgen05.cp from the
+// thread that issues the MMAs takes the tensor pipe 64 clocks for each 512 bytes, measured: 815
+// clocks a step of four MMAs and six copies against 512 for the MMAs alone.
+//
+// Tensor memory (512 columns): two accumulators of 256 columns that share 96 of them ([0, 256) and
+// [160, 416)), and four sets of 24 scale columns.  The main loop of the next tile may start once
+// the epilogue has taken the shared columns, which it takes first.
 //
 // The LoRA term is more K blocks of the same accumulator: for the distinct adapters d of the pair's
 // 256 tokens, columns d * r_max + j hold s[t, j] on the token side (zero unless t uses d; s is
@@ -41,23 +45,32 @@ using namespace ptx;
 // infinity or NaN in one tenant's B would reach the other tenants' rows as 0 * inf: such elements
 // are replaced by zeros here and the epilogue adds them to their own tokens alone.
 //
-// Warps: 0 loads, 1 issues MMAs (even CTA), 2-5 drain the accumulator, 6-9 build the LoRA blocks.
+// Warps: 0 loads codes, 1 issues MMAs (even CTA), 2-9 drain the accumulator, 10-13 build the LoRA
+// blocks, 14-17 bring in the scales.
 constexpr int kPM = 128;         // token rows per CTA
 constexpr int kPN = 256;         // features per pair tile
-constexpr int kPThreads = 320;
-constexpr int kPStages = 5;
+constexpr int kPThreads = 576;
 constexpr uint32_t kPXBytes = kPM * 128, kPWBytes = (kPN / 2) * 128;
-constexpr uint32_t kPSxBytes = 1024, kPSwBytes = 2048;
-constexpr uint32_t kPStageBytes = kPXBytes + kPWBytes + kPSxBytes + kPSwBytes;
-constexpr int kPAcc1 = 208;                         // first column of the second accumulator
-constexpr int kPScaleCol = 464;                     // first column of the scale sets (24 each)
+constexpr uint32_t kPStageBytes = kPXBytes + kPWBytes;
+constexpr int kPMaxStages = 6;
+constexpr int kPScaleSlots = 5;                     // shared-memory slots of scales: 1 KB of x, 2 KB of w
+constexpr uint32_t kPScaleBytes = 3072;
+constexpr int kPScaleSets = 4;                      // tensor-memory sets of 24 columns
+constexpr int kPScaleCol = 512 - 24 * kPScaleSets;
+constexpr int kPAcc1 = kPScaleCol - kPN;            // first column of the second accumulator
 constexpr int kPLoraChunk = kPM * 16;               // 8 columns of 128 rows, 16 bytes a row
 constexpr int kPLoraBytes = 2 * 4 * kPLoraChunk;    // one block: 4 chunks on each side
-constexpr int kPStageOut = 4 * 32 * 64 * 2;         // y staging: 32 rows x 64 16-bit columns a warp
 constexpr int kPScratch = 64 * 4 + 64 * 4 + 256 * 4 + 1024;
-constexpr size_t kPSmem = (size_t)kPStages * kPStageBytes + 2 * kPLoraBytes + kPStageOut + kPScratch + 256 + 1024;
-static_assert(kPSmem <= 227 * 1024, "shared memory of the pair kernel");
-static_assert(kPStageBytes % 1024 == 0, "swizzle atoms stay aligned");
+// after the stages: scales, LoRA blocks (if any), y staging (8 warps of 32 rows x 32 columns), the
+// LoRA scratch, barriers
+constexpr size_t pair_smem(int stages, bool fuse, size_t elt) {
+    return (size_t)stages * kPStageBytes + kPScaleSlots * kPScaleBytes + (fuse ? 2 * kPLoraBytes : 0) + 8 * 1024 * elt +
+           kPScratch + 256 + 1024;
+}
+constexpr size_t kSmemMax = 227 * 1024;
+static_assert(kPAcc1 >= kPN - 128, "the shared columns are within the first 128 the epilogue takes");
+static_assert(pair_smem(5, true, 2) <= kSmemMax && pair_smem(6, false, 2) <= kSmemMax && pair_smem(5, false, 4) <= kSmemMax,
+              "shared memory of the pair kernel");
 
 struct PairArgs {
     void* y;
@@ -66,35 +79,51 @@ struct PairArgs {
     const int32_t* idx;      // fuse: adapter slot by original token
     const void* s16;         // fuse: [n][R] shrink output in token-row order, 16-bit
     const void* B;           // fuse: pool's B slab
+    const uint8_t* sx;       // scale tiles of x and w
+    const uint8_t* sw;
     long long ldy;
-    int n, h_out, m_tiles, n_tiles, nkb, kt;
+    int n, h_out, m_tiles, n_tiles, nkb, kt, stages;
     int R, S, fuse, bf16, early_w, vec;
+};
+
+// A ring position: index and parity of its current use.
+struct Ring {
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
 };
 
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
-fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                const __grid_constant__ CUtensorMap tmSx, const __grid_constant__ CUtensorMap tmSw, const PairArgs a) {
+fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const PairArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
-    uint8_t* lora_sm = smem + kPStages * kPStageBytes;      // [2] blocks {token side, feature side}
-    uint8_t* yst = lora_sm + 2 * kPLoraBytes;               // [4 warps][32 rows][64] (f32: spills into lora_sm's room)
-    uint32_t* seen = reinterpret_cast<uint32_t*>(yst + kPStageOut);  // [64] slots the tile's tokens name
-    int* before = reinterpret_cast<int*>(seen + 64);        // [64] named slots below each word
-    int* dlist = before + 64;                               // [256] the tile's slots in order
-    uint32_t* badmap = reinterpret_cast<uint32_t*>(dlist + 256);  // [256] LoRA chunks with a non-finite B
-    uint64_t* full = reinterpret_cast<uint64_t*>(badmap + 256);   // even CTA: both halves of a stage
-    uint64_t* empty = full + kPStages;       // the even CTA's commits (multicast)
-    uint64_t* acc_full = empty + kPStages;   // [2] (multicast)
-    uint64_t* ov_free = acc_full + 2;        // even CTA: the shared columns are drained (8 warps)
+    const int stages = a.stages;
+    uint8_t* scale_sm = smem + stages * kPStageBytes;
+    uint8_t* lora_sm = scale_sm + kPScaleSlots * kPScaleBytes;   // [2] blocks {token side, feature side}
+    uint8_t* yst = lora_sm + (a.fuse ? 2 * kPLoraBytes : 0);     // [8 warps][32 rows][32]
+    uint32_t* seen = reinterpret_cast<uint32_t*>(yst + 8 * 1024 * sizeof(T));  // [64] slots the tile's tokens name
+    int* before = reinterpret_cast<int*>(seen + 64);             // [64] named slots below each word
+    int* dlist = before + 64;                                    // [256] the tile's slots in order
+    uint32_t* badmap = reinterpret_cast<uint32_t*>(dlist + 256); // [256] LoRA chunks with a non-finite B
+    uint64_t* full = reinterpret_cast<uint64_t*>(badmap + 256);  // even CTA: codes of both halves, 8 scale warps
+    uint64_t* empty = full + kPMaxStages;    // the even CTA's commits (multicast)
+    uint64_t* acc_full = empty + kPMaxStages;  // [2] (multicast)
+    uint64_t* ov_free = acc_full + 2;        // even CTA: the shared columns are drained (16 warps)
     uint64_t* lora_full = ov_free + 1;       // [2] even CTA: a LoRA block is written (8 warps)
     uint64_t* lora_empty = lora_full + 2;    // [2] (multicast)
     uint64_t* linfo = lora_empty + 2;        // even CTA: the tile's number of LoRA blocks is known
-    uint64_t* epi_done = linfo + 1;          // the epilogue is through with a tile (4 warps)
+    uint64_t* epi_done = linfo + 1;          // the epilogue is through with a tile (8 warps)
     uint64_t* lora_done = epi_done + 1;      // the tile's LoRA scratch is complete (4 warps)
     uint64_t* drained = lora_done + 1;       // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort, LoRA blocks, any bad chunk
+    static_assert((2 * kPMaxStages + 11) * 8 + 16 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -103,8 +132,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     const int nkb = a.nkb;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPStages; ++s) {
-            mbar_init(&full[s], 1);
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&full[s], 9);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -112,9 +141,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             mbar_init(&lora_full[b], 8);
             mbar_init(&lora_empty[b], 1);
         }
-        mbar_init(ov_free, 8);
+        mbar_init(ov_free, 16);
         mbar_init(linfo, 1);
-        mbar_init(epi_done, 4);
+        mbar_init(epi_done, 8);
         mbar_init(lora_done, 4);
         mbar_init(drained, 1);
         flags[0] = flags[1] = flags[2] = 0;
@@ -123,8 +152,6 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     if (warp == 0 && lane == 0) {
         prefetch_tmap(&tmX);
         prefetch_tmap(&tmW);
-        prefetch_tmap(&tmSx);
-        prefetch_tmap(&tmSw);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -140,46 +167,38 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     if (warp == 0) {
         if (lane == 0) {
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-            auto load = [&](int s, const CUtensorMap* m, uint32_t off, int c0, int c1) {
-                tma_load_2d_pair(smem + s * kPStageBytes + off, m, full0 + static_cast<uint32_t>(s) * 8u, c0, c1);
-            };
             auto load_w = [&](int s, int kb, int n0) {
                 if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPStageBytes);
-                load(s, &tmW, kPXBytes, kb * 128, n0 + static_cast<int>(rank) * (kPN / 2));
-                const int rt = n0 / 128;
-                load(s, &tmSw, kPXBytes + kPWBytes + kPSxBytes, 0, rt * a.kt + 2 * kb);
-                load(s, &tmSw, kPXBytes + kPWBytes + kPSxBytes + 1024, 0, (rt + 1) * a.kt + 2 * kb);
+                tma_load_2d_pair(smem + s * kPStageBytes + kPXBytes, &tmW, full0 + static_cast<uint32_t>(s) * 8u, kb * 128,
+                                 n0 + static_cast<int>(rank) * (kPN / 2));
             };
             auto load_x = [&](int s, int kb, int m0) {
-                const int row = m0 + static_cast<int>(rank) * kPM;
-                load(s, &tmX, 0, kb * 128, row);
-                load(s, &tmSx, kPXBytes + kPWBytes, 0, row / 128 * a.kt + 2 * kb);
+                tma_load_2d_pair(smem + s * kPStageBytes, &tmX, full0 + static_cast<uint32_t>(s) * 8u, kb * 128,
+                                 m0 + static_cast<int>(rank) * kPM);
             };
             // the first tile's weight boxes go out before the kernels ahead have finished
             int pre = 0;
             if (a.early_w && pair < total) {
-                pre = min(kPStages, nkb);
+                pre = min(stages, nkb);
                 for (int i = 0; i < pre; ++i) load_w(i, i, pair % a.n_tiles * kPN);
             }
             pdl_wait();
             int it = 0;
+            Ring r;
             for (int tile = pair; tile < total && !flags[0]; tile += npairs) {
                 const int m0 = tile / a.n_tiles * 2 * kPM, n0 = tile % a.n_tiles * kPN;
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = it % kPStages;
-                    if (it >= kPStages && !mbar_wait(&empty[s], ((it / kPStages) & 1) ^ 1, flags)) break;
-                    if (it >= pre) load_w(s, kb, n0);
-                    load_x(s, kb, m0);
+                for (int kb = 0; kb < nkb; ++kb, ++it, r.next(stages)) {
+                    if (it >= stages && !mbar_wait(&empty[r.i], r.ph ^ 1, flags)) break;
+                    if (it >= pre) load_w(r.i, kb, n0);
+                    load_x(r.i, kb, m0);
                 }
             }
-            // aborted: the even CTA lets every copy in flight (counted on its barriers) land
-            if (flags[0]) {
+            if (flags[0]) {  // aborted: give the copies in flight (both CTAs') time to land
                 if (a.status) report_timeout_status(a.status);
                 if (rank == 0)
-                    for (int i = max(0, it - kPStages); i < it; ++i) {
+                    for (int i = 0; i < stages; ++i) {
                         const unsigned long long t0 = globaltimer();
-                        while (!mbar_try_wait(&full[i % kPStages], (i / kPStages) & 1) &&
-                               globaltimer() - t0 < kWaitLimitNs) {
+                        while (!mbar_try_wait(&full[i], 0) && globaltimer() - t0 < kWaitLimitNs / 8) {
                         }
                     }
             }
@@ -188,40 +207,31 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         if (lane == 0 && rank == 0) {
             const uint32_t idesc_lora = idesc_f16(2 * kPM, kPN, a.bf16 != 0);
             int it = 0, local = 0, lb = 0;
+            Ring r;
             bool ok = true;
             for (int tile = pair; tile < total && ok; tile += npairs, ++local) {
                 const int buf = local & 1;
                 const uint32_t acc = tmem + buf * kPAcc1;
                 // the tile before has left the columns both accumulators share (and, the epilogue
                 // taking tiles in order, the one before that has left this accumulator)
-                if (local > 0 && !mbar_wait_cluster(ov_free, (local - 1) & 1, flags)) {
+                if (local > 0 && !mbar_wait(ov_free, (local - 1) & 1, flags)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                for (int kb = 0; kb < nkb; ++kb, ++it) {
-                    const int s = it % kPStages;
-                    if (!mbar_wait(&full[s], (it / kPStages) & 1, flags) ||
-                        // the scale columns' last readers
-                        (it >= 2 && !mbar_wait(&empty[(it - 2) % kPStages], ((it - 2) / kPStages) & 1, flags))) {
+                for (int kb = 0; kb < nkb; ++kb, ++it, r.next(stages)) {
+                    if (!mbar_wait(&full[r.i], r.ph, flags)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t xa = smem_u32(smem + s * kPStageBytes), wa = xa + kPXBytes, sc = wa + kPWBytes;
-                    const uint32_t sfa = tmem + kPScaleCol + (it & 1) * 24, sfb = sfa + 8;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        tmem_cp_scales_pair(sfa + 4 * j, sdesc_scales(sc + 512 * j));
-                        tmem_cp_scales_pair(sfb + 8 * j, sdesc_scales(sc + kPSxBytes + 512 * j));
-                        tmem_cp_scales_pair(sfb + 8 * j + 4, sdesc_scales(sc + kPSxBytes + 1024 + 512 * j));
-                    }
+                    const uint64_t xd = sdesc_sw128(smem_u32(smem + r.i * kPStageBytes));
+                    const uint64_t wd = xd + (kPXBytes >> 4);
+                    const uint32_t sfa = tmem + kPScaleCol + (it % kPScaleSets) * 24, sfb = sfa + 8;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        umma_pair_mxf4(acc, sdesc_sw128(xa + k * 32), sdesc_sw128(wa + k * 32),
-                                       idesc_mxf4(2 * kPM, kPN, (k & 1) * 2), sfa + 4 * (k >> 1), sfb + 8 * (k >> 1),
-                                       (kb > 0 || k > 0) ? 1u : 0u);
-                    umma_pair_commit(&empty[s], 0x3);
+                        umma_pair_mxf4(acc, xd + 2 * k, wd + 2 * k, idesc_mxf4(2 * kPM, kPN, (k & 1) * 2),
+                                       sfa + 4 * (k >> 1), sfb + 8 * (k >> 1), (kb > 0 || k > 0) ? 1u : 0u);
+                    umma_pair_commit(&empty[r.i], 0x3);
                 }
                 if (!ok) break;
                 if (a.fuse) {
@@ -255,11 +265,12 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kWaitLimitNs) {
             }
         }
-    } else if (warp < 6) {
-        // ---- epilogue: thread <-> token row (TMEM lane) of this CTA's half, 64 features a round ----
-        const int q = warp & 3;
-        constexpr int kCh = 64 * sizeof(T) / 16;  // 16-byte pieces of a staged row
-        uint8_t* ys = sizeof(T) == 2 ? yst + q * (32 * 64 * 2) : lora_sm + q * (32 * 64 * 4);  // f32 never fuses
+    } else if (warp < 10) {
+        // ---- epilogue: thread <-> token row (TMEM lane) of this CTA's half; two warps share a row,
+        // taking alternate pieces of 32 features ----
+        const int q = warp & 3, hv = (warp - 2) >> 2;
+        constexpr int kCh = 32 * sizeof(T) / 16;  // 16-byte pieces of a staged row
+        uint8_t* ys = yst + (warp - 2) * (1024 * sizeof(T));
         const uint32_t ov_free0 = mapa_shared(smem_u32(ov_free), 0);
         pdl_wait();
         const int status = a.status ? __ldcg(a.status) : LORA_OK;
@@ -277,69 +288,82 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const bool any_bad = a.fuse && flags[2] != 0;
             const int slot = any_bad && yrow >= 0 && status == LORA_OK ? __ldcg(a.idx + yrow) : -1;
             const uint32_t taddr = tmem + buf * kPAcc1 + (static_cast<uint32_t>(q * 32) << 16);
-            for (int u = 0; u < 4; ++u) {
-                const int c0 = (buf == 0 ? 3 - u : u) * 64;  // the shared columns first
-                uint32_t r[64];
+            uint32_t r[2][32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // this warp's two pieces of each half of the columns, those both accumulators share first
+                int cc[2];
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_ld16(taddr + c0 + 16 * i, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * i]));
+                for (int i = 0; i < 2; ++i) {
+                    const int pos = 4 * half + 2 * i + hv;
+                    cc[i] = (buf == 0 ? 7 - pos : pos) * 32;
+                    tmem_ld16(taddr + cc[i], *reinterpret_cast<uint32_t(*)[16]>(&r[i][0]));
+                    tmem_ld16(taddr + cc[i] + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[i][16]));
+                }
                 tmem_ld_wait();
-                if (u == 0) {
+                if (half == 0) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(ov_free0);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(ov_free0);
                 }
-                if (n0 + c0 >= a.h_out || status != LORA_OK) continue;
-                if constexpr (sizeof(T) == 2) {
-                    if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
-                        const int w = slot >> 5;
-                        const int d = before[w] + __popc(seen[w] & ((1u << (slot & 31)) - 1u));
-                        const int chunks = a.R / 8;
-                        for (int c = 0; c < chunks; ++c) {
-                            const int p = d * chunks + c;
-                            if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
-                            const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
-                                                                                   (size_t)row * a.R + c * 8));
-                            const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + n0 + c0) * a.R + c * 8;
+                if (status != LORA_OK) continue;
 #pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (n0 + c0 + i < a.h_out)
-                                    r[i] = __float_as_uint(
-                                        nonfinite_dot8<T>(__ldg(reinterpret_cast<const uint4*>(Bs + (size_t)i * a.R)), sv,
-                                                          __uint_as_float(r[i])));
+                for (int i = 0; i < 2; ++i) {
+                    const int c0 = n0 + cc[i];
+                    if (c0 >= a.h_out) continue;
+                    if constexpr (sizeof(T) == 2) {
+                        if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
+                            const int w = slot >> 5;
+                            const int d = before[w] + __popc(seen[w] & ((1u << (slot & 31)) - 1u));
+                            const int chunks = a.R / 8;
+                            for (int c = 0; c < chunks; ++c) {
+                                const int p = d * chunks + c;
+                                if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
+                                const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
+                                                                                       (size_t)row * a.R + c * 8));
+                                const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0) * a.R + c * 8;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (c0 + e < a.h_out)
+                                        r[i][e] = __float_as_uint(nonfinite_dot8<T>(
+                                            __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)e * a.R)), sv,
+                                            __uint_as_float(r[i][e])));
+                            }
                         }
                     }
-                }
-                // through shared memory (16-byte pieces permuted by row), so that eight lanes write
-                // 128 consecutive bytes of a row of y
-                __syncwarp();
+                    // through shared memory (16-byte pieces permuted by row), so that neighbouring lanes
+                    // write neighbouring bytes of a row of y
+                    __syncwarp();
 #pragma unroll
-                for (int c = 0; c < kCh; ++c) {
-                    constexpr int per = 16 / sizeof(T);
-                    alignas(16) T v[per];
+                    for (int c = 0; c < kCh; ++c) {
+                        constexpr int per = 16 / sizeof(T);
+                        alignas(16) T v[per];
 #pragma unroll
-                    for (int e = 0; e < per; ++e) v[e] = from_f32<T>(__uint_as_float(r[c * per + e]));
-                    *reinterpret_cast<uint4*>(ys + (lane * kCh + (c ^ (lane & 7))) * 16) = *reinterpret_cast<const uint4*>(v);
-                }
-                __syncwarp();
-                constexpr int kRows = 32 / kCh;  // rows a warp writes at once
-                const int c = lane % kCh;
-                const int col = n0 + c0 + c * (16 / (int)sizeof(T));
+                        for (int e = 0; e < per; ++e) v[e] = from_f32<T>(__uint_as_float(r[i][c * per + e]));
+                        *reinterpret_cast<uint4*>(ys + (lane * kCh + (c ^ (lane / (8 / kCh) % kCh))) * 16) =
+                            *reinterpret_cast<const uint4*>(v);
+                    }
+                    __syncwarp();
+                    constexpr int kRows = 32 / kCh;  // rows a warp writes at once
+                    const int c = lane % kCh;
+                    const int col = c0 + c * (16 / (int)sizeof(T));
 #pragma unroll
-                for (int i = 0; i < kCh; ++i) {
-                    const int rr = i * kRows + lane / kCh;
-                    const int yr = __shfl_sync(0xffffffffu, yrow, rr);
-                    const uint4 v = *reinterpret_cast<const uint4*>(ys + (rr * kCh + (c ^ (rr & 7))) * 16);
-                    if (yr < 0) continue;
-                    T* yp = y + (long long)yr * a.ldy + col;
-                    if (a.vec && col + (int)(16 / sizeof(T)) <= a.h_out) {
-                        *reinterpret_cast<uint4*>(yp) = v;
-                    } else {
-                        alignas(16) T e8[16 / sizeof(T)];
-                        *reinterpret_cast<uint4*>(e8) = v;
+                    for (int k = 0; k < kCh; ++k) {
+                        const int rr = k * kRows + lane / kCh;
+                        const int yr = __shfl_sync(0xffffffffu, yrow, rr);
+                        const uint4 v = *reinterpret_cast<const uint4*>(ys + (rr * kCh + (c ^ (rr / (8 / kCh) % kCh))) * 16);
+                        if (yr < 0) continue;
+                        T* yp = y + (long long)yr * a.ldy + col;
+                        if (a.vec && col + (int)(16 / sizeof(T)) <= a.h_out) {
+                            *reinterpret_cast<uint4*>(yp) = v;
+                        } else {
+                            alignas(16) T e8[16 / sizeof(T)];
+                            *reinterpret_cast<uint4*>(e8) = v;
 #pragma unroll
-                        for (int e = 0; e < (int)(16 / sizeof(T)); ++e)
-                            if (col + e < a.h_out) yp[e] = e8[e];
+                            for (int e = 0; e < (int)(16 / sizeof(T)); ++e)
+                                if (col + e < a.h_out) yp[e] = e8[e];
+                        }
                     }
                 }
             }
@@ -347,9 +371,89 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(epi_done);
         }
+    } else if (warp >= 14) {
+        // ---- scales: the four warps copy steps ahead together, and each fills its own 32 lanes ----
+        // A step of these warps has to stay shorter than the MMAs of a step (512 clocks), so the copies'
+        // addresses only advance, and their issue overlaps the stores to tensor memory.  By the
+        // load/store unit: TMA copies of 1 KB were slower (8191 x 11008 x 4096: 167 us as tensor boxes,
+        // 184 us as bulk copies).
+        constexpr int L = kPScaleSlots - 1;  // steps ahead
+        const int q = warp & 3, st = threadIdx.x - 448;
+        const uint32_t full0 = mapa_shared(smem_u32(full), 0);
+        const uint32_t taddr = tmem + kPScaleCol + (static_cast<uint32_t>(q * 32) << 16);
+        // threads 0-63 copy x's 1 KB and the second of w's, threads 64-127 the first of w's
+        int ltile = pair, lkb = 0, lslot = 0;  // next step to copy
+        const uint8_t *pa = nullptr, *pb = nullptr;
+        auto next_tile = [&]() {
+            pa = pb = nullptr;  // tiles past the last row are left out: what they scale is not stored
+            if (ltile >= total) return;
+            const int m = ltile / a.n_tiles * 2 + static_cast<int>(rank), rt = ltile % a.n_tiles * 2;
+            if (st >= 64) {
+                pa = a.sw + (size_t)rt * a.kt * 512 + (st - 64) * 16;
+            } else {
+                if (m * 128 < a.n) pa = a.sx + (size_t)m * a.kt * 512 + st * 16;
+                if ((rt + 1) * 128 < a.h_out) pb = a.sw + (size_t)(rt + 1) * a.kt * 512 + st * 16;
+            }
+        };
+        auto copy_next = [&]() {
+            uint8_t* dst = scale_sm + lslot * kPScaleBytes + st * 16;
+            if (pa) cp_async16(dst, pa), pa += 1024;
+            if (pb) cp_async16(dst + 2048, pb), pb += 1024;
+            cp_async_commit();  // (a group each step, empty ones too)
+            if (++lslot == kPScaleSlots) lslot = 0;
+            if (++lkb == nkb) {
+                lkb = 0;
+                ltile += npairs;
+                next_tile();
+            }
+        };
+        pdl_wait();
+        next_tile();
+        for (int i = 0; i < L; ++i) copy_next();
+        int slot = 0, set = 0, back = 0, warm = kPScaleSets;  // back: stage of the step kPScaleSets before
+        uint32_t backph = 0;
+        Ring cr;
+        bool ok = true;
+        for (int tile = pair; tile < total; tile += npairs) {
+            for (int kb = 0; kb < nkb; ++kb) {
+                cp_async_wait<L - 1>();
+                ok = named_bar_and(3, 128, ok);  // everyone's pieces of this step are there, the last step is read
+                if (!ok) break;
+                const uint4* sp = reinterpret_cast<const uint4*>(scale_sm + slot * kPScaleBytes) + lane;
+                if (++slot == kPScaleSlots) slot = 0;
+                const uint4 x0 = sp[0], x1 = sp[32];
+                const uint4 w00 = sp[64], w01 = sp[96], w10 = sp[128], w11 = sp[160];  // [row tile][step half]
+                // the set's last readers: the MMAs kPScaleSets steps before
+                if (warm > 0) {
+                    --warm;
+                } else {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&empty[back], backph, flags));
+                    if (++back == stages) {
+                        back = 0;
+                        backph ^= 1;
+                    }
+                    tc_fence_after();
+                }
+                if (ok) {
+                    const uint32_t t = taddr + set * 24;
+                    tmem_st8(t, x0, x1);
+                    tmem_st8(t + 8, w00, w10);
+                    tmem_st8(t + 16, w01, w11);
+                }
+                if (++set == kPScaleSets) set = 0;
+                copy_next();
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive_cluster_relaxed(full0 + static_cast<uint32_t>(cr.i) * 8u);
+                cr.next(stages);
+            }
+        }
+        if (!ok && a.status) report_timeout_status(a.status);
+        cp_async_wait<0>();
     } else if (a.fuse) {
         // ---- LoRA blocks ----
-        const int lt = threadIdx.x - 192;  // 0..127: a token row and a feature of this CTA's half
+        const int lt = threadIdx.x - 320;  // 0..127: a token row and a feature of this CTA's half
         if constexpr (sizeof(T) == 2) {
             pdl_wait();
             const int status = a.status ? __ldcg(a.status) : LORA_OK;
@@ -457,13 +561,13 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
 // Pairs the GPU holds at once (an SM left over in a group of SMs cannot host a pair).
 template <typename T>
 static int max_pairs() {
-    static int pairs = 0;
+    static int pairs = 0;  // every variant takes all of an SM's shared memory: the same for each
     if (!pairs) {
         cudaLaunchConfig_t q;
         memset(&q, 0, sizeof(q));
         q.gridDim = dim3(2 * (num_sms() / 2));
         q.blockDim = dim3(kPThreads);
-        q.dynamicSmemBytes = kPSmem;
+        q.dynamicSmemBytes = kSmemMax;
         cudaLaunchAttribute qa[1];
         qa[0].id = cudaLaunchAttributeClusterDimension;
         qa[0].val.clusterDim.x = 2;
@@ -496,6 +600,8 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
     a.nkb = x.ktiles / 2;
     a.kt = x.ktiles;
     a.early_w = early_w;
+    // six stages where neither the LoRA blocks nor float32 staging take the room of one
+    a.stages = !lora && sizeof(T) == 2 ? 6 : 5;
     // rows of y are written 16 bytes at a time when every row starts on a 16-byte boundary
     a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     if (lora) {
@@ -508,20 +614,21 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
         a.S = lora->S;
         a.bf16 = std::is_same<T, __nv_bfloat16>::value;
     }
-    CUtensorMap mX, mW, mSx, mSw;
+    a.sx = x.scales;
+    a.sw = w.scales;
+    CUtensorMap mX, mW;
     int rc = make_map_fp4(&mX, x.codes, x.pitch, x.rows, kPM);
     if (!rc) rc = make_map_fp4(&mW, w.codes, w.pitch, w.rows, kPN / 2);
-    if (!rc) rc = make_map_fp4_scales(&mSx, x.scales, (uint64_t)((x.rows + 127) / 128) * x.ktiles);
-    if (!rc) rc = make_map_fp4_scales(&mSw, w.scales, (uint64_t)((w.rows + 127) / 128) * w.ktiles);
     if (rc) return rc;
     static bool attr = false;
     if (!attr) {
-        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPSmem));
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax));
         attr = true;
     }
     const int pairs = (int)std::min<long long>((long long)a.m_tiles * a.n_tiles, max_pairs<T>());
-    void* args[] = {(void*)&mX, (void*)&mW, (void*)&mSx, (void*)&mSw, (void*)&a};
-    LORA_CUDA_TRY(launch_pdl((const void*)fp4_pair_kernel<T>, dim3(2 * pairs), dim3(kPThreads), kPSmem, st, args));
+    void* args[] = {(void*)&mX, (void*)&mW, (void*)&a};
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_pair_kernel<T>, dim3(2 * pairs), dim3(kPThreads),
+                             pair_smem(a.stages, a.fuse != 0, sizeof(T)), st, args));
     return LORA_OK;
 }
 

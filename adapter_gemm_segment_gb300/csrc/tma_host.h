@@ -110,21 +110,5 @@ inline int make_map_fp4(CUtensorMap* m, const void* codes, uint64_t pitch, uint6
     return LORA_OK;
 }
 
-// Scale tiles of a stored 4-bit matrix as rows of 512 bytes, box of 2 tiles (256 elements of K for
-// 128 rows); tiles past the end read as zeros.
-inline int make_map_fp4_scales(CUtensorMap* m, const void* scales, uint64_t tiles) {
-    auto fn = encode_fn();
-    if (!fn) return set_error(LORA_ECUDA, "cuTensorMapEncodeTiled is unavailable");
-    const cuuint64_t dims[2] = {128, tiles};
-    const cuuint64_t strides[1] = {512};
-    const cuuint32_t box[2] = {128u, 2u};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(scales), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return set_error(LORA_ECUDA, "cuTensorMapEncodeTiled (4-bit scales) failed (%d)", (int)r);
-    return LORA_OK;
-}
-
 }  // namespace tc
 }  // namespace lora
