@@ -27,20 +27,22 @@ constexpr int kFp4Cols = 256;     // columns per warp
 // 8 elements starting at column c of a row (zeros past cols).  VEC: rows are 16-byte aligned, so
 // whole groups of 8 take vector loads.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* __restrict__ row, int c, int cols, float (&f)[8]) {
+__device__ __forceinline__ Raw8<T> load8(const T* __restrict__ row, int c, int cols) {
+    Raw8<T> r;
     if (VEC && c + 8 <= cols) {
         if constexpr (sizeof(T) == 2) {
-            unpack8<T>(__ldg(reinterpret_cast<const uint4*>(row + c)), f);
+            r.v = __ldcs(reinterpret_cast<const uint4*>(row + c));
         } else {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(row + c));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(row + c + 4));
-            f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
-            f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+            r.a = __ldcs(reinterpret_cast<const float4*>(row + c));
+            r.b = __ldcs(reinterpret_cast<const float4*>(row + c + 4));
         }
-        return;
+        return r;
     }
+    alignas(16) T v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = c + e < cols ? to_f32(row[c + e]) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? row[c + e] : from_f32<T>(0.f);
+    memcpy(&r, v, sizeof(r));
+    return r;
 }
 
 template <typename T, bool VEC>
@@ -52,27 +54,23 @@ fp4_quantize_kernel(const T* __restrict__ x, long long ld, Fp4View q) {
     const int r32 = blockIdx.y * 8 + warp;  // row within each 32-row quarter
     const int r0 = blockIdx.z * 128 + r32;
     const int c = blockIdx.x * kFp4Cols + lane * 8;
-    float f[4][8];
+    Raw8<T> v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int r = r0 + 32 * j;
-        if (r < q.rows) {
-            load8<T, VEC>(x + (long long)r * ld, c, q.cols, f[j]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[j][e] = 0.f;
-        }
+        if (r < q.rows)
+            v[j] = load8<T, VEC>(x + (long long)r * ld, c, q.cols);
+        else
+            memset(&v[j], 0, sizeof(v[j]));
     }
-    uint32_t sw[4];
+    uint32_t codes[4], sw[4];
+    quantise_rows<T, 4>(v, codes, sw, lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t scale;
-        const uint32_t codes = quantise8(f[j], scale);
         const int r = r0 + 32 * j;
         // c / 32 < blocks: the last block's codes past cols are written (as zeros) too
         if (r < q.rows && c / 32 < q.blocks)
-            *reinterpret_cast<uint32_t*>(q.codes + (size_t)r * q.pitch + c / 2) = codes;
-        sw[j] = scale_word(scale, lane);
+            *reinterpret_cast<uint32_t*>(q.codes + (size_t)r * q.pitch + c / 2) = codes[j];
     }
     if ((lane & 15) == 0) {
         const size_t tile = (size_t)blockIdx.z * q.ktiles + blockIdx.x * 2 + (lane >> 4);
@@ -227,6 +225,8 @@ static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
     const int rc = lora_linear_workspace_bytes(pool, n, &s_bytes);
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
+    if (n > 256 && pool->desc.dtype != LORA_F32)
+        s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * n * pool->desc.r_max * 4;
     L->codes_off = align256(s_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
     L->total = L->scales_off + align256(fp4_scales_bytes(n, h_in));
@@ -328,7 +328,7 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         const Fp4View own = fp4_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
         rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, st);
         if (rc) return rc;
-        const Fp4Lora lora = {sv.perm, sv.idx, s_buf, pv.B, pv.R, pv.S};
+        const Fp4Lora lora = {sv.perm, sv.idx, s_buf, fp4_prepare_parts(n, own.ktiles), pv.B, pv.R};
         return launch_fp4_pair(own, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     }
     if (!xq) {

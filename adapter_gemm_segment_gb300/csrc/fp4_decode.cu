@@ -270,18 +270,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                             const int d = (p0 + j) / chunks, c = (p0 + j) - d * chunks;
                             uint4 v = make_uint4(0, 0, 0, 0);
                             if (p0 + j < P_all && slot == dlist[d]) {
-                                float s8[8] = {};
-                                for (int k = 0; k < a.s_parts; ++k) {
-                                    const float4* sp = reinterpret_cast<const float4*>(
-                                        a.s_in + ((size_t)k * n + t) * a.R + c * 8);
-                                    const float4 u0 = __ldcg(sp), u1 = __ldcg(sp + 1);
-                                    s8[0] += u0.x, s8[1] += u0.y, s8[2] += u0.z, s8[3] += u0.w;
-                                    s8[4] += u1.x, s8[5] += u1.y, s8[6] += u1.z, s8[7] += u1.w;
-                                }
-                                alignas(16) T h8[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) h8[e] = from_f32<T>(s8[e]);
-                                v = *reinterpret_cast<const uint4*>(h8);
+                                v = sum_parts8<T>(a.s_in + (size_t)t * a.R + c * 8, a.s_parts, (size_t)n * a.R);
                             }
                             *reinterpret_cast<uint4*>(blk + kDChunks * 2048 + j * schunk + t * 16) = v;
                         }
@@ -349,17 +338,10 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                             for (int k8 = 0; k8 < chunks; ++k8) {
                                 const int p = d * chunks + k8;
                                 if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
-                                alignas(16) T h8[8];
-                                for (int e = 0; e < 8; ++e) {
-                                    float v = 0.f;
-                                    for (int k = 0; k < a.s_parts; ++k)
-                                        v += __ldcg(a.s_in + ((size_t)k * n + t) * a.R + k8 * 8 + e);
-                                    h8[e] = from_f32<T>(v);
-                                }
+                                const uint4 sv = sum_parts8<T>(a.s_in + (size_t)t * a.R + k8 * 8, a.s_parts, (size_t)n * a.R);
                                 const uint4 bv = __ldg(reinterpret_cast<const uint4*>(
                                     static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + o) * a.R + k8 * 8));
-                                r[c] = __float_as_uint(nonfinite_dot8<T>(bv, *reinterpret_cast<const uint4*>(h8),
-                                                                         __uint_as_float(r[c])));
+                                r[c] = __float_as_uint(nonfinite_dot8<T>(bv, sv, __uint_as_float(r[c])));
                             }
                         }
                     }

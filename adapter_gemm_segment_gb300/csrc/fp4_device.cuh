@@ -6,50 +6,91 @@
 
 namespace lora {
 
-// Two float32 values to a byte of two e2m1 codes (lo in the low half), round to nearest even,
-// saturating.
-__device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
-    uint16_t r;
-    asm("{\n\t.reg .b8 t;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %2, %1;\n\t"
-        "cvt.u16.u8 %0, t;\n\t}"
-        : "=h"(r)
-        : "f"(lo), "f"(hi));
-    return r;
+// Quantisation of a block of 32 held by four neighbouring lanes, 8 elements each.  With E the biased
+// float32 exponent of the block's largest |x| the scale byte is max(E - 2, 0): the largest element
+// then lies in [4, 8) times the scale, of which [6, 8) saturates at 6.  Multiplying by the power of
+// two 2^(127 - byte) is exact wherever the result does not round to zero anyway, so the rounding to
+// e2m1 (to nearest, ties to even) is the only one.  E = 255, an infinity or a NaN, gives the NaN scale
+// and codes 0.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t E) { return E == 255 ? 255u : E > 2 ? E - 2 : 0u; }
+
+// 8 float32 values times 2^(127 - byte), as codes (0 with the NaN scale).
+__device__ __forceinline__ uint32_t codes8(const float (&f)[8], uint32_t byte) {
+    const float k = __uint_as_float((254u - min(byte, 253u)) << 23);  // 2^-125 .. 2^127
+    uint32_t c;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(c)
+        : "f"(f[0] * k), "f"(f[1] * k), "f"(f[2] * k), "f"(f[3] * k), "f"(f[4] * k), "f"(f[5] * k), "f"(f[6] * k),
+          "f"(f[7] * k));
+    return byte == 255 ? 0u : c;
 }
 
-// The codes of a lane's 8 elements and the scale byte of its block; four neighbouring lanes hold a
-// block of 32.  With E the biased float32 exponent of the block's largest |x| the byte is
-// max(E - 2, 0): the largest element then lies in [4, 8) times the scale, of which [6, 8) saturates
-// at 6.  2^(127 - byte) and the products with it are exact, so the rounding to e2m1 is the only one.
-__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], uint32_t& scale) {
-    // |x| as an integer orders like |x|, with infinities and NaNs on top
-    uint32_t m = 0;
+// A lane's 8 elements of a row: packed for the 16-bit types, as they are for float32.
+template <typename T> struct Raw8 {
+    uint4 v;
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+};
+// |x| as an integer orders like |x|, with infinities and NaNs on top: the largest of a lane's 8, for
+// two rows at once (16-bit types: row 0 in the low half), before it is reduced over the four lanes.
+__device__ __forceinline__ uint32_t top8_packed(const uint4& v) {
+    return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+}
+template <typename T> __device__ __forceinline__ uint32_t exponent16(uint32_t top);  // biased float32 exponent
+template <> __device__ __forceinline__ uint32_t exponent16<__nv_bfloat16>(uint32_t top) { return top >> 7; }
+template <> __device__ __forceinline__ uint32_t exponent16<__half>(uint32_t top) {
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top)))) >> 23;
+}
+
+// Quantises NR (even) rows at once: codes[j] are this lane's 8 codes of row j, words[j] the four scale
+// bytes of row j's 128 columns held by this half-warp (the same in each of its lanes).
+template <typename T, int NR>
+__device__ __forceinline__ void quantise_rows(const Raw8<T> (&x)[NR], uint32_t (&codes)[NR], uint32_t (&words)[NR],
+                                              int lane) {
+    uint32_t byte[NR];
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const uint32_t E = m >> 23;
-    if (E == 255) {
-        scale = 255;
-        return 0;
+        for (int j = 0; j < NR; j += 2) {
+            const uint32_t a = top8_packed(x[j].v), b = top8_packed(x[j + 1].v);
+            uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));  // two rows
+            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            byte[j] = scale_byte(exponent16<T>(m & 0xffffu));
+            byte[j + 1] = scale_byte(exponent16<T>(m >> 16));
+        }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            float f[8];
+            unpack8<T>(x[j].v, f);
+            codes[j] = codes8(f, byte[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const float f[8] = {x[j].a.x, x[j].a.y, x[j].a.z, x[j].a.w, x[j].b.x, x[j].b.y, x[j].b.z, x[j].b.w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            byte[j] = scale_byte(m >> 23);
+            codes[j] = codes8(f, byte[j]);
+        }
     }
-    scale = E > 2 ? E - 2 : 0;
-    const float k = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale): 2^-125 .. 2^127
-    uint32_t c = 0;
+    // byte i of a row's word comes from the lanes of block i
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c |= cvt_e2m1x2(f[2 * e] * k, f[2 * e + 1] * k) << (8 * e);
-    return c;
-}
-
-// The four scale bytes of a half-warp's 128 columns as one word (every lane of the half gets it).
-__device__ __forceinline__ uint32_t scale_word(uint32_t scale, int lane) {
-    const int h = lane & 16;
-    uint32_t w = __shfl_sync(0xffffffffu, scale, h);
-    w |= __shfl_sync(0xffffffffu, scale, h + 4) << 8;
-    w |= __shfl_sync(0xffffffffu, scale, h + 8) << 16;
-    w |= __shfl_sync(0xffffffffu, scale, h + 12) << 24;
-    return w;
+    for (int j = 0; j < NR; ++j) {
+        uint32_t w = byte[j] << (8 * ((lane >> 2) & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        w |= __shfl_xor_sync(0xffffffffu, w, 8);
+        words[j] = w;
+    }
 }
 
 // Whether any of 8 packed 16-bit values is an infinity or a NaN.
@@ -83,6 +124,20 @@ template <typename T> __device__ __forceinline__ float nonfinite_dot8(const uint
     for (int e = 0; e < 8; ++e)
         if ((__float_as_uint(bf[e]) & 0x7f800000u) == 0x7f800000u) acc = fmaf(bf[e], sf[e], acc);
     return acc;
+}
+
+// Eight shrink values summed over their K parts, rounded to the 16-bit type.
+template <typename T> __device__ __forceinline__ uint4 sum_parts8(const float* s, int parts, size_t stride) {
+    float4 a = __ldcg(reinterpret_cast<const float4*>(s)), b = __ldcg(reinterpret_cast<const float4*>(s) + 1);
+    for (int k = 1; k < parts; ++k) {
+        const float4 c = __ldcg(reinterpret_cast<const float4*>(s + k * stride));
+        const float4 d = __ldcg(reinterpret_cast<const float4*>(s + k * stride) + 1);
+        a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
+        b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+    }
+    alignas(16) T v[8] = {from_f32<T>(a.x), from_f32<T>(a.y), from_f32<T>(a.z), from_f32<T>(a.w),
+                          from_f32<T>(b.x), from_f32<T>(b.y), from_f32<T>(b.z), from_f32<T>(b.w)};
+    return *reinterpret_cast<const uint4*>(v);
 }
 
 }  // namespace lora

@@ -77,13 +77,13 @@ struct PairArgs {
     int32_t* status;         // nullable
     const int32_t* perm;     // row of y of each token row (nullptr: the same)
     const int32_t* idx;      // fuse: adapter slot by original token
-    const void* s16;         // fuse: [n][R] shrink output in token-row order, 16-bit
+    const float* s_in;       // fuse: [s_parts][n][R] shrink output in token-row order
     const void* B;           // fuse: pool's B slab
     const uint8_t* sx;       // scale tiles of x and w
     const uint8_t* sw;
     long long ldy;
     int n, h_out, m_tiles, n_tiles, nkb, kt, stages;
-    int R, S, fuse, bf16, early_w, vec;
+    int R, s_parts, fuse, bf16, early_w, vec;
 };
 
 // A ring position: index and parity of its current use.
@@ -320,8 +320,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                             for (int c = 0; c < chunks; ++c) {
                                 const int p = d * chunks + c;
                                 if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
-                                const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
-                                                                                       (size_t)row * a.R + c * 8));
+                                const uint4 sv = sum_parts8<T>(a.s_in + (size_t)row * a.R + c * 8, a.s_parts,
+                                                               (size_t)a.n * a.R);
                                 const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0) * a.R + c * 8;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
@@ -508,7 +508,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 }
                 const int o_own = n0 + static_cast<int>(rank) * (kPN / 2) + lt;
                 const int o_other = n0 + static_cast<int>(rank ^ 1) * (kPN / 2) + lt;
-                const T* srow = static_cast<const T*>(a.s16) + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
+                const float* srow = a.s_in + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
                 for (int b = 0; b < blocks; ++b, ++lb) {
                     const int lbuf = lb & 1;
                     uint4 sv[4], bv[4], bo[4];
@@ -519,7 +519,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                         if (p < P) {
                             const int d = p / chunks, c = p - d * chunks;
                             const int sl = dlist[d];
-                            if (sl == slot[0]) sv[j] = __ldcg(reinterpret_cast<const uint4*>(srow + c * 8));
+                            if (sl == slot[0]) sv[j] = sum_parts8<T>(srow + c * 8, a.s_parts, (size_t)a.n * a.R);
                             const T* Bs = static_cast<const T*>(a.B) + (size_t)sl * a.h_out * a.R + c * 8;
                             if (o_own < a.h_out) bv[j] = __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)o_own * a.R));
                             if (o_other < a.h_out) bo[j] = __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)o_other * a.R));
@@ -608,10 +608,10 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
         a.fuse = 1;
         a.perm = lora->perm;
         a.idx = lora->idx;
-        a.s16 = lora->s16;
+        a.s_in = lora->s_in;
+        a.s_parts = lora->s_parts;
         a.B = lora->B;
         a.R = lora->R;
-        a.S = lora->S;
         a.bf16 = std::is_same<T, __nv_bfloat16>::value;
     }
     a.sx = x.scales;
@@ -635,17 +635,18 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
 // ============================================================================================
 // before the product: x quantised and the LoRA shrink, one read of x
 // ============================================================================================
-// One CTA per 128 tokens in segment order.  Eight worker warps load the tokens' rows of x, 128
-// columns a step, quantise them from registers (as the quantise kernel does) and write the 16-bit
-// values to shared memory, where the tensor cores multiply them with the A rows of the tile's
-// adapters (TMA): s[t, :] = (alpha / r) x[t] A^T, kept in float32 until the one rounding to the
-// pool's 16-bit type on the way out.  Tiles whose adapters need more than 256 accumulator columns
-// take several passes over K.  With x already stored in 4 bits, the codes and scales are copied
-// instead.  Bound by the read of x; one kernel instead of two reads it once.
+// One CTA per 128 tokens in segment order and part of K.  Eight worker warps load the tokens' rows of
+// x, 128 columns a step, quantise them from registers (as the quantise kernel does) and write the
+// 16-bit values to shared memory, where the tensor cores multiply them with the A rows of the
+// tile's adapters (TMA): the part's share of s[t, :] = (alpha / r) x[t] A^T, in float32.  Tiles whose
+// adapters need more accumulator columns than a pass holds take several passes over their columns.
+// With x already stored in 4 bits, the codes and scales are copied instead.  Bound by the read of
+// x, which one kernel does once where a quantiser and a shrink would do it twice.
 constexpr int kQThreads = 320;  // warp 0: A rows, warp 1: MMAs, warps 2-9: workers
-constexpr uint32_t kQXBytes = 128 * 256, kQABytes = 256 * 256;  // two 64-column swizzled halves each
-constexpr uint32_t kQStageBytes = kQXBytes + kQABytes;
-constexpr size_t kQSmem = 2 * (size_t)kQStageBytes + 1024 + 128 * 4 * 2 + 64 * 8 + 256 * 4 + 256;
+constexpr uint32_t kQXBytes = 128 * 256;  // two 64-column swizzled halves
+// Accumulator columns (A rows) per pass: 64, so that two CTAs share an SM, unless one adapter has more.
+inline int prep_cap(int R) { return std::max(64, (R + 15) / 16 * 16); }
+inline size_t prep_smem(int cap) { return 2 * ((size_t)kQXBytes + cap * 256) + 1024 + 128 * 4 * 2 + 64 * 8 + 128 * 4 + 256; }
 
 struct PrepArgs {
     PoolView pool;
@@ -654,21 +655,22 @@ struct PrepArgs {
     Fp4View q;                 // out: rows in segment order
     const uint8_t* xq_codes;   // x already stored, rows in token order (nullable)
     const uint8_t* xq_scales;
-    void* s16;                 // out: [n][R]
-    int bf16;
+    float* s;                  // out: [parts][n][R], rows in segment order
+    int bf16, cap, steps;      // steps: 128-column steps per part
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kQThreads, 1)
+__global__ void __launch_bounds__(kQThreads)
 fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
-    int* src_sm = reinterpret_cast<int*>(smem + 2 * kQStageBytes);  // [128] token of each row (-1: none)
+    const uint32_t a_half = static_cast<uint32_t>(a.cap) * 128, stage_bytes = kQXBytes + 2 * a_half;
+    int* src_sm = reinterpret_cast<int*>(smem + 2 * stage_bytes);   // [128] token of each row (-1: none)
     int* slot_sm = src_sm + 128;                                    // [128]
     uint32_t* seen = reinterpret_cast<uint32_t*>(slot_sm + 128);    // [64]
     int* before = reinterpret_cast<int*>(seen + 64);                // [64]
     int* dlist = before + 64;                                       // [128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(dlist + 256);      // [2] 8 worker warps and the A rows
+    uint64_t* full = reinterpret_cast<uint64_t*>(dlist + 128);      // [2] 8 worker warps and the A rows
     uint64_t* empty = full + 2;                                     // [2]
     uint64_t* acc_full = empty + 2;
     uint64_t* acc_free = acc_full + 1;                              // 4 worker warps
@@ -678,6 +680,9 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
     const int m0 = blockIdx.x * 128;
     const int R = a.pool.R, h = a.pool.h_in;
+    const int ch0 = blockIdx.y * a.steps;                      // this part's steps of 128 columns
+    const int nch = min(a.q.ktiles, ch0 + a.steps) - ch0;
+    const uint32_t tmem_cols = a.cap <= 64 ? 64 : a.cap <= 128 ? 128 : 256;
     pdl_wait();
     pdl_trigger();
     if (__ldcg(a.seg.status) != LORA_OK) return;  // the product leaves y alone
@@ -701,7 +706,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
         seen[tid - 128] = 0;
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 256);
+        tmem_alloc(tmem_slot, tmem_cols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -718,9 +723,8 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     }
     __syncthreads();
     const int D = before[63] + __popc(seen[63]);
-    const int spp = 256 / R;                       // adapters per pass
+    const int spp = a.cap / R;                     // adapters per pass
     const int passes = (D + spp - 1) / spp;        // 0: no token of the tile has an adapter
-    const int nch = a.q.ktiles;                    // steps of 128 columns
 
     if (warp == 0) {
         if (lane == 0) {
@@ -731,11 +735,11 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                     const int s = it & 1;
                     if (it >= 2 && !mbar_wait(&empty[s], ((it >> 1) & 1) ^ 1, flags)) break;
                     mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(dn * R * 256));
-                    uint8_t* As = smem + s * kQStageBytes + kQXBytes;
+                    uint8_t* As = smem + s * stage_bytes + kQXBytes;
                     for (int d = 0; d < dn; ++d)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf)
-                            tma_load_2d_cta(As + hf * (kQABytes / 2) + d * R * 128, &tmA, &full[s], ch * 128 + hf * 64,
+                            tma_load_2d_cta(As + hf * a_half + d * R * 128, &tmA, &full[s], (ch0 + ch) * 128 + hf * 64,
                                             dlist[d0 + d] * R);
                 }
             }
@@ -753,7 +757,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
             int it = 0;
             bool ok = true;
             for (int p = 0; p < passes && ok; ++p) {
-                const int cols = (min(spp, D - p * spp) * R + 15) / 16 * 16;  // 8 more than loaded: not read
+                const int cols = (min(spp, D - p * spp) * R + 15) / 16 * 16;  // up to 8 more than loaded: not read
                 const uint32_t idesc = idesc_f16(128, cols, a.bf16 != 0);
                 if (p > 0 && !mbar_wait(acc_free, (p - 1) & 1, flags)) {
                     ok = false;
@@ -767,12 +771,11 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t xa = smem_u32(smem + s * kQStageBytes), aa = xa + kQXBytes;
+                    const uint32_t xa = smem_u32(smem + s * stage_bytes), aa = xa + kQXBytes;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         umma_f16(tmem, sdesc_sw128(xa + (k >> 2) * (kQXBytes / 2) + (k & 3) * 32),
-                                 sdesc_sw128(aa + (k >> 2) * (kQABytes / 2) + (k & 3) * 32), idesc,
-                                 (ch > 0 || k > 0) ? 1u : 0u);
+                                 sdesc_sw128(aa + (k >> 2) * a_half + (k & 3) * 32), idesc, (ch > 0 || k > 0) ? 1u : 0u);
                     umma_commit(&empty[s]);
                 }
                 umma_commit(acc_full);
@@ -784,48 +787,45 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
         }
     } else {
         const int ww = warp - 2, l16 = lane & 15;
-        // this thread's rows: r32 + 32 j2 for two r32 (j & 1) and the four quarters (j >> 1)
+        // this thread's rows: r0 + 2 (j & 1) + 32 (j >> 1), four quarters of two rows
         const int r0 = ww * 4 + (lane >> 4);
         int src[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) src[j] = src_sm[r0 + 2 * (j & 1) + 32 * (j >> 1)];
         const T* x = static_cast<const T*>(a.x);
-        auto load = [&](int ch, uint4 (&v)[8]) {
-            const int c = ch * 128 + l16 * 8;
+        auto load = [&](int ch, Raw8<T> (&v)[8]) {
+            const int c = (ch0 + ch) * 128 + l16 * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[j] = make_uint4(0, 0, 0, 0);
-                if (src[j] >= 0 && c < h) v[j] = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src[j] * h + c));
+                v[j].v = make_uint4(0, 0, 0, 0);
+                if (src[j] >= 0 && c < h) v[j].v = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src[j] * h + c));
             }
         };
-        auto quantise = [&](int ch, const uint4 (&v)[8]) {
-            const int c = ch * 128 + l16 * 8;
-            uint32_t sw[8];
+        auto quantise = [&](int ch, const Raw8<T> (&v)[8]) {
+            const int c = (ch0 + ch) * 128 + l16 * 8;
+            const bool live = c / 32 < a.q.blocks;
+            uint32_t codes[8], sw[8];
+            if (a.xq_codes) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = r0 + 2 * (j & 1) + 32 * (j >> 1);
-                uint32_t codes, scale;
-                if (a.xq_codes) {
-                    codes = 0;
-                    sw[j] = 0;
-                    if (src[j] >= 0) {
-                        if (c / 32 < a.q.blocks)
-                            codes = __ldg(reinterpret_cast<const uint32_t*>(a.xq_codes + (size_t)src[j] * a.q.pitch + c / 2));
-                        sw[j] = __ldg(reinterpret_cast<const uint32_t*>(
-                            a.xq_scales + ((size_t)(src[j] / 128) * a.q.ktiles + ch) * 512 + (src[j] % 32) * 16 +
-                            (src[j] % 128) / 32 * 4));
-                    }
-                } else {
-                    float f[8];
-                    unpack8<T>(v[j], f);
-                    codes = quantise8(f, scale);
-                    sw[j] = scale_word(scale, lane);
+                for (int j = 0; j < 8; ++j) {
+                    codes[j] = sw[j] = 0;
+                    if (src[j] < 0) continue;
+                    if (live)
+                        codes[j] = __ldg(reinterpret_cast<const uint32_t*>(a.xq_codes + (size_t)src[j] * a.q.pitch + c / 2));
+                    sw[j] = __ldg(reinterpret_cast<const uint32_t*>(
+                        a.xq_scales + ((size_t)(src[j] / 128) * a.q.ktiles + ch0 + ch) * 512 + (src[j] % 32) * 16 +
+                        (src[j] % 128) / 32 * 4));
                 }
-                if (m0 + r < a.q.rows && c / 32 < a.q.blocks)
-                    *reinterpret_cast<uint32_t*>(a.q.codes + (size_t)(m0 + r) * a.q.pitch + c / 2) = codes;
+            } else {
+                quantise_rows<T, 8>(v, codes, sw, lane);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (live && src[j] >= 0)
+                    *reinterpret_cast<uint32_t*>(a.q.codes + (size_t)(m0 + r0 + 2 * (j & 1) + 32 * (j >> 1)) * a.q.pitch +
+                                                 c / 2) = codes[j];
             if (l16 == 0) {
-                uint8_t* tile = a.q.scales + ((size_t)blockIdx.x * a.q.ktiles + ch) * 512;
+                uint8_t* tile = a.q.scales + ((size_t)blockIdx.x * a.q.ktiles + ch0 + ch) * 512;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     *reinterpret_cast<uint4*>(tile + (r0 + 2 * i) * 16) = make_uint4(sw[i], sw[2 + i], sw[4 + i], sw[6 + i]);
@@ -839,7 +839,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
         int it = 0;
         bool ok = true;
         for (int p = 0; p < rounds && ok; ++p) {
-            uint4 cur[8], nxt[8];
+            Raw8<T> cur[8], nxt[8];
             load(0, cur);
             for (int ch = 0; ch < nch; ++ch, ++it) {
                 if (ch + 1 < nch) load(ch + 1, nxt);
@@ -849,11 +849,11 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                         ok = false;
                         break;
                     }
-                    uint8_t* xs = smem + s * kQStageBytes + (l16 >> 3) * (kQXBytes / 2);
+                    uint8_t* xs = smem + s * stage_bytes + (l16 >> 3) * (kQXBytes / 2);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int r = r0 + 2 * (j & 1) + 32 * (j >> 1);
-                        *reinterpret_cast<uint4*>(xs + r * 128 + (((l16 & 7) ^ (r & 7)) << 4)) = cur[j];
+                        *reinterpret_cast<uint4*>(xs + r * 128 + (((l16 & 7) ^ (r & 7)) << 4)) = cur[j].v;
                     }
                     fence_proxy_async_smem();  // read by the tensor cores
                     __syncwarp();
@@ -872,21 +872,19 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
             const bool mine = dl >= d0 && dl < d0 + dn;
             const int col0 = (dl - d0) * R;
             const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            T* out = static_cast<T*>(a.s16) + (size_t)(m0 + row) * R;
+            float* out = a.s + ((size_t)blockIdx.y * a.seg.n + m0 + row) * R;
             for (int c0 = 0; c0 < dn * R; c0 += 16) {
                 uint32_t r[16];
                 __syncwarp();
                 tmem_ld16(taddr + c0, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int j = c0 + 8 * hf - col0;
-                    if (mine && j >= 0 && j < R) {
-                        alignas(16) T v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(scale * __uint_as_float(r[8 * hf + e]));
-                        *reinterpret_cast<uint4*>(out + j) = *reinterpret_cast<const uint4*>(v);
-                    }
+                for (int e = 0; e < 16; e += 4) {
+                    const int j = c0 + e - col0;
+                    if (mine && j >= 0 && j < R)
+                        *reinterpret_cast<float4*>(out + j) =
+                            make_float4(scale * __uint_as_float(r[e]), scale * __uint_as_float(r[e + 1]),
+                                        scale * __uint_as_float(r[e + 2]), scale * __uint_as_float(r[e + 3]));
                 }
             }
             tc_fence_before();
@@ -897,12 +895,12 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, 256);
+    if (warp == 1) tmem_dealloc(tmem, tmem_cols);
 }
 
 template <typename T>
 static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                            void* s16, cudaStream_t st) {
+                            float* s, cudaStream_t st) {
     PrepArgs a;
     a.pool = pv;
     a.seg = sv;
@@ -910,28 +908,41 @@ static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x
     a.q = q;
     a.xq_codes = xq ? xq->codes : nullptr;
     a.xq_scales = xq ? xq->scales : nullptr;
-    a.s16 = s16;
+    a.s = s;
     a.bf16 = std::is_same<T, __nv_bfloat16>::value;
+    a.cap = prep_cap(pv.R);
+    const int parts = fp4_prepare_parts(sv.n, q.ktiles);
+    a.steps = (q.ktiles + parts - 1) / parts;
     CUtensorMap mA;
     const int rc = make_map(&mA, pv.A, a.bf16, pv.h_in, (uint64_t)pv.S * pv.R, pv.R);
     if (rc) return rc;
     static bool attr = false;
     if (!attr) {
-        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_prepare_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQSmem));
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_prepare_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)prep_smem(256)));
         attr = true;
     }
     void* args[] = {(void*)&mA, (void*)&a};
-    LORA_CUDA_TRY(launch_pdl((const void*)fp4_prepare_kernel<T>, dim3((sv.n + 127) / 128), dim3(kQThreads), kQSmem, st,
-                             args));
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_prepare_kernel<T>, dim3((sv.n + 127) / 128, parts), dim3(kQThreads),
+                             prep_smem(a.cap), st, args));
     return LORA_OK;
 }
 
 }  // namespace tc
 
+// K parts: two CTAs share an SM, and a part is at least two steps of 128 columns and at most eight.
+int fp4_prepare_parts(int n, int ktiles) {
+    const int tiles = (n + 127) / 128;
+    int parts = std::max(1, 4 * num_sms() / tiles);
+    parts = std::min({parts, 8, ktiles / 2});
+    const int steps = (ktiles + parts - 1) / parts;
+    return (ktiles + steps - 1) / steps;
+}
+
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                       void* s16, cudaStream_t st) {
-    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, s16, st);
-    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, s16, st);
+                       float* s, cudaStream_t st) {
+    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, s, st);
+    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, s, st);
 }
 
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,

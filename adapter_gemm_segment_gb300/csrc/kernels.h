@@ -107,9 +107,10 @@ int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q
 struct Fp4Lora {
     const int32_t* perm;  // token of each row of x
     const int32_t* idx;   // slot of each token
-    const void* s16;      // [n][R], rows like x's
+    const float* s_in;    // [s_parts][n][R], rows like x's
+    int s_parts;
     const void* B;
-    int R, S;
+    int R;
 };
 // Up to 256 tokens.  lora: the pool, the slot of each token and the shrink output in K parts.
 struct Fp4DecodeLora {
@@ -123,10 +124,11 @@ int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, lo
 // More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
-// Quantises x (or copies xq) into q and writes the shrink output to s16 [n][R] (16-bit), rows of
+// Quantises x (or copies xq) into q and writes the shrink output in K parts, s [parts][n][R]; rows of
 // both in segment order.
+int fp4_prepare_parts(int n, int ktiles);
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                       void* s16, cudaStream_t st);
+                       float* s, cudaStream_t st);
 
 int num_sms();
 
