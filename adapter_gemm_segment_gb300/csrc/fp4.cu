@@ -216,18 +216,23 @@ static int check_rows(const void* p, int dtype, int64_t ld, int rows, int cols, 
 
 static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev, m->scales_dev, m->rows, m->cols); }
 
-// Workspace of lora_fp4_linear_fwd: the shrink output, then the stored form of x.
+// Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their rounded
+// sum), then the stored form of x.
 struct Fp4WsLayout {
-    size_t codes_off, scales_off, total;
+    size_t s16_off, codes_off, scales_off, total;
 };
 static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
     size_t s_bytes;
     const int rc = lora_linear_workspace_bytes(pool, n, &s_bytes);
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
-    if (n > 256 && pool->desc.dtype != LORA_F32)
-        s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * n * pool->desc.r_max * 4;
-    L->codes_off = align256(s_bytes);
+    size_t s16_bytes = 0;
+    if (n > 256 && pool->desc.dtype != LORA_F32) {
+        s16_bytes = (size_t)n * pool->desc.r_max * 2;
+        s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * 2 * s16_bytes;
+    }
+    L->s16_off = align256(s_bytes);
+    L->codes_off = L->s16_off + align256(s16_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
     L->total = L->scales_off + align256(fp4_scales_bytes(n, h_in));
     return LORA_OK;
@@ -326,9 +331,9 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
 
     if (n > 256 && pv.dtype != LORA_F32) {
         const Fp4View own = fp4_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
-        rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, st);
+        rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, ws + L.s16_off, st);
         if (rc) return rc;
-        const Fp4Lora lora = {sv.perm, sv.idx, s_buf, fp4_prepare_parts(n, own.ktiles), pv.B, pv.R};
+        const Fp4Lora lora = {sv.perm, sv.idx, ws + L.s16_off, pv.B, pv.R};
         return launch_fp4_pair(own, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     }
     if (!xq) {

@@ -60,7 +60,7 @@ constexpr int kPScaleCol = 512 - 24 * kPScaleSets;
 constexpr int kPAcc1 = kPScaleCol - kPN;            // first column of the second accumulator
 constexpr int kPLoraChunk = kPM * 16;               // 8 columns of 128 rows, 16 bytes a row
 constexpr int kPLoraBytes = 2 * 4 * kPLoraChunk;    // one block: 4 chunks on each side
-constexpr int kPScratch = 64 * 4 + 64 * 4 + 256 * 4 + 1024;
+constexpr int kPScratch = 64 * 4 + 256 * 4 + 8;
 // after the stages: scales, LoRA blocks (if any), y staging (8 warps of 32 rows x 32 columns), the
 // LoRA scratch, barriers
 constexpr size_t pair_smem(int stages, bool fuse, size_t elt) {
@@ -77,13 +77,13 @@ struct PairArgs {
     int32_t* status;         // nullable
     const int32_t* perm;     // row of y of each token row (nullptr: the same)
     const int32_t* idx;      // fuse: adapter slot by original token
-    const float* s_in;       // fuse: [s_parts][n][R] shrink output in token-row order
+    const void* s16;         // fuse: [n][R] shrink output in token-row order, 16-bit
     const void* B;           // fuse: pool's B slab
     const uint8_t* sx;       // scale tiles of x and w
     const uint8_t* sw;
     long long ldy;
     int n, h_out, m_tiles, n_tiles, nkb, kt, stages;
-    int R, s_parts, fuse, bf16, early_w, vec;
+    int R, fuse, bf16, early_w, vec;
 };
 
 // A ring position: index and parity of its current use.
@@ -108,22 +108,23 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     uint8_t* lora_sm = scale_sm + kPScaleSlots * kPScaleBytes;   // [2] blocks {token side, feature side}
     uint8_t* yst = lora_sm + (a.fuse ? 2 * kPLoraBytes : 0);     // [8 warps][32 rows][32]
     uint32_t* seen = reinterpret_cast<uint32_t*>(yst + 8 * 1024 * sizeof(T));  // [64] slots the tile's tokens name
-    int* before = reinterpret_cast<int*>(seen + 64);             // [64] named slots below each word
-    int* dlist = before + 64;                                    // [256] the tile's slots in order
-    uint32_t* badmap = reinterpret_cast<uint32_t*>(dlist + 256); // [256] LoRA chunks with a non-finite B
-    uint64_t* full = reinterpret_cast<uint64_t*>(badmap + 256);  // even CTA: codes of both halves, 8 scale warps
+    int* dlist = reinterpret_cast<int*>(seen + 64);              // [256] the tile's slots in order
+    int* distinct = dlist + 256;                                 // [2] their number
+    uint64_t* full = reinterpret_cast<uint64_t*>(distinct + 2);  // even CTA: codes of both halves, 8 scale warps
     uint64_t* empty = full + kPMaxStages;    // the even CTA's commits (multicast)
     uint64_t* acc_full = empty + kPMaxStages;  // [2] (multicast)
     uint64_t* ov_free = acc_full + 2;        // even CTA: the shared columns are drained (16 warps)
     uint64_t* lora_full = ov_free + 1;       // [2] even CTA: a LoRA block is written (8 warps)
     uint64_t* lora_empty = lora_full + 2;    // [2] (multicast)
-    uint64_t* linfo = lora_empty + 2;        // even CTA: the tile's number of LoRA blocks is known
-    uint64_t* epi_done = linfo + 1;          // the epilogue is through with a tile (8 warps)
-    uint64_t* lora_done = epi_done + 1;      // the tile's LoRA scratch is complete (4 warps)
-    uint64_t* drained = lora_done + 1;       // even CTA: every MMA has completed
+    // by parity of the tile (the LoRA warps may be a tile ahead of the others):
+    uint64_t* linfo = lora_empty + 2;        // [2] even CTA: the tile's number of LoRA blocks is known
+    uint64_t* epi_done = linfo + 2;          // [2] the epilogues are through with the tile (16 warps of both CTAs)
+    uint64_t* lora_done = epi_done + 2;      // [2] the tile's LoRA blocks are written (8 warps of both CTAs)
+    uint64_t* drained = lora_done + 2;       // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort, LoRA blocks, any bad chunk
-    static_assert((2 * kPMaxStages + 11) * 8 + 16 <= 256, "barrier area");
+    // abort, -, then by parity of the tile: [2] 1 + the last tile with a non-finite B, [2] LoRA blocks
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((2 * kPMaxStages + 14) * 8 + 28 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -140,13 +141,13 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             mbar_init(&acc_full[b], 1);
             mbar_init(&lora_full[b], 8);
             mbar_init(&lora_empty[b], 1);
+            mbar_init(&linfo[b], 1);
+            mbar_init(&epi_done[b], 16);
+            mbar_init(&lora_done[b], 8);
         }
         mbar_init(ov_free, 16);
-        mbar_init(linfo, 1);
-        mbar_init(epi_done, 8);
-        mbar_init(lora_done, 4);
         mbar_init(drained, 1);
-        flags[0] = flags[1] = flags[2] = 0;
+        for (int i = 0; i < 6; ++i) flags[i] = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -235,11 +236,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 }
                 if (!ok) break;
                 if (a.fuse) {
-                    if (!mbar_wait(linfo, local & 1, flags)) {
+                    if (!mbar_wait(&linfo[buf], (local >> 1) & 1, flags)) {
                         ok = false;
                         break;
                     }
-                    const int blocks = flags[1];
+                    const int blocks = flags[4 + buf];
                     for (int b = 0; b < blocks; ++b, ++lb) {
                         const int lbuf = lb & 1;
                         if (!mbar_wait_cluster(&lora_full[lbuf], (lb >> 1) & 1, flags)) {
@@ -272,6 +273,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         constexpr int kCh = 32 * sizeof(T) / 16;  // 16-byte pieces of a staged row
         uint8_t* ys = yst + (warp - 2) * (1024 * sizeof(T));
         const uint32_t ov_free0 = mapa_shared(smem_u32(ov_free), 0);
+        const uint32_t other_epi = mapa_shared(smem_u32(epi_done), rank ^ 1);
         pdl_wait();
         const int status = a.status ? __ldcg(a.status) : LORA_OK;
         T* y = static_cast<T*>(a.y);
@@ -282,10 +284,10 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const int row = m0 + q * 32 + lane;
             const int yrow = row < a.n ? (a.perm ? __ldcg(a.perm + row) : row) : -1;
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, flags) &&
-                                             (!a.fuse || mbar_wait(lora_done, local & 1, flags))))
+                                             (!a.fuse || mbar_wait_cluster(&lora_done[buf], (local >> 1) & 1, flags))))
                 break;
             tc_fence_after();
-            const bool any_bad = a.fuse && flags[2] != 0;
+            const bool any_bad = a.fuse && flags[2 + buf] == local + 1;
             const int slot = any_bad && yrow >= 0 && status == LORA_OK ? __ldcg(a.idx + yrow) : -1;
             const uint32_t taddr = tmem + buf * kPAcc1 + (static_cast<uint32_t>(q * 32) << 16);
             uint32_t r[2][32];
@@ -314,15 +316,10 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                     if (c0 >= a.h_out) continue;
                     if constexpr (sizeof(T) == 2) {
                         if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
-                            const int w = slot >> 5;
-                            const int d = before[w] + __popc(seen[w] & ((1u << (slot & 31)) - 1u));
-                            const int chunks = a.R / 8;
-                            for (int c = 0; c < chunks; ++c) {
-                                const int p = d * chunks + c;
-                                if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
-                                const uint4 sv = sum_parts8<T>(a.s_in + (size_t)row * a.R + c * 8, a.s_parts,
-                                                               (size_t)a.n * a.R);
-                                const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0) * a.R + c * 8;
+                            for (int c = 0; c < a.R; c += 8) {
+                                const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
+                                                                                       (size_t)row * a.R + c));
+                                const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0) * a.R + c;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     if (c0 + e < a.h_out)
@@ -369,7 +366,10 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(epi_done);
+            if (lane == 0 && a.fuse) {
+                mbar_arrive(&epi_done[buf]);
+                mbar_arrive_cluster_relaxed(other_epi + static_cast<uint32_t>(buf) * 8u);
+            }
         }
     } else if (warp >= 14) {
         // ---- scales: the four warps copy steps ahead together, and each fills its own 32 lanes ----
@@ -458,6 +458,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             pdl_wait();
             const int status = a.status ? __ldcg(a.status) : LORA_OK;
             const uint32_t lora_full0 = mapa_shared(smem_u32(lora_full), 0);
+            const uint32_t other_done = mapa_shared(smem_u32(lora_done), rank ^ 1);
+            const uint32_t other_flags = mapa_shared(smem_u32(const_cast<int*>(flags)), rank ^ 1);
             const int chunks = a.R / 8;
             int local = 0, lb = 0;
             bool ok = true;
@@ -471,60 +473,53 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                     slot[h] = -1;
                     if (row < a.n && status == LORA_OK) slot[h] = __ldcg(a.idx + __ldcg(a.perm + row));
                 }
-                // the epilogue reads this scratch for the tile before
-                if (local > 0 && !mbar_wait(epi_done, (local - 1) & 1, flags)) ok = false;
-                if (!named_bar_and(2, 128, ok)) break;  // all four warps leave together
                 if (lt < 64) seen[lt] = 0;
-                for (int i = lt; i < 256; i += 128) badmap[i] = 0;
-                if (lt == 0) flags[2] = 0;
-                named_bar_sync(2, 128);
+                // the epilogue has read this parity's flag of the tile two before (in both CTAs)
+                if (local >= 2 && !mbar_wait(&epi_done[local & 1], ((local >> 1) & 1) ^ 1, flags)) ok = false;
+                if (!named_bar_and(2, 128, ok)) break;  // all four warps leave together
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (slot[h] >= 0) atomicOr(&seen[slot[h] >> 5], 1u << (slot[h] & 31));
                 named_bar_sync(2, 128);
-                if (lt < 32) {  // words 2 lane and 2 lane + 1
-                    const int p0 = __popc(seen[2 * lt]), p1 = __popc(seen[2 * lt + 1]);
-                    int v = p0 + p1;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int o = __shfl_up_sync(0xffffffffu, v, d);
-                        if (lt >= d) v += o;
-                    }
-                    before[2 * lt] = v - p0 - p1;
-                    before[2 * lt + 1] = v - p1;
-                }
-                named_bar_sync(2, 128);
                 if (lt < 64) {
-                    int at = before[lt];
+                    int at = 0;
+                    for (int w = 0; w < lt; ++w) at += __popc(seen[w]);
                     for (uint32_t m = seen[lt]; m; m &= m - 1) dlist[at++] = lt * 32 + __ffs(m) - 1;
+                    if (lt == 63) *distinct = at;
                 }
                 named_bar_sync(2, 128);
-                const int D = before[63] + __popc(seen[63]);
-                const int P = D * chunks;            // 8-column chunks of the tile's adapters
+                const int P = *distinct * chunks;  // 8-column chunks of the tile's adapters
                 const int blocks = (P + 3) / 4;
                 if (rank == 0 && lt == 0) {
-                    flags[1] = blocks;
-                    mbar_arrive(linfo);
+                    flags[4 + (local & 1)] = blocks;
+                    mbar_arrive(&linfo[local & 1]);
                 }
-                const int o_own = n0 + static_cast<int>(rank) * (kPN / 2) + lt;
-                const int o_other = n0 + static_cast<int>(rank ^ 1) * (kPN / 2) + lt;
-                const float* srow = a.s_in + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
-                for (int b = 0; b < blocks; ++b, ++lb) {
-                    const int lbuf = lb & 1;
-                    uint4 sv[4], bv[4], bo[4];
+                const int o = n0 + static_cast<int>(rank) * (kPN / 2) + lt;
+                const T* srow = static_cast<const T*>(a.s16) + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
+                const T* Bcol = static_cast<const T*>(a.B) + (size_t)o * a.R;
+                int d = 0, c = 0;  // the next chunk: columns 8c.. of adapter dlist[d]
+                int sl = P > 0 ? dlist[0] : -1;
+                auto load = [&](uint4 (&sv)[4], uint4 (&bv)[4]) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int p = 4 * b + j;
-                        sv[j] = bv[j] = bo[j] = make_uint4(0, 0, 0, 0);
-                        if (p < P) {
-                            const int d = p / chunks, c = p - d * chunks;
-                            const int sl = dlist[d];
-                            if (sl == slot[0]) sv[j] = sum_parts8<T>(srow + c * 8, a.s_parts, (size_t)a.n * a.R);
-                            const T* Bs = static_cast<const T*>(a.B) + (size_t)sl * a.h_out * a.R + c * 8;
-                            if (o_own < a.h_out) bv[j] = __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)o_own * a.R));
-                            if (o_other < a.h_out) bo[j] = __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)o_other * a.R));
+                        const bool live = d * chunks + c < P;
+                        sv[j] = live && sl == slot[0] ? __ldcg(reinterpret_cast<const uint4*>(srow + c * 8))
+                                                      : make_uint4(0, 0, 0, 0);
+                        bv[j] = live && o < a.h_out
+                                    ? __ldg(reinterpret_cast<const uint4*>(Bcol + (size_t)sl * a.h_out * a.R + c * 8))
+                                    : make_uint4(0, 0, 0, 0);
+                        if (++c == chunks) {
+                            c = 0;
+                            ++d;
+                            if (d * chunks < P) sl = dlist[d];
                         }
                     }
+                };
+                uint4 sv[4], bv[4], sn[4], bn[4];
+                if (blocks > 0) load(sv, bv);
+                for (int b = 0; b < blocks; ++b, ++lb) {
+                    const int lbuf = lb & 1;
+                    if (b + 1 < blocks) load(sn, bn);  // the next block's loads in flight meanwhile
                     if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((lb >> 1) & 1) ^ 1, flags))) {
                         ok = false;
                         break;
@@ -532,21 +527,25 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                     uint8_t* blk = lora_sm + lbuf * kPLoraBytes;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (nonfinite8<T>(bv[j]) || nonfinite8<T>(bo[j])) {  // both CTAs see both halves
-                            const int p = 4 * b + j;
-                            atomicOr(&badmap[p >> 5], 1u << (p & 31));
-                            flags[2] = 1;
+                        if (nonfinite8<T>(bv[j])) {  // raise both CTAs' flags of this tile
                             bv[j] = finite8<T>(bv[j]);
+                            flags[2 + (local & 1)] = local + 1;
+                            st_dsmem_u32(other_flags + 4 * (2 + (local & 1)), local + 1);
                         }
                         *reinterpret_cast<uint4*>(blk + j * kPLoraChunk + lt * 16) = sv[j];
                         *reinterpret_cast<uint4*>(blk + (4 + j) * kPLoraChunk + lt * 16) = bv[j];
+                        sv[j] = sn[j];
+                        bv[j] = bn[j];
                     }
                     fence_proxy_async_smem();  // read by the tensor cores
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(lora_full0 + static_cast<uint32_t>(lbuf) * 8u);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(lora_done);
+                if (lane == 0) {
+                    mbar_arrive(&lora_done[local & 1]);
+                    mbar_arrive_cluster(other_done + static_cast<uint32_t>(local & 1) * 8u);
+                }
             }
             if (!ok && a.status) report_timeout_status(a.status);
         }
@@ -608,8 +607,7 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
         a.fuse = 1;
         a.perm = lora->perm;
         a.idx = lora->idx;
-        a.s_in = lora->s_in;
-        a.s_parts = lora->s_parts;
+        a.s16 = lora->s16;
         a.B = lora->B;
         a.R = lora->R;
         a.bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -635,18 +633,21 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
 // ============================================================================================
 // before the product: x quantised and the LoRA shrink, one read of x
 // ============================================================================================
-// One CTA per 128 tokens in segment order and part of K.  Eight worker warps load the tokens' rows of
+// One CTA per 128 tokens in segment order and part of K.  The worker warps load the tokens' rows of
 // x, 128 columns a step, quantise them from registers (as the quantise kernel does) and write the
 // 16-bit values to shared memory, where the tensor cores multiply them with the A rows of the
 // tile's adapters (TMA): the part's share of s[t, :] = (alpha / r) x[t] A^T, in float32.  Tiles whose
 // adapters need more accumulator columns than a pass holds take several passes over their columns.
+// The parts of a tile are a thread-block cluster: they leave their shares in global memory, and after
+// the cluster barrier each adds up some of the rows and rounds them to the pool's 16-bit type.
 // With x already stored in 4 bits, the codes and scales are copied instead.  Bound by the read of
 // x, which one kernel does once where a quantiser and a shrink would do it twice.
-constexpr int kQThreads = 320;  // warp 0: A rows, warp 1: MMAs, warps 2-9: workers
+constexpr int kQWorkers = 16;   // worker warps: with two CTAs an SM, 32 to hide their latencies
+constexpr int kQThreads = 64 + 32 * kQWorkers;  // warp 0: A rows, warp 1: MMAs
 constexpr uint32_t kQXBytes = 128 * 256;  // two 64-column swizzled halves
 // Accumulator columns (A rows) per pass: 64, so that two CTAs share an SM, unless one adapter has more.
 inline int prep_cap(int R) { return std::max(64, (R + 15) / 16 * 16); }
-inline size_t prep_smem(int cap) { return 2 * ((size_t)kQXBytes + cap * 256) + 1024 + 128 * 4 * 2 + 64 * 8 + 128 * 4 + 256; }
+inline size_t prep_smem(int cap) { return 2 * ((size_t)kQXBytes + cap * 256) + 1024 + 128 * 4 + 64 * 8 + 128 * 4 + 256; }
 
 struct PrepArgs {
     PoolView pool;
@@ -655,22 +656,22 @@ struct PrepArgs {
     Fp4View q;                 // out: rows in segment order
     const uint8_t* xq_codes;   // x already stored, rows in token order (nullable)
     const uint8_t* xq_scales;
-    float* s;                  // out: [parts][n][R], rows in segment order
-    int bf16, cap, steps;      // steps: 128-column steps per part
+    float* s;                  // scratch: [parts][n][R]
+    void* s16;                 // out: [n][R], rows in segment order
+    int bf16, cap, steps, parts;  // steps: 128-column steps per part
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, 2)
 fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
     const uint32_t a_half = static_cast<uint32_t>(a.cap) * 128, stage_bytes = kQXBytes + 2 * a_half;
-    int* src_sm = reinterpret_cast<int*>(smem + 2 * stage_bytes);   // [128] token of each row (-1: none)
-    int* slot_sm = src_sm + 128;                                    // [128]
+    int* slot_sm = reinterpret_cast<int*>(smem + 2 * stage_bytes);  // [128] slot of each row's token (-1: none)
     uint32_t* seen = reinterpret_cast<uint32_t*>(slot_sm + 128);    // [64]
     int* before = reinterpret_cast<int*>(seen + 64);                // [64]
     int* dlist = before + 64;                                       // [128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(dlist + 128);      // [2] 8 worker warps and the A rows
+    uint64_t* full = reinterpret_cast<uint64_t*>(dlist + 128);      // [2] the worker warps and the A rows
     uint64_t* empty = full + 2;                                     // [2]
     uint64_t* acc_full = empty + 2;
     uint64_t* acc_free = acc_full + 1;                              // 4 worker warps
@@ -683,13 +684,23 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     const int ch0 = blockIdx.y * a.steps;                      // this part's steps of 128 columns
     const int nch = min(a.q.ktiles, ch0 + a.steps) - ch0;
     const uint32_t tmem_cols = a.cap <= 64 ? 64 : a.cap <= 128 ? 128 : 256;
-    pdl_wait();
-    pdl_trigger();
-    if (__ldcg(a.seg.status) != LORA_OK) return;  // the product leaves y alone
-
+    const int l16 = lane & 15;
+    // a worker's rows: r0 + 32 j; its first step of x is on its way before the tile's adapters are found
+    const int r0 = (warp - 2) * 2 + (lane >> 4);
+    int src[4];
+    Raw8<T> cur[4];
+    const T* x = static_cast<const T*>(a.x);
+    auto load = [&](int ch, Raw8<T> (&v)[4]) {
+        const int c = (ch0 + ch) * 128 + l16 * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j].v = make_uint4(0, 0, 0, 0);
+            if (src[j] >= 0 && c < h) v[j].v = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src[j] * h + c));
+        }
+    };
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&full[s], 9);
+            mbar_init(&full[s], kQWorkers + 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
@@ -698,16 +709,26 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
         fence_barrier_init();
         prefetch_tmap(&tmA);
     }
-    if (tid < 128) {
-        const int src = m0 + tid < a.seg.n ? __ldcg(a.seg.perm + m0 + tid) : -1;
-        src_sm[tid] = src;
-        slot_sm[tid] = src >= 0 ? __ldcg(a.seg.idx + src) : -1;
-    } else if (tid < 192) {
-        seen[tid - 128] = 0;
-    }
     if (warp == 1) {
         tmem_alloc(tmem_slot, tmem_cols);
         tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+    const bool run = __ldcg(a.seg.status) == LORA_OK;  // otherwise the product leaves y alone
+    if (warp >= 2 && run) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = m0 + r0 + 32 * j;
+            src[j] = r < a.seg.n ? __ldcg(a.seg.perm + r) : -1;
+        }
+        load(0, cur);
+    }
+    if (tid < 128) {
+        const int t = run && m0 + tid < a.seg.n ? __ldcg(a.seg.perm + m0 + tid) : -1;
+        slot_sm[tid] = t >= 0 ? __ldcg(a.seg.idx + t) : -1;
+    } else if (tid < 192) {
+        seen[tid - 128] = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -715,11 +736,20 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     const uint32_t tmem = *tmem_slot;
     if (tid < 128 && slot_sm[tid] >= 0) atomicOr(&seen[slot_sm[tid] >> 5], 1u << (slot_sm[tid] & 31));
     __syncthreads();
-    if (tid < 64) {
-        int v = 0;
-        for (int w = 0; w < tid; ++w) v += __popc(seen[w]);
-        before[tid] = v;
-        for (uint32_t m = seen[tid]; m; m &= m - 1) dlist[v++] = tid * 32 + __ffs(m) - 1;
+    if (tid < 32) {  // words 2 tid and 2 tid + 1
+        const uint32_t w0 = seen[2 * tid], w1 = seen[2 * tid + 1];
+        int v = __popc(w0) + __popc(w1);
+        const int own = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, v, d);
+            if (tid >= d) v += o;
+        }
+        int at = v - own;
+        before[2 * tid] = at;
+        for (uint32_t m = w0; m; m &= m - 1) dlist[at++] = 2 * tid * 32 + __ffs(m) - 1;
+        before[2 * tid + 1] = at;
+        for (uint32_t m = w1; m; m &= m - 1) dlist[at++] = (2 * tid + 1) * 32 + __ffs(m) - 1;
     }
     __syncthreads();
     const int D = before[63] + __popc(seen[63]);
@@ -785,29 +815,14 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                 umma_commit(acc_full);
             }
         }
-    } else {
-        const int ww = warp - 2, l16 = lane & 15;
-        // this thread's rows: r0 + 2 (j & 1) + 32 (j >> 1), four quarters of two rows
-        const int r0 = ww * 4 + (lane >> 4);
-        int src[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) src[j] = src_sm[r0 + 2 * (j & 1) + 32 * (j >> 1)];
-        const T* x = static_cast<const T*>(a.x);
-        auto load = [&](int ch, Raw8<T> (&v)[8]) {
-            const int c = (ch0 + ch) * 128 + l16 * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j].v = make_uint4(0, 0, 0, 0);
-                if (src[j] >= 0 && c < h) v[j].v = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src[j] * h + c));
-            }
-        };
-        auto quantise = [&](int ch, const Raw8<T> (&v)[8]) {
+    } else if (run) {
+        auto quantise = [&](int ch, const Raw8<T> (&v)[4]) {
             const int c = (ch0 + ch) * 128 + l16 * 8;
             const bool live = c / 32 < a.q.blocks;
-            uint32_t codes[8], sw[8];
+            uint32_t codes[4], sw[4];
             if (a.xq_codes) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     codes[j] = sw[j] = 0;
                     if (src[j] < 0) continue;
                     if (live)
@@ -817,19 +832,15 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                         (src[j] % 128) / 32 * 4));
                 }
             } else {
-                quantise_rows<T, 8>(v, codes, sw, lane);
+                quantise_rows<T, 4>(v, codes, sw, lane);
             }
+            uint8_t* out = a.q.codes + (size_t)(m0 + r0) * a.q.pitch + c / 2;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (live && src[j] >= 0)
-                    *reinterpret_cast<uint32_t*>(a.q.codes + (size_t)(m0 + r0 + 2 * (j & 1) + 32 * (j >> 1)) * a.q.pitch +
-                                                 c / 2) = codes[j];
-            if (l16 == 0) {
-                uint8_t* tile = a.q.scales + ((size_t)blockIdx.x * a.q.ktiles + ch0 + ch) * 512;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4*>(tile + (r0 + 2 * i) * 16) = make_uint4(sw[i], sw[2 + i], sw[4 + i], sw[6 + i]);
-            }
+            for (int j = 0; j < 4; ++j)
+                if (live && src[j] >= 0) *reinterpret_cast<uint32_t*>(out + (size_t)(32 * j) * a.q.pitch) = codes[j];
+            if (l16 == 0)
+                *reinterpret_cast<uint4*>(a.q.scales + ((size_t)blockIdx.x * a.q.ktiles + ch0 + ch) * 512 + r0 * 16) =
+                    make_uint4(sw[0], sw[1], sw[2], sw[3]);
         };
         const int rounds = max(passes, 1);  // the first round quantises
         const int row = (warp & 3) * 32 + lane;
@@ -839,8 +850,8 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
         int it = 0;
         bool ok = true;
         for (int p = 0; p < rounds && ok; ++p) {
-            Raw8<T> cur[8], nxt[8];
-            load(0, cur);
+            Raw8<T> nxt[4];
+            if (p > 0) load(0, cur);
             for (int ch = 0; ch < nch; ++ch, ++it) {
                 if (ch + 1 < nch) load(ch + 1, nxt);
                 if (passes > 0) {
@@ -851,8 +862,8 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                     }
                     uint8_t* xs = smem + s * stage_bytes + (l16 >> 3) * (kQXBytes / 2);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int r = r0 + 2 * (j & 1) + 32 * (j >> 1);
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = r0 + 32 * j;
                         *reinterpret_cast<uint4*>(xs + r * 128 + (((l16 & 7) ^ (r & 7)) << 4)) = cur[j].v;
                     }
                     fence_proxy_async_smem();  // read by the tensor cores
@@ -861,7 +872,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                 }
                 if (p == 0) quantise(ch, cur);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) cur[j] = nxt[j];
+                for (int j = 0; j < 4; ++j) cur[j] = nxt[j];
             }
             if (passes == 0 || warp >= 6) continue;
             // ---- the pass's shrink output: thread <-> token row, the columns of its own adapter ----
@@ -873,18 +884,28 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
             const int col0 = (dl - d0) * R;
             const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
             float* out = a.s + ((size_t)blockIdx.y * a.seg.n + m0 + row) * R;
+            T* out16 = static_cast<T*>(a.s16) + (size_t)(m0 + row) * R;
             for (int c0 = 0; c0 < dn * R; c0 += 16) {
                 uint32_t r[16];
                 __syncwarp();
                 tmem_ld16(taddr + c0, r);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
+                for (int e = 0; e < 16; e += 8) {
                     const int j = c0 + e - col0;
-                    if (mine && j >= 0 && j < R)
-                        *reinterpret_cast<float4*>(out + j) =
-                            make_float4(scale * __uint_as_float(r[e]), scale * __uint_as_float(r[e + 1]),
-                                        scale * __uint_as_float(r[e + 2]), scale * __uint_as_float(r[e + 3]));
+                    if (!mine || j < 0 || j >= R) continue;
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = scale * __uint_as_float(r[e + i]);
+                    if (a.parts == 1) {
+                        alignas(16) T v16[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v16[i] = from_f32<T>(v[i]);
+                        *reinterpret_cast<uint4*>(out16 + j) = *reinterpret_cast<const uint4*>(v16);
+                    } else {
+                        reinterpret_cast<float4*>(out + j)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<float4*>(out + j)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    }
                 }
             }
             tc_fence_before();
@@ -896,11 +917,22 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, tmem_cols);
+    if (a.parts > 1) {
+        cluster_sync();  // every part's share is written
+        const int chunks = R / 8, per = (128 + a.parts - 1) / a.parts;
+        const int q0 = blockIdx.y * per, q1 = min(128, q0 + per);
+        for (int e = q0 * chunks + tid; e < q1 * chunks; e += kQThreads) {
+            const int row = e / chunks, c = e - row * chunks;
+            if (slot_sm[row] < 0) continue;
+            *reinterpret_cast<uint4*>(static_cast<T*>(a.s16) + (size_t)(m0 + row) * R + c * 8) =
+                sum_parts8<T>(a.s + (size_t)(m0 + row) * R + c * 8, a.parts, (size_t)a.seg.n * R);
+        }
+    }
 }
 
 template <typename T>
 static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                            float* s, cudaStream_t st) {
+                            float* s, void* s16, cudaStream_t st) {
     PrepArgs a;
     a.pool = pv;
     a.seg = sv;
@@ -909,10 +941,12 @@ static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x
     a.xq_codes = xq ? xq->codes : nullptr;
     a.xq_scales = xq ? xq->scales : nullptr;
     a.s = s;
+    a.s16 = s16;
     a.bf16 = std::is_same<T, __nv_bfloat16>::value;
     a.cap = prep_cap(pv.R);
     const int parts = fp4_prepare_parts(sv.n, q.ktiles);
     a.steps = (q.ktiles + parts - 1) / parts;
+    a.parts = parts;
     CUtensorMap mA;
     const int rc = make_map(&mA, pv.A, a.bf16, pv.h_in, (uint64_t)pv.S * pv.R, pv.R);
     if (rc) return rc;
@@ -923,26 +957,42 @@ static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x
         attr = true;
     }
     void* args[] = {(void*)&mA, (void*)&a};
-    LORA_CUDA_TRY(launch_pdl((const void*)fp4_prepare_kernel<T>, dim3((sv.n + 127) / 128, parts), dim3(kQThreads),
-                             prep_smem(a.cap), st, args));
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((sv.n + 127) / 128, parts);
+    cfg.blockDim = dim3(kQThreads);
+    cfg.dynamicSmemBytes = prep_smem(a.cap);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = parts;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    LORA_CUDA_TRY(cudaLaunchKernelExC(&cfg, (const void*)fp4_prepare_kernel<T>, args));
+    count_launch();
     return LORA_OK;
 }
 
 }  // namespace tc
 
-// K parts: two CTAs share an SM, and a part is at least two steps of 128 columns and at most eight.
+// K parts (a cluster): as many CTAs as the GPU holds at once, two an SM; a part is at least two steps
+// of 128 columns.
 int fp4_prepare_parts(int n, int ktiles) {
     const int tiles = (n + 127) / 128;
-    int parts = std::max(1, 4 * num_sms() / tiles);
+    int parts = std::max(1, 2 * num_sms() / tiles);
     parts = std::min({parts, 8, ktiles / 2});
     const int steps = (ktiles + parts - 1) / parts;
     return (ktiles + steps - 1) / steps;
 }
 
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                       float* s, cudaStream_t st) {
-    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, s, st);
-    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, s, st);
+                       float* s, void* s16, cudaStream_t st) {
+    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, s, s16, st);
+    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, s, s16, st);
 }
 
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,

@@ -107,8 +107,7 @@ int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q
 struct Fp4Lora {
     const int32_t* perm;  // token of each row of x
     const int32_t* idx;   // slot of each token
-    const float* s_in;    // [s_parts][n][R], rows like x's
-    int s_parts;
+    const void* s16;      // [n][R], rows like x's
     const void* B;
     int R;
 };
@@ -124,11 +123,11 @@ int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, lo
 // More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
-// Quantises x (or copies xq) into q and writes the shrink output in K parts, s [parts][n][R]; rows of
-// both in segment order.
+// Quantises x (or copies xq) into q and writes the shrink output to s16 [n][R] (16-bit), rows of both in
+// segment order; s: float32 scratch [fp4_prepare_parts][n][R].
 int fp4_prepare_parts(int n, int ktiles);
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                       float* s, cudaStream_t st);
+                       float* s, void* s16, cudaStream_t st);
 
 int num_sms();
 
