@@ -37,15 +37,86 @@ template <typename T> struct Raw8 {
 template <> struct Raw8<float> {
     float4 a, b;
 };
-// |x| as an integer orders like |x|, with infinities and NaNs on top: the largest of a lane's 8, for
-// two rows at once (16-bit types: row 0 in the low half), before it is reduced over the four lanes.
-__device__ __forceinline__ uint32_t top8_packed(const uint4& v) {
-    return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+// 16 bytes that are read once; issued where it stands (a plain load may be moved down to its use).
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+// Largest |x| of two packed pairs (a NaN wins), without and with the absolute values taken.
+template <typename T> __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 x, y;\n\tabs.bf16x2 x, %1;\n\tabs.bf16x2 y, %2;\n\tmax.NaN.bf16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t max_abs2<__half>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmax.NaN.f16x2 %0, x, y;\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
+    return r;
 }
 template <typename T> __device__ __forceinline__ uint32_t exponent16(uint32_t top);  // biased float32 exponent
 template <> __device__ __forceinline__ uint32_t exponent16<__nv_bfloat16>(uint32_t top) { return top >> 7; }
 template <> __device__ __forceinline__ uint32_t exponent16<__half>(uint32_t top) {
     return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top)))) >> 23;
+}
+
+// 8 packed 16-bit values times 2^(127 - byte), as codes (0 with the NaN scale).
+template <typename T> __device__ __forceinline__ uint32_t codes8_packed(const uint4& v, uint32_t byte);
+template <> __device__ __forceinline__ uint32_t codes8_packed<__nv_bfloat16>(const uint4& v, uint32_t byte) {
+    // bf16 times bf16 to float32 in one instruction each; the addend -0 keeps the sign of -0
+    const uint32_t k = (254u - min(byte, 253u)) << 7;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("{\n\t.reg .b16 l, h, k;\n\t"
+            "mov.b32 {l, h}, %2;\n\t"
+            "cvt.u16.u32 k, %3;\n\t"
+            "fma.rn.f32.bf16 %0, l, k, 0f80000000;\n\t"
+            "fma.rn.f32.bf16 %1, h, k, 0f80000000;\n\t}"
+            : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+            : "r"(w[i]), "r"(k));
+    uint32_t c;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(c)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return byte == 255 ? 0u : c;
+}
+template <> __device__ __forceinline__ uint32_t codes8_packed<__half>(const uint4& v, uint32_t byte) {
+    // The factor is 2^-13 .. 2^26 (an all-zero block's is not needed), in two that f16 holds.  A
+    // product that underflows was far below the smallest code.
+    const int K = min(127 - static_cast<int>(byte), 26), k1 = min(K, 14);
+    const uint32_t a = static_cast<uint32_t>(k1 + 15) * 0x04000400u, b = static_cast<uint32_t>(K - k1 + 15) * 0x04000400u;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 p = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&a)),
+                                  *reinterpret_cast<const __half2*>(&b));
+        m[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    uint32_t c;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(c)
+        : "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3]));
+    return byte == 255 ? 0u : c;
 }
 
 // Quantises NR (even) rows at once: codes[j] are this lane's 8 codes of row j, words[j] the four scale
@@ -57,18 +128,16 @@ __device__ __forceinline__ void quantise_rows(const Raw8<T> (&x)[NR], uint32_t (
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int j = 0; j < NR; j += 2) {
-            const uint32_t a = top8_packed(x[j].v), b = top8_packed(x[j + 1].v);
-            uint32_t m = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));  // two rows
-            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint4 &u = x[j].v, &v = x[j + 1].v;
+            const uint32_t a = max_abs2<T>(max_abs2<T>(u.x, u.y), max_abs2<T>(u.z, u.w));
+            const uint32_t b = max_abs2<T>(max_abs2<T>(v.x, v.y), max_abs2<T>(v.z, v.w));
+            uint32_t m = max_abs2<T>(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));  // two rows
+            m = max_abs2<T>(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max_abs2<T>(m, __shfl_xor_sync(0xffffffffu, m, 2));
             byte[j] = scale_byte(exponent16<T>(m & 0xffffu));
             byte[j + 1] = scale_byte(exponent16<T>(m >> 16));
-        }
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            float f[8];
-            unpack8<T>(x[j].v, f);
-            codes[j] = codes8(f, byte[j]);
+            codes[j] = codes8_packed<T>(u, byte[j]);
+            codes[j + 1] = codes8_packed<T>(v, byte[j + 1]);
         }
     } else {
 #pragma unroll
@@ -83,13 +152,15 @@ __device__ __forceinline__ void quantise_rows(const Raw8<T> (&x)[NR], uint32_t (
             codes[j] = codes8(f, byte[j]);
         }
     }
-    // byte i of a row's word comes from the lanes of block i
+    // byte i of a row's word comes from the lanes of block i; two rows travel together
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-        uint32_t w = byte[j] << (8 * ((lane >> 2) & 3));
+    for (int j = 0; j < NR; j += 2) {
+        uint32_t w = (byte[j] | byte[j + 1] << 16) << (8 * ((lane >> 2) & 1));
         w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        w |= __shfl_xor_sync(0xffffffffu, w, 8);
-        words[j] = w;
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 8);
+        const uint32_t lo = (lane & 8) ? o : w, hi = (lane & 8) ? w : o;
+        words[j] = __byte_perm(lo, hi, 0x5410);
+        words[j + 1] = __byte_perm(lo, hi, 0x7632);
     }
 }
 

@@ -695,7 +695,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             v[j].v = make_uint4(0, 0, 0, 0);
-            if (src[j] >= 0 && c < h) v[j].v = __ldg(reinterpret_cast<const uint4*>(x + (size_t)src[j] * h + c));
+            if (src[j] >= 0 && c < h) v[j].v = ld_stream16(x + (size_t)src[j] * h + c);
         }
     };
     if (tid == 0) {
