@@ -4,7 +4,9 @@
 // streams through once; K is split over the CTAs of a thread-block cluster until the grid fills the
 // GPU.  At 4 bits a 4096 x 4096 weight is 8.9 MB, 1.3 us of HBM time: the call is bound by latency
 // (launch, the first loads, the reduction), so every CTA has its share of the weight in flight
-// before it waits for anything, and the split sums meet in shared memory.
+// before it waits for anything, and the split sums meet in shared memory.  The block scales reach
+// tensor memory through registers, by the warps that drain the accumulator later: copied there by
+// tcgen05.cp from the MMA thread, a step of 256 along K took 580 ns whatever the batch.
 //
 // The LoRA term is more K blocks of the same accumulator, divided over the cluster's CTAs: for the
 // batch's distinct adapters d, columns d * r_max + j hold B_d[o, j] on the feature side (TMA boxes
@@ -30,10 +32,10 @@ namespace tc {
 using namespace ptx;
 
 constexpr int kDM = 128;         // features per tile
-constexpr int kDThreads = 320;   // warp 0 loads, 1 MMAs, 2-5 accumulator, 6-9 LoRA blocks
-constexpr uint32_t kDWBytes = kDM * 128, kDSwBytes = 1024;
+constexpr int kDThreads = 320;   // warp 0 loads, 1 MMAs, 2-5 scales, then accumulator, 6-9 LoRA blocks
+constexpr uint32_t kDWBytes = kDM * 128;
 constexpr int kDChunks = 4;      // 8-column chunks per LoRA block
-constexpr int kDScratch = 64 * 4 + 64 * 4 + 256 * 4 + 256 * 4 + 1024;
+constexpr int kDScratch = 64 * 4 + 64 * 4 + 3 * 256 * 4 + 1024;
 constexpr int kDBars = 512;
 
 struct Fp4DecodeArgs {
@@ -42,13 +44,64 @@ struct Fp4DecodeArgs {
     void* y;
     int32_t* status;      // nullable
     long long ldy;
-    int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, tmem_cols, kt, early_w;
+    int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, tmem_cols, kt, early, vec;
     // the LoRA term (fuse)
     int fuse, R, s_parts, bf16;
     const float* s_in;    // [s_parts][n][R]
     const int32_t* idx;
     const void* B;
 };
+
+// The token side of LoRA chunks p0 .. p0 + 3: for token t and chunk p, columns 8 c .. of its shrink
+// output if chunk p is c of t's own adapter (index dl[t] among the batch's), else zeros.  U (token,
+// chunk) items and K parts of the sum are loaded at once, whether they are wanted or not: a row's
+// loads then wait for memory once.
+template <typename T, int U, int K>
+__device__ __forceinline__ void build_tokens(const Fp4DecodeArgs& a, uint8_t* S, uint32_t schunk, const int* dl, int p0,
+                                             int chunks, int lt) {
+    const size_t part = (size_t)a.n * a.R;
+    for (int e0 = lt; e0 < a.n_pad * kDChunks; e0 += 128 * U) {
+        float4 lo[U], hi[U];
+        bool mine[U];
+        const float* src[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + 128 * u, t = min(e / kDChunks, a.n - 1);
+            const int c = p0 + e % kDChunks - dl[t] * chunks;
+            mine[u] = e / kDChunks < a.n && dl[t] >= 0 && c >= 0 && c < chunks;
+            src[u] = a.s_in + (size_t)t * a.R + max(0, min(c, chunks - 1)) * 8;
+            lo[u] = hi[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int k0 = 0; k0 < a.s_parts; k0 += K) {
+            float4 c[U][K], d[U][K];
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float4* p = reinterpret_cast<const float4*>(src[u] + min(k0 + k, a.s_parts - 1) * part);
+                    c[u][k] = __ldcg(p);
+                    d[u][k] = __ldcg(p + 1);
+                }
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k0 + k < a.s_parts)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        lo[u].x += c[u][k].x, lo[u].y += c[u][k].y, lo[u].z += c[u][k].z, lo[u].w += c[u][k].w;
+                        hi[u].x += d[u][k].x, hi[u].y += d[u][k].y, hi[u].z += d[u][k].z, hi[u].w += d[u][k].w;
+                    }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = e0 + 128 * u;
+            if (e >= a.n_pad * kDChunks) break;
+            alignas(16) T v[8] = {from_f32<T>(lo[u].x), from_f32<T>(lo[u].y), from_f32<T>(lo[u].z), from_f32<T>(lo[u].w),
+                                  from_f32<T>(hi[u].x), from_f32<T>(hi[u].y), from_f32<T>(hi[u].z), from_f32<T>(hi[u].w)};
+            *reinterpret_cast<uint4*>(S + (e % kDChunks) * schunk + e / kDChunks * 16) =
+                mine[u] ? *reinterpret_cast<const uint4*>(v) : make_uint4(0, 0, 0, 0);
+        }
+    }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kDThreads, 1)
@@ -57,17 +110,18 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
     const int stages = a.stages, n = a.n, n_pad = a.n_pad;
-    const int xt = n_pad > 128 ? 2 : 1;  // scale tiles of x
+    const bool xt2 = n_pad > 128;  // a second scale tile of x
     const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 128;
-    const uint32_t stage_bytes = kDWBytes + kDSwBytes + x_bytes + 1024u * xt;
+    const uint32_t stage_bytes = kDWBytes + x_bytes;
     const uint32_t schunk = static_cast<uint32_t>(n_pad) * 16;                 // token side of a chunk
     const uint32_t lora_bytes = a.fuse ? kDChunks * (2048 + schunk) : 0;
     uint8_t* lora_sm = smem + (size_t)stages * stage_bytes;                    // [2] {features, tokens}
     uint32_t* seen = reinterpret_cast<uint32_t*>(lora_sm + 2 * lora_bytes);    // [64]
     int* before = reinterpret_cast<int*>(seen + 64);                           // [64]
     int* dlist = before + 64;                                                  // [256]
-    int* slot_sm = dlist + 256;                                                // [256]
-    uint32_t* badmap = reinterpret_cast<uint32_t*>(slot_sm + 256);             // [256]
+    int* slot_sm = dlist + 256;                                                // [256] slot of each token
+    int* dl_sm = slot_sm + 256;                                                // [256] its index among the batch's
+    uint32_t* badmap = reinterpret_cast<uint32_t*>(dl_sm + 256);               // [256]
     uint64_t* full = reinterpret_cast<uint64_t*>(badmap + 256);
     uint64_t* empty = full + stages;
     uint64_t* acc_full = empty + stages;
@@ -78,7 +132,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     uint64_t* lora_done = linfo + 1;      // slots, bad chunks: complete (4 warps)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lora_done + 1);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort, LoRA blocks, any bad chunk
-    float* P = reinterpret_cast<float*>(smem);  // after the main loop: [n_pad][128] partial sums
+    float* P = reinterpret_cast<float*>(smem);  // after the main loop: [n_pad][128] (partial) sums
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m_tile = blockIdx.x, split = blockIdx.y;
@@ -91,19 +145,15 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         uint8_t* st = smem + (size_t)s * stage_bytes;
         mbar_arrive_expect_tx(&full[s], stage_bytes);
         tma_load_2d_cta(st, &tmW, &full[s], (kb0 + i) * 128, m_tile * kDM);
-        bulk_g2s(st + kDWBytes, a.sw + ((size_t)m_tile * a.kt + 2 * (kb0 + i)) * 512, 1024, &full[s]);
     };
     auto issue_x = [&](int i) {
         const int s = i % stages;
-        uint8_t* st = smem + (size_t)s * stage_bytes + kDWBytes + kDSwBytes;
-        tma_load_2d_cta(st, &tmX, &full[s], (kb0 + i) * 128, 0);
-        for (int h = 0; h < xt; ++h)
-            bulk_g2s(st + x_bytes + h * 1024, a.sx + ((size_t)h * a.kt + 2 * (kb0 + i)) * 512, 1024, &full[s]);
+        tma_load_2d_cta(smem + (size_t)s * stage_bytes + kDWBytes, &tmX, &full[s], (kb0 + i) * 128, 0);
     };
     const int pre = min(stages, nkb);
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 5);  // the loads and the four scale warps
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
@@ -118,9 +168,12 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         fence_barrier_init();
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmX);
-        // the weight is complete when this grid starts behind a kernel that waited for it
-        if (a.early_w)
-            for (int i = 0; i < pre; ++i) issue_w(i);
+        // w and x are complete when this grid starts behind a kernel that waited for their writers
+        if (a.early)
+            for (int i = 0; i < pre; ++i) {
+                issue_w(i);
+                issue_x(i);
+            }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, a.tmem_cols);
@@ -134,12 +187,12 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
 
     if (warp == 0) {
         if (lane == 0) {
-            pdl_wait();
-            int issued = 0;
-            for (int i = 0; i < nkb; ++i) {
+            if (!a.early) pdl_wait();
+            int issued = a.early ? pre : 0;
+            for (int i = issued; i < nkb; ++i) {
                 const int s = i % stages;
                 if (i >= stages && !mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)) break;
-                if (!a.early_w || i >= pre) issue_w(i);
+                issue_w(i);
                 issue_x(i);
                 ++issued;
             }
@@ -163,16 +216,9 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     break;
                 }
                 tc_fence_after();
-                const uint32_t wa = smem_u32(smem + (size_t)s * stage_bytes), sw = wa + kDWBytes;
-                const uint32_t xa = sw + kDSwBytes, sx = xa + x_bytes;
+                const uint32_t wa = smem_u32(smem + (size_t)s * stage_bytes), xa = wa + kDWBytes;
                 // each stage has its own scale columns: w's two tiles (4 each), x's two (8 each)
                 const uint32_t sfw = tmem + static_cast<uint32_t>(n_pad + s * 24), sfx = sfw + 8;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    tmem_cp_scales(sfw + 4 * j, sdesc_scales(sw + 512 * j));
-                    tmem_cp_scales(sfx + 8 * j, sdesc_scales(sx + 512 * j));
-                    if (xt == 2) tmem_cp_scales(sfx + 8 * j + 4, sdesc_scales(sx + 1024 + 512 * j));
-                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     umma_mxf4(tmem, sdesc_sw128(wa + k * 32), sdesc_sw128(xa + k * 32), (k & 1) ? id2 : id0,
@@ -232,6 +278,10 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 int at = before[lt];
                 for (uint32_t m = seen[lt]; m; m &= m - 1) dlist[at++] = lt * 32 + __ffs(m) - 1;
             }
+            for (int i = lt; i < 256; i += 128) {
+                const int sl = slot_sm[i];
+                dl_sm[i] = sl < 0 ? -1 : before[sl >> 5] + __popc(seen[sl >> 5] & ((1u << (sl & 31)) - 1u));
+            }
             named_bar_sync(2, 128);
             const int P_all = (before[63] + __popc(seen[63])) * chunks;
             const int blocks_all = (P_all + kDChunks - 1) / kDChunks;
@@ -261,20 +311,14 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     ok = __all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((b >> 1) & 1) ^ 1, flags));
                     if (ok && lt == 0) issue_b(b);
                 }
-                // token side: 16 bytes a token and chunk
-                if (ok)
-                    for (int t = lt; t < n_pad; t += 128) {
-                        const int slot = slot_sm[t];
-#pragma unroll
-                        for (int j = 0; j < kDChunks; ++j) {
-                            const int d = (p0 + j) / chunks, c = (p0 + j) - d * chunks;
-                            uint4 v = make_uint4(0, 0, 0, 0);
-                            if (p0 + j < P_all && slot == dlist[d]) {
-                                v = sum_parts8<T>(a.s_in + (size_t)t * a.R + c * 8, a.s_parts, (size_t)n * a.R);
-                            }
-                            *reinterpret_cast<uint4*>(blk + kDChunks * 2048 + j * schunk + t * 16) = v;
-                        }
-                    }
+                // token side: 16 bytes a token and chunk; several parts of one, or one part of several, at once
+                if (ok) {
+                    uint8_t* S = blk + kDChunks * 2048;
+                    if (a.s_parts > 1)
+                        build_tokens<T, 2, 4>(a, S, schunk, dl_sm, p0, chunks, lt);
+                    else
+                        build_tokens<T, 8, 1>(a, S, schunk, dl_sm, p0, chunks, lt);
+                }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(&lora_tma[lbuf], (b >> 1) & 1, flags));
                 if (!ok) break;
 #pragma unroll
@@ -310,6 +354,51 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         }
     }
 
+    if (warp >= 2 && warp < 6) {
+        // ---- scales: each warp fills its 32 lanes (the four hold the same), two steps' loads ahead ----
+        if (!a.early) pdl_wait();
+        const uint32_t taddr = tmem + static_cast<uint32_t>(n_pad) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint4* pw = reinterpret_cast<const uint4*>(a.sw + ((size_t)m_tile * a.kt + 2 * kb0) * 512) + lane;
+        const uint4* px = reinterpret_cast<const uint4*>(a.sx + (size_t)(2 * kb0) * 512) + lane;
+        const uint4* px2 = px + (size_t)a.kt * 32;
+        uint4 v[2][6];
+        auto load = [&](int i, uint4 (&u)[6]) {
+            if (i >= nkb) return;
+            u[0] = __ldg(pw + i * 64);
+            u[1] = __ldg(pw + i * 64 + 32);
+            u[2] = __ldcg(px + i * 64);
+            u[3] = __ldcg(px + i * 64 + 32);
+            if (xt2) {
+                u[4] = __ldcg(px2 + i * 64);
+                u[5] = __ldcg(px2 + i * 64 + 32);
+            }
+        };
+#pragma unroll
+        for (int e = 0; e < 6; ++e) v[0][e] = v[1][e] = make_uint4(0, 0, 0, 0);
+        load(0, v[0]);
+        load(1, v[1]);
+        for (int i = 0; i < nkb; i += 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (i + h >= nkb) break;
+                const int s = (i + h) % stages;
+                // the columns' last readers
+                if (i + h >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (((i + h) / stages) & 1) ^ 1, flags)))
+                    break;  // aborted: the other waits end the same way
+                tc_fence_after();
+                const uint32_t t = taddr + static_cast<uint32_t>(s * 24);
+                tmem_st8(t, v[h][0], v[h][1]);
+                tmem_st8(t + 8, v[h][2], v[h][4]);
+                tmem_st8(t + 16, v[h][3], v[h][5]);
+                load(i + 2 + h, v[h]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
+        }
+    }
+
     bool store = false;
     if (warp >= 2) {
         pdl_wait();
@@ -333,8 +422,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                         for (int c = 0; c < 16; ++c) {
                             const int t = c0 + c, slot = t < n ? slot_sm[t] : -1;
                             if (slot < 0) continue;
-                            const int w = slot >> 5;
-                            const int d = before[w] + __popc(seen[w] & ((1u << (slot & 31)) - 1u));
+                            const int d = dl_sm[t];
                             for (int k8 = 0; k8 < chunks; ++k8) {
                                 const int p = d * chunks + k8;
                                 if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
@@ -346,15 +434,8 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                         }
                     }
                 }
-                if (a.splits == 1) {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        if (store && c0 + c < n && o < a.h_out)
-                            y[(long long)(c0 + c) * a.ldy + o] = from_f32<T>(__uint_as_float(r[c]));
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
-                }
+                for (int c = 0; c < 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
             }
         } else if (lane == 0) {
             flags[0] = 1;
@@ -362,36 +443,60 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
-    if (a.splits > 1) {
-        // each CTA adds up the partial sums of its share of the tokens, in split order
-        const bool good = flags[0] == 0;
-        cluster_sync();
-        if (warp >= 2 && good && store) {
-            const int rt = threadIdx.x - 64, row = rt & 127, o = m_tile * kDM + row;
-            const int per = (n + a.splits - 1) / a.splits;
-            const int t_end = min(n, (split + 1) * per);
-            for (int t0 = split * per + (rt >> 7); t0 < t_end; t0 += 16) {
-                float v[8] = {};
-                for (int c = 0; c < a.splits; ++c) {
-                    const uint32_t base = mapa_shared(smem_u32(P + row), static_cast<uint32_t>(c));
-                    float u[8];
+    // each CTA adds up the partial sums of its share of the tokens, in split order, and stores them:
+    // 8 features a thread, 16 neighbouring threads a token's 128
+    const bool good = flags[0] == 0;
+    if (a.splits > 1) cluster_sync();
+    if (warp >= 2 && good && store) {
+        const int per = (n + a.splits - 1) / a.splits;
+        const int beg = split * per * 16, end = min(n, (split + 1) * per) * 16;
+        for (int e = beg + (int)threadIdx.x - 64; e < end; e += 256) {
+            const int t = e >> 4, o8 = (e & 15) * 8, o = m_tile * kDM + o8;
+            const float* own = P + t * kDM + o8;
+            float v[8];
+            if (a.splits == 1) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = t0 + 2 * i < t_end ? ld_dsmem_f32(base + (t0 + 2 * i) * (kDM * 4)) : 0.f;
+                for (int i = 0; i < 8; ++i) v[i] = own[i];
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] += u[i];
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                for (int c0 = 0; c0 < a.splits; c0 += 4) {  // four CTAs' loads in flight
+                    float4 lo[4], hi[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t at = mapa_shared(smem_u32(own), static_cast<uint32_t>(min(c0 + c, a.splits - 1)));
+                        lo[c] = ld_dsmem_f32x4(at);
+                        hi[c] = ld_dsmem_f32x4(at + 16);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c0 + c < a.splits) {
+                            v[0] += lo[c].x, v[1] += lo[c].y, v[2] += lo[c].z, v[3] += lo[c].w;
+                            v[4] += hi[c].x, v[5] += hi[c].y, v[6] += hi[c].z, v[7] += hi[c].w;
+                        }
                 }
+            }
+            T* yp = y + (long long)t * a.ldy + o;
+            alignas(16) T w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = from_f32<T>(v[i]);
+            if (a.vec && o + 8 <= a.h_out) {
+#pragma unroll
+                for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i)
+                    reinterpret_cast<uint4*>(yp)[i] = reinterpret_cast<const uint4*>(w)[i];
+            } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (t0 + 2 * i < t_end && o < a.h_out) y[(long long)(t0 + 2 * i) * a.ldy + o] = from_f32<T>(v[i]);
+                    if (o + i < a.h_out) yp[i] = w[i];
             }
         }
-        cluster_sync();  // no CTA leaves while its partial sums may still be read
     }
+    if (a.splits > 1) cluster_sync();  // no CTA leaves while its partial sums may still be read
     if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
 }
 
 template <typename T>
-static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, bool early_w,
+static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, bool early,
                                const Fp4DecodeLora* lora, cudaStream_t st) {
     Fp4DecodeArgs a;
     memset(&a, 0, sizeof(a));
@@ -405,7 +510,9 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
     a.h_out = w.rows;
     a.kt = x.ktiles;
     a.kb_total = x.ktiles / 2;
-    a.early_w = early_w;
+    a.early = early;
+    // y is written 16 bytes at a time when every row starts on a 16-byte boundary
+    a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     const int m_tiles = (w.rows + kDM - 1) / kDM;
     int splits = std::max(1, num_sms() / m_tiles);
     splits = std::min({splits, 8, a.kb_total});
@@ -422,9 +529,9 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
         a.idx = lora->idx;
         a.B = pv.B;
     }
-    const size_t stage_bytes = kDWBytes + kDSwBytes + (size_t)a.n_pad * 128 + (a.n_pad > 128 ? 2048 : 1024);
+    const size_t stage_bytes = kDWBytes + (size_t)a.n_pad * 128;
     const size_t fixed = (lora ? 2 * (size_t)kDChunks * (2048 + a.n_pad * 16) : 0) + kDScratch + kDBars + 1024;
-    const size_t park = a.splits > 1 ? (size_t)a.n_pad * kDM * 4 : 0;
+    const size_t park = (size_t)a.n_pad * kDM * 4;
     int stages = (int)((227 * 1024 - fixed) / stage_bytes);
     stages = std::min({stages, 8, a.kb_per_split});
     while ((size_t)stages * stage_bytes < park) ++stages;  // (park is at most 128 KB, 2.5 stages of its size)
@@ -469,11 +576,11 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
 }  // namespace tc
 
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
-                      bool early_w, const Fp4DecodeLora* lora, cudaStream_t st) {
+                      bool early, const Fp4DecodeLora* lora, cudaStream_t st) {
     switch (dtype) {
-        case LORA_F32: return tc::launch_fp4_decode_t<float>(x, w, y, ldy, status, early_w, nullptr, st);
-        case LORA_F16: return tc::launch_fp4_decode_t<__half>(x, w, y, ldy, status, early_w, lora, st);
-        default: return tc::launch_fp4_decode_t<__nv_bfloat16>(x, w, y, ldy, status, early_w, lora, st);
+        case LORA_F32: return tc::launch_fp4_decode_t<float>(x, w, y, ldy, status, early, nullptr, st);
+        case LORA_F16: return tc::launch_fp4_decode_t<__half>(x, w, y, ldy, status, early, lora, st);
+        default: return tc::launch_fp4_decode_t<__nv_bfloat16>(x, w, y, ldy, status, early, lora, st);
     }
 }
 

@@ -199,12 +199,21 @@ template <typename T> __device__ __forceinline__ float nonfinite_dot8(const uint
 
 // Eight shrink values summed over their K parts, rounded to the 16-bit type.
 template <typename T> __device__ __forceinline__ uint4 sum_parts8(const float* s, int parts, size_t stride) {
-    float4 a = __ldcg(reinterpret_cast<const float4*>(s)), b = __ldcg(reinterpret_cast<const float4*>(s) + 1);
-    for (int k = 1; k < parts; ++k) {
-        const float4 c = __ldcg(reinterpret_cast<const float4*>(s + k * stride));
-        const float4 d = __ldcg(reinterpret_cast<const float4*>(s + k * stride) + 1);
-        a.x += c.x, a.y += c.y, a.z += c.z, a.w += c.w;
-        b.x += d.x, b.y += d.y, b.z += d.z, b.w += d.w;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int k0 = 0; k0 < parts; k0 += 4) {  // four parts' loads in flight
+        float4 c[4], d[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float4* p = reinterpret_cast<const float4*>(s + min(k0 + k, parts - 1) * stride);
+            c[k] = __ldcg(p);
+            d[k] = __ldcg(p + 1);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k0 + k < parts) {
+                a.x += c[k].x, a.y += c[k].y, a.z += c[k].z, a.w += c[k].w;
+                b.x += d[k].x, b.y += d[k].y, b.z += d[k].z, b.w += d[k].w;
+            }
     }
     alignas(16) T v[8] = {from_f32<T>(a.x), from_f32<T>(a.y), from_f32<T>(a.z), from_f32<T>(a.w),
                           from_f32<T>(b.x), from_f32<T>(b.y), from_f32<T>(b.z), from_f32<T>(b.w)};

@@ -111,7 +111,8 @@ struct Fp4Lora {
     const void* B;
     int R;
 };
-// Up to 256 tokens.  lora: the pool, the slot of each token and the shrink output in K parts.
+// Up to 256 tokens.  early: every kernel that could have written w or x has completed when this grid
+// starts (only the shrink output is waited for).  lora: the pool, the slot of each token and the shrink output in K parts.
 struct Fp4DecodeLora {
     const PoolView* pool;
     const int32_t* idx;
@@ -119,7 +120,7 @@ struct Fp4DecodeLora {
     int s_parts;
 };
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
-                      bool early_w, const Fp4DecodeLora* lora, cudaStream_t st);
+                      bool early, const Fp4DecodeLora* lora, cudaStream_t st);
 // More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
