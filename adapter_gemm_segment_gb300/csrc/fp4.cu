@@ -143,6 +143,94 @@ fp4_dequantize_kernel(Fp4View q, T* __restrict__ out, long long ld) {
     }
 }
 
+// ---- before the product of a small batch: x quantised and the per-token shrink, one launch -------
+// One CTA per (token, 8 adapter rows, K part), 128 threads with 8 consecutive features each in sweeps
+// of 1024, as the framework's per-token shrink; the CTAs of the first 8 rows also quantise the features
+// they hold.  Bound by latency: a chain of slot, A rows and a reduction.
+template <typename T>
+__global__ void __launch_bounds__(128)
+fp4_front_kernel(PoolView pool, SegView seg, const T* __restrict__ x, Fp4View q, float* __restrict__ s_out) {
+    __shared__ float red[4][8];
+    pdl_wait();
+    pdl_trigger();
+    const int t = blockIdx.x, g = blockIdx.y, ks = blockIdx.z;
+    const int h = pool.h_in, R = pool.R, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int width = q.ktiles * 128;  // the last block of scale tiles is filled up with zeros
+    const int sweeps = ((width + 1023) / 1024 + gridDim.z - 1) / gridDim.z;
+    const int k_beg = ks * sweeps * 1024, k_end = min(width, k_beg + sweeps * 1024);
+    // independent loads first
+    const int status = __ldcg(seg.status);
+    const int slot = __ldcg(seg.idx + t);
+    const bool lora = slot >= 0 && status == LORA_OK && g * 8 < R;
+    const SlotEntry e = lora ? pool.table[slot] : SlotEntry{0, 0, 0.f, 0};
+    const T* xr = x + (size_t)t * h;
+    const T* Ab = static_cast<const T*>(pool.A) + ((size_t)max(slot, 0) * R + (size_t)g * 8) * h;
+    const bool rows = lora && g * 8 < e.rank;  // rows past the adapter's rank are zeros
+    const bool store = g == 0 && q.codes != nullptr && status == LORA_OK;
+    float acc[8] = {};
+    for (int k0 = k_beg; k0 < k_end; k0 += 1024) {
+        const int k = k0 + threadIdx.x * 8;
+        Raw8<T> v[2];
+        v[0].v = v[1].v = make_uint4(0, 0, 0, 0);
+        uint4 av[8];
+        if (k < h) {
+            v[0].v = __ldcg(reinterpret_cast<const uint4*>(xr + k));
+            if (rows)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) av[r] = __ldg(reinterpret_cast<const uint4*>(Ab + (size_t)r * h + k));
+        }
+        if (store) {
+            uint32_t codes[2], words[2];
+            quantise_rows<T, 2>(v, codes, words, lane);
+            if (k / 32 < q.blocks) *reinterpret_cast<uint32_t*>(q.codes + (size_t)t * q.pitch + k / 2) = codes[0];
+            if ((lane & 15) == 0 && k < width)
+                *reinterpret_cast<uint32_t*>(q.scales + ((size_t)(t / 128) * q.ktiles + k / 128) * 512 + (t % 32) * 16 +
+                                             (t % 128) / 32 * 4) = words[0];
+        }
+        if (rows && k < h) {
+            float xf[8];
+            unpack8<T>(v[0].v, xf);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                float af[8];
+                unpack8<T>(av[r], af);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[r] = fmaf(xf[i], af[i], acc[r]);
+            }
+        }
+    }
+    if (!lora) return;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        float v = acc[r];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if (lane == 0) red[warp][r] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x < 8) {
+        const int r = threadIdx.x;
+        s_out[((size_t)ks * seg.n + t) * R + g * 8 + r] = e.scale * (red[0][r] + red[1][r] + red[2][r] + red[3][r]);
+    }
+}
+
+template <typename T>
+static int launch_front_t(const PoolView& pv, const SegView& sv, const void* x, const Fp4View& q, float* s_out,
+                          int s_parts, cudaStream_t st) {
+    const T* xp = static_cast<const T*>(x);
+    void* args[] = {(void*)&pv, (void*)&sv, (void*)&xp, (void*)&q, (void*)&s_out};
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_front_kernel<T>, dim3(sv.n, pv.R / 8, s_parts), dim3(128), 0, st, args));
+    return LORA_OK;
+}
+
+int launch_fp4_front(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* q, float* s_out, int* s_parts,
+                     cudaStream_t st) {
+    *s_parts = shrink_parts(pv, sv.n, false);
+    const Fp4View view = q ? *q : fp4_view(nullptr, nullptr, sv.n, pv.h_in);
+    if (pv.dtype == LORA_F16) return launch_front_t<__half>(pv, sv, x, view, s_out, *s_parts, st);
+    return launch_front_t<__nv_bfloat16>(pv, sv, x, view, s_out, *s_parts, st);
+}
+
 static dim3 fp4_grid(const Fp4View& q) {
     return dim3(q.ktiles / 2, 4, (q.rows + 127) / 128);
 }
@@ -179,7 +267,7 @@ static int dequantize_t(const Fp4View& q, void* out, long long ld, cudaStream_t 
 
 static int launch_fp4_product(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                               bool early_w, cudaStream_t st) {
-    return x.rows <= 256 ? launch_fp4_decode(x, w, y, dtype, ldy, status, early_w, nullptr, st)
+    return x.rows <= 256 ? launch_fp4_decode(x, w, y, dtype, ldy, status, early_w ? 2 : 0, nullptr, st)
                          : launch_fp4_pair(x, w, y, dtype, ldy, status, early_w, nullptr, st);
 }
 
@@ -336,17 +424,30 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         const Fp4Lora lora = {sv.perm, sv.idx, ws + L.s16_off, pv.B, pv.R};
         return launch_fp4_pair(own, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     }
+    int s_parts = 1;
+    if (pv.dtype != LORA_F32) {
+        // One kernel quantises x and computes the per-token shrink; the product behind it streams its
+        // weight meanwhile.  Where the shrink reads each adapter once per 4 tokens instead (many rows of
+        // A), x is quantised first and the product's main loop overlaps the shrink.
+        int early = 1;
+        if (shrink_segmented(pv, n)) {
+            if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
+            if (!rc) rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/false, &s_parts);
+            early = 2;
+        } else {
+            rc = launch_fp4_front(pv, sv, x_dev, xq ? nullptr : &q, s_buf, &s_parts, st);
+            if (xq) early = 2;
+        }
+        if (rc) return rc;
+        const Fp4DecodeLora lora = {&pv, sv.idx, s_buf, s_parts};
+        return launch_fp4_decode(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, early, &lora, st);
+    }
     if (!xq) {
         rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (rc) return rc;
     }
-    int s_parts = 1;
     rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
     if (rc) return rc;
-    if (pv.dtype != LORA_F32) {
-        const Fp4DecodeLora lora = {&pv, sv.idx, s_buf, s_parts};
-        return launch_fp4_decode(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
-    }
     // float32 pools: the LoRA term in float32, by the expand kernel
     rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
     if (rc) return rc;

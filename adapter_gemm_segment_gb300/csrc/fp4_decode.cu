@@ -32,7 +32,7 @@ namespace tc {
 using namespace ptx;
 
 constexpr int kDM = 128;         // features per tile
-constexpr int kDThreads = 320;   // warp 0 loads, 1 MMAs, 2-5 scales, then accumulator, 6-9 LoRA blocks
+constexpr int kDThreads = 320;   // warp 0 loads, 1 MMAs, 2-5 scales, 2-9 LoRA blocks, 2-5 accumulator
 constexpr uint32_t kDWBytes = kDM * 128;
 constexpr int kDChunks = 4;      // 8-column chunks per LoRA block
 constexpr int kDScratch = 64 * 4 + 64 * 4 + 3 * 256 * 4 + 1024;
@@ -44,7 +44,7 @@ struct Fp4DecodeArgs {
     void* y;
     int32_t* status;      // nullable
     long long ldy;
-    int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, tmem_cols, kt, early, vec;
+    int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, tmem_cols, kt, early_w, early_x, vec, ring_bytes, push;
     // the LoRA term (fuse)
     int fuse, R, s_parts, bf16;
     const float* s_in;    // [s_parts][n][R]
@@ -60,13 +60,13 @@ template <typename T, int U, int K>
 __device__ __forceinline__ void build_tokens(const Fp4DecodeArgs& a, uint8_t* S, uint32_t schunk, const int* dl, int p0,
                                              int chunks, int lt) {
     const size_t part = (size_t)a.n * a.R;
-    for (int e0 = lt; e0 < a.n_pad * kDChunks; e0 += 128 * U) {
+    for (int e0 = lt; e0 < a.n_pad * kDChunks; e0 += 256 * U) {
         float4 lo[U], hi[U];
         bool mine[U];
         const float* src[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int e = e0 + 128 * u, t = min(e / kDChunks, a.n - 1);
+            const int e = e0 + 256 * u, t = min(e / kDChunks, a.n - 1);
             const int c = p0 + e % kDChunks - dl[t] * chunks;
             mine[u] = e / kDChunks < a.n && dl[t] >= 0 && c >= 0 && c < chunks;
             src[u] = a.s_in + (size_t)t * a.R + max(0, min(c, chunks - 1)) * 8;
@@ -93,7 +93,7 @@ __device__ __forceinline__ void build_tokens(const Fp4DecodeArgs& a, uint8_t* S,
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int e = e0 + 128 * u;
+            const int e = e0 + 256 * u;
             if (e >= a.n_pad * kDChunks) break;
             alignas(16) T v[8] = {from_f32<T>(lo[u].x), from_f32<T>(lo[u].y), from_f32<T>(lo[u].z), from_f32<T>(lo[u].w),
                                   from_f32<T>(hi[u].x), from_f32<T>(hi[u].y), from_f32<T>(hi[u].z), from_f32<T>(hi[u].w)};
@@ -116,7 +116,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     const uint32_t schunk = static_cast<uint32_t>(n_pad) * 16;                 // token side of a chunk
     const uint32_t lora_bytes = a.fuse ? kDChunks * (2048 + schunk) : 0;
     uint8_t* lora_sm = smem + (size_t)stages * stage_bytes;                    // [2] {features, tokens}
-    uint32_t* seen = reinterpret_cast<uint32_t*>(lora_sm + 2 * lora_bytes);    // [64]
+    uint32_t* seen = reinterpret_cast<uint32_t*>(smem + a.ring_bytes);         // [64]
     int* before = reinterpret_cast<int*>(seen + 64);                           // [64]
     int* dlist = before + 64;                                                  // [256]
     int* slot_sm = dlist + 256;                                                // [256] slot of each token
@@ -126,11 +126,12 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     uint64_t* empty = full + stages;
     uint64_t* acc_full = empty + stages;
     uint64_t* lora_tma = acc_full + 1;    // [2] feature side landed
-    uint64_t* lora_full = lora_tma + 2;   // [2] block complete (4 warps)
+    uint64_t* lora_full = lora_tma + 2;   // [2] block complete (8 warps)
     uint64_t* lora_empty = lora_full + 2; // [2]
     uint64_t* linfo = lora_empty + 2;     // number of LoRA blocks known
-    uint64_t* lora_done = linfo + 1;      // slots, bad chunks: complete (4 warps)
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(lora_done + 1);
+    uint64_t* lora_done = linfo + 1;      // slots, bad chunks: complete (8 warps)
+    uint64_t* rbar = lora_done + 1;       // the other CTAs' sums of this CTA's tokens have arrived
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + 1);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort, LoRA blocks, any bad chunk
     float* P = reinterpret_cast<float*>(smem);  // after the main loop: [n_pad][128] (partial) sums
 
@@ -159,20 +160,22 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         mbar_init(acc_full, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&lora_tma[b], 1);
-            mbar_init(&lora_full[b], 4);
+            mbar_init(&lora_full[b], 8);
             mbar_init(&lora_empty[b], 1);
         }
         mbar_init(linfo, 1);
-        mbar_init(lora_done, 4);
+        mbar_init(lora_done, 8);
+        mbar_init(rbar, 1);
         flags[0] = flags[1] = flags[2] = 0;
         fence_barrier_init();
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmX);
-        // w and x are complete when this grid starts behind a kernel that waited for their writers
-        if (a.early)
+        // what is complete when this grid starts, behind a kernel that waited for its writers, is
+        // loaded at once: the weight, or also x where it was stored before that kernel
+        if (a.early_w)
             for (int i = 0; i < pre; ++i) {
                 issue_w(i);
-                issue_x(i);
+                if (a.early_x) issue_x(i);
             }
     }
     if (warp == 1) {
@@ -187,8 +190,16 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
 
     if (warp == 0) {
         if (lane == 0) {
-            if (!a.early) pdl_wait();
-            int issued = a.early ? pre : 0;
+            int issued = 0;
+            if (a.early_w) {
+                if (!a.early_x) {
+                    pdl_wait();
+                    for (int i = 0; i < pre; ++i) issue_x(i);
+                }
+                issued = pre;
+            } else {
+                pdl_wait();
+            }
             for (int i = issued; i < nkb; ++i) {
                 const int s = i % stages;
                 if (i >= stages && !mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)) break;
@@ -247,46 +258,79 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             if (!ok && a.status) report_timeout_status(a.status);
             umma_commit(acc_full);  // also on abort: fires once the issued MMAs have finished
         }
-    } else if (warp >= 6 && a.fuse) {
+    }
+
+    if (warp >= 2 && warp < 6) {
+        // ---- scales: each warp fills its 32 lanes (the four hold the same), four steps' loads ahead ----
+        if (!a.early_w) pdl_wait();
+        const uint32_t taddr = tmem + static_cast<uint32_t>(n_pad) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint4* pw = reinterpret_cast<const uint4*>(a.sw + ((size_t)m_tile * a.kt + 2 * kb0) * 512) + lane;
+        const uint4* px = reinterpret_cast<const uint4*>(a.sx + (size_t)(2 * kb0) * 512) + lane;
+        const uint4* px2 = px + (size_t)a.kt * 32;
+        constexpr int kAhead = 4;
+        uint4 v[kAhead][6];
+        auto load_w = [&](int i, uint4 (&u)[6]) {
+            if (i >= nkb) return;
+            u[0] = __ldg(pw + i * 64);
+            u[1] = __ldg(pw + i * 64 + 32);
+        };
+        auto load_x = [&](int i, uint4 (&u)[6]) {
+            if (i >= nkb) return;
+            u[2] = __ldcg(px + i * 64);
+            u[3] = __ldcg(px + i * 64 + 32);
+            if (xt2) {
+                u[4] = __ldcg(px2 + i * 64);
+                u[5] = __ldcg(px2 + i * 64 + 32);
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) {
+#pragma unroll
+            for (int e = 0; e < 6; ++e) v[h][e] = make_uint4(0, 0, 0, 0);
+            load_w(h, v[h]);
+        }
+        if (a.early_w && !a.early_x) pdl_wait();
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h) load_x(h, v[h]);
+        // two steps per wait for the stores, whose latency (some 400 ns) is otherwise a step's
+        for (int i0 = 0; i0 < nkb; i0 += kAhead) {
+#pragma unroll
+            for (int g = 0; g < kAhead; g += 2) {
+                if (i0 + g >= nkb) break;
+                bool ok = true;
+#pragma unroll
+                for (int h = g; h < g + 2; ++h) {
+                    const int i = i0 + h, s = i % stages;
+                    if (i >= nkb) break;
+                    // the columns' last readers
+                    ok = ok && (i < stages || __all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)));
+                    tc_fence_after();
+                    const uint32_t t = taddr + static_cast<uint32_t>(s * 24);
+                    if (ok) {
+                        tmem_st8(t, v[h][0], v[h][1]);
+                        tmem_st8(t + 8, v[h][2], v[h][4]);
+                        tmem_st8(t + 16, v[h][3], v[h][5]);
+                    }
+                    load_w(i + kAhead, v[h]);
+                    load_x(i + kAhead, v[h]);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (!ok) break;  // aborted: the other waits end the same way
+                if (lane == 0) {
+                    mbar_arrive(&full[(i0 + g) % stages]);
+                    if (i0 + g + 1 < nkb) mbar_arrive(&full[(i0 + g + 1) % stages]);
+                }
+            }
+        }
+    }
+
+    if (warp >= 2 && a.fuse) {
         // ---- LoRA blocks: this CTA's share of the batch's (adapter, 8 columns) chunks ----
         if constexpr (sizeof(T) == 2) {
-            const int lt = threadIdx.x - 192;
             const int chunks = a.R / 8;
-            const bool st_ok = __ldcg(a.status) == LORA_OK;  // the segments are older than the kernel ahead
-            if (lt < 64) seen[lt] = 0;
-            for (int i = lt; i < 256; i += 128) {
-                badmap[i] = 0;
-                slot_sm[i] = st_ok && i < n ? __ldcg(a.idx + i) : -1;
-            }
-            named_bar_sync(2, 128);
-            for (int i = lt; i < 256; i += 128)
-                if (slot_sm[i] >= 0) atomicOr(&seen[slot_sm[i] >> 5], 1u << (slot_sm[i] & 31));
-            named_bar_sync(2, 128);
-            if (lt < 32) {
-                const int p0 = __popc(seen[2 * lt]), p1 = __popc(seen[2 * lt + 1]);
-                int v = p0 + p1;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, v, d);
-                    if (lt >= d) v += o;
-                }
-                before[2 * lt] = v - p0 - p1;
-                before[2 * lt + 1] = v - p1;
-            }
-            named_bar_sync(2, 128);
-            if (lt < 64) {
-                int at = before[lt];
-                for (uint32_t m = seen[lt]; m; m &= m - 1) dlist[at++] = lt * 32 + __ffs(m) - 1;
-            }
-            for (int i = lt; i < 256; i += 128) {
-                const int sl = slot_sm[i];
-                dl_sm[i] = sl < 0 ? -1 : before[sl >> 5] + __popc(seen[sl >> 5] & ((1u << (sl & 31)) - 1u));
-            }
-            named_bar_sync(2, 128);
-            const int P_all = (before[63] + __popc(seen[63])) * chunks;
-            const int blocks_all = (P_all + kDChunks - 1) / kDChunks;
-            const int blocks = blocks_all > split ? (blocks_all - split - 1) / a.splits + 1 : 0;
-            auto issue_b = [&](int b) {  // the feature side of this CTA's block b
+            auto issue_b = [&](int b, int P_all) {  // the feature side of this CTA's block b
                 const int p0 = (split + b * a.splits) * kDChunks, cnt = min(kDChunks, P_all - p0);
                 uint64_t* bar = &lora_tma[b & 1];
                 mbar_arrive_expect_tx(bar, static_cast<uint32_t>(cnt) * 2048);
@@ -296,11 +340,59 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                                     dlist[d] * a.h_out + m_tile * kDM);
                 }
             };
-            if (lt == 0) {
+            if (warp >= 6) {
+                // the batch's adapters, while the scale warps and the kernel ahead are at work (the
+                // segments are older than that kernel)
+                const int lt = threadIdx.x - 192;
+                const bool st_ok = __ldcg(a.status) == LORA_OK;
+                if (lt < 64) seen[lt] = 0;
+                int slot[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = lt + 128 * h;
+                    slot[h] = st_ok && t < n ? __ldcg(a.idx + t) : -1;
+                    slot_sm[t] = slot[h];
+                    badmap[t] = 0;
+                }
+                named_bar_sync(2, 128);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (slot[h] >= 0) atomicOr(&seen[slot[h] >> 5], 1u << (slot[h] & 31));
+                named_bar_sync(2, 128);
+                if (lt < 32) {  // words 2 lt and 2 lt + 1
+                    const uint32_t w0 = seen[2 * lt], w1 = seen[2 * lt + 1];
+                    int v = __popc(w0) + __popc(w1);
+                    const int own = v;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, v, d);
+                        if (lt >= d) v += o;
+                    }
+                    int at = v - own;
+                    before[2 * lt] = at;
+                    for (uint32_t m = w0; m; m &= m - 1) dlist[at++] = 2 * lt * 32 + __ffs(m) - 1;
+                    before[2 * lt + 1] = at;
+                    for (uint32_t m = w1; m; m &= m - 1) dlist[at++] = (2 * lt + 1) * 32 + __ffs(m) - 1;
+                }
+                named_bar_sync(2, 128);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    dl_sm[lt + 128 * h] =
+                        slot[h] < 0 ? -1 : before[slot[h] >> 5] + __popc(seen[slot[h] >> 5] & ((1u << (slot[h] & 31)) - 1u));
+            }
+            const int lt = threadIdx.x - 64;  // 0..255
+            auto count_blocks = [&](int P_all) {
+                const int all = (P_all + kDChunks - 1) / kDChunks;
+                return all > split ? (all - split - 1) / a.splits + 1 : 0;
+            };
+            if (threadIdx.x == 192) {
+                const int P_all = (before[63] + __popc(seen[63])) * chunks, blocks = count_blocks(P_all);
                 flags[1] = blocks;
                 mbar_arrive(linfo);
-                for (int b = 0; b < min(blocks, 2); ++b) issue_b(b);
+                for (int b = 0; b < min(blocks, 2); ++b) issue_b(b, P_all);
             }
+            named_bar_sync(3, 256);  // the scale warps join
+            const int P_all = (before[63] + __popc(seen[63])) * chunks, blocks = count_blocks(P_all);
             pdl_wait();  // s
             bool ok = true;
             for (int b = 0; b < blocks; ++b) {
@@ -309,7 +401,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 if (b >= 2) {
                     // the block two before is consumed; its feature side may be overwritten
                     ok = __all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((b >> 1) & 1) ^ 1, flags));
-                    if (ok && lt == 0) issue_b(b);
+                    if (ok && threadIdx.x == 192) issue_b(b, P_all);
                 }
                 // token side: 16 bytes a token and chunk; several parts of one, or one part of several, at once
                 if (ok) {
@@ -317,13 +409,14 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     if (a.s_parts > 1)
                         build_tokens<T, 2, 4>(a, S, schunk, dl_sm, p0, chunks, lt);
                     else
-                        build_tokens<T, 8, 1>(a, S, schunk, dl_sm, p0, chunks, lt);
+                        build_tokens<T, 4, 1>(a, S, schunk, dl_sm, p0, chunks, lt);
                 }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(&lora_tma[lbuf], (b >> 1) & 1, flags));
                 if (!ok) break;
 #pragma unroll
-                for (int j = 0; j < kDChunks; ++j) {
-                    uint4* bp = reinterpret_cast<uint4*>(blk + j * 2048 + lt * 16);
+                for (int jj = 0; jj < kDChunks / 2; ++jj) {
+                    const int j = 2 * jj + (lt >> 7);
+                    uint4* bp = reinterpret_cast<uint4*>(blk + j * 2048 + (lt & 127) * 16);
                     if (p0 + j >= P_all) {
                         *bp = make_uint4(0, 0, 0, 0);
                     } else {
@@ -344,57 +437,12 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             if (!ok) {
                 if (a.status) report_timeout_status(a.status);
                 // boxes in flight land before the CTA leaves
-                if (lt == 0)
+                if (threadIdx.x == 192)
                     for (int b = 0; b < 2; ++b) {
                         const unsigned long long t0 = globaltimer();
                         while (!mbar_try_wait(&lora_tma[b], 0) && globaltimer() - t0 < kWaitLimitNs) {
                         }
                     }
-            }
-        }
-    }
-
-    if (warp >= 2 && warp < 6) {
-        // ---- scales: each warp fills its 32 lanes (the four hold the same), two steps' loads ahead ----
-        if (!a.early) pdl_wait();
-        const uint32_t taddr = tmem + static_cast<uint32_t>(n_pad) + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const uint4* pw = reinterpret_cast<const uint4*>(a.sw + ((size_t)m_tile * a.kt + 2 * kb0) * 512) + lane;
-        const uint4* px = reinterpret_cast<const uint4*>(a.sx + (size_t)(2 * kb0) * 512) + lane;
-        const uint4* px2 = px + (size_t)a.kt * 32;
-        uint4 v[2][6];
-        auto load = [&](int i, uint4 (&u)[6]) {
-            if (i >= nkb) return;
-            u[0] = __ldg(pw + i * 64);
-            u[1] = __ldg(pw + i * 64 + 32);
-            u[2] = __ldcg(px + i * 64);
-            u[3] = __ldcg(px + i * 64 + 32);
-            if (xt2) {
-                u[4] = __ldcg(px2 + i * 64);
-                u[5] = __ldcg(px2 + i * 64 + 32);
-            }
-        };
-#pragma unroll
-        for (int e = 0; e < 6; ++e) v[0][e] = v[1][e] = make_uint4(0, 0, 0, 0);
-        load(0, v[0]);
-        load(1, v[1]);
-        for (int i = 0; i < nkb; i += 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (i + h >= nkb) break;
-                const int s = (i + h) % stages;
-                // the columns' last readers
-                if (i + h >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], (((i + h) / stages) & 1) ^ 1, flags)))
-                    break;  // aborted: the other waits end the same way
-                tc_fence_after();
-                const uint32_t t = taddr + static_cast<uint32_t>(s * 24);
-                tmem_st8(t, v[h][0], v[h][1]);
-                tmem_st8(t + 8, v[h][2], v[h][4]);
-                tmem_st8(t + 16, v[h][3], v[h][5]);
-                load(i + 2 + h, v[h]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
             }
         }
     }
@@ -410,72 +458,72 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         if (got) {
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            for (int c0 = 0; c0 < n_pad; c0 += 16) {
-                uint32_t r[16];
+            for (int c0 = 0; c0 < n_pad; c0 += 64) {  // one wait per 64 columns
+                uint32_t r[64];
                 __syncwarp();
-                tmem_ld16(taddr + c0, r);
-                tmem_ld_wait();
-                if constexpr (sizeof(T) == 2) {
-                    if (a.fuse && flags[2] && o < a.h_out) {  // elements of B left out of the blocks
-                        const int chunks = a.R / 8;
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const int t = c0 + c, slot = t < n ? slot_sm[t] : -1;
-                            if (slot < 0) continue;
-                            const int d = dl_sm[t];
-                            for (int k8 = 0; k8 < chunks; ++k8) {
-                                const int p = d * chunks + k8;
-                                if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
-                                const uint4 sv = sum_parts8<T>(a.s_in + (size_t)t * a.R + k8 * 8, a.s_parts, (size_t)n * a.R);
-                                const uint4 bv = __ldg(reinterpret_cast<const uint4*>(
-                                    static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + o) * a.R + k8 * 8));
-                                r[c] = __float_as_uint(nonfinite_dot8<T>(bv, sv, __uint_as_float(r[c])));
-                            }
+                for (int q = 0; q < 4; ++q)
+                    if (c0 + 16 * q < n_pad) tmem_ld16(taddr + c0 + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&r[16 * q]));
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c0 + 16 * q < n_pad)
+#pragma unroll
+                        for (int c = 16 * q; c < 16 * q + 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
+            }
+            if constexpr (sizeof(T) == 2) {
+                if (a.fuse && flags[2] && o < a.h_out) {  // elements of B left out of the blocks
+                    const int chunks = a.R / 8;
+                    for (int t = 0; t < n; ++t) {
+                        if (dl_sm[t] < 0) continue;
+                        for (int k8 = 0; k8 < chunks; ++k8) {
+                            const int p = dl_sm[t] * chunks + k8;
+                            if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
+                            const uint4 sv = sum_parts8<T>(a.s_in + (size_t)t * a.R + k8 * 8, a.s_parts, (size_t)n * a.R);
+                            const uint4 bv = __ldg(reinterpret_cast<const uint4*>(
+                                static_cast<const T*>(a.B) + ((size_t)slot_sm[t] * a.h_out + o) * a.R + k8 * 8));
+                            P[t * kDM + row] = nonfinite_dot8<T>(bv, sv, P[t * kDM + row]);
                         }
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
             }
+            fence_proxy_async_smem();  // read by the bulk copies
         } else if (lane == 0) {
             flags[0] = 1;
         }
     }
     tc_fence_before();
     __syncthreads();
-    // each CTA adds up the partial sums of its share of the tokens, in split order, and stores them:
-    // 8 features a thread, 16 neighbouring threads a token's 128
+    // Each CTA adds up the partial sums of its share of the tokens, in split order, and stores them:
+    // 8 features a thread, 16 neighbouring threads a token's 128.  The sums reach their owner by one
+    // bulk copy from each other CTA (a token's row is 512 bytes, an owner's rows are contiguous) where a
+    // receive buffer fits, else they are read remotely, which is slower (64 tokens, 4 CTAs: 1.9 us).
     const bool good = flags[0] == 0;
-    if (a.splits > 1) cluster_sync();
-    if (warp >= 2 && good && store) {
-        const int per = (n + a.splits - 1) / a.splits;
-        const int beg = split * per * 16, end = min(n, (split + 1) * per) * 16;
-        for (int e = beg + (int)threadIdx.x - 64; e < end; e += 256) {
-            const int t = e >> 4, o8 = (e & 15) * 8, o = m_tile * kDM + o8;
-            const float* own = P + t * kDM + o8;
-            float v[8];
-            if (a.splits == 1) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = own[i];
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                for (int c0 = 0; c0 < a.splits; c0 += 4) {  // four CTAs' loads in flight
-                    float4 lo[4], hi[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t at = mapa_shared(smem_u32(own), static_cast<uint32_t>(min(c0 + c, a.splits - 1)));
-                        lo[c] = ld_dsmem_f32x4(at);
-                        hi[c] = ld_dsmem_f32x4(at + 16);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c0 + c < a.splits) {
-                            v[0] += lo[c].x, v[1] += lo[c].y, v[2] += lo[c].z, v[3] += lo[c].w;
-                            v[4] += hi[c].x, v[5] += hi[c].y, v[6] += hi[c].z, v[7] += hi[c].w;
-                        }
-                }
+    const int per = (n + a.splits - 1) / a.splits;
+    const int t0 = min(n, split * per), cnt = min(n, t0 + per) - t0;
+    float* rcv = P + (size_t)n_pad * kDM;  // [splits - 1][per][128]
+    bool recv = true;
+    if (a.splits > 1) {
+        if (a.push && threadIdx.x == 64 && cnt > 0)
+            mbar_arrive_expect_tx(rbar, static_cast<uint32_t>((a.splits - 1) * cnt * kDM * 4));
+        cluster_sync();
+        if (a.push) {
+            const int dst = (int)threadIdx.x - 64;
+            if (dst >= 0 && dst < a.splits && dst != split) {
+                const int d0 = min(n, dst * per), dcnt = min(n, d0 + per) - d0;
+                if (dcnt > 0)
+                    bulk_s2cluster(mapa_shared(smem_u32(rcv + (size_t)(split < dst ? split : split - 1) * per * kDM),
+                                               static_cast<uint32_t>(dst)),
+                                   P + (size_t)d0 * kDM, static_cast<uint32_t>(dcnt * kDM * 4),
+                                   mapa_shared(smem_u32(rbar), static_cast<uint32_t>(dst)));
             }
+            __syncwarp();
+            if (cnt > 0) recv = __all_sync(0xffffffffu, mbar_wait(rbar, 0, flags));
+            cluster_arrive();  // (the last wait below: every copy out of this CTA has then landed)
+        }
+    }
+    if (warp >= 2 && good && store && recv) {
+        auto store8 = [&](int t, int o, const float (&v)[8]) {
             T* yp = y + (long long)t * a.ldy + o;
             alignas(16) T w[8];
 #pragma unroll
@@ -489,14 +537,58 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 for (int i = 0; i < 8; ++i)
                     if (o + i < a.h_out) yp[i] = w[i];
             }
+        };
+        const int o8 = ((int)threadIdx.x & 15) * 8, o = m_tile * kDM + o8;
+        if (a.splits == 1) {
+            for (int t = ((int)threadIdx.x - 64) >> 4; t < n; t += 16) {
+                const float4* own = reinterpret_cast<const float4*>(P + t * kDM + o8);
+                const float4 lo = own[0], hi = own[1];
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                store8(t, o, v);
+            }
+        } else {
+            for (int u = ((int)threadIdx.x - 64) >> 4; u < cnt; u += 16) {
+                const float* own = P + (t0 + u) * kDM + o8;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+                for (int c0 = 0; c0 < a.splits; c0 += 4) {  // four CTAs' loads in flight
+                    float4 lo[4], hi[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = min(c0 + k, a.splits - 1);
+                        if (a.push) {
+                            const float* p = c == split ? own : rcv + ((size_t)(c < split ? c : c - 1) * per + u) * kDM + o8;
+                            lo[k] = reinterpret_cast<const float4*>(p)[0];
+                            hi[k] = reinterpret_cast<const float4*>(p)[1];
+                        } else {
+                            const uint32_t at = mapa_shared(smem_u32(own), static_cast<uint32_t>(c));
+                            lo[k] = ld_dsmem_f32x4(at);
+                            hi[k] = ld_dsmem_f32x4(at + 16);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (c0 + k < a.splits) {
+                            v[0] += lo[k].x, v[1] += lo[k].y, v[2] += lo[k].z, v[3] += lo[k].w;
+                            v[4] += hi[k].x, v[5] += hi[k].y, v[6] += hi[k].z, v[7] += hi[k].w;
+                        }
+                }
+                store8(t0 + u, o, v);
+            }
         }
     }
-    if (a.splits > 1) cluster_sync();  // no CTA leaves while its partial sums may still be read
+    if (!recv && a.status) report_timeout_status(a.status);
+    // no CTA leaves while its partial sums may still be read or copied
+    if (a.splits > 1) {
+        if (!a.push) cluster_arrive();
+        cluster_wait();
+    }
     if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
 }
 
 template <typename T>
-static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, bool early,
+static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, int early,
                                const Fp4DecodeLora* lora, cudaStream_t st) {
     Fp4DecodeArgs a;
     memset(&a, 0, sizeof(a));
@@ -510,7 +602,8 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
     a.h_out = w.rows;
     a.kt = x.ktiles;
     a.kb_total = x.ktiles / 2;
-    a.early = early;
+    a.early_w = early >= 1;
+    a.early_x = early >= 2;
     // y is written 16 bytes at a time when every row starts on a 16-byte boundary
     a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     const int m_tiles = (w.rows + kDM - 1) / kDM;
@@ -530,16 +623,20 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
         a.B = pv.B;
     }
     const size_t stage_bytes = kDWBytes + (size_t)a.n_pad * 128;
-    const size_t fixed = (lora ? 2 * (size_t)kDChunks * (2048 + a.n_pad * 16) : 0) + kDScratch + kDBars + 1024;
-    const size_t park = (size_t)a.n_pad * kDM * 4;
-    int stages = (int)((227 * 1024 - fixed) / stage_bytes);
+    const size_t lora_bytes = lora ? 2 * (size_t)kDChunks * (2048 + a.n_pad * 16) : 0;
+    const size_t room = 227 * 1024 - kDScratch - kDBars - 1024;
+    int stages = (int)((room - lora_bytes) / stage_bytes);
     stages = std::min({stages, 8, a.kb_per_split});
-    while ((size_t)stages * stage_bytes < park) ++stages;  // (park is at most 128 KB, 2.5 stages of its size)
     a.stages = stages;
+    // the stages and LoRA blocks are idle when the sums are parked in their place
+    const int per = (x.rows + a.splits - 1) / a.splits;
+    const size_t park = (size_t)a.n_pad * kDM * 4, rcv = (size_t)(a.splits - 1) * per * kDM * 4;
+    a.push = a.splits > 1 && park + rcv <= room;
+    a.ring_bytes = (int)((std::max(stages * stage_bytes + lora_bytes, park + (a.push ? rcv : 0)) + 1023) / 1024 * 1024);
     int cols = 32;
     while (cols < a.n_pad + 24 * stages) cols <<= 1;
     a.tmem_cols = cols;
-    const size_t smem = (size_t)stages * stage_bytes + fixed;
+    const size_t smem = (size_t)a.ring_bytes + kDScratch + kDBars + 1024;
     if (smem > 227 * 1024 || cols > 512) return set_error(LORA_EUNSUP, "internal: 4-bit decode plan");
     CUtensorMap mX, mW, mB;
     int rc = make_map_fp4(&mX, x.codes, x.pitch, x.rows, a.n_pad);
@@ -576,7 +673,7 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
 }  // namespace tc
 
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
-                      bool early, const Fp4DecodeLora* lora, cudaStream_t st) {
+                      int early, const Fp4DecodeLora* lora, cudaStream_t st) {
     switch (dtype) {
         case LORA_F32: return tc::launch_fp4_decode_t<float>(x, w, y, ldy, status, early, nullptr, st);
         case LORA_F16: return tc::launch_fp4_decode_t<__half>(x, w, y, ldy, status, early, lora, st);

@@ -412,7 +412,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         for (int i = 0; i < L; ++i) copy_next();
         int slot = 0, set = 0, back = 0, warm = kPScaleSets;  // back: stage of the step kPScaleSets before
         uint32_t backph = 0;
-        Ring cr;
+        Ring cr;  // the stage last stored for
+        cr.i = -1;
         bool ok = true;
         for (int tile = pair; tile < total; tile += npairs) {
             for (int kb = 0; kb < nkb; ++kb) {
@@ -423,6 +424,14 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 if (++slot == kPScaleSlots) slot = 0;
                 const uint4 x0 = sp[0], x1 = sp[32];
                 const uint4 w00 = sp[64], w01 = sp[96], w10 = sp[128], w11 = sp[160];  // [row tile][step half]
+                // the step before is announced only now: its stores' latency overlapped the above
+                if (cr.i >= 0) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive_cluster_relaxed(full0 + static_cast<uint32_t>(cr.i) * 8u);
+                }
+                cr.next(stages);
                 // the set's last readers: the MMAs kPScaleSets steps before
                 if (warm > 0) {
                     --warm;
@@ -442,13 +451,12 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 }
                 if (++set == kPScaleSets) set = 0;
                 copy_next();
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (ok && lane == 0) mbar_arrive_cluster_relaxed(full0 + static_cast<uint32_t>(cr.i) * 8u);
-                cr.next(stages);
             }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0 && cr.i >= 0) mbar_arrive_cluster_relaxed(full0 + static_cast<uint32_t>(cr.i) * 8u);
         if (!ok && a.status) report_timeout_status(a.status);
         cp_async_wait<0>();
     } else if (a.fuse) {

@@ -111,8 +111,8 @@ struct Fp4Lora {
     const void* B;
     int R;
 };
-// Up to 256 tokens.  early: every kernel that could have written w or x has completed when this grid
-// starts (only the shrink output is waited for).  lora: the pool, the slot of each token and the shrink output in K parts.
+// Up to 256 tokens.  early: every kernel that could have written w (1), or w and x (2), has completed when
+// this grid starts; the rest is waited for.  lora: the pool, the slot of each token and the shrink output in K parts.
 struct Fp4DecodeLora {
     const PoolView* pool;
     const int32_t* idx;
@@ -120,7 +120,11 @@ struct Fp4DecodeLora {
     int s_parts;
 };
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
-                      bool early, const Fp4DecodeLora* lora, cudaStream_t st);
+                      int early, const Fp4DecodeLora* lora, cudaStream_t st);
+// The kernel before it for small batches: x quantised into q (nullptr: not) and the shrink output in
+// *s_parts K parts, in one launch (16-bit pools whose adapters the per-token shrink suits).
+int launch_fp4_front(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* q, float* s_out, int* s_parts,
+                     cudaStream_t st);
 // More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
