@@ -292,36 +292,44 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         if (a.early_w && !a.early_x) pdl_wait();
 #pragma unroll
         for (int h = 0; h < kAhead; ++h) load_x(h, v[h]);
-        // two steps per wait for the stores, whose latency (some 400 ns) is otherwise a step's
+        // the first stages' columns have no earlier readers: one wait for all their stores
+        auto put = [&](int s, const uint4 (&u)[6]) {
+            const uint32_t t = taddr + static_cast<uint32_t>(s * 24);
+            tmem_st8(t, u[0], u[1]);
+            tmem_st8(t + 8, u[2], u[4]);
+            tmem_st8(t + 16, u[3], u[5]);
+        };
+        const int first = min(kAhead, min(stages, nkb));
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            if (h < first) put(h, v[h]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            for (int h = 0; h < first; ++h) mbar_arrive(&full[h]);
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+            if (h < first) {
+                load_w(kAhead + h, v[h]);
+                load_x(kAhead + h, v[h]);
+            }
         for (int i0 = 0; i0 < nkb; i0 += kAhead) {
 #pragma unroll
-            for (int g = 0; g < kAhead; g += 2) {
-                if (i0 + g >= nkb) break;
-                bool ok = true;
-#pragma unroll
-                for (int h = g; h < g + 2; ++h) {
-                    const int i = i0 + h, s = i % stages;
-                    if (i >= nkb) break;
-                    // the columns' last readers
-                    ok = ok && (i < stages || __all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)));
-                    tc_fence_after();
-                    const uint32_t t = taddr + static_cast<uint32_t>(s * 24);
-                    if (ok) {
-                        tmem_st8(t, v[h][0], v[h][1]);
-                        tmem_st8(t + 8, v[h][2], v[h][4]);
-                        tmem_st8(t + 16, v[h][3], v[h][5]);
-                    }
-                    load_w(i + kAhead, v[h]);
-                    load_x(i + kAhead, v[h]);
-                }
+            for (int h = 0; h < kAhead; ++h) {
+                const int i = i0 + h, s = i % stages;
+                if (i < first || i >= nkb) continue;
+                // the columns' last readers
+                if (i >= stages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)))
+                    continue;  // aborted: the other waits end the same way
+                tc_fence_after();
+                put(s, v[h]);
+                load_w(i + kAhead, v[h]);
+                load_x(i + kAhead, v[h]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (!ok) break;  // aborted: the other waits end the same way
-                if (lane == 0) {
-                    mbar_arrive(&full[(i0 + g) % stages]);
-                    if (i0 + g + 1 < nkb) mbar_arrive(&full[(i0 + g + 1) % stages]);
-                }
+                if (lane == 0) mbar_arrive(&full[s]);
             }
         }
     }
