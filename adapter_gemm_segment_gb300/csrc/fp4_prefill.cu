@@ -61,7 +61,7 @@ constexpr int kPAcc1 = kPScaleCol - kPN;            // first column of the secon
 constexpr int kPLoraChunk = kPM * 16;               // 8 columns of 128 rows, 16 bytes a row
 constexpr int kPLoraBytes = 2 * 4 * kPLoraChunk;    // one block: 4 chunks on each side
 constexpr int kPScratch = 64 * 4 + 256 * 4 + 8;
-// after the stages: scales, LoRA blocks (if any), y staging (8 warps of 32 rows x 32 columns), the
+// after the stages: scales, LoRA blocks (if any), y staging (8 warps of 1024 elements), the
 // LoRA scratch, barriers
 constexpr size_t pair_smem(int stages, bool fuse, size_t elt) {
     return (size_t)stages * kPStageBytes + kPScaleSlots * kPScaleBytes + (fuse ? 2 * kPLoraBytes : 0) + 8 * 1024 * elt +
@@ -106,7 +106,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     const int stages = a.stages;
     uint8_t* scale_sm = smem + stages * kPStageBytes;
     uint8_t* lora_sm = scale_sm + kPScaleSlots * kPScaleBytes;   // [2] blocks {token side, feature side}
-    uint8_t* yst = lora_sm + (a.fuse ? 2 * kPLoraBytes : 0);     // [8 warps][32 rows][32]
+    uint8_t* yst = lora_sm + (a.fuse ? 2 * kPLoraBytes : 0);     // [8 warps][1024]
     uint32_t* seen = reinterpret_cast<uint32_t*>(yst + 8 * 1024 * sizeof(T));  // [64] slots the tile's tokens name
     int* dlist = reinterpret_cast<int*>(seen + 64);              // [256] the tile's slots in order
     int* distinct = dlist + 256;                                 // [2] their number
@@ -268,9 +268,12 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         }
     } else if (warp < 10) {
         // ---- epilogue: thread <-> token row (TMEM lane) of this CTA's half; two warps share a row,
-        // taking alternate pieces of 32 features ----
+        // taking alternate pieces of 128 bytes of y ----
         const int q = warp & 3, hv = (warp - 2) >> 2;
-        constexpr int kCh = 32 * sizeof(T) / 16;  // 16-byte pieces of a staged row
+        constexpr int kCols = 128 / sizeof(T);          // features of a piece
+        constexpr int kUnits = 64 / kCols;              // pieces a warp holds at once
+        constexpr int kStaged = 1024 * sizeof(T) / 128; // rows staged at once
+        constexpr int per = 16 / sizeof(T);
         uint8_t* ys = yst + (warp - 2) * (1024 * sizeof(T));
         const uint32_t ov_free0 = mapa_shared(smem_u32(ov_free), 0);
         const uint32_t other_epi = mapa_shared(smem_u32(epi_done), rank ^ 1);
@@ -283,87 +286,98 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const int m0 = tile / a.n_tiles * 2 * kPM + static_cast<int>(rank) * kPM, n0 = tile % a.n_tiles * kPN;
             const int row = m0 + q * 32 + lane;
             const int yrow = row < a.n ? (a.perm ? __ldcg(a.perm + row) : row) : -1;
-            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, flags) &&
-                                             (!a.fuse || mbar_wait_cluster(&lora_done[buf], (local >> 1) & 1, flags))))
-                break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, flags))) break;
             tc_fence_after();
-            const bool any_bad = a.fuse && flags[2 + buf] == local + 1;
-            const int slot = any_bad && yrow >= 0 && status == LORA_OK ? __ldcg(a.idx + yrow) : -1;
+            bool any_bad = false, gone = false;
+            int slot = -1;
             const uint32_t taddr = tmem + buf * kPAcc1 + (static_cast<uint32_t>(q * 32) << 16);
-            uint32_t r[2][32];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                // this warp's two pieces of each half of the columns, those both accumulators share first
-                int cc[2];
+                // the half of the columns that holds those both accumulators share comes first
+                int c0[kUnits];
+                uint32_t r[64];
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int pos = 4 * half + 2 * i + hv;
-                    cc[i] = (buf == 0 ? 7 - pos : pos) * 32;
-                    tmem_ld16(taddr + cc[i], *reinterpret_cast<uint32_t(*)[16]>(&r[i][0]));
-                    tmem_ld16(taddr + cc[i] + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[i][16]));
+                for (int i = 0; i < kUnits; ++i) {
+                    const int u = 2 * (half * kUnits + i) + hv;
+                    const int cc = (buf == 0 ? kPN / kCols - 1 - u : u) * kCols;
+                    c0[i] = n0 + cc;
+#pragma unroll
+                    for (int k = 0; k < kCols; k += 16)
+                        tmem_ld16(taddr + cc + k, *reinterpret_cast<uint32_t(*)[16]>(&r[i * kCols + k]));
                 }
                 tmem_ld_wait();
                 if (half == 0) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(ov_free0);
+                    if (a.fuse) {
+                        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&lora_done[buf], (local >> 1) & 1, flags))) {
+                            gone = true;
+                            break;
+                        }
+                        any_bad = flags[2 + buf] == local + 1;
+                        if (any_bad && yrow >= 0 && status == LORA_OK) slot = __ldcg(a.idx + yrow);
+                    }
                 }
                 if (status != LORA_OK) continue;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c0 = n0 + cc[i];
-                    if (c0 >= a.h_out) continue;
+                for (int i = 0; i < kUnits; ++i) {
+                    if (c0[i] >= a.h_out) continue;
                     if constexpr (sizeof(T) == 2) {
                         if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
                             for (int c = 0; c < a.R; c += 8) {
                                 const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
                                                                                        (size_t)row * a.R + c));
-                                const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0) * a.R + c;
+                                const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0[i]) * a.R + c;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (c0 + e < a.h_out)
-                                        r[i][e] = __float_as_uint(nonfinite_dot8<T>(
+                                for (int e = 0; e < kCols; ++e)
+                                    if (c0[i] + e < a.h_out)
+                                        r[i * kCols + e] = __float_as_uint(nonfinite_dot8<T>(
                                             __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)e * a.R)), sv,
-                                            __uint_as_float(r[i][e])));
+                                            __uint_as_float(r[i * kCols + e])));
                             }
                         }
                     }
-                    // through shared memory (16-byte pieces permuted by row), so that neighbouring lanes
-                    // write neighbouring bytes of a row of y
-                    __syncwarp();
+                    // through shared memory (16-byte pieces permuted by row), so that eight neighbouring
+                    // lanes write 128 consecutive bytes of a row of y.  (Whole 32-byte sectors straight from
+                    // the registers were slower: 131 against 120 us for 8191 x 11008 x 4096 in float32.)
+                    const int c = lane & 7, col = c0[i] + c * per;
 #pragma unroll
-                    for (int c = 0; c < kCh; ++c) {
-                        constexpr int per = 16 / sizeof(T);
-                        alignas(16) T v[per];
+                    for (int r0 = 0; r0 < 32; r0 += kStaged) {
+                        __syncwarp();
+                        if (lane >= r0 && lane < r0 + kStaged) {
 #pragma unroll
-                        for (int e = 0; e < per; ++e) v[e] = from_f32<T>(__uint_as_float(r[i][c * per + e]));
-                        *reinterpret_cast<uint4*>(ys + (lane * kCh + (c ^ (lane / (8 / kCh) % kCh))) * 16) =
-                            *reinterpret_cast<const uint4*>(v);
-                    }
-                    __syncwarp();
-                    constexpr int kRows = 32 / kCh;  // rows a warp writes at once
-                    const int c = lane % kCh;
-                    const int col = c0 + c * (16 / (int)sizeof(T));
+                            for (int k = 0; k < 8; ++k) {
+                                alignas(16) T v[per];
 #pragma unroll
-                    for (int k = 0; k < kCh; ++k) {
-                        const int rr = k * kRows + lane / kCh;
-                        const int yr = __shfl_sync(0xffffffffu, yrow, rr);
-                        const uint4 v = *reinterpret_cast<const uint4*>(ys + (rr * kCh + (c ^ (rr / (8 / kCh) % kCh))) * 16);
-                        if (yr < 0) continue;
-                        T* yp = y + (long long)yr * a.ldy + col;
-                        if (a.vec && col + (int)(16 / sizeof(T)) <= a.h_out) {
-                            *reinterpret_cast<uint4*>(yp) = v;
-                        } else {
-                            alignas(16) T e8[16 / sizeof(T)];
-                            *reinterpret_cast<uint4*>(e8) = v;
+                                for (int e = 0; e < per; ++e) v[e] = from_f32<T>(__uint_as_float(r[i * kCols + k * per + e]));
+                                *reinterpret_cast<uint4*>(ys + (lane - r0) * 128 + ((k ^ (lane & 7)) << 4)) =
+                                    *reinterpret_cast<const uint4*>(v);
+                            }
+                        }
+                        __syncwarp();
 #pragma unroll
-                            for (int e = 0; e < (int)(16 / sizeof(T)); ++e)
-                                if (col + e < a.h_out) yp[e] = e8[e];
+                        for (int k = 0; k < kStaged; k += 4) {
+                            const int rr = k + (lane >> 3);
+                            const int yr = __shfl_sync(0xffffffffu, yrow, r0 + rr);
+                            const uint4 v = *reinterpret_cast<const uint4*>(ys + rr * 128 + ((c ^ (rr & 7)) << 4));
+                            if (yr < 0) continue;
+                            T* yp = y + (long long)yr * a.ldy + col;
+                            if (a.vec && col + per <= a.h_out) {
+                                *reinterpret_cast<uint4*>(yp) = v;
+                            } else {
+                                alignas(16) T e8[per];
+                                *reinterpret_cast<uint4*>(e8) = v;
+#pragma unroll
+                                for (int e = 0; e < per; ++e)
+                                    if (col + e < a.h_out) yp[e] = e8[e];
+                            }
                         }
                     }
                 }
             }
+            if (gone) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0 && a.fuse) {
