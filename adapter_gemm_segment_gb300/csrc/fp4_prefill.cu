@@ -6,6 +6,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstring>
 
 #include "common.cuh"
@@ -620,6 +621,8 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
     a.n_tiles = (w.rows + kPN - 1) / kPN;
     a.nkb = x.ktiles / 2;
     a.kt = x.ktiles;
+    if ((long long)a.m_tiles * a.n_tiles > INT_MAX / 2)
+        return set_error(LORA_EUNSUP, "4-bit product of %d x %d outputs is too large", x.rows, w.rows);
     a.early_w = early_w;
     // six stages where neither the LoRA blocks nor float32 staging take the room of one
     a.stages = !lora && sizeof(T) == 2 ? 6 : 5;
