@@ -13,6 +13,7 @@
 // (16-byte loads of 16-bit data, a warp's lanes side by side), four lanes share a block (two
 // shuffles give its maximum), and the 4 x 4 scale bytes of those rows' four blocks are 16
 // consecutive bytes of a scale tile, written by one lane.
+#include <algorithm>
 #include <cstring>
 
 #include "common.cuh"
@@ -319,6 +320,8 @@ static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
         s16_bytes = (size_t)n * pool->desc.r_max * 2;
         s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * 2 * s16_bytes;
     }
+    if (pool->desc.dtype == LORA_F32)
+        s_bytes = (size_t)f32_shrink_parts(pool_view(pool), n) * std::max(n, 1) * pool->desc.r_max * 4;
     L->s16_off = align256(s_bytes);
     L->codes_off = L->s16_off + align256(s16_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
@@ -442,16 +445,16 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         const Fp4DecodeLora lora = {&pv, sv.idx, s_buf, s_parts};
         return launch_fp4_decode(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, early, &lora, st);
     }
+    // float32 pools: the LoRA term in float32, around the product
     if (!xq) {
         rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (rc) return rc;
     }
-    rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
+    rc = launch_f32_shrink(pv, sv, x_dev, s_buf, st);
     if (rc) return rc;
-    // float32 pools: the LoRA term in float32, by the expand kernel
     rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
     if (rc) return rc;
-    return launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
+    return launch_f32_expand(pv, sv, s_buf, f32_shrink_parts(pv, n), y_dev, st);
 }
 
 }  // extern "C"

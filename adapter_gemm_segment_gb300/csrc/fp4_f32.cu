@@ -1,0 +1,262 @@
+// float32 pools over a 4-bit base: the LoRA term in float32 on CUDA cores (the tensor cores have no
+// float32 product of that accuracy), around the 4-bit product.
+//
+// Both kernels are register-tiled products over tiles of up to 64 tokens of one segment (tokens that
+// share an adapter), so an adapter's rows are read once per 64 of its tokens:
+//   shrink  s[t, j] = (alpha / r) sum_k x[t, k] A[j, k]     64 tokens x 16, 32 or 64 rows, part of K
+//   expand  y[t, o] += sum_j s[t, j] B[o, j]                64 tokens x 64 features
+// 256 threads; a thread keeps 4 tokens x up to 4 columns.  Operands pass through shared memory 32 deep,
+// k-major, so that a step of k is one or two 16-byte reads for 4 to 16 multiply-adds; the next 32 are
+// on their way meanwhile.  Bound by the multiply-adds at r_max 64, by the read of x and of y below.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace lora {
+
+constexpr int kFTok = 64;   // tokens per tile
+constexpr int kFK = 32;     // depth of a step
+constexpr int kFPad = 4;    // keeps rows of the k-major tiles 16-byte aligned and off one another's banks
+
+// The tile blockIdx.x of up to kFTok sorted tokens of one adapter segment: its slot (-1: none), first
+// sorted position and count.
+struct SegTile {
+    int slot, j0, cnt;
+};
+__device__ __forceinline__ SegTile find_tile(const SegView& seg, SegTile* sh) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x, nseg = __ldcg(seg.nseg);
+        int run = 0;
+        SegTile t{-1, 0, 0};
+        for (int base = 0; base < nseg; base += 32) {
+            const int i = base + lane;
+            int slot = -1, beg = 0, end = 0, tiles = 0;
+            if (i < nseg) {
+                slot = __ldcg(seg.seg_slot + i);
+                beg = __ldcg(seg.seg_start + i);
+                end = __ldcg(seg.seg_start + i + 1);
+                if (slot >= 0) tiles = (end - beg + kFTok - 1) / kFTok;
+            }
+            int v = tiles;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d) v += u;
+            }
+            const int first = run + v - tiles, want = (int)blockIdx.x;
+            if (want >= first && want < first + tiles) {
+                const int j0 = beg + (want - first) * kFTok;
+                *sh = SegTile{slot, j0, min(kFTok, end - j0)};
+            }
+            run += __shfl_sync(0xffffffffu, v, 31);
+            if (want < run) break;
+        }
+        if ((int)blockIdx.x >= run && lane == 0) *sh = t;
+    }
+    __syncthreads();
+    return *sh;
+}
+
+// Four consecutive floats of a row from column c (zeros past cols).
+__device__ __forceinline__ float4 load4(const float* row, int c, int cols, bool vec) {
+    if (vec && c + 4 <= cols) return __ldcg(reinterpret_cast<const float4*>(row + c));
+    float4 v;
+    v.x = c < cols ? __ldcg(row + c) : 0.f;
+    v.y = c + 1 < cols ? __ldcg(row + c + 1) : 0.f;
+    v.z = c + 2 < cols ? __ldcg(row + c + 2) : 0.f;
+    v.w = c + 3 < cols ? __ldcg(row + c + 3) : 0.f;
+    return v;
+}
+
+// RN columns per thread: 16 RN adapter rows per CTA.
+template <int RN>
+__global__ void __launch_bounds__(256)
+f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float* __restrict__ s_out, int vec, int steps) {
+    constexpr int RT = 16 * RN;
+    __shared__ float xs[kFK][kFTok + kFPad];
+    __shared__ float as[kFK][RT + kFPad];
+    __shared__ SegTile sh;
+    __shared__ int tok[kFTok];
+    pdl_wait();
+    pdl_trigger();
+    if (__ldcg(seg.status) != LORA_OK) return;
+    const SegTile tile = find_tile(seg, &sh);
+    if (tile.slot < 0) return;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    if (tid < kFTok) tok[tid] = tid < tile.cnt ? __ldcg(seg.perm + tile.j0 + tid) : -1;
+    __syncthreads();
+    const int h = pool.h_in, R = pool.R, r0 = blockIdx.y * RT;
+    const int k_beg = blockIdx.z * steps * kFK, k_end = min(h, k_beg + steps * kFK);
+    const float* A = static_cast<const float*>(pool.A) + ((size_t)tile.slot * R + r0) * h;
+    // loads: thread -> row tid / 8 (and the rows 32 further), columns 4 (tid % 8) of a step
+    const int lr = tid >> 3, lc = (tid & 7) * 4;
+    constexpr int AR = (RT + 31) / 32;
+    float4 xv[2], av[AR];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = tok[lr + 32 * i];
+            xv[i] = t >= 0 ? load4(x + (size_t)t * h, k0 + lc, k_end, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < AR; ++i) {
+            const int r = lr + 32 * i;
+            av[i] = r < RT && r0 + r < R ? load4(A + (size_t)r * h, k0 + lc, k_end, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    float acc[4][RN] = {};
+    load(k_beg);
+    for (int k0 = k_beg; k0 < k_end; k0 += kFK) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            xs[lc][lr + 32 * i] = xv[i].x, xs[lc + 1][lr + 32 * i] = xv[i].y;
+            xs[lc + 2][lr + 32 * i] = xv[i].z, xs[lc + 3][lr + 32 * i] = xv[i].w;
+        }
+#pragma unroll
+        for (int i = 0; i < AR; ++i) {
+            const int r = lr + 32 * i;
+            if (r < RT) as[lc][r] = av[i].x, as[lc + 1][r] = av[i].y, as[lc + 2][r] = av[i].z, as[lc + 3][r] = av[i].w;
+        }
+        __syncthreads();
+        if (k0 + kFK < k_end) load(k0 + kFK);
+#pragma unroll 8
+        for (int kk = 0; kk < kFK; ++kk) {
+            const float4 xq = *reinterpret_cast<const float4*>(&xs[kk][ty * 4]);
+            float a[RN];
+#pragma unroll
+            for (int j = 0; j < RN; ++j) a[j] = as[kk][tx * RN + j];
+#pragma unroll
+            for (int j = 0; j < RN; ++j) {
+                acc[0][j] = fmaf(xq.x, a[j], acc[0][j]);
+                acc[1][j] = fmaf(xq.y, a[j], acc[1][j]);
+                acc[2][j] = fmaf(xq.z, a[j], acc[2][j]);
+                acc[3][j] = fmaf(xq.w, a[j], acc[3][j]);
+            }
+        }
+    }
+    const float scale = pool.table[tile.slot].scale;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = tok[ty * 4 + i];
+        if (t < 0) continue;
+        float* out = s_out + ((size_t)blockIdx.z * seg.n + t) * R + r0;
+#pragma unroll
+        for (int j = 0; j < RN; ++j)
+            if (r0 + tx * RN + j < R) out[tx * RN + j] = scale * acc[i][j];
+    }
+}
+
+__global__ void __launch_bounds__(256)
+f32_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, int s_parts, float* __restrict__ y, int vec) {
+    __shared__ float ss[kFK][kFTok + kFPad];
+    __shared__ float bs[kFK][64 + kFPad];
+    __shared__ SegTile sh;
+    __shared__ int tok[kFTok];
+    pdl_wait();
+    pdl_trigger();
+    if (__ldcg(seg.status) != LORA_OK) return;
+    const SegTile tile = find_tile(seg, &sh);
+    if (tile.slot < 0) return;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    if (tid < kFTok) tok[tid] = tid < tile.cnt ? __ldcg(seg.perm + tile.j0 + tid) : -1;
+    __syncthreads();
+    const int h_out = pool.h_out, R = pool.R, o0 = blockIdx.y * 64;
+    const float* B = static_cast<const float*>(pool.B) + ((size_t)tile.slot * h_out + o0) * R;
+    const int lr = tid >> 3, lc = (tid & 7) * 4;
+    // y is read while the product runs
+    float yv[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = tok[ty * 4 + i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int o = o0 + tx * 4 + j;
+            yv[i][j] = t >= 0 && o < h_out ? __ldcg(y + (size_t)t * h_out + o) : 0.f;
+        }
+    }
+    float acc[4][4] = {};
+    for (int k0 = 0; k0 < R; k0 += kFK) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = lr + 32 * i, t = tok[r];
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t >= 0)
+                for (int p0 = 0; p0 < s_parts; p0 += 4) {  // four parts' loads in flight
+                    float4 u[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        u[p] = load4(s_in + ((size_t)min(p0 + p, s_parts - 1) * seg.n + t) * R, k0 + lc, R, vec);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        if (p0 + p < s_parts) v.x += u[p].x, v.y += u[p].y, v.z += u[p].z, v.w += u[p].w;
+                }
+            const float4 b = o0 + r < h_out ? load4(B + (size_t)r * R, k0 + lc, R, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
+            ss[lc][r] = v.x, ss[lc + 1][r] = v.y, ss[lc + 2][r] = v.z, ss[lc + 3][r] = v.w;
+            bs[lc][r] = b.x, bs[lc + 1][r] = b.y, bs[lc + 2][r] = b.z, bs[lc + 3][r] = b.w;
+        }
+        __syncthreads();
+        const int depth = min(kFK, R - k0);
+        for (int kk = 0; kk < depth; ++kk) {
+            const float4 sq = *reinterpret_cast<const float4*>(&ss[kk][ty * 4]);
+            const float4 bq = *reinterpret_cast<const float4*>(&bs[kk][tx * 4]);
+            const float s4[4] = {sq.x, sq.y, sq.z, sq.w}, b4[4] = {bq.x, bq.y, bq.z, bq.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s4[i], b4[j], acc[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = tok[ty * 4 + i];
+        if (t < 0) continue;
+        float* yr = y + (size_t)t * h_out + o0 + tx * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (o0 + tx * 4 + j < h_out) yr[j] = yv[i][j] + acc[i][j];
+    }
+}
+
+static int f32_tiles(const PoolView& pv, int n) { return (n + kFTok - 1) / kFTok + std::min(n, pv.S); }
+
+// K parts of the shrink (the expand adds them up): two CTAs an SM where K allows parts of at least 8
+// steps.
+int f32_shrink_parts(const PoolView& pv, int n) {
+    const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
+    const int ctas = std::max(1, (n + kFTok - 1) / kFTok * ((pv.R + rows - 1) / rows));
+    const int steps = (pv.h_in + kFK - 1) / kFK;
+    int parts = std::max(1, std::min({2 * num_sms() / ctas, 8, steps / 8}));
+    const int per = (steps + parts - 1) / parts;
+    return (steps + per - 1) / per;
+}
+
+int launch_f32_shrink(const PoolView& pv, const SegView& sv, const void* x, float* s_out, cudaStream_t st) {
+    const float* xp = static_cast<const float*>(x);
+    // 16-byte loads where rows of x and A start on 16-byte boundaries
+    int vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && pv.h_in % 4 == 0;
+    const int parts = f32_shrink_parts(pv, sv.n), all = (pv.h_in + kFK - 1) / kFK;
+    int steps = (all + parts - 1) / parts;
+    void* args[] = {(void*)&pv, (void*)&sv, (void*)&xp, (void*)&s_out, (void*)&vec, (void*)&steps};
+    const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
+    const void* fn = rows == 16   ? (const void*)f32_shrink_kernel<1>
+                     : rows == 32 ? (const void*)f32_shrink_kernel<2>
+                                  : (const void*)f32_shrink_kernel<4>;
+    const dim3 grid(f32_tiles(pv, sv.n), (pv.R + rows - 1) / rows, parts);
+    LORA_CUDA_TRY(launch_pdl(fn, grid, dim3(256), 0, st, args));
+    return LORA_OK;
+}
+
+int launch_f32_expand(const PoolView& pv, const SegView& sv, const float* s_in, int s_parts, void* y, cudaStream_t st) {
+    float* yp = static_cast<float*>(y);
+    int vec = pv.R % 4 == 0;
+    void* args[] = {(void*)&pv, (void*)&sv, (void*)&s_in, (void*)&s_parts, (void*)&yp, (void*)&vec};
+    const dim3 grid(f32_tiles(pv, sv.n), (pv.h_out + 63) / 64);
+    if (grid.y > 65535) return set_error(LORA_EUNSUP, "float32 expand of %d features", pv.h_out);
+    LORA_CUDA_TRY(launch_pdl((const void*)f32_expand_kernel, grid, dim3(256), 0, st, args));
+    return LORA_OK;
+}
+
+}  // namespace lora

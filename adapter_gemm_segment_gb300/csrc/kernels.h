@@ -125,6 +125,10 @@ int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, lo
 // *s_parts K parts, in one launch (16-bit pools whose adapters the per-token shrink suits).
 int launch_fp4_front(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* q, float* s_out, int* s_parts,
                      cudaStream_t st);
+// float32 pools: the shrink in K parts (s_out [f32_shrink_parts][n][R]), and y += s B^T.
+int f32_shrink_parts(const PoolView& pv, int n);
+int launch_f32_shrink(const PoolView& pv, const SegView& sv, const void* x, float* s_out, cudaStream_t st);
+int launch_f32_expand(const PoolView& pv, const SegView& sv, const float* s_in, int s_parts, void* y, cudaStream_t st);
 // More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
