@@ -536,7 +536,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             alignas(16) T w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = from_f32<T>(v[i]);
-            if (a.vec && o + 8 <= a.h_out) {
+            if (o + 8 <= a.h_out) {
 #pragma unroll
                 for (int i = 0; i < (int)(8 * sizeof(T) / 16); ++i)
                     reinterpret_cast<uint4*>(yp)[i] = reinterpret_cast<const uint4*>(w)[i];
@@ -547,7 +547,22 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             }
         };
         const int o8 = ((int)threadIdx.x & 15) * 8, o = m_tile * kDM + o8;
-        if (a.splits == 1) {
+        if (!a.vec) {  // rows off 16-byte boundaries: a feature a thread, neighbours side by side
+            const int f = (int)threadIdx.x & 127, of = m_tile * kDM + f;
+            for (int u = ((int)threadIdx.x - 64) >> 7; u < cnt; u += 2) {
+                const float* own = P + (t0 + u) * kDM + f;
+                float v = 0.f;
+                for (int c = 0; c < a.splits; ++c) {
+                    if (a.splits == 1 || (a.push && c == split))
+                        v += *own;
+                    else if (a.push)
+                        v += rcv[((size_t)(c < split ? c : c - 1) * per + u) * kDM + f];
+                    else
+                        v += ld_dsmem_f32(mapa_shared(smem_u32(own), static_cast<uint32_t>(c)));
+                }
+                if (of < a.h_out) y[(long long)(t0 + u) * a.ldy + of] = from_f32<T>(v);
+            }
+        } else if (a.splits == 1) {
             for (int t = ((int)threadIdx.x - 64) >> 4; t < n; t += 16) {
                 const float4* own = reinterpret_cast<const float4*>(P + t * kDM + o8);
                 const float4 lo = own[0], hi = own[1];

@@ -5,9 +5,11 @@
 // share an adapter), so an adapter's rows are read once per 64 of its tokens:
 //   shrink  s[t, j] = (alpha / r) sum_k x[t, k] A[j, k]     64 tokens x 16, 32 or 64 rows, part of K
 //   expand  y[t, o] += sum_j s[t, j] B[o, j]                64 tokens x 64 features
-// 256 threads; a thread keeps 4 tokens x up to 4 columns.  Operands pass through shared memory 32 deep,
-// k-major, so that a step of k is one or two 16-byte reads for 4 to 16 multiply-adds; the next 32 are
-// on their way meanwhile.  Bound by the multiply-adds at r_max 64, by the read of x and of y below.
+// 256 threads; a thread keeps 4 tokens x 4 columns.  Operands pass through shared memory 32 deep, k-major,
+// so that a step of k is two 16-byte reads for 16 multiply-adds; the next 32 are on their way meanwhile.
+// Bound by the multiply-adds at r_max 64, by the reads of x and y below.  The 16-bit pools' tensor-core
+// kernels take 3 to 5 times less (1000 tokens, 4096 x 1000, r_max 32: 67 against 34 us a linear).  Where segments hold few
+// tokens, the expand gives a thread one feature of up to 8 tokens instead.
 #include <algorithm>
 
 #include "common.cuh"
@@ -19,11 +21,12 @@ constexpr int kFTok = 64;   // tokens per tile
 constexpr int kFK = 32;     // depth of a step
 constexpr int kFPad = 4;    // keeps rows of the k-major tiles 16-byte aligned and off one another's banks
 
-// The tile blockIdx.x of up to kFTok sorted tokens of one adapter segment: its slot (-1: none), first
+// The tile blockIdx.x of up to TOK sorted tokens of one adapter segment: its slot (-1: none), first
 // sorted position and count.
 struct SegTile {
     int slot, j0, cnt;
 };
+template <int TOK = kFTok>
 __device__ __forceinline__ SegTile find_tile(const SegView& seg, SegTile* sh) {
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x, nseg = __ldcg(seg.nseg);
@@ -36,7 +39,7 @@ __device__ __forceinline__ SegTile find_tile(const SegView& seg, SegTile* sh) {
                 slot = __ldcg(seg.seg_slot + i);
                 beg = __ldcg(seg.seg_start + i);
                 end = __ldcg(seg.seg_start + i + 1);
-                if (slot >= 0) tiles = (end - beg + kFTok - 1) / kFTok;
+                if (slot >= 0) tiles = (end - beg + TOK - 1) / TOK;
             }
             int v = tiles;
 #pragma unroll
@@ -46,8 +49,8 @@ __device__ __forceinline__ SegTile find_tile(const SegView& seg, SegTile* sh) {
             }
             const int first = run + v - tiles, want = (int)blockIdx.x;
             if (want >= first && want < first + tiles) {
-                const int j0 = beg + (want - first) * kFTok;
-                *sh = SegTile{slot, j0, min(kFTok, end - j0)};
+                const int j0 = beg + (want - first) * TOK;
+                *sh = SegTile{slot, j0, min(TOK, end - j0)};
             }
             run += __shfl_sync(0xffffffffu, v, 31);
             if (want < run) break;
@@ -69,13 +72,15 @@ __device__ __forceinline__ float4 load4(const float* row, int c, int cols, bool 
     return v;
 }
 
-// RN columns per thread: 16 RN adapter rows per CTA.
-template <int RN>
+// RT adapter rows per CTA.  A thread keeps 4 tokens x 4 rows; with fewer than 64 rows the threads form
+// 64 / RT groups that take every so-manieth k and are added up at the end.
+template <int RT>
 __global__ void __launch_bounds__(256)
 f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float* __restrict__ s_out, int vec, int steps) {
-    constexpr int RT = 16 * RN;
+    constexpr int G = 64 / RT, TX = RT / 4;
     __shared__ float xs[kFK][kFTok + kFPad];
     __shared__ float as[kFK][RT + kFPad];
+    __shared__ float red[G > 1 ? G - 1 : 1][kFTok * RT];
     __shared__ SegTile sh;
     __shared__ int tok[kFTok];
     pdl_wait();
@@ -83,7 +88,7 @@ f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float
     if (__ldcg(seg.status) != LORA_OK) return;
     const SegTile tile = find_tile(seg, &sh);
     if (tile.slot < 0) return;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int tid = threadIdx.x, grp = tid / (16 * TX), in = tid % (16 * TX), ty = in / TX, tx = in % TX;
     if (tid < kFTok) tok[tid] = tid < tile.cnt ? __ldcg(seg.perm + tile.j0 + tid) : -1;
     __syncthreads();
     const int h = pool.h_in, R = pool.R, r0 = blockIdx.y * RT;
@@ -105,7 +110,7 @@ f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float
             av[i] = r < RT && r0 + r < R ? load4(A + (size_t)r * h, k0 + lc, k_end, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
-    float acc[4][RN] = {};
+    float acc[4][4] = {};
     load(k_beg);
     for (int k0 = k_beg; k0 < k_end; k0 += kFK) {
         __syncthreads();
@@ -122,19 +127,26 @@ f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float
         __syncthreads();
         if (k0 + kFK < k_end) load(k0 + kFK);
 #pragma unroll 8
-        for (int kk = 0; kk < kFK; ++kk) {
-            const float4 xq = *reinterpret_cast<const float4*>(&xs[kk][ty * 4]);
-            float a[RN];
+        for (int kk = 0; kk < kFK / G; ++kk) {
+            const float4 xq = *reinterpret_cast<const float4*>(&xs[kk * G + grp][ty * 4]);
+            const float4 aq = *reinterpret_cast<const float4*>(&as[kk * G + grp][tx * 4]);
+            const float x4[4] = {xq.x, xq.y, xq.z, xq.w}, a4[4] = {aq.x, aq.y, aq.z, aq.w};
 #pragma unroll
-            for (int j = 0; j < RN; ++j) a[j] = as[kk][tx * RN + j];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < RN; ++j) {
-                acc[0][j] = fmaf(xq.x, a[j], acc[0][j]);
-                acc[1][j] = fmaf(xq.y, a[j], acc[1][j]);
-                acc[2][j] = fmaf(xq.z, a[j], acc[2][j]);
-                acc[3][j] = fmaf(xq.w, a[j], acc[3][j]);
-            }
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x4[i], a4[j], acc[i][j]);
         }
+    }
+    if (G > 1) {
+        if (grp > 0)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) red[grp - 1][e * 16 * TX + in] = acc[e / 4][e % 4];
+        __syncthreads();
+        if (grp > 0) return;
+#pragma unroll
+        for (int g = 1; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e / 4][e % 4] += red[g - 1][e * 16 * TX + in];
     }
     const float scale = pool.table[tile.slot].scale;
 #pragma unroll
@@ -143,8 +155,8 @@ f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float
         if (t < 0) continue;
         float* out = s_out + ((size_t)blockIdx.z * seg.n + t) * R + r0;
 #pragma unroll
-        for (int j = 0; j < RN; ++j)
-            if (r0 + tx * RN + j < R) out[tx * RN + j] = scale * acc[i][j];
+        for (int j = 0; j < 4; ++j)
+            if (r0 + tx * 4 + j < R) out[tx * 4 + j] = scale * acc[i][j];
     }
 }
 
@@ -220,6 +232,59 @@ f32_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, in
     }
 }
 
+constexpr int kFSmallTok = 8;
+__global__ void __launch_bounds__(128)
+f32_expand_small_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, int s_parts, float* __restrict__ y,
+                        int vec) {
+    __shared__ __align__(16) float ss[kFSmallTok][kMaxRank];
+    __shared__ SegTile sh;
+    pdl_wait();
+    pdl_trigger();
+    if (__ldcg(seg.status) != LORA_OK) return;
+    const SegTile tile = find_tile<kFSmallTok>(seg, &sh);
+    if (tile.slot < 0) return;
+    const int h_out = pool.h_out, R = pool.R, o = blockIdx.y * 128 + threadIdx.x;
+    int tok[kFSmallTok];
+    float yv[kFSmallTok], acc[kFSmallTok];
+#pragma unroll
+    for (int i = 0; i < kFSmallTok; ++i) tok[i] = i < tile.cnt ? __ldcg(seg.perm + tile.j0 + i) : -1;
+#pragma unroll
+    for (int i = 0; i < kFSmallTok; ++i) {
+        yv[i] = tok[i] >= 0 && o < h_out ? __ldcg(y + (size_t)tok[i] * h_out + o) : 0.f;
+        acc[i] = 0.f;
+    }
+    for (int e = threadIdx.x; e < tile.cnt * R; e += 128) {
+        const int i = e / R, j = e - i * R, t = __ldcg(seg.perm + tile.j0 + i);
+        float v = 0.f;
+        for (int p0 = 0; p0 < s_parts; p0 += 8) {
+            float u[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) u[p] = __ldcg(s_in + ((size_t)min(p0 + p, s_parts - 1) * seg.n + t) * R + j);
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                if (p0 + p < s_parts) v += u[p];
+        }
+        ss[i][j] = v;
+    }
+    __syncthreads();
+    if (o >= h_out) return;
+    const float* Br = static_cast<const float*>(pool.B) + ((size_t)tile.slot * h_out + o) * R;
+    for (int j = 0; j < R; j += 4) {
+        const float4 b = load4(Br, j, R, vec);
+#pragma unroll
+        for (int i = 0; i < kFSmallTok; ++i) {
+            if (i >= tile.cnt) break;
+            acc[i] = fmaf(b.x, ss[i][j], acc[i]);
+            if (j + 1 < R) acc[i] = fmaf(b.y, ss[i][j + 1], acc[i]);
+            if (j + 2 < R) acc[i] = fmaf(b.z, ss[i][j + 2], acc[i]);
+            if (j + 3 < R) acc[i] = fmaf(b.w, ss[i][j + 3], acc[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kFSmallTok; ++i)
+        if (tok[i] >= 0) y[(size_t)tok[i] * h_out + o] = yv[i] + acc[i];
+}
+
 static int f32_tiles(const PoolView& pv, int n) { return (n + kFTok - 1) / kFTok + std::min(n, pv.S); }
 
 // K parts of the shrink (the expand adds them up): two CTAs an SM where K allows parts of at least 8
@@ -241,9 +306,9 @@ int launch_f32_shrink(const PoolView& pv, const SegView& sv, const void* x, floa
     int steps = (all + parts - 1) / parts;
     void* args[] = {(void*)&pv, (void*)&sv, (void*)&xp, (void*)&s_out, (void*)&vec, (void*)&steps};
     const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
-    const void* fn = rows == 16   ? (const void*)f32_shrink_kernel<1>
-                     : rows == 32 ? (const void*)f32_shrink_kernel<2>
-                                  : (const void*)f32_shrink_kernel<4>;
+    const void* fn = rows == 16   ? (const void*)f32_shrink_kernel<16>
+                     : rows == 32 ? (const void*)f32_shrink_kernel<32>
+                                  : (const void*)f32_shrink_kernel<64>;
     const dim3 grid(f32_tiles(pv, sv.n), (pv.R + rows - 1) / rows, parts);
     LORA_CUDA_TRY(launch_pdl(fn, grid, dim3(256), 0, st, args));
     return LORA_OK;
@@ -253,6 +318,14 @@ int launch_f32_expand(const PoolView& pv, const SegView& sv, const float* s_in, 
     float* yp = static_cast<float*>(y);
     int vec = pv.R % 4 == 0;
     void* args[] = {(void*)&pv, (void*)&sv, (void*)&s_in, (void*)&s_parts, (void*)&yp, (void*)&vec};
+    // up to 8 tokens a slot (64 tokens over 100 slots, r_max 8, 4096 features: 76 -> 35 us a linear); with
+    // more the tiled kernel reads B less often (200 tokens over 6 slots, r_max 64: 158 -> 132 us)
+    if (sv.n <= 8 * std::min(sv.n, pv.S)) {
+        const dim3 small((sv.n + kFSmallTok - 1) / kFSmallTok + std::min(sv.n, pv.S), (pv.h_out + 127) / 128);
+        if (small.y > 65535) return set_error(LORA_EUNSUP, "float32 expand of %d features", pv.h_out);
+        LORA_CUDA_TRY(launch_pdl((const void*)f32_expand_small_kernel, small, dim3(128), 0, st, args));
+        return LORA_OK;
+    }
     const dim3 grid(f32_tiles(pv, sv.n), (pv.h_out + 63) / 64);
     if (grid.y > 65535) return set_error(LORA_EUNSUP, "float32 expand of %d features", pv.h_out);
     LORA_CUDA_TRY(launch_pdl((const void*)f32_expand_kernel, grid, dim3(256), 0, st, args));

@@ -358,6 +358,18 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                             }
                         }
                         __syncwarp();
+                        if (!a.vec) {  // rows off 16-byte boundaries: an element a lane, neighbours side by side
+                            for (int rr = 0; rr < kStaged; ++rr) {
+                                const int yr = __shfl_sync(0xffffffffu, yrow, r0 + rr);
+                                if (yr < 0) continue;
+#pragma unroll
+                                for (int e = lane; e < kCols; e += 32)
+                                    if (c0[i] + e < a.h_out)
+                                        y[(long long)yr * a.ldy + c0[i] + e] = *reinterpret_cast<const T*>(
+                                            ys + rr * 128 + (((e / per) ^ (rr & 7)) << 4) + e % per * sizeof(T));
+                            }
+                            continue;
+                        }
 #pragma unroll
                         for (int k = 0; k < kStaged; k += 4) {
                             const int rr = k + (lane >> 3);
@@ -365,7 +377,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                             const uint4 v = *reinterpret_cast<const uint4*>(ys + rr * 128 + ((c ^ (rr & 7)) << 4));
                             if (yr < 0) continue;
                             T* yp = y + (long long)yr * a.ldy + col;
-                            if (a.vec && col + per <= a.h_out) {
+                            if (col + per <= a.h_out) {
                                 *reinterpret_cast<uint4*>(yp) = v;
                             } else {
                                 alignas(16) T e8[per];
