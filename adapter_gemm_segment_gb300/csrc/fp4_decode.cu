@@ -46,7 +46,7 @@ struct Fp4DecodeArgs {
     long long ldy;
     int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, tmem_cols, kt, early_w, early_x, vec, ring_bytes, push;
     // the LoRA term (fuse)
-    int fuse, R, s_parts, bf16;
+    int R, s_parts, bf16;
     const float* s_in;    // [s_parts][n][R]
     const int32_t* idx;
     const void* B;
@@ -103,7 +103,8 @@ __device__ __forceinline__ void build_tokens(const Fp4DecodeArgs& a, uint8_t* S,
     }
 }
 
-template <typename T>
+// FUSE: with the LoRA term.  Without it the kernel is a third as long.
+template <typename T, bool FUSE>
 __global__ void __launch_bounds__(kDThreads, 1)
 fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                   const __grid_constant__ CUtensorMap tmB, const Fp4DecodeArgs a) {
@@ -114,7 +115,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 128;
     const uint32_t stage_bytes = kDWBytes + x_bytes;
     const uint32_t schunk = static_cast<uint32_t>(n_pad) * 16;                 // token side of a chunk
-    const uint32_t lora_bytes = a.fuse ? kDChunks * (2048 + schunk) : 0;
+    const uint32_t lora_bytes = FUSE ? kDChunks * (2048 + schunk) : 0;
     uint8_t* lora_sm = smem + (size_t)stages * stage_bytes;                    // [2] {features, tokens}
     uint32_t* seen = reinterpret_cast<uint32_t*>(smem + a.ring_bytes);         // [64]
     int* before = reinterpret_cast<int*>(seen + 64);                           // [64]
@@ -236,7 +237,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                               sfw + 4 * (k >> 1), sfx + 8 * (k >> 1), (i > 0 || k > 0) ? 1u : 0u);
                 umma_commit(&empty[s]);
             }
-            if (ok && a.fuse) {
+            if (FUSE && ok) {
                 ok = mbar_wait(linfo, 0, flags);
                 const int blocks = ok ? flags[1] : 0;
                 const uint32_t idesc_lora = idesc_f16(kDM, n_pad, a.bf16 != 0);
@@ -334,9 +335,9 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         }
     }
 
-    if (warp >= 2 && a.fuse) {
+    if constexpr (FUSE) {
         // ---- LoRA blocks: this CTA's share of the batch's (adapter, 8 columns) chunks ----
-        if constexpr (sizeof(T) == 2) {
+        if (warp >= 2) {
             const int chunks = a.R / 8;
             auto issue_b = [&](int b, int P_all) {  // the feature side of this CTA's block b
                 const int p0 = (split + b * a.splits) * kDChunks, cnt = min(kDChunks, P_all - p0);
@@ -462,7 +463,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     }
     if (warp >= 2 && warp < 6) {
         const int row = (warp & 3) * 32 + lane, o = m_tile * kDM + row;
-        const bool got = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, flags) && (!a.fuse || mbar_wait(lora_done, 0, flags)));
+        const bool got = __all_sync(0xffffffffu, mbar_wait(acc_full, 0, flags) && (!FUSE || mbar_wait(lora_done, 0, flags)));
         if (got) {
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -479,8 +480,8 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
 #pragma unroll
                         for (int c = 16 * q; c < 16 * q + 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
             }
-            if constexpr (sizeof(T) == 2) {
-                if (a.fuse && flags[2] && o < a.h_out) {  // elements of B left out of the blocks
+            if constexpr (FUSE) {
+                if (flags[2] && o < a.h_out) {  // elements of B left out of the blocks
                     const int chunks = a.R / 8;
                     for (int t = 0; t < n; ++t) {
                         if (dl_sm[t] < 0) continue;
@@ -610,7 +611,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     if (warp == 1) tmem_dealloc(tmem, a.tmem_cols);
 }
 
-template <typename T>
+template <typename T, bool FUSE>
 static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long long ldy, int32_t* status, int early,
                                const Fp4DecodeLora* lora, cudaStream_t st) {
     Fp4DecodeArgs a;
@@ -637,7 +638,6 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
     PoolView pv;
     if (lora) {
         pv = *lora->pool;
-        a.fuse = 1;
         a.R = pv.R;
         a.s_parts = lora->s_parts;
         a.bf16 = pv.dtype == LORA_BF16;
@@ -669,7 +669,7 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
     if (!lora) mB = mW;  // not used
     static bool attr_set = false;
     if (!attr_set) {
-        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_decode_kernel<T, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
         attr_set = true;
     }
     void* args[] = {(void*)&mW, (void*)&mX, (void*)&mB, (void*)&a};
@@ -688,7 +688,7 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    LORA_CUDA_TRY(cudaLaunchKernelExC(&cfg, (const void*)fp4_decode_kernel<T>, args));
+    LORA_CUDA_TRY(cudaLaunchKernelExC(&cfg, (const void*)fp4_decode_kernel<T, FUSE>, args));
     count_launch();
     return LORA_OK;
 }
@@ -697,10 +697,13 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
 
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                       int early, const Fp4DecodeLora* lora, cudaStream_t st) {
+    if (lora && dtype == LORA_F16)
+        return tc::launch_fp4_decode_t<__half, true>(x, w, y, ldy, status, early, lora, st);
+    if (lora) return tc::launch_fp4_decode_t<__nv_bfloat16, true>(x, w, y, ldy, status, early, lora, st);
     switch (dtype) {
-        case LORA_F32: return tc::launch_fp4_decode_t<float>(x, w, y, ldy, status, early, nullptr, st);
-        case LORA_F16: return tc::launch_fp4_decode_t<__half>(x, w, y, ldy, status, early, lora, st);
-        default: return tc::launch_fp4_decode_t<__nv_bfloat16>(x, w, y, ldy, status, early, lora, st);
+        case LORA_F32: return tc::launch_fp4_decode_t<float, false>(x, w, y, ldy, status, early, nullptr, st);
+        case LORA_F16: return tc::launch_fp4_decode_t<__half, false>(x, w, y, ldy, status, early, nullptr, st);
+        default: return tc::launch_fp4_decode_t<__nv_bfloat16, false>(x, w, y, ldy, status, early, nullptr, st);
     }
 }
 
