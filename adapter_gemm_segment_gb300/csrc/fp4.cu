@@ -268,8 +268,15 @@ static int dequantize_t(const Fp4View& q, void* out, long long ld, cudaStream_t 
 
 static int launch_fp4_product(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                               bool early_w, cudaStream_t st) {
-    return x.rows <= 256 ? launch_fp4_decode(x, w, y, dtype, ldy, status, early_w ? 2 : 0, nullptr, st)
-                         : launch_fp4_pair(x, w, y, dtype, ldy, status, early_w, nullptr, st);
+    // The pair kernel also for batches whose split sums would not fit beside the receive buffer (more than
+    // 224 tokens), unless K is long, and for wide outputs, where the decode kernel does not split K.
+    // Measured, us a call, decode / pair: 256 tokens 4096 x 4096 14.5 / 11.8, 1024 x 1024 12.2 / 8.0,
+    // 11008 x 4096 20.0 / 21.3; 160 tokens 4096 x 11008 14.5 / 12.8, 4096 x 4096 9.9 / 11.6; 96 tokens
+    // 4096 x 11008 12.9 / 12.6, 4096 x 4096 8.0 / 11.6.
+    const bool wide = (w.rows + 127) / 128 * 2 > num_sms();
+    const bool pair = x.rows > 256 || (x.rows > 224 && x.cols <= 8192) || (x.rows > 64 && wide);
+    return pair ? launch_fp4_pair(x, w, y, dtype, ldy, status, early_w, nullptr, st)
+                : launch_fp4_decode(x, w, y, dtype, ldy, status, early_w ? 2 : 0, nullptr, st);
 }
 
 // grid.z counts 128-row tiles
@@ -305,6 +312,17 @@ static int check_rows(const void* p, int dtype, int64_t ld, int rows, int cols, 
 
 static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev, m->scales_dev, m->rows, m->cols); }
 
+// Batches of more than 256 tokens whose tokens are spread over many adapters (fewer than 16 a slot) at
+// ranks of up to 32: the product without the LoRA term, and the segmented expand after it, as the
+// framework's separate variant.  The fused product then builds a LoRA block for almost every adapter in
+// every tile.  Measured, us a linear separate / fused, 4096 x 4096, 100 slots, r_max 16, every token its
+// own adapter: 300 tokens 31 / 50, 600 34 / 65, 1200 47 / 75, 2400 76 / 73; a run of 512 tokens an
+// adapter: 600 tokens 32 / 26, 1200 45 / 33.  At r_max 64 the expand's re-reads of B cost what the blocks
+// do (600 tokens 86 / 198 spread, 65 / 28 in runs), and the fused product stays.
+static bool fp4_separate(int n, int S, int R, int dtype) {
+    return dtype != LORA_F32 && n > 256 && R <= 32 && n < 16LL * std::min(n, S);
+}
+
 // Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their rounded
 // sum), then the stored form of x.
 struct Fp4WsLayout {
@@ -316,7 +334,7 @@ static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
     size_t s16_bytes = 0;
-    if (n > 256 && pool->desc.dtype != LORA_F32) {
+    if (n > 256 && pool->desc.dtype != LORA_F32 && !fp4_separate(n, pool->desc.n_slots, pool->desc.r_max, pool->desc.dtype)) {
         s16_bytes = (size_t)n * pool->desc.r_max * 2;
         s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * 2 * s16_bytes;
     }
@@ -420,6 +438,13 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
     const SegView sv = seg_view(seg);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
 
+    if (fp4_separate(n, pv.S, pv.R, pv.dtype)) {
+        int s_parts = 1;
+        if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
+        if (!rc) rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/false, &s_parts);
+        if (!rc) rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
+        return rc ? rc : launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
+    }
     if (n > 256 && pv.dtype != LORA_F32) {
         const Fp4View own = fp4_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
         rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, ws + L.s16_off, st);

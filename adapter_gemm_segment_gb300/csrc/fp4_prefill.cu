@@ -115,17 +115,18 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     uint64_t* empty = full + kPMaxStages;    // the even CTA's commits (multicast)
     uint64_t* acc_full = empty + kPMaxStages;  // [2] (multicast)
     uint64_t* ov_free = acc_full + 2;        // even CTA: the shared columns are drained (16 warps)
-    uint64_t* lora_full = ov_free + 1;       // [2] even CTA: a LoRA block is written (8 warps)
-    uint64_t* lora_empty = lora_full + 2;    // [2] (multicast)
+    uint64_t* lora_own = ov_free + 1;        // [2] a LoRA block of this CTA is written (4 warps)
+    uint64_t* lora_peer = lora_own + 2;      // [2] even CTA: the odd CTA's block is written (relayed)
+    uint64_t* lora_empty = lora_peer + 2;    // [2] (multicast)
     // by parity of the tile (the LoRA warps may be a tile ahead of the others):
-    uint64_t* linfo = lora_empty + 2;        // [2] even CTA: the tile's number of LoRA blocks is known
-    uint64_t* epi_done = linfo + 2;          // [2] the epilogues are through with the tile (16 warps of both CTAs)
+    uint64_t* linfo = lora_empty + 2;        // [2] the tile's number of LoRA blocks is known
+    uint64_t* epi_done = linfo + 2;          // [2] the epilogues (16 warps of both CTAs) and the odd CTA's relay are through
     uint64_t* lora_done = epi_done + 2;      // [2] the tile's LoRA blocks are written (8 warps of both CTAs)
     uint64_t* drained = lora_done + 2;       // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     // abort, -, then by parity of the tile: [2] 1 + the last tile with a non-finite B, [2] LoRA blocks
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kPMaxStages + 14) * 8 + 28 <= 256, "barrier area");
+    static_assert((2 * kPMaxStages + 16) * 8 + 28 <= 256, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -140,10 +141,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&lora_full[b], 8);
+            mbar_init(&lora_own[b], 4);
+            mbar_init(&lora_peer[b], 1);
             mbar_init(&lora_empty[b], 1);
             mbar_init(&linfo[b], 1);
-            mbar_init(&epi_done[b], 16);
+            mbar_init(&epi_done[b], rank == 1 ? 17 : 16);
             mbar_init(&lora_done[b], 8);
         }
         mbar_init(ov_free, 16);
@@ -244,7 +246,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                     const int blocks = flags[4 + buf];
                     for (int b = 0; b < blocks; ++b, ++lb) {
                         const int lbuf = lb & 1;
-                        if (!mbar_wait_cluster(&lora_full[lbuf], (lb >> 1) & 1, flags)) {
+                        if (!mbar_wait(&lora_own[lbuf], (lb >> 1) & 1, flags) ||
+                            !mbar_wait_cluster(&lora_peer[lbuf], (lb >> 1) & 1, flags)) {
                             ok = false;
                             break;
                         }
@@ -266,6 +269,23 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const unsigned long long t0 = globaltimer();
             while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kWaitLimitNs) {
             }
+        } else if (lane == 0 && a.fuse) {
+            // odd CTA: tells the even one that a LoRA block is written.  A release at cluster scope waits
+            // for every access of its thread, so it is this thread's and not the writers', whose next
+            // loads it would wait for (600 tokens over 100 adapters of rank 16: 76 against 65 us).
+            const uint32_t peer0 = mapa_shared(smem_u32(lora_peer), 0);
+            int local = 0, lb = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok; tile += npairs, ++local) {
+                ok = mbar_wait(&linfo[local & 1], (local >> 1) & 1, flags);
+                const int blocks = ok ? flags[4 + (local & 1)] : 0;
+                for (int b = 0; b < blocks && ok; ++b, ++lb) {
+                    ok = mbar_wait(&lora_own[lb & 1], (lb >> 1) & 1, flags);
+                    if (ok) mbar_arrive_cluster(peer0 + static_cast<uint32_t>(lb & 1) * 8u);
+                }
+                if (ok) mbar_arrive(&epi_done[local & 1]);
+            }
+            if (!ok && a.status) report_timeout_status(a.status);
         }
     } else if (warp < 10) {
         // ---- epilogue: thread <-> token row (TMEM lane) of this CTA's half; two warps share a row,
@@ -492,7 +512,6 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         if constexpr (sizeof(T) == 2) {
             pdl_wait();
             const int status = a.status ? __ldcg(a.status) : LORA_OK;
-            const uint32_t lora_full0 = mapa_shared(smem_u32(lora_full), 0);
             const uint32_t other_done = mapa_shared(smem_u32(lora_done), rank ^ 1);
             const uint32_t other_flags = mapa_shared(smem_u32(const_cast<int*>(flags)), rank ^ 1);
             const int chunks = a.R / 8;
@@ -525,7 +544,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 named_bar_sync(2, 128);
                 const int P = *distinct * chunks;  // 8-column chunks of the tile's adapters
                 const int blocks = (P + 3) / 4;
-                if (rank == 0 && lt == 0) {
+                if (lt == 0) {
                     flags[4 + (local & 1)] = blocks;
                     mbar_arrive(&linfo[local & 1]);
                 }
@@ -550,11 +569,10 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                         }
                     }
                 };
-                uint4 sv[4], bv[4], sn[4], bn[4];
+                uint4 sv[4], bv[4];
                 if (blocks > 0) load(sv, bv);
                 for (int b = 0; b < blocks; ++b, ++lb) {
                     const int lbuf = lb & 1;
-                    if (b + 1 < blocks) load(sn, bn);  // the next block's loads in flight meanwhile
                     if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((lb >> 1) & 1) ^ 1, flags))) {
                         ok = false;
                         break;
@@ -569,12 +587,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                         }
                         *reinterpret_cast<uint4*>(blk + j * kPLoraChunk + lt * 16) = sv[j];
                         *reinterpret_cast<uint4*>(blk + (4 + j) * kPLoraChunk + lt * 16) = bv[j];
-                        sv[j] = sn[j];
-                        bv[j] = bn[j];
                     }
                     fence_proxy_async_smem();  // read by the tensor cores
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(lora_full0 + static_cast<uint32_t>(lbuf) * 8u);
+                    if (lane == 0) mbar_arrive(&lora_own[lbuf]);
+                    if (b + 1 < blocks) load(sv, bv);  // in flight while the buffer is waited for
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -683,8 +700,14 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
 constexpr int kQWorkers = 16;   // worker warps: with two CTAs an SM, 32 to hide their latencies
 constexpr int kQThreads = 64 + 32 * kQWorkers;  // warp 0: A rows, warp 1: MMAs
 constexpr uint32_t kQXBytes = 128 * 256;  // two 64-column swizzled halves
-// Accumulator columns (A rows) per pass: 64, so that two CTAs share an SM, unless one adapter has more.
-inline int prep_cap(int R) { return std::max(64, (R + 15) / 16 * 16); }
+// Accumulator columns (A rows) per pass.  64 lets two CTAs share an SM; 256 (one CTA) where the grid does not
+// fill the SMs twice anyway, or where 128 sorted tokens are likely to name more adapters than 64 columns
+// hold, each pass reading x again.
+inline int prep_cap(int n, int S, int R, int ctas) {
+    const int per_adapter = std::max(1, n / std::max(1, std::min(n, S)));
+    const int columns = std::min(S, 128 / per_adapter + 1) * R;
+    return ctas <= num_sms() || columns > 64 ? 256 : std::max(64, (R + 15) / 16 * 16);
+}
 inline size_t prep_smem(int cap) { return 2 * ((size_t)kQXBytes + cap * 256) + 1024 + 128 * 4 + 64 * 8 + 128 * 4 + 256; }
 
 struct PrepArgs {
@@ -992,10 +1015,10 @@ static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x
     a.s = s;
     a.s16 = s16;
     a.bf16 = std::is_same<T, __nv_bfloat16>::value;
-    a.cap = prep_cap(pv.R);
     const int parts = fp4_prepare_parts(sv.n, q.ktiles);
     a.steps = (q.ktiles + parts - 1) / parts;
     a.parts = parts;
+    a.cap = prep_cap(sv.n, pv.S, pv.R, (sv.n + 127) / 128 * parts);
     CUtensorMap mA;
     const int rc = make_map(&mA, pv.A, a.bf16, pv.h_in, (uint64_t)pv.S * pv.R, pv.R);
     if (rc) return rc;
