@@ -37,14 +37,6 @@ template <typename T> struct Raw8 {
 template <> struct Raw8<float> {
     float4 a, b;
 };
-// 16 bytes that are read once; issued where it stands (a plain load may be moved down to its use).
-__device__ __forceinline__ uint4 ld_stream16(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
 // Largest |x| of two packed pairs (a NaN wins), without and with the absolute values taken.
 template <typename T> __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b);
 template <> __device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t a, uint32_t b) {
