@@ -99,6 +99,27 @@ struct Ring {
     }
 };
 
+// 16 bytes of T from float32 bits, each rounded once.
+template <typename T> __device__ __forceinline__ uint4 round16(const uint32_t* r) {
+    if constexpr (sizeof(T) == 4) {
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            if constexpr (std::is_same<T, __half>::value) {
+                const __half2 h = __float22half2_rn(f);
+                memcpy(&w[i], &h, 4);
+            } else {
+                const __nv_bfloat162 h = __float22bfloat162_rn(f);
+                memcpy(&w[i], &h, 4);
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const PairArgs a) {
@@ -364,18 +385,16 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                     // lanes write 128 consecutive bytes of a row of y.  (Whole 32-byte sectors straight from
                     // the registers were slower: 131 against 120 us for 8191 x 11008 x 4096 in float32.)
                     const int c = lane & 7, col = c0[i] + c * per;
+                    uint4 w[8];  // the piece in y's type
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = round16<T>(&r[i * kCols + k * per]);
 #pragma unroll
                     for (int r0 = 0; r0 < 32; r0 += kStaged) {
                         __syncwarp();
                         if (lane >= r0 && lane < r0 + kStaged) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                alignas(16) T v[per];
-#pragma unroll
-                                for (int e = 0; e < per; ++e) v[e] = from_f32<T>(__uint_as_float(r[i * kCols + k * per + e]));
-                                *reinterpret_cast<uint4*>(ys + (lane - r0) * 128 + ((k ^ (lane & 7)) << 4)) =
-                                    *reinterpret_cast<const uint4*>(v);
-                            }
+                            for (int k = 0; k < 8; ++k)
+                                *reinterpret_cast<uint4*>(ys + (lane - r0) * 128 + ((k ^ (lane & 7)) << 4)) = w[k];
                         }
                         __syncwarp();
                         if (!a.vec) {  // rows off 16-byte boundaries: an element a lane, neighbours side by side

@@ -463,3 +463,79 @@ def test_large_offsets(lib):
     y = torch.empty(70000, 16640, dtype=torch.bfloat16, device="cuda")
     lib.lora_fp4_matmul(big, w, y)
     assert (y[-1] == 64).all() and bool((y.sum(1, dtype=torch.float32) == 64.0 * 16640).all())
+
+
+# ---- sizes at which the calls above change their path --------------------------------------------
+
+@pytest.mark.parametrize("n,m,k,dtype,pad", [
+    (225, 136, 300, 0, 0), (240, 1000, 8192, 1, 1), (240, 300, 8200, 2, 0), (256, 1, 33, 0, 0), (65, 9736, 256, 2, 0),
+    (64, 9736, 256, 1, 0), (100, 11008, 130, 0, 3), (224, 264, 512, 1, 0)])
+def test_product_between_small_and_large(lib, n, m, k, dtype, pad):
+    g = torch.Generator().manual_seed(n + m + k)
+    check_product(lib, torch.randn(n, k, generator=g), torch.randn(m, k, generator=g) * 0.02, DTYPES[dtype], pad)
+
+
+HEAVY = [  # n, h_in, ranks, r_max, run: small batches with many rows of A, and of few or many adapters
+    (64, 2048, [64, 8, 32], 64, 1), (200, 2048, [64, 8, 16, 64, 33, 1], 64, 1), (129, 11008, [40] * 3, 40, 43),
+    (256, 4096, [8], 8, 256), (250, 1000, [256, 100], 256, 1), (33, 1032, [256, 3], 256, 2), (256, 520, [128, 64, 1], 128, 7),
+    (250, 2048, [64] * 30, 64, 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,h_in,ranks,r_max,run", HEAVY)
+def test_linear_small_batches_of_high_rank(lib, dtype, n, h_in, ranks, r_max, run):
+    rng = np.random.default_rng([n, h_in])
+    idx = np.repeat(rng.integers(-1, len(ranks), size=(n + run - 1) // run), run)[:n]
+    case = wl.random_case(51, n, h_in, 264, ranks, r_max=r_max, dtype=dtype, idx=idx)
+    a = check_linear(lib, case)
+    assert torch.equal(a, check_linear(lib, case, with_xq=True))
+    check_linear(lib, case, zero_base=True)
+
+
+@pytest.mark.parametrize("n,h_in,slots,r_max", [(200, 2048, 3, 64), (250, 2048, 30, 64), (300, 512, 40, 16), (700, 256, 100, 32)])
+@pytest.mark.parametrize("poison", ["A", "B", "x"])
+def test_a_broken_input_stays_with_its_tokens(lib, n, h_in, slots, r_max, poison):
+    """A NaN in one tenant's adapter, or in one token, at the sizes of the paths above."""
+    idx = (np.arange(n) % (slots + 1) - 1).astype(np.int32)
+    case = wl.random_case(52, n, h_in, 136, [r_max] * slots, r_max=r_max, dtype=torch.float16, idx=idx)
+    w = stored(lib, case.W)
+
+    def run():
+        pool = make_pool(lib, case)
+        y = pool.fp4_linear(w, case.x.cuda(), pool.segment(case.idx.cuda()))
+        torch.cuda.synchronize()
+        pool.close()
+        return y
+
+    clean = run()
+    if poison == "x":
+        case.x[n - 2, 5] = float("nan")
+        own = np.arange(n) == n - 2
+    else:
+        getattr(case.adapters, poison)[1].view(-1)[3] = float("nan")
+        own = idx == 1
+    dirty = run()
+    others = torch.from_numpy(~own).cuda()
+    assert torch.equal(dirty[others], clean[others])
+    assert torch.isnan(dirty[~others]).any(dim=1).all()
+
+
+@pytest.mark.parametrize("n,h_in,slots,r_max", [(200, 2048, 3, 64), (256, 4096, 2, 8), (300, 512, 40, 16)])
+@pytest.mark.parametrize("what", ["none", "last", "invalid"])
+def test_patterns_at_those_sizes(lib, n, h_in, slots, r_max, what):
+    idx = np.full(n, -1, np.int32)
+    if what == "last":
+        idx[-1] = slots - 1
+    case = wl.random_case(53, n, h_in, 136, [r_max] * slots, r_max=r_max, dtype=torch.bfloat16, idx=idx)
+    if what != "invalid":
+        check_linear(lib, case)
+        return
+    pool = make_pool(lib, case)
+    bad = case.idx.clone()
+    bad[0] = slots
+    seg = pool.segment(bad.cuda())
+    y = torch.full((n, 136), 3.0, dtype=torch.bfloat16, device="cuda")
+    pool.fp4_linear(stored(lib, case.W), case.x.cuda(), seg, y=y)
+    assert lib.lora_segment_status(seg) == lib.LORA_EIDX
+    assert (y == 3.0).all()
+    pool.close()
