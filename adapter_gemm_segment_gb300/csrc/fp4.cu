@@ -353,8 +353,20 @@ static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev,
 // own adapter: 300 tokens 31 / 50, 600 34 / 65, 1200 47 / 75, 2400 76 / 73; a run of 512 tokens an
 // adapter: 600 tokens 32 / 26, 1200 45 / 33.  At r_max 64 the expand's re-reads of B cost what the blocks
 // do (600 tokens 86 / 198 spread, 65 / 28 in runs), and the fused product stays.
-static bool fp4_separate(int n, int S, int R, int dtype) {
-    return dtype != LORA_F32 && n > 256 && R <= 32 && n < 16LL * std::min(n, S);
+//
+// From 32 to 256 tokens the same choice weighs, in us, the blocks that each of the decode kernel's CTAs
+// would build if as many adapters as can be are there, against the expand and its launch.  Measured,
+// fused / separate, Zipf-distributed adapters, 4096 -> 4096 and 4096 -> 11008 features: 64 tokens, 100 slots
+// r_max 8 13.9 / 15.3 and 20.5 / 19.8, r_max 32 22.7 / 19.6 and 49 / 25; 128 tokens, 30 slots r_max 16
+// 19.4 / 19.1 and 28.7 / 26.8; 250 tokens, 6 slots r_max 64 29.9 / 41.9 and 37 / 57, 100 slots r_max 64
+// 75 / 50 and 209 / 93.  (16 tokens: fused throughout.)
+static bool fp4_separate(const PoolView& pv, int n) {
+    if (pv.dtype == LORA_F32) return false;
+    const int adapters = std::min(n, pv.S);
+    if (n > 256) return pv.R <= 32 && n < 16LL * adapters;
+    if (n < 32) return false;
+    const double blocks = (double)adapters * pv.R / 32 / fp4_decode_splits(pv.h_out, pv.h_in);
+    return blocks * (0.35 + 0.0025 * n) > 4 + (double)n * pv.R * pv.h_out / 6e6;
 }
 
 // Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their rounded
@@ -368,7 +380,7 @@ static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
     size_t s16_bytes = 0;
-    if (n > 256 && pool->desc.dtype != LORA_F32 && !fp4_separate(n, pool->desc.n_slots, pool->desc.r_max, pool->desc.dtype)) {
+    if (n > 256 && pool->desc.dtype != LORA_F32 && !fp4_separate(pool_view(pool), n)) {
         s16_bytes = (size_t)n * pool->desc.r_max * 2;
         s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * 2 * s16_bytes;
     }
@@ -472,7 +484,7 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
     const SegView sv = seg_view(seg);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
 
-    if (fp4_separate(n, pv.S, pv.R, pv.dtype)) {
+    if (fp4_separate(pv, n)) {
         int s_parts = 1;
         if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (!rc) rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/false, &s_parts);

@@ -631,10 +631,8 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
     // y is written 16 bytes at a time when every row starts on a 16-byte boundary
     a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     const int m_tiles = (w.rows + kDM - 1) / kDM;
-    int splits = std::max(1, num_sms() / m_tiles);
-    splits = std::min({splits, 8, a.kb_total});
-    a.kb_per_split = (a.kb_total + splits - 1) / splits;
-    a.splits = (a.kb_total + a.kb_per_split - 1) / a.kb_per_split;
+    a.splits = fp4_decode_splits(w.rows, w.cols);
+    a.kb_per_split = (a.kb_total + a.splits - 1) / a.splits;
     PoolView pv;
     if (lora) {
         pv = *lora->pool;
@@ -694,6 +692,13 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
 }
 
 }  // namespace tc
+
+// CTAs (a cluster) that share K: as many as let every feature tile have an SM a CTA.
+int fp4_decode_splits(int h_out, int h_in) {
+    const int m_tiles = (h_out + tc::kDM - 1) / tc::kDM, steps = (h_in + 255) / 256;
+    const int splits = std::min({std::max(1, num_sms() / m_tiles), 8, steps}), per = (steps + splits - 1) / splits;
+    return (steps + per - 1) / per;
+}
 
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                       int early, const Fp4DecodeLora* lora, cudaStream_t st) {

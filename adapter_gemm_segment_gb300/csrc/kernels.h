@@ -119,6 +119,7 @@ struct Fp4DecodeLora {
     const float* s_in;
     int s_parts;
 };
+int fp4_decode_splits(int h_out, int h_in);
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                       int early, const Fp4DecodeLora* lora, cudaStream_t st);
 // The kernel before it for small batches: x quantised into q (nullptr: not) and the shrink output in
