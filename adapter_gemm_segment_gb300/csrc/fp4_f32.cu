@@ -8,7 +8,7 @@
 // 256 threads; a thread keeps 4 tokens x 4 columns.  Operands pass through shared memory 32 deep, k-major,
 // so that a step of k is two 16-byte reads for 16 multiply-adds; the next 32 are on their way meanwhile.
 // Bound by the multiply-adds at r_max 64, by the reads of x and y below.  The 16-bit pools' tensor-core
-// kernels take 3 to 5 times less (1000 tokens, 4096 x 1000, r_max 32: 67 against 34 us a linear).  Where segments hold few
+// kernels take 3 to 5 times less (1000 tokens, 4096 x 1000, r_max 32: 49 against 34 us a linear).  Where segments hold few
 // tokens, the expand gives a thread one feature of up to 8 tokens instead.
 #include <algorithm>
 
@@ -160,9 +160,15 @@ f32_shrink_kernel(PoolView pool, SegView seg, const float* __restrict__ x, float
     }
 }
 
+// A CTA keeps its tokens' s in shared memory and goes over every gridDim.y-th tile of 64 features: finding
+// its tokens takes five dependent loads, as long as the product of one feature tile.  (6122 tokens, 2992
+// features, r_max 24, a CTA per feature tile: 93 us, this way 54.)  B of the next step and y of the next
+// feature tile are on their way while a step is multiplied.
 __global__ void __launch_bounds__(256)
-f32_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, int s_parts, float* __restrict__ y, int vec) {
-    __shared__ float ss[kFK][kFTok + kFPad];
+f32_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, int s_parts, float* __restrict__ y, int vec,
+                  int vec_y) {
+    extern __shared__ float4 ss_raw[];
+    float(*ss)[kFTok + kFPad] = reinterpret_cast<float(*)[kFTok + kFPad]>(ss_raw);  // [r_max rounded up to kFK]
     __shared__ float bs[kFK][64 + kFPad];
     __shared__ SegTile sh;
     __shared__ int tok[kFTok];
@@ -174,23 +180,28 @@ f32_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, in
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
     if (tid < kFTok) tok[tid] = tid < tile.cnt ? __ldcg(seg.perm + tile.j0 + tid) : -1;
     __syncthreads();
-    const int h_out = pool.h_out, R = pool.R, o0 = blockIdx.y * 64;
-    const float* B = static_cast<const float*>(pool.B) + ((size_t)tile.slot * h_out + o0) * R;
+    const int h_out = pool.h_out, R = pool.R, step_o = gridDim.y * 64;
+    const float* B = static_cast<const float*>(pool.B) + (size_t)tile.slot * h_out * R;
     const int lr = tid >> 3, lc = (tid & 7) * 4;
-    // y is read while the product runs
-    float yv[4][4];
+    float4 bv[2], yv[4];
+    auto load_b = [&](int o0, int k0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = tok[ty * 4 + i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int o = o0 + tx * 4 + j;
-            yv[i][j] = t >= 0 && o < h_out ? __ldcg(y + (size_t)t * h_out + o) : 0.f;
+        for (int i = 0; i < 2; ++i) {
+            const int o = o0 + lr + 32 * i;
+            bv[i] = o < h_out ? load4(B + (size_t)o * R, k0 + lc, R, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    }
-    float acc[4][4] = {};
+    };
+    auto load_y = [&](int o0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = tok[ty * 4 + i];
+            yv[i] = t >= 0 ? load4(y + (size_t)t * h_out, o0 + tx * 4, h_out, vec_y) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    int o0 = blockIdx.y * 64;
+    load_b(o0, 0);
+    load_y(o0);
     for (int k0 = 0; k0 < R; k0 += kFK) {
-        __syncthreads();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = lr + 32 * i, t = tok[r];
@@ -205,30 +216,50 @@ f32_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, in
                     for (int p = 0; p < 4; ++p)
                         if (p0 + p < s_parts) v.x += u[p].x, v.y += u[p].y, v.z += u[p].z, v.w += u[p].w;
                 }
-            const float4 b = o0 + r < h_out ? load4(B + (size_t)r * R, k0 + lc, R, vec) : make_float4(0.f, 0.f, 0.f, 0.f);
-            ss[lc][r] = v.x, ss[lc + 1][r] = v.y, ss[lc + 2][r] = v.z, ss[lc + 3][r] = v.w;
-            bs[lc][r] = b.x, bs[lc + 1][r] = b.y, bs[lc + 2][r] = b.z, bs[lc + 3][r] = b.w;
-        }
-        __syncthreads();
-        const int depth = min(kFK, R - k0);
-        for (int kk = 0; kk < depth; ++kk) {
-            const float4 sq = *reinterpret_cast<const float4*>(&ss[kk][ty * 4]);
-            const float4 bq = *reinterpret_cast<const float4*>(&bs[kk][tx * 4]);
-            const float s4[4] = {sq.x, sq.y, sq.z, sq.w}, b4[4] = {bq.x, bq.y, bq.z, bq.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s4[i], b4[j], acc[i][j]);
+            ss[k0 + lc][r] = v.x, ss[k0 + lc + 1][r] = v.y, ss[k0 + lc + 2][r] = v.z, ss[k0 + lc + 3][r] = v.w;
         }
     }
+    for (; o0 < h_out; o0 += step_o) {
+        float acc[4][4] = {};
+        for (int k0 = 0; k0 < R; k0 += kFK) {
+            __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = tok[ty * 4 + i];
-        if (t < 0) continue;
-        float* yr = y + (size_t)t * h_out + o0 + tx * 4;
+            for (int i = 0; i < 2; ++i) {
+                const int r = lr + 32 * i;
+                bs[lc][r] = bv[i].x, bs[lc + 1][r] = bv[i].y, bs[lc + 2][r] = bv[i].z, bs[lc + 3][r] = bv[i].w;
+            }
+            __syncthreads();
+            if (k0 + kFK < R)
+                load_b(o0, k0 + kFK);
+            else if (o0 + step_o < h_out)
+                load_b(o0 + step_o, 0);
+            const int depth = min(kFK, R - k0);
+            for (int kk = 0; kk < depth; ++kk) {
+                const float4 sq = *reinterpret_cast<const float4*>(&ss[k0 + kk][ty * 4]);
+                const float4 bq = *reinterpret_cast<const float4*>(&bs[kk][tx * 4]);
+                const float s4[4] = {sq.x, sq.y, sq.z, sq.w}, b4[4] = {bq.x, bq.y, bq.z, bq.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (o0 + tx * 4 + j < h_out) yr[j] = yv[i][j] + acc[i][j];
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s4[i], b4[j], acc[i][j]);
+            }
+        }
+        const int o = o0 + tx * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = tok[ty * 4 + i];
+            if (t < 0) continue;
+            float* yr = y + (size_t)t * h_out + o;
+            const float v[4] = {yv[i].x + acc[i][0], yv[i].y + acc[i][1], yv[i].z + acc[i][2], yv[i].w + acc[i][3]};
+            if (vec_y && o + 4 <= h_out) {
+                *reinterpret_cast<float4*>(yr) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (o + j < h_out) yr[j] = v[j];
+            }
+        }
+        if (o0 + step_o < h_out) load_y(o0 + step_o);
     }
 }
 
@@ -287,13 +318,14 @@ f32_expand_small_kernel(PoolView pool, SegView seg, const float* __restrict__ s_
 
 static int f32_tiles(const PoolView& pv, int n) { return (n + kFTok - 1) / kFTok + std::min(n, pv.S); }
 
-// K parts of the shrink (the expand adds them up): two CTAs an SM where K allows parts of at least 8
-// steps.
+// K parts of the shrink (the expand adds them up): four CTAs an SM where K allows parts of at least 3
+// steps.  Measured, us a linear with two CTAs an SM and 8 steps / this way: 98 tokens, 312 x 96, r_max 24
+// 24.7 / 19.2; 3218 tokens, 10056 x 368, r_max 16 183 / 118; 16384 tokens, 4096 x 4096, r_max 16 520 / 411.
 int f32_shrink_parts(const PoolView& pv, int n) {
     const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
     const int ctas = std::max(1, (n + kFTok - 1) / kFTok * ((pv.R + rows - 1) / rows));
     const int steps = (pv.h_in + kFK - 1) / kFK;
-    int parts = std::max(1, std::min({2 * num_sms() / ctas, 8, steps / 8}));
+    int parts = std::max(1, std::min({4 * num_sms() / ctas, 24, steps / 3}));
     const int per = (steps + parts - 1) / parts;
     return (steps + per - 1) / per;
 }
@@ -326,9 +358,19 @@ int launch_f32_expand(const PoolView& pv, const SegView& sv, const float* s_in, 
         LORA_CUDA_TRY(launch_pdl((const void*)f32_expand_small_kernel, small, dim3(128), 0, st, args));
         return LORA_OK;
     }
-    const dim3 grid(f32_tiles(pv, sv.n), (pv.h_out + 63) / 64);
-    if (grid.y > 65535) return set_error(LORA_EUNSUP, "float32 expand of %d features", pv.h_out);
-    LORA_CUDA_TRY(launch_pdl((const void*)f32_expand_kernel, grid, dim3(256), 0, st, args));
+    // feature tiles are spread over as many CTAs as make about four an SM
+    const int tiles = (sv.n + kFTok - 1) / kFTok, features = (pv.h_out + 63) / 64;
+    const dim3 grid(f32_tiles(pv, sv.n), std::min(features, (4 * num_sms() + tiles - 1) / tiles));
+    const size_t smem = (size_t)(pv.R + kFK - 1) / kFK * kFK * (kFTok + kFPad) * 4;
+    static bool attr = false;
+    if (!attr) {
+        LORA_CUDA_TRY(cudaFuncSetAttribute(f32_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           kMaxRank * (kFTok + kFPad) * 4));
+        attr = true;
+    }
+    int vec_y = reinterpret_cast<uintptr_t>(y) % 16 == 0 && pv.h_out % 4 == 0;
+    void* targs[] = {(void*)&pv, (void*)&sv, (void*)&s_in, (void*)&s_parts, (void*)&yp, (void*)&vec, (void*)&vec_y};
+    LORA_CUDA_TRY(launch_pdl((const void*)f32_expand_kernel, grid, dim3(256), smem, st, targs));
     return LORA_OK;
 }
 
