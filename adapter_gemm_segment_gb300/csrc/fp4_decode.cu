@@ -548,20 +548,29 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             }
         };
         const int o8 = ((int)threadIdx.x & 15) * 8, o = m_tile * kDM + o8;
-        if (!a.vec) {  // rows off 16-byte boundaries: a feature a thread, neighbours side by side
+        if (!a.vec) {
+            // rows off 16-byte boundaries: a feature a thread, neighbours side by side, eight tokens' sums at
+            // once (204 x 105 x 2507 in float32: 20.5 us one token after the other, 12.4 so)
             const int f = (int)threadIdx.x & 127, of = m_tile * kDM + f;
-            for (int u = ((int)threadIdx.x - 64) >> 7; u < cnt; u += 2) {
-                const float* own = P + (t0 + u) * kDM + f;
-                float v = 0.f;
-                for (int c = 0; c < a.splits; ++c) {
-                    if (a.splits == 1 || (a.push && c == split))
-                        v += *own;
-                    else if (a.push)
-                        v += rcv[((size_t)(c < split ? c : c - 1) * per + u) * kDM + f];
-                    else
-                        v += ld_dsmem_f32(mapa_shared(smem_u32(own), static_cast<uint32_t>(c)));
-                }
-                if (of < a.h_out) y[(long long)(t0 + u) * a.ldy + of] = from_f32<T>(v);
+            for (int u0 = ((int)threadIdx.x - 64) >> 7; u0 < cnt; u0 += 16) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = 0.f;
+                for (int c = 0; c < a.splits; ++c)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int u = min(u0 + 2 * k, cnt - 1);
+                        const float* own = P + (t0 + u) * kDM + f;
+                        if (a.splits == 1 || (a.push && c == split))
+                            v[k] += *own;
+                        else if (a.push)
+                            v[k] += rcv[((size_t)(c < split ? c : c - 1) * per + u) * kDM + f];
+                        else
+                            v[k] += ld_dsmem_f32(mapa_shared(smem_u32(own), static_cast<uint32_t>(c)));
+                    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (u0 + 2 * k < cnt && of < a.h_out) y[(long long)(t0 + u0 + 2 * k) * a.ldy + of] = from_f32<T>(v[k]);
             }
         } else if (a.splits == 1) {
             for (int t = ((int)threadIdx.x - 64) >> 4; t < n; t += 16) {

@@ -84,7 +84,7 @@ struct PairArgs {
     const uint8_t* sw;
     long long ldy;
     int n, h_out, m_tiles, n_tiles, nkb, kt, stages;
-    int R, fuse, bf16, early_w, vec;
+    int R, fuse, bf16, early_w;
 };
 
 // A ring position: index and parity of its current use.
@@ -120,7 +120,9 @@ template <typename T> __device__ __forceinline__ uint4 round16(const uint32_t* r
     }
 }
 
-template <typename T>
+// VEC: y is written 16 bytes at a time (rows on 16-byte boundaries).  A kernel of its own for the other
+// rows, for which the common one would spill registers (16384 x 4096 x 4096 bf16: 97.5 against 93.4 us).
+template <typename T, bool VEC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const PairArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -330,106 +332,117 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const int yrow = row < a.n ? (a.perm ? __ldcg(a.perm + row) : row) : -1;
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1, flags))) break;
             tc_fence_after();
-            bool any_bad = false, gone = false;
+            bool any_bad = false;
             int slot = -1;
+            if (a.fuse) {
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(&lora_done[buf], (local >> 1) & 1, flags))) break;
+                any_bad = flags[2 + buf] == local + 1;
+                if (any_bad && yrow >= 0 && status == LORA_OK) slot = __ldcg(a.idx + yrow);
+            }
             const uint32_t taddr = tmem + buf * kPAcc1 + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                // the half of the columns that holds those both accumulators share comes first
+                // the half of the columns that holds those both accumulators share comes first, 32 columns
+                // at a time (64 spill)
                 int c0[kUnits];
-                uint32_t r[64];
-                __syncwarp();
+                uint4 w[kUnits][8];  // in y's type
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
                     const int u = 2 * (half * kUnits + i) + hv;
                     const int cc = (buf == 0 ? kPN / kCols - 1 - u : u) * kCols;
                     c0[i] = n0 + cc;
 #pragma unroll
-                    for (int k = 0; k < kCols; k += 16)
-                        tmem_ld16(taddr + cc + k, *reinterpret_cast<uint32_t(*)[16]>(&r[i * kCols + k]));
-                }
-                tmem_ld_wait();
-                if (half == 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(ov_free0);
-                    if (a.fuse) {
-                        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&lora_done[buf], (local >> 1) & 1, flags))) {
-                            gone = true;
-                            break;
+                    for (int k = 0; k < kCols; k += 32) {
+                        uint32_t r[32];
+                        __syncwarp();
+                        tmem_ld16(taddr + cc + k, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+                        tmem_ld16(taddr + cc + k + 16, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+                        tmem_ld_wait();
+                        if (half == 0 && i == kUnits - 1 && k + 32 == kCols) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster_relaxed(ov_free0);
                         }
-                        any_bad = flags[2 + buf] == local + 1;
-                        if (any_bad && yrow >= 0 && status == LORA_OK) slot = __ldcg(a.idx + yrow);
+                        if constexpr (sizeof(T) == 2) {
+                            if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
+                                for (int c = 0; c < a.R; c += 8) {
+                                    const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
+                                                                                           (size_t)row * a.R + c));
+                                    const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0[i] + k) * a.R + c;
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (c0[i] + k + e < a.h_out)
+                                            r[e] = __float_as_uint(
+                                                nonfinite_dot8<T>(__ldg(reinterpret_cast<const uint4*>(Bs + (size_t)e * a.R)),
+                                                                  sv, __uint_as_float(r[e])));
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += per) w[i][(k + e) / per] = round16<T>(&r[e]);
                     }
                 }
                 if (status != LORA_OK) continue;
 #pragma unroll
                 for (int i = 0; i < kUnits; ++i) {
                     if (c0[i] >= a.h_out) continue;
-                    if constexpr (sizeof(T) == 2) {
-                        if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
-                            for (int c = 0; c < a.R; c += 8) {
-                                const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
-                                                                                       (size_t)row * a.R + c));
-                                const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0[i]) * a.R + c;
-#pragma unroll
-                                for (int e = 0; e < kCols; ++e)
-                                    if (c0[i] + e < a.h_out)
-                                        r[i * kCols + e] = __float_as_uint(nonfinite_dot8<T>(
-                                            __ldg(reinterpret_cast<const uint4*>(Bs + (size_t)e * a.R)), sv,
-                                            __uint_as_float(r[i * kCols + e])));
-                            }
-                        }
-                    }
                     // through shared memory (16-byte pieces permuted by row), so that eight neighbouring
                     // lanes write 128 consecutive bytes of a row of y.  (Whole 32-byte sectors straight from
                     // the registers were slower: 131 against 120 us for 8191 x 11008 x 4096 in float32.)
                     const int c = lane & 7, col = c0[i] + c * per;
-                    uint4 w[8];  // the piece in y's type
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = round16<T>(&r[i * kCols + k * per]);
 #pragma unroll
                     for (int r0 = 0; r0 < 32; r0 += kStaged) {
                         __syncwarp();
                         if (lane >= r0 && lane < r0 + kStaged) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                *reinterpret_cast<uint4*>(ys + (lane - r0) * 128 + ((k ^ (lane & 7)) << 4)) = w[k];
+                                *reinterpret_cast<uint4*>(ys + (lane - r0) * 128 + ((k ^ (lane & 7)) << 4)) = w[i][k];
                         }
                         __syncwarp();
-                        if (!a.vec) {  // rows off 16-byte boundaries: an element a lane, neighbours side by side
-                            for (int rr = 0; rr < kStaged; ++rr) {
-                                const int yr = __shfl_sync(0xffffffffu, yrow, r0 + rr);
-                                if (yr < 0) continue;
+                        if constexpr (!VEC) {
+                            // rows off 16-byte boundaries: an element a lane, neighbours side by side, eight rows'
+                            // reads at once (15323 x 66 x 3695 in float16: 85 us one row after the other, 55 so)
+                            for (int k = 0; k < kStaged; k += 8) {
+                                T v[8][kCols / 32];
 #pragma unroll
-                                for (int e = lane; e < kCols; e += 32)
-                                    if (c0[i] + e < a.h_out)
-                                        y[(long long)yr * a.ldy + c0[i] + e] = *reinterpret_cast<const T*>(
-                                            ys + rr * 128 + (((e / per) ^ (rr & 7)) << 4) + e % per * sizeof(T));
+                                for (int b = 0; b < 8; ++b)
+#pragma unroll
+                                    for (int h = 0; h < kCols / 32; ++h) {
+                                        const int e = lane + 32 * h;
+                                        v[b][h] = *reinterpret_cast<const T*>(ys + (k + b) * 128 + (((e / per) ^ b) << 4) +
+                                                                              e % per * sizeof(T));
+                                    }
+#pragma unroll
+                                for (int b = 0; b < 8; ++b) {
+                                    const int yr = __shfl_sync(0xffffffffu, yrow, r0 + k + b);
+#pragma unroll
+                                    for (int h = 0; h < kCols / 32; ++h)
+                                        if (yr >= 0 && c0[i] + lane + 32 * h < a.h_out)
+                                            y[(long long)yr * a.ldy + c0[i] + lane + 32 * h] = v[b][h];
+                                }
                             }
-                            continue;
-                        }
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < kStaged; k += 4) {
-                            const int rr = k + (lane >> 3);
-                            const int yr = __shfl_sync(0xffffffffu, yrow, r0 + rr);
-                            const uint4 v = *reinterpret_cast<const uint4*>(ys + rr * 128 + ((c ^ (rr & 7)) << 4));
-                            if (yr < 0) continue;
-                            T* yp = y + (long long)yr * a.ldy + col;
-                            if (col + per <= a.h_out) {
-                                *reinterpret_cast<uint4*>(yp) = v;
-                            } else {
-                                alignas(16) T e8[per];
-                                *reinterpret_cast<uint4*>(e8) = v;
+                            for (int k = 0; k < kStaged; k += 4) {
+                                const int rr = k + (lane >> 3);
+                                const int yr = __shfl_sync(0xffffffffu, yrow, r0 + rr);
+                                const uint4 v = *reinterpret_cast<const uint4*>(ys + rr * 128 + ((c ^ (rr & 7)) << 4));
+                                if (yr < 0) continue;
+                                T* yp = y + (long long)yr * a.ldy + col;
+                                if (col + per <= a.h_out) {
+                                    *reinterpret_cast<uint4*>(yp) = v;
+                                } else {
+                                    alignas(16) T e8[per];
+                                    *reinterpret_cast<uint4*>(e8) = v;
 #pragma unroll
-                                for (int e = 0; e < per; ++e)
-                                    if (col + e < a.h_out) yp[e] = e8[e];
+                                    for (int e = 0; e < per; ++e)
+                                        if (col + e < a.h_out) yp[e] = e8[e];
+                                }
                             }
                         }
                     }
                 }
             }
-            if (gone) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0 && a.fuse) {
@@ -646,7 +659,7 @@ static int max_pairs() {
         q.attrs = qa;
         q.numAttrs = 1;
         int c = 0;
-        if (cudaOccupancyMaxActiveClusters(&c, (const void*)fp4_pair_kernel<T>, &q) != cudaSuccess || c < 1) {
+        if (cudaOccupancyMaxActiveClusters(&c, (const void*)fp4_pair_kernel<T, true>, &q) != cudaSuccess || c < 1) {
             (void)cudaGetLastError();
             c = num_sms() / 2;
         }
@@ -675,7 +688,7 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
     // six stages where neither the LoRA blocks nor float32 staging take the room of one
     a.stages = !lora && sizeof(T) == 2 ? 6 : 5;
     // rows of y are written 16 bytes at a time when every row starts on a 16-byte boundary
-    a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
+    const bool vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     if (lora) {
         a.fuse = 1;
         a.perm = lora->perm;
@@ -693,12 +706,13 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
     if (rc) return rc;
     static bool attr = false;
     if (!attr) {
-        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax));
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_pair_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax));
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fp4_pair_kernel<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax));
         attr = true;
     }
     const int pairs = (int)std::min<long long>((long long)a.m_tiles * a.n_tiles, max_pairs<T>());
     void* args[] = {(void*)&mX, (void*)&mW, (void*)&a};
-    LORA_CUDA_TRY(launch_pdl((const void*)fp4_pair_kernel<T>, dim3(2 * pairs), dim3(kPThreads),
+    LORA_CUDA_TRY(launch_pdl(vec ? (const void*)fp4_pair_kernel<T, true> : (const void*)fp4_pair_kernel<T, false>, dim3(2 * pairs), dim3(kPThreads),
                              pair_smem(a.stages, a.fuse != 0, sizeof(T)), st, args));
     return LORA_OK;
 }
