@@ -48,6 +48,11 @@ using namespace ptx;
 //
 // Warps: 0 loads codes, 1 issues MMAs (even CTA), 2-9 drain the accumulator, 10-13 build the LoRA
 // blocks, 14-17 bring in the scales.
+//
+// Measured: 8191 x 11008 x 4096 to float32 in 120 us, 6.1 PFLOP/s, 63 % of the MMAs' own rate.  A step's
+// 32 KB arrive in shared memory and are read once by the MMAs, 64 KB in 512 clocks at 128 bytes a clock:
+// that port is what the steps wait for (686 clocks each).  Where K is short it is the epilogue's pass
+// through shared memory: 16384 x 1024 x 4096 takes 46 us in bf16, 28 in a copy that leaves the pass out.
 constexpr int kPM = 128;         // token rows per CTA
 constexpr int kPN = 256;         // features per pair tile
 constexpr int kPThreads = 576;
@@ -729,7 +734,8 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
 // The parts of a tile are a thread-block cluster: they leave their shares in global memory, and after
 // the cluster barrier each adds up some of the rows and rounds them to the pool's 16-bit type.
 // With x already stored in 4 bits, the codes and scales are copied instead.  Bound by the read of
-// x, which one kernel does once where a quantiser and a shrink would do it twice.
+// x, which one kernel does once where a quantiser and a shrink would do it twice: 50 us for 16384 x 4096,
+// 41 with no adapter in the batch (the quantiser alone 28).
 constexpr int kQWorkers = 16;   // worker warps: with two CTAs an SM, 32 to hide their latencies
 constexpr int kQThreads = 64 + 32 * kQWorkers;  // warp 0: A rows, warp 1: MMAs
 constexpr uint32_t kQXBytes = 128 * 256;  // two 64-column swizzled halves

@@ -394,7 +394,10 @@ int lora_fp4_dequantize(const lora_fp4_matrix* q, void* out_dev, int dtype, int6
 
 /* y_dev [x.rows, w.rows] = x w^T of two stored matrices with the same cols (float32 accumulation,
  * one rounding to dtype, row stride ldy >= w.rows elements, aligned to its element).  A NaN scale
- * makes the outputs of its row NaN and no others. */
+ * makes the outputs of its row NaN and no others.  One kernel on `stream`: two kinds, for small and
+ * for large x.rows (the change lies between 65 and 257 rows, by shape).  Every wait on the device
+ * is bounded; the call has no status word, so a wait that runs out (it does not unless the GPU is
+ * stopped for seconds) leaves rows of y unwritten without a report. */
 int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_dev, int dtype, int64_t ldy,
                     void* stream);
 
@@ -403,7 +406,14 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
  * w: stored [h_out, h_in].  The base term takes x quantised as lora_fp4_quantize does (into the
  * workspace; or, when xq is not NULL, takes xq as the stored form of x, which projections that read
  * the same x share); the LoRA term takes x as it is, in the pool's dtype.  x_dev, y_dev, seg,
- * errors and the device status word as in lora_linear_fwd. */
+ * errors and the device status word as in lora_linear_fwd.
+ * 16-bit pools: the LoRA term joins the product's float32 accumulator, its shrink output s = (alpha / r)
+ * x A^T (float32 sums) rounded to the pool's dtype; an infinity or NaN in one adapter reaches that
+ * adapter's tokens only.  Batches that may name many adapters for their size (32 tokens and more)
+ * take a separate expand instead: s stays in float32, and y is rounded to the pool's dtype once
+ * before the LoRA term is added and once after, as in lora_linear_fwd's separate variant.  float32
+ * pools: the LoRA term in float32 throughout, added to the product's float32 y.  The same call gives
+ * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 4 kernels. */
 int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes);
 int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* x_dev, const lora_fp4_matrix* xq,
                         void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);
