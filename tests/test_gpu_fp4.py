@@ -539,3 +539,15 @@ def test_patterns_at_those_sizes(lib, n, h_in, slots, r_max, what):
     assert lib.lora_segment_status(seg) == lib.LORA_EIDX
     assert (y == 3.0).all()
     pool.close()
+
+
+@pytest.mark.parametrize("n,h_in,h_out,ranks,r_max,run", [
+    (6000, 64, 1031, [40, 7, 33], 41, 100), (9000, 40, 392, [8] * 3, 8, 1), (5000, 300, 776, [256, 16], 256, 512),
+    (40, 3000, 136, [8] * 2, 8, 1), (300, 5000, 72, [20] * 9, 20, 3)])
+def test_linear_float32_tiles(lib, n, h_in, h_out, ranks, r_max, run):
+    """Several feature tiles a CTA of the float32 expand, and many K parts of its shrink."""
+    rng = np.random.default_rng([n, h_out])
+    idx = np.repeat(rng.integers(-1, len(ranks), size=(n + run - 1) // run), run)[:n]
+    case = wl.random_case(54, n, h_in, h_out, ranks, r_max=r_max, dtype=torch.float32, idx=idx)
+    check_linear(lib, case)
+    check_linear(lib, case, zero_base=True)
