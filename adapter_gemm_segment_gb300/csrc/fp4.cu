@@ -446,9 +446,17 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
 int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes) {
     if (!pool || !bytes) return set_error(LORA_EINVAL, "pool/bytes is NULL");
     Fp4WsLayout L;
-    const int rc = fp4_ws_layout(pool, n_tokens, &L);
+    int rc = fp4_ws_layout(pool, n_tokens, &L);
     if (rc) return rc;
     *bytes = L.total;
+    // Smaller batches may need more: they split K into more parts.  The parts change at most once every 64
+    // tokens from 256 on, and there is one part from 64 tokens for each of 4 CTAs an SM on.
+    const int last = std::min(n_tokens, 64 * 4 * num_sms() + 128);
+    for (int m = 1; m < last; m += m < 256 ? 1 : 64) {
+        rc = fp4_ws_layout(pool, m, &L);
+        if (rc) return rc;
+        *bytes = std::max(*bytes, L.total);
+    }
     return LORA_OK;
 }
 

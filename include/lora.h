@@ -413,7 +413,8 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
  * take a separate expand instead: s stays in float32, and y is rounded to the pool's dtype once
  * before the LoRA term is added and once after, as in lora_linear_fwd's separate variant.  float32
  * pools: the LoRA term in float32 throughout, added to the product's float32 y.  The same call gives
- * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 4 kernels. */
+ * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 4 kernels.
+ * A workspace of lora_fp4_linear_workspace_bytes(pool, n) serves every batch of up to n tokens. */
 int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes);
 int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* x_dev, const lora_fp4_matrix* xq,
                         void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);

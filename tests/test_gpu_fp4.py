@@ -551,3 +551,24 @@ def test_linear_float32_tiles(lib, n, h_in, h_out, ranks, r_max, run):
     case = wl.random_case(54, n, h_in, h_out, ranks, r_max=r_max, dtype=torch.float32, idx=idx)
     check_linear(lib, case)
     check_linear(lib, case, zero_base=True)
+
+
+@pytest.mark.parametrize("h_in,h_out,slots,r_max,dtype", [
+    (1024, 64, 4, 256, 0), (4096, 4096, 100, 8, 0), (2048, 512, 30, 64, 1), (8192, 256, 3, 16, 2), (64, 64, 1, 8, 0)])
+def test_a_workspace_serves_every_smaller_batch(lib, h_in, h_out, slots, r_max, dtype):
+    pool = lib.LoraPool(h_in, h_out, r_max, slots, DTYPES[dtype], "cuda")
+    counts = list(range(0, 300, 7)) + [64, 128, 256, 257, 320, 511, 512, 513] + list(range(600, 50000, 509)) + [1 << 17]
+    need = [lib.lora_fp4_linear_workspace_bytes(pool.handle, n) for n in sorted(counts)]
+    assert all(a <= b for a, b in zip(need, need[1:]))
+    pool.close()
+
+
+def test_one_workspace_for_batches_of_many_sizes(lib):
+    """Batches of every path in a workspace sized for the largest."""
+    case = wl.random_case(55, 700, 1024, 136, [8, 24, 64], r_max=64, dtype=torch.float32, p_base=0.2)
+    pool = make_pool(lib, case)
+    w, ws = stored(lib, case.W), pool.fp4_linear_workspace(700)
+    for n in (700, 1, 64, 200, 300, 513):
+        x, seg = case.x[:n].cuda(), pool.segment(case.idx[:n].cuda())
+        assert torch.equal(pool.fp4_linear(w, x, seg, ws=ws), pool.fp4_linear(w, x, seg))
+    pool.close()
