@@ -177,11 +177,19 @@ fp4_dequantize_kernel(Fp4View q, T* __restrict__ out, long long ld) {
     }
 }
 
+__device__ __forceinline__ void unpack_raw(const Raw8<__half>& v, float (&f)[8]) { unpack8<__half>(v.v, f); }
+__device__ __forceinline__ void unpack_raw(const Raw8<__nv_bfloat16>& v, float (&f)[8]) { unpack8<__nv_bfloat16>(v.v, f); }
+__device__ __forceinline__ void unpack_raw(const Raw8<float>& v, float (&f)[8]) {
+    f[0] = v.a.x, f[1] = v.a.y, f[2] = v.a.z, f[3] = v.a.w;
+    f[4] = v.b.x, f[5] = v.b.y, f[6] = v.b.z, f[7] = v.b.w;
+}
+
 // ---- before the product of a small batch: x quantised and the per-token shrink, one launch -------
 // One CTA per (token, 8 adapter rows, K part), 128 threads with 8 consecutive features each in sweeps
 // of 1024, as the framework's per-token shrink; the CTAs of the first 8 rows also quantise the features
-// they hold.  Bound by latency: a chain of slot, A rows and a reduction.
-template <typename T>
+// they hold.  Bound by latency: a chain of slot, A rows and a reduction.  W: bytes of a load, as above
+// (16-bit pools have rows on 16-byte boundaries).
+template <typename T, int W>
 __global__ void __launch_bounds__(128)
 fp4_front_kernel(PoolView pool, SegView seg, const T* __restrict__ x, Fp4View q, float* __restrict__ s_out) {
     __shared__ float red[4][8];
@@ -204,14 +212,21 @@ fp4_front_kernel(PoolView pool, SegView seg, const T* __restrict__ x, Fp4View q,
     float acc[8] = {};
     for (int k0 = k_beg; k0 < k_end; k0 += 1024) {
         const int k = k0 + threadIdx.x * 8;
-        Raw8<T> v[2];
-        v[0].v = v[1].v = make_uint4(0, 0, 0, 0);
-        uint4 av[8];
+        Raw8<T> v[2], av[8];
+        memset(v, 0, sizeof(v));
         if (k < h) {
-            v[0].v = __ldcg(reinterpret_cast<const uint4*>(xr + k));
+            if constexpr (sizeof(T) == 2)
+                v[0].v = __ldcg(reinterpret_cast<const uint4*>(xr + k));
+            else
+                v[0] = load8<T, W>(xr, k, h);
             if (rows)
 #pragma unroll
-                for (int r = 0; r < 8; ++r) av[r] = __ldg(reinterpret_cast<const uint4*>(Ab + (size_t)r * h + k));
+                for (int r = 0; r < 8; ++r) {
+                    if constexpr (sizeof(T) == 2)
+                        av[r].v = __ldg(reinterpret_cast<const uint4*>(Ab + (size_t)r * h + k));
+                    else
+                        av[r] = load8<T, W>(Ab + (size_t)min(r, R - 1 - g * 8) * h, k, h);  // (r_max not a multiple of 8)
+                }
         }
         if (store) {
             uint32_t codes[2], words[2];
@@ -223,11 +238,11 @@ fp4_front_kernel(PoolView pool, SegView seg, const T* __restrict__ x, Fp4View q,
         }
         if (rows && k < h) {
             float xf[8];
-            unpack8<T>(v[0].v, xf);
+            unpack_raw(v[0], xf);
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
                 float af[8];
-                unpack8<T>(av[r], af);
+                unpack_raw(av[r], af);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[r] = fmaf(xf[i], af[i], acc[r]);
             }
@@ -242,27 +257,49 @@ fp4_front_kernel(PoolView pool, SegView seg, const T* __restrict__ x, Fp4View q,
         if (lane == 0) red[warp][r] = v;
     }
     __syncthreads();
-    if (threadIdx.x < 8) {
+    if (threadIdx.x < 8 && g * 8 + threadIdx.x < R) {
         const int r = threadIdx.x;
         s_out[((size_t)ks * seg.n + t) * R + g * 8 + r] = e.scale * (red[0][r] + red[1][r] + red[2][r] + red[3][r]);
     }
 }
 
-template <typename T>
+template <typename T, int W>
 static int launch_front_t(const PoolView& pv, const SegView& sv, const void* x, const Fp4View& q, float* s_out,
                           int s_parts, cudaStream_t st) {
     const T* xp = static_cast<const T*>(x);
     void* args[] = {(void*)&pv, (void*)&sv, (void*)&xp, (void*)&q, (void*)&s_out};
-    LORA_CUDA_TRY(launch_pdl((const void*)fp4_front_kernel<T>, dim3(sv.n, pv.R / 8, s_parts), dim3(128), 0, st, args));
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_front_kernel<T, W>, dim3(sv.n, (pv.R + 7) / 8, s_parts), dim3(128), 0, st, args));
     return LORA_OK;
+}
+
+// float32 pools: whether the per-token shrink (which reads an adapter's rows for each of its tokens) takes
+// the batch, with the quantisation in the same launch, rather than the tiled one; and its K parts.  Both
+// are weighed in us: the tiled one by its tiles' steps of 32 features (as many adapters as can be), and the
+// launch that it adds, the per-token one by its sweeps of 1024 features.  Measured, us a linear, tiled / per
+// token: 1 token 4096 x 4096 r_max 16 17.2 / 11.3; 64 tokens, 100 slots, r_max 8 29.2 / 16.1; 200 tokens,
+// 6 slots, 11008 x 4096 r_max 64 105 / 67; 1000 tokens, 10 slots, 4096 x 1000 r_max 32 48 / 55; 15226
+// tokens, 336 x 488 r_max 64 88 / 314; 4096 tokens, 100 slots, 4096 x 512 r_max 8 95 / 74.
+static bool f32_front(const PoolView& pv, int n) {
+    const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
+    const double tiles = n / 64. + std::min(n, pv.S), groups = (pv.R + rows - 1) / rows, steps = (pv.h_in + 31) / 32;
+    const double tiled = 4 + tiles * groups * steps * (rows == 16 ? 0.004 : rows == 32 ? 0.008 : 0.014);
+    return (double)n * ((pv.R + 7) / 8) * ((pv.h_in + 1023) / 1024) * 0.0024 <= tiled;
+}
+static int f32_front_parts(const PoolView& pv, int n) {
+    return std::max(1, std::min({(pv.h_in + 1023) / 1024, 4, 256 / std::max(n, 1)}));
 }
 
 int launch_fp4_front(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* q, float* s_out, int* s_parts,
                      cudaStream_t st) {
-    *s_parts = shrink_parts(pv, sv.n, false);
     const Fp4View view = q ? *q : fp4_view(nullptr, nullptr, sv.n, pv.h_in);
-    if (pv.dtype == LORA_F16) return launch_front_t<__half>(pv, sv, x, view, s_out, *s_parts, st);
-    return launch_front_t<__nv_bfloat16>(pv, sv, x, view, s_out, *s_parts, st);
+    if (pv.dtype == LORA_F32) {
+        *s_parts = f32_front_parts(pv, sv.n);
+        return row_width(x, pv.h_in, 4) == 16 ? launch_front_t<float, 16>(pv, sv, x, view, s_out, *s_parts, st)
+                                              : launch_front_t<float, 4>(pv, sv, x, view, s_out, *s_parts, st);
+    }
+    *s_parts = shrink_parts(pv, sv.n, false);
+    if (pv.dtype == LORA_F16) return launch_front_t<__half, 16>(pv, sv, x, view, s_out, *s_parts, st);
+    return launch_front_t<__nv_bfloat16, 16>(pv, sv, x, view, s_out, *s_parts, st);
 }
 
 static dim3 fp4_grid(const Fp4View& q) {
@@ -371,6 +408,8 @@ static bool fp4_separate(const PoolView& pv, int n) {
     return blocks * (0.35 + 0.0025 * n) > 4 + (double)n * pv.R * pv.h_out / 6e6;
 }
 
+static int f32_parts(const PoolView& pv, int n) { return f32_front(pv, n) ? f32_front_parts(pv, n) : f32_shrink_parts(pv, n); }
+
 // Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their rounded
 // sum), then the stored form of x.
 struct Fp4WsLayout {
@@ -387,7 +426,7 @@ static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
         s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * 2 * s16_bytes;
     }
     if (pool->desc.dtype == LORA_F32)
-        s_bytes = (size_t)f32_shrink_parts(pool_view(pool), n) * std::max(n, 1) * pool->desc.r_max * 4;
+        s_bytes = (size_t)f32_parts(pool_view(pool), n) * std::max(n, 1) * pool->desc.r_max * 4;
     L->s16_off = align256(s_bytes);
     L->codes_off = L->s16_off + align256(s16_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
@@ -449,8 +488,9 @@ int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* byte
     int rc = fp4_ws_layout(pool, n_tokens, &L);
     if (rc) return rc;
     *bytes = L.total;
-    // Smaller batches may need more: they split K into more parts.  The parts change at most once every 64
-    // tokens from 256 on, and there is one part from 64 tokens for each of 4 CTAs an SM on.
+    // Smaller batches may need more: they split K into more parts.  From 256 tokens on the need grows within
+    // each 64 (the paths before and after a change of path too: the one for more tokens needs no less), and
+    // there is one part from 64 tokens for each of 4 CTAs an SM on.
     const int last = std::min(n_tokens, 64 * 4 * num_sms() + 128);
     for (int m = 1; m < last; m += m < 256 ? 1 : 64) {
         rc = fp4_ws_layout(pool, m, &L);
@@ -527,15 +567,17 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         return launch_fp4_decode(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, early, &lora, st);
     }
     // float32 pools: the LoRA term in float32, around the product
-    if (!xq) {
-        rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
-        if (rc) return rc;
+    if (f32_front(pv, n)) {
+        rc = launch_fp4_front(pv, sv, x_dev, xq ? nullptr : &q, s_buf, &s_parts, st);
+    } else {
+        s_parts = f32_shrink_parts(pv, n);
+        if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
+        if (!rc) rc = launch_f32_shrink(pv, sv, x_dev, s_buf, st);
     }
-    rc = launch_f32_shrink(pv, sv, x_dev, s_buf, st);
     if (rc) return rc;
     rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
     if (rc) return rc;
-    return launch_f32_expand(pv, sv, s_buf, f32_shrink_parts(pv, n), y_dev, st);
+    return launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);
 }
 
 }  // extern "C"

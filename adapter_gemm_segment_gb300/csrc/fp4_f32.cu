@@ -7,9 +7,10 @@
 //   expand  y[t, o] += sum_j s[t, j] B[o, j]                64 tokens x 64 features
 // 256 threads; a thread keeps 4 tokens x 4 columns.  Operands pass through shared memory 32 deep, k-major,
 // so that a step of k is two 16-byte reads for 16 multiply-adds; the next 32 are on their way meanwhile.
-// Bound by the multiply-adds at r_max 64, by the reads of x and y below.  The 16-bit pools' tensor-core
-// kernels take 3 to 5 times less (1000 tokens, 4096 x 1000, r_max 32: 49 against 34 us a linear).  Where segments hold few
-// tokens, the expand gives a thread one feature of up to 8 tokens instead.
+// Bound by the multiply-adds at r_max 64, by the reads of x and y below.  (1000 tokens, 4096 x 1000, r_max 32:
+// 48 us a linear, against 34 with a 16-bit pool on the tensor cores.)  Where segments hold few tokens, the
+// expand gives a thread one feature of up to 8 tokens instead, and the shrink goes token by token,
+// together with the quantisation (fp4_front_kernel).
 #include <algorithm>
 
 #include "common.cuh"
