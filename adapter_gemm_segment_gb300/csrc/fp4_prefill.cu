@@ -60,7 +60,7 @@ constexpr uint32_t kPXBytes = kPM * 128, kPWBytes = (kPN / 2) * 128;
 constexpr uint32_t kPStageBytes = kPXBytes + kPWBytes;
 constexpr int kPMaxStages = 6;
 constexpr int kPScaleSlots = 5;                     // shared-memory slots of scales: 1 KB of x, 2 KB of w
-constexpr uint32_t kPScaleBytes = 3072;
+constexpr uint32_t kPScaleBytes = 3 * 1024;
 constexpr int kPScaleSets = 4;                      // tensor-memory sets of 24 columns
 constexpr int kPScaleCol = 512 - 24 * kPScaleSets;
 constexpr int kPAcc1 = kPScaleCol - kPN;            // first column of the second accumulator
