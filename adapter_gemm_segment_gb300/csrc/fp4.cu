@@ -410,25 +410,26 @@ static bool fp4_separate(const PoolView& pv, int n) {
 
 static int f32_parts(const PoolView& pv, int n) { return f32_front(pv, n) ? f32_front_parts(pv, n) : f32_shrink_parts(pv, n); }
 
-// Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their rounded
-// sum), then the stored form of x.
+// Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their sum), then
+// the stored form of x.
 struct Fp4WsLayout {
-    size_t s16_off, codes_off, scales_off, total;
+    size_t sum_off, codes_off, scales_off, total;
 };
 static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
     size_t s_bytes;
     const int rc = lora_linear_workspace_bytes(pool, n, &s_bytes);
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
-    size_t s16_bytes = 0;
+    size_t sum_bytes = 0;
     if (n > 256 && pool->desc.dtype != LORA_F32 && !fp4_separate(pool_view(pool), n)) {
-        s16_bytes = (size_t)n * pool->desc.r_max * 2;
-        s_bytes = (size_t)fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles) * 2 * s16_bytes;
+        const int parts = fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles);
+        sum_bytes = (size_t)n * pool->desc.r_max * 4;
+        s_bytes = parts > 1 ? (size_t)parts * sum_bytes : 0;
     }
     if (pool->desc.dtype == LORA_F32)
         s_bytes = (size_t)f32_parts(pool_view(pool), n) * std::max(n, 1) * pool->desc.r_max * 4;
-    L->s16_off = align256(s_bytes);
-    L->codes_off = L->s16_off + align256(s16_bytes);
+    L->sum_off = align256(s_bytes);
+    L->codes_off = L->sum_off + align256(sum_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
     L->total = L->scales_off + align256(fp4_scales_bytes(n, h_in));
     return LORA_OK;
@@ -542,10 +543,11 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         return rc ? rc : launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
     }
     if (n > 256 && pv.dtype != LORA_F32) {
+        float* sum = reinterpret_cast<float*>(ws + L.sum_off);
         const Fp4View own = fp4_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
-        rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, ws + L.s16_off, st);
+        rc = launch_fp4_prepare(pv, sv, x_dev, xq ? &q : nullptr, own, s_buf, sum, st);
         if (rc) return rc;
-        const Fp4Lora lora = {sv.perm, sv.idx, ws + L.s16_off, pv.B, pv.R};
+        const Fp4Lora lora = {sv.perm, sv.idx, sum, pv.B, pv.R};
         return launch_fp4_pair(own, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     }
     int s_parts = 1;

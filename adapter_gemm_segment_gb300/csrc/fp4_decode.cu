@@ -12,10 +12,11 @@
 // The LoRA term is more K blocks of the same accumulator, divided over the cluster's CTAs: for the
 // batch's distinct adapters d, columns d * r_max + j hold B_d[o, j] on the feature side (TMA boxes
 // of 128 rows x 8 columns, which land as the tensor cores take them) and s[t, j] on the token side
-// (zero unless token t uses d; rounded to the pool's 16-bit type here).  An adapter's B rows are
-// thus read once per feature tile, however many tokens use it.  Infinities and NaNs in B are
-// replaced by zeros in the block -- 0 * inf would reach every token -- and added afterwards to the
-// tokens of that adapter alone.
+// (zero unless token t uses d), in two 16-bit parts that multiply the same B: one would add its own
+// rounding to y's.  An adapter's B rows are thus read once per feature tile, however many tokens use
+// it.  Infinities and NaNs in B are replaced by zeros in the block -- 0 * inf would reach every
+// token -- and added afterwards to the tokens of that adapter alone, as is what of s a float16 cannot
+// hold.
 #include <cuda.h>
 
 #include <algorithm>
@@ -54,12 +55,13 @@ struct Fp4DecodeArgs {
 };
 
 // The token side of LoRA chunks p0 .. p0 + 3: for token t and chunk p, columns 8 c .. of its shrink
-// output if chunk p is c of t's own adapter (index dl[t] among the batch's), else zeros.  U (token,
-// chunk) items and K parts of the sum are loaded at once, whether they are wanted or not: a row's
-// loads then wait for memory once.
+// output if chunk p is c of t's own adapter (index dl[t] among the batch's), else zeros; the four
+// chunks' high parts, then their low ones.  U (token, chunk) items and K parts of the sum are loaded
+// at once, whether they are wanted or not: a row's loads then wait for memory once.  Chunks with
+// values that the parts leave out are marked in badmap.
 template <typename T, int U, int K>
 __device__ __forceinline__ void build_tokens(const Fp4DecodeArgs& a, uint8_t* S, uint32_t schunk, const int* dl, int p0,
-                                             int chunks, int lt) {
+                                             int chunks, int lt, uint32_t* badmap, volatile int* any_bad) {
     const size_t part = (size_t)a.n * a.R;
     for (int e0 = lt; e0 < a.n_pad * kDChunks; e0 += 256 * U) {
         float4 lo[U], hi[U];
@@ -96,10 +98,16 @@ __device__ __forceinline__ void build_tokens(const Fp4DecodeArgs& a, uint8_t* S,
         for (int u = 0; u < U; ++u) {
             const int e = e0 + 256 * u;
             if (e >= a.n_pad * kDChunks) break;
-            alignas(16) T v[8] = {from_f32<T>(lo[u].x), from_f32<T>(lo[u].y), from_f32<T>(lo[u].z), from_f32<T>(lo[u].w),
-                                  from_f32<T>(hi[u].x), from_f32<T>(hi[u].y), from_f32<T>(hi[u].z), from_f32<T>(hi[u].w)};
-            *reinterpret_cast<uint4*>(S + (e % kDChunks) * schunk + e / kDChunks * 16) =
-                mine[u] ? *reinterpret_cast<const uint4*>(v) : make_uint4(0, 0, 0, 0);
+            const float v[8] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w};
+            uint4 h16 = make_uint4(0, 0, 0, 0), l16 = h16;
+            const int p = p0 + e % kDChunks;
+            if (mine[u] && split8<T>(v, h16, l16)) {
+                atomicOr(&badmap[p >> 5], 1u << (p & 31));
+                *any_bad = 1;
+            }
+            uint8_t* at = S + (e % kDChunks) * schunk + e / kDChunks * 16;
+            *reinterpret_cast<uint4*>(at) = h16;
+            *reinterpret_cast<uint4*>(at + kDChunks * schunk) = l16;
         }
     }
 }
@@ -116,8 +124,8 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 128;
     const uint32_t stage_bytes = kDWBytes + x_bytes;
     const uint32_t schunk = static_cast<uint32_t>(n_pad) * 16;                 // token side of a chunk
-    const uint32_t lora_bytes = FUSE ? kDChunks * (2048 + schunk) : 0;
-    uint8_t* lora_sm = smem + (size_t)stages * stage_bytes;                    // [2] {features, tokens}
+    const uint32_t lora_bytes = FUSE ? kDChunks * (2048 + 2 * schunk) : 0;
+    uint8_t* lora_sm = smem + (size_t)stages * stage_bytes;                    // [2] {features, tokens' high parts, low parts}
     uint32_t* seen = reinterpret_cast<uint32_t*>(smem + a.ring_bytes);         // [64]
     int* before = reinterpret_cast<int*>(seen + 64);                           // [64]
     int* dlist = before + 64;                                                  // [256]
@@ -251,8 +259,8 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     tc_fence_after();
                     const uint32_t ba = smem_u32(lora_sm + lbuf * lora_bytes), sa = ba + kDChunks * 2048;
 #pragma unroll
-                    for (int k = 0; k < kDChunks / 2; ++k)
-                        umma_f16(tmem, sdesc_chunks(ba + 2 * k * 2048, 2048), sdesc_chunks(sa + 2 * k * schunk, schunk),
+                    for (int k = 0; k < kDChunks; ++k)  // the high parts' two steps, then the low parts'
+                        umma_f16(tmem, sdesc_chunks(ba + (k & 1) * 2 * 2048, 2048), sdesc_chunks(sa + 2 * k * schunk, schunk),
                                  idesc_lora, 1u);
                     umma_commit(&lora_empty[lbuf]);
                 }
@@ -413,13 +421,13 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     ok = __all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((b >> 1) & 1) ^ 1, flags));
                     if (ok && threadIdx.x == 192) issue_b(b, P_all);
                 }
-                // token side: 16 bytes a token and chunk; several parts of one, or one part of several, at once
+                // token side: 32 bytes a token and chunk; several parts of one, or one part of several, at once
                 if (ok) {
                     uint8_t* S = blk + kDChunks * 2048;
                     if (a.s_parts > 1)
-                        build_tokens<T, 2, 4>(a, S, schunk, dl_sm, p0, chunks, lt);
+                        build_tokens<T, 2, 4>(a, S, schunk, dl_sm, p0, chunks, lt, badmap, &flags[2]);
                     else
-                        build_tokens<T, 4, 1>(a, S, schunk, dl_sm, p0, chunks, lt);
+                        build_tokens<T, 4, 1>(a, S, schunk, dl_sm, p0, chunks, lt, badmap, &flags[2]);
                 }
                 ok = ok && __all_sync(0xffffffffu, mbar_wait(&lora_tma[lbuf], (b >> 1) & 1, flags));
                 if (!ok) break;
@@ -482,14 +490,15 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                         for (int c = 16 * q; c < 16 * q + 16; ++c) P[(c0 + c) * kDM + row] = __uint_as_float(r[c]);
             }
             if constexpr (FUSE) {
-                if (flags[2] && o < a.h_out) {  // elements of B left out of the blocks
+                if (flags[2] && o < a.h_out) {  // products left out of the blocks
                     const int chunks = a.R / 8;
                     for (int t = 0; t < n; ++t) {
                         if (dl_sm[t] < 0) continue;
                         for (int k8 = 0; k8 < chunks; ++k8) {
                             const int p = dl_sm[t] * chunks + k8;
                             if (!((badmap[p >> 5] >> (p & 31)) & 1u)) continue;
-                            const uint4 sv = sum_parts8<T>(a.s_in + (size_t)t * a.R + k8 * 8, a.s_parts, (size_t)n * a.R);
+                            float sv[8];
+                            sum_parts8(a.s_in + (size_t)t * a.R + k8 * 8, a.s_parts, (size_t)n * a.R, sv);
                             const uint4 bv = __ldg(reinterpret_cast<const uint4*>(
                                 static_cast<const T*>(a.B) + ((size_t)slot_sm[t] * a.h_out + o) * a.R + k8 * 8));
                             P[t * kDM + row] = nonfinite_dot8<T>(bv, sv, P[t * kDM + row]);
@@ -654,7 +663,7 @@ static int launch_fp4_decode_t(const Fp4View& x, const Fp4View& w, void* y, long
         a.B = pv.B;
     }
     const size_t stage_bytes = kDWBytes + (size_t)a.n_pad * 128;
-    const size_t lora_bytes = lora ? 2 * (size_t)kDChunks * (2048 + a.n_pad * 16) : 0;
+    const size_t lora_bytes = lora ? 2 * (size_t)kDChunks * (2048 + 2 * a.n_pad * 16) : 0;
     const size_t room = 227 * 1024 - kDScratch - kDBars - 1024;
     int stages = (int)((room - lora_bytes) / stage_bytes);
     stages = std::min({stages, 8, a.kb_per_split});

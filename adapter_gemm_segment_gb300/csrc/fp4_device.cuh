@@ -178,19 +178,43 @@ template <typename T> __device__ __forceinline__ uint4 finite8(const uint4& v) {
     return make_uint4(v.x & ~__vcmpeq2(v.x & mask, mask), v.y & ~__vcmpeq2(v.y & mask, mask),
                       v.z & ~__vcmpeq2(v.z & mask, mask), v.w & ~__vcmpeq2(v.w & mask, mask));
 }
-// Sum over the infinities and NaNs among b's 8 values of b times s (the part finite8 leaves out).
-template <typename T> __device__ __forceinline__ float nonfinite_dot8(const uint4& b, const uint4& s, float acc) {
-    float bf[8], sf[8];
+// The largest |s| that a 16-bit part holds: float16 takes 65520 and more for an infinity, bfloat16 has float32's range.
+template <typename T> __device__ __forceinline__ bool too_large(float s) { return false; }
+template <> __device__ __forceinline__ bool too_large<__half>(float s) {
+    const float a = fabsf(s);
+    return a >= 65520.f && a <= 3.402823466e38f;
+}
+// Eight shrink values for the tensor cores: s = hi + lo, each of the 16-bit type, which multiply the same
+// elements of B.  The two carry s to 2^-16 of itself in bfloat16, 2^-22 (and no nearer than 2^-25) in float16;
+// hi alone would lose as much as the rounding of y does.  An infinity or NaN stays in hi.  What float16 does not
+// hold is left out (both 0) and the result true: nonfinite_dot8 adds it.
+template <typename T> __device__ __forceinline__ bool split8(const float (&s)[8], uint4& hi, uint4& lo) {
+    alignas(16) T h[8], l[8];
+    bool left_out = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool big = too_large<T>(s[e]);
+        left_out |= big;
+        h[e] = from_f32<T>(big ? 0.f : s[e]);
+        const float rest = s[e] - to_f32(h[e]);
+        l[e] = from_f32<T>(fabsf(rest) <= fabsf(s[e]) && !big ? rest : 0.f);  // (inf - inf, NaN: 0)
+    }
+    hi = *reinterpret_cast<const uint4*>(h);
+    lo = *reinterpret_cast<const uint4*>(l);
+    return left_out;
+}
+// Sum over b times s of what the blocks leave out: b an infinity or NaN (finite8), or s too large (split8).
+template <typename T> __device__ __forceinline__ float nonfinite_dot8(const uint4& b, const float (&s)[8], float acc) {
+    float bf[8];
     unpack8<T>(b, bf);
-    unpack8<T>(s, sf);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if ((__float_as_uint(bf[e]) & 0x7f800000u) == 0x7f800000u) acc = fmaf(bf[e], sf[e], acc);
+        if ((__float_as_uint(bf[e]) & 0x7f800000u) == 0x7f800000u || too_large<T>(s[e])) acc = fmaf(bf[e], s[e], acc);
     return acc;
 }
 
-// Eight shrink values summed over their K parts, rounded to the 16-bit type.
-template <typename T> __device__ __forceinline__ uint4 sum_parts8(const float* s, int parts, size_t stride) {
+// Eight shrink values summed over their K parts.
+__device__ __forceinline__ void sum_parts8(const float* s, int parts, size_t stride, float (&v)[8]) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
     for (int k0 = 0; k0 < parts; k0 += 4) {  // four parts' loads in flight
         float4 c[4], d[4];
@@ -207,9 +231,7 @@ template <typename T> __device__ __forceinline__ uint4 sum_parts8(const float* s
                 b.x += d[k].x, b.y += d[k].y, b.z += d[k].z, b.w += d[k].w;
             }
     }
-    alignas(16) T v[8] = {from_f32<T>(a.x), from_f32<T>(a.y), from_f32<T>(a.z), from_f32<T>(a.w),
-                          from_f32<T>(b.x), from_f32<T>(b.y), from_f32<T>(b.z), from_f32<T>(b.w)};
-    return *reinterpret_cast<const uint4*>(v);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
 }  // namespace lora

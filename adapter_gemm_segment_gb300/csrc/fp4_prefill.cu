@@ -40,11 +40,12 @@ using namespace ptx;
 // the epilogue has taken the shared columns, which it takes first.
 //
 // The LoRA term is more K blocks of the same accumulator: for the distinct adapters d of the pair's
-// 256 tokens, columns d * r_max + j hold s[t, j] on the token side (zero unless t uses d; s is
-// rounded to the 16-bit type by the kernel before) and B_d[o, j] on the feature side, kind::f16, 32
-// columns a block, two block buffers.  Because those products reach every token of the tile, an
-// infinity or NaN in one tenant's B would reach the other tenants' rows as 0 * inf: such elements
-// are replaced by zeros here and the epilogue adds them to their own tokens alone.
+// 256 tokens, columns d * r_max + j hold s[t, j] on the token side (zero unless t uses d) and B_d[o, j]
+// on the feature side, kind::f16, 16 columns a block, two block buffers.  s is float32 and goes in as two
+// 16-bit parts (split8) that multiply the same B: in one, its rounding would add to y's.  Because those
+// products reach every token of the tile, an infinity or NaN in one tenant's B would reach the other
+// tenants' rows as 0 * inf: such elements are replaced by zeros here and the epilogue adds them to
+// their own tokens alone, as it does what of s a float16 cannot hold.
 //
 // Warps: 0 loads codes, 1 issues MMAs (even CTA), 2-9 drain the accumulator, 10-13 build the LoRA
 // blocks, 14-17 bring in the scales.
@@ -65,7 +66,7 @@ constexpr int kPScaleSets = 4;                      // tensor-memory sets of 24 
 constexpr int kPScaleCol = 512 - 24 * kPScaleSets;
 constexpr int kPAcc1 = kPScaleCol - kPN;            // first column of the second accumulator
 constexpr int kPLoraChunk = kPM * 16;               // 8 columns of 128 rows, 16 bytes a row
-constexpr int kPLoraBytes = 2 * 4 * kPLoraChunk;    // one block: 4 chunks on each side
+constexpr int kPLoraBytes = 6 * kPLoraChunk;        // one block: 2 chunks of s's high parts, low parts, B
 constexpr int kPScratch = 64 * 4 + 256 * 4 + 8;
 // after the stages: scales, LoRA blocks (if any), y staging (8 warps of 1024 elements), the
 // LoRA scratch, barriers
@@ -83,7 +84,7 @@ struct PairArgs {
     int32_t* status;         // nullable
     const int32_t* perm;     // row of y of each token row (nullptr: the same)
     const int32_t* idx;      // fuse: adapter slot by original token
-    const void* s16;         // fuse: [n][R] shrink output in token-row order, 16-bit
+    const float* s;          // fuse: [n][R] shrink output in token-row order
     const void* B;           // fuse: pool's B slab
     const uint8_t* sx;       // scale tiles of x and w
     const uint8_t* sw;
@@ -152,7 +153,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     uint64_t* lora_done = epi_done + 2;      // [2] the tile's LoRA blocks are written (8 warps of both CTAs)
     uint64_t* drained = lora_done + 2;       // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-    // abort, -, then by parity of the tile: [2] 1 + the last tile with a non-finite B, [2] LoRA blocks
+    // abort, -, then by parity of the tile: [2] 1 + the last tile whose blocks left products out, [2] LoRA blocks
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((2 * kPMaxStages + 16) * 8 + 28 <= 256, "barrier area");
 
@@ -282,9 +283,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                         tc_fence_after();
                         const uint32_t sa = smem_u32(lora_sm + lbuf * kPLoraBytes), ba = sa + 4 * kPLoraChunk;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                        for (int k = 0; k < 2; ++k)  // the high parts, the low ones
                             umma_pair_f16(acc, sdesc_chunks(sa + 2 * k * kPLoraChunk, kPLoraChunk),
-                                          sdesc_chunks(ba + 2 * k * kPLoraChunk, kPLoraChunk), idesc_lora, 1u);
+                                          sdesc_chunks(ba, kPLoraChunk), idesc_lora, 1u);
                         umma_pair_commit(&lora_empty[lbuf], 0x3);
                     }
                     if (!ok) break;
@@ -369,10 +370,10 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                             if (lane == 0) mbar_arrive_cluster_relaxed(ov_free0);
                         }
                         if constexpr (sizeof(T) == 2) {
-                            if (any_bad && slot >= 0) {  // the elements of B left out of the LoRA blocks
+                            if (any_bad && slot >= 0) {  // the products left out of the LoRA blocks
                                 for (int c = 0; c < a.R; c += 8) {
-                                    const uint4 sv = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.s16) +
-                                                                                           (size_t)row * a.R + c));
+                                    float sv[8];
+                                    sum_parts8(a.s + (size_t)row * a.R + c, 1, 0, sv);
                                     const T* Bs = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + c0[i] + k) * a.R + c;
 #pragma unroll
                                     for (int e = 0; e < 32; ++e)
@@ -580,25 +581,31 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                 }
                 named_bar_sync(2, 128);
                 const int P = *distinct * chunks;  // 8-column chunks of the tile's adapters
-                const int blocks = (P + 3) / 4;
+                const int blocks = (P + 1) / 2;
                 if (lt == 0) {
                     flags[4 + (local & 1)] = blocks;
                     mbar_arrive(&linfo[local & 1]);
                 }
                 const int o = n0 + static_cast<int>(rank) * (kPN / 2) + lt;
-                const T* srow = static_cast<const T*>(a.s16) + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
+                const float* srow = a.s + (size_t)(m0 + static_cast<int>(rank) * kPM + lt) * a.R;
                 const T* Bcol = static_cast<const T*>(a.B) + (size_t)o * a.R;
                 int d = 0, c = 0;  // the next chunk: columns 8c.. of adapter dlist[d]
                 int sl = P > 0 ? dlist[0] : -1;
-                auto load = [&](uint4 (&sv)[4], uint4 (&bv)[4]) {
+                struct Block {  // this thread's row and feature of a block
+                    float4 s[2][2];
+                    uint4 b[2];
+                } even, odd;
+                auto load = [&](Block& v) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         const bool live = d * chunks + c < P;
-                        sv[j] = live && sl == slot[0] ? __ldcg(reinterpret_cast<const uint4*>(srow + c * 8))
-                                                      : make_uint4(0, 0, 0, 0);
-                        bv[j] = live && o < a.h_out
-                                    ? __ldg(reinterpret_cast<const uint4*>(Bcol + (size_t)sl * a.h_out * a.R + c * 8))
-                                    : make_uint4(0, 0, 0, 0);
+                        const float4* sp = reinterpret_cast<const float4*>(srow + c * 8);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            v.s[j][h] = live && sl == slot[0] ? __ldcg(sp + h) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        v.b[j] = live && o < a.h_out
+                                     ? __ldg(reinterpret_cast<const uint4*>(Bcol + (size_t)sl * a.h_out * a.R + c * 8))
+                                     : make_uint4(0, 0, 0, 0);
                         if (++c == chunks) {
                             c = 0;
                             ++d;
@@ -606,29 +613,45 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                         }
                     }
                 };
-                uint4 sv[4], bv[4];
-                if (blocks > 0) load(sv, bv);
-                for (int b = 0; b < blocks; ++b, ++lb) {
-                    const int lbuf = lb & 1;
-                    if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lbuf], ((lb >> 1) & 1) ^ 1, flags))) {
+                auto put = [&](Block& v) {
+                    if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lb & 1], ((lb >> 1) & 1) ^ 1, flags))) {
                         ok = false;
-                        break;
+                        return;
                     }
-                    uint8_t* blk = lora_sm + lbuf * kPLoraBytes;
+                    uint8_t* blk = lora_sm + (lb & 1) * kPLoraBytes + lt * 16;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (nonfinite8<T>(bv[j])) {  // raise both CTAs' flags of this tile
-                            bv[j] = finite8<T>(bv[j]);
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 &lo = v.s[j][0], &hi = v.s[j][1];
+                        const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        uint4 high, low;
+                        bool left_out = split8<T>(f, high, low);
+                        if (nonfinite8<T>(v.b[j])) {
+                            v.b[j] = finite8<T>(v.b[j]);
+                            left_out = true;
+                        }
+                        if (left_out) {  // raise both CTAs' flags of this tile
                             flags[2 + (local & 1)] = local + 1;
                             st_dsmem_u32(other_flags + 4 * (2 + (local & 1)), local + 1);
                         }
-                        *reinterpret_cast<uint4*>(blk + j * kPLoraChunk + lt * 16) = sv[j];
-                        *reinterpret_cast<uint4*>(blk + (4 + j) * kPLoraChunk + lt * 16) = bv[j];
+                        *reinterpret_cast<uint4*>(blk + j * kPLoraChunk) = high;
+                        *reinterpret_cast<uint4*>(blk + (2 + j) * kPLoraChunk) = low;
+                        *reinterpret_cast<uint4*>(blk + (4 + j) * kPLoraChunk) = v.b[j];
                     }
                     fence_proxy_async_smem();  // read by the tensor cores
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&lora_own[lbuf]);
-                    if (b + 1 < blocks) load(sv, bv);  // in flight while the buffer is waited for
+                    if (lane == 0) mbar_arrive(&lora_own[lb & 1]);
+                    ++lb;
+                };
+                if (blocks > 0) load(even);
+                if (blocks > 1) load(odd);
+                for (int b = 0; b < blocks; b += 2) {  // two blocks in flight while a buffer is waited for
+                    put(even);
+                    if (!ok) break;
+                    if (b + 2 < blocks) load(even);
+                    if (b + 1 == blocks) break;
+                    put(odd);
+                    if (!ok) break;
+                    if (b + 3 < blocks) load(odd);
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -698,7 +721,7 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
         a.fuse = 1;
         a.perm = lora->perm;
         a.idx = lora->idx;
-        a.s16 = lora->s16;
+        a.s = lora->s;
         a.B = lora->B;
         a.R = lora->R;
         a.bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -732,7 +755,7 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
 // ahead spill, which waits for them at once: 58 us against 50 for 16384 x 4096, r_max 16.)  Tiles whose
 // adapters need more accumulator columns than a pass holds take several passes over their columns.
 // The parts of a tile are a thread-block cluster: they leave their shares in global memory, and after
-// the cluster barrier each adds up some of the rows and rounds them to the pool's 16-bit type.
+// the cluster barrier each adds up some of the rows.
 // With x already stored in 4 bits, the codes and scales are copied instead.  Bound by the read of
 // x, which one kernel does once where a quantiser and a shrink would do it twice: 50 us for 16384 x 4096,
 // 41 with no adapter in the batch (the quantiser alone 28).
@@ -756,8 +779,8 @@ struct PrepArgs {
     Fp4View q;                 // out: rows in segment order
     const uint8_t* xq_codes;   // x already stored, rows in token order (nullable)
     const uint8_t* xq_scales;
-    float* s;                  // scratch: [parts][n][R]
-    void* s16;                 // out: [n][R], rows in segment order
+    float* parts_s;            // scratch: [parts][n][R]
+    float* s;                  // out: [n][R], rows in segment order (the scratch itself where there is one part)
     int bf16, cap, steps, parts;  // steps: 128-column steps per part
 };
 
@@ -993,8 +1016,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
             const bool mine = dl >= d0 && dl < d0 + dn;
             const int col0 = (dl - d0) * R;
             const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-            float* out = a.s + ((size_t)blockIdx.y * a.seg.n + m0 + row) * R;
-            T* out16 = static_cast<T*>(a.s16) + (size_t)(m0 + row) * R;
+            float* out = a.parts_s + ((size_t)blockIdx.y * a.seg.n + m0 + row) * R;
             for (int c0 = 0; c0 < dn * R; c0 += 16) {
                 uint32_t r[16];
                 __syncwarp();
@@ -1007,15 +1029,8 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
                     float v[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = scale * __uint_as_float(r[e + i]);
-                    if (a.parts == 1) {
-                        alignas(16) T v16[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v16[i] = from_f32<T>(v[i]);
-                        *reinterpret_cast<uint4*>(out16 + j) = *reinterpret_cast<const uint4*>(v16);
-                    } else {
-                        reinterpret_cast<float4*>(out + j)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                        reinterpret_cast<float4*>(out + j)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                    }
+                    reinterpret_cast<float4*>(out + j)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    reinterpret_cast<float4*>(out + j)[1] = make_float4(v[4], v[5], v[6], v[7]);
                 }
             }
             tc_fence_before();
@@ -1035,15 +1050,18 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
         for (int e = q0 * chunks + tid; e < q1 * chunks; e += kQThreads) {
             const int row = e / chunks, c = e - row * chunks;
             if (slot_sm[row] < 0) continue;
-            *reinterpret_cast<uint4*>(static_cast<T*>(a.s16) + (size_t)(m0 + row) * R + c * 8) =
-                sum_parts8<T>(a.s + (size_t)(m0 + row) * R + c * 8, a.parts, (size_t)a.seg.n * R);
+            const size_t at = (size_t)(m0 + row) * R + c * 8;
+            float v[8];
+            sum_parts8(a.parts_s + at, a.parts, (size_t)a.seg.n * R, v);
+            reinterpret_cast<float4*>(a.s + at)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(a.s + at)[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     }
 }
 
 template <typename T>
 static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                            float* s, void* s16, cudaStream_t st) {
+                            float* parts_s, float* s, cudaStream_t st) {
     PrepArgs a;
     a.pool = pv;
     a.seg = sv;
@@ -1052,11 +1070,11 @@ static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x
     a.xq_codes = xq ? xq->codes : nullptr;
     a.xq_scales = xq ? xq->scales : nullptr;
     a.s = s;
-    a.s16 = s16;
     a.bf16 = std::is_same<T, __nv_bfloat16>::value;
     const int parts = fp4_prepare_parts(sv.n, q.ktiles);
     a.steps = (q.ktiles + parts - 1) / parts;
     a.parts = parts;
+    a.parts_s = parts > 1 ? parts_s : s;
     a.cap = prep_cap(sv.n, pv.S, pv.R, (sv.n + 127) / 128 * parts);
     CUtensorMap mA;
     const int rc = make_map(&mA, pv.A, a.bf16, pv.h_in, (uint64_t)pv.S * pv.R, pv.R);
@@ -1101,9 +1119,9 @@ int fp4_prepare_parts(int n, int ktiles) {
 }
 
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                       float* s, void* s16, cudaStream_t st) {
-    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, s, s16, st);
-    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, s, s16, st);
+                       float* parts_s, float* s, cudaStream_t st) {
+    if (pv.dtype == LORA_F16) return tc::launch_prepare_t<__half>(pv, sv, x, xq, q, parts_s, s, st);
+    return tc::launch_prepare_t<__nv_bfloat16>(pv, sv, x, xq, q, parts_s, s, st);
 }
 
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,

@@ -107,7 +107,7 @@ int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q
 struct Fp4Lora {
     const int32_t* perm;  // token of each row of x
     const int32_t* idx;   // slot of each token
-    const void* s16;      // [n][R], rows like x's
+    const float* s;       // [n][R], rows like x's
     const void* B;
     int R;
 };
@@ -133,11 +133,11 @@ int launch_f32_expand(const PoolView& pv, const SegView& sv, const float* s_in, 
 // More than 256 tokens.
 int launch_fp4_pair(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const Fp4Lora* lora, cudaStream_t st);
-// Quantises x (or copies xq) into q and writes the shrink output to s16 [n][R] (16-bit), rows of both in
-// segment order; s: float32 scratch [fp4_prepare_parts][n][R].
+// Quantises x (or copies xq) into q and writes the shrink output to s [n][R], rows of both in segment order;
+// parts_s: scratch [fp4_prepare_parts][n][R], not used where that is one part.
 int fp4_prepare_parts(int n, int ktiles);
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
-                       float* s, void* s16, cudaStream_t st);
+                       float* parts_s, float* s, cudaStream_t st);
 
 int num_sms();
 

@@ -408,8 +408,9 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
  * the same x share); the LoRA term takes x as it is, in the pool's dtype.  x_dev, y_dev, seg,
  * errors and the device status word as in lora_linear_fwd.
  * 16-bit pools: the LoRA term joins the product's float32 accumulator, its shrink output s = (alpha / r)
- * x A^T (float32 sums) rounded to the pool's dtype; an infinity or NaN in one adapter reaches that
- * adapter's tokens only.  Batches that may name many adapters for their size (32 tokens and more)
+ * x A^T (float32 sums) carried in two parts of the pool's dtype, to 2^-16 of itself or better (float16:
+ * no nearer than 2^-25; what float16 cannot hold is added in float32); an infinity or NaN in one adapter
+ * reaches that adapter's tokens only.  Batches that may name many adapters for their size (32 tokens and more)
  * take a separate expand instead: s stays in float32, and y is rounded to the pool's dtype once
  * before the LoRA term is added and once after, as in lora_linear_fwd's separate variant.  float32
  * pools: the LoRA term in float32 throughout, added to the product's float32 y.  The same call gives
