@@ -848,10 +848,7 @@ fp4_prepare_kernel(const __grid_constant__ CUtensorMap tmA, const PrepArgs a) {
             src[j] = r < a.seg.n ? __ldcg(a.seg.perm + r) : -1;
         }
         fetch(0, 0);
-        if (nch > 1)
-            fetch(1, 1);
-        else
-            cp_async_commit();
+        fetch(nch > 1 ? 1 : 0, 1);  // (a part of one step starts its second pass in the other stage)
     }
     if (tid < 128) {
         const int t = run && m0 + tid < a.seg.n ? __ldcg(a.seg.perm + m0 + tid) : -1;
@@ -1109,7 +1106,7 @@ static int launch_prepare_t(const PoolView& pv, const SegView& sv, const void* x
 }  // namespace tc
 
 // K parts (a cluster): as many CTAs as the GPU holds at once, two an SM; a part is at least two steps
-// of 128 columns.
+// of 128 columns, the last one what is left, at times a single step.
 int fp4_prepare_parts(int n, int ktiles) {
     const int tiles = (n + 127) / 128;
     int parts = std::max(1, 2 * num_sms() / tiles);
