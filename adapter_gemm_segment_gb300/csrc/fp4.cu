@@ -339,8 +339,9 @@ static int dequantize_t(const Fp4View& q, void* out, long long ld, cudaStream_t 
     return LORA_OK;
 }
 
+// early: as launch_fp4_decode's.
 static int launch_fp4_product(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
-                              bool early_w, cudaStream_t st) {
+                              int early, cudaStream_t st) {
     // The pair kernel also for batches whose split sums would not fit beside the receive buffer (more than
     // 224 tokens), unless K is long, and for wide outputs, where the decode kernel does not split K.
     // Measured, us a call, decode / pair: 256 tokens 4096 x 4096 14.5 / 11.8, 1024 x 1024 12.2 / 8.0,
@@ -348,8 +349,8 @@ static int launch_fp4_product(const Fp4View& x, const Fp4View& w, void* y, int d
     // 4096 x 11008 12.9 / 12.6, 4096 x 4096 8.0 / 11.6.
     const bool wide = (w.rows + 127) / 128 * 2 > num_sms();
     const bool pair = x.rows > 256 || (x.rows > 224 && x.cols <= 8192) || (x.rows > 64 && wide);
-    return pair ? launch_fp4_pair(x, w, y, dtype, ldy, status, early_w, nullptr, st)
-                : launch_fp4_decode(x, w, y, dtype, ldy, status, early_w ? 2 : 0, nullptr, st);
+    return pair ? launch_fp4_pair(x, w, y, dtype, ldy, status, /*early_w=*/early >= 1, nullptr, st)
+                : launch_fp4_decode(x, w, y, dtype, ldy, status, early, nullptr, st);
 }
 
 // grid.z counts 128-row tiles
@@ -479,7 +480,7 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
     if (x->cols != w->cols) return set_error(LORA_EINVAL, "x has %d columns, w %d", x->cols, w->cols);
     rc = check_rows(y_dev, dtype, ldy, w->rows ? x->rows : 0, w->rows, "y");
     if (rc || x->rows == 0 || w->rows == 0) return rc;
-    return launch_fp4_product(view_of(x), view_of(w), y_dev, dtype, ldy, nullptr, /*early_w=*/false,
+    return launch_fp4_product(view_of(x), view_of(w), y_dev, dtype, ldy, nullptr, /*early=*/0,
                               static_cast<cudaStream_t>(stream));
 }
 
@@ -539,7 +540,7 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         int s_parts = 1;
         if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (!rc) rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/false, &s_parts);
-        if (!rc) rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
+        if (!rc) rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, st);
         return rc ? rc : launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
     }
     if (n > 256 && pv.dtype != LORA_F32) {
@@ -569,15 +570,17 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         return launch_fp4_decode(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, early, &lora, st);
     }
     // float32 pools: the LoRA term in float32, around the product
+    int early = 2;
     if (f32_front(pv, n)) {
         rc = launch_fp4_front(pv, sv, x_dev, xq ? nullptr : &q, s_buf, &s_parts, st);
+        if (!xq) early = 1;  // the kernel just launched stores x
     } else {
         s_parts = f32_shrink_parts(pv, n);
         if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (!rc) rc = launch_f32_shrink(pv, sv, x_dev, s_buf, st);
     }
     if (rc) return rc;
-    rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, st);
+    rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, early, st);
     if (rc) return rc;
     return launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);
 }
