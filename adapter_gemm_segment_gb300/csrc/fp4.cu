@@ -112,8 +112,9 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 template <typename T, int W>
 __global__ void __launch_bounds__(kFp4Threads)
 fp4_dequantize_kernel(Fp4View q, T* __restrict__ out, long long ld) {
+    // No early release of the kernels behind: out may be the weight of a 16-bit linear, whose GEMM streams
+    // it without waiting for more than its release.
     pdl_wait();
-    pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r32 = blockIdx.y * 8 + warp;
     const int r0 = blockIdx.z * 128 + r32;

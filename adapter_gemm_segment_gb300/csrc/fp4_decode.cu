@@ -196,7 +196,8 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
+    // a product by itself releases nothing early: its y may be a weight that a 16-bit linear streams unwaited
+    if (a.early_w) pdl_trigger();
 
     if (warp == 0) {
         if (lane == 0) {

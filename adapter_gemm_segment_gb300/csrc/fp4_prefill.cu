@@ -195,7 +195,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     cluster_sync();  // both CTAs' barriers exist before either arrives on the other's
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
+    // a product by itself releases nothing early: its y may be a weight that a 16-bit linear streams unwaited
+    if (a.early_w) pdl_trigger();
 
     if (warp == 0) {
         if (lane == 0) {

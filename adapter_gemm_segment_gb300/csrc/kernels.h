@@ -102,7 +102,8 @@ inline size_t fp4_scales_bytes(int rows, int cols) {
 }
 int launch_fp4_quantize(const void* x, int dtype, long long ld, const Fp4View& q, cudaStream_t st);
 // y = x w^T (dtype, row stride ldy).  status: nullable device word; y stays untouched unless it is
-// LORA_OK.  early_w: every kernel that could have written w has completed when this grid starts.
+// LORA_OK.  early_w: every kernel that could have written w has completed when this grid starts (the
+// products inside a linear; only these release the kernel behind them early).
 // lora (nullable, 16-bit y): the LoRA term, for launch_fp4_pair with x's rows in the order of perm.
 struct Fp4Lora {
     const int32_t* perm;  // token of each row of x

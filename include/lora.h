@@ -415,7 +415,10 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
  * before the LoRA term is added and once after, as in lora_linear_fwd's separate variant.  float32
  * pools: the LoRA term in float32 throughout, added to the product's float32 y.  The same call gives
  * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 4 kernels.
- * A workspace of lora_fp4_linear_workspace_bytes(pool, n) serves every batch of up to n tokens. */
+ * A workspace of lora_fp4_linear_workspace_bytes(pool, n) serves every batch of up to n tokens.
+ * The 16-bit linears stream their weights ahead of the linear before them, so the y of a linear, this one
+ * included, is not to be their W without a wait in between; what lora_fp4_dequantize or lora_fp4_matmul
+ * wrote may be. */
 int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes);
 int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* x_dev, const lora_fp4_matrix* xq,
                         void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);
