@@ -13,6 +13,7 @@ host-tier cache entry points), plus small ``LoraPool`` and ``LoraCache`` conveni
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -667,8 +668,24 @@ def _device_bytes(nbytes: int, device) -> torch.Tensor:
     return t
 
 
+def _on_stream(stream):
+    """A context in which torch allocates for work on `stream` (as the calls here take it)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream).value
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _capturing() -> bool:
+    return torch.cuda.is_current_stream_capturing()
+
+
 class LoraPool:
-    """One adapter pool (one linear layer) in a device buffer this object owns."""
+    """One adapter pool (one linear layer) in a device buffer this object owns.  Where a call is given no
+    workspace the pool keeps one for each stream, so that calls on several streams do not share one; a call
+    under stream capture gets one of its graph's own."""
 
     def __init__(self, h_in: int, h_out: int, r_max: int, n_slots: int, dtype: torch.dtype, device="cuda",
                  stream=None):
@@ -704,13 +721,26 @@ class LoraPool:
                y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         n = int(seg.n_tokens)
         if y is None:
-            y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
+            with _on_stream(stream):
+                y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
         if ws is None:
-            key = (n, x.device)
-            if key not in self._ws:
-                self._ws[key] = self.linear_workspace(n, x.device)
-            ws = self._ws[key]
+            ws = self._own_workspace("linear", n, x.device, stream)
         return lora_linear_fwd(self.handle, W, x, y, seg, ws, variant, stream)
+
+    def _own_workspace(self, kind: str, n: int, device, stream) -> torch.Tensor:
+        """The workspace of this pool's calls of n tokens on one stream.  The 4-bit linear keeps the largest
+        asked for, which serves every smaller batch; the 16-bit linear's may need more for fewer tokens, so
+        it keeps one for each n."""
+        make = lora_fp4_linear_workspace_bytes if kind == "fp4" else lora_linear_workspace_bytes
+        with _on_stream(stream):
+            if _capturing():
+                return torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
+            key = (kind, device, _stream(stream).value) + (() if kind == "fp4" else (n,))
+            held, ws = self._ws.get(key, (-1, None))
+            if held < n:
+                ws = torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
+                self._ws[key] = (n, ws)
+        return ws
 
     def fp4_linear_workspace(self, n_tokens: int, device="cuda") -> torch.Tensor:
         return _device_bytes(lora_fp4_linear_workspace_bytes(self.handle, n_tokens), device)
@@ -720,12 +750,10 @@ class LoraPool:
         """``linear`` over a 4-bit base weight."""
         n = int(seg.n_tokens)
         if y is None:
-            y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
+            with _on_stream(stream):
+                y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
         if ws is None:
-            key = ("fp4", n, x.device)
-            if key not in self._ws:
-                self._ws[key] = self.fp4_linear_workspace(n, x.device)
-            ws = self._ws[key]
+            ws = self._own_workspace("fp4", n, x.device, stream)
         return lora_fp4_linear_fwd(self.handle, w, x, y, seg, ws, xq, stream)
 
     def close(self) -> None:
