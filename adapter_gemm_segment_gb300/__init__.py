@@ -244,6 +244,7 @@ def lora_pool_create(h_in: int, h_out: int, r_max: int, n_slots: int, dtype: tor
     h = ctypes.c_void_p()
     _check(_lib.lora_pool_create(ctypes.byref(d), _ptr(_dev(dev_mem, "dev_mem")),
                                  dev_mem.numel() * dev_mem.element_size(), _stream(stream), ctypes.byref(h)))
+    h.dtype = dtype  # for the checks of calls that take tensors
     return h
 
 
@@ -635,8 +636,13 @@ def lora_fp4_linear_workspace_bytes(pool_handle, n_tokens: int) -> int:
 
 def lora_fp4_linear_fwd(pool_handle, w: Fp4Matrix, x: torch.Tensor, y: torch.Tensor, seg: lora_segments,
                         ws: torch.Tensor, xq: Optional[Fp4Matrix] = None, stream=None) -> torch.Tensor:
-    """lora_linear_fwd over a 4-bit base weight; xq: the stored form of x, where another projection
-    of the same x has made it already (it is made in the workspace otherwise)."""
+    """lora_linear_fwd over a 4-bit base weight; x [..., w.cols] and y [..., w.rows] of n_tokens rows in the
+    pool's dtype; xq: the stored form of x, where another projection of the same x has made it already
+    (it is made in the workspace otherwise)."""
+    n, dt = int(seg.n_tokens), getattr(pool_handle, "dtype", x.dtype)
+    for t, name, cols in ((x, "x", w.cols), (y, "y", w.rows)):
+        if t.dtype != dt or t.dim() == 0 or t.shape[-1] != cols or t.numel() != n * cols:
+            raise LoraError(LORA_EINVAL, f"{name} must be {dt} [{n}, {cols}], got {t.dtype} {list(t.shape)}")
     _check(_lib.lora_fp4_linear_fwd(pool_handle, ctypes.byref(w.struct), _dev(x, "x").data_ptr(),
                                     None if xq is None else ctypes.byref(xq.struct), _dev(y, "y").data_ptr(),
                                     ctypes.byref(seg), _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size(),
