@@ -575,6 +575,8 @@ class Fp4Matrix:
     writes; before that they are undefined."""
 
     def __init__(self, rows: int, cols: int, device="cuda"):
+        if torch.device(device).type != "cuda":
+            raise ValueError("a 4-bit matrix lives in CUDA memory")  # the kernels take its bare addresses
         nc, ns = lora_fp4_bytes(rows, cols)
         self.rows, self.cols = int(rows), int(cols)
         self.codes = torch.empty(max(nc, 256), dtype=torch.uint8, device=device)

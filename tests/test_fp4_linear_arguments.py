@@ -62,6 +62,12 @@ def test_other_shapes_and_types_are_refused(call, x, y):
     assert e.value.code == ags.LORA_EINVAL and not call.reached
 
 
+@pytest.mark.parametrize("device", ["cpu", "meta", torch.device("cpu")])
+def test_a_matrix_off_the_gpu_is_refused(device):
+    with pytest.raises(ValueError):
+        ags.Fp4Matrix(64, 256, device)
+
+
 @pytest.mark.gpu
 def test_refusals_through_a_pool(lib):
     pool = lib.LoraPool(256, 64, 8, 1, torch.float16, "cuda")
