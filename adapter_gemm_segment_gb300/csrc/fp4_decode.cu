@@ -518,7 +518,7 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     // 8 features a thread, 16 neighbouring threads a token's 128.  The sums reach their owner by one
     // bulk copy from each other CTA (a token's row is 512 bytes, an owner's rows are contiguous) where a
     // receive buffer fits, else they are read remotely, which is slower (64 tokens, 4 CTAs: 1.9 us).
-    const bool good = flags[0] == 0;
+    bool good = flags[0] == 0;
     const int per = (n + a.splits - 1) / a.splits;
     const int t0 = min(n, split * per), cnt = min(n, t0 + per) - t0;
     float* rcv = P + (size_t)n_pad * kDM;  // [splits - 1][per][128]
@@ -538,8 +538,11 @@ fp4_decode_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                                    mapa_shared(smem_u32(rbar), static_cast<uint32_t>(dst)));
             }
             __syncwarp();
+            good = cluster_unaborted(flags, a.splits);  // sums of a CTA that gave up are no one's; read while the copies fly
             if (cnt > 0) recv = __all_sync(0xffffffffu, mbar_wait(rbar, 0, flags));
             cluster_arrive();  // (the last wait below: every copy out of this CTA has then landed)
+        } else {
+            good = cluster_unaborted(flags, a.splits);
         }
     }
     if (warp >= 2 && good && store && recv) {

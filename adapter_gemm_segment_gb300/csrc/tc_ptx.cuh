@@ -416,6 +416,19 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
     return v;
 }
 
+// Whether none of the cluster's CTAs has raised the abort flag at this address (whole warps; behind a
+// cluster barrier that follows the last wait which may raise it, and ahead of one before any CTA leaves).
+__device__ __forceinline__ bool cluster_unaborted(const volatile int* flag, int ctas) {
+    const int lane = threadIdx.x & 31;
+    uint32_t raised = 0;
+    if (lane < ctas)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(raised)
+                     : "r"(mapa_shared(smem_u32(const_cast<const int*>(flag)), static_cast<uint32_t>(lane)))
+                     : "memory");
+    return __all_sync(0xffffffffu, raised == 0);
+}
+
 __device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
