@@ -273,6 +273,100 @@ static int launch_front_t(const PoolView& pv, const SegView& sv, const void* x, 
     return LORA_OK;
 }
 
+// ---- after the product where the LoRA term is separate: y = product + s B^T, rounded once ---------
+// One CTA per work item (up to 4 sorted tokens of one adapter) and 256 * fpt features, as the framework's
+// segmented expand, but the product comes in float32 and y is written here alone; the CTAs behind the
+// items' take the tokens without an adapter, four at a time.  Bound by latency: item, then s, B and the
+// product's rows, which are in L2.
+constexpr int kFp4ItemTok = 4;  // tokens of a work item
+template <typename T>
+__global__ void __launch_bounds__(256)
+fp4_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, int s_parts,
+                  const float* __restrict__ y32, T* __restrict__ y, int fpt, int items, int rank_aware) {
+    extern __shared__ float ss[];  // [4][R]: the item's shrink rows (K parts summed)
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.x, R = pool.R, h_out = pool.h_out;
+    if (__ldcg(seg.status) != LORA_OK) return;
+    int slot = -1, nt, tok[kFp4ItemTok];
+    if (b < items) {
+        if (b >= __ldcg(seg.nseg + 1)) return;
+        const int4 head = __ldcg(reinterpret_cast<const int4*>(seg.items + (size_t)b * 8));      // slot, count, tokens 0, 1
+        const int2 tail = __ldcg(reinterpret_cast<const int2*>(seg.items + (size_t)b * 8 + 4));  // tokens 2, 3
+        slot = head.x, nt = head.y;
+        tok[0] = head.z, tok[1] = head.w, tok[2] = tail.x, tok[3] = tail.y;
+    } else {  // the segment of no adapter is the first
+        const int j0 = (b - items) * kFp4ItemTok;
+        const int end = __ldcg(seg.nseg) > 0 && __ldcg(seg.seg_slot) < 0 ? __ldcg(seg.seg_start + 1) : 0;
+        nt = min(kFp4ItemTok, end - j0);
+        if (nt <= 0) return;
+#pragma unroll
+        for (int u = 0; u < kFp4ItemTok; ++u) tok[u] = __ldcg(seg.perm + j0 + min(u, nt - 1));
+    }
+    const int o = blockIdx.y * 256 * fpt + threadIdx.x;
+    const bool live[2] = {o < h_out, fpt == 2 && o + 256 < h_out};
+    float acc[2][kFp4ItemTok];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int u = 0; u < kFp4ItemTok; ++u)
+            acc[f][u] = live[f] && u < nt ? __ldcg(y32 + (size_t)tok[u] * h_out + o + 256 * f) : 0.f;
+    if (slot >= 0) {
+        for (int e = threadIdx.x; e < kFp4ItemTok * R; e += blockDim.x) {
+            const int u = e / R, j = e - u * R, t = u == 0 ? tok[0] : u == 1 ? tok[1] : u == 2 ? tok[2] : tok[3];
+            float v = 0.f;
+            if (u < nt)
+                for (int k = 0; k < s_parts; ++k) v += __ldcg(s_in + ((size_t)k * seg.n + t) * R + j);
+            ss[e] = v;
+        }
+        __syncthreads();
+        if (live[0]) {
+            const T* Br = static_cast<const T*>(pool.B) + ((size_t)slot * h_out + o) * R;
+            // columns past the adapter's true rank are zeros
+            const int jmax = rank_aware ? min(R, (max(pool.table[slot].rank, 1) + 7) & ~7) : R;
+            float term[2][kFp4ItemTok] = {};  // summed by itself: y32 may be far larger
+            for (int j = 0; j < jmax; j += 8) {
+                float b0[8], b1[8];
+                unpack8<T>(__ldg(reinterpret_cast<const uint4*>(Br + j)), b0);
+                unpack8<T>(live[1] ? __ldg(reinterpret_cast<const uint4*>(Br + (size_t)256 * R + j)) : make_uint4(0, 0, 0, 0), b1);
+#pragma unroll
+                for (int u = 0; u < kFp4ItemTok; ++u)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float sv = ss[u * R + j + e];
+                        term[0][u] = fmaf(b0[e], sv, term[0][u]);
+                        term[1][u] = fmaf(b1[e], sv, term[1][u]);
+                    }
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int u = 0; u < kFp4ItemTok; ++u) acc[f][u] += term[f][u];
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int u = 0; u < kFp4ItemTok; ++u)
+            if (live[f] && u < nt) y[(size_t)tok[u] * h_out + o + 256 * f] = from_f32<T>(acc[f][u]);
+}
+
+template <typename T>
+static int launch_fp4_expand_t(const PoolView& pv, const SegView& sv, const float* s_in, int s_parts, const float* y32,
+                               void* y, cudaStream_t st) {
+    // at most one item per LoRA token, and per segment one partial item beyond n / 4
+    const int quads = (sv.n + kFp4ItemTok - 1) / kFp4ItemTok;
+    int items = std::min(sv.n, std::min(sv.n, pv.S) + quads);
+    // two features a thread where the grid keeps two CTAs an SM that way
+    int fpt = (long long)items * ((pv.h_out + 511) / 512) >= 2LL * num_sms() ? 2 : 1;
+    int rank_aware = has_padded_slots(pv);
+    T* yp = static_cast<T*>(y);
+    void* args[] = {(void*)&pv, (void*)&sv, (void*)&s_in, (void*)&s_parts, (void*)&y32, (void*)&yp, (void*)&fpt, (void*)&items, (void*)&rank_aware};
+    const dim3 grid(items + quads, (pv.h_out + 256 * fpt - 1) / (256 * fpt));
+    LORA_CUDA_TRY(launch_pdl((const void*)fp4_expand_kernel<T>, grid, dim3(256), sizeof(float) * kFp4ItemTok * pv.R, st, args));
+    return LORA_OK;
+}
+
 // float32 pools: whether the per-token shrink (which reads an adapter's rows for each of its tokens) takes
 // the batch, with the quantisation in the same launch, rather than the tiled one; and its K parts.  Both
 // are weighed in us: the tiled one by its tiles' steps of 32 features (as many adapters as can be), and the
@@ -401,8 +495,12 @@ static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev,
 // r_max 8 13.9 / 15.3 and 20.5 / 19.8, r_max 32 22.7 / 19.6 and 49 / 25; 128 tokens, 30 slots r_max 16
 // 19.4 / 19.1 and 28.7 / 26.8; 250 tokens, 6 slots r_max 64 29.9 / 41.9 and 37 / 57, 100 slots r_max 64
 // 75 / 50 and 209 / 93.  (16 tokens: fused throughout.)
+//
+// The product then goes to the workspace in float32 (4 n h_out bytes), so that y is rounded once: at most
+// kFp4SumElements of it.
+constexpr long long kFp4SumElements = 32 << 20;
 static bool fp4_separate(const PoolView& pv, int n) {
-    if (pv.dtype == LORA_F32) return false;
+    if (pv.dtype == LORA_F32 || (long long)n * pv.h_out > kFp4SumElements) return false;
     const int adapters = std::min(n, pv.S);
     if (n > 256) return pv.R <= 32 && n < 16LL * adapters;
     if (n < 32) return false;
@@ -410,28 +508,38 @@ static bool fp4_separate(const PoolView& pv, int n) {
     return blocks * (0.35 + 0.0025 * n) > 4 + (double)n * pv.R * pv.h_out / 6e6;
 }
 
+// The largest batch of more than 256 and at most n tokens for which that holds (0: none).
+static int fp4_separate_most(const PoolView& pv, int n) {
+    const int m = (int)std::min<long long>({(long long)n, 16LL * pv.S - 1, kFp4SumElements / pv.h_out});
+    return m > 256 && fp4_separate(pv, m) ? m : 0;
+}
+
 static int f32_parts(const PoolView& pv, int n) { return f32_front(pv, n) ? f32_front_parts(pv, n) : f32_shrink_parts(pv, n); }
 
-// Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their sum), then
-// the stored form of x.
+// Workspace of lora_fp4_linear_fwd: the shrink output (in K parts, and for large batches their sum), the
+// product where the expand is separate, then the stored form of x.
 struct Fp4WsLayout {
-    size_t sum_off, codes_off, scales_off, total;
+    size_t sum_off, y32_off, codes_off, scales_off, total;
 };
 static int fp4_ws_layout(lora_pool_t pool, int n, Fp4WsLayout* L) {
     size_t s_bytes;
     const int rc = lora_linear_workspace_bytes(pool, n, &s_bytes);
     if (rc) return rc;
     const int h_in = pool->desc.h_in;
-    size_t sum_bytes = 0;
-    if (n > 256 && pool->desc.dtype != LORA_F32 && !fp4_separate(pool_view(pool), n)) {
+    size_t sum_bytes = 0, y32_bytes = 0;
+    const PoolView pv = pool_view(pool);
+    if (fp4_separate(pv, n)) {
+        y32_bytes = (size_t)n * pv.h_out * 4;
+    } else if (n > 256 && pv.dtype != LORA_F32) {
         const int parts = fp4_prepare_parts(n, fp4_view(nullptr, nullptr, n, h_in).ktiles);
         sum_bytes = (size_t)n * pool->desc.r_max * 4;
         s_bytes = parts > 1 ? (size_t)parts * sum_bytes : 0;
     }
     if (pool->desc.dtype == LORA_F32)
-        s_bytes = (size_t)f32_parts(pool_view(pool), n) * std::max(n, 1) * pool->desc.r_max * 4;
+        s_bytes = (size_t)f32_parts(pv, n) * std::max(n, 1) * pool->desc.r_max * 4;
     L->sum_off = align256(s_bytes);
-    L->codes_off = L->sum_off + align256(sum_bytes);
+    L->y32_off = L->sum_off + align256(sum_bytes);
+    L->codes_off = L->y32_off + align256(y32_bytes);
     L->scales_off = L->codes_off + align256(fp4_codes_bytes(n, h_in));
     L->total = L->scales_off + align256(fp4_scales_bytes(n, h_in));
     return LORA_OK;
@@ -493,10 +601,17 @@ int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* byte
     *bytes = L.total;
     // Smaller batches may need more: they split K into more parts.  From 256 tokens on the need grows within
     // each 64 (the paths before and after a change of path too: the one for more tokens needs no less), and
-    // there is one part from 64 tokens for each of 4 CTAs an SM on.
+    // there is one part from 64 tokens for each of 4 CTAs an SM on.  The separate expand's largest batch is
+    // looked up by itself.
     const int last = std::min(n_tokens, 64 * 4 * num_sms() + 128);
     for (int m = 1; m < last; m += m < 256 ? 1 : 64) {
         rc = fp4_ws_layout(pool, m, &L);
+        if (rc) return rc;
+        *bytes = std::max(*bytes, L.total);
+    }
+    const int separate = fp4_separate_most(pool_view(pool), n_tokens);
+    if (separate) {
+        rc = fp4_ws_layout(pool, separate, &L);
         if (rc) return rc;
         *bytes = std::max(*bytes, L.total);
     }
@@ -541,8 +656,11 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         int s_parts = 1;
         if (!xq) rc = launch_fp4_quantize(x_dev, pv.dtype, pv.h_in, q, st);
         if (!rc) rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/false, &s_parts);
-        if (!rc) rc = launch_fp4_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, st);
-        return rc ? rc : launch_expand(pv, sv, s_buf, s_parts, y_dev, st);
+        float* y32 = reinterpret_cast<float*>(ws + L.y32_off);
+        if (!rc) rc = launch_fp4_product(q, view_of(w), y32, LORA_F32, pv.h_out, sv.status, /*early=*/2, st);
+        if (rc) return rc;
+        return pv.dtype == LORA_F16 ? launch_fp4_expand_t<__half>(pv, sv, s_buf, s_parts, y32, y_dev, st)
+                                    : launch_fp4_expand_t<__nv_bfloat16>(pv, sv, s_buf, s_parts, y32, y_dev, st);
     }
     if (n > 256 && pv.dtype != LORA_F32) {
         float* sum = reinterpret_cast<float*>(ws + L.sum_off);

@@ -411,9 +411,8 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
  * x A^T (float32 sums) carried in two parts of the pool's dtype, to 2^-16 of itself or better (float16:
  * no nearer than 2^-25; what float16 cannot hold is added in float32); an infinity or NaN in one adapter
  * reaches that adapter's tokens only.  Batches that may name many adapters for their size (32 tokens and more)
- * take a separate expand instead: s stays in float32, and y is rounded to the pool's dtype once
- * before the LoRA term is added and once after, as in lora_linear_fwd's separate variant.  float32
- * pools: the LoRA term in float32 throughout, added to the product's float32 y.  The same call gives
+ * take a separate expand instead, which adds the LoRA term to the product in float32.  float32 pools: the
+ * LoRA term in float32 throughout, added to the product's float32 y.  In each y is rounded once. The same call gives
  * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 4 kernels.
  * A workspace of lora_fp4_linear_workspace_bytes(pool, n) serves every batch of up to n tokens.
  * The 16-bit linears stream their weights ahead of the linear before them, so the y of a linear, this one
