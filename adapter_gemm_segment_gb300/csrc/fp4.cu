@@ -9,8 +9,8 @@
 // e2m1 is the only one.
 //
 // Both kernels move every byte once and are bound by memory: 16384 x 4096 bf16, 134 MB of x and 36 MB
-// stored, quantised and read back one after the other in 51.6 us together, 6.6 TB/s, against 50.1 at the
-// measured copy rate; below about 4 MB by the launch (one row of 4096: 3.7 us each).  A warp takes 256
+// stored, quantised and read back one after the other in 51.9 us together, 6.5 TB/s, against 50.1 at the
+// measured copy rate; below about 4 MB by the launch (one row of 4096: 4 us each).  A warp takes 256
 // columns of the four rows r, r + 32, r + 64, r + 96 of a 128-row tile: a lane holds 8 consecutive
 // elements of each row (16-byte loads of 16-bit data, a warp's lanes side by side), four lanes share a
 // block (two shuffles give its maximum), and the 4 x 4 scale bytes of those rows' four blocks are 16
@@ -371,9 +371,9 @@ static int launch_fp4_expand_t(const PoolView& pv, const SegView& sv, const floa
 // the batch, with the quantisation in the same launch, rather than the tiled one; and its K parts.  Both
 // are weighed in us: the tiled one by its tiles' steps of 32 features (as many adapters as can be), and the
 // launch that it adds, the per-token one by its sweeps of 1024 features.  Measured, us a linear, tiled / per
-// token: 1 token 4096 x 4096 r_max 16 17.2 / 11.3; 64 tokens, 100 slots, r_max 8 29.2 / 16.1; 200 tokens,
-// 6 slots, 11008 x 4096 r_max 64 105 / 67; 1000 tokens, 10 slots, 4096 x 1000 r_max 32 48 / 55; 15226
-// tokens, 336 x 488 r_max 64 88 / 314; 4096 tokens, 100 slots, 4096 x 512 r_max 8 95 / 74.
+// token: 1 token 4096 x 4096 r_max 16 16.5 / 11.6; 64 tokens, 100 slots, r_max 8 31.5 / 16.6; 200 tokens,
+// 6 slots, 11008 x 4096 r_max 64 110 / 84; 1000 tokens, 10 slots, 4096 x 1000 r_max 32 50.6 / 60.3; 15226
+// tokens, 10 slots, 336 x 488 r_max 64 94 / 341; 4096 tokens, 100 slots, 4096 x 512 r_max 8 101 / 84.
 static bool f32_front(const PoolView& pv, int n) {
     const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
     const double tiles = n / 64. + std::min(n, pv.S), groups = (pv.R + rows - 1) / rows, steps = (pv.h_in + 31) / 32;
@@ -439,9 +439,10 @@ static int launch_fp4_product(const Fp4View& x, const Fp4View& w, void* y, int d
                               int early, cudaStream_t st) {
     // The pair kernel also for batches whose split sums would not fit beside the receive buffer (more than
     // 224 tokens), unless K is long, and for wide outputs, where the decode kernel does not split K.
-    // Measured, us a call, decode / pair: 256 tokens 4096 x 4096 14.5 / 11.8, 1024 x 1024 12.2 / 8.0,
-    // 11008 x 4096 20.0 / 21.3; 160 tokens 4096 x 11008 14.5 / 12.8, 4096 x 4096 9.9 / 11.6; 96 tokens
-    // 4096 x 11008 12.9 / 12.6, 4096 x 4096 8.0 / 11.6.
+    // Measured, us a call, decode / pair: 256 tokens 4096 x 4096 14.6 / 11.6, 1024 x 1024 11.3 / 7.5,
+    // 11008 x 4096 17.9 / 20.4, 4096 x 11008 14.4 / 12.1; 160 tokens 4096 x 4096 10.0 / 11.5; 96 tokens
+    // 4096 x 4096 8.0 / 11.5, 11008 x 11008 27.8 / 21.2, 4096 x 32000 27.6 / 20.2.  Wide outputs of few tiles lose
+    // by it up to 128 tokens (96 tokens 4096 x 11008 10.4 / 11.9, 1024 x 11008 5.1 / 8.0).
     const bool wide = (w.rows + 127) / 128 * 2 > num_sms();
     const bool pair = x.rows > 256 || (x.rows > 224 && x.cols <= 8192) || (x.rows > 64 && wide);
     return pair ? launch_fp4_pair(x, w, y, dtype, ldy, status, /*early_w=*/early >= 1, nullptr, st)
@@ -482,19 +483,20 @@ static int check_rows(const void* p, int dtype, int64_t ld, int rows, int cols, 
 static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev, m->scales_dev, m->rows, m->cols); }
 
 // Batches of more than 256 tokens whose tokens are spread over many adapters (fewer than 16 a slot) at
-// ranks of up to 32: the product without the LoRA term, and the segmented expand after it, as the
-// framework's separate variant.  The fused product then builds a LoRA block for almost every adapter in
-// every tile.  Measured, us a linear separate / fused, 4096 x 4096, 100 slots, r_max 16, every token its
-// own adapter: 300 tokens 31 / 50, 600 34 / 65, 1200 47 / 75, 2400 76 / 73; a run of 512 tokens an
-// adapter: 600 tokens 32 / 26, 1200 45 / 33.  At r_max 64 the expand's re-reads of B cost what the blocks
-// do (600 tokens 86 / 198 spread, 65 / 28 in runs), and the fused product stays.
+// ranks of up to 32: the product without the LoRA term, and a segmented expand after it.  The fused
+// product then builds LoRA blocks for almost every adapter in every tile.  Measured, us a linear
+// separate / fused, 4096 x 4096, 100 slots, r_max 16, every token its own adapter: 300 tokens 33.8 / 64.7,
+// 600 41 / 82, 1200 62 / 89, 2400 96 / 85; a run of 512 tokens an adapter: 600 tokens 36 / 26, 1200 55 / 34.
+// At r_max 64 the expand loses as much where tokens come in runs (600 tokens 70 / 32) as it gains where
+// they are spread (88 / 238), which the host cannot tell apart, and the fused product stays.  Slots count
+// as adapters whether mounted or not, and more than 100 were not measured.
 //
 // From 32 to 256 tokens the same choice weighs, in us, the blocks that each of the decode kernel's CTAs
 // would build if as many adapters as can be are there, against the expand and its launch.  Measured,
 // fused / separate, Zipf-distributed adapters, 4096 -> 4096 and 4096 -> 11008 features: 64 tokens, 100 slots
-// r_max 8 13.9 / 15.3 and 20.5 / 19.8, r_max 32 22.7 / 19.6 and 49 / 25; 128 tokens, 30 slots r_max 16
-// 19.4 / 19.1 and 28.7 / 26.8; 250 tokens, 6 slots r_max 64 29.9 / 41.9 and 37 / 57, 100 slots r_max 64
-// 75 / 50 and 209 / 93.  (16 tokens: fused throughout.)
+// r_max 8 13.9 / 15.8 and 25.8 / 27.3, r_max 32 25.0 / 19.9 and 61 / 34; 128 tokens, 30 slots r_max 16
+// 20.4 / 20.6 and 37.9 / 31.8; 250 tokens, 6 slots r_max 64 30.5 / 41.3 and 47 / 68, 100 slots r_max 64
+// 88 / 56 and 251 / 98.  (16 tokens: fused throughout.)
 //
 // The product then goes to the workspace in float32 (4 n h_out bytes), so that y is rounded once: at most
 // kFp4SumElements of it.

@@ -1,5 +1,5 @@
-// float32 pools over a 4-bit base: the LoRA term in float32 on CUDA cores (the tensor cores have no
-// float32 product of that accuracy), around the 4-bit product.
+// float32 pools over a 4-bit base: the LoRA term in float32 on CUDA cores, around the 4-bit product.  (The
+// tensor cores have no float32 product; one from operands split into 16-bit parts was not tried.)
 //
 // Both kernels are register-tiled products over tiles of up to 64 tokens of one segment (tokens that
 // share an adapter), so an adapter's rows are read once per 64 of its tokens:
@@ -8,7 +8,7 @@
 // 256 threads; a thread keeps 4 tokens x 4 columns.  Operands pass through shared memory 32 deep, k-major,
 // so that a step of k is two 16-byte reads for 16 multiply-adds; the next 32 are on their way meanwhile.
 // Bound by the multiply-adds at r_max 64, by the reads of x and y below.  (1000 tokens, 4096 x 1000, r_max 32:
-// 48 us a linear, against 34 with a 16-bit pool on the tensor cores.)  Where segments hold few tokens, the
+// 51 us a linear, against 31 with a 16-bit pool on the tensor cores.)  Where segments hold few tokens, the
 // expand gives a thread one feature of up to 8 tokens instead, and the shrink goes token by token,
 // together with the quantisation (fp4_front_kernel).
 #include <algorithm>

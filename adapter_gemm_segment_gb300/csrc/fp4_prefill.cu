@@ -32,8 +32,8 @@ using namespace ptx;
 //
 // Block scales reach tensor memory through registers: four warps read a step's 3 KB from shared
 // memory and store it to their 32 lanes (tcgen05.st).  Copying it there by tcgen05.cp from the
-// thread that issues the MMAs takes the tensor pipe 64 clocks for each 512 bytes, measured: 815
-// clocks a step of four MMAs and six copies against 512 for the MMAs alone.
+// thread that issues the MMAs holds the tensor pipe: a step of four MMAs and six copies of 512 bytes
+// took 815 clocks, the MMAs alone 512, about 50 clocks a copy.
 //
 // Tensor memory (512 columns): two accumulators of 256 columns that share 96 of them ([0, 256) and
 // [160, 416)), and four sets of 24 scale columns.  The main loop of the next tile may start once
@@ -50,10 +50,12 @@ using namespace ptx;
 // Warps: 0 loads codes, 1 issues MMAs (even CTA), 2-9 drain the accumulator, 10-13 build the LoRA
 // blocks, 14-17 bring in the scales.
 //
-// Measured: 8191 x 11008 x 4096 to float32 in 120 us, 6.1 PFLOP/s, 63 % of the MMAs' own rate.  A step's
-// 32 KB arrive in shared memory and are read once by the MMAs, 64 KB in 512 clocks at 128 bytes a clock:
-// that port is what the steps wait for (686 clocks each).  Where K is short it is the epilogue's pass
-// through shared memory: 16384 x 1024 x 4096 takes 46 us in bf16, 28 in a copy that leaves the pass out.
+// Measured: 8191 x 11008 x 4096 to float32 in 121 us (112 on some boxes), 6.1 PFLOP/s, 63 % of the MMAs' own
+// rate, 686 clocks a step where its MMAs take 512.  The likeliest bound is the shared-memory port, 128
+// bytes a clock: a step's 32 KB of codes arrive and are read once by the MMAs (64 KB), its 3 KB of scales
+// arrive and are read by each of four warps (15 KB), and y's pass adds 6 KB, 85 KB or 680 clocks.  Where
+// K is short it is the epilogue's pass through shared memory: 16384 x 1024 x 4096 takes 46.7 us in bf16,
+// 28 in a copy that left the pass out.
 constexpr int kPM = 128;         // token rows per CTA
 constexpr int kPN = 256;         // features per pair tile
 constexpr int kPThreads = 576;
@@ -302,7 +304,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         } else if (lane == 0 && a.fuse) {
             // odd CTA: tells the even one that a LoRA block is written.  A release at cluster scope waits
             // for every access of its thread, so it is this thread's and not the writers', whose next
-            // loads it would wait for (600 tokens over 100 adapters of rank 16: 76 against 65 us).
+            // loads it would wait for (600 tokens over 100 adapters of rank 16, s in one part: 76 against 65 us).
             const uint32_t peer0 = mapa_shared(smem_u32(lora_peer), 0);
             int local = 0, lb = 0;
             bool ok = true;
@@ -757,9 +759,10 @@ static int launch_pair_t(const Fp4View& x, const Fp4View& w, void* y, long long 
 // adapters need more accumulator columns than a pass holds take several passes over their columns.
 // The parts of a tile are a thread-block cluster: they leave their shares in global memory, and after
 // the cluster barrier each adds up some of the rows.
-// With x already stored in 4 bits, the codes and scales are copied instead.  Bound by the read of
-// x, which one kernel does once where a quantiser and a shrink would do it twice: 50 us for 16384 x 4096,
-// 41 with no adapter in the batch (the quantiser alone 28).
+// With x already stored in 4 bits, the codes and scales are copied instead.  One read of x where a
+// quantiser and a shrink would take two: 50 us for 16384 x 4096, 41 with no adapter in the batch (the
+// quantiser alone 28).  That is 3 TB/s and 53 % of the issue slots, 63 % on the SMs that hold two CTAs:
+// neither is full, and which of the two holds it is not settled.
 constexpr int kQWorkers = 16;   // worker warps: with two CTAs an SM, 32 to hide their latencies
 constexpr int kQThreads = 64 + 32 * kQWorkers;  // warp 0: A rows, warp 1: MMAs
 constexpr uint32_t kQXBytes = 128 * 256;  // two 64-column swizzled halves

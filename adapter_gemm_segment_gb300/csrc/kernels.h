@@ -124,7 +124,7 @@ int fp4_decode_splits(int h_out, int h_in);
 int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, long long ldy, int32_t* status,
                       int early, const Fp4DecodeLora* lora, cudaStream_t st);
 // The kernel before it for small batches: x quantised into q (nullptr: not) and the shrink output in
-// *s_parts K parts, in one launch (16-bit pools whose adapters the per-token shrink suits).
+// *s_parts K parts, in one launch (pools of any type whose adapters the per-token shrink suits).
 int launch_fp4_front(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* q, float* s_out, int* s_parts,
                      cudaStream_t st);
 // float32 pools: the shrink in K parts (s_out [f32_shrink_parts][n][R]), and y += s B^T.
