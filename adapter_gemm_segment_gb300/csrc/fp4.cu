@@ -287,22 +287,22 @@ fp4_expand_kernel(PoolView pool, SegView seg, const float* __restrict__ s_in, in
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.x, R = pool.R, h_out = pool.h_out;
-    if (__ldcg(seg.status) != LORA_OK) return;
+    const int status = __ldcg(seg.status);  // (independent loads first)
     int slot = -1, nt, tok[kFp4ItemTok];
     if (b < items) {
-        if (b >= __ldcg(seg.nseg + 1)) return;
+        const int n_items = __ldcg(seg.nseg + 1);
         const int4 head = __ldcg(reinterpret_cast<const int4*>(seg.items + (size_t)b * 8));      // slot, count, tokens 0, 1
         const int2 tail = __ldcg(reinterpret_cast<const int2*>(seg.items + (size_t)b * 8 + 4));  // tokens 2, 3
-        slot = head.x, nt = head.y;
+        slot = head.x, nt = b < n_items ? head.y : 0;
         tok[0] = head.z, tok[1] = head.w, tok[2] = tail.x, tok[3] = tail.y;
     } else {  // the segment of no adapter is the first
         const int j0 = (b - items) * kFp4ItemTok;
-        const int end = __ldcg(seg.nseg) > 0 && __ldcg(seg.seg_slot) < 0 ? __ldcg(seg.seg_start + 1) : 0;
-        nt = min(kFp4ItemTok, end - j0);
-        if (nt <= 0) return;
+        const int nseg = __ldcg(seg.nseg), first = __ldcg(seg.seg_slot), end = __ldcg(seg.seg_start + 1);
 #pragma unroll
-        for (int u = 0; u < kFp4ItemTok; ++u) tok[u] = __ldcg(seg.perm + j0 + min(u, nt - 1));
+        for (int u = 0; u < kFp4ItemTok; ++u) tok[u] = __ldcg(seg.perm + min(j0 + u, seg.n - 1));
+        nt = nseg > 0 && first < 0 ? min(kFp4ItemTok, end - j0) : 0;
     }
+    if (status != LORA_OK || nt <= 0) return;
     const int o = blockIdx.y * 256 * fpt + threadIdx.x;
     const bool live[2] = {o < h_out, fpt == 2 && o + 256 < h_out};
     float acc[2][kFp4ItemTok];
@@ -485,18 +485,17 @@ static Fp4View view_of(const lora_fp4_matrix* m) { return fp4_view(m->codes_dev,
 // Batches of more than 256 tokens whose tokens are spread over many adapters (fewer than 16 a slot) at
 // ranks of up to 32: the product without the LoRA term, and a segmented expand after it.  The fused
 // product then builds LoRA blocks for almost every adapter in every tile.  Measured, us a linear
-// separate / fused, 4096 x 4096, 100 slots, r_max 16, every token its own adapter: 300 tokens 33.8 / 64.7,
-// 600 41 / 82, 1200 62 / 89, 2400 96 / 85; a run of 512 tokens an adapter: 600 tokens 36 / 26, 1200 55 / 34.
-// At r_max 64 the expand loses as much where tokens come in runs (600 tokens 70 / 32) as it gains where
-// they are spread (88 / 238), which the host cannot tell apart, and the fused product stays.  Slots count
+// separate / fused, 4096 x 4096, 100 slots, r_max 16, every token its own adapter: 300 tokens 32.8 / 66.4,
+// 600 39 / 84, 1200 60 / 92, 2400 93 / 87; a run of 512 tokens an adapter: 600 tokens 34 / 26, 1200 53 / 34.
+// At r_max 64 the expand takes 69 / 32 where 600 tokens come in runs and 86 / 243 where they are spread, which the host cannot tell apart, and the fused product stays.  Slots count
 // as adapters whether mounted or not, and more than 100 were not measured.
 //
 // From 32 to 256 tokens the same choice weighs, in us, the blocks that each of the decode kernel's CTAs
 // would build if as many adapters as can be are there, against the expand and its launch.  Measured,
 // fused / separate, Zipf-distributed adapters, 4096 -> 4096 and 4096 -> 11008 features: 64 tokens, 100 slots
-// r_max 8 13.9 / 15.8 and 25.8 / 27.3, r_max 32 25.0 / 19.9 and 61 / 34; 128 tokens, 30 slots r_max 16
-// 20.4 / 20.6 and 37.9 / 31.8; 250 tokens, 6 slots r_max 64 30.5 / 41.3 and 47 / 68, 100 slots r_max 64
-// 88 / 56 and 251 / 98.  (16 tokens: fused throughout.)
+// r_max 8 13.8 / 15.3 and 25.8 / 26.5, r_max 32 25.0 / 19.6 and 62 / 33; 128 tokens, 30 slots r_max 16
+// 20.3 / 20.0 and 37.9 / 30.8; 250 tokens, 6 slots r_max 64 30.4 / 40.9 and 47 / 68, 100 slots r_max 64
+// 88 / 55 and 249 / 97.  (16 tokens: fused throughout.)
 //
 // The product then goes to the workspace in float32 (4 n h_out bytes), so that y is rounded once: at most
 // kFp4SumElements of it.

@@ -5,7 +5,7 @@
 // GPU.  At 4 bits a 4096 x 4096 weight is 8.9 MB, 1.3 us of HBM time: the call is bound by latency
 // (launch, the first loads, the reduction), so every CTA has its share of the weight in flight
 // before it waits for anything, and the split sums meet in shared memory.  (One token 4096 x 4096: 5.6 us;
-// the 64 tokens of a decode batch with their adapters, with the kernel before it, 13.8.)  The block scales reach
+// the 64 tokens of a decode batch with their adapters, with the kernel before it, 13.4.)  The block scales reach
 // tensor memory through registers, by the warps that drain the accumulator later: copied there by
 // tcgen05.cp from the MMA thread, a step of 256 along K took 580 ns whatever the batch.
 //

@@ -184,23 +184,38 @@ template <> __device__ __forceinline__ bool too_large<__half>(float s) {
     const float a = fabsf(s);
     return a >= 65520.f && a <= 3.402823466e38f;
 }
+// Two float32 values in the 16-bit type, the first in the low half, and back.
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 // Eight shrink values for the tensor cores: s = hi + lo, each of the 16-bit type, which multiply the same
 // elements of B.  The two carry s to 2^-16 of itself in bfloat16, 2^-22 (and no nearer than 2^-25) in float16;
 // hi alone would lose as much as the rounding of y does.  An infinity or NaN stays in hi.  What float16 does not
 // hold is left out (both 0) and the result true: nonfinite_dot8 adds it.
 template <typename T> __device__ __forceinline__ bool split8(const float (&s)[8], uint4& hi, uint4& lo) {
-    alignas(16) T h[8], l[8];
+    hi = make_uint4(pack2<T>(s[0], s[1]), pack2<T>(s[2], s[3]), pack2<T>(s[4], s[5]), pack2<T>(s[6], s[7]));
+    float h[8];
+    unpack8<T>(hi, h);
+    lo = make_uint4(pack2<T>(s[0] - h[0], s[1] - h[1]), pack2<T>(s[2] - h[2], s[3] - h[3]),
+                    pack2<T>(s[4] - h[4], s[5] - h[5]), pack2<T>(s[6] - h[6], s[7] - h[7]));
+    if (!nonfinite8<T>(hi)) return false;
+    lo = finite8<T>(lo);  // (inf - inf, NaN)
+    alignas(16) T v[8];
+    *reinterpret_cast<uint4*>(v) = hi;
     bool left_out = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const bool big = too_large<T>(s[e]);
-        left_out |= big;
-        h[e] = from_f32<T>(big ? 0.f : s[e]);
-        const float rest = s[e] - to_f32(h[e]);
-        l[e] = from_f32<T>(fabsf(rest) <= fabsf(s[e]) && !big ? rest : 0.f);  // (inf - inf, NaN: 0)
-    }
-    hi = *reinterpret_cast<const uint4*>(h);
-    lo = *reinterpret_cast<const uint4*>(l);
+    for (int e = 0; e < 8; ++e)
+        if (too_large<T>(s[e])) {
+            v[e] = from_f32<T>(0.f);
+            left_out = true;
+        }
+    hi = *reinterpret_cast<const uint4*>(v);
     return left_out;
 }
 // Sum over b times s of what the blocks leave out: b an infinity or NaN (finite8), or s too large (split8).
