@@ -641,10 +641,10 @@ def lora_fp4_linear_fwd(pool_handle, w: Fp4Matrix, x: torch.Tensor, y: torch.Ten
     """lora_linear_fwd over a 4-bit base weight; x [..., w.cols] and y [..., w.rows] of n_tokens rows in the
     pool's dtype; xq: the stored form of x, where another projection of the same x has made it already
     (it is made in the workspace otherwise)."""
-    n, dt = int(seg.n_tokens), getattr(pool_handle, "dtype", x.dtype)
-    for t, name, cols in ((x, "x", w.cols), (y, "y", w.rows)):
-        if t.dtype != dt or t.dim() == 0 or t.shape[-1] != cols or t.numel() != n * cols:
-            raise LoraError(LORA_EINVAL, f"{name} must be {dt} [{n}, {cols}], got {t.dtype} {list(t.shape)}")
+    n, dt = seg.n_tokens, getattr(pool_handle, "dtype", x.dtype)
+    for t, cols in ((x, w.cols), (y, w.rows)):
+        if t.dtype is not dt or t.numel() != n * cols or t.dim() == 0 or t.size(-1) != cols:
+            raise LoraError(LORA_EINVAL, f"{'x' if t is x else 'y'} must be {dt} [{n}, {cols}], got {t.dtype} {list(t.shape)}")
     _check(_lib.lora_fp4_linear_fwd(pool_handle, ctypes.byref(w.struct), _dev(x, "x").data_ptr(),
                                     None if xq is None else ctypes.byref(xq.struct), _dev(y, "y").data_ptr(),
                                     ctypes.byref(seg), _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size(),
@@ -739,14 +739,20 @@ class LoraPool:
         """The workspace of this pool's calls of n tokens on one stream.  The 4-bit linear keeps the largest
         asked for, which serves every smaller batch; the 16-bit linear's may need more for fewer tokens, so
         it keeps one for each n."""
-        make = lora_fp4_linear_workspace_bytes if kind == "fp4" else lora_linear_workspace_bytes
-        with _on_stream(stream):
-            if _capturing():
-                return torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
-            key = (kind, device, _stream(stream).value) + (() if kind == "fp4" else (n,))
-            held, ws = self._ws.get(key, (-1, None))
-            if held < n:
-                ws = torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
+        if stream is not None:
+            with _on_stream(stream):
+                return self._stream_workspace(kind, n, device, _stream(stream).value)
+        return self._stream_workspace(kind, n, device, _stream(None).value)
+
+    def _stream_workspace(self, kind: str, n: int, device, handle) -> torch.Tensor:
+        """_own_workspace on the current stream, whose handle that is."""
+        key = (kind, device, handle) if kind == "fp4" else (kind, device, handle, n)
+        captured = _capturing()
+        held, ws = self._ws.get(key, (-1, None))
+        if captured or held < n:
+            make = lora_fp4_linear_workspace_bytes if kind == "fp4" else lora_linear_workspace_bytes
+            ws = torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
+            if not captured:
                 self._ws[key] = (n, ws)
         return ws
 
