@@ -16,6 +16,7 @@
 // block (two shuffles give its maximum), and the 4 x 4 scale bytes of those rows' four blocks are 16
 // consecutive bytes of a scale tile, written by one lane.
 #include <algorithm>
+#include <climits>
 #include <cstring>
 
 #include "common.cuh"
@@ -642,6 +643,9 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
     if ((reinterpret_cast<uintptr_t>(x_dev) | reinterpret_cast<uintptr_t>(y_dev)) % align)
         return set_error(LORA_EINVAL, "x/y must be %zu-byte aligned", align);
     if (reinterpret_cast<uintptr_t>(ws_dev) % 256) return set_error(LORA_EINVAL, "ws must be 256-byte aligned");
+    // the fused decode kernel's boxes of B have 32-bit coordinates (slot * h_out + feature)
+    if (pv.dtype != LORA_F32 && n <= 256 && !fp4_separate(pv, n) && (long long)pv.S * pv.h_out > INT_MAX)
+        return set_error(LORA_EUNSUP, "4-bit linear of %d tokens over %d slots x %d features", n, pv.S, pv.h_out);
     Fp4WsLayout L;
     rc = fp4_ws_layout(pool, n, &L);
     if (rc) return rc;

@@ -414,6 +414,7 @@ int lora_fp4_matmul(const lora_fp4_matrix* x, const lora_fp4_matrix* w, void* y_
  * take a separate expand instead, which adds the LoRA term to the product in float32.  float32 pools: the
  * LoRA term in float32 throughout, added to the product's float32 y.  In each y is rounded once. The same call gives
  * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 4 kernels.
+ * LORA_EUNSUP: up to 256 tokens of a 16-bit pool of 2^31 slots x features and more.
  * A workspace of lora_fp4_linear_workspace_bytes(pool, n) serves every batch of up to n tokens.
  * The 16-bit linears stream their weights ahead of the linear before them, so the y of a linear, this one
  * included, is not to be their W without a wait in between; what lora_fp4_dequantize or lora_fp4_matmul

@@ -84,3 +84,25 @@ def test_refusals_through_a_pool(lib):
             pool.fp4_linear(w, x, seg, y=bad)
         assert e.value.code == lib.LORA_EINVAL
     pool.close()
+
+
+@pytest.mark.gpu
+def test_pools_past_32_bit_box_coordinates(lib):
+    """2048 slots x 2^20 features are 2^31 rows of B (34 GB): small batches, whose kernel addresses them in
+    boxes with 32-bit coordinates, are refused; larger ones read the last slot."""
+    h_out = 1 << 20
+    pool = lib.LoraPool(64, h_out, 8, 2048, torch.float16, "cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    A = torch.randn(8, 64, generator=gen, device="cuda").half()
+    B = torch.randn(h_out, 8, generator=gen, device="cuda").half()
+    pool.load_slot(2047, A, B, 8.0)
+    w = lib.lora_fp4_quantize(torch.zeros(h_out, 64, device="cuda"), lib.Fp4Matrix(h_out, 64))
+    x = torch.randn(300, 64, generator=gen, device="cuda").half()
+    idx = torch.full((300,), 2047, dtype=torch.int32, device="cuda")
+    with pytest.raises(lib.LoraError) as e:
+        pool.fp4_linear(w, x[:20], pool.segment(idx[:20]))
+    assert e.value.code == lib.LORA_EUNSUP
+    y = pool.fp4_linear(w, x, pool.segment(idx))
+    ref = (x[-2:].double() @ A.double().T) @ B.double().T
+    assert (y[-2:].double() - ref).abs().max() <= 2e-3 * ref.abs().max()
+    pool.close()
