@@ -42,6 +42,8 @@ EXPORTED = (
     "lora_loader_stats",
     "lora_fp4_bytes", "lora_fp4_quantize", "lora_fp4_dequantize", "lora_fp4_matmul",
     "lora_fp4_linear_workspace_bytes", "lora_fp4_linear_fwd",
+    "lora_i8_bytes", "lora_i8_quantize", "lora_i8_dequantize", "lora_i8_rmsnorm", "lora_i8_matmul_workspace_bytes",
+    "lora_i8_matmul", "lora_i8_linear_workspace_bytes", "lora_i8_linear_fwd",
 )
 
 
@@ -59,6 +61,18 @@ class lora_pool_desc(ctypes.Structure):
 class lora_fp4_matrix(ctypes.Structure):
     _fields_ = [("codes_dev", ctypes.c_void_p), ("scales_dev", ctypes.c_void_p), ("rows", ctypes.c_int32),
                 ("cols", ctypes.c_int32)]
+
+
+class lora_i8_matrix(ctypes.Structure):
+    _fields_ = [("codes_dev", ctypes.c_void_p), ("scales_dev", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32)]
+
+
+class lora_i8_norm(ctypes.Structure):
+    _fields_ = [("x_dev", ctypes.c_void_p), ("residual_dev", ctypes.c_void_p), ("weight_dev", ctypes.c_void_p),
+                ("residual_out_dev", ctypes.c_void_p), ("y_dev", ctypes.c_void_p), ("out", ctypes.POINTER(lora_i8_matrix)),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldro", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class lora_segments(ctypes.Structure):
@@ -115,6 +129,14 @@ def _load() -> ctypes.CDLL:
         "lora_fp4_matmul": [P(lora_fp4_matrix), P(lora_fp4_matrix), vp, i32, ctypes.c_int64, vp],
         "lora_fp4_linear_workspace_bytes": [vp, i32, P(sz)],
         "lora_fp4_linear_fwd": [vp, P(lora_fp4_matrix), vp, P(lora_fp4_matrix), vp, P(lora_segments), vp, sz, vp],
+        "lora_i8_bytes": [i32, i32, P(sz), P(sz)],
+        "lora_i8_quantize": [vp, i32, ctypes.c_int64, P(lora_i8_matrix), vp],
+        "lora_i8_dequantize": [P(lora_i8_matrix), vp, i32, ctypes.c_int64, vp],
+        "lora_i8_rmsnorm": [P(lora_i8_norm), vp],
+        "lora_i8_matmul_workspace_bytes": [i32, i32, i32, P(sz)],
+        "lora_i8_matmul": [P(lora_i8_matrix), P(lora_i8_matrix), vp, i32, ctypes.c_int64, vp, sz, vp],
+        "lora_i8_linear_workspace_bytes": [vp, i32, P(sz)],
+        "lora_i8_linear_fwd": [vp, P(lora_i8_matrix), vp, P(lora_i8_matrix), vp, P(lora_segments), vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -588,7 +610,7 @@ class Fp4Matrix:
         return self.codes.numel() + self.scales.numel()
 
 
-def _fp4_rows(t: torch.Tensor, rows: int, cols: int, name: str):
+def _rows_of(t: torch.Tensor, rows: int, cols: int, name: str):
     """dtype code and row stride of a CUDA tensor [rows, cols] whose rows are contiguous."""
     dt = TORCH_TO_LORA.get(t.dtype)
     if dt is None:
@@ -611,21 +633,21 @@ def _fp4_rows(t: torch.Tensor, rows: int, cols: int, name: str):
 
 def lora_fp4_quantize(x: torch.Tensor, out: Fp4Matrix, stream=None) -> Fp4Matrix:
     """Quantise x [rows, cols] (contiguous rows, any row stride) into out."""
-    dt, ld = _fp4_rows(x, out.rows, out.cols, "x")
+    dt, ld = _rows_of(x, out.rows, out.cols, "x")
     _check(_lib.lora_fp4_quantize(x.data_ptr(), dt, ld, ctypes.byref(out.struct), _stream(stream)))
     return out
 
 
 def lora_fp4_dequantize(q: Fp4Matrix, out: torch.Tensor, stream=None) -> torch.Tensor:
     """Read q back into out [rows, cols] (contiguous rows, any row stride)."""
-    dt, ld = _fp4_rows(out, q.rows, q.cols, "out")
+    dt, ld = _rows_of(out, q.rows, q.cols, "out")
     _check(_lib.lora_fp4_dequantize(ctypes.byref(q.struct), out.data_ptr(), dt, ld, _stream(stream)))
     return out
 
 
 def lora_fp4_matmul(x: Fp4Matrix, w: Fp4Matrix, y: torch.Tensor, stream=None) -> torch.Tensor:
     """y [x.rows, w.rows] = x w^T of two stored matrices (y: contiguous rows, any row stride)."""
-    dt, ld = _fp4_rows(y, x.rows, w.rows, "y")
+    dt, ld = _rows_of(y, x.rows, w.rows, "y")
     _check(_lib.lora_fp4_matmul(ctypes.byref(x.struct), ctypes.byref(w.struct), y.data_ptr(), dt, ld, _stream(stream)))
     return y
 
@@ -649,6 +671,121 @@ def lora_fp4_linear_fwd(pool_handle, w: Fp4Matrix, x: torch.Tensor, y: torch.Ten
                                     None if xq is None else ctypes.byref(xq.struct), _dev(y, "y").data_ptr(),
                                     ctypes.byref(seg), _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size(),
                                     _stream(stream)))
+    return y
+
+
+# ---- 8-bit integer base weights ---------------------------------------------------------------
+
+def lora_i8_bytes(rows: int, cols: int):
+    """(codes bytes, scales bytes) of a stored 8-bit matrix [rows, cols]."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib.lora_i8_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+class I8Matrix:
+    """A stored 8-bit integer matrix [rows, cols] (layout in include/lora.h) in device buffers this object
+    owns: ``codes`` int8 [rows, pitch] (pitch: cols rounded up to 16) and ``scales`` float32 [rows].  Its
+    contents are what ``lora_i8_quantize`` or ``lora_i8_rmsnorm`` writes; before that they are undefined."""
+
+    def __init__(self, rows: int, cols: int, device="cuda"):
+        if torch.device(device).type != "cuda":
+            raise ValueError("an 8-bit matrix lives in CUDA memory")  # the kernels take its bare addresses
+        nc, ns = lora_i8_bytes(rows, cols)
+        self.rows, self.cols = int(rows), int(cols)
+        self._mem = (torch.empty(max(nc, 256), dtype=torch.int8, device=device),
+                     torch.empty(max(ns // 4, 64), dtype=torch.float32, device=device))
+        self.codes = self._mem[0][:nc].view(self.rows, -1) if nc else self._mem[0][:0].view(0, (self.cols + 15) // 16 * 16)
+        self.scales = self._mem[1][:self.rows]
+        self.struct = lora_i8_matrix(self._mem[0].data_ptr(), self._mem[1].data_ptr(), self.rows, self.cols)
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in self._mem)
+
+
+def lora_i8_quantize(x: torch.Tensor, out: I8Matrix, stream=None) -> I8Matrix:
+    """Quantise x [rows, cols] (contiguous rows, any row stride) into out."""
+    dt, ld = _rows_of(x, out.rows, out.cols, "x")
+    _check(_lib.lora_i8_quantize(x.data_ptr(), dt, ld, ctypes.byref(out.struct), _stream(stream)))
+    return out
+
+
+def lora_i8_dequantize(q: I8Matrix, out: torch.Tensor, stream=None) -> torch.Tensor:
+    """Read q back into out [rows, cols] (contiguous rows, any row stride)."""
+    dt, ld = _rows_of(out, q.rows, q.cols, "out")
+    _check(_lib.lora_i8_dequantize(ctypes.byref(q.struct), out.data_ptr(), dt, ld, _stream(stream)))
+    return out
+
+
+def lora_i8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Optional[I8Matrix] = None,
+                    y: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                    residual_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """h = x + residual into residual_out (the residual itself where it is not given); the root-mean-square
+    norm of h times weight into y and, as 8-bit integers, into out (either may be left out).  x, residual,
+    residual_out, y: [rows, cols] of one dtype, contiguous rows, any row stride; weight [cols]."""
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    rows, cols = x.shape
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    a = lora_i8_norm()
+    a.rows, a.cols, a.eps, a.dtype = rows, cols, float(eps), TORCH_TO_LORA.get(x.dtype, -1)
+    for t, name, ptr, ld in ((x, "x", "x_dev", "ldx"), (residual, "residual", "residual_dev", "ldr"),
+                             (residual_out, "residual_out", "residual_out_dev", "ldro"), (y, "y", "y_dev", "ldy")):
+        if t is not None:
+            dt, stride = _rows_of(t, rows, cols, name)
+            if t.dtype is not x.dtype:
+                raise ValueError(f"{name} must be {x.dtype}")
+            setattr(a, ptr, t.data_ptr())
+            setattr(a, ld, stride)
+    if weight.dtype is not x.dtype or weight.shape != (cols,):
+        raise ValueError(f"weight must be {x.dtype} [{cols}]")
+    a.weight_dev = _dev(weight, "weight").data_ptr()
+    if out is not None:
+        a.out = ctypes.pointer(out.struct)
+    _check(_lib.lora_i8_rmsnorm(ctypes.byref(a), _stream(stream)))
+
+
+def lora_i8_matmul_workspace_bytes(x_rows: int, w_rows: int, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_i8_matmul_workspace_bytes(x_rows, w_rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def lora_i8_matmul(x: I8Matrix, w: I8Matrix, y: torch.Tensor, ws: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """y [x.rows, w.rows] = x w^T of two stored matrices (y: contiguous rows, any row stride); ws: a workspace
+    of lora_i8_matmul_workspace_bytes(x.rows, w.rows, x.cols), made for the call where it is not given."""
+    dt, ld = _rows_of(y, x.rows, w.rows, "y")
+    if ws is None:
+        with _on_stream(stream):
+            ws = torch.empty(max(256, lora_i8_matmul_workspace_bytes(x.rows, w.rows, x.cols)), dtype=torch.uint8,
+                             device=y.device)
+    _check(_lib.lora_i8_matmul(ctypes.byref(x.struct), ctypes.byref(w.struct), y.data_ptr(), dt, ld,
+                               _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+    return y
+
+
+def lora_i8_linear_workspace_bytes(pool_handle, n_tokens: int) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.lora_i8_linear_workspace_bytes(pool_handle, n_tokens, ctypes.byref(out)))
+    return out.value
+
+
+def lora_i8_linear_fwd(pool_handle, w: I8Matrix, x: torch.Tensor, y: torch.Tensor, seg: lora_segments,
+                       ws: torch.Tensor, xq: Optional[I8Matrix] = None, stream=None) -> torch.Tensor:
+    """lora_linear_fwd over an 8-bit base weight; x [..., w.cols] and y [..., w.rows] of n_tokens rows in the
+    pool's dtype; xq: the stored form of x, where another projection of the same x or the norm before it has
+    made it already (it is made in the workspace otherwise)."""
+    n, dt = seg.n_tokens, getattr(pool_handle, "dtype", x.dtype)
+    for t, cols in ((x, w.cols), (y, w.rows)):
+        if t.dtype is not dt or t.numel() != n * cols or t.dim() == 0 or t.size(-1) != cols:
+            raise LoraError(LORA_EINVAL, f"{'x' if t is x else 'y'} must be {dt} [{n}, {cols}], got {t.dtype} {list(t.shape)}")
+    _check(_lib.lora_i8_linear_fwd(pool_handle, ctypes.byref(w.struct), _dev(x, "x").data_ptr(),
+                                   None if xq is None else ctypes.byref(xq.struct), _dev(y, "y").data_ptr(),
+                                   ctypes.byref(seg), _dev(ws, "ws").data_ptr(), ws.numel() * ws.element_size(),
+                                   _stream(stream)))
     return y
 
 
@@ -736,8 +873,8 @@ class LoraPool:
         return lora_linear_fwd(self.handle, W, x, y, seg, ws, variant, stream)
 
     def _own_workspace(self, kind: str, n: int, device, stream) -> torch.Tensor:
-        """The workspace of this pool's calls of n tokens on one stream.  The 4-bit linear keeps the largest
-        asked for, which serves every smaller batch; the 16-bit linear's may need more for fewer tokens, so
+        """The workspace of this pool's calls of n tokens on one stream.  The 4-bit and 8-bit linears keep the
+        largest asked for, which serves every smaller batch; the 16-bit linear's may need more for fewer tokens, so
         it keeps one for each n."""
         if stream is not None:
             with _on_stream(stream):
@@ -746,11 +883,12 @@ class LoraPool:
 
     def _stream_workspace(self, kind: str, n: int, device, handle) -> torch.Tensor:
         """_own_workspace on the current stream, whose handle that is."""
-        key = (kind, device, handle) if kind == "fp4" else (kind, device, handle, n)
+        key = (kind, device, handle, n) if kind == "linear" else (kind, device, handle)
         captured = _capturing()
         held, ws = self._ws.get(key, (-1, None))
         if captured or held < n:
-            make = lora_fp4_linear_workspace_bytes if kind == "fp4" else lora_linear_workspace_bytes
+            make = {"fp4": lora_fp4_linear_workspace_bytes, "i8": lora_i8_linear_workspace_bytes,
+                    "linear": lora_linear_workspace_bytes}[kind]
             ws = torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
             if not captured:
                 self._ws[key] = (n, ws)
@@ -769,6 +907,20 @@ class LoraPool:
         if ws is None:
             ws = self._own_workspace("fp4", n, x.device, stream)
         return lora_fp4_linear_fwd(self.handle, w, x, y, seg, ws, xq, stream)
+
+    def i8_linear_workspace(self, n_tokens: int, device="cuda") -> torch.Tensor:
+        return _device_bytes(lora_i8_linear_workspace_bytes(self.handle, n_tokens), device)
+
+    def i8_linear(self, w: I8Matrix, x: torch.Tensor, seg, xq: Optional[I8Matrix] = None,
+                  y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """``linear`` over an 8-bit base weight."""
+        n = int(seg.n_tokens)
+        if y is None:
+            with _on_stream(stream):
+                y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
+        if ws is None:
+            ws = self._own_workspace("i8", n, x.device, stream)
+        return lora_i8_linear_fwd(self.handle, w, x, y, seg, ws, xq, stream)
 
     def close(self) -> None:
         if self.handle is not None:

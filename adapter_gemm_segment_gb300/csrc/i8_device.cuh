@@ -1,0 +1,71 @@
+// Device code shared by the 8-bit integer kernels.
+#pragma once
+#include "common.cuh"
+
+namespace lora {
+
+// a + b = s + e exactly.
+__device__ __forceinline__ float two_sum(float a, float b, float& e) {
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+    return s;
+}
+
+// The scale of a row whose largest |x| is amax: the float32 nearest amax / 127.  A row that holds an
+// infinity or a NaN has a NaN scale.
+__device__ __forceinline__ float i8_scale(float amax) {
+    return amax <= 3.402823466e38f ? __fdiv_rn(amax, 127.f) : __uint_as_float(0x7fc00000u);
+}
+
+// What a row's elements are divided by: x / s is (x * up) * inv to 2^-23 of itself, where up is a power
+// of two that keeps the quotient's parts clear of subnormals; s is then s * up.  inv = 0 gives codes 0
+// (a row of zeros, of values too small for a scale, or one that holds an infinity or a NaN).
+struct I8Divisor {
+    float up, s, inv;
+};
+__device__ __forceinline__ I8Divisor i8_divisor(float s) {
+    I8Divisor d;
+    d.up = s < 8.2718e-25f ? 1.2676506e30f : 1.f;  // 2^-80, 2^100
+    d.s = s * d.up;
+    d.inv = s > 0.f ? __frcp_rn(d.s) : 0.f;
+    return d;
+}
+
+// The whole number nearest x / s, ties to the even one.  (x up) inv is off by at most 1.6e-5, so only
+// near the border of two codes does the sign of x - (k +- 1/2) s decide, which one fused multiply-add
+// gives exactly: the codes are those of the real quotient.
+__device__ __forceinline__ int i8_code(float x, const I8Divisor& d) {
+    const float xs = d.inv == 0.f ? 0.f : x * d.up;
+    const float v = xs * d.inv;
+    float k = rintf(v);
+    if (fabsf(v - k) > 0.4999f) {
+        const float side = v > k ? 1.f : -1.f;
+        const float past = side * fmaf(-(k + 0.5f * side), d.s, xs);
+        if (past > 0.f || (past == 0.f && (static_cast<int>(k) & 1) != 0)) k += side;
+    }
+    return static_cast<int>(fminf(fmaxf(k, -127.f), 127.f));
+}
+
+// Four codes in a word, the first in the lowest byte.
+__device__ __forceinline__ uint32_t i8_pack4(int a, int b, int c, int d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// Four codes of a word as float16, exactly: with the sign bit flipped a byte b stands for b - 128, and
+// 0x6400 + b is the float16 1024 + b.
+__device__ __forceinline__ uint2 i8_to_f16x4(uint32_t w) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// A product's value from its whole-number sum: the scales are applied one after the other, the larger
+// number first in, so that a small scale times a small scale does not underflow on the way.
+__device__ __forceinline__ float i8_scaled(int sum, float sx, float sw) {
+    return __int2float_rn(sum) * sx * sw;
+}
+
+}  // namespace lora

@@ -140,6 +140,31 @@ int fp4_prepare_parts(int n, int ktiles);
 int launch_fp4_prepare(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* xq, const Fp4View& q,
                        float* parts_s, float* s, cudaStream_t st);
 
+// A stored 8-bit matrix as the kernels see it (layout in lora.h).
+struct I8View {
+    int8_t* codes;
+    float* scales;
+    int rows, cols;
+    size_t pitch;  // bytes per row of codes
+};
+inline size_t i8_pitch(int cols) { return ((size_t)cols + 15) / 16 * 16; }
+inline I8View i8_view(void* codes, void* scales, int rows, int cols) {
+    return I8View{static_cast<int8_t*>(codes), static_cast<float*>(scales), rows, cols, i8_pitch(cols)};
+}
+int launch_i8_quantize(const void* x, int dtype, long long ld, const I8View& q, cudaStream_t st);
+// The LoRA term of a product: the slot of each token and the shrink output in K parts.
+struct I8Lora {
+    const PoolView* pool;
+    const int32_t* idx;
+    const float* s_in;  // [s_parts][n][R], token order
+    int s_parts;
+};
+// y = sx sw (Cx Cw^T) (+ the LoRA term), dtype, row stride ldy; y stays untouched unless *status
+// (nullable) is LORA_OK.  early_w: every kernel that could have written w has completed when this grid
+// starts (the products inside a linear; only these release the kernel behind them early).
+int launch_i8_small(const I8View& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
+                    const I8Lora* lora, cudaStream_t st);
+
 int num_sms();
 
 }  // namespace lora

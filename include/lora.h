@@ -423,6 +423,85 @@ int lora_fp4_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* byte
 int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* x_dev, const lora_fp4_matrix* xq,
                         void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);
 
+/* ---- 8-bit integer base weights ------------------------------------------------------------
+ *
+ * A frozen base weight under 16-bit adapters held in 8-bit integers with one scale a row (an output
+ * channel), and activations held the same way (one scale a token): half the bytes of 16 bits, and
+ * products whose sums are whole numbers, hence exact and the same whatever the batch.  The multi-LoRA
+ * pages have no counterpart to these entry points.
+ *
+ * A stored matrix [rows, cols] is two device buffers (sizes from lora_i8_bytes, contents written by
+ * lora_i8_quantize or lora_i8_rmsnorm, or by the caller in the same layout):
+ *   codes   row r at r * pitch, pitch = 16 * ceil(cols / 16) bytes: int8, 0 from cols to pitch
+ *   scales  float32, one a row; element (r, k) stands for codes[r][k] * scales[r]
+ * Both 256-byte aligned, owned by the caller.  rows >= 0, 1 <= cols <= 131071 (LORA_EUNSUP above: a sum
+ * of products has 32 bits). */
+typedef struct {
+    void* codes_dev;
+    void* scales_dev;
+    int32_t rows;
+    int32_t cols;
+} lora_i8_matrix;
+
+/* Bytes of the two buffers of a [rows, cols] matrix.  LORA_EINVAL on a bad shape. */
+int lora_i8_bytes(int rows, int cols, size_t* codes_bytes, size_t* scales_bytes);
+
+/* Quantise x_dev [rows, cols] (dtype a lora_dtype, consecutive rows ld elements apart, ld >= cols;
+ * aligned to its element) into out.  Scale: max|x| / 127 of the row, rounded to float32; code: the whole
+ * number nearest x / scale (the real quotient, ties to the even number), at most 127 either way; a row of
+ * zeros has scale 0.  Equal inputs give equal bytes for every dtype.  A row that holds an infinity or a
+ * NaN gets a NaN scale and codes 0.  One kernel on `stream`. */
+int lora_i8_quantize(const void* x_dev, int dtype, int64_t ld, const lora_i8_matrix* out, void* stream);
+
+/* Read a stored matrix back: out_dev [rows, cols] (dtype, row stride ld >= cols), the float32 product of
+ * code and scale rounded to dtype.  One kernel on `stream`. */
+int lora_i8_dequantize(const lora_i8_matrix* q, void* out_dev, int dtype, int64_t ld, void* stream);
+
+/* Residual addition, root-mean-square norm and its output in 8 bits, one kernel on `stream`:
+ *     h = x + residual (rounded to dtype; x where residual is NULL)
+ *     v = h / sqrt(mean(h^2) + eps) * weight
+ * residual_out receives h, y receives v rounded once to dtype, out the stored form of v itself (not of y).
+ * The row's statistics are held to about 2^-44, so out's codes are those of the real v.  A row that holds an
+ * infinity or a NaN gets a NaN scale and codes 0.
+ *   x, residual (nullable), residual_out (nullable without residual; may be residual or x), y (nullable;
+ *   may be x): [rows, cols] of dtype with row strides ldx, ldr, ldro, ldy >= cols; weight [cols];
+ *   out (nullable): a stored matrix [rows, cols].  y or out is wanted.  eps in [1e-12, 1]. */
+typedef struct {
+    const void* x_dev;
+    const void* residual_dev;
+    const void* weight_dev;
+    void* residual_out_dev;
+    void* y_dev;
+    const lora_i8_matrix* out;
+    int64_t ldx, ldr, ldro, ldy;
+    int32_t rows, cols;
+    int32_t dtype;
+    float eps;
+} lora_i8_norm;
+int lora_i8_rmsnorm(const lora_i8_norm* args, void* stream);
+
+/* y_dev [x.rows, w.rows] = sx sw (Cx Cw^T) of two stored matrices with the same cols: the sums of code
+ * products exact, then times x's and w's scales in float32 and rounded once to dtype (row stride ldy >=
+ * w.rows elements, aligned to its element).  A NaN scale makes the outputs of its row NaN and no others.
+ * ws_dev: >= lora_i8_matmul_workspace_bytes (which may be 0: ws_dev is then not used), 256-byte aligned;
+ * successive calls on one stream may share it.  The same row of x gives the same bits in every batch. */
+int lora_i8_matmul_workspace_bytes(int x_rows, int w_rows, int cols, size_t* bytes);
+int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev, int dtype, int64_t ldy, void* ws_dev,
+                   size_t ws_bytes, void* stream);
+
+/* lora_linear_fwd over an 8-bit base weight:
+ *     y[t,:] = Q(x)[t,:] w^T + (alpha_s / r_s) (x[t,:] A_s^T) B_s^T
+ * w: stored [h_out, h_in].  The base term takes x quantised as lora_i8_quantize does (into the workspace),
+ * or, when xq is not NULL, xq (x's stored form from lora_i8_quantize, or lora_i8_rmsnorm's out beside its y
+ * as x; projections that read the same x share it); the LoRA term takes x as it is, in the pool's dtype.
+ * x_dev, y_dev, seg, errors and the device status word as in lora_linear_fwd.  The LoRA term is computed in
+ * float32 and added to the base term in float32; y is rounded once.  An infinity or NaN in one adapter
+ * reaches that adapter's tokens only.  A workspace of lora_i8_linear_workspace_bytes(pool, n) serves every
+ * batch of up to n tokens.  The y of a linear is not to be w's codes or scales without a wait in between. */
+int lora_i8_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes);
+int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_dev, const lora_i8_matrix* xq,
+                       void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);
+
 /* Message of the last failed call on this host thread ("" if none). */
 const char* lora_last_error(void);
 

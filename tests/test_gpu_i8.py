@@ -1,0 +1,355 @@
+"""Matrices in 8-bit integers on the GPU against the float64 oracle.
+
+Stored codes and scales are compared bit for bit: the definition leaves no freedom, and the norm holds its
+row statistics closely enough (about 2^-44) that an element within that of a border of two codes does not
+occur in these inputs.  A product's sum is a whole number and exact; its output is that sum rounded to
+float32 and two float32 multiplications, then one rounding to its type: 3 * 2^-24 of itself and half a step
+of the type.  The LoRA term adds float32 sums of h_in and of r_max products.
+"""
+import numpy as np
+import pytest
+import torch
+
+from adapter_gemm_segment_gb300 import workloads as wl
+from oracle import i8_oracle as Q
+from oracle import lora_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}  # half an ulp, relative
+TINY = {torch.float32: 2.0 ** -149, torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -133}  # half a subnormal step
+F = 2.0 ** -24
+
+
+def special_rows(rows, cols, dtype, seed=0):
+    """Rows that meet every branch: ties, zeros, tiny and huge rows, infinities, NaN, -0."""
+    rng = np.random.default_rng([seed, rows, cols])
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-8, 8, size=(rows, 1)))
+    ties = rng.integers(-254, 255, size=(rows, cols)) / 2.0
+    ties[:, 0] = 127
+    kind = rng.integers(0, 8, size=(rows, 1))
+    x = np.where(kind == 0, ties, x)
+    x = np.where(kind == 1, 0.0, x)
+    x = np.where(kind == 2, x * 2.0 ** (-16 if dtype == torch.float16 else -125), x)
+    x = np.where(kind == 3, x * 2.0 ** (6 if dtype == torch.float16 else 118), x)
+    x[rng.random((rows, cols)) < 0.05] = -0.0
+    t = torch.from_numpy(x).to(dtype)
+    if rows > 4:
+        t[1, cols // 2] = float("inf")
+        t[2, cols // 3] = float("nan")
+        t[3, cols // 2] = torch.finfo(dtype).max
+        t[4] = torch.finfo(dtype).smallest_normal / 8
+    return t
+
+
+def guarded_matrix(lib, rows, cols):
+    """A stored matrix whose buffers are exactly as long as lora_i8_bytes says, between canaries."""
+    m = lib.I8Matrix(rows, cols)
+    nc, ns = lib.lora_i8_bytes(rows, cols)
+    bufs = []
+    for n in (nc, ns):
+        full = torch.full((2 * 4096 + (n + 255) // 256 * 256,), 0x25, dtype=torch.int8, device="cuda")
+        bufs.append((full, n))
+    m.codes = bufs[0][0][4096:4096 + nc].view(rows, -1)
+    m.scales = bufs[1][0][4096:4096 + ns].view(torch.float32)
+    m.struct = lib.lora_i8_matrix(m.codes.data_ptr(), m.scales.data_ptr(), rows, cols)
+    m.bufs = bufs
+    return m
+
+
+def check_stored(m, cols, codes, scales):
+    got = m.codes.cpu().numpy()
+    s = m.scales.cpu().numpy()
+    assert np.array_equal(s, scales, equal_nan=True)
+    assert np.array_equal(got[:, :cols], codes) and (got[:, cols:] == 0).all()
+    for full, n in getattr(m, "bufs", ()):
+        assert (full[:4096] == 0x25).all() and (full[4096 + n:] == 0x25).all()
+
+
+SHAPES = [(1, 1, 0, 0), (1, 4096, 0, 0), (3, 31, 0, 0), (5, 33, 0, 1), (129, 257, 0, 0), (700, 255, 1, 0), (64, 1000, 24, 0),
+          (900, 1009, 31, 3), (400, 4097, 0, 0), (400, 4104, 0, 0), (7, 11008, 8, 8), (350, 17000, 0, 0), (3, 70001, 0, 0),
+          (320, 20008, 1, 0)]
+
+
+def strided(rows, cols, pad, shift, dtype, fill=float("nan")):
+    wide = torch.full((rows * (cols + pad) + shift + 8,), fill, dtype=dtype, device="cuda")
+    return wide, wide[shift:shift + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,pad,shift", SHAPES)
+def test_quantize_bytes_and_read_back(lib, dtype, rows, cols, pad, shift):
+    src = special_rows(rows, cols, dtype)
+    _, x = strided(rows, cols, pad, shift, dtype)
+    x.copy_(src)
+    m = guarded_matrix(lib, rows, cols)
+    lib.lora_i8_quantize(x, m)
+    codes, scales = Q.quantise(src)
+    check_stored(m, cols, codes, scales)
+    for out_dtype in DTYPES:
+        out = torch.full((rows, cols + pad + 3), 7.0, dtype=out_dtype, device="cuda")
+        lib.lora_i8_dequantize(m, out[:, :cols])
+        with np.errstate(all="ignore"):
+            want = codes.astype(np.float32) * scales[:, None]
+        ref = torch.from_numpy(want).to(out_dtype)
+        assert torch.equal(out[:, :cols].cpu().nan_to_num(nan=12345.0), ref.nan_to_num(nan=12345.0))
+        assert (out[:, cols:] == 7.0).all()
+
+
+def test_quantize_is_the_same_for_every_dtype(lib):
+    x = (torch.randn(70, 300, generator=torch.Generator().manual_seed(1)) * 3).to(torch.bfloat16)
+    x = x.to(torch.float16).to(torch.bfloat16)  # values every type holds
+    out = []
+    for dtype in DTYPES:
+        m = lib.lora_i8_quantize(x.to(dtype).cuda(), lib.I8Matrix(70, 300))
+        out.append((m.codes.clone(), m.scales.clone()))
+    for c, s in out[1:]:
+        assert torch.equal(c, out[0][0]) and torch.equal(s, out[0][1])
+
+
+# ---- norm -----------------------------------------------------------------------------------------
+
+def norm_inputs(rows, cols, dtype, seed):
+    rng = np.random.default_rng([seed, rows, cols])
+    x = torch.from_numpy(rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-6, 6, (rows, 1)))).to(dtype)
+    res = torch.from_numpy(rng.standard_normal((rows, cols)) * 2).to(dtype)
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(cols)).to(dtype)
+    if rows > 3:
+        x[0] = 0
+        res[0] = 0
+        x[1] = x[1] * 2.0 ** -10
+        res[1] = 0
+    return x, res, w
+
+
+def check_norm(y, h, w, eps, dtype):
+    ref = Q.rmsnorm(h, w, eps)
+    err = np.abs(y.cpu().double().numpy() - ref)
+    # r rounded to float32, the product h w (exact for 16-bit types), that product times r, the type's rounding
+    assert (err <= (4 * F + UNIT[dtype]) * np.abs(ref) + TINY[dtype]).all()
+    return ref
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,pad,shift", SHAPES)
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm(lib, dtype, rows, cols, pad, shift, residual):
+    eps = 1e-5
+    x0, res0, w0 = norm_inputs(rows, cols, dtype, 1)
+    _, x = strided(rows, cols, pad, shift, dtype)
+    x.copy_(x0)
+    w = w0.cuda()
+    m = guarded_matrix(lib, rows, cols)
+    y = torch.full((rows, cols + 5), 7.0, dtype=dtype, device="cuda")
+    h = x0
+    if residual:
+        wide, res = strided(rows, cols, pad, shift, dtype, 7.0)
+        res.copy_(res0)
+        lib.lora_i8_rmsnorm(x, w, eps, out=m, y=y[:, :cols], residual=res)  # in place
+        h = (x0.double() + res0.double()).to(dtype)
+        assert torch.equal(res.cpu(), h)
+        assert (wide[:shift] == 7.0).all() and (wide[-8:] == 7.0).all()
+        assert torch.equal(x.cpu(), x0)
+    else:
+        lib.lora_i8_rmsnorm(x, w, eps, out=m, y=y[:, :cols])
+    ref = check_norm(y[:, :cols], h, w0, eps, dtype)
+    assert (y[:, cols:] == 7.0).all()
+    check_stored(m, cols, *Q.quantise(ref))
+    # either output by itself gives the same
+    m2, y2 = lib.I8Matrix(rows, cols), torch.empty(rows, cols, dtype=dtype, device="cuda")
+    hd = h.cuda()
+    lib.lora_i8_rmsnorm(hd, w, eps, out=m2)
+    lib.lora_i8_rmsnorm(hd, w, eps, y=y2)
+    assert torch.equal(m2.codes, m.codes) and torch.equal(m2.scales, m.scales) and torch.equal(y2, y[:, :cols])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [200, 4096, 9000])
+def test_norm_special_rows(lib, dtype, cols):
+    """Zeros, infinities and NaN, and rows whose squares overflow float32."""
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.standard_normal((7, cols))).to(dtype)
+    x[0] = 0
+    x[1, 7] = float("inf")
+    x[2, cols - 1] = float("nan")
+    if dtype != torch.float16:
+        x[3] *= 2.0 ** 120
+        x[4] *= 2.0 ** 70
+    x[5, 1:] = 0
+    w = torch.ones(cols, dtype=dtype)
+    w[3] = 0
+    m, y = lib.I8Matrix(7, cols), torch.empty(7, cols, dtype=dtype, device="cuda")
+    lib.lora_i8_rmsnorm(x.cuda(), w.cuda(), 1e-6, out=m, y=y)
+    ok = [0, 3, 4, 5, 6]
+    ref = check_norm(y[ok], x[ok], w, 1e-6, dtype)
+    codes, scales = Q.quantise(ref)
+    assert np.array_equal(m.codes[ok, :cols].cpu().numpy(), codes) and np.array_equal(m.scales[ok].cpu().numpy(), scales)
+    assert m.scales[[1, 2]].isnan().all() and (m.codes[[1, 2]] == 0).all()
+    assert y[1, 7].isnan() and y[2].isnan().all() and (y[1, :7] == 0).all()
+
+
+def test_norm_outputs_over_their_inputs(lib):
+    """residual_out and y over x, and a column window of a wider buffer."""
+    x0, res0, w0 = norm_inputs(50, 264, torch.bfloat16, 5)
+    w = w0.cuda()
+    h = (x0.float() + res0.float()).bfloat16()
+    m = lib.I8Matrix(50, 264)
+    x = x0.cuda()
+    lib.lora_i8_rmsnorm(x, w, 1e-5, out=m, residual=res0.cuda(), residual_out=x)
+    assert torch.equal(x.cpu(), h)
+    check_stored(m, 264, *Q.quantise(Q.rmsnorm(h, w0, 1e-5)))
+    x = x0.cuda()
+    lib.lora_i8_rmsnorm(x, w, 1e-5, y=x, residual=res0.cuda(), residual_out=torch.empty_like(x))
+    check_norm(x, h, w0, 1e-5, torch.bfloat16)
+
+
+# ---- product ----------------------------------------------------------------------------------------
+
+def stored(lib, t):
+    return lib.lora_i8_quantize(t.cuda(), lib.I8Matrix(t.shape[0], t.shape[1]))
+
+
+def check_product(lib, x, w, dtype, pad=0):
+    n, m = x.shape[0], w.shape[0]
+    y = torch.full((n + 2, m + pad + 1), 7.0, dtype=dtype, device="cuda")
+    yv = y[1:n + 1, :m]
+    lib.lora_i8_matmul(stored(lib, x), stored(lib, w), yv)
+    (cx, sx), (cw, sw) = Q.quantise(x), Q.quantise(w)
+    ref = Q.sums(cx, cw).astype(np.float64) * sx.astype(np.float64)[:, None] * sw.astype(np.float64)
+    err = np.abs(yv.cpu().double().numpy() - ref)
+    assert (err <= (3 * F + UNIT[dtype]) * np.abs(ref) + TINY[dtype]).all()
+    assert (y[0] == 7.0).all() and (y[n + 1] == 7.0).all() and (y[1:n + 1, m:] == 7.0).all()
+
+
+def gauss(rows, cols, seed, dtype=torch.float32, scale=1.0):
+    return (torch.randn(rows, cols, generator=torch.Generator().manual_seed(seed)) * scale).to(dtype)
+
+
+@pytest.mark.parametrize("k", [1, 15, 16, 17, 127, 128, 129, 1000, 1025, 2100])
+@pytest.mark.parametrize("n,m,dtype", [(1, 1, 0), (1, 300, 1), (2, 129, 2), (3, 8, 0), (7, 129, 2), (8, 640, 1), (9, 130, 1),
+                                       (17, 640, 1), (64, 128, 2), (100, 257, 0)])
+def test_product_small_batches(lib, n, m, k, dtype):
+    check_product(lib, gauss(n, k, 1), gauss(m, k, 2, scale=0.02), DTYPES[dtype], pad=m % 3)
+
+
+@pytest.mark.parametrize("n,m,k,dtype", [(128, 512, 4096, 2), (129, 300, 700, 0), (200, 264, 1500, 1), (256, 1024, 1024, 2),
+                                         (257, 100, 64, 1), (300, 513, 2048, 0), (777, 391, 1111, 2), (1500, 1003, 520, 1),
+                                         (2050, 640, 130, 0), (5000, 77, 33, 2)])
+def test_product_large_batches(lib, n, m, k, dtype):
+    check_product(lib, gauss(n, k, 3), gauss(m, k, 4, scale=0.02), DTYPES[dtype], pad=(8 - m % 8) % 8 + 7)
+
+
+@pytest.mark.parametrize("n", [1, 5, 16, 60, 130, 300, 700])
+@pytest.mark.parametrize("k", [1024, 1100, 5000, 40000])
+def test_sums_are_exact_at_their_largest(lib, n, k):
+    """Every code -128 (which a caller may store) or 127: partial sums far past 2^24 stay whole."""
+    m = 200
+    rng = np.random.default_rng([n, k])
+    x, w = lib.I8Matrix(n, k), lib.I8Matrix(m, k)
+    cx = np.where(rng.random((n, 1)) < 0.5, -128, 127) * np.ones((1, k), np.int64)
+    cw = np.where(rng.random((m, 1)) < 0.5, -128, 127) * np.ones((1, k), np.int64)
+    cx[:, -3:] = rng.integers(-128, 128, (n, 3))
+    cw[:, -3:] = rng.integers(-128, 128, (m, 3))
+    for q, c in ((x, cx), (w, cw)):
+        q.codes.zero_()
+        q.codes[:, :k].copy_(torch.from_numpy(c.astype(np.int8)))
+        q.scales.fill_(1.0)
+    y = torch.empty(n, m, device="cuda")
+    lib.lora_i8_matmul(x, w, y)
+    ref = (cx @ cw.T).astype(np.float32)  # the float32 nearest the whole number
+    assert np.array_equal(y.cpu().numpy(), ref)
+
+
+def test_a_row_gives_the_same_bits_in_every_batch(lib):
+    x, w = gauss(700, 1300, 8), gauss(390, 1300, 9, scale=0.02)
+    q = stored(lib, w)
+    full = torch.empty(700, 390, device="cuda")
+    lib.lora_i8_matmul(stored(lib, x), q, full)
+    for n in (1, 2, 4, 8, 9, 33, 64, 100, 128, 129, 256, 257, 512):
+        y = torch.empty(n, 390, device="cuda")
+        lib.lora_i8_matmul(stored(lib, x[:n]), q, y)
+        assert torch.equal(y, full[:n]), n
+
+
+def test_scales_that_are_not_numbers_stay_in_their_row(lib):
+    for n in (3, 40, 300):
+        x, w = gauss(n, 200, 5), gauss(150, 200, 6)
+        x[1, 5] = float("inf")
+        w[7, 9] = float("nan")
+        y = torch.empty(n, 150, device="cuda")
+        lib.lora_i8_matmul(stored(lib, x), stored(lib, w), y)
+        bad = y.isnan().cpu()
+        want = torch.zeros(n, 150, dtype=torch.bool)
+        want[1] = True
+        want[:, 7] = True
+        assert torch.equal(bad, want)
+
+
+# ---- linear -----------------------------------------------------------------------------------------
+
+def make_pool(lib, case):
+    ad = case.adapters
+    pool = lib.LoraPool(case.h_in, case.h_out, ad.r_max, ad.n_slots, case.dtype, "cuda")
+    for s in range(ad.n_slots):
+        pool.load_slot(s, ad.A[s].cuda(), ad.B[s].cuda(), ad.alphas[s])
+    return pool
+
+
+def linear_reference(case, codes=None):
+    """(float64 y, bound on its error)."""
+    cx, sx = Q.quantise(case.x) if codes is None else codes
+    cw, sw = Q.quantise(case.W)
+    base = Q.sums(cx, cw).astype(np.float64) * sx.astype(np.float64)[:, None] * sw.astype(np.float64)
+    pool = O.pool_of_case(case)
+    x = case.x.double().numpy()
+    y, mag = base.copy(), np.zeros_like(base)
+    for t, s in enumerate(case.idx.tolist()):
+        if s < 0:
+            continue
+        y[t] += pool.scale[s] * (pool.B[s] @ (pool.A[s] @ x[t]))
+        mag[t] = abs(pool.scale[s]) * (np.abs(pool.B[s]) @ (np.abs(pool.A[s]) @ np.abs(x[t])))
+    # float32 sums of h_in and then r_max products, the scale, the sum over K parts; the base term's three
+    # roundings, the addition, the type's rounding
+    terms = case.h_in + case.adapters.r_max + 32
+    bound = terms * F * mag + 3 * F * np.abs(base) + (F + UNIT[case.dtype]) * np.abs(y) + TINY[case.dtype]
+    return y, bound
+
+
+def check_linear(lib, case, **kw):
+    pool = make_pool(lib, case)
+    w = stored(lib, case.W)
+    seg = pool.segment(case.idx.cuda())
+    n = case.x.shape[0]
+    y = torch.full((n + 2, case.h_out), 7.0, dtype=case.dtype, device="cuda")
+    if (case.h_out * y.element_size()) % 16 and case.dtype != torch.float32:
+        raise AssertionError("a test of 16-bit pools has 16-byte rows")
+    x = case.x.cuda()
+    pool.i8_linear(w, x, seg, y=y[1:n + 1])
+    assert lib.lora_segment_status(seg) == lib.LORA_OK
+    ref, bound = linear_reference(case)
+    err = np.abs(y[1:n + 1].cpu().double().numpy() - ref)
+    assert (err <= bound).all(), f"{(err / bound).max()}"
+    assert (y[0] == 7.0).all() and (y[n + 1] == 7.0).all()
+    # with x's stored form from outside: the same bits
+    y2 = pool.i8_linear(w, x, seg, xq=stored(lib, case.x))
+    assert torch.equal(y2, y[1:n + 1])
+    pool.close()
+    return y2
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,h_in,h_out,ranks,r_max,p_base", [
+    (1, 64, 8, [8], 8, 0.0), (1, 4096, 136, [8, 8], 8, 0.0), (2, 264, 72, [1, 16], 16, 0.5), (5, 1000, 200, [3, 8, 24], 24, 0.2),
+    (8, 512, 128, [8] * 20, 8, 0.1), (9, 256, 256, [64, 8], 64, 0.0), (16, 2056, 136, [16, 2], 16, 0.3), (40, 256, 384, [8, 16, 8], 16, 0.2),
+    (64, 1024, 264, [8] * 100, 8, 0.1), (100, 3000, 128, [64, 8, 16], 64, 0.15), (128, 520, 520, [5] * 7, 8, 0.2),
+    (129, 520, 136, [8, 256], 256, 0.2), (200, 1200, 264, [8, 16, 64] * 2, 64, 0.15), (256, 256, 264, [32] * 40, 32, 0.0),
+    (257, 256, 264, [8, 16], 16, 0.2), (300, 1032, 392, [16] * 60, 16, 0.1), (700, 264, 520, [8, 64, 24], 64, 0.3),
+    (1300, 520, 264, [16] * 9, 16, 1.0)])
+def test_linear(lib, dtype, n, h_in, h_out, ranks, r_max, p_base):
+    check_linear(lib, wl.random_case(n + h_in, n, h_in, h_out, ranks, r_max=r_max, dtype=dtype, p_base=p_base))
+
+
+@pytest.mark.parametrize("n,h_in,h_out,r_max", [(3, 37, 5, 3), (20, 101, 33, 5), (150, 77, 131, 7), (400, 333, 91, 12)])
+def test_linear_float32_odd_sizes(lib, n, h_in, h_out, r_max):
+    check_linear(lib, wl.random_case(n, n, h_in, h_out, [r_max, 1, 2], r_max=r_max, dtype=torch.float32, p_base=0.2))
