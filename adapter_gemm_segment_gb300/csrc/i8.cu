@@ -99,9 +99,11 @@ __device__ __forceinline__ MaxPair max_pair(MaxPair a, MaxPair b) {
 // One read of x, one write of the codes: bound by memory.  A row is held in registers between its maximum
 // and its codes, by a warp (rows of up to 1024 elements) or by a CTA; longer rows than a CTA holds are
 // read twice, in pieces.
-template <typename T, int NV, bool VEC>
+// F16: codes as float16 into x16 [rows][pitch], row r from row perm[r] of x (see launch_i8_quantize_f16).
+template <typename T, int NV, bool VEC, bool F16>
 __global__ void __launch_bounds__(kRowThreads)
-i8_quantize_kernel(const T* x, long long ld, I8View q, int G, int pieces) {
+i8_quantize_kernel(const T* x, long long ld, I8View q, int G, int pieces, const int32_t* perm, const int32_t* status,
+                   __half* x16) {
     __shared__ float red[kRowThreads / 32];
     pdl_wait();
     pdl_trigger();
@@ -110,6 +112,10 @@ i8_quantize_kernel(const T* x, long long ld, I8View q, int G, int pieces) {
     const long long r = (long long)blockIdx.x * (blockDim.x / G) + team;
     if (r >= q.rows) return;  // (whole warps; G is the CTA where it is more than a warp)
     const T* row = x + r * ld;
+    if constexpr (F16) {
+        if (status != nullptr && __ldcg(status) != LORA_OK) return;  // (perm is not valid either)
+        if (perm != nullptr) row = x + (long long)__ldcg(perm + r) * ld;
+    }
     const int span = G * NV * 8, pitch = (int)q.pitch;
     float v[NV][8];
     float m = 0.f;
@@ -131,17 +137,41 @@ i8_quantize_kernel(const T* x, long long ld, I8View q, int G, int pieces) {
     const float s = i8_scale(m);
     if (tid == 0) q.scales[r] = s;
     const I8Divisor d = i8_divisor(s);
-    int8_t* out = q.codes + r * q.pitch;
     for (int off = 0; off < pitch; off += span) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (off > 0) Part::load(row + off, q.cols - off, i, tid, G, v[i]);
-            int c[8];
+            if constexpr (F16) {
+                float c[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) c[e] = i8_code(v[i][e], d);
-            Part::store_codes(out + off, pitch - off, i, tid, G, c);
+                for (int e = 0; e < 8; ++e) c[e] = static_cast<float>(i8_code(v[i][e], d));
+                RowPart<__half, VEC>::store(x16 + r * pitch + off, pitch - off, i, tid, G, c);
+            } else {
+                int c[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) c[e] = i8_code(v[i][e], d);
+                Part::store_codes(q.codes + r * pitch + off, pitch - off, i, tid, G, c);
+            }
         }
     }
+}
+
+// Stored codes as float16, rows in the order of perm.  16 codes a thread; bound by memory.
+__global__ void __launch_bounds__(256)
+i8_expand_kernel(I8View q, const int32_t* perm, const int32_t* status, uint4* x16, float* scales) {
+    pdl_wait();
+    pdl_trigger();
+    if (status != nullptr && __ldcg(status) != LORA_OK) return;
+    const int per_row = (int)(q.pitch / 16);
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int r = (int)(e / per_row), c = (int)(e - (long long)r * per_row);
+    if (r >= q.rows) return;
+    const int from = perm ? __ldcg(perm + r) : r;
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(q.codes + (size_t)from * q.pitch) + c);
+    const uint2 a = i8_to_f16x4(w.x), b = i8_to_f16x4(w.y), f = i8_to_f16x4(w.z), g = i8_to_f16x4(w.w);
+    x16[2 * e] = make_uint4(a.x, a.y, b.x, b.y);
+    x16[2 * e + 1] = make_uint4(f.x, f.y, g.x, g.y);
+    if (c == 0) scales[r] = __ldg(q.scales + from);
 }
 
 // ---- read back ------------------------------------------------------------------------------------------
@@ -377,14 +407,17 @@ static bool aligned16(const void* p, long long ld, int rows, size_t elt) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld * (long long)elt) % 16 == 0);
 }
 
-template <typename T>
-static int quantize_t(const void* x, long long ld, const I8View& q, cudaStream_t st) {
-    const RowPlan p = row_plan(q.rows, q.cols);
+template <typename T, bool F16>
+static int quantize_t(const void* x, long long ld, const I8View& q, const int32_t* perm, const int32_t* status, void* x16,
+                      cudaStream_t st) {
     const bool vec = aligned16(x, ld, q.rows, sizeof(T));
+    const RowPlan p = row_plan(q.rows, q.cols);
     const T* xp = static_cast<const T*>(x);
-    void* args[] = {(void*)&xp, (void*)&ld, (void*)&q, (void*)&p.G, (void*)&p.pieces};
-    const void* fn = p.nv == 1 ? (vec ? (const void*)i8_quantize_kernel<T, 1, true> : (const void*)i8_quantize_kernel<T, 1, false>)
-                               : (vec ? (const void*)i8_quantize_kernel<T, 4, true> : (const void*)i8_quantize_kernel<T, 4, false>);
+    __half* hp = static_cast<__half*>(x16);
+    void* args[] = {(void*)&xp, (void*)&ld, (void*)&q, (void*)&p.G, (void*)&p.pieces, (void*)&perm, (void*)&status, (void*)&hp};
+    const void* fn = p.nv == 1
+                         ? (vec ? (const void*)i8_quantize_kernel<T, 1, true, F16> : (const void*)i8_quantize_kernel<T, 1, false, F16>)
+                         : (vec ? (const void*)i8_quantize_kernel<T, 4, true, F16> : (const void*)i8_quantize_kernel<T, 4, false, F16>);
     LORA_CUDA_TRY(launch_pdl(fn, dim3(p.blocks), dim3(p.threads), 0, st, args));
     return LORA_OK;
 }
@@ -392,10 +425,29 @@ static int quantize_t(const void* x, long long ld, const I8View& q, cudaStream_t
 int launch_i8_quantize(const void* x, int dtype, long long ld, const I8View& q, cudaStream_t st) {
     if (q.rows == 0) return LORA_OK;
     switch (dtype) {
-        case LORA_F32: return quantize_t<float>(x, ld, q, st);
-        case LORA_F16: return quantize_t<__half>(x, ld, q, st);
-        default: return quantize_t<__nv_bfloat16>(x, ld, q, st);
+        case LORA_F32: return quantize_t<float, false>(x, ld, q, nullptr, nullptr, nullptr, st);
+        case LORA_F16: return quantize_t<__half, false>(x, ld, q, nullptr, nullptr, nullptr, st);
+        default: return quantize_t<__nv_bfloat16, false>(x, ld, q, nullptr, nullptr, nullptr, st);
     }
+}
+
+int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const int32_t* perm, const int32_t* status,
+                           void* x16, float* scales, cudaStream_t st) {
+    const I8View q = i8_view(nullptr, scales, rows, cols);
+    switch (dtype) {
+        case LORA_F32: return quantize_t<float, true>(x, cols, q, perm, status, x16, st);
+        case LORA_F16: return quantize_t<__half, true>(x, cols, q, perm, status, x16, st);
+        default: return quantize_t<__nv_bfloat16, true>(x, cols, q, perm, status, x16, st);
+    }
+}
+
+int launch_i8_expand(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales, cudaStream_t st) {
+    const long long chunks = (long long)x.rows * (long long)(x.pitch / 16);
+    uint4* out = static_cast<uint4*>(x16);
+    void* args[] = {(void*)&x, (void*)&perm, (void*)&status, (void*)&out, (void*)&scales};
+    if (chunks > 256LL * INT_MAX) return set_error(LORA_EUNSUP, "8-bit matrix of %d rows", x.rows);
+    LORA_CUDA_TRY(launch_pdl((const void*)i8_expand_kernel, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st, args));
+    return LORA_OK;
 }
 
 template <typename T>
@@ -462,16 +514,17 @@ static int check_rows(const void* p, int dtype, int64_t ld, int rows, int cols, 
 
 static I8View view_of(const lora_i8_matrix* m) { return i8_view(m->codes_dev, m->scales_dev, m->rows, m->cols); }
 
-static size_t product_ws(int n, int h_out, int h_in) { return 0; }
+// Up to this many tokens the dot products of i8_small.cu.
+constexpr int kI8Small = 8;
 
-static int launch_product(const I8View& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status,
-                          bool early_w, const I8Lora* lora, char* ws, cudaStream_t st) {
-    return launch_i8_small(x, w, y, dtype, ldy, status, early_w, lora, st);
-}
+// x in float16 codes and its scales: what a product of n rows keeps in its workspace.
+static size_t rows_bytes(int n, int h_in) { return n <= kI8Small ? 0 : align256((size_t)n * i8_pitch(h_in) * 2); }
+static size_t product_ws(int n, int h_in) { return n <= kI8Small ? 0 : rows_bytes(n, h_in) + align256((size_t)n * 4); }
 
-// Workspace of lora_i8_linear_fwd: the shrink output in its K parts, the stored form of x, the product's own.
+// Workspace of lora_i8_linear_fwd: the shrink output in its K parts, x's codes (in bytes for a few tokens,
+// else in float16) and scales.
 struct I8WsLayout {
-    size_t codes_off, scales_off, product_off, total;
+    size_t codes_off, scales_off, total;
 };
 static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     if (n < 0) return set_error(LORA_EINVAL, "n_tokens < 0");
@@ -482,9 +535,8 @@ static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     const long long m = std::max(n, 1);
     const long long rows = std::max(m, pv.dtype == LORA_F32 ? std::min(24 * m, 4LL * num_sms() * 64) : std::min(4 * m, 256LL));
     L->codes_off = align256((size_t)rows * pv.R * 4);
-    L->scales_off = L->codes_off + align256((size_t)n * i8_pitch(pv.h_in));
-    L->product_off = L->scales_off + align256((size_t)n * 4);
-    L->total = L->product_off + align256(product_ws(n, pv.h_out, pv.h_in));
+    L->scales_off = L->codes_off + align256((size_t)n * i8_pitch(pv.h_in) * (n <= kI8Small ? 1 : 2));
+    L->total = L->scales_off + align256((size_t)n * 4);
     return LORA_OK;
 }
 
@@ -571,7 +623,7 @@ int lora_i8_matmul_workspace_bytes(int x_rows, int w_rows, int cols, size_t* byt
     int rc = check_shape(x_rows, cols);
     if (!rc) rc = check_shape(w_rows, cols);
     if (rc) return rc;
-    *bytes = product_ws(x_rows, w_rows, cols);
+    *bytes = product_ws(x_rows, cols);
     return LORA_OK;
 }
 
@@ -583,12 +635,19 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
     if (x->cols != w->cols) return set_error(LORA_EINVAL, "x has %d columns, w %d", x->cols, w->cols);
     rc = check_rows(y_dev, dtype, ldy, w->rows ? x->rows : 0, w->rows, "y");
     if (rc || x->rows == 0 || w->rows == 0) return rc;
-    const size_t need = product_ws(x->rows, w->rows, x->cols);
+    const size_t need = product_ws(x->rows, x->cols);
     if (need && !ws_dev) return set_error(LORA_EINVAL, "ws is NULL");
     if (reinterpret_cast<uintptr_t>(ws_dev) % 256) return set_error(LORA_EINVAL, "ws must be 256-byte aligned");
     if (ws_bytes < need) return set_error(LORA_ENOSPACE, "8-bit product workspace needs %zu bytes, got %zu", need, ws_bytes);
-    return launch_product(view_of(x), view_of(w), y_dev, dtype, ldy, nullptr, /*early_w=*/false, nullptr,
-                          static_cast<char*>(ws_dev), static_cast<cudaStream_t>(stream));
+    const I8View xv = view_of(x), wv = view_of(w);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (x->rows <= kI8Small) return launch_i8_small(xv, wv, y_dev, dtype, ldy, nullptr, /*early_w=*/false, nullptr, st);
+    char* ws = static_cast<char*>(ws_dev);
+    float* sx = reinterpret_cast<float*>(ws + rows_bytes(x->rows, x->cols));
+    rc = launch_i8_expand(xv, nullptr, nullptr, ws, sx, st);
+    if (rc) return rc;
+    const I8Rows rows = {ws, sx, nullptr, x->rows, x->cols};
+    return launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st);
 }
 
 int lora_i8_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes) {
@@ -630,10 +689,16 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         return set_error(LORA_ENOSPACE, "8-bit linear workspace needs %zu bytes, got %zu", L.total, ws_bytes);
     char* ws = static_cast<char*>(ws_dev);
     float* s_buf = reinterpret_cast<float*>(ws);
-    const I8View q = xq ? view_of(xq) : i8_view(ws + L.codes_off, ws + L.scales_off, n, pv.h_in);
+    float* sx = reinterpret_cast<float*>(ws + L.scales_off);
     const SegView sv = seg_view(seg);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (!xq) rc = launch_i8_quantize(x_dev, pv.dtype, pv.h_in, q, st);
+    const bool few = n <= kI8Small;
+    const I8View q = xq ? view_of(xq) : i8_view(ws + L.codes_off, sx, n, pv.h_in);
+    if (!few)  // rows in the order of the segments
+        rc = xq ? launch_i8_expand(q, sv.perm, sv.status, ws + L.codes_off, sx, st)
+                : launch_i8_quantize_f16(x_dev, pv.dtype, n, pv.h_in, sv.perm, sv.status, ws + L.codes_off, sx, st);
+    else if (!xq)
+        rc = launch_i8_quantize(x_dev, pv.dtype, pv.h_in, q, st);
     int s_parts = 1;
     if (!rc) {
         if (pv.dtype == LORA_F32) {
@@ -647,8 +712,9 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
     }
     if (rc) return rc;
     const I8Lora lora = {&pv, sv.idx, s_buf, s_parts};
-    return launch_product(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora,
-                          ws + L.product_off, st);
+    if (few) return launch_i8_small(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
+    const I8Rows rows = {ws + L.codes_off, sx, sv.perm, n, pv.h_in};
+    return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
 }
 
 }  // extern "C"

@@ -152,6 +152,12 @@ inline I8View i8_view(void* codes, void* scales, int rows, int cols) {
     return I8View{static_cast<int8_t*>(codes), static_cast<float*>(scales), rows, cols, i8_pitch(cols)};
 }
 int launch_i8_quantize(const void* x, int dtype, long long ld, const I8View& q, cudaStream_t st);
+// Codes as float16 [rows][pitch] (whole numbers, which it holds exactly) with their scales: what the
+// tensor-core products take x in.  Row r is row perm[r] of x (nullptr: r); untouched unless *status
+// (nullable) is LORA_OK.  From x itself, quantised, or from its stored form.
+int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const int32_t* perm, const int32_t* status,
+                           void* x16, float* scales, cudaStream_t st);
+int launch_i8_expand(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales, cudaStream_t st);
 // The LoRA term of a product: the slot of each token and the shrink output in K parts.
 struct I8Lora {
     const PoolView* pool;
@@ -159,9 +165,21 @@ struct I8Lora {
     const float* s_in;  // [s_parts][n][R], token order
     int s_parts;
 };
+// x in float16 codes (above), rows in the order of perm.
+struct I8Rows {
+    const void* x16;
+    const float* scales;
+    const int32_t* perm;  // nullptr: as they are
+    int rows, cols;
+};
+// On the tensor cores.  early: every kernel that could have written w (1), or w and x (2), has completed when
+// this grid starts.  release: the kernel behind may be released early (never a product by itself, whose y may be
+// a weight that a 16-bit linear streams unwaited).
+int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, int early,
+                   bool release, const I8Lora* lora, cudaStream_t st);
 // y = sx sw (Cx Cw^T) (+ the LoRA term), dtype, row stride ldy; y stays untouched unless *status
 // (nullable) is LORA_OK.  early_w: every kernel that could have written w has completed when this grid
-// starts (the products inside a linear; only these release the kernel behind them early).
+// starts (the products inside a linear; only these release the kernel behind them early).  For a few tokens.
 int launch_i8_small(const I8View& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_w,
                     const I8Lora* lora, cudaStream_t st);
 
