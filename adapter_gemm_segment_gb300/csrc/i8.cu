@@ -517,6 +517,26 @@ static I8View view_of(const lora_i8_matrix* m) { return i8_view(m->codes_dev, m-
 // Up to this many tokens the dot products of i8_small.cu.
 constexpr int kI8Small = 8;
 
+// Above this many tokens the pair kernel.
+constexpr int kI8Tile = 256;
+
+// The K parts of the shrink output added up: the pair kernel reads each row many times.
+__global__ void __launch_bounds__(256)
+i8_sum_parts_kernel(float* s, int parts, size_t part) {
+    pdl_wait();
+    pdl_trigger();
+    const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= part) return;
+    float v = s[e];
+    for (int p = 1; p < parts; ++p) v += s[p * part + e];
+    s[e] = v;
+}
+static int launch_sum_parts(float* s, int parts, size_t part, cudaStream_t st) {
+    void* args[] = {(void*)&s, (void*)&parts, (void*)&part};
+    LORA_CUDA_TRY(launch_pdl((const void*)i8_sum_parts_kernel, dim3((unsigned)((part + 255) / 256)), dim3(256), 0, st, args));
+    return LORA_OK;
+}
+
 // x in float16 codes and its scales: what a product of n rows keeps in its workspace.
 static size_t rows_bytes(int n, int h_in) { return n <= kI8Small ? 0 : align256((size_t)n * i8_pitch(h_in) * 2); }
 static size_t product_ws(int n, int h_in) { return n <= kI8Small ? 0 : rows_bytes(n, h_in) + align256((size_t)n * 4); }
@@ -647,7 +667,8 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
     rc = launch_i8_expand(xv, nullptr, nullptr, ws, sx, st);
     if (rc) return rc;
     const I8Rows rows = {ws, sx, nullptr, x->rows, x->cols};
-    return launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st);
+    return x->rows > kI8Tile ? launch_i8_pair(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st)
+                             : launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st);
 }
 
 int lora_i8_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes) {
@@ -711,9 +732,16 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         }
     }
     if (rc) return rc;
+    if (n > kI8Tile && s_parts > 1) {
+        rc = launch_sum_parts(s_buf, s_parts, (size_t)n * pv.R, st);
+        if (rc) return rc;
+        s_parts = 1;
+    }
     const I8Lora lora = {&pv, sv.idx, s_buf, s_parts};
     if (few) return launch_i8_small(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     const I8Rows rows = {ws + L.codes_off, sx, sv.perm, n, pv.h_in};
+    if (n > kI8Tile)
+        return launch_i8_pair(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
     return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
 }
 

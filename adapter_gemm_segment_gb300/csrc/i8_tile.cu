@@ -58,26 +58,6 @@ struct I8TileArgs {
     int R, s_parts;
 };
 
-// Eight consecutive elements of a row of B (R elements), zeros past R.
-template <typename T> __device__ __forceinline__ void load_b8(const T* row, int j, int R, float (&f)[8]);
-template <> __device__ __forceinline__ void load_b8<__half>(const __half* row, int j, int R, float (&f)[8]) {
-    unpack8<__half>(__ldg(reinterpret_cast<const uint4*>(row + j)), f);
-}
-template <>
-__device__ __forceinline__ void load_b8<__nv_bfloat16>(const __nv_bfloat16* row, int j, int R, float (&f)[8]) {
-    unpack8<__nv_bfloat16>(__ldg(reinterpret_cast<const uint4*>(row + j)), f);
-}
-template <> __device__ __forceinline__ void load_b8<float>(const float* row, int j, int R, float (&f)[8]) {
-    if (R % 4 == 0) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(row + j));
-        const float4 b = j + 4 < R ? __ldg(reinterpret_cast<const float4*>(row + j + 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = j + e < R ? __ldg(row + j + e) : 0.f;
-    }
-}
-
 template <typename T, bool FUSE>
 __global__ void __launch_bounds__(kIThreads, 1)
 i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8TileArgs a) {
