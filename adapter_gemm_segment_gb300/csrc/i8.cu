@@ -171,7 +171,7 @@ i8_expand_kernel(I8View q, const int32_t* perm, const int32_t* status, uint4* x1
     const uint2 a = i8_to_f16x4(w.x), b = i8_to_f16x4(w.y), f = i8_to_f16x4(w.z), g = i8_to_f16x4(w.w);
     x16[2 * e] = make_uint4(a.x, a.y, b.x, b.y);
     x16[2 * e + 1] = make_uint4(f.x, f.y, g.x, g.y);
-    if (c == 0) scales[r] = __ldg(q.scales + from);
+    if (c == 0 && scales != nullptr) scales[r] = __ldg(q.scales + from);
 }
 
 // ---- read back ------------------------------------------------------------------------------------------
@@ -537,14 +537,24 @@ static int launch_sum_parts(float* s, int parts, size_t part, cudaStream_t st) {
     return LORA_OK;
 }
 
-// x in float16 codes and its scales: what a product of n rows keeps in its workspace.
-static size_t rows_bytes(int n, int h_in) { return n <= kI8Small ? 0 : align256((size_t)n * i8_pitch(h_in) * 2); }
-static size_t product_ws(int n, int h_in) { return n <= kI8Small ? 0 : rows_bytes(n, h_in) + align256((size_t)n * 4); }
+// What a product keeps in its workspace: x in float16 codes and its scales, and above kI8Tile rows the weight
+// in float16 codes.
+struct I8ProductWs {
+    size_t scales_off, w_off, total;
+};
+static I8ProductWs product_ws(int n, int h_out, int h_in) {
+    I8ProductWs L = {0, 0, 0};
+    if (n <= kI8Small) return L;
+    L.scales_off = align256((size_t)n * i8_pitch(h_in) * 2);
+    L.w_off = L.scales_off + align256((size_t)n * 4);
+    L.total = L.w_off + (n > kI8Tile ? align256((size_t)h_out * i8_pitch(h_in) * 2) : 0);
+    return L;
+}
 
 // Workspace of lora_i8_linear_fwd: the shrink output in its K parts, x's codes (in bytes for a few tokens,
-// else in float16) and scales.
+// else in float16) and scales, the weight in float16 codes.
 struct I8WsLayout {
-    size_t codes_off, scales_off, total;
+    size_t codes_off, scales_off, w_off, total;
 };
 static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     if (n < 0) return set_error(LORA_EINVAL, "n_tokens < 0");
@@ -555,8 +565,10 @@ static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     const long long m = std::max(n, 1);
     const long long rows = std::max(m, pv.dtype == LORA_F32 ? std::min(24 * m, 4LL * num_sms() * 64) : std::min(4 * m, 256LL));
     L->codes_off = align256((size_t)rows * pv.R * 4);
-    L->scales_off = L->codes_off + align256((size_t)n * i8_pitch(pv.h_in) * (n <= kI8Small ? 1 : 2));
-    L->total = L->scales_off + align256((size_t)n * 4);
+    const I8ProductWs P = product_ws(n, pv.h_out, pv.h_in);
+    L->scales_off = L->codes_off + (n <= kI8Small ? align256((size_t)n * i8_pitch(pv.h_in)) : P.scales_off);
+    L->w_off = L->scales_off + align256((size_t)n * 4);
+    L->total = L->w_off + P.total - P.w_off;
     return LORA_OK;
 }
 
@@ -643,7 +655,7 @@ int lora_i8_matmul_workspace_bytes(int x_rows, int w_rows, int cols, size_t* byt
     int rc = check_shape(x_rows, cols);
     if (!rc) rc = check_shape(w_rows, cols);
     if (rc) return rc;
-    *bytes = product_ws(x_rows, cols);
+    *bytes = product_ws(x_rows, w_rows, cols).total;
     return LORA_OK;
 }
 
@@ -655,20 +667,25 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
     if (x->cols != w->cols) return set_error(LORA_EINVAL, "x has %d columns, w %d", x->cols, w->cols);
     rc = check_rows(y_dev, dtype, ldy, w->rows ? x->rows : 0, w->rows, "y");
     if (rc || x->rows == 0 || w->rows == 0) return rc;
-    const size_t need = product_ws(x->rows, x->cols);
-    if (need && !ws_dev) return set_error(LORA_EINVAL, "ws is NULL");
+    const I8ProductWs L = product_ws(x->rows, w->rows, x->cols);
+    if (L.total && !ws_dev) return set_error(LORA_EINVAL, "ws is NULL");
     if (reinterpret_cast<uintptr_t>(ws_dev) % 256) return set_error(LORA_EINVAL, "ws must be 256-byte aligned");
-    if (ws_bytes < need) return set_error(LORA_ENOSPACE, "8-bit product workspace needs %zu bytes, got %zu", need, ws_bytes);
+    if (ws_bytes < L.total)
+        return set_error(LORA_ENOSPACE, "8-bit product workspace needs %zu bytes, got %zu", L.total, ws_bytes);
     const I8View xv = view_of(x), wv = view_of(w);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (x->rows <= kI8Small) return launch_i8_small(xv, wv, y_dev, dtype, ldy, nullptr, /*early_w=*/false, nullptr, st);
     char* ws = static_cast<char*>(ws_dev);
-    float* sx = reinterpret_cast<float*>(ws + rows_bytes(x->rows, x->cols));
+    float* sx = reinterpret_cast<float*>(ws + L.scales_off);
     rc = launch_i8_expand(xv, nullptr, nullptr, ws, sx, st);
     if (rc) return rc;
     const I8Rows rows = {ws, sx, nullptr, x->rows, x->cols};
-    return x->rows > kI8Tile ? launch_i8_pair(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st)
-                             : launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st);
+    if (x->rows <= kI8Tile)
+        return launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st);
+    rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
+    if (rc) return rc;
+    const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, w->rows, w->cols};
+    return launch_i8_pair(rows, wrows, y_dev, dtype, ldy, nullptr, /*release=*/false, nullptr, st);
 }
 
 int lora_i8_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes) {
@@ -740,8 +757,13 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
     const I8Lora lora = {&pv, sv.idx, s_buf, s_parts};
     if (few) return launch_i8_small(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     const I8Rows rows = {ws + L.codes_off, sx, sv.perm, n, pv.h_in};
-    if (n > kI8Tile)
-        return launch_i8_pair(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
+    if (n > kI8Tile) {
+        const I8View wv = view_of(w);
+        rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
+        if (rc) return rc;
+        const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, wv.rows, wv.cols};
+        return launch_i8_pair(rows, wrows, y_dev, pv.dtype, pv.h_out, sv.status, /*release=*/true, &lora, st);
+    }
     return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
 }
 

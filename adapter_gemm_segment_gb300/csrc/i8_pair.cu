@@ -1,17 +1,17 @@
 // Products of many tokens over an 8-bit weight: persistent tiles on CTA pairs (tcgen05 cta_group::2).
 //
-// As in i8_tile.cu codes are float16 operands, the weight goes through tensor memory (the MMA's A) and every
-// 1024 codes the accumulator is read into 32-bit integers, so sums are exact.  A pair of CTAs shares a tile of
-// 256 features x N tokens: each converts its own 128 features and stages half of the tokens, so that an SM
-// takes in 16 KB of codes and N/2 * 256 bytes of tokens a step of 128 along K, about 110 bytes a clock at the
-// tensor cores' rate, where a 128 x 128 tile by itself takes 190 and its port gives 128 (measured 37 % of the
-// rate).
+// As in i8_tile.cu codes are float16 operands and every 1024 codes the accumulator is read into 32-bit
+// integers, so sums are exact.  A pair of CTAs shares a tile of 256 features x N <= 256 tokens, each staging
+// half of both.  Here both operands come as float16: with hundreds of tokens the weight's 3 bytes a code of
+// extra traffic, once a call, cost less than converting it on the SM for every tile of tokens (through
+// tensor memory, as i8_tile.cu does: 8191 x 11008 x 4096 took 580 us, its MMAs alone 364; the thread that
+// issues them then waits for two more barriers and commits to two more every 64 codes).
 //
-// Tensor memory: two accumulators of N <= 192 columns, and four slots of 32 columns for 64 codes of the weight.
+// Tensor memory: two accumulators of N columns, so that the MMAs go on while one is read.
 //
-// Warps: 0 loads, 1 issues MMAs (even CTA), 2-5 convert, 6-13 drain the accumulator: lane <-> feature, every
-// second 16 tokens.  They add the LoRA term in float32 (tokens come in the order of the segments: neighbours
-// share their adapter's rows of B) and write y through shared memory while the MMAs are at the next tile.
+// Warps: 0 loads, 1 issues MMAs (even CTA), 2-9 drain the accumulator: lane <-> feature, every second 16
+// tokens.  They add the LoRA term in float32 (tokens come in the order of the segments: neighbours share
+// their adapter's rows of B) and write y through shared memory while the MMAs are at the next tile.
 #include <cuda.h>
 
 #include <algorithm>
@@ -30,15 +30,12 @@ namespace tc {
 using namespace ptx;
 
 constexpr int kJM = 128;           // features per CTA
-constexpr int kJMaxN = 192;        // tokens per pair tile, at most
-constexpr int kJThreads = 448;
-constexpr int kJChunk = 8;         // steps of 128 codes between two readings of the accumulator
+constexpr int kJMaxN = 256;        // tokens per pair tile, at most
+constexpr int kJThreads = 320;
+constexpr int kJChunk = 16;        // steps of 64 codes between two readings of the accumulator
 constexpr uint32_t kJWBytes = kJM * 128;
 constexpr int kJMaxStages = 8;
-constexpr int kJASlots = 4;
-constexpr int kJACol = 512 - 32 * kJASlots;
 constexpr int kJUnits = kJMaxN / 32;  // 16-token units of a drain warp, at most
-static_assert(2 * kJMaxN <= kJACol, "tensor memory");
 constexpr int kJStage = 16 * 33;      // floats a drain warp stages: 16 tokens x 32 features, rows padded
 constexpr size_t kJTail = 8 * kJStage * 4 + kJMaxN * 12 + 512 + 1024;
 constexpr size_t kJSmemMax = 227 * 1024;
@@ -50,7 +47,7 @@ struct I8PairArgs {
     const float* sx;
     const float* sw;
     long long ldy;
-    int n, N, h_out, m_tiles, n_tiles, nkb, stages, early, release, vec;
+    int n, N, h_out, m_tiles, n_tiles, nkb, stages, release, vec;
     // the LoRA term (FUSE)
     const SlotEntry* table;
     const void* B;
@@ -65,23 +62,20 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
     const int stages = a.stages, N = a.N;
-    const uint32_t x_half = static_cast<uint32_t>(N) * 64;      // N / 2 rows of 64 float16
-    const uint32_t stage_bytes = kJWBytes + 2 * x_half;
+    const uint32_t x_bytes = static_cast<uint32_t>(N) * 64;      // N / 2 rows of 64 float16
+    const uint32_t stage_bytes = kJWBytes + x_bytes;
     float* staged = reinterpret_cast<float*>(smem + stages * stage_bytes);  // [8 warps][16][33]
     int* row_sm = reinterpret_cast<int*>(staged + 8 * kJStage);  // [N] row of y of a token of the tile (-1: none)
     int* slot_sm = row_sm + kJMaxN;                              // [N] its adapter
     float* sx_sm = reinterpret_cast<float*>(slot_sm + kJMaxN);   // [N] its scale
-    uint64_t* full_w = reinterpret_cast<uint64_t*>(sx_sm + kJMaxN);  // own codes landed
-    uint64_t* full_x = full_w + kJMaxStages;   // even CTA: both halves of the tokens landed
-    uint64_t* empty = full_x + kJMaxStages;    // (multicast)
-    uint64_t* conv = empty + kJMaxStages;      // [4] even CTA: 64 codes are in tensor memory (4 warps of both CTAs)
-    uint64_t* a_free = conv + kJASlots;        // [4] (multicast)
-    uint64_t* acc_full = a_free + kJASlots;    // [2] (multicast)
+    uint64_t* full = reinterpret_cast<uint64_t*>(sx_sm + kJMaxN);  // even CTA: both CTAs' halves landed
+    uint64_t* empty = full + kJMaxStages;      // (multicast)
+    uint64_t* acc_full = empty + kJMaxStages;  // [2] (multicast)
     uint64_t* acc_empty = acc_full + 2;        // [2] even CTA (8 warps of both CTAs)
     uint64_t* drained = acc_empty + 2;         // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort
-    static_assert((3 * kJMaxStages + 2 * kJASlots + 5) * 8 + 8 <= 512, "barrier area");
+    static_assert((2 * kJMaxStages + 5) * 8 + 8 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -91,13 +85,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&full_w[s], 1);
-            mbar_init(&full_x[s], 1);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-        }
-        for (int s = 0; s < kJASlots; ++s) {
-            mbar_init(&conv[s], 8);
-            mbar_init(&a_free[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -126,25 +115,16 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // the tokens of few tiles and the whole weight
     if (warp == 0) {
         if (lane == 0) {
-            const uint32_t full_x0 = mapa_shared(smem_u32(full_x), 0);
+            const uint32_t full0 = mapa_shared(smem_u32(full), 0);
             auto load_w = [&](int s, int kb, int m0) {
-                mbar_arrive_expect_tx(&full_w[s], kJWBytes);
-                tma_load_2d_cta(smem + s * stage_bytes, &tmW, &full_w[s], kb * 128, m0 + static_cast<int>(rank) * kJM);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+                tma_load_2d_pair(smem + s * stage_bytes, &tmW, full0 + static_cast<uint32_t>(s) * 8u, kb * 64,
+                                 m0 + static_cast<int>(rank) * kJM);
             };
             auto load_x = [&](int s, int kb, int n0) {
-                uint8_t* dst = smem + s * stage_bytes + kJWBytes;
-                const uint32_t bar = full_x0 + static_cast<uint32_t>(s) * 8u;
-                const int r = n0 + static_cast<int>(rank) * (N / 2);
-                if (rank == 0) mbar_arrive_expect_tx(&full_x[s], 4 * x_half);
-                tma_load_2d_pair(dst, &tmX, bar, kb * 128, r);
-                tma_load_2d_pair(dst + x_half, &tmX, bar, kb * 128 + 64, r);
+                tma_load_2d_pair(smem + s * stage_bytes + kJWBytes, &tmX, full0 + static_cast<uint32_t>(s) * 8u, kb * 64,
+                                 n0 + static_cast<int>(rank) * (N / 2));
             };
-            // the first tile's weight goes out before the kernels ahead have finished
-            int pre = 0;
-            if (a.early >= 1 && pair < total) {
-                pre = min(stages, nkb);
-                for (int i = 0; i < pre; ++i) load_w(i, i, pair % a.m_tiles * 2 * kJM);
-            }
             pdl_wait();
             int it = 0, s = 0;
             uint32_t ph = 0;
@@ -152,7 +132,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const int m0 = tile % a.m_tiles * 2 * kJM, n0 = tile / a.m_tiles * N;
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     if (it >= stages && !mbar_wait(&empty[s], ph ^ 1, flags)) break;
-                    if (it >= pre) load_w(s, kb, m0);
+                    load_w(s, kb, m0);
                     load_x(s, kb, n0);
                     if (++s == stages) s = 0, ph ^= 1;
                 }
@@ -168,40 +148,30 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         if (lane == 0 && rank == 0) {
             const uint32_t idesc = idesc_f16(2 * kJM, N, false);
             bool ok = true;
-            int s = 0, slot = 0, chunk = 0;
-            uint32_t ph = 0, aph = 0;
+            int s = 0, chunk = 0;
+            uint32_t ph = 0;
             for (int tile = pair; tile < total && ok; tile += npairs) {
                 for (int kb = 0; kb < nkb && ok; ++chunk) {
                     const int buf = chunk & 1, end = min(nkb, kb + kJChunk);
                     const uint32_t acc = tmem + buf * N;
-                    if (chunk >= 2 && !mbar_wait_cluster(&acc_empty[buf], ((chunk >> 1) & 1) ^ 1, flags)) {
+                    if (chunk >= 2 && !mbar_wait(&acc_empty[buf], ((chunk >> 1) & 1) ^ 1, flags)) {
                         ok = false;
                         break;
                     }
+                    tc_fence_after();
                     uint32_t more = 0;
                     for (; kb < end; ++kb) {
-                        if (!mbar_wait(&full_x[s], ph, flags)) {
+                        if (!mbar_wait(&full[s], ph, flags)) {
                             ok = false;
                             break;
                         }
-                        const uint64_t xd = sdesc_sw128(smem_u32(smem + s * stage_bytes + kJWBytes));
+                        tc_fence_after();
+                        const uint64_t wd = sdesc_sw128(smem_u32(smem + s * stage_bytes)), xd = wd + (kJWBytes >> 4);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!mbar_wait_cluster(&conv[slot], aph, flags)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                            const uint32_t wa = tmem + kJACol + slot * 32;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                umma_pair_f16_ta(acc, wa + k * 8, xd + h * (x_half >> 4) + 2 * k, idesc, more);
-                                more = 1;
-                            }
-                            umma_pair_commit(&a_free[slot], 0x3);
-                            if (++slot == kJASlots) slot = 0, aph ^= 1;
+                        for (int k = 0; k < 4; ++k) {
+                            umma_pair_f16(acc, wd + 2 * k, xd + 2 * k, idesc, more);
+                            more = 1;
                         }
-                        if (!ok) break;
                         umma_pair_commit(&empty[s], 0x3);
                         if (++s == stages) s = 0, ph ^= 1;
                     }
@@ -215,52 +185,12 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kWaitLimitNs) {
             }
         }
-    } else if (warp < 6) {
-        // ---- codes to float16 in tensor memory: 32 features a warp, 64 codes at a time ----
-        const int q = warp & 3, row = q * 32 + lane;
-        const uint32_t conv0 = mapa_shared(smem_u32(conv), 0);
-        const uint32_t taddr = tmem + kJACol + (static_cast<uint32_t>(q * 32) << 16);
-        int s = 0, slot = 0;
-        uint32_t ph = 0, aph = 1;  // (the slots start free)
-        bool ok = true;
-        const int steps = (total - pair + npairs - 1) / npairs * nkb;
-        for (int i = 0; i < steps && ok; ++i) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&full_w[s], ph, flags));
-            if (!ok) break;
-            const uint8_t* wr = smem + s * stage_bytes + row * 128;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t r[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(wr + (((h * 4 + c) ^ (row & 7)) << 4));
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint2 f = i8_to_f16x4(w[e]);
-                        r[c * 8 + e * 2] = f.x;
-                        r[c * 8 + e * 2 + 1] = f.y;
-                    }
-                }
-                ok = __all_sync(0xffffffffu, mbar_wait(&a_free[slot], aph, flags));
-                if (!ok) break;
-                tc_fence_after();
-                tmem_st32(taddr + slot * 32, r);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(conv0 + static_cast<uint32_t>(slot) * 8u);
-                if (++slot == kJASlots) slot = 0, aph ^= 1;
-            }
-            if (++s == stages) s = 0, ph ^= 1;
-        }
-        if (!ok && a.status && lane == 0) report_timeout_status(a.status);
     } else {
         // ---- drain ----
-        const int q = warp & 3, hv = (warp - 6) >> 2, lt = threadIdx.x - 192;
+        const int q = warp & 3, hv = (warp - 2) >> 2, lt = threadIdx.x - 64;
         const int units = N / 16;
         const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
-        float* st = staged + (warp - 6) * kJStage;
+        float* st = staged + (warp - 2) * kJStage;
         pdl_wait();
         const bool store = !a.status || __ldcg(a.status) == LORA_OK;
         T* y = static_cast<T*>(a.y);
@@ -436,7 +366,7 @@ static int max_pairs() {
 }
 
 template <typename T, bool FUSE>
-static int launch_pair_t(const I8Rows& x, const I8View& w, void* y, long long ldy, int32_t* status, int early, bool release,
+static int launch_pair_t(const I8Rows& x, const I8Rows& w, void* y, long long ldy, int32_t* status, bool release,
                          const I8Lora* lora, cudaStream_t st) {
     static bool attr = false;
     if (!attr) {
@@ -455,14 +385,14 @@ static int launch_pair_t(const I8Rows& x, const I8View& w, void* y, long long ld
     a.n = x.rows;
     a.h_out = w.rows;
     a.m_tiles = (w.rows + 2 * kJM - 1) / (2 * kJM);
-    a.nkb = (int)((w.pitch + 127) / 128);
-    a.early = early;
+    const size_t pitch = i8_pitch(x.cols);
+    a.nkb = (int)((pitch + 63) / 64);
     a.release = release;
     a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     // tokens a tile: as few as fill the pairs' last round best
     const int pairs = max_pairs();
     long long best = LLONG_MAX;
-    for (int N = kJMaxN; N >= 96; N -= 16) {
+    for (int N = kJMaxN; N >= 96; N -= 32) {
         const long long tiles = (long long)a.m_tiles * ((x.rows + N - 1) / N), cost = (tiles + pairs - 1) / pairs * (N + 8);
         if (cost < best) best = cost, a.N = N;
     }
@@ -477,11 +407,11 @@ static int launch_pair_t(const I8Rows& x, const I8View& w, void* y, long long ld
         a.s = lora->s_in;
         a.R = pv.R;
     }
-    const size_t stage_bytes = kJWBytes + (size_t)a.N * 128;
+    const size_t stage_bytes = kJWBytes + (size_t)a.N * 64;
     a.stages = (int)std::min<size_t>((kJSmemMax - kJTail) / stage_bytes, kJMaxStages);
     CUtensorMap mW, mX;
-    int rc = make_map_fp4(&mW, w.codes, w.pitch, w.rows, kJM);  // (bytes in boxes of 128)
-    if (!rc) rc = make_map(&mX, x.x16, 0, w.pitch, x.rows, a.N / 2);
+    int rc = make_map(&mW, w.x16, 0, pitch, w.rows, kJM);
+    if (!rc) rc = make_map(&mX, x.x16, 0, pitch, x.rows, a.N / 2);
     if (rc) return rc;
     void* args[] = {(void*)&mW, (void*)&mX, (void*)&a};
     LORA_CUDA_TRY(launch_pdl((const void*)i8_pair_kernel<T, FUSE>, dim3(2 * (unsigned)std::min<long long>(tiles, pairs)),
@@ -491,18 +421,18 @@ static int launch_pair_t(const I8Rows& x, const I8View& w, void* y, long long ld
 
 }  // namespace tc
 
-int launch_i8_pair(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, int early,
+int launch_i8_pair(const I8Rows& x, const I8Rows& w, void* y, int dtype, long long ldy, int32_t* status,
                    bool release, const I8Lora* lora, cudaStream_t st) {
     switch (dtype) {
         case LORA_F32:
-            return lora ? tc::launch_pair_t<float, true>(x, w, y, ldy, status, early, release, lora, st)
-                        : tc::launch_pair_t<float, false>(x, w, y, ldy, status, early, release, nullptr, st);
+            return lora ? tc::launch_pair_t<float, true>(x, w, y, ldy, status, release, lora, st)
+                        : tc::launch_pair_t<float, false>(x, w, y, ldy, status, release, nullptr, st);
         case LORA_F16:
-            return lora ? tc::launch_pair_t<__half, true>(x, w, y, ldy, status, early, release, lora, st)
-                        : tc::launch_pair_t<__half, false>(x, w, y, ldy, status, early, release, nullptr, st);
+            return lora ? tc::launch_pair_t<__half, true>(x, w, y, ldy, status, release, lora, st)
+                        : tc::launch_pair_t<__half, false>(x, w, y, ldy, status, release, nullptr, st);
         default:
-            return lora ? tc::launch_pair_t<__nv_bfloat16, true>(x, w, y, ldy, status, early, release, lora, st)
-                        : tc::launch_pair_t<__nv_bfloat16, false>(x, w, y, ldy, status, early, release, nullptr, st);
+            return lora ? tc::launch_pair_t<__nv_bfloat16, true>(x, w, y, ldy, status, release, lora, st)
+                        : tc::launch_pair_t<__nv_bfloat16, false>(x, w, y, ldy, status, release, nullptr, st);
     }
 }
 
