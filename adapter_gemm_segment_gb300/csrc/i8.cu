@@ -520,23 +520,6 @@ constexpr int kI8Small = 8;
 // Above this many tokens the pair kernel.
 constexpr int kI8Tile = 256;
 
-// The K parts of the shrink output added up: the pair kernel reads each row many times.
-__global__ void __launch_bounds__(256)
-i8_sum_parts_kernel(float* s, int parts, size_t part) {
-    pdl_wait();
-    pdl_trigger();
-    const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= part) return;
-    float v = s[e];
-    for (int p = 1; p < parts; ++p) v += s[p * part + e];
-    s[e] = v;
-}
-static int launch_sum_parts(float* s, int parts, size_t part, cudaStream_t st) {
-    void* args[] = {(void*)&s, (void*)&parts, (void*)&part};
-    LORA_CUDA_TRY(launch_pdl((const void*)i8_sum_parts_kernel, dim3((unsigned)((part + 255) / 256)), dim3(256), 0, st, args));
-    return LORA_OK;
-}
-
 // What a product keeps in its workspace: x in float16 codes and its scales, and above kI8Tile rows the weight
 // in float16 codes.
 struct I8ProductWs {
@@ -749,11 +732,6 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         }
     }
     if (rc) return rc;
-    if (n > kI8Tile && s_parts > 1) {
-        rc = launch_sum_parts(s_buf, s_parts, (size_t)n * pv.R, st);
-        if (rc) return rc;
-        s_parts = 1;
-    }
     const I8Lora lora = {&pv, sv.idx, s_buf, s_parts};
     if (few) return launch_i8_small(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     const I8Rows rows = {ws + L.codes_off, sx, sv.perm, n, pv.h_in};
@@ -762,7 +740,9 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
         if (rc) return rc;
         const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, wv.rows, wv.cols};
-        return launch_i8_pair(rows, wrows, y_dev, pv.dtype, pv.h_out, sv.status, /*release=*/true, &lora, st);
+        rc = launch_i8_pair(rows, wrows, y_dev, pv.dtype, pv.h_out, sv.status, /*release=*/true, &lora, st);
+        if (rc || pv.dtype != LORA_F32) return rc;
+        return launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);
     }
     return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
 }

@@ -9,9 +9,16 @@
 //
 // Tensor memory: two accumulators of N columns, so that the MMAs go on while one is read.
 //
-// Warps: 0 loads, 1 issues MMAs (even CTA), 2-9 drain the accumulator: lane <-> feature, every second 16
-// tokens.  They add the LoRA term in float32 (tokens come in the order of the segments: neighbours share
-// their adapter's rows of B) and write y through shared memory while the MMAs are at the next tile.
+// The LoRA term is one more accumulator of a tile that meets adapters.  Tokens come in the order of the
+// segments, so a tile meets few: for its distinct adapters d, K columns d * r_max + j hold B_d[o, j] on the
+// feature side and s[t, j] on the token side (zero unless t uses d), kind::tf32, 8 columns a block.  B is a
+// tf32 number exactly; s goes in as two (22 bits), each multiplying the same B.  0 * inf would carry an
+// infinity or NaN of one tenant's B to the other tokens of the tile: such elements are replaced by zeros and
+// added to their own tokens by the warps that drain the accumulators.
+//
+// Warps: 0 loads, 1 issues MMAs (even CTA), 4-7 build LoRA blocks, 8-15 drain: lane <-> feature, every second
+// 16 tokens.  y is stored from the registers: the MMAs' operands arrive (64 KB every 512 clocks) and are read at
+// the rate of the shared-memory port, which would make staging there wait.
 #include <cuda.h>
 
 #include <algorithm>
@@ -19,6 +26,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "fp4_device.cuh"
 #include "i8_device.cuh"
 #include "kernels.h"
 #include "tc_ptx.cuh"
@@ -31,23 +39,27 @@ using namespace ptx;
 
 constexpr int kJM = 128;           // features per CTA
 constexpr int kJMaxN = 256;        // tokens per pair tile, at most
-constexpr int kJThreads = 320;
+constexpr int kJThreads = 512;
+// registers a thread of the warpgroups 0, 1 and 2-3: together what the block is launched with, 128 a thread
+constexpr int kJRegs0 = 56, kJRegs1 = 72, kJRegs2 = 192;
+static_assert(kJRegs0 + kJRegs1 + 2 * kJRegs2 == 4 * 128, "register split");
 constexpr int kJChunk = 16;        // steps of 64 codes between two readings of the accumulator
 constexpr uint32_t kJWBytes = kJM * 128;
 constexpr int kJMaxStages = 8;
 constexpr int kJUnits = kJMaxN / 32;  // 16-token units of a drain warp, at most
-constexpr int kJStage = 16 * 33;      // floats a drain warp stages: 16 tokens x 32 features, rows padded
-constexpr size_t kJTail = 8 * kJStage * 4 + kJMaxN * 12 + 512 + 1024;
+// a LoRA block: 8 columns of B for 128 features, then of s in two parts for N / 2 <= 128 tokens
+constexpr int kJLoraB = kJM * 32, kJLoraBytes = kJLoraB + 2 * (kJMaxN / 2) * 32;
+constexpr size_t kJTail = kJMaxN * 12 + 64 * 4 + 256 * 4 + 16 + 512 + 1024;
 constexpr size_t kJSmemMax = 227 * 1024;
 
 struct I8PairArgs {
     void* y;
     int32_t* status;       // nullable
-    const int32_t* perm;   // row of y of each row of x (nullable)
+    const int32_t* perm;   // row of y of each row of x (nullable without the LoRA term)
     const float* sx;
     const float* sw;
     long long ldy;
-    int n, N, h_out, m_tiles, n_tiles, nkb, stages, release, vec;
+    int n, N, h_out, m_tiles, n_tiles, nkb, stages, release, pairs;
     // the LoRA term (FUSE)
     const SlotEntry* table;
     const void* B;
@@ -56,26 +68,58 @@ struct I8PairArgs {
     int R;
 };
 
+// s = hi + lo to 2^-23 of itself, both tf32 numbers; an infinity or NaN stays in hi.
+__device__ __forceinline__ void split_tf32(float s, uint32_t& hi, uint32_t& lo) {
+    const uint32_t b = __float_as_uint(s);
+    if ((b & 0x7f800000u) == 0x7f800000u) {
+        hi = b;
+        lo = 0;
+        return;
+    }
+    hi = (b + 0x1000u) & 0xffffe000u;
+    if ((hi & 0x7f800000u) == 0x7f800000u) hi = b & 0xffffe000u;  // (it rounded up to an infinity)
+    lo = (__float_as_uint(s - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
+}
+
+// Sum over b times s of what the LoRA blocks leave out: b an infinity or a NaN.
+template <typename T> __device__ __noinline__ float bad_dot(const I8PairArgs& a, int slot, int row, int o, float acc) {
+    const T* b = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + o) * a.R;
+    for (int j = 0; j < a.table[slot].rank; ++j) {
+        const float f = to_f32<T>(b[j]);
+        if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) acc = fmaf(f, a.s[(size_t)row * a.R + j], acc);
+    }
+    return acc;
+}
+
 template <typename T, bool FUSE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kJThreads, 1)
 i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8PairArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
     const int stages = a.stages, N = a.N;
-    const uint32_t x_bytes = static_cast<uint32_t>(N) * 64;      // N / 2 rows of 64 float16
-    const uint32_t stage_bytes = kJWBytes + x_bytes;
-    float* staged = reinterpret_cast<float*>(smem + stages * stage_bytes);  // [8 warps][16][33]
-    int* row_sm = reinterpret_cast<int*>(staged + 8 * kJStage);  // [N] row of y of a token of the tile (-1: none)
+    const uint32_t stage_bytes = kJWBytes + static_cast<uint32_t>(N) * 64;  // 128 features, N / 2 tokens of 64 float16
+    uint8_t* lora_sm = smem + stages * stage_bytes;              // [2] blocks
+    int* row_sm = reinterpret_cast<int*>(lora_sm + (FUSE ? 2 * kJLoraBytes : 0));  // [N] row of y of a token of the tile
     int* slot_sm = row_sm + kJMaxN;                              // [N] its adapter
     float* sx_sm = reinterpret_cast<float*>(slot_sm + kJMaxN);   // [N] its scale
-    uint64_t* full = reinterpret_cast<uint64_t*>(sx_sm + kJMaxN);  // even CTA: both CTAs' halves landed
+    uint32_t* seen = reinterpret_cast<uint32_t*>(sx_sm + kJMaxN);  // [64] slots the tile's tokens name
+    int* dlist = reinterpret_cast<int*>(seen + 64);              // [256] in order
+    int* distinct = dlist + 256;                                 // [2] their number
+    uint64_t* full = reinterpret_cast<uint64_t*>(distinct + 4);  // even CTA: both CTAs' halves landed
     uint64_t* empty = full + kJMaxStages;      // (multicast)
     uint64_t* acc_full = empty + kJMaxStages;  // [2] (multicast)
     uint64_t* acc_empty = acc_full + 2;        // [2] even CTA (8 warps of both CTAs)
-    uint64_t* drained = acc_empty + 2;         // even CTA: every MMA has completed
+    uint64_t* lora_own = acc_empty + 2;        // [2] a LoRA block of this CTA is written (4 warps)
+    uint64_t* lora_peer = lora_own + 2;        // [2] even CTA: the odd CTA's block is written (relayed)
+    uint64_t* lora_empty = lora_peer + 2;      // [2] (multicast)
+    // by parity of the tile (the warps that build blocks may be a tile ahead of the others):
+    uint64_t* linfo = lora_empty + 2;          // [2] the tile's number of LoRA blocks is known
+    uint64_t* tile_done = linfo + 2;           // [2] it has been used (8 drain warps, the MMA or relay thread)
+    uint64_t* drained = tile_done + 2;         // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort
-    static_assert((2 * kJMaxStages + 5) * 8 + 8 <= 512, "barrier area");
+    // abort, -, then by parity of the tile: [2] LoRA blocks, [2] 1 + the last tile whose blocks left products out
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    static_assert((2 * kJMaxStages + 15) * 8 + 28 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -91,9 +135,14 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 16);
+            mbar_init(&lora_own[b], 4);
+            mbar_init(&lora_peer[b], 1);
+            mbar_init(&lora_empty[b], 1);
+            mbar_init(&linfo[b], 1);
+            mbar_init(&tile_done[b], 9);
         }
         mbar_init(drained, 1);
-        flags[0] = 0;
+        for (int i = 0; i < 6; ++i) flags[i] = 0;
         fence_barrier_init();
     }
     if (warp == 0 && lane == 0) {
@@ -113,27 +162,22 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
     // tile -> features 256 (tile % m_tiles).., tokens N (tile / m_tiles)..: the pairs at work at one time share
     // the tokens of few tiles and the whole weight
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        registers_down<kJRegs0>();
+        if (warp == 0 && lane == 0) {
             const uint32_t full0 = mapa_shared(smem_u32(full), 0);
-            auto load_w = [&](int s, int kb, int m0) {
-                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
-                tma_load_2d_pair(smem + s * stage_bytes, &tmW, full0 + static_cast<uint32_t>(s) * 8u, kb * 64,
-                                 m0 + static_cast<int>(rank) * kJM);
-            };
-            auto load_x = [&](int s, int kb, int n0) {
-                tma_load_2d_pair(smem + s * stage_bytes + kJWBytes, &tmX, full0 + static_cast<uint32_t>(s) * 8u, kb * 64,
-                                 n0 + static_cast<int>(rank) * (N / 2));
-            };
             pdl_wait();
             int it = 0, s = 0;
             uint32_t ph = 0;
             for (int tile = pair; tile < total && !flags[0]; tile += npairs) {
-                const int m0 = tile % a.m_tiles * 2 * kJM, n0 = tile / a.m_tiles * N;
+                const int m0 = tile % a.m_tiles * 2 * kJM + static_cast<int>(rank) * kJM;
+                const int n0 = tile / a.m_tiles * N + static_cast<int>(rank) * (N / 2);
                 for (int kb = 0; kb < nkb; ++kb, ++it) {
                     if (it >= stages && !mbar_wait(&empty[s], ph ^ 1, flags)) break;
-                    load_w(s, kb, m0);
-                    load_x(s, kb, n0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+                    const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
+                    tma_load_2d_pair(smem + s * stage_bytes, &tmW, bar, kb * 64, m0);
+                    tma_load_2d_pair(smem + s * stage_bytes + kJWBytes, &tmX, bar, kb * 64, n0);
                     if (++s == stages) s = 0, ph ^= 1;
                 }
             }
@@ -143,14 +187,12 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 while (globaltimer() - t0 < kWaitLimitNs / 8) {
                 }
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            const uint32_t idesc = idesc_f16(2 * kJM, N, false);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_f16(2 * kJM, N, false), idesc_lora = idesc_tf32(2 * kJM, N);
             bool ok = true;
-            int s = 0, chunk = 0;
+            int s = 0, chunk = 0, local = 0, lb = 0;
             uint32_t ph = 0;
-            for (int tile = pair; tile < total && ok; tile += npairs) {
+            for (int tile = pair; tile < total && ok; tile += npairs, ++local) {
                 for (int kb = 0; kb < nkb && ok; ++chunk) {
                     const int buf = chunk & 1, end = min(nkb, kb + kJChunk);
                     const uint32_t acc = tmem + buf * N;
@@ -177,6 +219,39 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     }
                     if (ok) umma_pair_commit(&acc_full[buf], 0x3);
                 }
+                if constexpr (FUSE) {
+                    if (!ok) break;
+                    if (!mbar_wait(&linfo[local & 1], (local >> 1) & 1, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    const int blocks = flags[2 + (local & 1)];
+                    mbar_arrive(&tile_done[local & 1]);
+                    if (blocks == 0) continue;
+                    const int buf = chunk & 1;
+                    if (chunk >= 2 && !mbar_wait(&acc_empty[buf], ((chunk >> 1) & 1) ^ 1, flags)) {
+                        ok = false;
+                        break;
+                    }
+                    ++chunk;
+                    for (int b = 0; b < blocks; ++b, ++lb) {
+                        const int lbuf = lb & 1;
+                        if (!mbar_wait(&lora_own[lbuf], (lb >> 1) & 1, flags) ||
+                            !mbar_wait_cluster(&lora_peer[lbuf], (lb >> 1) & 1, flags)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t ba = smem_u32(lora_sm + lbuf * kJLoraBytes), sa = ba + kJLoraB;
+                        const uint32_t half = static_cast<uint32_t>(N) * 16;  // a part of s: N / 2 tokens
+#pragma unroll
+                        for (uint32_t k = 0; k < 2; ++k)
+                            umma_pair_tf32(tmem + buf * N, sdesc_chunks(ba, kJM * 16), sdesc_chunks(sa + k * half, half / 2),
+                                           idesc_lora, (b > 0 || k > 0) ? 1u : 0u);
+                        umma_pair_commit(&lora_empty[lbuf], 0x3);
+                    }
+                    if (ok) umma_pair_commit(&acc_full[buf], 0x3);
+                }
             }
             if (!ok && a.status) report_timeout_status(a.status);
             // every MMA issued above has completed before the pair may tear down
@@ -184,32 +259,170 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             const unsigned long long t0 = globaltimer();
             while (!mbar_try_wait(drained, 0) && globaltimer() - t0 < kWaitLimitNs) {
             }
+        } else if (FUSE && warp == 1 && lane == 0) {
+            // odd CTA: tells the even one that a LoRA block is written.  (A release at cluster scope waits for every
+            // access of its thread: this thread's, not the writers'.)
+            const uint32_t peer0 = mapa_shared(smem_u32(lora_peer), 0);
+            int local = 0, lb = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total && ok; tile += npairs, ++local) {
+                ok = mbar_wait(&linfo[local & 1], (local >> 1) & 1, flags);
+                const int blocks = ok ? flags[2 + (local & 1)] : 0;
+                if (ok) mbar_arrive(&tile_done[local & 1]);
+                for (int b = 0; b < blocks && ok; ++b, ++lb) {
+                    ok = mbar_wait(&lora_own[lb & 1], (lb >> 1) & 1, flags);
+                    if (ok) mbar_arrive_cluster(peer0 + static_cast<uint32_t>(lb & 1) * 8u);
+                }
+            }
+            if (!ok && a.status) report_timeout_status(a.status);
+        }
+    } else if (warp < 8) {
+        registers_down<kJRegs1>();
+        if constexpr (FUSE) {
+            // ---- LoRA blocks: a feature of this CTA and a token of its half a thread ----
+            const int lt = threadIdx.x - 128;
+            pdl_wait();
+            const bool st_ok = !a.status || __ldcg(a.status) == LORA_OK;
+            const int chunks = a.R / 8;
+            int local = 0, lb = 0;
+            bool ok = true;
+            for (int tile = pair; tile < total; tile += npairs, ++local) {
+                const int n0 = tile / a.m_tiles * N;
+                // the slots of the tile's tokens: this thread's of its CTA's half, then of the other's
+                int slot[2], tok = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = n0 + static_cast<int>(rank ^ h) * (N / 2) + lt;
+                    slot[h] = -1;
+                    if (lt < N / 2 && r < a.n && st_ok) {
+                        const int t = __ldcg(a.perm + r);
+                        slot[h] = __ldcg(a.idx + t);
+                        if (h == 0) tok = t;
+                    }
+                }
+                const int own_rank = slot[0] >= 0 ? a.table[slot[0]].rank : 0;
+                if (lt < 64) seen[lt] = 0;
+                // this parity's count and flag, of the tile two before, have been used
+                if (local >= 2 && !mbar_wait(&tile_done[local & 1], ((local >> 1) & 1) ^ 1, flags)) ok = false;
+                if (!named_bar_and(4, 128, ok)) {  // all four warps leave together
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (slot[h] >= 0) atomicOr(&seen[slot[h] >> 5], 1u << (slot[h] & 31));
+                named_bar_sync(4, 128);
+                if (lt < 64) {
+                    int at = 0;
+                    for (int w = 0; w < lt; ++w) at += __popc(seen[w]);
+                    for (uint32_t m = seen[lt]; m; m &= m - 1) dlist[at++] = lt * 32 + __ffs(m) - 1;
+                    if (lt == 63) *distinct = at;
+                }
+                named_bar_sync(4, 128);
+                const int blocks = *distinct * chunks;
+                if (lt == 0) {
+                    flags[2 + (local & 1)] = blocks;
+                    mbar_arrive(&linfo[local & 1]);
+                }
+                const int o = tile % a.m_tiles * 2 * kJM + static_cast<int>(rank) * kJM + lt;
+                const float* srow = a.s + (size_t)tok * a.R;
+                const T* Bcol = static_cast<const T*>(a.B) + (size_t)o * a.R;
+                int d = 0, c = 0;  // the next block: columns 8c.. of adapter dlist[d]
+                struct Block {     // this thread's token and feature of a block
+                    float4 s[2];
+                    uint4 b;
+                } now, next;
+                auto load = [&](Block& v) {
+                    const int sl = dlist[d];
+                    const bool mine = sl == slot[0] && c * 8 < own_rank;
+                    const float4* sp = reinterpret_cast<const float4*>(srow + c * 8);
+                    v.s[0] = v.s[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (mine) v.s[0] = __ldcg(sp), v.s[1] = __ldcg(sp + 1);
+                    v.b = o < a.h_out ? __ldg(reinterpret_cast<const uint4*>(Bcol + (size_t)sl * a.h_out * a.R + c * 8))
+                                      : make_uint4(0, 0, 0, 0);
+                    // (columns past the rank: B's are zeros, s may not have been written)
+                    if (mine && c * 8 + 8 > own_rank) {
+                        float* f = reinterpret_cast<float*>(v.s);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c * 8 + e >= own_rank) f[e] = 0.f;
+                    }
+                    if (++c == chunks) c = 0, ++d;
+                };
+                if (blocks > 0) load(next);
+                for (int b = 0; b < blocks; ++b, ++lb) {
+                    now = next;
+                    if (b + 1 < blocks) load(next);  // a block ahead
+                    if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lb & 1], ((lb >> 1) & 1) ^ 1, flags))) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* blk = lora_sm + (lb & 1) * kJLoraBytes;
+                    if (nonfinite8<T>(now.b)) {
+                        now.b = finite8<T>(now.b);
+                        flags[4 + (local & 1)] = local + 1;
+                    }
+                    float bf[8];
+                    unpack8<T>(now.b, bf);
+                    uint4* fb = reinterpret_cast<uint4*>(blk + lt * 16);
+                    fb[0] = make_uint4(__float_as_uint(bf[0]), __float_as_uint(bf[1]), __float_as_uint(bf[2]), __float_as_uint(bf[3]));
+                    fb[kJM] = make_uint4(__float_as_uint(bf[4]), __float_as_uint(bf[5]), __float_as_uint(bf[6]), __float_as_uint(bf[7]));
+                    if (lt < N / 2) {
+                        const float f[8] = {now.s[0].x, now.s[0].y, now.s[0].z, now.s[0].w,
+                                            now.s[1].x, now.s[1].y, now.s[1].z, now.s[1].w};
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) split_tf32(f[e], hi[e], lo[e]);
+                        uint4* sb = reinterpret_cast<uint4*>(blk + kJLoraB + lt * 16);
+                        const int q = N / 2;  // rows of a chunk of 16 bytes
+                        sb[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        sb[q] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                        sb[2 * q] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        sb[3 * q] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                    }
+                    fence_proxy_async_smem();  // read by the tensor cores
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&lora_own[lb & 1]);
+                }
+                if (!ok) flags[0] = 1;
+            }
+            if (!ok && a.status && lane == 0) report_timeout_status(a.status);
         }
     } else {
+        registers_up<kJRegs2>();
         // ---- drain ----
-        const int q = warp & 3, hv = (warp - 2) >> 2, lt = threadIdx.x - 64;
+        const int q = warp & 3, hv = (warp - 8) >> 2, lt = threadIdx.x - 256;
         const int units = N / 16;
         const uint32_t acc_empty0 = mapa_shared(smem_u32(acc_empty), 0);
-        float* st = staged + (warp - 2) * kJStage;
         pdl_wait();
         const bool store = !a.status || __ldcg(a.status) == LORA_OK;
         T* y = static_cast<T*>(a.y);
-        int chunk = 0;
+        int chunk = 0, local = 0;
         bool ok = true;
-        for (int tile = pair; tile < total; tile += npairs) {
-            const int o0 = tile % a.m_tiles * 2 * kJM + static_cast<int>(rank) * kJM + q * 32, n0 = tile / a.m_tiles * N;
-            const int o = o0 + lane;
+        struct {
+            int row, slot;
+            float sx;
+        } next = {-1, -1, 0.f};
+        auto look_up = [&](int tile) {  // token lt of the tile
+            const int r = tile / a.m_tiles * N + lt;
+            const bool live = lt < N && r < a.n && store;
+            next.row = !live ? -1 : a.perm ? __ldcg(a.perm + r) : r;
+            next.sx = live ? __ldcg(a.sx + r) : 0.f;
+            if constexpr (FUSE) next.slot = live ? __ldcg(a.idx + next.row) : -1;
+        };
+        if (pair < total) look_up(pair);
+        for (int tile = pair; tile < total; tile += npairs, ++local) {
+            const int o = tile % a.m_tiles * 2 * kJM + static_cast<int>(rank) * kJM + q * 32 + lane;
             named_bar_sync(2, 256);  // the tile before is through with the tokens' rows
             if (lt < N) {
-                const int r = n0 + lt;
-                const bool live = r < a.n && store;
-                const int t = !live ? -1 : a.perm ? __ldcg(a.perm + r) : r;
-                row_sm[lt] = t;
-                sx_sm[lt] = live ? __ldcg(a.sx + r) : 0.f;
-                if constexpr (FUSE) slot_sm[lt] = live ? __ldcg(a.idx + t) : -1;
+                row_sm[lt] = next.row;
+                sx_sm[lt] = next.sx;
+                if constexpr (FUSE) slot_sm[lt] = next.slot;
             }
             const float sw = o < a.h_out ? __ldg(a.sw + o) : 0.f;
-            named_bar_sync(2, 256);
+            const bool lora = FUSE && !named_bar_and(2, 256, next.slot < 0);
+            if constexpr (!FUSE) named_bar_sync(2, 256);
+            if (tile + npairs < total) look_up(tile + npairs);
             int sum[kJUnits][16];
 #pragma unroll
             for (int i = 0; i < kJUnits; ++i)
@@ -237,96 +450,88 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0 + static_cast<uint32_t>(buf) * 8u);
             }
+            const int lbuf = chunk & 1;
+            bool left_out = false;
+            if (lora && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[lbuf], (chunk >> 1) & 1, flags));
+                ++chunk;
+                tc_fence_after();
+                left_out = flags[4 + (local & 1)] == local + 1;
+            }
             // all eight warps leave together
-            if (!named_bar_and(3, 256, ok)) break;
-            if (!store) continue;
+            if (!named_bar_and(3, 256, ok)) {
+                ok = false;
+                break;
+            }
+            const uint32_t laddr = tmem + lbuf * N + (static_cast<uint32_t>(q * 32) << 16);
 #pragma unroll 1
             for (int i = 0; i < kJUnits; ++i) {
                 const int u = 2 * i + hv;
-                if (u >= units) break;
-                __syncwarp();
+                if (u >= units || !store) break;
+                float v[16];
 #pragma unroll
                 for (int j = 0; j < kJUnits; ++j)
                     if (j == i)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) st[e * 33 + lane] = i8_scaled(sum[j][e], sx_sm[u * 16 + e], sw);
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 sx = *reinterpret_cast<const float4*>(sx_sm + u * 16 + e);
+                            v[e] = i8_scaled(sum[j][e], sx.x, sw);
+                            v[e + 1] = i8_scaled(sum[j][e + 1], sx.y, sw);
+                            v[e + 2] = i8_scaled(sum[j][e + 2], sx.z, sw);
+                            v[e + 3] = i8_scaled(sum[j][e + 3], sx.w, sw);
+                        }
                 if constexpr (FUSE) {
-                    const T* Bo = static_cast<const T*>(a.B) + (size_t)min(o, a.h_out - 1) * a.R;
-                    const size_t slot_elems = (size_t)a.h_out * a.R;
-#pragma unroll 1
-                    for (int e0 = 0; e0 < 16; e0 += 4) {
-                        int slot[4];
-                        const float* sp[4];
-                        bool same = true, any = false;
+                    if (lora) {
+                        uint32_t r[16];
+                        __syncwarp();
+                        tmem_ld16(laddr + u * 16, r);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int t = u * 16 + e0 + k;
-                            slot[k] = slot_sm[t];
-                            sp[k] = a.s + (size_t)max(row_sm[t], 0) * a.R;
-                            same = same && slot[k] == slot[0];
-                            any = any || slot[k] >= 0;
+                        for (int e = 0; e < 16; ++e) {
+                            float l = __uint_as_float(r[e]);
+                            if (left_out && slot_sm[u * 16 + e] >= 0 && o < a.h_out)
+                                l = bad_dot<T>(a, slot_sm[u * 16 + e], row_sm[u * 16 + e], o, l);
+                            v[e] += l;
                         }
-                        if (!any) continue;
-                        float acc[4] = {};
-                        if (same) {
-                            const T* b = Bo + slot[0] * slot_elems;
-                            const int jl = a.table[slot[0]].rank;  // columns past the rank are zeros
-                            for (int j = 0; j < jl; j += 8) {
-                                float bf[8];
-                                load_b8<T>(b, j, a.R, bf);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    float sv[8];
-                                    load_s8(sp[k], j, a.R, jl, sv);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) acc[k] = fmaf(bf[e], sv[e], acc[k]);
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (slot[k] < 0) continue;
-                                const T* b = Bo + slot[k] * slot_elems;
-                                const int jl = a.table[slot[k]].rank;
-                                for (int j = 0; j < jl; j += 8) {
-                                    float bf[8], sv[8];
-                                    load_b8<T>(b, j, a.R, bf);
-                                    load_s8(sp[k], j, a.R, jl, sv);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) acc[k] = fmaf(bf[e], sv[e], acc[k]);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) st[(e0 + k) * 33 + lane] += acc[k];
                     }
                 }
-                __syncwarp();
-                if (a.vec) {
-                    // 16 bytes a lane, neighbouring lanes a token's 32 features
-                    constexpr int per = 16 / sizeof(T), lanes = 32 / per;
-                    const int c = (lane % lanes) * per, col = o0 + c;
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int e0 = 0; e0 < 16; e0 += 32 / lanes) {
-                        const int e = e0 + lane / lanes, row = row_sm[u * 16 + e];
-                        alignas(16) T w[per];
-#pragma unroll
-                        for (int k = 0; k < per; ++k) w[k] = from_f32<T>(st[e * 33 + c + k]);
-                        if (row < 0) continue;
-                        T* yp = y + (long long)row * a.ldy + col;
-                        if (col + per <= a.h_out) {
-                            *reinterpret_cast<uint4*>(yp) = *reinterpret_cast<const uint4*>(w);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < per; ++k)
-                                if (col + k < a.h_out) yp[k] = w[k];
-                        }
-                    }
-                } else if (o < a.h_out) {
                     for (int e = 0; e < 16; ++e) {
                         const int row = row_sm[u * 16 + e];
-                        if (row >= 0) y[(long long)row * a.ldy + o] = from_f32<T>(st[e * 33 + lane]);
+                        if (row >= 0 && o < a.h_out) y[(long long)row * a.ldy + o] = v[e];
                     }
+                } else if (a.pairs) {
+                    // neighbouring lanes exchange a value: an even lane then has two features of one token, an odd one of
+                    // the next
+                    const bool odd = lane & 1;
+                    const int oe = o & ~1;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[e] : v[e + 1], 1);
+                        const uint32_t w = odd ? pack2<T>(other, v[e + 1]) : pack2<T>(v[e], other);
+                        const int row = row_sm[u * 16 + e + (odd ? 1 : 0)];
+                        if (row < 0) continue;
+                        T* yp = y + (long long)row * a.ldy + oe;
+                        if (oe + 1 < a.h_out)
+                            *reinterpret_cast<uint32_t*>(yp) = w;
+                        else if (oe < a.h_out)
+                            *reinterpret_cast<uint16_t*>(yp) = static_cast<uint16_t>(w);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int row = row_sm[u * 16 + e];
+                        if (row >= 0 && o < a.h_out) y[(long long)row * a.ldy + o] = from_f32<T>(v[e]);
+                    }
+                }
+            }
+            if constexpr (FUSE) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (lora) mbar_arrive_cluster_relaxed(acc_empty0 + static_cast<uint32_t>(lbuf) * 8u);
+                    mbar_arrive(&tile_done[local & 1]);
                 }
             }
         }
@@ -388,12 +593,12 @@ static int launch_pair_t(const I8Rows& x, const I8Rows& w, void* y, long long ld
     const size_t pitch = i8_pitch(x.cols);
     a.nkb = (int)((pitch + 63) / 64);
     a.release = release;
-    a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
-    // tokens a tile: as few as fill the pairs' last round best
+    a.pairs = reinterpret_cast<uintptr_t>(y) % 4 == 0 && ldy % 2 == 0;  // 16-bit y: two features at a time
+    // tokens a tile: what the rounds of all pairs take, with 48 tokens' time a tile for what does not shrink with it
     const int pairs = max_pairs();
     long long best = LLONG_MAX;
     for (int N = kJMaxN; N >= 96; N -= 32) {
-        const long long tiles = (long long)a.m_tiles * ((x.rows + N - 1) / N), cost = (tiles + pairs - 1) / pairs * (N + 8);
+        const long long tiles = (long long)a.m_tiles * ((x.rows + N - 1) / N), cost = (tiles + pairs - 1) / pairs * (N + 48);
         if (cost < best) best = cost, a.N = N;
     }
     a.n_tiles = (x.rows + a.N - 1) / a.N;
@@ -407,26 +612,24 @@ static int launch_pair_t(const I8Rows& x, const I8Rows& w, void* y, long long ld
         a.s = lora->s_in;
         a.R = pv.R;
     }
-    const size_t stage_bytes = kJWBytes + (size_t)a.N * 64;
-    a.stages = (int)std::min<size_t>((kJSmemMax - kJTail) / stage_bytes, kJMaxStages);
+    const size_t stage_bytes = kJWBytes + (size_t)a.N * 64, tail = kJTail + (FUSE ? 2 * kJLoraBytes : 0);
+    a.stages = (int)std::min<size_t>((kJSmemMax - tail) / stage_bytes, kJMaxStages);
     CUtensorMap mW, mX;
     int rc = make_map(&mW, w.x16, 0, pitch, w.rows, kJM);
     if (!rc) rc = make_map(&mX, x.x16, 0, pitch, x.rows, a.N / 2);
     if (rc) return rc;
     void* args[] = {(void*)&mW, (void*)&mX, (void*)&a};
     LORA_CUDA_TRY(launch_pdl((const void*)i8_pair_kernel<T, FUSE>, dim3(2 * (unsigned)std::min<long long>(tiles, pairs)),
-                             dim3(kJThreads), a.stages * stage_bytes + kJTail, st, args));
+                             dim3(kJThreads), a.stages * stage_bytes + tail, st, args));
     return LORA_OK;
 }
 
 }  // namespace tc
 
-int launch_i8_pair(const I8Rows& x, const I8Rows& w, void* y, int dtype, long long ldy, int32_t* status,
-                   bool release, const I8Lora* lora, cudaStream_t st) {
+int launch_i8_pair(const I8Rows& x, const I8Rows& w, void* y, int dtype, long long ldy, int32_t* status, bool release,
+                   const I8Lora* lora, cudaStream_t st) {
     switch (dtype) {
-        case LORA_F32:
-            return lora ? tc::launch_pair_t<float, true>(x, w, y, ldy, status, release, lora, st)
-                        : tc::launch_pair_t<float, false>(x, w, y, ldy, status, release, nullptr, st);
+        case LORA_F32: return tc::launch_pair_t<float, false>(x, w, y, ldy, status, release, nullptr, st);
         case LORA_F16:
             return lora ? tc::launch_pair_t<__half, true>(x, w, y, ldy, status, release, lora, st)
                         : tc::launch_pair_t<__half, false>(x, w, y, ldy, status, release, nullptr, st);

@@ -177,7 +177,8 @@ struct I8Rows {
 // a weight that a 16-bit linear streams unwaited).
 int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, int early,
                    bool release, const I8Lora* lora, cudaStream_t st);
-// The same for many tokens: the weight in float16 codes too, the shrink output in one part.
+// The same for many tokens: the weight in float16 codes too; 16-bit y: the shrink output in one part (float32:
+// without the LoRA term).
 int launch_i8_pair(const I8Rows& x, const I8Rows& w, void* y, int dtype, long long ldy, int32_t* status, bool release,
                    const I8Lora* lora, cudaStream_t st);
 // y = sx sw (Cx Cw^T) (+ the LoRA term), dtype, row stride ldy; y stays untouched unless *status
