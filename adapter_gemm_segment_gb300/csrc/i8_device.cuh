@@ -11,6 +11,50 @@ __device__ __forceinline__ float two_sum(float a, float b, float& e) {
     return s;
 }
 
+// Two float32 values, worked on by one instruction.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 two_sum2(F2 a, F2 b, F2& e) {
+    const F2 s = add2(a, b), bb = sub2(s, a);
+    e = add2(sub2(a, sub2(s, bb)), sub2(b, bb));
+    return s;
+}
+// The whole numbers nearest two values of at most 127.5 either way (ties to even): as floats, and as bits whose
+// lowest byte is the number (1.5 * 2^23 added: the sum's last bit is 1).
+__device__ __forceinline__ F2 nearest2(F2 v, uint32_t& a, uint32_t& b) {
+    const F2 magic = f2(12582912.f, 12582912.f), t = add2(v, magic);
+    const float2 u = unpack(t);
+    a = __float_as_uint(u.x);
+    b = __float_as_uint(u.y);
+    return sub2(t, magic);
+}
+
 // The scale of a row whose largest |x| is amax: the float32 nearest amax / 127.  A row that holds an
 // infinity or a NaN has a NaN scale.
 __device__ __forceinline__ float i8_scale(float amax) {
@@ -31,23 +75,23 @@ __device__ __forceinline__ I8Divisor i8_divisor(float s) {
     return d;
 }
 
-// The whole number nearest x / s, ties to the even one.  (x up) inv is off by at most 1.6e-5, so only
-// near the border of two codes does the sign of x - (k +- 1/2) s decide, which one fused multiply-add
-// gives exactly: the codes are those of the real quotient.
+// The whole number nearest x / s, ties to the even one, where x / s = k + rest is computed to 1.6e-5 (k nearest
+// to it) and lies next to the border of two codes: the sign of x - (k +- 1/2) s decides, which one fused
+// multiply-add gives exactly, so that the codes are those of the real quotient.
+__device__ __forceinline__ int i8_border(float x, float s, int k, float rest) {
+    const int side = rest > 0.f ? 1 : -1;
+    const float past = fmaf(-(static_cast<float>(k) + 0.5f * side), s, x) * static_cast<float>(side);
+    return past > 0.f || (past == 0.f && (k & 1) != 0) ? k + side : k;
+}
 __device__ __forceinline__ int i8_code(float x, const I8Divisor& d) {
-    const float xs = d.inv == 0.f ? 0.f : x * d.up;
-    const float v = xs * d.inv;
-    float k = rintf(v);
-    if (fabsf(v - k) > 0.4999f) {
-        const float side = v > k ? 1.f : -1.f;
-        const float past = side * fmaf(-(k + 0.5f * side), d.s, xs);
-        if (past > 0.f || (past == 0.f && (static_cast<int>(k) & 1) != 0)) k += side;
-    }
-    return static_cast<int>(fminf(fmaxf(k, -127.f), 127.f));
+    const float xs = d.inv == 0.f ? 0.f : x * d.up, v = xs * d.inv, k = rintf(v);
+    int c = static_cast<int>(k);
+    if (fabsf(v - k) > 0.4999f) c = i8_border(xs, d.s, c, v - k);
+    return min(max(c, -127), 127);
 }
 
-// Four codes in a word, the first in the lowest byte.
-__device__ __forceinline__ uint32_t i8_pack4(int a, int b, int c, int d) {
+// Four lowest bytes in a word, the first in its lowest.
+__device__ __forceinline__ uint32_t i8_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 

@@ -1,0 +1,687 @@
+// Rows of 8-bit integer matrices: quantisation, reading back, and the root-mean-square norm that writes its
+// output so.
+//
+// Stored form (lora.h): a row x becomes codes c and a scale s, s = max|x| / 127 rounded to float32 and c
+// the whole number nearest x / s (ties to even).  Codes are those of the real quotient, not of a rounded
+// one: a 16384 x 4096 batch has hundreds of elements whose float32 quotient rounds onto the border of two
+// codes (and where a bfloat16 row's largest value is even, one element in 200 lies that close), and with
+// them equal inputs would not give equal bytes on every path.
+//
+// Every kernel here moves its rows once and is bound by memory, below a few MB by the launch.
+#include <algorithm>
+#include <climits>
+#include <cstring>
+#include <type_traits>
+
+#include "common.cuh"
+#include "i8_device.cuh"
+#include "kernels.h"
+
+namespace lora {
+
+constexpr float kFltMax = 3.402823466e38f;
+constexpr int kRowThreads = 512;             // at most, a row
+constexpr size_t kRowSmem = 200 * 1024;      // a row is kept in shared memory up to this size
+
+// Eight elements of a row as they are in memory.
+template <typename T> struct Raw {
+    uint4 v;
+};
+template <> struct Raw<float> {
+    uint4 v, w;
+};
+template <typename T> __device__ __forceinline__ void to8(const Raw<T>& r, float (&f)[8]) { unpack8<T>(r.v, f); }
+template <> __device__ __forceinline__ void to8<float>(const Raw<float>& r, float (&f)[8]) {
+    f[0] = __uint_as_float(r.v.x), f[1] = __uint_as_float(r.v.y), f[2] = __uint_as_float(r.v.z), f[3] = __uint_as_float(r.v.w);
+    f[4] = __uint_as_float(r.w.x), f[5] = __uint_as_float(r.w.y), f[6] = __uint_as_float(r.w.z), f[7] = __uint_as_float(r.w.w);
+}
+// T(a + b): the sum of two 16-bit numbers rounded once.
+template <typename T> __device__ __forceinline__ uint32_t add_word(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t add_word<float>(uint32_t a, uint32_t b) {
+    return __float_as_uint(__fadd_rn(__uint_as_float(a), __uint_as_float(b)));
+}
+template <> __device__ __forceinline__ uint32_t add_word<__half>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t add_word<__nv_bfloat16>(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <typename T> __device__ __forceinline__ void add_raw(Raw<T>& a, const Raw<T>& b) {
+    a.v = make_uint4(add_word<T>(a.v.x, b.v.x), add_word<T>(a.v.y, b.v.y), add_word<T>(a.v.z, b.v.z), add_word<T>(a.v.w, b.v.w));
+    if constexpr (sizeof(T) == 4)
+        a.w = make_uint4(add_word<T>(a.w.x, b.w.x), add_word<T>(a.w.y, b.w.y), add_word<T>(a.w.z, b.w.z), add_word<T>(a.w.w, b.w.w));
+}
+
+// Vector i of the row's G threads is thread i % G's: with VEC elements 8 i .. + 7, moved 16 bytes at a time;
+// without (rows off 16-byte boundaries) element e is 8 (i - i % G) + e G + i % G, so that neighbouring threads
+// still touch neighbours.
+template <typename T, bool VEC> struct RowPart {
+    static __device__ __forceinline__ int at(int i, int e, int tid, int G) { return VEC ? 8 * i + e : 8 * (i - tid) + e * G + tid; }
+    // zeros past cols
+    static __device__ __forceinline__ Raw<T> load(const T* row, int cols, int i, int tid, int G) {
+        Raw<T> r;
+        const int k = at(i, 0, tid, G);
+        if (VEC && k + 8 <= cols) {
+            memcpy(&r.v, __builtin_assume_aligned(row + k, 16), 16);
+            if constexpr (sizeof(T) == 4) memcpy(&r.w, __builtin_assume_aligned(row + k + 4, 16), 16);
+        } else {
+            alignas(16) T v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = at(i, e, tid, G);
+                v[e] = j < cols ? row[j] : from_f32<T>(0.f);
+            }
+            memcpy(&r, v, sizeof(r));
+        }
+        return r;
+    }
+    static __device__ __forceinline__ void store(T* row, int cols, int i, int tid, int G, const Raw<T>& r) {
+        const int k = at(i, 0, tid, G);
+        if (VEC && k + 8 <= cols) {
+            *reinterpret_cast<uint4*>(row + k) = r.v;
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(row + k + 4) = r.w;
+        } else {
+            alignas(16) T v[8];
+            memcpy(v, &r, sizeof(r));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = at(i, e, tid, G);
+                if (j < cols) row[j] = v[e];
+            }
+        }
+    }
+    // codes (lowest bytes of c; 0 past cols, up to pitch)
+    static __device__ __forceinline__ void store_codes(int8_t* row, int pitch, int i, int tid, int G, const uint32_t (&c)[8]) {
+        const int k = at(i, 0, tid, G);
+        if (VEC) {
+            if (k < pitch)
+                *reinterpret_cast<uint2*>(row + k) =
+                    make_uint2(i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = at(i, e, tid, G);
+                if (j < pitch) row[j] = static_cast<int8_t>(c[e]);
+            }
+        }
+    }
+    // the same as float16
+    static __device__ __forceinline__ void store_codes(__half* row, int pitch, int i, int tid, int G, const uint32_t (&c)[8]) {
+        const int k = at(i, 0, tid, G);
+        if (VEC) {
+            const uint2 a = i8_to_f16x4(i8_pack4(c[0], c[1], c[2], c[3])), b = i8_to_f16x4(i8_pack4(c[4], c[5], c[6], c[7]));
+            if (k < pitch) *reinterpret_cast<uint4*>(row + k) = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = at(i, e, tid, G);
+                if (j < pitch) row[j] = __int2half_rn(static_cast<int8_t>(c[e]));
+            }
+        }
+    }
+};
+template <typename T> __device__ __forceinline__ Raw<T> from8(const float (&f)[8]) {
+    alignas(16) T v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = from_f32<T>(f[e]);
+    Raw<T> r;
+    memcpy(&r, v, sizeof(r));
+    return r;
+}
+
+// A row's place in a launch: G threads (a warp, several rows a CTA, or the CTA), its vectors, and whether they
+// are kept in shared memory between the two passes over the row (else the second reads them again).  Registers
+// would hold a quarter as many rows on an SM (16384 x 4096 bfloat16 quantised: 102 us).
+struct RowPlan {
+    int G, vecs, keep;
+};
+
+// The larger; a NaN wins.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+struct MaxPair {  // a largest |value| and what its float32 left off
+    float hi, lo;
+};
+__device__ __forceinline__ MaxPair max_pair(MaxPair a, MaxPair b) {
+    // NaN wins (comparisons with it are false)
+    const bool take = !(b.hi <= a.hi) || (b.hi == a.hi && b.lo > a.lo);
+    return a.hi != a.hi ? a : take ? b : a;
+}
+// ---- quantise ----------------------------------------------------------------------------------------
+// F16: codes as float16 into x16 [rows][pitch], row r from row perm[r] of x (see launch_i8_quantize_f16).
+// U: vectors whose loads are in flight together.
+template <typename T, int U, bool VEC, bool F16>
+__global__ void __launch_bounds__(kRowThreads)
+i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t* perm, const int32_t* status, __half* x16) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    __shared__ float red[kRowThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    using Part = RowPart<T, VEC>;
+    const int G = pl.G, team = threadIdx.x / G, tid = threadIdx.x - team * G;
+    const long long r = (long long)blockIdx.x * (blockDim.x / G) + team;
+    if (r >= q.rows) return;  // (whole warps; G is the CTA where it is more than a warp)
+    const T* row = x + r * ld;
+    if constexpr (F16) {
+        if (status != nullptr && __ldcg(status) != LORA_OK) return;  // (perm is not valid either)
+        if (perm != nullptr) row = x + (long long)__ldcg(perm + r) * ld;
+    }
+    Raw<T>* kept = reinterpret_cast<Raw<T>*>(row_smem) + (size_t)team * pl.vecs;
+    float m = 0.f;
+    for (int i0 = tid; i0 < pl.vecs; i0 += U * G) {
+        Raw<T> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * G < pl.vecs) v[u] = Part::load(row, q.cols, i0 + u * G, tid, G);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u * G >= pl.vecs) break;
+            if (pl.keep) kept[i0 + u * G] = v[u];
+            float f[8];
+            to8(v[u], f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[e]));
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (G > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+        __syncthreads();
+        for (int w = 0; w < G / 32; ++w) m = max_nan(m, red[w]);
+    }
+    const float s = i8_scale(m);
+    if (tid == 0) q.scales[r] = s;
+    const I8Divisor d = i8_divisor(s);
+    const bool plain = d.up == 1.f && d.inv != 0.f;
+    const int pitch = (int)q.pitch;
+#pragma unroll 2
+    for (int i = tid; i < pl.vecs; i += G) {
+        float f[8];
+        to8(pl.keep ? kept[i] : Part::load(row, q.cols, i, tid, G), f);
+        uint32_t c[8];
+        if (plain) {
+            float rest[8], far = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const F2 v = mul2(f2(f[e], f[e + 1]), f2(d.inv, d.inv));
+                const float2 t = unpack(sub2(v, nearest2(v, c[e], c[e + 1])));
+                rest[e] = t.x, rest[e + 1] = t.y;
+                far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
+            }
+            if (far > 0.4999f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (fabsf(rest[e]) > 0.4999f) c[e] = i8_border(f[e], d.s, static_cast<int8_t>(c[e]), rest[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] = i8_code(f[e], d);
+        }
+        if constexpr (F16)
+            Part::store_codes(x16 + r * pitch, pitch, i, tid, G, c);
+        else
+            Part::store_codes(q.codes + r * pitch, pitch, i, tid, G, c);
+    }
+}
+
+// Stored codes as float16, rows in the order of perm.  16 codes a thread; bound by memory.
+__global__ void __launch_bounds__(256)
+i8_expand_kernel(I8View q, const int32_t* perm, const int32_t* status, uint4* x16, float* scales) {
+    pdl_wait();
+    pdl_trigger();
+    if (status != nullptr && __ldcg(status) != LORA_OK) return;
+    const int per_row = (int)(q.pitch / 16);
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int r = (int)(e / per_row), c = (int)(e - (long long)r * per_row);
+    if (r >= q.rows) return;
+    const int from = perm ? __ldcg(perm + r) : r;
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(q.codes + (size_t)from * q.pitch) + c);
+    const uint2 a = i8_to_f16x4(w.x), b = i8_to_f16x4(w.y), f = i8_to_f16x4(w.z), g = i8_to_f16x4(w.w);
+    x16[2 * e] = make_uint4(a.x, a.y, b.x, b.y);
+    x16[2 * e + 1] = make_uint4(f.x, f.y, g.x, g.y);
+    if (c == 0 && scales != nullptr) scales[r] = __ldg(q.scales + from);
+}
+
+// ---- read back ------------------------------------------------------------------------------------------
+// Bound by memory.  VEC: 16 codes a thread and 16-byte stores; else an element a thread, neighbours side by
+// side.  No early release of the kernels behind: out may be the weight of a 16-bit linear, whose GEMM
+// streams it without waiting for more than its release.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+i8_dequantize_kernel(I8View q, T* __restrict__ out, long long ld) {
+    pdl_wait();
+    const long long r = (long long)blockIdx.y * 8 + threadIdx.x / 32 + (long long)blockIdx.z * 65535 * 8;
+    if (r >= q.rows) return;
+    const int lane = threadIdx.x & 31;
+    const float s = __ldg(q.scales + r);
+    const int8_t* codes = q.codes + r * q.pitch;
+    T* row = out + r * ld;
+    if constexpr (VEC) {
+        const int k = (blockIdx.x * 32 + lane) * 16;
+        if (k >= q.cols) return;
+        const int4 w = __ldcs(reinterpret_cast<const int4*>(codes + k));
+        const int words[4] = {w.x, w.y, w.z, w.w};
+        alignas(16) T v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = from_f32<T>(__int2float_rn((words[i / 4] << (24 - 8 * (i & 3))) >> 24) * s);
+        if (k + 16 <= q.cols) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i)
+                reinterpret_cast<uint4*>(row + k)[i] = reinterpret_cast<const uint4*>(v)[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (k + i < q.cols) row[k + i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int k = blockIdx.x * 512 + i * 32 + lane;
+            if (k < q.cols) row[k] = from_f32<T>(__int2float_rn(codes[k]) * s);
+        }
+    }
+}
+
+// ---- residual addition, root-mean-square norm, output in 8 bits -------------------------------------------
+// h = T(x + residual), r = 1 / sqrt(mean h^2 + eps), y = T(h r w), and the stored form of h r w.  The codes
+// have to be those of the real h r w / s, so what a whole row shares is held in two float32 parts: the sum
+// of squares (each square and each addition with its rounding error), r and r / s, to about 2^-44.  An
+// element then costs one product u = h w (exact in two parts) times r / s, and near the border of two codes
+// the second parts decide.
+struct NormArgs {
+    const void* x;
+    const void* residual;  // nullable
+    const void* w;
+    void* h;               // nullable: where x + residual goes
+    void* y;               // nullable
+    I8View q;              // codes nullable
+    long long ldx, ldr, ldh, ldy;
+    float eps;
+    int rows, cols;
+    RowPlan pl;
+};
+
+struct Two {
+    float hi, lo;
+};
+
+// What a row shares, from its sum of squares and largest |u| (of the row times f).
+struct NormRow {
+    float r, s;  // 1 / sqrt(mean + eps) / f, and the scale
+    float c;     // a power of two that keeps r / s in range
+    Two g;       // r / (s c); 0 where every code is 0
+};
+__device__ __forceinline__ NormRow norm_row(Two ss, MaxPair m, int cols, float eps, float f) {
+    NormRow o;
+    const float n = static_cast<float>(cols), q0 = __fdiv_rn(ss.hi, n);
+    const float q1 = (fmaf(-q0, n, ss.hi) + ss.lo) / n;
+    float err;
+    const float hi = two_sum(q0, eps * f * f, err), lo = err + q1;
+    const float r0 = rsqrtf(hi), p = __fmul_rn(r0, r0);
+    float e = fmaf(-hi, p, 1.f);
+    e = fmaf(-hi, fmaf(r0, r0, -p), e);
+    e = fmaf(-lo, p, e);
+    const Two r = {r0, hi <= kFltMax ? r0 * fmaf(0.375f * e, e, 0.5f * e) : 0.f};
+    o.r = r.hi + r.lo;
+    // s = max|u| r / 127
+    const float t = __fmul_rn(m.hi, r.hi);
+    const float tl = fmaf(m.hi, r.hi, -t) + fmaf(m.hi, r.lo, m.lo * r.hi);
+    const float s0 = __fdiv_rn(t, 127.f);
+    o.s = s0 + (fmaf(-127.f, s0, t) + tl) / 127.f;
+    if (!(m.hi <= kFltMax) || !(o.s <= kFltMax)) o.s = __uint_as_float(0x7fc00000u);
+    o.c = o.s < 1e-20f ? 18446744073709551616.f : 1.f;  // 2^64
+    o.g = Two{0.f, 0.f};
+    if (o.s > 0.f) {
+        const float sc = o.s * o.c;
+        o.g.hi = __fdiv_rn(r.hi, sc);
+        o.g.lo = (fmaf(-o.g.hi, sc, r.hi) + r.lo) / sc;
+    }
+    return o;
+}
+// The code of an element h f w whose quotient v = k + rest lies next to the border of two.
+template <bool EXACT>
+__device__ __forceinline__ int norm_border(float h, float w, float f, const NormRow& o, float v, int k) {
+    const float gh = h * f, u = __fmul_rn(gh, w), uc = u * o.c;
+    float rest = fmaf(uc, o.g.hi, -v) + uc * o.g.lo;
+    if (!EXACT) rest += fmaf(gh, w, -u) * o.c * o.g.hi;  // (16-bit numbers' products are exact)
+    const int side = v > static_cast<float>(k) ? 1 : -1;
+    const float past = side * ((v - (static_cast<float>(k) + 0.5f * side)) + rest);
+    return past > 0.f || (past == 0.f && (k & 1) != 0) ? k + side : k;
+}
+
+template <typename T, int U, bool VEC>
+__global__ void __launch_bounds__(kRowThreads)
+i8_rmsnorm_kernel(const NormArgs a) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    __shared__ __align__(16) float red[kRowThreads / 32][4];
+    pdl_wait();
+    pdl_trigger();
+    using Part = RowPart<T, VEC>;
+    constexpr bool EXACT = sizeof(T) == 2;  // squares and products of two 16-bit numbers are float32 numbers
+    const int G = a.pl.G, vecs = a.pl.vecs, team = threadIdx.x / G, tid = threadIdx.x - team * G, cols = a.cols;
+    const long long r = (long long)blockIdx.x * (blockDim.x / G) + team;
+    if (r >= a.rows) return;
+    const T* xr = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* rr = a.residual ? static_cast<const T*>(a.residual) + r * a.ldr : nullptr;
+    T* hr = a.h ? static_cast<T*>(a.h) + r * a.ldh : nullptr;
+    const T* wr = static_cast<const T*>(a.w);
+    Raw<T>* kept = reinterpret_cast<Raw<T>*>(row_smem) + (size_t)team * vecs;
+    // vector i of the sum on a later pass
+    auto again = [&](int i) -> Raw<T> {
+        if (a.pl.keep) return kept[i];
+        if (hr) return Part::load(hr, cols, i, tid, G);
+        return Part::load(xr, cols, i, tid, G);  // (without residual_out there is no residual)
+    };
+    // the row's threads' sums and maxima together
+    auto reduce = [&](Two& ss, MaxPair& m, bool second) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            float err;
+            const float oh = __shfl_xor_sync(0xffffffffu, ss.hi, d), ol = __shfl_xor_sync(0xffffffffu, ss.lo, d);
+            ss.hi = two_sum(ss.hi, oh, err);
+            ss.lo += ol + err;
+            if constexpr (EXACT)
+                m.hi = max_nan(m.hi, __shfl_xor_sync(0xffffffffu, m.hi, d));
+            else
+                m = max_pair(m, MaxPair{__shfl_xor_sync(0xffffffffu, m.hi, d), __shfl_xor_sync(0xffffffffu, m.lo, d)});
+        }
+        if (G > 32) {
+            if (second) __syncthreads();  // (the CTA is one row: all or none come here)
+            if ((threadIdx.x & 31) == 0)
+                *reinterpret_cast<float4*>(red[threadIdx.x >> 5]) = make_float4(ss.hi, ss.lo, m.hi, m.lo);
+            __syncthreads();
+            ss = Two{0.f, 0.f};
+            m = MaxPair{0.f, 0.f};
+#pragma unroll 1
+            for (int k = 0; k < G / 32; ++k) {
+                const float4 o = *reinterpret_cast<const float4*>(red[k]);
+                float err;
+                ss.hi = two_sum(ss.hi, o.x, err);
+                ss.lo += o.y + err;
+                m = max_pair(m, MaxPair{o.z, o.w});
+            }
+        }
+    };
+    F2 sh = f2(0.f, 0.f), sl = sh;
+    MaxPair m = {0.f, 0.f};
+    for (int i0 = tid; i0 < vecs; i0 += U * G) {
+        Raw<T> v[U], t[U], wv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * G < vecs) v[u] = Part::load(xr, cols, i0 + u * G, tid, G);
+        if (rr)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * G < vecs) t[u] = Part::load(rr, cols, i0 + u * G, tid, G);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u * G < vecs) wv[u] = Part::load(wr, cols, i0 + u * G, tid, G);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * G;
+            if (i >= vecs) break;
+            if (rr) add_raw(v[u], t[u]);
+            if (hr) Part::store(hr, cols, i, tid, G, v[u]);
+            if (a.pl.keep) kept[i] = v[u];
+            float h[8], w[8];
+            to8(v[u], h);
+            to8(wv[u], w);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const F2 g = f2(h[e], h[e + 1]), sq = mul2(g, g);
+                const float2 p = unpack(mul2(g, f2(w[e], w[e + 1])));
+                F2 err;
+                sh = two_sum2(sh, sq, err);
+                if constexpr (EXACT) {
+                    m.hi = max_nan(m.hi, max_nan(fabsf(p.x), fabsf(p.y)));
+                } else {
+                    const float2 q = unpack(sq);
+                    err = add2(err, f2(fmaf(h[e], h[e], -q.x), fmaf(h[e + 1], h[e + 1], -q.y)));
+                    const float lx = fmaf(h[e], w[e], -p.x), ly = fmaf(h[e + 1], w[e + 1], -p.y);
+                    m = max_pair(m, MaxPair{fabsf(p.x), p.x < 0.f ? -lx : lx});
+                    m = max_pair(m, MaxPair{fabsf(p.y), p.y < 0.f ? -ly : ly});
+                }
+                sl = add2(sl, err);
+            }
+        }
+    }
+    float f = 1.f;  // the row is taken times f
+    Two ss;
+    {
+        const float2 hi = unpack(sh), lo = unpack(sl);
+        float err;
+        ss.hi = two_sum(hi.x, hi.y, err);
+        ss.lo = lo.x + lo.y + err;
+    }
+    reduce(ss, m, false);
+    if (!(ss.hi <= 1e30f)) {
+        // squares that overflow float32 (elements from about 2^50 on) are taken of a smaller row
+        f = 7.888609052210118e-31f;  // 2^-100
+        ss = Two{0.f, 0.f};
+        m = MaxPair{0.f, 0.f};
+#pragma unroll 1
+        for (int i = tid; i < vecs; i += G) {
+            float h[8], w[8];
+            to8(again(i), h);
+            to8(Part::load(wr, cols, i, tid, G), w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float g = h[e] * f, sq = __fmul_rn(g, g), u = __fmul_rn(g, w[e]), l = fmaf(g, w[e], -u);
+                float err;
+                ss.hi = two_sum(ss.hi, sq, err);
+                ss.lo += err + fmaf(g, g, -sq);
+                m = max_pair(m, MaxPair{fabsf(u), EXACT ? 0.f : u < 0.f ? -l : l});
+            }
+        }
+        reduce(ss, m, true);
+    }
+    const NormRow o = norm_row(ss, m, cols, a.eps, f);
+    if (a.q.codes && tid == 0) a.q.scales[r] = o.s;
+    // both factors are 1 but for rows of enormous or of tiny elements
+    const F2 f22 = f2(f, f), g2 = f2(o.g.hi, o.g.hi), c2 = f2(o.c, o.c);
+    const bool plain = o.c == 1.f;
+#pragma unroll 2
+    for (int i = tid; i < vecs; i += G) {
+        float h[8], w[8];
+        to8(again(i), h);
+        to8(Part::load(wr, cols, i, tid, G), w);
+        F2 u[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = mul2(mul2(f2(h[2 * e], h[2 * e + 1]), f22), f2(w[2 * e], w[2 * e + 1]));
+        if (a.q.codes) {
+            uint32_t code[8];
+            float v[8], far = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const F2 q = mul2(mul2(u[e / 2], c2), g2);
+                const float2 t = unpack(sub2(q, nearest2(q, code[e], code[e + 1]))), vv = unpack(q);
+                v[e] = vv.x, v[e + 1] = vv.y;
+                far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
+            }
+            if (!(o.g.hi > 0.f)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) code[e] = 0;
+            } else if (far > 0.4999f || !plain) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // (a tiny scale is rounded coarsely: quotients may pass 127)
+                    int k = plain ? static_cast<int8_t>(code[e]) : static_cast<int>(fminf(fmaxf(rintf(v[e]), -127.f), 127.f));
+                    if (fabsf(v[e] - static_cast<float>(k)) > 0.4999f) k = norm_border<EXACT>(h[e], w[e], f, o, v[e], k);
+                    code[e] = min(max(k, -127), 127);
+                }
+            }
+            Part::store_codes(a.q.codes + r * a.q.pitch, (int)a.q.pitch, i, tid, G, code);
+        }
+        if (a.y) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 p = unpack(mul2(u[e], f2(o.r, o.r)));
+                y[2 * e] = p.x, y[2 * e + 1] = p.y;
+            }
+            Part::store(static_cast<T*>(a.y) + r * a.ldy, cols, i, tid, G, from8<T>(y));
+        }
+    }
+}
+
+static bool aligned16(const void* p, long long ld, int rows, size_t elt) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld * (long long)elt) % 16 == 0);
+}
+
+// Threads a row, vectors a thread loads at once (1 or 4), threads a CTA, shared memory.  Few rows: a thread a
+// vector, for the row's latency; many: four vectors a thread.
+struct RowLaunch {
+    RowPlan pl;
+    int U, threads;
+    unsigned blocks;
+    size_t smem;
+};
+static RowLaunch row_launch(int rows, int cols, size_t elt) {
+    RowLaunch l;
+    const int vecs = (int)(i8_pitch(cols) / 8);
+    l.U = rows <= 2 * num_sms() ? 1 : 4;
+    const int need = (vecs + l.U - 1) / l.U;
+    l.pl.G = std::min(kRowThreads, (need + 31) / 32 * 32);
+    // whole rounds of G, so that without VEC a round's 8 G elements are all some thread's
+    l.pl.vecs = (vecs + l.pl.G - 1) / l.pl.G * l.pl.G;
+    l.threads = l.pl.G > 32 ? l.pl.G : 256;
+    const int per = l.threads / l.pl.G;
+    l.blocks = (unsigned)(((long long)rows + per - 1) / per);
+    l.smem = (size_t)per * l.pl.vecs * 8 * elt;
+    l.pl.keep = l.smem <= kRowSmem;
+    if (!l.pl.keep) l.smem = 0;
+    return l;
+}
+template <typename K> static int allow_smem(K fn, bool& done) {
+    if (!done) {
+        LORA_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowSmem));
+        done = true;
+    }
+    return LORA_OK;
+}
+
+template <typename T, int U, bool VEC, bool F16>
+static int quantize_l(const T* x, long long ld, const I8View& q, const RowLaunch& l, const int32_t* perm,
+                      const int32_t* status, __half* x16, cudaStream_t st) {
+    static bool done = false;
+    const auto fn = i8_quantize_kernel<T, U, VEC, F16>;
+    const int rc = allow_smem(fn, done);
+    if (rc) return rc;
+    void* args[] = {(void*)&x, (void*)&ld, (void*)&q, (void*)&l.pl, (void*)&perm, (void*)&status, (void*)&x16};
+    LORA_CUDA_TRY(launch_pdl((const void*)fn, dim3(l.blocks), dim3(l.threads), l.smem, st, args));
+    return LORA_OK;
+}
+template <typename T, bool F16>
+static int quantize_t(const void* x, long long ld, const I8View& q, const int32_t* perm, const int32_t* status, void* x16,
+                      cudaStream_t st) {
+    const bool vec = aligned16(x, ld, q.rows, sizeof(T));
+    const RowLaunch l = row_launch(q.rows, q.cols, sizeof(T));
+    const T* xp = static_cast<const T*>(x);
+    __half* hp = static_cast<__half*>(x16);
+    if (l.U == 1)
+        return vec ? quantize_l<T, 1, true, F16>(xp, ld, q, l, perm, status, hp, st)
+                   : quantize_l<T, 1, false, F16>(xp, ld, q, l, perm, status, hp, st);
+    return vec ? quantize_l<T, 4, true, F16>(xp, ld, q, l, perm, status, hp, st)
+               : quantize_l<T, 4, false, F16>(xp, ld, q, l, perm, status, hp, st);
+}
+
+int launch_i8_quantize(const void* x, int dtype, long long ld, const I8View& q, cudaStream_t st) {
+    if (q.rows == 0) return LORA_OK;
+    switch (dtype) {
+        case LORA_F32: return quantize_t<float, false>(x, ld, q, nullptr, nullptr, nullptr, st);
+        case LORA_F16: return quantize_t<__half, false>(x, ld, q, nullptr, nullptr, nullptr, st);
+        default: return quantize_t<__nv_bfloat16, false>(x, ld, q, nullptr, nullptr, nullptr, st);
+    }
+}
+
+int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const int32_t* perm, const int32_t* status,
+                           void* x16, float* scales, cudaStream_t st) {
+    const I8View q = i8_view(nullptr, scales, rows, cols);
+    switch (dtype) {
+        case LORA_F32: return quantize_t<float, true>(x, cols, q, perm, status, x16, st);
+        case LORA_F16: return quantize_t<__half, true>(x, cols, q, perm, status, x16, st);
+        default: return quantize_t<__nv_bfloat16, true>(x, cols, q, perm, status, x16, st);
+    }
+}
+
+int launch_i8_expand(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales, cudaStream_t st) {
+    const long long chunks = (long long)x.rows * (long long)(x.pitch / 16);
+    uint4* out = static_cast<uint4*>(x16);
+    void* args[] = {(void*)&x, (void*)&perm, (void*)&status, (void*)&out, (void*)&scales};
+    if (chunks > 256LL * INT_MAX) return set_error(LORA_EUNSUP, "8-bit matrix of %d rows", x.rows);
+    LORA_CUDA_TRY(launch_pdl((const void*)i8_expand_kernel, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, st, args));
+    return LORA_OK;
+}
+
+template <typename T>
+static int dequantize_t(const I8View& q, void* out, long long ld, cudaStream_t st) {
+    T* op = static_cast<T*>(out);
+    void* args[] = {(void*)&q, (void*)&op, (void*)&ld};
+    const void* fn = aligned16(out, ld, q.rows, sizeof(T)) ? (const void*)i8_dequantize_kernel<T, true>
+                                                           : (const void*)i8_dequantize_kernel<T, false>;
+    const unsigned groups = (unsigned)(((long long)q.rows + 7) / 8);
+    const dim3 grid((q.cols + 511) / 512, std::min(groups, 65535u), (groups + 65534u) / 65535u);
+    LORA_CUDA_TRY(launch_pdl(fn, grid, dim3(256), 0, st, args));
+    return LORA_OK;
+}
+
+int launch_i8_dequantize(const I8View& q, void* out, int dtype, long long ld, cudaStream_t st) {
+    switch (dtype) {
+        case LORA_F32: return dequantize_t<float>(q, out, ld, st);
+        case LORA_F16: return dequantize_t<__half>(q, out, ld, st);
+        default: return dequantize_t<__nv_bfloat16>(q, out, ld, st);
+    }
+}
+
+template <typename T, int U, bool VEC> static int rmsnorm_l(const NormArgs& a, const RowLaunch& l, cudaStream_t st) {
+    static bool done = false;
+    const auto fn = i8_rmsnorm_kernel<T, U, VEC>;
+    const int rc = allow_smem(fn, done);
+    if (rc) return rc;
+    void* args[] = {(void*)&a};
+    LORA_CUDA_TRY(launch_pdl((const void*)fn, dim3(l.blocks), dim3(l.threads), l.smem, st, args));
+    return LORA_OK;
+}
+template <typename T> static int rmsnorm_t(NormArgs a, cudaStream_t st) {
+    const bool vec = aligned16(a.x, a.ldx, a.rows, sizeof(T)) && aligned16(a.residual, a.ldr, a.rows, sizeof(T)) &&
+                     aligned16(a.h, a.ldh, a.rows, sizeof(T)) && aligned16(a.y, a.ldy, a.rows, sizeof(T)) &&
+                     aligned16(a.w, 0, 1, sizeof(T));
+    const RowLaunch l = row_launch(a.rows, a.cols, sizeof(T));
+    a.pl = l.pl;
+    if (l.U == 1) return vec ? rmsnorm_l<T, 1, true>(a, l, st) : rmsnorm_l<T, 1, false>(a, l, st);
+    return vec ? rmsnorm_l<T, 4, true>(a, l, st) : rmsnorm_l<T, 4, false>(a, l, st);
+}
+
+int launch_i8_rmsnorm(const lora_i8_norm& p, cudaStream_t st) {
+    NormArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = p.x_dev;
+    a.residual = p.residual_dev;
+    a.w = p.weight_dev;
+    a.h = p.residual_out_dev;
+    a.y = p.y_dev;
+    if (p.out) a.q = i8_view(p.out->codes_dev, p.out->scales_dev, p.out->rows, p.out->cols);
+    a.ldx = p.ldx;
+    a.ldr = p.ldr;
+    a.ldh = p.ldro;
+    a.ldy = p.ldy;
+    a.eps = p.eps;
+    a.rows = p.rows;
+    a.cols = p.cols;
+    switch (p.dtype) {
+        case LORA_F32: return rmsnorm_t<float>(a, st);
+        case LORA_F16: return rmsnorm_t<__half>(a, st);
+        default: return rmsnorm_t<__nv_bfloat16>(a, st);
+    }
+}
+
+}  // namespace lora

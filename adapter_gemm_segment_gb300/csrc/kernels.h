@@ -152,6 +152,8 @@ inline I8View i8_view(void* codes, void* scales, int rows, int cols) {
     return I8View{static_cast<int8_t*>(codes), static_cast<float*>(scales), rows, cols, i8_pitch(cols)};
 }
 int launch_i8_quantize(const void* x, int dtype, long long ld, const I8View& q, cudaStream_t st);
+int launch_i8_dequantize(const I8View& q, void* out, int dtype, long long ld, cudaStream_t st);
+int launch_i8_rmsnorm(const lora_i8_norm& args, cudaStream_t st);
 // Codes as float16 [rows][pitch] (whole numbers, which it holds exactly) with their scales: what the
 // tensor-core products take x in.  Row r is row perm[r] of x (nullptr: r); untouched unless *status
 // (nullable) is LORA_OK.  From x itself, quantised, or from its stored form.
