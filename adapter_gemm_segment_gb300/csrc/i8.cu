@@ -170,7 +170,7 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
     if (rc) return rc;
     const I8Rows rows = {ws, sx, nullptr, x->rows, x->cols};
     if (x->rows <= kI8Tile)
-        return launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early=*/1, /*release=*/false, nullptr, st);
+        return launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early_x=*/false, /*release=*/false, nullptr, st);
     rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
     if (rc) return rc;
     const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, w->rows, w->cols};
@@ -250,7 +250,7 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         if (rc || pv.dtype != LORA_F32) return rc;
         return launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);
     }
-    return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early=*/2, /*release=*/true, &lora, st);
+    return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_x=*/true, /*release=*/true, &lora, st);
 }
 
 }  // extern "C"

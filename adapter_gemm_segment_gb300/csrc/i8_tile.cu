@@ -6,14 +6,17 @@
 // started again.
 //
 // The weight is the MMA's M side (128 features a tile) and up to 128 tokens its N side.  The weight stays
-// in bytes until it is on the SM: TMA brings 128 x 128 codes, eight warps turn them into float16 and store
+// in bytes until it is on the SM: TMA brings 128 x 128 codes, sixteen warps turn them into float16 and store
 // them to tensor memory as the MMA's A operand (tcgen05.st), so float16 weights never pass through shared
-// memory.  K is split over the CTAs of a thread-block cluster until the grid fills the GPU; the split sums
-// (integers: any order gives the same) meet in shared memory, each CTA finishing its share of the tokens.
+// memory.  A warp's turn (waits, loads, conversion, store) takes about 900 clocks for 32 features x 64 codes,
+// a step of 128 codes from HBM 700: eight warps would not keep up.
 //
-// The LoRA term is added there in float32: y[t, o] = sx sw sum + s[t, :] . B[o, :].  The warps that drain
-// the accumulator are idle during the main loop, and compute it then for the tokens their CTA will finish.
-// Tokens come in the order of the segments, so neighbouring tokens share their adapter's rows of B.
+// K is split over the CTAs of a thread-block cluster until the grid fills the GPU; each CTA finishes a share of
+// the tokens, into whose shared memory the others store their sums (integers: any order gives the same).
+//
+// The LoRA term is added there in float32: y[t, o] = sx sw sum + s[t, :] . B[o, :].  Eight more warps compute it
+// during the main loop for the tokens their CTA will finish.  Tokens come in the order of the segments, so
+// neighbouring tokens share their adapter's rows of B.
 #include <cuda.h>
 
 #include <algorithm>
@@ -35,12 +38,14 @@ constexpr int kIM = 128;          // features per tile
 constexpr int kIN = 128;          // tokens per tile, at most
 constexpr int kIK = 128;          // codes of a step along K
 constexpr int kIChunk = 8;        // steps between two readings of the accumulator: 1024 codes
-constexpr int kIThreads = 576;    // warp 0 loads, 1 MMAs, 2-9 convert, 10-17 LoRA term and accumulator
-constexpr int kIASlots = 4;       // at most: steps of the weight in tensor memory, 64 columns each
+constexpr int kIWorkers = 16;     // warps 2-17: convert (half of them the even steps, half the odd), drain
+constexpr int kIThreads = 64 + 32 * kIWorkers;  // warp 0 loads, 1 MMAs
+constexpr int kILora = 256;       // more threads for the LoRA term
+constexpr int kIASlots = 4;       // steps of the weight in tensor memory, 64 columns each
 constexpr int kIACol = 2 * kIN;   // behind two accumulators
-constexpr int kISRanks = 32;      // columns of the shrink output staged at once
+constexpr int kISRanks = 16;      // columns of the shrink output staged at once
 constexpr uint32_t kIWBytes = kIM * kIK;
-constexpr int kIBars = 512;
+constexpr int kIBars = 384;
 
 struct I8TileArgs {
     void* y;
@@ -49,7 +54,7 @@ struct I8TileArgs {
     const float* sx;
     const float* sw;
     long long ldy;
-    int n, n_pad, h_out, kb_total, kb_per_split, splits, stages, aslots, early, release, vec, ring_bytes, push, per;
+    int n, n_pad, h_out, kb_total, kb_per_split, splits, wstages, xstages, early_x, release, vec, ring_bytes, per, per_inv;
     // the LoRA term (FUSE)
     const SlotEntry* table;
     const void* B;
@@ -59,68 +64,81 @@ struct I8TileArgs {
 };
 
 template <typename T, bool FUSE>
-__global__ void __launch_bounds__(kIThreads, 1)
+__global__ void __launch_bounds__(kIThreads + (FUSE ? kILora : 0), 1)
 i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8TileArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align(smem_raw, 1024);
-    const int stages = a.stages, aslots = a.aslots, n_pad = a.n_pad;
+    // stages of the weight's codes, which the warps that convert them free, and of the tokens', which the MMAs free
+    const int ws = a.wstages, xs = a.xstages, n_pad = a.n_pad;
     const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 256;  // two boxes of 64 float16 columns
-    const uint32_t stage_bytes = kIWBytes + x_bytes;
-    float* L = reinterpret_cast<float*>(smem + a.ring_bytes);            // FUSE: [per][128] LoRA terms
-    float* S = L + (FUSE ? a.per * kIM : 0);                             // FUSE: [per][kISRanks] shrink output
-    int* tok_slot = reinterpret_cast<int*>(S + (FUSE ? a.per * kISRanks : 0));  // FUSE: [per]
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_align(reinterpret_cast<uint8_t*>(tok_slot + (FUSE ? a.per : 0)), 8));
-    uint64_t* empty = full + stages;
-    uint64_t* conv = empty + stages;          // [kIASlots] the step's weight is in tensor memory (8 warps)
-    uint64_t* acc_full = conv + kIASlots;     // [2]
-    uint64_t* acc_empty = acc_full + 2;       // [2] (8 warps)
-    uint64_t* rbar = acc_empty + 2;           // the other CTAs' sums of this CTA's tokens have arrived
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rbar + 1);
-    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort
-    int* P = reinterpret_cast<int*>(smem);    // after the main loop: [n_pad][128] sums of this CTA's part of K
+    uint8_t* xring = smem + ws * kIWBytes;
+    // sums of the tokens this CTA finishes, from each CTA of the cluster [splits][per][128]; of a CTA by itself, in
+    // the ring once that is idle
+    int* G = reinterpret_cast<int*>(smem + (a.splits > 1 ? a.ring_bytes : 0));
+    float* L = reinterpret_cast<float*>(smem + a.ring_bytes) + (a.splits > 1 ? a.splits * a.per * kIM : 0);  // FUSE: [per][128] their LoRA terms
+    float* S = L + (FUSE ? a.per * kIM : 0);                      // FUSE: [per][kISRanks] shrink output
+    int* tok_slot = reinterpret_cast<int*>(S + (FUSE ? a.per * kISRanks : 0));  // FUSE: [per] slots of the CTA's tokens,
+    int* row_sm = tok_slot + (FUSE ? a.per : 0);                 // [per] their rows of y,
+    float* sx_sm = reinterpret_cast<float*>(row_sm + a.per);     // [per] and scales
+    float* sw_sm = sx_sm + a.per;                                // [128]
+    uint64_t* full_w = reinterpret_cast<uint64_t*>(smem_align(reinterpret_cast<uint8_t*>(sw_sm + kIM), 8));  // [8]
+    uint64_t* empty_w = full_w + 8;           // [8] (8 of the warps)
+    uint64_t* full_x = empty_w + 8;           // [4]
+    uint64_t* empty_x = full_x + 4;           // [4]
+    uint64_t* conv = empty_x + 4;             // [kIASlots] the step's weight is in tensor memory (8 of the warps)
+    uint64_t* a_free = conv + kIASlots;       // [kIASlots] the slot's MMAs have completed
+    uint64_t* acc_full = a_free + kIASlots;   // [2]
+    uint64_t* acc_empty = acc_full + 2;       // [2] (16 warps)
+    uint64_t* drained = acc_empty + 2;        // (after an abort) every MMA has completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort; a CTA of the cluster has aborted
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m_tile = blockIdx.x, split = blockIdx.y, row0 = blockIdx.z * kIN;
-    const int n = min(a.n - row0, kIN);
+    const int m_tile = blockIdx.x, split = blockIdx.y, row0 = blockIdx.z * a.n_pad;
+    const int n = min(a.n - row0, a.n_pad);
     const int kb0 = split * a.kb_per_split;
     const int nkb = min(a.kb_total, kb0 + a.kb_per_split) - kb0;
     const int nchunks = (nkb + kIChunk - 1) / kIChunk;
     // the tokens this CTA finishes
     const int t0 = min(n, split * a.per), cnt = min(n, t0 + a.per) - t0;
 
-    auto issue_w = [&](int i) {
-        const int s = i % stages;
-        mbar_arrive_expect_tx(&full[s], stage_bytes);
-        tma_load_2d_cta(smem + (size_t)s * stage_bytes, &tmW, &full[s], (kb0 + i) * kIK, m_tile * kIM);
+    auto issue_w = [&](int i, int st) {
+        mbar_arrive_expect_tx(&full_w[st], kIWBytes);
+        tma_load_2d_cta(smem + st * kIWBytes, &tmW, &full_w[st], (kb0 + i) * kIK, m_tile * kIM);
     };
-    auto issue_x = [&](int i) {
-        const int s = i % stages;
-        uint8_t* dst = smem + (size_t)s * stage_bytes + kIWBytes;
-        tma_load_2d_cta(dst, &tmX, &full[s], (kb0 + i) * kIK, row0);
-        tma_load_2d_cta(dst + n_pad * 128, &tmX, &full[s], (kb0 + i) * kIK + 64, row0);
+    auto issue_x = [&](int i, int st) {
+        uint8_t* dst = xring + st * x_bytes;
+        mbar_arrive_expect_tx(&full_x[st], x_bytes);
+        tma_load_2d_cta(dst, &tmX, &full_x[st], (kb0 + i) * kIK, row0);
+        tma_load_2d_cta(dst + n_pad * 128, &tmX, &full_x[st], (kb0 + i) * kIK + 64, row0);
     };
-    const int pre = min(stages, nkb);
+    const int pre_w = min(ws, nkb), pre_x = min(xs, nkb);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+        for (int i = 0; i < ws; ++i) {
+            mbar_init(&full_w[i], 1);
+            mbar_init(&empty_w[i], 8);
         }
-        for (int s = 0; s < kIASlots; ++s) mbar_init(&conv[s], 8);
+        for (int i = 0; i < xs; ++i) {
+            mbar_init(&full_x[i], 1);
+            mbar_init(&empty_x[i], 1);
+        }
+        for (int i = 0; i < kIASlots; ++i) {
+            mbar_init(&conv[i], 8);
+            mbar_init(&a_free[i], 1);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], kIWorkers);
         }
-        mbar_init(rbar, 1);
-        flags[0] = 0;
+        mbar_init(drained, 1);
+        flags[0] = flags[1] = 0;
         fence_barrier_init();
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmX);
-        // what is complete when this grid starts is loaded at once
-        if (a.early >= 1)
-            for (int i = 0; i < pre; ++i) {
-                issue_w(i);
-                if (a.early >= 2) issue_x(i);
-            }
+        // what is complete when this grid starts is loaded at once: the weight, or also x
+        for (int i = 0; i < pre_w; ++i) issue_w(i, i);
+        if (a.early_x)
+            for (int i = 0; i < pre_x; ++i) issue_x(i, i);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
@@ -130,90 +148,179 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (a.splits > 1) cluster_arrive();  // (waited for before the first store into another CTA)
     if (a.release) pdl_trigger();
 
     if (warp == 0) {
         if (lane == 0) {
-            int issued = 0;
-            if (a.early < 2) pdl_wait();
-            if (a.early >= 1) {
-                if (a.early < 2)
-                    for (int i = 0; i < pre; ++i) issue_x(i);
-                issued = pre;
+            if (!a.early_x) {
+                pdl_wait();
+                for (int i = 0; i < pre_x; ++i) issue_x(i, i);
             }
-            for (int i = issued; i < nkb; ++i) {
-                const int s = i % stages;
-                if (i >= stages && !mbar_wait(&empty[s], ((i / stages) & 1) ^ 1, flags)) break;
-                issue_w(i);
-                issue_x(i);
-                ++issued;
-            }
-            if (flags[0]) {
-                if (a.status) report_timeout_status(a.status);
-                for (int i = max(0, issued - stages); i < issued; ++i) {
-                    const unsigned long long t = globaltimer();
-                    while (!mbar_try_wait(&full[i % stages], (i / stages) & 1) && globaltimer() - t < kWaitLimitNs) {
+            // whichever of the two has a stage free next
+            int iw = pre_w, ix = pre_x, sw = 0, sx = 0;
+            uint32_t phw = 0, phx = 0;
+            unsigned long long since = globaltimer();
+            int last = iw + ix;
+            for (uint32_t spin = 1; (iw < nkb || ix < nkb) && !flags[0]; ++spin) {
+                if (iw < nkb && mbar_test(&empty_w[sw], phw)) {
+                    issue_w(iw++, sw);
+                    if (++sw == ws) sw = 0, phw ^= 1;
+                }
+                if (ix < nkb && mbar_test(&empty_x[sx], phx)) {
+                    issue_x(ix++, sx);
+                    if (++sx == xs) sx = 0, phx ^= 1;
+                }
+                if ((spin & 1023u) == 0) {
+                    if (iw + ix != last) {
+                        last = iw + ix;
+                        since = globaltimer();
+                    } else if (globaltimer() - since > kWaitLimitNs) {
+                        flags[0] = 1;
                     }
                 }
             }
+            if (flags[0]) {  // give the copies in flight time to land
+                if (a.status) report_timeout_status(a.status);
+                const unsigned long long t = globaltimer();
+                while (globaltimer() - t < kWaitLimitNs / 8) {
+                }
+            }
+        }
+        __syncwarp();
+        // what the stores will need
+        pdl_wait();
+        const bool st_ok = !a.status || __ldcg(a.status) == LORA_OK;
+        for (int e = lane; e < kIM; e += 32) sw_sm[e] = m_tile * kIM + e < a.h_out ? __ldg(a.sw + m_tile * kIM + e) : 0.f;
+        for (int u = lane; u < cnt; u += 32) {
+            const int r = row0 + t0 + u;
+            sx_sm[u] = __ldcg(a.sx + r);
+            if (!FUSE) row_sm[u] = a.perm && st_ok ? __ldcg(a.perm + r) : r;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            bool ok = true;
-            const uint32_t idesc = idesc_f16(kIM, n_pad, false);
-            int i = 0;
-            for (int c = 0; c < nchunks && ok; ++c) {
-                const int buf = c & 1, end = min(nkb, (c + 1) * kIChunk);
-                const uint32_t acc = tmem + buf * n_pad;
-                if (c >= 2 && !mbar_wait(&acc_empty[buf], ((c >> 1) & 1) ^ 1, flags)) {
-                    ok = false;
-                    break;
-                }
-                for (bool first = true; i < end; ++i) {
-                    const int s = i % stages, slot = i % aslots;
-                    if (!mbar_wait(&full[s], (i / stages) & 1, flags) || !mbar_wait(&conv[slot], (i / aslots) & 1, flags)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t xa = smem_u32(smem + (size_t)s * stage_bytes + kIWBytes);
-                    const uint32_t wa = tmem + kIACol + slot * 64;
+        bool ok = true;
+        const uint32_t idesc = idesc_f16(kIM, n_pad, false);
+        int i = 0, s = 0, slot = 0;
+        uint32_t ph = 0, aph = 0;
+        for (int c = 0; c < nchunks && ok; ++c) {
+            const int buf = c & 1, end = min(nkb, (c + 1) * kIChunk);
+            const uint32_t acc = tmem + buf * n_pad;
+            if (c >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((c >> 1) & 1) ^ 1, flags));
+            uint32_t more = 0;
+            for (; i < end && ok; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_x[s], ph, flags) && mbar_wait(&conv[slot], aph, flags));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t xd = sdesc_sw128(smem_u32(xring + s * x_bytes));
+                const uint32_t wa = tmem + kIACol + slot * 64;
+                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        umma_f16_ta(acc, wa + k * 8, sdesc_sw128(xa + (k >> 2) * n_pad * 128 + (k & 3) * 32), idesc,
-                                    first ? 0u : 1u);
-                        first = false;
-                    }
-                    umma_commit(&empty[s]);
+                    for (int k = 0; k < 8; ++k)
+                        umma_f16_ta(acc, wa + k * 8, xd + (k >> 2) * (n_pad * 8) + (k & 3) * 2, idesc, k > 0 ? 1u : more);
+                    umma_commit(&a_free[slot]);
+                    umma_commit(&empty_x[s]);
                 }
-                if (ok) umma_commit(&acc_full[buf]);
+                __syncwarp();
+                more = 1;
+                if (++s == xs) s = 0, ph ^= 1;
+                if (++slot == kIASlots) slot = 0, aph ^= 1;
             }
-            if (!ok) {
-                if (a.status) report_timeout_status(a.status);
-                // every MMA issued above completes before the CTA may leave
-                umma_commit(rbar);
-                const unsigned long long t = globaltimer();
-                while (!mbar_try_wait(rbar, 0) && globaltimer() - t < kWaitLimitNs) {
-                }
-            }
+            if (ok && elect_one()) umma_commit(&acc_full[buf]);
+            __syncwarp();
         }
-    } else if (warp < 10) {
-        // ---- codes to float16 in tensor memory: 32 features and 64 codes of a step a warp ----
-        const int q = warp & 3, h = (warp - 2) >> 2;
+        if (!ok) {
+            if (lane == 0 && a.status) report_timeout_status(a.status);
+            // every MMA issued above completes before the CTA may leave
+            if (elect_one()) umma_commit(drained);
+            const unsigned long long t = globaltimer();
+            while (!mbar_try_wait(drained, 0) && globaltimer() - t < kWaitLimitNs) {
+            }
+            __syncwarp();
+        }
+    } else if (warp < 2 + kIWorkers) {
+        // ---- codes to float16 in tensor memory: 32 features and 64 codes of every second step a warp; and the
+        // accumulator, 32 features and every fourth 16 tokens a warp ----
+        const int q = warp & 3, h = ((warp - 2) >> 2) & 1, set = (warp - 2) >> 3;
         const int row = q * 32 + lane;
         const uint32_t taddr = tmem + kIACol + h * 32 + (static_cast<uint32_t>(q * 32) << 16);
-        for (int i = 0; i < nkb; ++i) {
-            const int s = i % stages, slot = i % aslots;
-            bool ok = mbar_wait(&full[s], (i / stages) & 1, flags);
-            // the slot's last readers
-            if (ok && i >= aslots) ok = mbar_wait(&empty[(i - aslots) % stages], ((i - aslots) / stages) & 1, flags);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            const uint8_t* wr = smem + (size_t)s * stage_bytes + row * 128;
+        const uint32_t sums = smem_u32(G) + (split * a.per * kIM + row) * 4;
+        const int units = n_pad / 16;
+        bool ok = true;
+        int chunk = 0;  // the next to drain
+        bool started = a.splits == 1;
+        int sum[kIN / 64][16];  // (indexed at run time: in local memory, touched once in 1024 codes, not in registers)
+        auto drain = [&]() {
+            const int buf = chunk & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (chunk >> 1) & 1, flags));
+            if (!ok) return;
+            tc_fence_after();
+            const bool first = chunk == 0, last = ++chunk == nchunks;
+            if (last && !started) {
+                cluster_wait();  // every CTA of the cluster has started
+                started = true;
+            }
+            const uint32_t aaddr = tmem + buf * n_pad + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+            for (int u = h * 2 + set, j = 0; u < units; u += 4, ++j) {
+                uint32_t r[16];
+                tmem_ld16(aaddr + u * 16, r);
+                tmem_ld_wait();
+                if (!first)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = static_cast<uint32_t>(sum[j][e] + __float2int_rn(__uint_as_float(r[e])));
+                else
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(r[e])));
+                if (!last) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[j][e] = static_cast<int>(r[e]);
+                } else if (a.splits == 1) {
+                    // (the last accumulator is complete: every MMA has read its operands, the ring is idle)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) G[(u * 16 + e) * kIM + row] = static_cast<int>(r[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int t = u * 16 + e, dst = (t * a.per_inv) >> 16;  // = t / per
+                        if (t < n) st_dsmem_u32(mapa_shared(sums + (t - dst * a.per) * kIM * 4, static_cast<uint32_t>(dst)), r[e]);
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        };
+        // step i has stage i % ws and slot i % kIASlots, both even numbers: a warp's steps share theirs with no others
+        int s = set, slot = set, before = -1;
+        uint32_t ph = 0, fph = 1;  // (the slots start free)
+        uint4 v[4];
+        auto read = [&]() {  // the warp's next codes, once they are there
+            const uint8_t* wr = smem + s * kIWBytes + row * 128;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = *reinterpret_cast<const uint4*>(wr + (((h * 4 + c) ^ (row & 7)) << 4));
+        };
+        auto release = [&]() {  // (after their first use: the loads have returned)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty_w[s]);
+            if ((s += 2) >= ws) s -= ws, ph ^= 1;
+        };
+        auto announce = [&]() {  // the slot stored last, once the store has landed
+            if (before < 0) return;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&conv[before]);
+        };
+        if (set < nkb) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full_w[s], 0, flags));
+            if (ok) read();
+        }
+        for (int i = set; i < nkb && ok; i += 2) {
             uint32_t r[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4*>(wr + (((h * 4 + c) ^ (row & 7)) << 4));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint2 f = i8_to_f16x4(w[e]);
@@ -221,21 +328,42 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     r[c * 8 + e * 2 + 1] = f.y;
                 }
             }
+            release();
+            announce();  // (its latency was covered by the conversion)
+            ok = __all_sync(0xffffffffu, mbar_wait(&a_free[slot], fph, flags));
+            if (!ok) break;
             tc_fence_after();
             tmem_st32(taddr + slot * 64, r);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&conv[slot]);
+            before = slot;
+            if ((slot += 2) >= kIASlots) slot -= kIASlots, fph ^= 1;
+            const bool done = i >= (chunk + 1) * kIChunk + kIChunk / 2;  // the chunk before is complete by now
+            const bool more = i + 2 < nkb;
+            if (done || (more && !__all_sync(0xffffffffu, mbar_test(&full_w[s], ph)))) {
+                announce();  // (the MMAs need not wait for what follows)
+                before = -1;
+            }
+            if (done) drain();
+            if (more && ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full_w[s], ph, flags));
+                if (ok) read();
+            }
         }
-    } else {
-        const int lt = threadIdx.x - 320;  // 0..255
-        if constexpr (FUSE) {
-            // ---- the LoRA terms of this CTA's tokens: a feature a thread, every second token ----
+        if (ok) announce();
+        while (ok && chunk < nchunks) drain();
+        if (!started) cluster_wait();
+        if (!ok && lane == 0) flags[0] = 1;
+    } else if constexpr (FUSE) {
+        const int lt = threadIdx.x - kIThreads;  // 0..255
+        if (!a.early_x) pdl_wait();
+        // (perm and the segments are older than the kernel ahead)
+        const bool st_ok = !a.status || __ldcg(a.status) == LORA_OK;
+        if (lt < cnt) {  // (per <= 128)
+            const int t = st_ok ? __ldcg(a.perm + row0 + t0 + lt) : 0;
+            row_sm[lt] = t;
+            tok_slot[lt] = st_ok ? __ldcg(a.idx + t) : -1;
+        }
+        // ---- the LoRA terms of this CTA's tokens: a feature a thread, every second token ----
             const int f = lt & 127, half = lt >> 7, o = m_tile * kIM + f, R = a.R;
-            if (a.early < 2) pdl_wait();  // (perm and the segments are older than the kernel ahead otherwise)
-            const bool st_ok = !a.status || __ldcg(a.status) == LORA_OK;
-            for (int u = lt; u < cnt; u += 256) tok_slot[u] = st_ok ? __ldcg(a.idx + __ldcg(a.perm + row0 + t0 + u)) : -1;
             pdl_wait();  // the shrink output
             const size_t part = (size_t)a.n * R;
             for (int j0 = 0; j0 < R; j0 += kISRanks) {
@@ -244,7 +372,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     const int u = e / kISRanks, j = j0 + e % kISRanks;
                     float v = 0.f;
                     if (tok_slot[u] >= 0 && j < a.table[tok_slot[u]].rank) {
-                        const float* sp = a.s_in + (size_t)__ldcg(a.perm + row0 + t0 + u) * R + j;
+                        const float* sp = a.s_in + (size_t)row_sm[u] * R + j;
                         for (int p = 0; p < a.s_parts; ++p) v += __ldcg(sp + p * part);
                     }
                     S[e] = v;
@@ -301,123 +429,42 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 }
             }
         }
-        // ---- accumulator: 32 features a warp, every second 16 tokens; its chunks added up in integers ----
-        const int q = warp & 3, hv = (warp - 10) >> 2;
-        const int units = n_pad / 16;
-        int sum[4][16] = {};
-        bool ok = true;
-        for (int c = 0; c < nchunks && ok; ++c) {
-            const int buf = c & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (c >> 1) & 1, flags));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t taddr = tmem + buf * n_pad + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = 2 * i + hv;
-                if (u < units) {
-                    uint32_t r[16];
-                    __syncwarp();
-                    tmem_ld16(taddr + u * 16, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) sum[i][e] += __float2int_rn(__uint_as_float(r[e]));
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
-        }
-        if (ok) {
-            // (the last accumulator is complete: every MMA has read its operands, the ring is idle)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = 2 * i + hv;
-                if (u < units)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) P[(u * 16 + e) * kIM + q * 32 + lane] = sum[i][e];
-            }
-            fence_proxy_async_smem();  // read by the bulk copies
-        } else if (lane == 0) {
-            flags[0] = 1;
-        }
-    }
-    bool store = false;
-    if (warp >= 2) {
-        pdl_wait();
-        store = !a.status || __ldcg(a.status) == LORA_OK;
-    }
+
     tc_fence_before();
     __syncthreads();
-    // ---- each CTA adds up its share of the tokens and stores them.  The sums reach their owner by one bulk copy
-    // from each other CTA (a token's row is 512 bytes, an owner's rows are contiguous) where a receive buffer
-    // fits, else they are read remotely. ----
+    tc_fence_after();
     bool good = flags[0] == 0;
-    int* rcv = P + (size_t)n_pad * kIM;  // [splits - 1][per][128]
-    bool recv = true;
     if (a.splits > 1) {
-        if (a.push && threadIdx.x == 64 && cnt > 0 && good)
-            mbar_arrive_expect_tx(rbar, static_cast<uint32_t>((a.splits - 1) * cnt * kIM * 4));
-        cluster_sync();
-        good = cluster_unaborted(flags, a.splits);
-        if (a.push) {
-            const int dst = (int)threadIdx.x - 64;
-            if (good && dst >= 0 && dst < a.splits && dst != split) {
-                const int d0 = min(n, dst * a.per), dcnt = min(n, d0 + a.per) - d0;
-                if (dcnt > 0)
-                    bulk_s2cluster(mapa_shared(smem_u32(rcv + (size_t)(split < dst ? split : split - 1) * a.per * kIM),
-                                               static_cast<uint32_t>(dst)),
-                                   P + (size_t)d0 * kIM, static_cast<uint32_t>(dcnt * kIM * 4),
-                                   mapa_shared(smem_u32(rbar), static_cast<uint32_t>(dst)));
-            }
-            __syncwarp();
-            if (good && cnt > 0) recv = __all_sync(0xffffffffu, mbar_wait(rbar, 0, flags));
-            cluster_arrive();  // (the last wait below: every copy out of this CTA has then landed)
-        }
+        if (warp < 2 || warp >= 2 + kIWorkers) cluster_wait();  // (the workers have waited)
+        // sums of which a CTA gave up its part are no one's
+        if (!good && threadIdx.x < a.splits)
+            st_dsmem_u32(mapa_shared(smem_u32(const_cast<int*>(flags + 1)), threadIdx.x), 1u);
+        cluster_sync();  // every CTA has added its sums
+        good = good && flags[1] == 0;
     }
-    if (warp >= 2 && good && store && recv) {
+    pdl_wait();
+    if (good && cnt > 0 && (!a.status || __ldcg(a.status) == LORA_OK)) {
+        // ---- this CTA's share of the tokens ----
         T* y = static_cast<T*>(a.y);
-        auto yrow = [&](int u) -> T* {
-            const int r = row0 + t0 + u;
-            return y + (long long)(a.perm ? __ldcg(a.perm + r) : r) * a.ldy;
-        };
-        const int ot = threadIdx.x - 64;  // 0..511
         if (a.vec) {
             // 8 features a thread, 16 neighbouring threads a token's 128
-            const int o8 = (ot & 15) * 8, o = m_tile * kIM + o8;
-            float sw[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sw[e] = o + e < a.h_out ? __ldg(a.sw + o + e) : 0.f;
-            for (int u = ot >> 4; u < cnt; u += 32) {
-                int v[8];
-                const int4* own = reinterpret_cast<const int4*>(P + (t0 + u) * kIM + o8);
-                *reinterpret_cast<int4*>(v) = own[0];
-                *reinterpret_cast<int4*>(v + 4) = own[1];
+            const int o8 = (threadIdx.x & 15) * 8, o = m_tile * kIM + o8;
+            for (int u = threadIdx.x >> 4; u < cnt; u += blockDim.x / 16) {
+                int v[8] = {};
                 for (int c = 0; c < a.splits; ++c) {
-                    if (c == split) continue;
-                    if (a.push) {
-                        const int4* p =
-                            reinterpret_cast<const int4*>(rcv + ((size_t)(c < split ? c : c - 1) * a.per + u) * kIM + o8);
-                        const int4 lo = p[0], hi = p[1];
-                        v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
-                        v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
-                    } else {
-                        const uint32_t at = mapa_shared(smem_u32(own), static_cast<uint32_t>(c));
-                        const float4 lo = ld_dsmem_f32x4(at), hi = ld_dsmem_f32x4(at + 16);
-                        v[0] += __float_as_int(lo.x), v[1] += __float_as_int(lo.y), v[2] += __float_as_int(lo.z);
-                        v[3] += __float_as_int(lo.w), v[4] += __float_as_int(hi.x), v[5] += __float_as_int(hi.y);
-                        v[6] += __float_as_int(hi.z), v[7] += __float_as_int(hi.w);
-                    }
+                    const int4* p = reinterpret_cast<const int4*>(G + (c * a.per + u) * kIM + o8);
+                    const int4 lo = p[0], hi = p[1];
+                    v[0] += lo.x, v[1] += lo.y, v[2] += lo.z, v[3] += lo.w;
+                    v[4] += hi.x, v[5] += hi.y, v[6] += hi.z, v[7] += hi.w;
                 }
-                const float sx = __ldcg(a.sx + row0 + t0 + u);
                 alignas(16) T w[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float r = i8_scaled(v[e], sx, sw[e]);
+                    float r = i8_scaled(v[e], sx_sm[u], sw_sm[o8 + e]);
                     if constexpr (FUSE) r += L[u * kIM + o8 + e];
                     w[e] = from_f32<T>(r);
                 }
-                T* yp = yrow(u) + o;
+                T* yp = y + (long long)row_sm[u] * a.ldy + o;
                 if (o + 8 <= a.h_out) {
 #pragma unroll
                     for (int e = 0; e < (int)(8 * sizeof(T) / 16); ++e)
@@ -429,34 +476,22 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 }
             }
         } else {
-            // rows off 16-byte boundaries: a feature a thread, neighbours side by side
-            const int f = ot & 127, o = m_tile * kIM + f;
-            const float sw = o < a.h_out ? __ldg(a.sw + o) : 0.f;
-            for (int u = ot >> 7; u < cnt; u += 4) {
-                const int* own = P + (t0 + u) * kIM + f;
-                int v = *own;
-                for (int c = 0; c < a.splits; ++c) {
-                    if (c == split) continue;
-                    v += a.push ? rcv[((size_t)(c < split ? c : c - 1) * a.per + u) * kIM + f]
-                                : __float_as_int(ld_dsmem_f32(mapa_shared(smem_u32(own), static_cast<uint32_t>(c))));
-                }
-                float r = i8_scaled(v, __ldcg(a.sx + row0 + t0 + u), sw);
-                if constexpr (FUSE) r += L[u * kIM + f];
-                if (o < a.h_out) yrow(u)[o] = from_f32<T>(r);
+            // rows off 16-byte boundaries: neighbouring threads store neighbours
+            for (int e = threadIdx.x; e < cnt * kIM; e += blockDim.x) {
+                const int u = e / kIM, f = e % kIM, o = m_tile * kIM + f;
+                int v = 0;
+                for (int c = 0; c < a.splits; ++c) v += G[c * a.per * kIM + e];
+                float r = i8_scaled(v, sx_sm[u], sw_sm[f]);
+                if constexpr (FUSE) r += L[e];
+                if (o < a.h_out) y[(long long)row_sm[u] * a.ldy + o] = from_f32<T>(r);
             }
         }
-    }
-    if (!recv && a.status) report_timeout_status(a.status);
-    // no CTA leaves while its sums may still be read or copied
-    if (a.splits > 1) {
-        if (!a.push) cluster_arrive();
-        cluster_wait();
     }
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 template <typename T, bool FUSE>
-static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ldy, int32_t* status, int early, bool release,
+static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ldy, int32_t* status, bool early_x, bool release,
                          const I8Lora* lora, cudaStream_t st) {
     I8TileArgs a;
     memset(&a, 0, sizeof(a));
@@ -467,21 +502,43 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
     a.sw = w.scales;
     a.ldy = ldy;
     a.n = x.rows;
-    a.n_pad = (std::min(x.rows, kIN) + 15) / 16 * 16;
     a.h_out = w.rows;
     a.kb_total = (int)((w.pitch + kIK - 1) / kIK);
-    a.early = early;
+    a.early_x = early_x;
     a.release = release;
     // y is written 16 bytes at a time when every row starts on a 16-byte boundary
     a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
-    const int m_tiles = (w.rows + kIM - 1) / kIM, groups = (x.rows + kIN - 1) / kIN;
-    if (groups > 65535) return set_error(LORA_EUNSUP, "8-bit product of %d rows", x.rows);
-    // CTAs (a cluster) that share K: as many as let every tile have an SM a CTA
-    const long long tiles = (long long)m_tiles * groups;
-    const int splits = (int)std::min<long long>({std::max<long long>(1, num_sms() / tiles), 8, a.kb_total});
-    a.kb_per_split = (a.kb_total + splits - 1) / splits;
-    a.splits = (a.kb_total + a.kb_per_split - 1) / a.kb_per_split;
-    a.per = (std::min(x.rows, kIN) + a.splits - 1) / a.splits;
+    const int m_tiles = (w.rows + kIM - 1) / kIM;
+    int groups = 0;
+    size_t smem = 0;
+    // groups of up to 128 tokens, of 64 where those leave no room for the stages
+    for (int most = kIN; most >= kIN / 2; most /= 2) {
+        groups = (x.rows + most - 1) / most;
+        a.n_pad = ((x.rows + groups - 1) / groups + 15) / 16 * 16;
+        groups = (x.rows + a.n_pad - 1) / a.n_pad;
+        // CTAs (a cluster) that share K: as many as let every tile have an SM a CTA
+        const long long tiles = (long long)m_tiles * groups;
+        const int splits = (int)std::min<long long>({std::max<long long>(1, num_sms() / tiles), 8, a.kb_total});
+        a.kb_per_split = (a.kb_total + splits - 1) / splits;
+        a.splits = (a.kb_total + a.kb_per_split - 1) / a.kb_per_split;
+        a.per = (std::min(x.rows, a.n_pad) + a.splits - 1) / a.splits;
+        a.per_inv = 65535 / a.per + 1;  // t / per = t * per_inv >> 16 for t < 256
+        const size_t words = (size_t)(a.splits > 1 ? a.splits * a.per * kIM : 0) + (FUSE ? a.per * (kIM + kISRanks + 1) : 0) + 2 * a.per + kIM;
+        const size_t tail = words * 4 + kIBars + 1024 + 16;
+        // stages of x (at most 4), then of w (4, 6 or 8: an even number, as the workers' halves alternate)
+        const size_t room = 227 * 1024 - tail, x_bytes = (size_t)a.n_pad * 256;
+        a.xstages = a.wstages = 0;
+        for (int x = 4; x >= 2 && !a.wstages; --x) {
+            const size_t left = room > x * x_bytes ? room - x * x_bytes : 0;
+            a.xstages = x;
+            a.wstages = (int)std::min<size_t>(left / kIWBytes / 2 * 2, 8);
+            if (a.wstages < (x > 2 ? 6 : 4)) a.wstages = 0;
+        }
+        a.ring_bytes = (int)std::max<size_t>(a.wstages * kIWBytes + a.xstages * x_bytes, a.splits > 1 ? 0 : (size_t)a.n_pad * kIM * 4);
+        smem = a.ring_bytes + tail;
+        if (a.wstages) break;
+    }
+    if (!a.wstages || smem > 227 * 1024 || groups > 65535) return set_error(LORA_EUNSUP, "8-bit product of %d rows", x.rows);
     if (lora) {
         const PoolView& pv = *lora->pool;
         a.table = pv.table;
@@ -491,17 +548,6 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
         a.R = pv.R;
         a.s_parts = lora->s_parts;
     }
-    const size_t tail = (FUSE ? (size_t)a.per * (kIM + kISRanks + 1) * 4 : 0) + kIBars + 1024 + 16;
-    const size_t room = 227 * 1024 - tail;
-    const size_t stage_bytes = kIWBytes + (size_t)a.n_pad * 256;
-    a.stages = (int)std::min<size_t>({room / stage_bytes, 8, (size_t)a.kb_per_split});
-    a.aslots = std::min(kIASlots, a.stages);  // (no more: a slot's last reader is found by its stage's barrier)
-    // the stages are idle when the sums are parked in their place
-    const size_t park = (size_t)a.n_pad * kIM * 4, rcv = (size_t)(a.splits - 1) * a.per * kIM * 4;
-    a.push = a.splits > 1 && park + rcv <= room / 1024 * 1024;
-    a.ring_bytes = (int)((std::max(a.stages * stage_bytes, park + (a.push ? rcv : 0)) + 1023) / 1024 * 1024);
-    const size_t smem = a.ring_bytes + tail;
-    if (a.stages < 1 || smem > 227 * 1024) return set_error(LORA_EUNSUP, "internal: 8-bit tile plan");
     CUtensorMap mW, mX;
     int rc = make_map_fp4(&mW, w.codes, w.pitch, w.rows, kIM);  // (bytes in boxes of 128)
     if (!rc) rc = make_map(&mX, x.x16, 0, w.pitch, x.rows, a.n_pad);
@@ -515,7 +561,7 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(m_tiles, a.splits, groups);
-    cfg.blockDim = dim3(kIThreads);
+    cfg.blockDim = dim3(kIThreads + (FUSE ? kILora : 0));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -534,18 +580,18 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
 
 }  // namespace tc
 
-int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, int early,
+int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_x,
                    bool release, const I8Lora* lora, cudaStream_t st) {
     switch (dtype) {
         case LORA_F32:
-            return lora ? tc::launch_tile_t<float, true>(x, w, y, ldy, status, early, release, lora, st)
-                        : tc::launch_tile_t<float, false>(x, w, y, ldy, status, early, release, nullptr, st);
+            return lora ? tc::launch_tile_t<float, true>(x, w, y, ldy, status, early_x, release, lora, st)
+                        : tc::launch_tile_t<float, false>(x, w, y, ldy, status, early_x, release, nullptr, st);
         case LORA_F16:
-            return lora ? tc::launch_tile_t<__half, true>(x, w, y, ldy, status, early, release, lora, st)
-                        : tc::launch_tile_t<__half, false>(x, w, y, ldy, status, early, release, nullptr, st);
+            return lora ? tc::launch_tile_t<__half, true>(x, w, y, ldy, status, early_x, release, lora, st)
+                        : tc::launch_tile_t<__half, false>(x, w, y, ldy, status, early_x, release, nullptr, st);
         default:
-            return lora ? tc::launch_tile_t<__nv_bfloat16, true>(x, w, y, ldy, status, early, release, lora, st)
-                        : tc::launch_tile_t<__nv_bfloat16, false>(x, w, y, ldy, status, early, release, nullptr, st);
+            return lora ? tc::launch_tile_t<__nv_bfloat16, true>(x, w, y, ldy, status, early_x, release, lora, st)
+                        : tc::launch_tile_t<__nv_bfloat16, false>(x, w, y, ldy, status, early_x, release, nullptr, st);
     }
 }
 

@@ -174,10 +174,10 @@ struct I8Rows {
     const int32_t* perm;  // nullptr: as they are
     int rows, cols;
 };
-// On the tensor cores.  early: every kernel that could have written w (1), or w and x (2), has completed when
-// this grid starts.  release: the kernel behind may be released early (never a product by itself, whose y may be
+// On the tensor cores.  Every kernel that could have written w has completed when this grid starts (the kernel
+// ahead waited for it); early_x: so has x.  release: the kernel behind may be released early (never a product by itself, whose y may be
 // a weight that a 16-bit linear streams unwaited).
-int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, int early,
+int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_x,
                    bool release, const I8Lora* lora, cudaStream_t st);
 // The same for many tokens: the weight in float16 codes too; 16-bit y: the shrink output in one part (float32:
 // without the LoRA term).
