@@ -35,14 +35,14 @@ namespace tc {
 using namespace ptx;
 
 constexpr int kIM = 128;          // features per tile
-constexpr int kIN = 128;          // tokens per tile, at most
+constexpr int kIN = 256;          // tokens per tile, at most
 constexpr int kIK = 128;          // codes of a step along K
 constexpr int kIChunk = 8;        // steps between two readings of the accumulator: 1024 codes
 constexpr int kIWorkers = 16;     // warps 2-17: convert (half of them the even steps, half the odd), drain
 constexpr int kIThreads = 64 + 32 * kIWorkers;  // warp 0 loads, 1 MMAs
 constexpr int kILora = 256;       // more threads for the LoRA term
 constexpr int kIASlots = 4;       // steps of the weight in tensor memory, 64 columns each
-constexpr int kIACol = 2 * kIN;   // behind two accumulators
+constexpr int kIACol = 256;       // behind two accumulators of up to 128 tokens, or one of more
 constexpr int kISRanks = 16;      // columns of the shrink output staged at once
 constexpr uint32_t kIWBytes = kIM * kIK;
 constexpr int kIBars = 384;
@@ -54,7 +54,7 @@ struct I8TileArgs {
     const float* sx;
     const float* sw;
     long long ldy;
-    int n, n_pad, h_out, kb_total, kb_per_split, splits, wstages, xstages, early_x, release, vec, ring_bytes, per, per_inv;
+    int n, n_pad, h_out, kb_total, kb_per_split, splits, wstages, xstages, xk, early_x, release, vec, ring_bytes, alias, per, per_inv;
     // the LoRA term (FUSE)
     const SlotEntry* table;
     const void* B;
@@ -70,12 +70,12 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint8_t* smem = smem_align(smem_raw, 1024);
     // stages of the weight's codes, which the warps that convert them free, and of the tokens', which the MMAs free
     const int ws = a.wstages, xs = a.xstages, n_pad = a.n_pad;
-    const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 256;  // two boxes of 64 float16 columns
+    const uint32_t x_bytes = static_cast<uint32_t>(n_pad) * 128 * a.xk;  // xk (1 or 2) boxes of 64 float16 columns
     uint8_t* xring = smem + ws * kIWBytes;
-    // sums of the tokens this CTA finishes, from each CTA of the cluster [splits][per][128]; of a CTA by itself, in
-    // the ring once that is idle
-    int* G = reinterpret_cast<int*>(smem + (a.splits > 1 ? a.ring_bytes : 0));
-    float* L = reinterpret_cast<float*>(smem + a.ring_bytes) + (a.splits > 1 ? a.splits * a.per * kIM : 0);  // FUSE: [per][128] their LoRA terms
+    // sums of the tokens this CTA finishes, from each CTA of the cluster [splits][per][128]; with alias in the ring,
+    // once that is idle
+    int* G = reinterpret_cast<int*>(smem + (a.alias ? 0 : a.ring_bytes));
+    float* L = reinterpret_cast<float*>(smem + a.ring_bytes) + (a.alias ? 0 : a.splits * a.per * kIM);  // FUSE: [per][128] their LoRA terms
     float* S = L + (FUSE ? a.per * kIM : 0);                      // FUSE: [per][kISRanks] shrink output
     int* tok_slot = reinterpret_cast<int*>(S + (FUSE ? a.per * kISRanks : 0));  // FUSE: [per] slots of the CTA's tokens,
     int* row_sm = tok_slot + (FUSE ? a.per : 0);                 // [per] their rows of y,
@@ -102,17 +102,30 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // the tokens this CTA finishes
     const int t0 = min(n, split * a.per), cnt = min(n, t0 + a.per) - t0;
 
+    // Each feature tile starts at another place along K (sums of whole numbers come in any order): together, the
+    // CTAs would all read the same few lines of x at a time.
+    const int rot = m_tile % nkb;
+    auto column = [&](int i) {  // of step i
+        const int k = i + rot;
+        return (kb0 + (k < nkb ? k : k - nkb)) * kIK;
+    };
     auto issue_w = [&](int i, int st) {
         mbar_arrive_expect_tx(&full_w[st], kIWBytes);
-        tma_load_2d_cta(smem + st * kIWBytes, &tmW, &full_w[st], (kb0 + i) * kIK, m_tile * kIM);
+        tma_load_2d_cta(smem + st * kIWBytes, &tmW, &full_w[st], column(i), m_tile * kIM);
     };
     auto issue_x = [&](int i, int st) {
         uint8_t* dst = xring + st * x_bytes;
         mbar_arrive_expect_tx(&full_x[st], x_bytes);
-        tma_load_2d_cta(dst, &tmX, &full_x[st], (kb0 + i) * kIK, row0);
-        tma_load_2d_cta(dst + n_pad * 128, &tmX, &full_x[st], (kb0 + i) * kIK + 64, row0);
+        if (a.xk == 2) {
+            tma_load_2d_cta(dst, &tmX, &full_x[st], column(i), row0);
+            tma_load_2d_cta(dst + n_pad * 128, &tmX, &full_x[st], column(i) + 64, row0);
+        } else {
+            tma_load_2d_cta(dst, &tmX, &full_x[st], column(i >> 1) + (i & 1) * 64, row0);
+        }
     };
-    const int pre_w = min(ws, nkb), pre_x = min(xs, nkb);
+    const int nkx = nkb * (3 - a.xk);  // the tokens' stages, 64 or 128 codes each
+    const int pre_w = min(ws, nkb), pre_x = min(xs, nkx);
+    const int nbuf = n_pad <= 128 ? 2 : 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ws; ++i) {
             mbar_init(&full_w[i], 1);
@@ -148,7 +161,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (a.splits > 1) cluster_arrive();  // (waited for before the first store into another CTA)
+    if (a.splits > 1 && !a.alias) cluster_arrive();  // (waited for before the first store into another CTA)
     if (a.release) pdl_trigger();
 
     if (warp == 0) {
@@ -162,12 +175,12 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             uint32_t phw = 0, phx = 0;
             unsigned long long since = globaltimer();
             int last = iw + ix;
-            for (uint32_t spin = 1; (iw < nkb || ix < nkb) && !flags[0]; ++spin) {
+            for (uint32_t spin = 1; (iw < nkb || ix < nkx) && !flags[0]; ++spin) {
                 if (iw < nkb && mbar_test(&empty_w[sw], phw)) {
                     issue_w(iw++, sw);
                     if (++sw == ws) sw = 0, phw ^= 1;
                 }
-                if (ix < nkb && mbar_test(&empty_x[sx], phx)) {
+                if (ix < nkx && mbar_test(&empty_x[sx], phx)) {
                     issue_x(ix++, sx);
                     if (++sx == xs) sx = 0, phx ^= 1;
                 }
@@ -203,25 +216,38 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         int i = 0, s = 0, slot = 0;
         uint32_t ph = 0, aph = 0;
         for (int c = 0; c < nchunks && ok; ++c) {
-            const int buf = c & 1, end = min(nkb, (c + 1) * kIChunk);
+            const int buf = c % nbuf, end = min(nkb, (c + 1) * kIChunk);
             const uint32_t acc = tmem + buf * n_pad;
-            if (c >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], ((c >> 1) & 1) ^ 1, flags));
+            if (c >= nbuf) ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], (c / nbuf & 1) ^ 1, flags));
             uint32_t more = 0;
             for (; i < end && ok; ++i) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&full_x[s], ph, flags) && mbar_wait(&conv[slot], aph, flags));
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t xd = sdesc_sw128(smem_u32(xring + s * x_bytes));
+                uint64_t xd = sdesc_sw128(smem_u32(xring + s * x_bytes));
                 const uint32_t wa = tmem + kIACol + slot * 64;
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_f16_ta(acc, wa + k * 8, xd + (k >> 2) * (n_pad * 8) + (k & 3) * 2, idesc, k > 0 ? 1u : more);
+                    for (int k = 0; k < 4; ++k) umma_f16_ta(acc, wa + k * 8, xd + k * 2, idesc, k > 0 ? 1u : more);
+                    if (a.xk == 1) umma_commit(&empty_x[s]);
+                }
+                __syncwarp();
+                more = 1;
+                xd += n_pad * 8;
+                if (a.xk == 1) {
+                    if (++s == xs) s = 0, ph ^= 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&full_x[s], ph, flags));
+                    if (!ok) break;
+                    tc_fence_after();
+                    xd = sdesc_sw128(smem_u32(xring + s * x_bytes));
+                }
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_f16_ta(acc, wa + 32 + k * 8, xd + k * 2, idesc, 1u);
                     umma_commit(&a_free[slot]);
                     umma_commit(&empty_x[s]);
                 }
                 __syncwarp();
-                more = 1;
                 if (++s == xs) s = 0, ph ^= 1;
                 if (++slot == kIASlots) slot = 0, aph ^= 1;
             }
@@ -247,11 +273,18 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const int units = n_pad / 16;
         bool ok = true;
         int chunk = 0;  // the next to drain
-        bool started = a.splits == 1;
+        bool started = a.splits == 1 || a.alias;
         int sum[kIN / 64][16];  // (indexed at run time: in local memory, touched once in 1024 codes, not in registers)
+        auto hand_over = [&](int u, const uint32_t* r) {  // to the CTAs that finish these 16 tokens
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int t = u * 16 + e, dst = (t * a.per_inv) >> 16;  // = t / per
+                if (t < n) st_dsmem_u32(mapa_shared(sums + (t - dst * a.per) * kIM * 4, static_cast<uint32_t>(dst)), r[e]);
+            }
+        };
         auto drain = [&]() {
-            const int buf = chunk & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (chunk >> 1) & 1, flags));
+            const int buf = chunk % nbuf;
+            ok = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], chunk / nbuf & 1, flags));
             if (!ok) return;
             tc_fence_after();
             const bool first = chunk == 0, last = ++chunk == nchunks;
@@ -271,7 +304,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 else
 #pragma unroll
                     for (int e = 0; e < 16; ++e) r[e] = static_cast<uint32_t>(__float2int_rn(__uint_as_float(r[e])));
-                if (!last) {
+                if (!last || (a.alias && a.splits > 1)) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) sum[j][e] = static_cast<int>(r[e]);
                 } else if (a.splits == 1) {
@@ -279,11 +312,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 #pragma unroll
                     for (int e = 0; e < 16; ++e) G[(u * 16 + e) * kIM + row] = static_cast<int>(r[e]);
                 } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int t = u * 16 + e, dst = (t * a.per_inv) >> 16;  // = t / per
-                        if (t < n) st_dsmem_u32(mapa_shared(sums + (t - dst * a.per) * kIM * 4, static_cast<uint32_t>(dst)), r[e]);
-                    }
+                    hand_over(u, r);
                 }
                 __syncwarp();
             }
@@ -336,7 +365,8 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             tmem_st32(taddr + slot * 64, r);
             before = slot;
             if ((slot += 2) >= kIASlots) slot -= kIASlots, fph ^= 1;
-            const bool done = i >= (chunk + 1) * kIChunk + kIChunk / 2;  // the chunk before is complete by now
+            // the chunk before is complete by now; or (one accumulator) holds the MMAs up, and enough is converted
+            const bool done = i >= (chunk + 1) * kIChunk + (nbuf == 2 ? kIChunk / 2 : 2);
             const bool more = i + 2 < nkb;
             if (done || (more && !__all_sync(0xffffffffu, mbar_test(&full_w[s], ph)))) {
                 announce();  // (the MMAs need not wait for what follows)
@@ -352,6 +382,17 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         while (ok && chunk < nchunks) drain();
         if (!started) cluster_wait();
         if (!ok && lane == 0) flags[0] = 1;
+        if (a.alias && a.splits > 1) {
+            cluster_sync();  // every CTA's MMAs have read their operands: the rings are idle
+            if (ok)
+#pragma unroll 1
+                for (int u = h * 2 + set, j = 0; u < units; u += 4, ++j) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) r[e] = static_cast<uint32_t>(sum[j][e]);
+                    hand_over(u, r);
+                }
+        }
     } else if constexpr (FUSE) {
         const int lt = threadIdx.x - kIThreads;  // 0..255
         if (!a.early_x) pdl_wait();
@@ -430,12 +471,16 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
         }
 
+    if (a.splits > 1 && (warp < 2 || warp >= 2 + kIWorkers)) {  // (as the workers have)
+        if (a.alias) cluster_arrive();
+        cluster_wait();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     bool good = flags[0] == 0;
     if (a.splits > 1) {
-        if (warp < 2 || warp >= 2 + kIWorkers) cluster_wait();  // (the workers have waited)
+
         // sums of which a CTA gave up its part are no one's
         if (!good && threadIdx.x < a.splits)
             st_dsmem_u32(mapa_shared(smem_u32(const_cast<int*>(flags + 1)), threadIdx.x), 1u);
@@ -511,8 +556,8 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
     const int m_tiles = (w.rows + kIM - 1) / kIM;
     int groups = 0;
     size_t smem = 0;
-    // groups of up to 128 tokens, of 64 where those leave no room for the stages
-    for (int most = kIN; most >= kIN / 2; most /= 2) {
+    // groups of up to 256 tokens, of 128 or 64 where those leave no room for the stages
+    for (int most = kIN; most >= 64; most /= 2) {
         groups = (x.rows + most - 1) / most;
         a.n_pad = ((x.rows + groups - 1) / groups + 15) / 16 * 16;
         groups = (x.rows + a.n_pad - 1) / a.n_pad;
@@ -523,18 +568,23 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
         a.splits = (a.kb_total + a.kb_per_split - 1) / a.kb_per_split;
         a.per = (std::min(x.rows, a.n_pad) + a.splits - 1) / a.splits;
         a.per_inv = 65535 / a.per + 1;  // t / per = t * per_inv >> 16 for t < 256
-        const size_t words = (size_t)(a.splits > 1 ? a.splits * a.per * kIM : 0) + (FUSE ? a.per * (kIM + kISRanks + 1) : 0) + 2 * a.per + kIM;
+        a.alias = a.splits == 1 || a.n_pad > 128;
+        const size_t words = (size_t)(a.alias ? 0 : a.splits * a.per * kIM) + (FUSE ? a.per * (kIM + kISRanks + 1) : 0) + 2 * a.per + kIM;
         const size_t tail = words * 4 + kIBars + 1024 + 16;
-        // stages of x (at most 4), then of w (4, 6 or 8: an even number, as the workers' halves alternate)
-        const size_t room = 227 * 1024 - tail, x_bytes = (size_t)a.n_pad * 256;
+        // stages of x (at most 4; of 64 codes for more than 128 tokens), then of w (4, 6 or 8: an even number, as the
+        // workers' halves alternate)
+        a.xk = a.n_pad > 128 ? 1 : 2;
+        const size_t room = 227 * 1024 - tail, x_bytes = (size_t)a.n_pad * 128 * a.xk;
         a.xstages = a.wstages = 0;
-        for (int x = 4; x >= 2 && !a.wstages; --x) {
+        for (int x = 4; x >= 2 && !a.wstages && tail < 227 * 1024; --x) {
             const size_t left = room > x * x_bytes ? room - x * x_bytes : 0;
             a.xstages = x;
             a.wstages = (int)std::min<size_t>(left / kIWBytes / 2 * 2, 8);
-            if (a.wstages < (x > 2 ? 6 : 4)) a.wstages = 0;
+            if (a.wstages < (x > 2 && a.xk == 2 ? 6 : 4) || (a.xk == 1 && x < 3)) a.wstages = 0;
         }
-        a.ring_bytes = (int)std::max<size_t>(a.wstages * kIWBytes + a.xstages * x_bytes, a.splits > 1 ? 0 : (size_t)a.n_pad * kIM * 4);
+        a.ring_bytes = (int)std::max<size_t>(a.wstages * kIWBytes + a.xstages * x_bytes,
+                                             a.alias ? (size_t)a.splits * a.per * kIM * 4 : 0);
+        if (a.splits == 1) a.ring_bytes = (int)std::max<size_t>(a.ring_bytes, (size_t)a.n_pad * kIM * 4);
         smem = a.ring_bytes + tail;
         if (a.wstages) break;
     }
