@@ -368,6 +368,12 @@ static int launch_fp4_expand_t(const PoolView& pv, const SegView& sv, const floa
     return LORA_OK;
 }
 
+int launch_sum_expand(const PoolView& pv, const SegView& sv, const float* s_in, int s_parts, const float* y32, void* y,
+                      cudaStream_t st) {
+    return pv.dtype == LORA_F16 ? launch_fp4_expand_t<__half>(pv, sv, s_in, s_parts, y32, y, st)
+                                : launch_fp4_expand_t<__nv_bfloat16>(pv, sv, s_in, s_parts, y32, y, st);
+}
+
 // float32 pools: whether the per-token shrink (which reads an adapter's rows for each of its tokens) takes
 // the batch, with the quantisation in the same launch, rather than the tiled one; and its K parts.  Both
 // are weighed in us: the tiled one by its tiles' steps of 32 features (as many adapters as can be), and the
@@ -375,7 +381,7 @@ static int launch_fp4_expand_t(const PoolView& pv, const SegView& sv, const floa
 // token: 1 token 4096 x 4096 r_max 16 16.5 / 11.6; 64 tokens, 100 slots, r_max 8 31.5 / 16.6; 200 tokens,
 // 6 slots, 11008 x 4096 r_max 64 110 / 84; 1000 tokens, 10 slots, 4096 x 1000 r_max 32 50.6 / 60.3; 15226
 // tokens, 10 slots, 336 x 488 r_max 64 94 / 341; 4096 tokens, 100 slots, 4096 x 512 r_max 8 101 / 84.
-static bool f32_front(const PoolView& pv, int n) {
+bool f32_front(const PoolView& pv, int n) {
     const int rows = pv.R <= 16 ? 16 : pv.R <= 32 ? 32 : 64;
     const double tiles = n / 64. + std::min(n, pv.S), groups = (pv.R + rows - 1) / rows, steps = (pv.h_in + 31) / 32;
     const double tiled = 4 + tiles * groups * steps * (rows == 16 ? 0.004 : rows == 32 ? 0.008 : 0.014);
@@ -664,8 +670,7 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
         float* y32 = reinterpret_cast<float*>(ws + L.y32_off);
         if (!rc) rc = launch_fp4_product(q, view_of(w), y32, LORA_F32, pv.h_out, sv.status, /*early=*/2, st);
         if (rc) return rc;
-        return pv.dtype == LORA_F16 ? launch_fp4_expand_t<__half>(pv, sv, s_buf, s_parts, y32, y_dev, st)
-                                    : launch_fp4_expand_t<__nv_bfloat16>(pv, sv, s_buf, s_parts, y32, y_dev, st);
+        return launch_sum_expand(pv, sv, s_buf, s_parts, y32, y_dev, st);
     }
     if (n > 256 && pv.dtype != LORA_F32) {
         float* sum = reinterpret_cast<float*>(ws + L.sum_off);

@@ -65,10 +65,23 @@ static I8ProductWs product_ws(int n, int h_out, int h_in) {
     return L;
 }
 
+// Batches of more than 256 tokens that may be spread over many adapters (fewer than 16 tokens a slot): the product
+// in float32 into the workspace, and a segmented expand after it.  The pair kernel would build blocks of B for
+// almost every adapter in every tile.
+constexpr long long kI8SumElements = 32 << 20;
+static bool separate(const PoolView& pv, int n) {
+    return pv.dtype != LORA_F32 && n > kI8Tile && n < 16LL * std::min(n, pv.S) && (long long)n * pv.h_out <= kI8SumElements;
+}
+// The largest such batch of at most n tokens (0: none).
+static int most_separate(const PoolView& pv, int n) {
+    const int m = (int)std::min<long long>({(long long)n, 16LL * pv.S - 1, kI8SumElements / pv.h_out});
+    return separate(pv, m) ? m : 0;
+}
+
 // Workspace of lora_i8_linear_fwd: the shrink output in its K parts, x's codes (in bytes for a few tokens,
-// else in float16) and scales, the weight in float16 codes.
+// else in float16) and scales, the weight in float16 codes, the product where the expand is separate.
 struct I8WsLayout {
-    size_t codes_off, scales_off, w_off, total;
+    size_t codes_off, scales_off, w_off, y32_off, total;
 };
 static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     if (n < 0) return set_error(LORA_EINVAL, "n_tokens < 0");
@@ -82,7 +95,8 @@ static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     const I8ProductWs P = product_ws(n, pv.h_out, pv.h_in);
     L->scales_off = L->codes_off + (n <= kI8Small ? align256((size_t)n * i8_pitch(pv.h_in)) : P.scales_off);
     L->w_off = L->scales_off + align256((size_t)n * 4);
-    L->total = L->w_off + P.total - P.w_off;
+    L->y32_off = L->w_off + P.total - P.w_off;
+    L->total = L->y32_off + align256((size_t)most_separate(pv, n) * pv.h_out * 4);
     return LORA_OK;
 }
 
@@ -220,37 +234,53 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
     const SegView sv = seg_view(seg);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool few = n <= kI8Small;
-    const I8View q = xq ? view_of(xq) : i8_view(ws + L.codes_off, sx, n, pv.h_in);
-    if (!few)  // rows in the order of the segments
-        rc = xq ? launch_i8_expand(q, sv.perm, sv.status, ws + L.codes_off, sx, st)
-                : launch_i8_quantize_f16(x_dev, pv.dtype, n, pv.h_in, sv.perm, sv.status, ws + L.codes_off, sx, st);
-    else if (!xq)
-        rc = launch_i8_quantize(x_dev, pv.dtype, pv.h_in, q, st);
+    const bool front = n <= kI8Tile && (pv.dtype == LORA_F32 ? f32_front(pv, n) : !shrink_segmented(pv, n));
+    char* codes = ws + L.codes_off;
+    I8View xv, stored;
+    if (xq) stored = view_of(xq);
     int s_parts = 1;
-    if (!rc) {
+    if (front) {
+        rc = launch_i8_front(pv, sv, x_dev, xq ? &stored : nullptr, codes, !few, sx, s_buf, &s_parts, st);
+    } else {
+        if (!few)  // rows in the order of the segments
+            rc = xq ? launch_i8_expand(stored, sv.perm, sv.status, codes, sx, st)
+                    : launch_i8_quantize_f16(x_dev, pv.dtype, n, pv.h_in, sv.perm, sv.status, codes, sx, st);
+        else if (!xq)
+            rc = launch_i8_quantize(x_dev, pv.dtype, pv.h_in, i8_view(codes, sx, n, pv.h_in), st);
+        if (rc) return rc;
         if (pv.dtype == LORA_F32) {
             s_parts = f32_shrink_parts(pv, n);
             rc = launch_f32_shrink(pv, sv, x_dev, s_buf, st);
-        } else if (n > 256 && shrink_tc_supported(pv)) {
+        } else if (n > kI8Tile && shrink_tc_supported(pv)) {
             rc = launch_shrink_tc(pv, sv, x_dev, s_buf, st);
         } else {
-            rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > 256, &s_parts);
+            rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > kI8Tile, &s_parts);
         }
     }
     if (rc) return rc;
+    const I8View wv = view_of(w);
     const I8Lora lora = {&pv, sv.idx, s_buf, s_parts};
-    if (few) return launch_i8_small(q, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
-    const I8Rows rows = {ws + L.codes_off, sx, sv.perm, n, pv.h_in};
-    if (n > kI8Tile) {
-        const I8View wv = view_of(w);
-        rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
-        if (rc) return rc;
-        const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, wv.rows, wv.cols};
-        rc = launch_i8_pair(rows, wrows, y_dev, pv.dtype, pv.h_out, sv.status, /*release=*/true, &lora, st);
-        if (rc || pv.dtype != LORA_F32) return rc;
-        return launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);
+    if (few) {
+        xv = xq ? stored : i8_view(codes, sx, n, pv.h_in);
+        return launch_i8_small(xv, wv, y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     }
-    return launch_i8_tile(rows, view_of(w), y_dev, pv.dtype, pv.h_out, sv.status, /*early_x=*/true, /*release=*/true, &lora, st);
+    const I8Rows rows = {codes, sx, sv.perm, n, pv.h_in};
+    if (n <= kI8Tile)
+        // x is stored by the kernel ahead where that makes the shrink too
+        return launch_i8_tile(rows, wv, y_dev, pv.dtype, pv.h_out, sv.status, /*early_x=*/!front, /*release=*/true, &lora, st);
+    rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
+    if (rc) return rc;
+    const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, wv.rows, wv.cols};
+    if (pv.dtype == LORA_F32) {
+        rc = launch_i8_pair(rows, wrows, y_dev, LORA_F32, pv.h_out, sv.status, /*release=*/true, nullptr, st);
+        return rc ? rc : launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);
+    }
+    if (separate(pv, n)) {
+        float* y32 = reinterpret_cast<float*>(ws + L.y32_off);
+        rc = launch_i8_pair(rows, wrows, y32, LORA_F32, pv.h_out, sv.status, /*release=*/true, nullptr, st);
+        return rc ? rc : launch_sum_expand(pv, sv, s_buf, s_parts, y32, y_dev, st);
+    }
+    return launch_i8_pair(rows, wrows, y_dev, pv.dtype, pv.h_out, sv.status, /*release=*/true, &lora, st);
 }
 
 }  // extern "C"

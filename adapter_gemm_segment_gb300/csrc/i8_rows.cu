@@ -155,31 +155,18 @@ __device__ __forceinline__ MaxPair max_pair(MaxPair a, MaxPair b) {
     return a.hi != a.hi ? a : take ? b : a;
 }
 // ---- quantise ----------------------------------------------------------------------------------------
-// F16: codes as float16 into x16 [rows][pitch], row r from row perm[r] of x (see launch_i8_quantize_f16).
-// U: vectors whose loads are in flight together.
-template <typename T, int U, bool VEC, bool F16>
-__global__ void __launch_bounds__(kRowThreads)
-i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t* perm, const int32_t* status, __half* x16) {
-    extern __shared__ __align__(16) uint8_t row_smem[];
-    __shared__ float red[kRowThreads / 32];
-    pdl_wait();
-    pdl_trigger();
+// One row by its G threads.  U: vectors whose loads are in flight together.  Codes go to out as bytes or float16.
+template <typename T, int U, bool VEC, typename C>
+__device__ __forceinline__ void quantise_row(const T* row, int cols, int pitch, const RowPlan& pl, int tid, Raw<T>* kept,
+                                             float* red, float* scale, C* out) {
     using Part = RowPart<T, VEC>;
-    const int G = pl.G, team = threadIdx.x / G, tid = threadIdx.x - team * G;
-    const long long r = (long long)blockIdx.x * (blockDim.x / G) + team;
-    if (r >= q.rows) return;  // (whole warps; G is the CTA where it is more than a warp)
-    const T* row = x + r * ld;
-    if constexpr (F16) {
-        if (status != nullptr && __ldcg(status) != LORA_OK) return;  // (perm is not valid either)
-        if (perm != nullptr) row = x + (long long)__ldcg(perm + r) * ld;
-    }
-    Raw<T>* kept = reinterpret_cast<Raw<T>*>(row_smem) + (size_t)team * pl.vecs;
+    const int G = pl.G;
     float m = 0.f;
     for (int i0 = tid; i0 < pl.vecs; i0 += U * G) {
         Raw<T> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i0 + u * G < pl.vecs) v[u] = Part::load(row, q.cols, i0 + u * G, tid, G);
+            if (i0 + u * G < pl.vecs) v[u] = Part::load(row, cols, i0 + u * G, tid, G);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (i0 + u * G >= pl.vecs) break;
@@ -198,14 +185,13 @@ i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t
         for (int w = 0; w < G / 32; ++w) m = max_nan(m, red[w]);
     }
     const float s = i8_scale(m);
-    if (tid == 0) q.scales[r] = s;
+    if (tid == 0) *scale = s;
     const I8Divisor d = i8_divisor(s);
     const bool plain = d.up == 1.f && d.inv != 0.f;
-    const int pitch = (int)q.pitch;
 #pragma unroll 2
     for (int i = tid; i < pl.vecs; i += G) {
         float f[8];
-        to8(pl.keep ? kept[i] : Part::load(row, q.cols, i, tid, G), f);
+        to8(pl.keep ? kept[i] : Part::load(row, cols, i, tid, G), f);
         uint32_t c[8];
         if (plain) {
             float rest[8], far = 0.f;
@@ -225,10 +211,125 @@ i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t
 #pragma unroll
             for (int e = 0; e < 8; ++e) c[e] = i8_code(f[e], d);
         }
-        if constexpr (F16)
-            Part::store_codes(x16 + r * pitch, pitch, i, tid, G, c);
+        Part::store_codes(out, pitch, i, tid, G, c);
+    }
+}
+
+// F16: codes as float16 into x16 [rows][pitch], row r from row perm[r] of x (see launch_i8_quantize_f16).
+template <typename T, int U, bool VEC, bool F16>
+__global__ void __launch_bounds__(kRowThreads)
+i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t* perm, const int32_t* status, __half* x16) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    __shared__ float red[kRowThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int team = threadIdx.x / pl.G, tid = threadIdx.x - team * pl.G;
+    const long long r = (long long)blockIdx.x * (blockDim.x / pl.G) + team;
+    if (r >= q.rows) return;  // (whole warps; G is the CTA where it is more than a warp)
+    const T* row = x + r * ld;
+    Raw<T>* kept = reinterpret_cast<Raw<T>*>(row_smem) + (size_t)team * pl.vecs;
+    if constexpr (F16) {
+        if (status != nullptr && __ldcg(status) != LORA_OK) return;  // (perm is not valid either)
+        if (perm != nullptr) row = x + (long long)__ldcg(perm + r) * ld;
+        quantise_row<T, U, VEC>(row, q.cols, (int)q.pitch, pl, tid, kept, red, q.scales + r, x16 + r * q.pitch);
+    } else {
+        quantise_row<T, U, VEC>(row, q.cols, (int)q.pitch, pl, tid, kept, red, q.scales + r, q.codes + r * q.pitch);
+    }
+}
+
+// ---- before the product of a small batch: x's codes and the per-token shrink, one launch -------------------
+// The first n CTAs each take a row of x: quantise it (or turn its stored codes into float16); the others each a
+// token, 8 rows of its adapter's A and a part of K, s[part][t][j] = (alpha / r) x[t] . A[j] over the part.  Both
+// read x, a few KB; bound by latency, which one launch less shortens (one token 4096 x 4096 float16: 25 us for
+// the linear as three launches).
+constexpr int kFrontThreads = 256;
+struct FrontArgs {
+    PoolView pool;
+    const int32_t* perm;    // rows of x16
+    const int32_t* idx;
+    const int32_t* status;
+    const void* x;
+    I8View q;               // quantised into (codes, or scales alone with x16), or (stored) expanded from
+    __half* x16;            // nullable: codes as bytes
+    float* scales;
+    float* s;
+    RowPlan pl;
+    int n, stored, rows, parts;  // rows: CTAs that take rows of x (n, or 0)
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kFrontThreads)
+i8_front_kernel(const FrontArgs a) {
+    extern __shared__ __align__(16) uint8_t row_smem[];
+    __shared__ float red[kFrontThreads / 32][8];
+    pdl_wait();
+    pdl_trigger();
+    const int status = __ldcg(a.status);  // (independent loads first)
+    const int h = a.pool.h_in, R = a.pool.R, tid = threadIdx.x;
+    if ((int)blockIdx.x < a.rows) {
+        const int r = blockIdx.x;
+        const int from = a.x16 && a.perm ? __ldcg(a.perm + r) : r;
+        if (status != LORA_OK) return;
+        if (a.stored) {
+            const int8_t* codes = a.q.codes + (size_t)from * a.q.pitch;
+            for (int k = tid * 16; k < (int)a.q.pitch; k += kFrontThreads * 16) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + k));
+                const uint2 c0 = i8_to_f16x4(w.x), c1 = i8_to_f16x4(w.y), c2 = i8_to_f16x4(w.z), c3 = i8_to_f16x4(w.w);
+                uint4* out = reinterpret_cast<uint4*>(a.x16 + (size_t)r * a.q.pitch + k);
+                out[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+                out[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
+            }
+            if (tid == 0) a.scales[r] = __ldg(a.q.scales + from);
+            return;
+        }
+        const T* row = static_cast<const T*>(a.x) + (size_t)from * h;
+        Raw<T>* kept = reinterpret_cast<Raw<T>*>(row_smem);
+        if (a.x16)
+            quantise_row<T, 2, VEC>(row, h, (int)a.q.pitch, a.pl, tid, kept, &red[0][0], a.scales + r, a.x16 + (size_t)r * a.q.pitch);
         else
-            Part::store_codes(q.codes + r * pitch, pitch, i, tid, G, c);
+            quantise_row<T, 2, VEC>(row, h, (int)a.q.pitch, a.pl, tid, kept, &red[0][0], a.scales + r, a.q.codes + (size_t)r * a.q.pitch);
+        return;
+    }
+    using Part = RowPart<T, VEC>;
+    const int groups = (R + 7) / 8, b = blockIdx.x - a.rows;
+    const int t = b / (groups * a.parts), g = b / a.parts % groups, p = b % a.parts;
+    const int slot = __ldcg(a.idx + t);
+    if (slot < 0 || status != LORA_OK) return;
+    const SlotEntry e = a.pool.table[slot];
+    if (g * 8 >= e.rank) return;  // (what reads s leaves out the columns past the rank)
+    const T* xr = static_cast<const T*>(a.x) + (size_t)t * h;
+    const T* Ab = static_cast<const T*>(a.pool.A) + ((size_t)slot * R + (size_t)g * 8) * h;
+    const int vecs = (h + 7) / 8, per = ((vecs + kFrontThreads - 1) / kFrontThreads + a.parts - 1) / a.parts * kFrontThreads;
+    float acc[8] = {};
+    for (int i0 = p * per; i0 < min(vecs, (p + 1) * per); i0 += kFrontThreads) {
+        const int i = i0 + tid;
+        if (Part::at(i, 0, tid, kFrontThreads) >= h) continue;
+        float xf[8];
+        Raw<T> av[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) av[r] = Part::load(Ab + (size_t)min(r, R - 1 - g * 8) * h, h, i, tid, kFrontThreads);
+        to8(Part::load(xr, h, i, tid, kFrontThreads), xf);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            float af[8];
+            to8(av[r], af);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[r] = fmaf(xf[c], af[c], acc[r]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        float v = acc[r];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if ((tid & 31) == 0) red[tid >> 5][r] = v;
+    }
+    __syncthreads();
+    if (tid < 8 && g * 8 + tid < R) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFrontThreads / 32; ++w) v += red[w][tid];
+        a.s[((size_t)p * a.n + t) * R + g * 8 + tid] = e.scale * v;
     }
 }
 
@@ -610,6 +711,51 @@ int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const i
         case LORA_F32: return quantize_t<float, true>(x, cols, q, perm, status, x16, st);
         case LORA_F16: return quantize_t<__half, true>(x, cols, q, perm, status, x16, st);
         default: return quantize_t<__nv_bfloat16, true>(x, cols, q, perm, status, x16, st);
+    }
+}
+
+// K parts of the front's shrink.
+int i8_front_parts(const PoolView& pv, int n) {
+    return std::max(1, std::min({(pv.h_in + 8 * kFrontThreads - 1) / (8 * kFrontThreads), 4, 256 / std::max(n, 1)}));
+}
+
+template <typename T> static int front_t(FrontArgs a, cudaStream_t st) {
+    // rows of x and of A on 16-byte boundaries
+    const bool vec = aligned16(a.x, a.pool.h_in, 2, sizeof(T));
+    const int vecs = (int)(a.q.pitch / 8);
+    a.pl.G = kFrontThreads;
+    a.pl.vecs = (vecs + kFrontThreads - 1) / kFrontThreads * kFrontThreads;
+    size_t smem = a.rows && !a.stored ? (size_t)a.pl.vecs * 8 * sizeof(T) : 0;
+    a.pl.keep = smem <= 48 * 1024 - 1024;
+    if (!a.pl.keep) smem = 0;
+    const long long grid = a.rows + (long long)a.n * ((a.pool.R + 7) / 8) * a.parts;
+    const void* fn = vec ? (const void*)i8_front_kernel<T, true> : (const void*)i8_front_kernel<T, false>;
+    void* args[] = {(void*)&a};
+    LORA_CUDA_TRY(launch_pdl(fn, dim3((unsigned)grid), dim3(kFrontThreads), smem, st, args));
+    return LORA_OK;
+}
+
+int launch_i8_front(const PoolView& pv, const SegView& sv, const void* x, const I8View* xq, void* codes, bool f16,
+                    float* scales, float* s, int* s_parts, cudaStream_t st) {
+    FrontArgs a;
+    memset(&a, 0, sizeof(a));
+    a.pool = pv;
+    a.perm = sv.perm;
+    a.idx = sv.idx;
+    a.status = sv.status;
+    a.x = x;
+    a.stored = xq != nullptr;
+    a.q = xq ? *xq : i8_view(codes, scales, sv.n, pv.h_in);
+    a.x16 = f16 ? static_cast<__half*>(codes) : nullptr;
+    a.scales = scales;
+    a.s = s;
+    a.n = sv.n;
+    a.rows = xq && !f16 ? 0 : sv.n;
+    a.parts = *s_parts = i8_front_parts(pv, sv.n);
+    switch (pv.dtype) {
+        case LORA_F32: return front_t<float>(a, st);
+        case LORA_F16: return front_t<__half>(a, st);
+        default: return front_t<__nv_bfloat16>(a, st);
     }
 }
 

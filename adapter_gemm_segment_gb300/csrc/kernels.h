@@ -127,6 +127,11 @@ int launch_fp4_decode(const Fp4View& x, const Fp4View& w, void* y, int dtype, lo
 // *s_parts K parts, in one launch (pools of any type whose adapters the per-token shrink suits).
 int launch_fp4_front(const PoolView& pv, const SegView& sv, const void* x, const Fp4View* q, float* s_out, int* s_parts,
                      cudaStream_t st);
+// y = y32 (float32 [n, h_out]) + s B^T of 16-bit pools, rounded once.
+int launch_sum_expand(const PoolView& pv, const SegView& sv, const float* s_in, int s_parts, const float* y32, void* y,
+                      cudaStream_t st);
+// Whether a float32 batch takes a per-token shrink beside x's codes rather than the tiled one.
+bool f32_front(const PoolView& pv, int n);
 // float32 pools: the shrink in K parts (s_out [f32_shrink_parts][n][R]), and y += s B^T.
 int f32_shrink_parts(const PoolView& pv, int n);
 int launch_f32_shrink(const PoolView& pv, const SegView& sv, const void* x, float* s_out, cudaStream_t st);
@@ -160,6 +165,12 @@ int launch_i8_rmsnorm(const lora_i8_norm& args, cudaStream_t st);
 int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const int32_t* perm, const int32_t* status,
                            void* x16, float* scales, cudaStream_t st);
 int launch_i8_expand(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales, cudaStream_t st);
+// For small batches, one launch: x's codes (as bytes, rows as x's; or f16: as float16, rows in the order of the
+// segments; xq: from its stored form, nothing to do where bytes will serve) and the per-token shrink in *s_parts K
+// parts, the columns past an adapter's rank not written.
+int i8_front_parts(const PoolView& pv, int n);
+int launch_i8_front(const PoolView& pv, const SegView& sv, const void* x, const I8View* xq, void* codes, bool f16,
+                    float* scales, float* s, int* s_parts, cudaStream_t st);
 // The LoRA term of a product: the slot of each token and the shrink output in K parts.
 struct I8Lora {
     const PoolView* pool;
