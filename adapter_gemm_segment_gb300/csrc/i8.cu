@@ -251,10 +251,12 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         if (pv.dtype == LORA_F32) {
             s_parts = f32_shrink_parts(pv, n);
             rc = launch_f32_shrink(pv, sv, x_dev, s_buf, st);
-        } else if (n > kI8Tile && shrink_tc_supported(pv)) {
+        } else if (n <= kI8Tile || separate(pv, n)) {
+            rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/false, &s_parts);
+        } else if (shrink_tc_supported(pv)) {
             rc = launch_shrink_tc(pv, sv, x_dev, s_buf, st);
         } else {
-            rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/n > kI8Tile, &s_parts);
+            rc = launch_shrink(pv, sv, x_dev, s_buf, st, /*tiled=*/true, &s_parts);
         }
     }
     if (rc) return rc;

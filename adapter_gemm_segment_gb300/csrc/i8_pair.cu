@@ -82,7 +82,8 @@ __device__ __forceinline__ void split_tf32(float s, uint32_t& hi, uint32_t& lo) 
 }
 
 // Sum over b times s of what the LoRA blocks leave out: b an infinity or a NaN.
-template <typename T> __device__ __noinline__ float bad_dot(const I8PairArgs& a, int slot, int row, int o, float acc) {
+template <typename T> __device__ __noinline__ float bad_dot(const I8PairArgs& a, int slot, int row, int o) {
+    float acc = 0.f;
     const T* b = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + o) * a.R;
     for (int j = 0; j < a.table[slot].rank; ++j) {
         const float f = to_f32<T>(b[j]);
@@ -463,7 +464,36 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 ok = false;
                 break;
             }
+            // values first, which leaves the LoRA accumulator to the next tile's MMAs, then the stores
             const uint32_t laddr = tmem + lbuf * N + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll
+            for (int i = 0; i < kJUnits; ++i) {
+                const int u = 2 * i + hv;
+                if (u < units) {
+                    uint32_t r[16];
+                    if (lora) {
+                        __syncwarp();
+                        tmem_ld16(laddr + u * 16, r);
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 sx = *reinterpret_cast<const float4*>(sx_sm + u * 16 + e);
+                        const float s4[4] = {sx.x, sx.y, sx.z, sx.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float v = i8_scaled(sum[i][e + k], s4[k], sw);
+                            if (lora) v += __uint_as_float(r[e + k]);
+                            sum[i][e + k] = __float_as_int(v);
+                        }
+                    }
+                }
+            }
+            if constexpr (FUSE) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && lora) mbar_arrive_cluster_relaxed(acc_empty0 + static_cast<uint32_t>(lbuf) * 8u);
+            }
 #pragma unroll 1
             for (int i = 0; i < kJUnits; ++i) {
                 const int u = 2 * i + hv;
@@ -473,27 +503,13 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 for (int j = 0; j < kJUnits; ++j)
                     if (j == i)
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4) {
-                            const float4 sx = *reinterpret_cast<const float4*>(sx_sm + u * 16 + e);
-                            v[e] = i8_scaled(sum[j][e], sx.x, sw);
-                            v[e + 1] = i8_scaled(sum[j][e + 1], sx.y, sw);
-                            v[e + 2] = i8_scaled(sum[j][e + 2], sx.z, sw);
-                            v[e + 3] = i8_scaled(sum[j][e + 3], sx.w, sw);
-                        }
+                        for (int e = 0; e < 16; ++e) v[e] = __int_as_float(sum[j][e]);
                 if constexpr (FUSE) {
-                    if (lora) {
-                        uint32_t r[16];
-                        __syncwarp();
-                        tmem_ld16(laddr + u * 16, r);
-                        tmem_ld_wait();
+                    if (left_out)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float l = __uint_as_float(r[e]);
-                            if (left_out && slot_sm[u * 16 + e] >= 0 && o < a.h_out)
-                                l = bad_dot<T>(a, slot_sm[u * 16 + e], row_sm[u * 16 + e], o, l);
-                            v[e] += l;
-                        }
-                    }
+                        for (int e = 0; e < 16; ++e)
+                            if (slot_sm[u * 16 + e] >= 0 && o < a.h_out)
+                                v[e] += bad_dot<T>(a, slot_sm[u * 16 + e], row_sm[u * 16 + e], o);
                 }
                 if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -527,12 +543,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 }
             }
             if constexpr (FUSE) {
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (lora) mbar_arrive_cluster_relaxed(acc_empty0 + static_cast<uint32_t>(lbuf) * 8u);
-                    mbar_arrive(&tile_done[local & 1]);
-                }
+                if (lane == 0) mbar_arrive(&tile_done[local & 1]);
             }
         }
         if (!ok && a.status && lane == 0) report_timeout_status(a.status);
