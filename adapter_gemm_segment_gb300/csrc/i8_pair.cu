@@ -40,14 +40,16 @@ using namespace ptx;
 constexpr int kJM = 128;           // features per CTA
 constexpr int kJMaxN = 256;        // tokens per pair tile, at most
 constexpr int kJThreads = 512;
-// registers a thread of the warpgroups 0, 1 and 2-3: together what the block is launched with, 128 a thread
-constexpr int kJRegs0 = 56, kJRegs1 = 72, kJRegs2 = 192;
+// registers a thread of the warpgroups 0, 1 and 2-3: together what the block is launched with, 128 a thread.  (With
+// 192 the drain spills: the prefill batch of 16384 x 4096 x 4096 with rank 16 took 478 us instead of 437.)
+constexpr int kJRegs0 = 56, kJRegs1 = 56, kJRegs2 = 200;
 static_assert(kJRegs0 + kJRegs1 + 2 * kJRegs2 == 4 * 128, "register split");
 constexpr int kJChunk = 16;        // steps of 64 codes between two readings of the accumulator
 constexpr uint32_t kJWBytes = kJM * 128;
 constexpr int kJMaxStages = 8;
 constexpr int kJUnits = kJMaxN / 32;  // 16-token units of a drain warp, at most
 // a LoRA block: 8 columns of B for 128 features, then of s in two parts for N / 2 <= 128 tokens
+constexpr int kJBufs = 4;  // blocks ahead of the MMAs: a tile of two adapters of rank 16 takes four
 constexpr int kJLoraB = kJM * 32, kJLoraBytes = kJLoraB + 2 * (kJMaxN / 2) * 32;
 constexpr size_t kJTail = kJMaxN * 12 + 64 * 4 + 256 * 4 + 16 + 512 + 1024;
 constexpr size_t kJSmemMax = 227 * 1024;
@@ -81,15 +83,16 @@ __device__ __forceinline__ void split_tf32(float s, uint32_t& hi, uint32_t& lo) 
     lo = (__float_as_uint(s - __uint_as_float(hi)) + 0x1000u) & 0xffffe000u;
 }
 
-// Sum over b times s of what the LoRA blocks leave out: b an infinity or a NaN.
-template <typename T> __device__ __noinline__ float bad_dot(const I8PairArgs& a, int slot, int row, int o) {
-    float acc = 0.f;
+// Adds to y what the LoRA blocks left out: the products of B's infinities and NaN.
+template <typename T> __device__ __noinline__ void add_bad(const I8PairArgs& a, int slot, int row, int o) {
     const T* b = static_cast<const T*>(a.B) + ((size_t)slot * a.h_out + o) * a.R;
+    float acc = 0.f;
     for (int j = 0; j < a.table[slot].rank; ++j) {
         const float f = to_f32<T>(b[j]);
         if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) acc = fmaf(f, a.s[(size_t)row * a.R + j], acc);
     }
-    return acc;
+    T* y = static_cast<T*>(a.y) + (long long)row * a.ldy + o;
+    if (acc != 0.f) *y = from_f32<T>(to_f32<T>(*y) + acc);
 }
 
 template <typename T, bool FUSE>
@@ -99,8 +102,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint8_t* smem = smem_align(smem_raw, 1024);
     const int stages = a.stages, N = a.N;
     const uint32_t stage_bytes = kJWBytes + static_cast<uint32_t>(N) * 64;  // 128 features, N / 2 tokens of 64 float16
-    uint8_t* lora_sm = smem + stages * stage_bytes;              // [2] blocks
-    int* row_sm = reinterpret_cast<int*>(lora_sm + (FUSE ? 2 * kJLoraBytes : 0));  // [N] row of y of a token of the tile
+    uint8_t* lora_sm = smem + stages * stage_bytes;              // [kJBufs] blocks
+    int* row_sm = reinterpret_cast<int*>(lora_sm + (FUSE ? kJBufs * kJLoraBytes : 0));  // [N] row of y of a token of the tile
     int* slot_sm = row_sm + kJMaxN;                              // [N] its adapter
     float* sx_sm = reinterpret_cast<float*>(slot_sm + kJMaxN);   // [N] its scale
     uint32_t* seen = reinterpret_cast<uint32_t*>(sx_sm + kJMaxN);  // [64] slots the tile's tokens name
@@ -110,17 +113,17 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint64_t* empty = full + kJMaxStages;      // (multicast)
     uint64_t* acc_full = empty + kJMaxStages;  // [2] (multicast)
     uint64_t* acc_empty = acc_full + 2;        // [2] even CTA (8 warps of both CTAs)
-    uint64_t* lora_own = acc_empty + 2;        // [2] a LoRA block of this CTA is written (4 warps)
-    uint64_t* lora_peer = lora_own + 2;        // [2] even CTA: the odd CTA's block is written (relayed)
-    uint64_t* lora_empty = lora_peer + 2;      // [2] (multicast)
+    uint64_t* lora_own = acc_empty + 2;        // [kJBufs] a LoRA block of this CTA is written (4 warps)
+    uint64_t* lora_peer = lora_own + kJBufs;   // [kJBufs] even CTA: the odd CTA's block is written (relayed)
+    uint64_t* lora_empty = lora_peer + kJBufs;  // [kJBufs] (multicast)
     // by parity of the tile (the warps that build blocks may be a tile ahead of the others):
-    uint64_t* linfo = lora_empty + 2;          // [2] the tile's number of LoRA blocks is known
+    uint64_t* linfo = lora_empty + kJBufs;          // [2] the tile's number of LoRA blocks is known
     uint64_t* tile_done = linfo + 2;           // [2] it has been used (8 drain warps, the MMA or relay thread)
     uint64_t* drained = tile_done + 2;         // even CTA: every MMA has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
     // abort, -, then by parity of the tile: [2] LoRA blocks, [2] 1 + the last tile whose blocks left products out
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    static_assert((2 * kJMaxStages + 15) * 8 + 28 <= 512, "barrier area");
+    static_assert((2 * kJMaxStages + 3 * kJBufs + 9) * 8 + 28 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -136,11 +139,13 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 16);
+            mbar_init(&linfo[b], 1);
+            mbar_init(&tile_done[b], 9);
+        }
+        for (int b = 0; b < kJBufs; ++b) {
             mbar_init(&lora_own[b], 4);
             mbar_init(&lora_peer[b], 1);
             mbar_init(&lora_empty[b], 1);
-            mbar_init(&linfo[b], 1);
-            mbar_init(&tile_done[b], 9);
         }
         mbar_init(drained, 1);
         for (int i = 0; i < 6; ++i) flags[i] = 0;
@@ -236,9 +241,9 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     }
                     ++chunk;
                     for (int b = 0; b < blocks; ++b, ++lb) {
-                        const int lbuf = lb & 1;
-                        if (!mbar_wait(&lora_own[lbuf], (lb >> 1) & 1, flags) ||
-                            !mbar_wait_cluster(&lora_peer[lbuf], (lb >> 1) & 1, flags)) {
+                        const int lbuf = lb % kJBufs;
+                        if (!mbar_wait(&lora_own[lbuf], (lb / kJBufs) & 1, flags) ||
+                            !mbar_wait_cluster(&lora_peer[lbuf], (lb / kJBufs) & 1, flags)) {
                             ok = false;
                             break;
                         }
@@ -271,8 +276,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 const int blocks = ok ? flags[2 + (local & 1)] : 0;
                 if (ok) mbar_arrive(&tile_done[local & 1]);
                 for (int b = 0; b < blocks && ok; ++b, ++lb) {
-                    ok = mbar_wait(&lora_own[lb & 1], (lb >> 1) & 1, flags);
-                    if (ok) mbar_arrive_cluster(peer0 + static_cast<uint32_t>(lb & 1) * 8u);
+                    ok = mbar_wait(&lora_own[lb % kJBufs], (lb / kJBufs) & 1, flags);
+                    if (ok) mbar_arrive_cluster(peer0 + static_cast<uint32_t>(lb % kJBufs) * 8u);
                 }
             }
             if (!ok && a.status) report_timeout_status(a.status);
@@ -354,11 +359,11 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 for (int b = 0; b < blocks; ++b, ++lb) {
                     now = next;
                     if (b + 1 < blocks) load(next);  // a block ahead
-                    if (lb >= 2 && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lb & 1], ((lb >> 1) & 1) ^ 1, flags))) {
+                    if (lb >= kJBufs && !__all_sync(0xffffffffu, mbar_wait(&lora_empty[lb % kJBufs], ((lb / kJBufs) & 1) ^ 1, flags))) {
                         ok = false;
                         break;
                     }
-                    uint8_t* blk = lora_sm + (lb & 1) * kJLoraBytes;
+                    uint8_t* blk = lora_sm + (lb % kJBufs) * kJLoraBytes;
                     if (nonfinite8<T>(now.b)) {
                         now.b = finite8<T>(now.b);
                         flags[4 + (local & 1)] = local + 1;
@@ -383,7 +388,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     }
                     fence_proxy_async_smem();  // read by the tensor cores
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&lora_own[lb & 1]);
+                    if (lane == 0) mbar_arrive(&lora_own[lb % kJBufs]);
                 }
                 if (!ok) flags[0] = 1;
             }
@@ -504,13 +509,6 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     if (j == i)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] = __int_as_float(sum[j][e]);
-                if constexpr (FUSE) {
-                    if (left_out)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (slot_sm[u * 16 + e] >= 0 && o < a.h_out)
-                                v[e] += bad_dot<T>(a, slot_sm[u * 16 + e], row_sm[u * 16 + e], o);
-                }
                 if constexpr (sizeof(T) == 4) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -543,6 +541,11 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                 }
             }
             if constexpr (FUSE) {
+                __syncwarp();
+                if (left_out && store && o < a.h_out)
+#pragma unroll 1
+                    for (int t = 0; t < N; ++t)  // this warp's tokens: infinities and NaN onto what it has stored
+                        if ((t / 16 & 1) == hv && slot_sm[t] >= 0) add_bad<T>(a, slot_sm[t], row_sm[t], o);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tile_done[local & 1]);
             }
@@ -624,7 +627,7 @@ static int launch_pair_t(const I8Rows& x, const I8Rows& w, void* y, long long ld
         a.s = lora->s_in;
         a.R = pv.R;
     }
-    const size_t stage_bytes = kJWBytes + (size_t)a.N * 64, tail = kJTail + (FUSE ? 2 * kJLoraBytes : 0);
+    const size_t stage_bytes = kJWBytes + (size_t)a.N * 64, tail = kJTail + (FUSE ? kJBufs * kJLoraBytes : 0);
     a.stages = (int)std::min<size_t>((kJSmemMax - tail) / stage_bytes, kJMaxStages);
     CUtensorMap mW, mX;
     int rc = make_map(&mW, w.x16, 0, pitch, w.rows, kJM);

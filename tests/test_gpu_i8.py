@@ -353,3 +353,225 @@ def test_linear(lib, dtype, n, h_in, h_out, ranks, r_max, p_base):
 @pytest.mark.parametrize("n,h_in,h_out,r_max", [(3, 37, 5, 3), (20, 101, 33, 5), (150, 77, 131, 7), (400, 333, 91, 12)])
 def test_linear_float32_odd_sizes(lib, n, h_in, h_out, r_max):
     check_linear(lib, wl.random_case(n, n, h_in, h_out, [r_max, 1, 2], r_max=r_max, dtype=torch.float32, p_base=0.2))
+
+
+@pytest.mark.parametrize("n,slots,r_max", [(300, 100, 8), (900, 60, 64), (2000, 3, 256), (1700, 100, 24), (5000, 100, 8)])
+def test_linear_many_adapters_in_large_batches(lib, n, slots, r_max):
+    """The separate expand (few tokens a slot) and tiles of several adapters."""
+    check_linear(lib, wl.random_case(n + slots, n, 136, 264, [max(1, r_max // (1 + s % 3)) for s in range(slots)], r_max=r_max,
+                                     dtype=torch.bfloat16, p_base=0.1))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 7, 40, 130, 300, 700])
+def test_adapters_that_are_not_finite_reach_their_own_tokens_only(lib, dtype, n):
+    slots = 3 if n < 100 else 4
+    case = wl.random_case(n, n, 264, 136, [8] * slots, r_max=8, dtype=dtype, p_base=0.1)
+    case.idx[0] = 1
+    ad = case.adapters
+    clean = make_pool(lib, case)
+    w, x = stored(lib, case.W), case.x.cuda()
+    seg = clean.segment(case.idx.cuda())
+    want = clean.i8_linear(w, x, seg).cpu()
+    ad.B[1][5, 3] = float("inf")
+    ad.B[1][9, 0] = float("nan")
+    ad.A[slots - 1][2, 7] = float("nan")
+    pool = make_pool(lib, case)
+    got = pool.i8_linear(w, x, pool.segment(case.idx.cuda())).cpu()
+    idx = case.idx
+    ok = torch.ones_like(got, dtype=torch.bool)
+    ok[idx == 1, 5] = False
+    ok[idx == 1, 9] = False
+    ok[idx == slots - 1] = False
+    assert torch.equal(got[ok], want[ok])
+    assert got[idx == slots - 1].isnan().all()
+    assert got[idx == 1][:, 9].isnan().all() and not got[idx == 1][:, 5].isfinite().any()
+    clean.close()
+    pool.close()
+
+
+@pytest.mark.parametrize("n", [1, 8, 9, 64, 200, 300])
+def test_refused_batches_leave_y_untouched(lib, n):
+    case = wl.random_case(n, n, 264, 136, [8, 8], r_max=8, dtype=torch.float16)
+    pool = make_pool(lib, case)
+    idx = case.idx.clone()
+    idx[n // 2] = 7
+    seg = pool.segment(idx.cuda())
+    y = torch.full((n, 136), 7.0, dtype=torch.float16, device="cuda")
+    pool.i8_linear(stored(lib, case.W), case.x.cuda(), seg, y=y)
+    assert lib.lora_segment_status(seg) == lib.LORA_EIDX
+    assert (y == 7.0).all()
+    pool.close()
+
+
+def test_empty_batches(lib):
+    pool = lib.LoraPool(64, 32, 8, 2, torch.float16, "cuda")
+    w = stored(lib, gauss(32, 64, 1))
+    x = torch.empty(0, 64, dtype=torch.float16, device="cuda")
+    seg = pool.segment(torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert pool.i8_linear(w, x, seg).shape == (0, 32)
+    q = lib.lora_i8_quantize(x, lib.I8Matrix(0, 64))
+    y = torch.empty(0, 32, device="cuda")
+    lib.lora_i8_matmul(q, w, y)
+    lib.lora_i8_dequantize(q, x)
+    lib.lora_i8_rmsnorm(x, torch.ones(64, dtype=torch.float16, device="cuda"), 1e-5, out=q, y=x)
+    pool.close()
+
+
+def test_workspaces(lib):
+    pool = lib.LoraPool(512, 256, 16, 100, torch.bfloat16, "cuda")
+    last = 0
+    for n in (0, 1, 2, 8, 9, 20, 64, 100, 256, 257, 300, 1000, 1599, 1600, 5000):
+        need = lib.lora_i8_linear_workspace_bytes(pool.handle, n)
+        assert need >= last
+        last = need
+    w = stored(lib, gauss(256, 512, 1))
+    for n in (3, 30, 300):
+        x = torch.zeros(n, 512, dtype=torch.bfloat16, device="cuda")
+        seg = pool.segment(torch.full((n,), -1, dtype=torch.int32, device="cuda"))
+        y = torch.empty(n, 256, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(lib.lora_i8_linear_workspace_bytes(pool.handle, n), dtype=torch.uint8, device="cuda")
+        lib.lora_i8_linear_fwd(pool.handle, w, x, y, seg, ws)
+        with pytest.raises(lib.LoraError) as e:
+            lib.lora_i8_linear_fwd(pool.handle, w, x, y, seg, ws[:-1])
+        assert e.value.code == lib.LORA_ENOSPACE
+        with pytest.raises(lib.LoraError) as e:
+            lib.lora_i8_linear_fwd(pool.handle, w, x, y, seg, ws, xq=lib.I8Matrix(n + 1, 512))
+        assert e.value.code == lib.LORA_EINVAL
+    with pytest.raises(lib.LoraError) as e:
+        pool.i8_linear(stored(lib, gauss(255, 512, 1)), x, seg, y=y)
+    assert e.value.code == lib.LORA_EINVAL
+    pool.close()
+
+
+# ---- together --------------------------------------------------------------------------------------
+
+class Layer:
+    """A norm with its residual and two projections over 8-bit bases that share its output."""
+
+    def __init__(self, lib, h, dtype, seed, slots=5):
+        self.lib, self.h = lib, h
+        self.case = [wl.random_case(seed + i, 4, h, o, [8, 4, 8, 2, 8][:slots], r_max=8, dtype=dtype) for i, o in enumerate((h, 2 * h))]
+        self.pools = [make_pool(lib, c) for c in self.case]
+        self.W = [c.W for c in self.case]
+        self.w = [stored(lib, c.W) for c in self.case]
+        self.gamma = (1 + 0.1 * gauss(1, h, seed)[0]).to(dtype)
+        self.g = self.gamma.cuda()
+
+    def run(self, x, res, seg, q, y, out, stream=None):
+        self.lib.lora_i8_rmsnorm(x, self.g, 1e-5, out=q, y=y, residual=res, stream=stream)
+        for pool, w, o in zip(self.pools, self.w, out):
+            pool.i8_linear(w, y, seg, xq=q, y=o, stream=stream)
+
+    def buffers(self, n, dtype):
+        lib = self.lib
+        return (lib.I8Matrix(n, self.h), torch.empty(n, self.h, dtype=dtype, device="cuda"),
+                [torch.empty(n, w.rows, dtype=dtype, device="cuda") for w in self.w])
+
+    def reference(self, x, res, idx):
+        h = (x.double() + res.double()).to(x.dtype)
+        v = Q.rmsnorm(h, self.gamma, 1e-5)
+        y = torch.from_numpy(v).to(x.dtype)
+        codes = Q.quantise(v)
+        return h, [linear_reference(wl.LinearCase("layer", y, W, c.adapters, idx), codes) for W, c in zip(self.W, self.case)]
+
+
+@pytest.mark.parametrize("n", [1, 6, 50, 300])
+def test_norm_and_projections(lib, n):
+    """As they are used: the norm's codes and values go to the projections, on another stream than the default."""
+    dtype = torch.bfloat16
+    layer = Layer(lib, 256, dtype, 11)
+    x, res = gauss(n, 256, 1).to(dtype), gauss(n, 256, 2, scale=2.0).to(dtype)
+    idx = torch.randint(-1, 5, (n,), generator=torch.Generator().manual_seed(n), dtype=torch.int32)
+    stream = torch.cuda.Stream()
+    q, y, out = layer.buffers(n, dtype)
+    xd, rd, di = x.cuda(), res.cuda(), idx.cuda()
+    torch.cuda.synchronize()
+    seg = layer.pools[0].segment(di, stream=stream)
+    layer.run(xd, rd, seg, q, y, out, stream=stream)
+    stream.synchronize()
+    h, refs = layer.reference(x, res, idx)
+    assert torch.equal(rd.cpu(), h)
+    for got, (ref, bound) in zip(out, refs):
+        # y (the LoRA term's input) may round the other way where float32 and float64 differ: a unit of the LoRA term
+        err = np.abs(got.cpu().double().numpy() - ref)
+        assert (err <= 2 * bound + 2.0 ** -7 * np.abs(ref).max() * 0.01).all()
+    for p in layer.pools:
+        p.close()
+
+
+def test_two_graphs_and_an_eager_call_share_nothing(lib):
+    """Two captured layers replayed on two streams at once, an eager call between them: each its own result."""
+    dtype = torch.bfloat16
+    layer = Layer(lib, 512, dtype, 21)
+    runs = []
+    for n, seed in ((20, 1), (300, 2)):
+        x, res = gauss(n, 512, seed).to(dtype).cuda(), gauss(n, 512, seed + 7).to(dtype).cuda()
+        idx = torch.randint(-1, 5, (n,), generator=torch.Generator().manual_seed(n), dtype=torch.int32).cuda()
+        seg = layer.pools[0].segment(idx)
+        want_res = res.clone()
+        q, y, want = layer.buffers(n, dtype)
+        layer.run(x, want_res, seg, q, y, want)
+        stream = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        q, y, out = layer.buffers(n, dtype)
+        r = res.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            layer.run(x, r, seg, q, y, out)
+        runs.append((graph, stream, x, res, r, seg, q, y, out, want, want_res))
+    eager = layer.buffers(20, dtype)
+    for _ in range(20):
+        for run in runs:
+            run[4].copy_(run[3])
+            for o in run[8]:
+                o.zero_()
+        er = runs[0][3].clone()
+        torch.cuda.synchronize()
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        layer.run(runs[0][2], er, runs[0][5], *eager)
+        torch.cuda.synchronize()
+        for _, _, _, _, r, _, _, _, out, want, want_res in runs:
+            assert torch.equal(r, want_res)
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(torch.equal(a, b) for a, b in zip(eager[2], runs[0][9]))
+    for p in layer.pools:
+        p.close()
+
+
+def test_repeated_calls_give_the_same_bits(lib):
+    for n in (1, 30, 200, 400, 3000):
+        case = wl.random_case(n, n, 1032, 392, [16] * 10, r_max=16, dtype=torch.float16, p_base=0.2)
+        pool = make_pool(lib, case)
+        w, x = stored(lib, case.W), case.x.cuda()
+        seg = pool.segment(case.idx.cuda())
+        first = pool.i8_linear(w, x, seg)
+        for _ in range(5):
+            assert torch.equal(pool.i8_linear(w, x, seg), first)
+        pool.close()
+
+
+def test_weights_quantised_right_before_their_product(lib):
+    """The products load their weight ahead of the kernel before them: a weight just stored is complete all the same."""
+    x = gauss(64, 2048, 1, torch.bfloat16).cuda()
+    for n in (2, 64):
+        q = lib.lora_i8_quantize(x[:n], lib.I8Matrix(n, 2048))
+        w = lib.I8Matrix(1024, 2048)
+        y = torch.empty(n, 1024, device="cuda")
+        pool = lib.LoraPool(2048, 1024, 8, 1, torch.bfloat16, "cuda")
+        seg = pool.segment(torch.full((n,), -1, dtype=torch.int32, device="cuda"))
+        for seed in range(6):
+            W = torch.randn(1024, 2048, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").bfloat16()
+            torch.cuda.synchronize()
+            lib.lora_i8_quantize(W, w)
+            lib.lora_i8_matmul(q, w, y)
+            lib.lora_i8_quantize(-W, w)
+            z = pool.i8_linear(w, x[:n], seg)
+            # (whole-number sums: of products of values, 64 bits each, float64 would round sums that are 0)
+            (cx, sx), (cw, sw) = Q.quantise(x[:n]), Q.quantise(W)
+            ref = torch.from_numpy(Q.sums(cx, cw) * sx.astype(np.float64)[:, None] * sw.astype(np.float64))
+            assert ((y.cpu().double() - ref).abs() <= 2.0 ** -20 * ref.abs() + 1e-30).all()
+            assert ((z.cpu().double() + ref).abs() <= 2.0 ** -7.9 * ref.abs() + 1e-30).all()
+        pool.close()
