@@ -700,6 +700,10 @@ class I8Matrix:
         self.struct = lora_i8_matrix(self._mem[0].data_ptr(), self._mem[1].data_ptr(), self.rows, self.cols)
 
     @property
+    def pointer(self):
+        return ctypes.pointer(self.struct)
+
+    @property
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self._mem)
 
@@ -726,24 +730,28 @@ def lora_i8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Opti
     residual_out, y: [rows, cols] of one dtype, contiguous rows, any row stride; weight [cols]."""
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
-    rows, cols = x.shape
     if residual is not None and residual_out is None:
         residual_out = residual
-    a = lora_i8_norm()
-    a.rows, a.cols, a.eps, a.dtype = rows, cols, float(eps), TORCH_TO_LORA.get(x.dtype, -1)
-    for t, name, ptr, ld in ((x, "x", "x_dev", "ldx"), (residual, "residual", "residual_dev", "ldr"),
-                             (residual_out, "residual_out", "residual_out_dev", "ldro"), (y, "y", "y_dev", "ldy")):
-        if t is not None:
-            dt, stride = _rows_of(t, rows, cols, name)
-            if t.dtype is not x.dtype:
-                raise ValueError(f"{name} must be {x.dtype}")
-            setattr(a, ptr, t.data_ptr())
-            setattr(a, ld, stride)
-    if weight.dtype is not x.dtype or weight.shape != (cols,):
-        raise ValueError(f"weight must be {x.dtype} [{cols}]")
-    a.weight_dev = _dev(weight, "weight").data_ptr()
-    if out is not None:
-        a.out = ctypes.pointer(out.struct)
+    shape, dtype = x.shape, x.dtype
+    rows, cols = shape
+    dt, ldx = _rows_of(x, rows, cols, "x")
+
+    def like_x(t, name):  # address and row stride
+        if t is None:
+            return None, 0
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}")
+        if t.shape == shape and t.is_contiguous() and t.is_cuda:  # (the usual case, in half the time)
+            return t.data_ptr(), cols
+        return t.data_ptr(), _rows_of(t, rows, cols, name)[1]
+
+    res, ldr = like_x(residual, "residual")
+    ro, ldro = like_x(residual_out, "residual_out")
+    yp, ldy = like_x(y, "y")
+    if weight.dtype is not dtype or weight.dim() != 1 or weight.numel() != cols:
+        raise ValueError(f"weight must be {dtype} [{cols}]")
+    a = lora_i8_norm(x.data_ptr(), res, _dev(weight, "weight").data_ptr(), ro, yp, None if out is None else out.pointer,
+                     ldx, ldr, ldro, ldy, rows, cols, dt, eps)
     _check(_lib.lora_i8_rmsnorm(ctypes.byref(a), _stream(stream)))
 
 
