@@ -94,7 +94,20 @@ template <typename T, bool VEC> struct RowPart {
             }
         }
     }
-    // codes (lowest bytes of c; 0 past cols, up to pitch)
+    // codes, four a word (0 past cols, up to pitch)
+    static __device__ __forceinline__ void store_words(int8_t* row, int pitch, int i, int tid, int G, uint2 w) {
+        const int k = at(i, 0, tid, G);
+        if (VEC) {
+            if (k < pitch) *reinterpret_cast<uint2*>(row + k) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = at(i, e, tid, G);
+                if (j < pitch) row[j] = static_cast<int8_t>((e < 4 ? w.x : w.y) >> (8 * (e & 3)));
+            }
+        }
+    }
+    // codes (lowest bytes of c)
     static __device__ __forceinline__ void store_codes(int8_t* row, int pitch, int i, int tid, int G, const uint32_t (&c)[8]) {
         const int k = at(i, 0, tid, G);
         if (VEC) {
@@ -188,7 +201,7 @@ __device__ __forceinline__ void quantise_row(const T* row, int cols, int pitch, 
     if (tid == 0) *scale = s;
     const I8Divisor d = i8_divisor(s);
     const bool plain = d.up == 1.f && d.inv != 0.f;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = tid; i < pl.vecs; i += G) {
         float f[8];
         to8(pl.keep ? kept[i] : Part::load(row, cols, i, tid, G), f);
@@ -447,15 +460,29 @@ __device__ __forceinline__ NormRow norm_row(Two ss, MaxPair m, int cols, float e
     }
     return o;
 }
-// The code of an element h f w whose quotient v = k + rest lies next to the border of two.
-template <bool EXACT>
-__device__ __forceinline__ int norm_border(float h, float w, float f, const NormRow& o, float v, int k) {
-    const float gh = h * f, u = __fmul_rn(gh, w), uc = u * o.c;
-    float rest = fmaf(uc, o.g.hi, -v) + uc * o.g.lo;
-    if (!EXACT) rest += fmaf(gh, w, -u) * o.c * o.g.hi;  // (16-bit numbers' products are exact)
-    const int side = v > static_cast<float>(k) ? 1 : -1;
-    const float past = side * ((v - (static_cast<float>(k) + 0.5f * side)) + rest);
-    return past > 0.f || (past == 0.f && (k & 1) != 0) ? k + side : k;
+// Codes of eight elements h f w, the first four in x: those next to the border of two, or of a row with a tiny
+// scale.  (Out of line: in line its registers cost the common path occupancy, 144 us against 123 for 16384 x 4096.)
+template <typename T> __device__ __noinline__ uint2 norm_codes(Raw<T> hr, Raw<T> wr, float f, NormRow o) {
+    constexpr bool EXACT = sizeof(T) == 2;
+    float h[8], w[8];
+    to8(hr, h);
+    to8(wr, w);
+    uint32_t c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float gh = h[e] * f, u = __fmul_rn(gh, w[e]), uc = u * o.c, v = __fmul_rn(uc, o.g.hi);
+        // (a tiny scale is rounded coarsely: quotients may pass 127)
+        int k = static_cast<int>(fminf(fmaxf(rintf(v), -127.f), 127.f));
+        if (fabsf(v - static_cast<float>(k)) > 0.4999f) {
+            float rest = fmaf(uc, o.g.hi, -v) + uc * o.g.lo;
+            if (!EXACT) rest += fmaf(gh, w[e], -u) * o.c * o.g.hi;  // (16-bit numbers' products are exact)
+            const int side = v > static_cast<float>(k) ? 1 : -1;
+            const float past = side * ((v - (static_cast<float>(k) + 0.5f * side)) + rest);
+            if (past > 0.f || (past == 0.f && (k & 1) != 0)) k += side;
+        }
+        c[e] = static_cast<uint32_t>(min(max(k, -127), 127));
+    }
+    return make_uint2(i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7]));
 }
 
 template <typename T, int U, bool VEC>
@@ -511,10 +538,8 @@ i8_rmsnorm_kernel(const NormArgs a) {
             }
         }
     };
-    F2 sh = f2(0.f, 0.f), sl = sh;
-    MaxPair m = {0.f, 0.f};
     for (int i0 = tid; i0 < vecs; i0 += U * G) {
-        Raw<T> v[U], t[U], wv[U];
+        Raw<T> v[U], t[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i0 + u * G < vecs) v[u] = Part::load(xr, cols, i0 + u * G, tid, G);
@@ -523,35 +548,39 @@ i8_rmsnorm_kernel(const NormArgs a) {
             for (int u = 0; u < U; ++u)
                 if (i0 + u * G < vecs) t[u] = Part::load(rr, cols, i0 + u * G, tid, G);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u * G < vecs) wv[u] = Part::load(wr, cols, i0 + u * G, tid, G);
-#pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = i0 + u * G;
             if (i >= vecs) break;
             if (rr) add_raw(v[u], t[u]);
             if (hr) Part::store(hr, cols, i, tid, G, v[u]);
             if (a.pl.keep) kept[i] = v[u];
-            float h[8], w[8];
-            to8(v[u], h);
-            to8(wv[u], w);
+        }
+    }
+    // (rolled up, as the loop at the end: unrolled they do not fit the instruction cache, 16384 x 4096 bfloat16
+    // 147 us against 118)
+    F2 sh = f2(0.f, 0.f), sl = sh;
+    MaxPair m = {0.f, 0.f};
+#pragma unroll 1
+    for (int i = tid; i < vecs; i += G) {
+        float h[8], w[8];
+        to8(again(i), h);
+        to8(Part::load(wr, cols, i, tid, G), w);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const F2 g = f2(h[e], h[e + 1]), sq = mul2(g, g);
-                const float2 p = unpack(mul2(g, f2(w[e], w[e + 1])));
-                F2 err;
-                sh = two_sum2(sh, sq, err);
-                if constexpr (EXACT) {
-                    m.hi = max_nan(m.hi, max_nan(fabsf(p.x), fabsf(p.y)));
-                } else {
-                    const float2 q = unpack(sq);
-                    err = add2(err, f2(fmaf(h[e], h[e], -q.x), fmaf(h[e + 1], h[e + 1], -q.y)));
-                    const float lx = fmaf(h[e], w[e], -p.x), ly = fmaf(h[e + 1], w[e + 1], -p.y);
-                    m = max_pair(m, MaxPair{fabsf(p.x), p.x < 0.f ? -lx : lx});
-                    m = max_pair(m, MaxPair{fabsf(p.y), p.y < 0.f ? -ly : ly});
-                }
-                sl = add2(sl, err);
+        for (int e = 0; e < 8; e += 2) {
+            const F2 g = f2(h[e], h[e + 1]), sq = mul2(g, g);
+            const float2 p = unpack(mul2(g, f2(w[e], w[e + 1])));
+            F2 err;
+            sh = two_sum2(sh, sq, err);
+            if constexpr (EXACT) {
+                m.hi = max_nan(m.hi, max_nan(fabsf(p.x), fabsf(p.y)));
+            } else {
+                const float2 q = unpack(sq);
+                err = add2(err, f2(fmaf(h[e], h[e], -q.x), fmaf(h[e + 1], h[e + 1], -q.y)));
+                const float lx = fmaf(h[e], w[e], -p.x), ly = fmaf(h[e + 1], w[e + 1], -p.y);
+                m = max_pair(m, MaxPair{fabsf(p.x), p.x < 0.f ? -lx : lx});
+                m = max_pair(m, MaxPair{fabsf(p.y), p.y < 0.f ? -ly : ly});
             }
+            sl = add2(sl, err);
         }
     }
     float f = 1.f;  // the row is taken times f
@@ -589,37 +618,30 @@ i8_rmsnorm_kernel(const NormArgs a) {
     // both factors are 1 but for rows of enormous or of tiny elements
     const F2 f22 = f2(f, f), g2 = f2(o.g.hi, o.g.hi), c2 = f2(o.c, o.c);
     const bool plain = o.c == 1.f;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = tid; i < vecs; i += G) {
+        const Raw<T> hraw = again(i), wraw = Part::load(wr, cols, i, tid, G);
         float h[8], w[8];
-        to8(again(i), h);
-        to8(Part::load(wr, cols, i, tid, G), w);
+        to8(hraw, h);
+        to8(wraw, w);
         F2 u[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[e] = mul2(mul2(f2(h[2 * e], h[2 * e + 1]), f22), f2(w[2 * e], w[2 * e + 1]));
         if (a.q.codes) {
             uint32_t code[8];
-            float v[8], far = 0.f;
+            float far = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 const F2 q = mul2(mul2(u[e / 2], c2), g2);
-                const float2 t = unpack(sub2(q, nearest2(q, code[e], code[e + 1]))), vv = unpack(q);
-                v[e] = vv.x, v[e + 1] = vv.y;
+                const float2 t = unpack(sub2(q, nearest2(q, code[e], code[e + 1])));
                 far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
             }
-            if (!(o.g.hi > 0.f)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) code[e] = 0;
-            } else if (far > 0.4999f || !plain) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // (a tiny scale is rounded coarsely: quotients may pass 127)
-                    int k = plain ? static_cast<int8_t>(code[e]) : static_cast<int>(fminf(fmaxf(rintf(v[e]), -127.f), 127.f));
-                    if (fabsf(v[e] - static_cast<float>(k)) > 0.4999f) k = norm_border<EXACT>(h[e], w[e], f, o, v[e], k);
-                    code[e] = min(max(k, -127), 127);
-                }
-            }
-            Part::store_codes(a.q.codes + r * a.q.pitch, (int)a.q.pitch, i, tid, G, code);
+            uint2 words = make_uint2(i8_pack4(code[0], code[1], code[2], code[3]), i8_pack4(code[4], code[5], code[6], code[7]));
+            if (!(o.g.hi > 0.f))
+                words = make_uint2(0, 0);
+            else if (far > 0.4999f || !plain)
+                words = norm_codes<T>(hraw, wraw, f, o);
+            Part::store_words(a.q.codes + r * a.q.pitch, (int)a.q.pitch, i, tid, G, words);
         }
         if (a.y) {
             float y[8];
@@ -803,7 +825,8 @@ template <typename T> static int rmsnorm_t(NormArgs a, cudaStream_t st) {
     const RowLaunch l = row_launch(a.rows, a.cols, sizeof(T));
     a.pl = l.pl;
     if (l.U == 1) return vec ? rmsnorm_l<T, 1, true>(a, l, st) : rmsnorm_l<T, 1, false>(a, l, st);
-    return vec ? rmsnorm_l<T, 4, true>(a, l, st) : rmsnorm_l<T, 4, false>(a, l, st);
+    constexpr int U = sizeof(T) == 4 ? 2 : 4;  // (16384 x 4096 float32: 184 us against 197 with four)
+    return vec ? rmsnorm_l<T, U, true>(a, l, st) : rmsnorm_l<T, U, false>(a, l, st);
 }
 
 int launch_i8_rmsnorm(const lora_i8_norm& p, cudaStream_t st) {
