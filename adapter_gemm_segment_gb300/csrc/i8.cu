@@ -60,7 +60,7 @@ static I8ProductWs product_ws(int n, int h_out, int h_in) {
     I8ProductWs L = {0, 0, 0};
     if (n <= kI8Small) return L;
     L.scales_off = align256((size_t)n * i8_pitch(h_in) * 2);
-    L.w_off = L.scales_off + align256((size_t)n * 4);
+    L.w_off = L.scales_off + 2 * align256((size_t)n * 4);  // scales, peaks
     L.total = L.w_off + (n > kI8Tile ? align256((size_t)h_out * i8_pitch(h_in) * 2) : 0);
     return L;
 }
@@ -94,7 +94,7 @@ static int ws_layout(lora_pool_t pool, int n, I8WsLayout* L) {
     L->codes_off = align256((size_t)rows * pv.R * 4);
     const I8ProductWs P = product_ws(n, pv.h_out, pv.h_in);
     L->scales_off = L->codes_off + (n <= kI8Small ? align256((size_t)n * i8_pitch(pv.h_in)) : P.scales_off);
-    L->w_off = L->scales_off + align256((size_t)n * 4);
+    L->w_off = L->scales_off + 2 * align256((size_t)n * 4);  // scales, peaks
     L->y32_off = L->w_off + P.total - P.w_off;
     L->total = L->y32_off + align256((size_t)most_separate(pv, n) * pv.h_out * 4);
     return LORA_OK;
@@ -180,14 +180,16 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
     if (x->rows <= kI8Small) return launch_i8_small(xv, wv, y_dev, dtype, ldy, nullptr, /*early_w=*/false, nullptr, st);
     char* ws = static_cast<char*>(ws_dev);
     float* sx = reinterpret_cast<float*>(ws + L.scales_off);
-    rc = launch_i8_expand(xv, nullptr, nullptr, ws, sx, st);
+    int* peak = reinterpret_cast<int*>(ws + L.scales_off + align256((size_t)x->rows * 4));
+    rc = x->rows <= kI8Tile ? launch_i8_expand_small(xv, nullptr, nullptr, ws, sx, peak, st)
+                            : launch_i8_expand(xv, nullptr, nullptr, ws, sx, st);
     if (rc) return rc;
-    const I8Rows rows = {ws, sx, nullptr, x->rows, x->cols};
+    const I8Rows rows = {ws, sx, nullptr, x->rows, x->cols, peak};
     if (x->rows <= kI8Tile)
         return launch_i8_tile(rows, wv, y_dev, dtype, ldy, nullptr, /*early_x=*/false, /*release=*/false, nullptr, st);
     rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
     if (rc) return rc;
-    const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, w->rows, w->cols};
+    const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, w->rows, w->cols, nullptr};
     return launch_i8_pair(rows, wrows, y_dev, dtype, ldy, nullptr, /*release=*/false, nullptr, st);
 }
 
@@ -231,6 +233,7 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
     char* ws = static_cast<char*>(ws_dev);
     float* s_buf = reinterpret_cast<float*>(ws);
     float* sx = reinterpret_cast<float*>(ws + L.scales_off);
+    int* peak = reinterpret_cast<int*>(ws + L.scales_off + align256((size_t)n * 4));
     const SegView sv = seg_view(seg);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool few = n <= kI8Small;
@@ -240,11 +243,13 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
     if (xq) stored = view_of(xq);
     int s_parts = 1;
     if (front) {
-        rc = launch_i8_front(pv, sv, x_dev, xq ? &stored : nullptr, codes, !few, sx, s_buf, &s_parts, st);
+        rc = launch_i8_front(pv, sv, x_dev, xq ? &stored : nullptr, codes, !few, sx, peak, s_buf, &s_parts, st);
     } else {
         if (!few)  // rows in the order of the segments
-            rc = xq ? launch_i8_expand(stored, sv.perm, sv.status, codes, sx, st)
-                    : launch_i8_quantize_f16(x_dev, pv.dtype, n, pv.h_in, sv.perm, sv.status, codes, sx, st);
+            rc = !xq            ? launch_i8_quantize_f16(x_dev, pv.dtype, n, pv.h_in, sv.perm, sv.status, codes, sx,
+                                                         n <= kI8Tile ? peak : nullptr, st)
+                 : n <= kI8Tile ? launch_i8_expand_small(stored, sv.perm, sv.status, codes, sx, peak, st)
+                                : launch_i8_expand(stored, sv.perm, sv.status, codes, sx, st);
         else if (!xq)
             rc = launch_i8_quantize(x_dev, pv.dtype, pv.h_in, i8_view(codes, sx, n, pv.h_in), st);
         if (rc) return rc;
@@ -266,13 +271,13 @@ int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_
         xv = xq ? stored : i8_view(codes, sx, n, pv.h_in);
         return launch_i8_small(xv, wv, y_dev, pv.dtype, pv.h_out, sv.status, /*early_w=*/true, &lora, st);
     }
-    const I8Rows rows = {codes, sx, sv.perm, n, pv.h_in};
+    const I8Rows rows = {codes, sx, sv.perm, n, pv.h_in, peak};
     if (n <= kI8Tile)
         // x is stored by the kernel ahead where that makes the shrink too
         return launch_i8_tile(rows, wv, y_dev, pv.dtype, pv.h_out, sv.status, /*early_x=*/!front, /*release=*/true, &lora, st);
     rc = launch_i8_expand(wv, nullptr, nullptr, ws + L.w_off, nullptr, st);
     if (rc) return rc;
-    const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, wv.rows, wv.cols};
+    const I8Rows wrows = {ws + L.w_off, wv.scales, nullptr, wv.rows, wv.cols, nullptr};
     if (pv.dtype == LORA_F32) {
         rc = launch_i8_pair(rows, wrows, y_dev, LORA_F32, pv.h_out, sv.status, /*release=*/true, nullptr, st);
         return rc ? rc : launch_f32_expand(pv, sv, s_buf, s_parts, y_dev, st);

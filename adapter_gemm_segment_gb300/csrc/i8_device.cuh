@@ -95,6 +95,14 @@ __device__ __forceinline__ uint32_t i8_pack4(uint32_t a, uint32_t b, uint32_t c,
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// Sum of the absolute values of a word's four codes.
+__device__ __forceinline__ int i8_abs_sum(uint32_t w) {
+    int sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += abs(static_cast<int>(w << (24 - 8 * e)) >> 24);
+    return sum;
+}
+
 // Four codes of a word as float16, exactly: with the sign bit flipped a byte b stands for b - 128, and
 // 0x6400 + b is the float16 1024 + b.
 __device__ __forceinline__ uint2 i8_to_f16x4(uint32_t w) {

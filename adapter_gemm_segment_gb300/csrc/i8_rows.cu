@@ -167,11 +167,23 @@ __device__ __forceinline__ MaxPair max_pair(MaxPair a, MaxPair b) {
     const bool take = !(b.hi <= a.hi) || (b.hi == a.hi && b.lo > a.lo);
     return a.hi != a.hi ? a : take ? b : a;
 }
+// The largest of a row's warps' tops.
+__device__ __forceinline__ void row_peak(int top, int G, int tid, float* red, int* peak) {
+    if (G > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = __int_as_float(top);
+        __syncthreads();
+        for (int w = 0; w < G / 32; ++w) top = max(top, __float_as_int(red[w]));
+    }
+    if (tid == 0) *peak = top;
+}
+
 // ---- quantise ----------------------------------------------------------------------------------------
 // One row by its G threads.  U: vectors whose loads are in flight together.  Codes go to out as bytes or float16.
+// peak (nullable): at least the largest sum of |code| over an aligned block of 256 (see I8Rows::peak).
 template <typename T, int U, bool VEC, typename C>
 __device__ __forceinline__ void quantise_row(const T* row, int cols, int pitch, const RowPlan& pl, int tid, Raw<T>* kept,
-                                             float* red, float* scale, C* out) {
+                                             float* red, float* scale, C* out, int* peak) {
     using Part = RowPart<T, VEC>;
     const int G = pl.G;
     float m = 0.f;
@@ -201,6 +213,7 @@ __device__ __forceinline__ void quantise_row(const T* row, int cols, int pitch, 
     if (tid == 0) *scale = s;
     const I8Divisor d = i8_divisor(s);
     const bool plain = d.up == 1.f && d.inv != 0.f;
+    int top = VEC ? 0 : 256 * 127;  // (without VEC a warp's codes are no block)
 #pragma unroll 1
     for (int i = tid; i < pl.vecs; i += G) {
         float f[8];
@@ -224,14 +237,22 @@ __device__ __forceinline__ void quantise_row(const T* row, int cols, int pitch, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) c[e] = i8_code(f[e], d);
         }
+        if (VEC && peak != nullptr) {  // (a warp's 32 vectors are an aligned block)
+            int sum = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += abs(static_cast<int>(static_cast<int8_t>(c[e])));
+            top = max(top, __reduce_add_sync(0xffffffffu, sum));
+        }
         Part::store_codes(out, pitch, i, tid, G, c);
     }
+    if (peak != nullptr) row_peak(top, G, tid, red, peak);
 }
 
 // F16: codes as float16 into x16 [rows][pitch], row r from row perm[r] of x (see launch_i8_quantize_f16).
 template <typename T, int U, bool VEC, bool F16>
 __global__ void __launch_bounds__(kRowThreads)
-i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t* perm, const int32_t* status, __half* x16) {
+i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t* perm, const int32_t* status, __half* x16,
+                   int* peak) {
     extern __shared__ __align__(16) uint8_t row_smem[];
     __shared__ float red[kRowThreads / 32];
     pdl_wait();
@@ -244,9 +265,10 @@ i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t
     if constexpr (F16) {
         if (status != nullptr && __ldcg(status) != LORA_OK) return;  // (perm is not valid either)
         if (perm != nullptr) row = x + (long long)__ldcg(perm + r) * ld;
-        quantise_row<T, U, VEC>(row, q.cols, (int)q.pitch, pl, tid, kept, red, q.scales + r, x16 + r * q.pitch);
+        quantise_row<T, U, VEC>(row, q.cols, (int)q.pitch, pl, tid, kept, red, q.scales + r, x16 + r * q.pitch,
+                                peak ? peak + r : nullptr);
     } else {
-        quantise_row<T, U, VEC>(row, q.cols, (int)q.pitch, pl, tid, kept, red, q.scales + r, q.codes + r * q.pitch);
+        quantise_row<T, U, VEC>(row, q.cols, (int)q.pitch, pl, tid, kept, red, q.scales + r, q.codes + r * q.pitch, nullptr);
     }
 }
 
@@ -265,6 +287,7 @@ struct FrontArgs {
     I8View q;               // quantised into (codes, or scales alone with x16), or (stored) expanded from
     __half* x16;            // nullable: codes as bytes
     float* scales;
+    int* peak;              // with x16
     float* s;
     RowPlan pl;
     int n, stored, rows, parts;  // rows: CTAs that take rows of x (n, or 0)
@@ -277,30 +300,42 @@ i8_front_kernel(const FrontArgs a) {
     __shared__ float red[kFrontThreads / 32][8];
     pdl_wait();
     pdl_trigger();
-    const int status = __ldcg(a.status);  // (independent loads first)
-    const int h = a.pool.h_in, R = a.pool.R, tid = threadIdx.x;
+    const int status = a.status ? __ldcg(a.status) : LORA_OK;  // (independent loads first)
+    const int h = a.q.cols, R = a.pool.R, tid = threadIdx.x;
     if ((int)blockIdx.x < a.rows) {
         const int r = blockIdx.x;
         const int from = a.x16 && a.perm ? __ldcg(a.perm + r) : r;
         if (status != LORA_OK) return;
         if (a.stored) {
             const int8_t* codes = a.q.codes + (size_t)from * a.q.pitch;
-            for (int k = tid * 16; k < (int)a.q.pitch; k += kFrontThreads * 16) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + k));
-                const uint2 c0 = i8_to_f16x4(w.x), c1 = i8_to_f16x4(w.y), c2 = i8_to_f16x4(w.z), c3 = i8_to_f16x4(w.w);
-                uint4* out = reinterpret_cast<uint4*>(a.x16 + (size_t)r * a.q.pitch + k);
-                out[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
-                out[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
+            int top = 0;
+            for (int k0 = 0; k0 < (int)a.q.pitch; k0 += kFrontThreads * 16) {
+                const int k = k0 + tid * 16;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (k < (int)a.q.pitch) {
+                    w = __ldg(reinterpret_cast<const uint4*>(codes + k));
+                    const uint2 c0 = i8_to_f16x4(w.x), c1 = i8_to_f16x4(w.y), c2 = i8_to_f16x4(w.z), c3 = i8_to_f16x4(w.w);
+                    uint4* out = reinterpret_cast<uint4*>(a.x16 + (size_t)r * a.q.pitch + k);
+                    out[0] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+                    out[1] = make_uint4(c2.x, c2.y, c3.x, c3.y);
+                }
+                int sum = i8_abs_sum(w.x) + i8_abs_sum(w.y) + i8_abs_sum(w.z) + i8_abs_sum(w.w);
+#pragma unroll
+                for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);  // (16 lanes a block)
+                top = max(top, max(sum, __shfl_xor_sync(0xffffffffu, sum, 16)));
             }
+            row_peak(top, kFrontThreads, tid, &red[0][0], a.peak + r);
             if (tid == 0) a.scales[r] = __ldg(a.q.scales + from);
             return;
         }
         const T* row = static_cast<const T*>(a.x) + (size_t)from * h;
         Raw<T>* kept = reinterpret_cast<Raw<T>*>(row_smem);
         if (a.x16)
-            quantise_row<T, 2, VEC>(row, h, (int)a.q.pitch, a.pl, tid, kept, &red[0][0], a.scales + r, a.x16 + (size_t)r * a.q.pitch);
+            quantise_row<T, 2, VEC>(row, h, (int)a.q.pitch, a.pl, tid, kept, &red[0][0], a.scales + r, a.x16 + (size_t)r * a.q.pitch,
+                                      a.peak + r);
         else
-            quantise_row<T, 2, VEC>(row, h, (int)a.q.pitch, a.pl, tid, kept, &red[0][0], a.scales + r, a.q.codes + (size_t)r * a.q.pitch);
+            quantise_row<T, 2, VEC>(row, h, (int)a.q.pitch, a.pl, tid, kept, &red[0][0], a.scales + r, a.q.codes + (size_t)r * a.q.pitch,
+                                      nullptr);
         return;
     }
     using Part = RowPart<T, VEC>;
@@ -693,45 +728,45 @@ template <typename K> static int allow_smem(K fn, bool& done) {
 
 template <typename T, int U, bool VEC, bool F16>
 static int quantize_l(const T* x, long long ld, const I8View& q, const RowLaunch& l, const int32_t* perm,
-                      const int32_t* status, __half* x16, cudaStream_t st) {
+                      const int32_t* status, __half* x16, int* peak, cudaStream_t st) {
     static bool done = false;
     const auto fn = i8_quantize_kernel<T, U, VEC, F16>;
     const int rc = allow_smem(fn, done);
     if (rc) return rc;
-    void* args[] = {(void*)&x, (void*)&ld, (void*)&q, (void*)&l.pl, (void*)&perm, (void*)&status, (void*)&x16};
+    void* args[] = {(void*)&x, (void*)&ld, (void*)&q, (void*)&l.pl, (void*)&perm, (void*)&status, (void*)&x16, (void*)&peak};
     LORA_CUDA_TRY(launch_pdl((const void*)fn, dim3(l.blocks), dim3(l.threads), l.smem, st, args));
     return LORA_OK;
 }
 template <typename T, bool F16>
 static int quantize_t(const void* x, long long ld, const I8View& q, const int32_t* perm, const int32_t* status, void* x16,
-                      cudaStream_t st) {
+                      int* peak, cudaStream_t st) {
     const bool vec = aligned16(x, ld, q.rows, sizeof(T));
     const RowLaunch l = row_launch(q.rows, q.cols, sizeof(T));
     const T* xp = static_cast<const T*>(x);
     __half* hp = static_cast<__half*>(x16);
     if (l.U == 1)
-        return vec ? quantize_l<T, 1, true, F16>(xp, ld, q, l, perm, status, hp, st)
-                   : quantize_l<T, 1, false, F16>(xp, ld, q, l, perm, status, hp, st);
-    return vec ? quantize_l<T, 4, true, F16>(xp, ld, q, l, perm, status, hp, st)
-               : quantize_l<T, 4, false, F16>(xp, ld, q, l, perm, status, hp, st);
+        return vec ? quantize_l<T, 1, true, F16>(xp, ld, q, l, perm, status, hp, peak, st)
+                   : quantize_l<T, 1, false, F16>(xp, ld, q, l, perm, status, hp, peak, st);
+    return vec ? quantize_l<T, 4, true, F16>(xp, ld, q, l, perm, status, hp, peak, st)
+               : quantize_l<T, 4, false, F16>(xp, ld, q, l, perm, status, hp, peak, st);
 }
 
 int launch_i8_quantize(const void* x, int dtype, long long ld, const I8View& q, cudaStream_t st) {
     if (q.rows == 0) return LORA_OK;
     switch (dtype) {
-        case LORA_F32: return quantize_t<float, false>(x, ld, q, nullptr, nullptr, nullptr, st);
-        case LORA_F16: return quantize_t<__half, false>(x, ld, q, nullptr, nullptr, nullptr, st);
-        default: return quantize_t<__nv_bfloat16, false>(x, ld, q, nullptr, nullptr, nullptr, st);
+        case LORA_F32: return quantize_t<float, false>(x, ld, q, nullptr, nullptr, nullptr, nullptr, st);
+        case LORA_F16: return quantize_t<__half, false>(x, ld, q, nullptr, nullptr, nullptr, nullptr, st);
+        default: return quantize_t<__nv_bfloat16, false>(x, ld, q, nullptr, nullptr, nullptr, nullptr, st);
     }
 }
 
 int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const int32_t* perm, const int32_t* status,
-                           void* x16, float* scales, cudaStream_t st) {
+                           void* x16, float* scales, int* peak, cudaStream_t st) {
     const I8View q = i8_view(nullptr, scales, rows, cols);
     switch (dtype) {
-        case LORA_F32: return quantize_t<float, true>(x, cols, q, perm, status, x16, st);
-        case LORA_F16: return quantize_t<__half, true>(x, cols, q, perm, status, x16, st);
-        default: return quantize_t<__nv_bfloat16, true>(x, cols, q, perm, status, x16, st);
+        case LORA_F32: return quantize_t<float, true>(x, cols, q, perm, status, x16, peak, st);
+        case LORA_F16: return quantize_t<__half, true>(x, cols, q, perm, status, x16, peak, st);
+        default: return quantize_t<__nv_bfloat16, true>(x, cols, q, perm, status, x16, peak, st);
     }
 }
 
@@ -757,7 +792,7 @@ template <typename T> static int front_t(FrontArgs a, cudaStream_t st) {
 }
 
 int launch_i8_front(const PoolView& pv, const SegView& sv, const void* x, const I8View* xq, void* codes, bool f16,
-                    float* scales, float* s, int* s_parts, cudaStream_t st) {
+                    float* scales, int* peak, float* s, int* s_parts, cudaStream_t st) {
     FrontArgs a;
     memset(&a, 0, sizeof(a));
     a.pool = pv;
@@ -769,6 +804,7 @@ int launch_i8_front(const PoolView& pv, const SegView& sv, const void* x, const 
     a.q = xq ? *xq : i8_view(codes, scales, sv.n, pv.h_in);
     a.x16 = f16 ? static_cast<__half*>(codes) : nullptr;
     a.scales = scales;
+    a.peak = peak;
     a.s = s;
     a.n = sv.n;
     a.rows = xq && !f16 ? 0 : sv.n;
@@ -778,6 +814,23 @@ int launch_i8_front(const PoolView& pv, const SegView& sv, const void* x, const 
         case LORA_F16: return front_t<__half>(a, st);
         default: return front_t<__nv_bfloat16>(a, st);
     }
+}
+
+int launch_i8_expand_small(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales,
+                           int* peak, cudaStream_t st) {
+    FrontArgs a;
+    memset(&a, 0, sizeof(a));
+    a.perm = perm;
+    a.status = status;
+    a.q = x;
+    a.x16 = static_cast<__half*>(x16);
+    a.scales = scales;
+    a.peak = peak;
+    a.stored = 1;
+    a.rows = x.rows;  // (and no token's shrink)
+    void* args[] = {(void*)&a};
+    LORA_CUDA_TRY(launch_pdl((const void*)i8_front_kernel<__half, true>, dim3(x.rows), dim3(kFrontThreads), 0, st, args));
+    return LORA_OK;
 }
 
 int launch_i8_expand(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales, cudaStream_t st) {

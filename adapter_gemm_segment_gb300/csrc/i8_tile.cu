@@ -1,9 +1,10 @@
 // Products over an 8-bit weight on the tensor cores, whole-number sums kept exact.
 //
 // sm_103a's tensor cores take no 8-bit integers, but a code is a float16 number and a product of two codes
-// is exact in float32, so is a sum of 1024 of them (1024 * 128 * 128 = 2^24).  Codes go through
-// tcgen05.mma kind::f16; every 1024 of K the accumulator is read into 32-bit integers in registers and
-// started again.
+// is exact in float32, so is a sum of 1024 of them (1024 * 128 * 128 = 2^24), or of more where the tokens' codes
+// are small: the kernel before this one leaves each token's largest sum of |code| over 256, which bounds the
+// partial sums.  Codes go through tcgen05.mma kind::f16; every chunk of so many the accumulator is read into
+// 32-bit integers and started again (usually once, at the end).
 //
 // The weight is the MMA's M side (128 features a tile) and up to 128 tokens its N side.  The weight stays
 // in bytes until it is on the SM: TMA brings 128 x 128 codes, sixteen warps turn them into float16 and store
@@ -37,7 +38,7 @@ using namespace ptx;
 constexpr int kIM = 128;          // features per tile
 constexpr int kIN = 256;          // tokens per tile, at most
 constexpr int kIK = 128;          // codes of a step along K
-constexpr int kIChunk = 8;        // steps between two readings of the accumulator: 1024 codes
+constexpr int kIChunk = 8;        // steps between two readings of the accumulator, at least: 1024 codes
 constexpr int kIWorkers = 16;     // warps 2-17: convert (half of them the even steps, half the odd), drain
 constexpr int kIThreads = 64 + 32 * kIWorkers;  // warp 0 loads, 1 MMAs
 constexpr int kILora = 256;       // more threads for the LoRA term
@@ -52,6 +53,7 @@ struct I8TileArgs {
     int32_t* status;       // nullable
     const int32_t* perm;   // row of y of each row of x (nullable)
     const float* sx;
+    const int* peak;
     const float* sw;
     long long ldy;
     int n, n_pad, h_out, kb_total, kb_per_split, splits, wstages, xstages, xk, early_x, release, vec, ring_bytes, alias, per, per_inv;
@@ -98,7 +100,6 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     const int n = min(a.n - row0, a.n_pad);
     const int kb0 = split * a.kb_per_split;
     const int nkb = min(a.kb_total, kb0 + a.kb_per_split) - kb0;
-    const int nchunks = (nkb + kIChunk - 1) / kIChunk;
     // the tokens this CTA finishes
     const int t0 = min(n, split * a.per), cnt = min(n, t0 + a.per) - t0;
 
@@ -164,6 +165,19 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     if (a.splits > 1 && !a.alias) cluster_arrive();  // (waited for before the first store into another CTA)
     if (a.release) pdl_trigger();
 
+    // Steps a chunk, and chunks: blocks of 256 codes whose products with 128 stay below 2^24 (two blocks less for
+    // those that a chunk has a part of).  An accumulator of more than 128 tokens has no second one beside it, and
+    // reading it holds the MMAs up: 200 x 11008 x 4096, chunks of 1024 codes 41 us, as long as the codes let them 33.
+    int chunk_steps = nkb, nchunks = 1;
+    if (warp >= 1 && warp < 2 + kIWorkers && nkb > kIChunk) {
+        if (!a.early_x) pdl_wait();
+        int top = 1;
+        for (int t = lane; t < n; t += 32) top = max(top, __ldcg(a.peak + row0 + t));
+        top = __reduce_max_sync(0xffffffffu, top);
+        chunk_steps = max(kIChunk, 2 * ((1 << 17) / top - 2));
+        nchunks = (nkb + chunk_steps - 1) / chunk_steps;
+    }
+
     if (warp == 0) {
         if (lane == 0) {
             if (!a.early_x) {
@@ -216,7 +230,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         int i = 0, s = 0, slot = 0;
         uint32_t ph = 0, aph = 0;
         for (int c = 0; c < nchunks && ok; ++c) {
-            const int buf = c % nbuf, end = min(nkb, (c + 1) * kIChunk);
+            const int buf = c % nbuf, end = min(nkb, (c + 1) * chunk_steps);
             const uint32_t acc = tmem + buf * n_pad;
             if (c >= nbuf) ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[buf], (c / nbuf & 1) ^ 1, flags));
             uint32_t more = 0;
@@ -274,7 +288,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         bool ok = true;
         int chunk = 0;  // the next to drain
         bool started = a.splits == 1 || a.alias;
-        int sum[kIN / 64][16];  // (indexed at run time: in local memory, touched once in 1024 codes, not in registers)
+        int sum[kIN / 64][16];  // (indexed at run time: in local memory, touched once a chunk, not in registers)
         auto hand_over = [&](int u, const uint32_t* r) {  // to the CTAs that finish these 16 tokens
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -366,7 +380,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             before = slot;
             if ((slot += 2) >= kIASlots) slot -= kIASlots, fph ^= 1;
             // the chunk before is complete by now; or (one accumulator) holds the MMAs up, and enough is converted
-            const bool done = i >= (chunk + 1) * kIChunk + (nbuf == 2 ? kIChunk / 2 : 2);
+            const bool done = i >= (chunk + 1) * chunk_steps + (nbuf == 2 ? kIChunk / 2 : 2);
             const bool more = i + 2 < nkb;
             if (done || (more && !__all_sync(0xffffffffu, mbar_test(&full_w[s], ph)))) {
                 announce();  // (the MMAs need not wait for what follows)
@@ -544,6 +558,7 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
     a.status = status;
     a.perm = x.perm;
     a.sx = x.scales;
+    a.peak = x.peak;
     a.sw = w.scales;
     a.ldy = ldy;
     a.n = x.rows;

@@ -163,14 +163,17 @@ int launch_i8_rmsnorm(const lora_i8_norm& args, cudaStream_t st);
 // tensor-core products take x in.  Row r is row perm[r] of x (nullptr: r); untouched unless *status
 // (nullable) is LORA_OK.  From x itself, quantised, or from its stored form.
 int launch_i8_quantize_f16(const void* x, int dtype, int rows, int cols, const int32_t* perm, const int32_t* status,
-                           void* x16, float* scales, cudaStream_t st);
+                           void* x16, float* scales, int* peak, cudaStream_t st);
+// (peak nullable; of stored codes, with it, a CTA a row: for small batches)
+int launch_i8_expand_small(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales,
+                           int* peak, cudaStream_t st);
 int launch_i8_expand(const I8View& x, const int32_t* perm, const int32_t* status, void* x16, float* scales, cudaStream_t st);
 // For small batches, one launch: x's codes (as bytes, rows as x's; or f16: as float16, rows in the order of the
 // segments; xq: from its stored form, nothing to do where bytes will serve) and the per-token shrink in *s_parts K
 // parts, the columns past an adapter's rank not written.
 int i8_front_parts(const PoolView& pv, int n);
 int launch_i8_front(const PoolView& pv, const SegView& sv, const void* x, const I8View* xq, void* codes, bool f16,
-                    float* scales, float* s, int* s_parts, cudaStream_t st);
+                    float* scales, int* peak, float* s, int* s_parts, cudaStream_t st);
 // The LoRA term of a product: the slot of each token and the shrink output in K parts.
 struct I8Lora {
     const PoolView* pool;
@@ -184,6 +187,9 @@ struct I8Rows {
     const float* scales;
     const int32_t* perm;  // nullptr: as they are
     int rows, cols;
+    // launch_i8_tile: of each row at least the largest sum of |code| over an aligned block of 256 codes, which bounds
+    // how many products are sure to stay whole numbers in float32
+    const int* peak;
 };
 // On the tensor cores.  Every kernel that could have written w has completed when this grid starts (the kernel
 // ahead waited for it); early_x: so has x.  release: the kernel behind may be released early (never a product by itself, whose y may be

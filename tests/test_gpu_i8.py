@@ -261,6 +261,50 @@ def test_sums_are_exact_at_their_largest(lib, n, k):
     assert np.array_equal(y.cpu().numpy(), ref)
 
 
+@pytest.mark.parametrize("n", [10, 60, 200])
+@pytest.mark.parametrize("k", [5001, 40000, 100000])
+def test_sums_are_exact_where_tokens_codes_are_small(lib, n, k):
+    """The smaller a batch's codes, the longer its sums stay in float32: every size of code at its largest sums, all
+    of one sign, each an odd number."""
+    m = 140
+    rng = np.random.default_rng([n, k])
+    w = lib.I8Matrix(m, k)
+    cw = np.where(rng.random((m, 1)) < 0.5, -128, 127) * np.ones((1, k), np.int64)
+    cw[:, -3:] = rng.integers(-128, 128, (m, 3))
+    sign = np.where(rng.random((n, 1)) < 0.5, -1, 1)
+    for c in (1, 3, 9, 13, 23, 41, 63, 101):
+        cx = sign * c * np.ones((1, k), np.int64)
+        if c == 13:
+            cx[n // 2, k // 3: k // 3 + 300] = 127  # one token's codes are large, in three blocks
+        if c == 3:
+            cx[:, 100:k - 100] = 0
+        x = lib.I8Matrix(n, k)
+        for q, codes in ((x, cx), (w, cw)):
+            q.codes.zero_()
+            q.codes[:, :k].copy_(torch.from_numpy(codes.astype(np.int8)))
+            q.scales.fill_(1.0)
+        y = torch.empty(n, m, device="cuda")
+        lib.lora_i8_matmul(x, w, y)
+        ref = (cx @ cw.T).astype(np.float32)
+        assert np.array_equal(y.cpu().numpy(), ref), c
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,k,slots,r_max", [(12, 20000, 2, 8), (40, 30001, 2, 8), (130, 20000, 3, 16), (200, 20008, 60, 8)])
+@pytest.mark.parametrize("small", [0.02, 0.1, 0.4])
+def test_linear_of_rows_with_few_large_values(lib, dtype, n, k, slots, r_max, small):
+    """Rows whose scale is that of a few values: small codes along most of K."""
+    if dtype != torch.float32:
+        k = k // 8 * 8
+    case = wl.random_case(k, n, k, 264, [r_max] * slots, r_max=r_max, dtype=dtype, p_base=0.5)
+    x = case.x.float().sign() * (1 - 0.1 * torch.rand(n, k, generator=torch.Generator().manual_seed(k)))
+    x[:, 1:] *= small
+    x[:, k // 2: k // 2 + 5] = -1.0
+    case.x = x.to(dtype)
+    case.W = (case.W.float().abs() * case.x[0].float().sign()).to(dtype)  # (sums of one sign for the first token)
+    check_linear(lib, case)
+
+
 def test_a_row_gives_the_same_bits_in_every_batch(lib):
     x, w = gauss(700, 1300, 8), gauss(390, 1300, 9, scale=0.02)
     q = stored(lib, w)
