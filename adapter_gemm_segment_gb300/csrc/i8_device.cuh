@@ -139,19 +139,5 @@ template <> __device__ __forceinline__ void load_b8<float>(const float* row, int
         for (int e = 0; e < 8; ++e) f[e] = j + e < R ? __ldg(row + j + e) : 0.f;
     }
 }
-// Eight consecutive elements of a row of the shrink output (R floats), zeros past jl.
-__device__ __forceinline__ void load_s8(const float* s, int j, int R, int jl, float (&f)[8]) {
-    if (R % 4 == 0) {
-        const float4 a = *reinterpret_cast<const float4*>(s + j);
-        const float4 b = j + 4 < jl ? *reinterpret_cast<const float4*>(s + j + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = j + e < jl ? s[j + e] : 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (j + e >= jl) f[e] = 0.f;  // (what lies past the adapter's rank may not have been written)
-}
 
 }  // namespace lora

@@ -484,7 +484,8 @@ int lora_i8_rmsnorm(const lora_i8_norm* args, void* stream);
  * products exact, then times x's and w's scales in float32 and rounded once to dtype (row stride ldy >=
  * w.rows elements, aligned to its element).  A NaN scale makes the outputs of its row NaN and no others.
  * ws_dev: >= lora_i8_matmul_workspace_bytes (which may be 0: ws_dev is then not used), 256-byte aligned;
- * successive calls on one stream may share it.  The same row of x gives the same bits in every batch. */
+ * successive calls on one stream may share it.  The same row of x gives the same bits in every batch.  LORA_EUNSUP
+ * as for lora_i8_linear_fwd.  1 to 3 kernels. */
 int lora_i8_matmul_workspace_bytes(int x_rows, int w_rows, int cols, size_t* bytes);
 int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev, int dtype, int64_t ldy, void* ws_dev,
                    size_t ws_bytes, void* stream);
@@ -495,9 +496,15 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
  * or, when xq is not NULL, xq (x's stored form from lora_i8_quantize, or lora_i8_rmsnorm's out beside its y
  * as x; projections that read the same x share it); the LoRA term takes x as it is, in the pool's dtype.
  * x_dev, y_dev, seg, errors and the device status word as in lora_linear_fwd.  The LoRA term is computed in
- * float32 and added to the base term in float32; y is rounded once.  An infinity or NaN in one adapter
- * reaches that adapter's tokens only.  A workspace of lora_i8_linear_workspace_bytes(pool, n) serves every
- * batch of up to n tokens.  The y of a linear is not to be w's codes or scales without a wait in between. */
+ * float32 and added to the base term in float32; y is rounded once.  (Batches of more than 256 tokens of
+ * 16-bit pools take it from the tensor cores, its shrink output s = (alpha / r) x A^T carried in two parts, to
+ * 2^-23 of itself.)  An infinity or NaN in one adapter reaches that adapter's tokens only.  The same call gives
+ * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 5 kernels.
+ * LORA_EUNSUP: batches of more than 256 tokens with x or w of 2^36 codes and more, or of 2^52 products.
+ * A workspace of lora_i8_linear_workspace_bytes(pool, n) serves every batch of up to n tokens.  The y of a
+ * linear, this one included, is not to be w's codes or scales without a wait in between; nor is it, or what
+ * lora_i8_rmsnorm wrote, to be the W of a 16-bit linear.  What lora_i8_quantize, lora_i8_dequantize or
+ * lora_i8_matmul wrote may be used as it is. */
 int lora_i8_linear_workspace_bytes(lora_pool_t pool, int n_tokens, size_t* bytes);
 int lora_i8_linear_fwd(lora_pool_t pool, const lora_i8_matrix* w, const void* x_dev, const lora_i8_matrix* xq,
                        void* y_dev, const lora_segments* seg, void* ws_dev, size_t ws_bytes, void* stream);

@@ -6,6 +6,10 @@ occur in these inputs.  A product's sum is a whole number and exact; its output 
 float32 and two float32 multiplications, then one rounding to its type: 3 * 2^-24 of itself and half a step
 of the type.  The LoRA term adds float32 sums of h_in and of r_max products.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -544,6 +548,36 @@ def test_norm_and_projections(lib, n):
         p.close()
 
 
+@pytest.mark.parametrize("n,h_in,r_max", [(1, 512, 8), (8, 4096, 256), (8, 512, 8), (64, 4096, 64), (256, 2048, 32), (300, 1024, 16),
+                                          (1500, 512, 16)])
+@pytest.mark.parametrize("with_xq", [False, True])
+def test_linears_of_what_was_just_written(lib, n, h_in, r_max, with_xq):
+    """Kernels start before those ahead of them end: back to back, every call still sees its own x, and nothing that it
+    shares with the call before is overwritten under that one."""
+    case = wl.random_case(n, n, h_in, 264, [r_max] * 20, r_max=r_max, dtype=torch.bfloat16, p_base=0.1)
+    pool = make_pool(lib, case)
+    w, ones = stored(lib, case.W), torch.ones(h_in, dtype=torch.bfloat16, device="cuda")
+    seg, ws = pool.segment(case.idx.cuda()), pool.i8_linear_workspace(n)
+    xs = [(case.x.float() * f).roll(f, 0).to(torch.bfloat16).cuda() for f in (1, 2, 3, 4, 5)]
+    x, q = torch.empty_like(xs[0]), lib.I8Matrix(n, h_in)
+
+    def chain(wait):
+        out = []
+        for src in xs:
+            lib.lora_i8_rmsnorm(src, ones, 1e-5, out=q, y=x)
+            wait()
+            out.append(pool.i8_linear(w, x, seg, xq=q if with_xq else None, ws=ws))
+            wait()
+        torch.cuda.synchronize()
+        return out
+
+    apart = chain(torch.cuda.synchronize)
+    for _ in range(4):
+        for a, b in zip(chain(lambda: None), apart):
+            assert torch.equal(a, b)
+    pool.close()
+
+
 def test_two_graphs_and_an_eager_call_share_nothing(lib):
     """Two captured layers replayed on two streams at once, an eager call between them: each its own result."""
     dtype = torch.bfloat16
@@ -619,3 +653,11 @@ def test_weights_quantised_right_before_their_product(lib):
             assert ((y.cpu().double() - ref).abs() <= 2.0 ** -20 * ref.abs() + 1e-30).all()
             assert ((z.cpu().double() + ref).abs() <= 2.0 ** -7.9 * ref.abs() + 1e-30).all()
         pool.close()
+
+
+def test_the_layer_example_runs():
+    out = subprocess.run([sys.executable, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "i8_layer.py"),
+                          "--tokens", "12", "--prefill", "600", "--adapters", "3", "--hidden", "264", "--ff", "520"],
+                         capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr[-2000:]
+    assert out.stdout.count("relative difference") == 10
