@@ -107,6 +107,9 @@ struct GroupView {
     // writes this value to the segments' x-ready word once its own dependency wait has
     // returned (every kernel before it complete); the GEMM reads x after seeing that value.
     int xready;
+    // Nonzero: the small-batch shrink runs beside the kernel just before it, which releases it after its own wait
+    // and writes nothing that it reads (see shrink_dependency_wait).
+    int beside;
 };
 
 // Whether some slot of the pool (empty slots count at r_max) holds fewer 8-column chunks than

@@ -12,9 +12,9 @@ namespace lora {
 // 1024 input features), *s_parts = ceil(h_in / 1024).  tiled: one CTA per (segment, 64 tokens)
 // through shared memory, *s_parts = 1.  float32: one warp per (token, rows), *s_parts = 1.
 // xready: nonzero for the small-batch kernels ahead of a fused decode GEMM launched with the
-// same value (GroupView::xready).
+// same value (GroupView::xready).  beside: see GroupView::beside (small batches of 16-bit data).
 int launch_shrink(const PoolView& pv, const SegView& sv, const void* x, float* s_out, cudaStream_t st, bool tiled,
-                  int* s_parts, int xready = 0);
+                  int* s_parts, int xready = 0, int beside = 0);
 int shrink_parts(const PoolView& pv, int n, bool tiled);
 // Whether the small-batch shrink of 16-bit data takes the segmented kernel (A rows read once per
 // work item) rather than the per-token one.

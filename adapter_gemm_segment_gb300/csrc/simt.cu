@@ -78,12 +78,17 @@ shrink_warp_kernel(PoolView pool, SegView seg, const T* __restrict__ x, float* _
 // one, they are released at once -- the GEMM starts streaming its weight while the previous
 // linear finishes -- and the first CTA publishes the value once the wait has returned (x and
 // the segments complete); the GEMM loads x after reading it and waits for s as before.
+// beside: every grid before the last one is complete already, and x, the segments and A are not that one's
+// work, so only the first CTA waits for it, for the kernels behind: those wait for this grid's end.
 __device__ __forceinline__ void shrink_dependency_wait(const GroupView& grp, const SegView& seg) {
     if (grp.xready) {
         pdl_trigger();
         pdl_wait();
         if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
             st_release_gpu(const_cast<int32_t*>(seg.nseg) + kXreadyWord, grp.xready);
+    } else if (grp.beside) {
+        pdl_trigger();
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) pdl_wait();
     } else {
         pdl_wait();
         pdl_trigger();
@@ -625,9 +630,10 @@ int shrink_segmented(const PoolView& pv, int n) {
 }
 
 int launch_shrink(const PoolView& pv, const SegView& sv, const void* x, float* s_out, cudaStream_t st, bool tiled,
-                  int* s_parts, int xready) {
+                  int* s_parts, int xready, int beside) {
     GroupView g = single_group(pv);
     g.xready = xready;
+    g.beside = beside;
     return launch_shrink_group(pv, g, sv, x, s_out, st, tiled, s_parts);
 }
 
