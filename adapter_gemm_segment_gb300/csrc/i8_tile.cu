@@ -18,6 +18,12 @@
 // The LoRA term is added there in float32: y[t, o] = sx sw sum + s[t, :] . B[o, :].  Eight more warps compute it
 // during the main loop for the tokens their CTA will finish.  Tokens come in the order of the segments, so
 // neighbouring tokens share their adapter's rows of B.
+//
+// Measured (launches in a graph, the kernel that makes x's codes included): 16, 64, 256 tokens 4096 x 4096 float16
+// 10.6, 11.3, 22.6 us; 256 x 4096 x 11008 32, of which the MMAs take 17: 86 tiles leave 66 of 152 SMs idle, and a
+// split of K would need 172.  With adapters, 64 tokens over 100 of rank 8 14.7; of rank 64 30 (without their B 18); 200
+// tokens 11008 x 4096 over 6 of rank 64 51, of which the shrink before it 12.  Small batches are a chain of latencies: the
+// kernel ahead, its x through TMA, eight steps, the sums' way through the cluster.
 #include <cuda.h>
 
 #include <algorithm>
@@ -44,7 +50,7 @@ constexpr int kIThreads = 64 + 32 * kIWorkers;  // warp 0 loads, 1 MMAs
 constexpr int kILora = 256;       // more threads for the LoRA term
 constexpr int kIASlots = 4;       // steps of the weight in tensor memory, 64 columns each
 constexpr int kIACol = 256;       // behind two accumulators of up to 128 tokens, or one of more
-constexpr int kISRanks = 16;      // columns of the shrink output staged at once
+constexpr int kIMostS = 64;       // columns of the shrink output staged at once, at most
 constexpr uint32_t kIWBytes = kIM * kIK;
 constexpr int kIBars = 384;
 
@@ -62,7 +68,27 @@ struct I8TileArgs {
     const void* B;
     const int32_t* idx;    // by token
     const float* s_in;     // [s_parts][n][R], by token
-    int R, s_parts;
+    int R, s_parts, s_cols;
+};
+
+// Eight columns of a row of B as they are in memory; zeros past `left`.
+template <typename T> struct BRow {
+    uint4 v;  // (16-bit pools: rows of B are whole 16-byte pieces)
+    __device__ __forceinline__ void load(const T* p, int left) {
+        v = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const { unpack8<T>(v, f); }
+};
+template <> struct BRow<float> {
+    float v[8];
+    __device__ __forceinline__ void load(const float* p, int left) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < left ? __ldg(p + e) : 0.f;
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v[e];
+    }
 };
 
 template <typename T, bool FUSE>
@@ -78,9 +104,10 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // once that is idle
     int* G = reinterpret_cast<int*>(smem + (a.alias ? 0 : a.ring_bytes));
     float* L = reinterpret_cast<float*>(smem + a.ring_bytes) + (a.alias ? 0 : a.splits * a.per * kIM);  // FUSE: [per][128] their LoRA terms
-    float* S = L + (FUSE ? a.per * kIM : 0);                      // FUSE: [per][kISRanks] shrink output
-    int* tok_slot = reinterpret_cast<int*>(S + (FUSE ? a.per * kISRanks : 0));  // FUSE: [per] slots of the CTA's tokens,
-    int* row_sm = tok_slot + (FUSE ? a.per : 0);                 // [per] their rows of y,
+    float* S = L + (FUSE ? a.per * kIM : 0);                      // FUSE: [per][s_cols] shrink output
+    int* tok_slot = reinterpret_cast<int*>(S + (FUSE ? a.per * a.s_cols : 0));  // FUSE: [per] slots of the CTA's tokens,
+    int* tok_rank = tok_slot + (FUSE ? a.per : 0);               // FUSE: [per] and their ranks,
+    int* row_sm = tok_rank + (FUSE ? a.per : 0);                 // [per] their rows of y,
     float* sx_sm = reinterpret_cast<float*>(row_sm + a.per);     // [per] and scales
     float* sw_sm = sx_sm + a.per;                                // [128]
     uint64_t* full_w = reinterpret_cast<uint64_t*>(smem_align(reinterpret_cast<uint8_t*>(sw_sm + kIM), 8));  // [8]
@@ -92,8 +119,9 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint64_t* acc_full = a_free + kIASlots;   // [2]
     uint64_t* acc_empty = acc_full + 2;       // [2] (16 warps)
     uint64_t* drained = acc_empty + 2;        // (after an abort) every MMA has completed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
-    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort; a CTA of the cluster has aborted
+    uint64_t* cut = drained + 1;              // flags[2] is known
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut + 1);
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);  // abort; a CTA of the cluster has aborted; steps a chunk
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m_tile = blockIdx.x, split = blockIdx.y, row0 = blockIdx.z * a.n_pad;
@@ -145,6 +173,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             mbar_init(&acc_empty[b], kIWorkers);
         }
         mbar_init(drained, 1);
+        mbar_init(cut, 1);
         flags[0] = flags[1] = 0;
         fence_barrier_init();
         prefetch_tmap(&tmW);
@@ -164,19 +193,6 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     const uint32_t tmem = *tmem_slot;
     if (a.splits > 1 && !a.alias) cluster_arrive();  // (waited for before the first store into another CTA)
     if (a.release) pdl_trigger();
-
-    // Steps a chunk, and chunks: blocks of 256 codes whose products with 128 stay below 2^24 (two blocks less for
-    // those that a chunk has a part of).  An accumulator of more than 128 tokens has no second one beside it, and
-    // reading it holds the MMAs up: 200 x 11008 x 4096, chunks of 1024 codes 41 us, as long as the codes let them 33.
-    int chunk_steps = nkb, nchunks = 1;
-    if (warp >= 1 && warp < 2 + kIWorkers && nkb > kIChunk) {
-        if (!a.early_x) pdl_wait();
-        int top = 1;
-        for (int t = lane; t < n; t += 32) top = max(top, __ldcg(a.peak + row0 + t));
-        top = __reduce_max_sync(0xffffffffu, top);
-        chunk_steps = max(kIChunk, 2 * ((1 << 17) / top - 2));
-        nchunks = (nkb + chunk_steps - 1) / chunk_steps;
-    }
 
     if (warp == 0) {
         if (lane == 0) {
@@ -227,6 +243,22 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     } else if (warp == 1) {
         bool ok = true;
         const uint32_t idesc = idesc_f16(kIM, n_pad, false);
+        // Steps a chunk: blocks of 256 codes whose products with 128 stay below 2^24 (two blocks less for those that
+        // a chunk has a part of).  An accumulator of more than 128 tokens has no second one beside it, and reading
+        // it holds the MMAs up: 200 x 11008 x 4096, chunks of 1024 codes 41 us, as long as the codes let them 33.
+        int chunk_steps = kIChunk;
+        if (nkb > kIChunk) {
+            if (!a.early_x) pdl_wait();
+            int top = 1;
+            for (int t = lane; t < n; t += 32) top = max(top, __ldcg(a.peak + row0 + t));
+            top = __reduce_max_sync(0xffffffffu, top);
+            chunk_steps = max(kIChunk, 2 * ((1 << 17) / top - 2));
+            if (lane == 0) {
+                flags[2] = chunk_steps;
+                mbar_arrive(cut);
+            }
+        }
+        const int nchunks = (nkb + chunk_steps - 1) / chunk_steps;
         int i = 0, s = 0, slot = 0;
         uint32_t ph = 0, aph = 0;
         for (int c = 0; c < nchunks && ok; ++c) {
@@ -286,7 +318,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const uint32_t sums = smem_u32(G) + (split * a.per * kIM + row) * 4;
         const int units = n_pad / 16;
         bool ok = true;
-        int chunk = 0;  // the next to drain
+        int chunk = 0, chunk_steps = kIChunk, nchunks = 1;  // the next to drain; (known from step kIChunk on)
         bool started = a.splits == 1 || a.alias;
         int sum[kIN / 64][16];  // (indexed at run time: in local memory, touched once a chunk, not in registers)
         auto hand_over = [&](int u, const uint32_t* r) {  // to the CTAs that finish these 16 tokens
@@ -359,6 +391,13 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             ok = __all_sync(0xffffffffu, mbar_wait(&full_w[s], 0, flags));
             if (ok) read();
         }
+        auto learn = [&]() {  // the chunks: once, by step kIChunk
+            if (nchunks > 1 || chunk_steps >= nkb) return;
+            ok = __all_sync(0xffffffffu, mbar_wait(cut, 0, flags));
+            if (!ok) return;
+            chunk_steps = flags[2];
+            nchunks = (nkb + chunk_steps - 1) / chunk_steps;
+        };
         for (int i = set; i < nkb && ok; i += 2) {
             uint32_t r[32];
 #pragma unroll
@@ -380,7 +419,8 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             before = slot;
             if ((slot += 2) >= kIASlots) slot -= kIASlots, fph ^= 1;
             // the chunk before is complete by now; or (one accumulator) holds the MMAs up, and enough is converted
-            const bool done = i >= (chunk + 1) * chunk_steps + (nbuf == 2 ? kIChunk / 2 : 2);
+            if (i >= kIChunk) learn();
+            const bool done = ok && i >= (chunk + 1) * chunk_steps + (nbuf == 2 ? kIChunk / 2 : 2);
             const bool more = i + 2 < nkb;
             if (done || (more && !__all_sync(0xffffffffu, mbar_test(&full_w[s], ph)))) {
                 announce();  // (the MMAs need not wait for what follows)
@@ -393,6 +433,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
         }
         if (ok) announce();
+        if (ok) learn();
         while (ok && chunk < nchunks) drain();
         if (!started) cluster_wait();
         if (!ok && lane == 0) flags[0] = 1;
@@ -409,81 +450,99 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         }
     } else if constexpr (FUSE) {
         const int lt = threadIdx.x - kIThreads;  // 0..255
-        if (!a.early_x) pdl_wait();
         // (perm and the segments are older than the kernel ahead)
         const bool st_ok = !a.status || __ldcg(a.status) == LORA_OK;
         if (lt < cnt) {  // (per <= 128)
             const int t = st_ok ? __ldcg(a.perm + row0 + t0 + lt) : 0;
             row_sm[lt] = t;
-            tok_slot[lt] = st_ok ? __ldcg(a.idx + t) : -1;
+            const int slot = st_ok ? __ldcg(a.idx + t) : -1;
+            tok_slot[lt] = slot;
+            tok_rank[lt] = slot >= 0 ? a.table[slot].rank : 0;
         }
-        // ---- the LoRA terms of this CTA's tokens: a feature a thread, every second token ----
-            const int f = lt & 127, half = lt >> 7, o = m_tile * kIM + f, R = a.R;
-            pdl_wait();  // the shrink output
-            const size_t part = (size_t)a.n * R;
-            for (int j0 = 0; j0 < R; j0 += kISRanks) {
-                named_bar_sync(2, 256);
-                for (int e = lt; e < cnt * kISRanks; e += 256) {
-                    const int u = e / kISRanks, j = j0 + e % kISRanks;
-                    float v = 0.f;
-                    if (tok_slot[u] >= 0 && j < a.table[tok_slot[u]].rank) {
-                        const float* sp = a.s_in + (size_t)row_sm[u] * R + j;
-                        for (int p = 0; p < a.s_parts; ++p) v += __ldcg(sp + p * part);
-                    }
-                    S[e] = v;
+        // ---- the LoRA terms of this CTA's tokens: a feature a thread, half of the tokens, four at a time.  What
+        // costs is the latency of B: its rows are held while the tokens' adapter is the same, and those of four
+        // adapters are in flight together where it is not ----
+        const int f = lt & 127, half = lt >> 7, o = m_tile * kIM + f, R = a.R, cols = a.s_cols;
+        const int mid = (cnt + 1) / 2, ub = half ? mid : 0, ue = half ? cnt : mid;
+        constexpr int CH = sizeof(T) == 2 ? 2 : 1;  // pieces of 8 columns at once
+        pdl_wait();  // the shrink output
+        const size_t part = (size_t)a.n * R;
+        for (int j0 = 0; j0 < R; j0 += cols) {
+            __syncwarp();
+            named_bar_sync(2, kILora);
+            for (int e = lt; e < cnt * cols; e += kILora) {
+                const int u = e / cols, j = j0 + e - u * cols;
+                float v = 0.f;
+                if (j < tok_rank[u]) {
+                    const float* sp = a.s_in + (size_t)row_sm[u] * R + j;
+                    for (int p = 0; p < a.s_parts; ++p) v += __ldcg(sp + p * part);
                 }
-                named_bar_sync(2, 256);
-                const int jn = min(kISRanks, R - j0);
-                for (int u0 = half; u0 < cnt; u0 += 8) {  // four tokens at once
+                S[e] = v;
+            }
+            named_bar_sync(2, kILora);
+            if (o >= a.h_out) continue;
+            for (int j = 0; j < min(cols, R - j0); j += 8 * CH) {
+                BRow<T> b[4][CH];
+                const T* Bo = static_cast<const T*>(a.B) + (size_t)o * R + j0 + j;
+                auto load = [&](int k, int slot, int rank) {  // (columns past the rank are zeros)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        b[k][c].load(Bo + (size_t)max(slot, 0) * a.h_out * R + 8 * c, rank > j0 + j + 8 * c ? R - j0 - j - 8 * c : 0);
+                };
+                auto add = [&](int c, const float (&bf)[8], int u, float& acc) {
+                    const float4* sp = reinterpret_cast<const float4*>(S + u * cols + j + 8 * c);
+                    const float4 lo = sp[0], hi = sp[1];
+                    const float sf[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc = fmaf(bf[e], sf[e], acc);
+                };
+                const int pieces = min(CH, (R - j0 - j + 7) / 8);
+                int held = INT_MIN;
+                for (int u0 = ub; u0 < ue; u0 += 4) {
                     float acc[4];
                     int slot[4];
                     bool same = true;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int u = u0 + 2 * k;
-                        slot[k] = u < cnt ? tok_slot[u] : -1;
-                        acc[k] = j0 > 0 && u < cnt ? L[u * kIM + f] : 0.f;
+                        const int u = min(u0 + k, ue - 1);
+                        slot[k] = tok_slot[u];
+                        acc[k] = j0 + j > 0 ? L[u * kIM + f] : 0.f;
                         same = same && slot[k] == slot[0];
                     }
-                    if (o < a.h_out) {
-                        const T* Bo = static_cast<const T*>(a.B) + (size_t)o * R + j0;
-                        if (same) {
-                            if (slot[0] >= 0) {
-                                const T* b = Bo + (size_t)slot[0] * a.h_out * R;
-                                const int jl = min(jn, a.table[slot[0]].rank - j0);  // columns past the rank are zeros
-                                for (int j = 0; j < jl; j += 8) {
-                                    float bf[8];
-                                    load_b8<T>(b, j, R - j0, bf);
+                    if (same) {
+                        if (slot[0] != held) load(0, slot[0], tok_rank[u0]);
+                        held = slot[0];
+                        if (held >= 0)
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const float* sp = S + min(u0 + 2 * k, cnt - 1) * kISRanks + j;
+                            for (int c = 0; c < CH; ++c) {
+                                if (c >= pieces) break;
+                                float bf[8];
+                                b[0][c].get(bf);
 #pragma unroll
-                                        for (int e = 0; e < 8; ++e) acc[k] = fmaf(bf[e], sp[e], acc[k]);
-                                    }
-                                }
+                                for (int k = 0; k < 4; ++k) add(c, bf, min(u0 + k, ue - 1), acc[k]);
                             }
-                        } else {
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) load(k, slot[k], tok_rank[min(u0 + k, ue - 1)]);
+                        held = INT_MIN;
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            if (c >= pieces) break;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                if (slot[k] < 0) continue;
-                                const T* b = Bo + (size_t)slot[k] * a.h_out * R;
-                                const int jl = min(jn, a.table[slot[k]].rank - j0);
-                                const float* sp = S + (u0 + 2 * k) * kISRanks;
-                                for (int j = 0; j < jl; j += 8) {
-                                    float bf[8];
-                                    load_b8<T>(b, j, R - j0, bf);
-#pragma unroll
-                                    for (int e = 0; e < 8; ++e) acc[k] = fmaf(bf[e], sp[j + e], acc[k]);
-                                }
+                                float bf[8];
+                                b[k][c].get(bf);
+                                add(c, bf, min(u0 + k, ue - 1), acc[k]);
                             }
                         }
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        if (u0 + 2 * k < cnt) L[(u0 + 2 * k) * kIM + f] = acc[k];
+                        if (u0 + k < ue) L[(u0 + k) * kIM + f] = acc[k];
                 }
             }
         }
+    }
 
     if (a.splits > 1 && (warp < 2 || warp >= 2 + kIWorkers)) {  // (as the workers have)
         if (a.alias) cluster_arrive();
@@ -584,7 +643,8 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
         a.per = (std::min(x.rows, a.n_pad) + a.splits - 1) / a.splits;
         a.per_inv = 65535 / a.per + 1;  // t / per = t * per_inv >> 16 for t < 256
         a.alias = a.splits == 1 || a.n_pad > 128;
-        const size_t words = (size_t)(a.alias ? 0 : a.splits * a.per * kIM) + (FUSE ? a.per * (kIM + kISRanks + 1) : 0) + 2 * a.per + kIM;
+        if (FUSE) a.s_cols = a.per <= 64 ? std::min(kIMostS, (lora->pool->R + 15) / 16 * 16) : 16;
+        const size_t words = (size_t)(a.alias ? 0 : a.splits * a.per * kIM) + (FUSE ? a.per * (kIM + a.s_cols + 2) : 0) + 2 * a.per + kIM;
         const size_t tail = words * 4 + kIBars + 1024 + 16;
         // stages of x (at most 4; of 64 codes for more than 128 tokens), then of w (4, 6 or 8: an even number, as the
         // workers' halves alternate)
