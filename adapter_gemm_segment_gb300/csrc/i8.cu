@@ -49,7 +49,7 @@ static I8View view_of(const lora_i8_matrix* m) { return i8_view(m->codes_dev, m-
 constexpr int kI8Small = 8;
 
 // Above this many tokens the pair kernel.
-constexpr int kI8Tile = 256;
+constexpr int kI8Tile = 512;
 
 // What a product keeps in its workspace: x in float16 codes and its scales, and above kI8Tile rows the weight
 // in float16 codes.

@@ -53,6 +53,7 @@ constexpr int kIACol = 256;       // behind two accumulators of up to 128 tokens
 constexpr int kIMostS = 64;       // columns of the shrink output staged at once, at most
 constexpr uint32_t kIWBytes = kIM * kIK;
 constexpr int kIBars = 384;
+constexpr size_t kISmemMax = 227 * 1024;
 
 struct I8TileArgs {
     void* y;
@@ -452,7 +453,7 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const int lt = threadIdx.x - kIThreads;  // 0..255
         // (perm and the segments are older than the kernel ahead)
         const bool st_ok = !a.status || __ldcg(a.status) == LORA_OK;
-        if (lt < cnt) {  // (per <= 128)
+        if (lt < cnt) {  // (per <= kILora)
             const int t = st_ok ? __ldcg(a.perm + row0 + t0 + lt) : 0;
             row_sm[lt] = t;
             const int slot = st_ok ? __ldcg(a.idx + t) : -1;
@@ -608,6 +609,76 @@ i8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// Clusters of that many CTAs that the GPU holds at once: of 4 nearly a quarter of the SMs, of 8 far fewer than an eighth,
+// as a cluster lies in one group of SMs.
+static int max_clusters(int size) {
+    static int held[9] = {};  // every variant takes most of an SM's shared memory: the same for each
+    if (size == 1) return num_sms();
+    if (!held[size]) {
+        cudaLaunchConfig_t q;
+        memset(&q, 0, sizeof(q));
+        q.gridDim = dim3(1, size);
+        q.blockDim = dim3(kIThreads + kILora);
+        q.dynamicSmemBytes = kISmemMax;
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = 1;
+        qa[0].val.clusterDim.y = size;
+        qa[0].val.clusterDim.z = 1;
+        q.attrs = qa;
+        q.numAttrs = 1;
+        int c = 0;
+        if (cudaFuncSetAttribute(i8_tile_kernel<float, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kISmemMax) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&c, (const void*)i8_tile_kernel<float, true>, &q) != cudaSuccess || c < 1) {
+            (void)cudaGetLastError();
+            c = std::max(1, num_sms() / size / 2);
+        }
+        held[size] = c;
+    }
+    return held[size];
+}
+
+// How a launch cuts its work: tokens in groups of n_pad, K among `splits` CTAs, and the stages that leaves room for.
+struct TilePlan {
+    int n_pad, groups, splits, kb_per_split, per, alias, xk, xstages, wstages, s_cols, ring_bytes;
+    size_t smem;
+};
+static bool tile_plan(int n, int m_tiles, int kb, bool fuse, int R, int groups, int splits, TilePlan& p) {
+    p.n_pad = ((n + groups - 1) / groups + 15) / 16 * 16;
+    p.groups = (n + p.n_pad - 1) / p.n_pad;
+    p.kb_per_split = (kb + splits - 1) / splits;
+    p.splits = (kb + p.kb_per_split - 1) / p.kb_per_split;
+    p.per = (std::min(n, p.n_pad) + p.splits - 1) / p.splits;
+    p.alias = p.splits == 1 || p.n_pad > 128;
+    p.s_cols = !fuse ? 0 : p.per <= 64 ? std::min(kIMostS, (R + 15) / 16 * 16) : 16;
+    const size_t words = (size_t)(p.alias ? 0 : p.splits * p.per * kIM) + (fuse ? p.per * (kIM + p.s_cols + 2) : 0) + 2 * p.per + kIM;
+    const size_t tail = words * 4 + kIBars + 1024 + 16;
+    // stages of x (at most 4; of 64 codes for more than 128 tokens), then of w (4, 6 or 8: an even number, as the
+    // workers' halves alternate)
+    p.xk = p.n_pad > 128 ? 1 : 2;
+    const size_t x_bytes = (size_t)p.n_pad * 128 * p.xk;
+    p.wstages = 0;
+    for (int x = 4; x >= 2 && !p.wstages && tail < kISmemMax; --x) {
+        const size_t room = kISmemMax - tail, left = room > x * x_bytes ? room - x * x_bytes : 0;
+        p.xstages = x;
+        p.wstages = (int)std::min<size_t>(left / kIWBytes / 2 * 2, 8);
+        if (p.wstages < (x > 2 && p.xk == 2 ? 6 : 4) || (p.xk == 1 && x < 3)) p.wstages = 0;
+    }
+    p.ring_bytes = (int)std::max<size_t>(p.wstages * kIWBytes + p.xstages * x_bytes,
+                                         p.alias ? (size_t)p.splits * p.per * kIM * 4 : 0);
+    p.smem = p.ring_bytes + tail;
+    return p.wstages && p.smem <= kISmemMax;
+}
+// What a plan takes, in units of 10 ns: rounds of the grid, a CTA's steps of 128 codes, and what does not depend on K.
+// Above 128 tokens there is one accumulator and the sums cross the cluster once the rings are idle.  (4096 x 4096: groups
+// of 128 tokens 13.3 us with 8 steps, 17.8 with 16, 24.3 with 32; of 256 22.3 with 8, 27.0 with 16.)
+static long long tile_cost(const TilePlan& p, int m_tiles) {
+    const long long clusters = (long long)m_tiles * p.groups, held = max_clusters(p.splits);
+    const int n = p.n_pad;
+    const int fix = n <= 128 ? 400 + 2 * n : 300 + (p.splits > 1 ? 4 : 2) * n, step = n <= 128 ? 45 : 45 + (n - 128) / 9;
+    return (clusters + held - 1) / held * (fix + (long long)p.kb_per_split * step);
+}
+
 template <typename T, bool FUSE>
 static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ldy, int32_t* status, bool early_x, bool release,
                          const I8Lora* lora, cudaStream_t st) {
@@ -628,42 +699,27 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
     // y is written 16 bytes at a time when every row starts on a 16-byte boundary
     a.vec = reinterpret_cast<uintptr_t>(y) % 16 == 0 && (ldy * (long long)sizeof(T)) % 16 == 0;
     const int m_tiles = (w.rows + kIM - 1) / kIM;
-    int groups = 0;
-    size_t smem = 0;
-    // groups of up to 256 tokens, of 128 or 64 where those leave no room for the stages
-    for (int most = kIN; most >= 64; most /= 2) {
-        groups = (x.rows + most - 1) / most;
-        a.n_pad = ((x.rows + groups - 1) / groups + 15) / 16 * 16;
-        groups = (x.rows + a.n_pad - 1) / a.n_pad;
-        // CTAs (a cluster) that share K: as many as let every tile have an SM a CTA
-        const long long tiles = (long long)m_tiles * groups;
-        const int splits = (int)std::min<long long>({std::max<long long>(1, num_sms() / tiles), 8, a.kb_total});
-        a.kb_per_split = (a.kb_total + splits - 1) / splits;
-        a.splits = (a.kb_total + a.kb_per_split - 1) / a.kb_per_split;
-        a.per = (std::min(x.rows, a.n_pad) + a.splits - 1) / a.splits;
-        a.per_inv = 65535 / a.per + 1;  // t / per = t * per_inv >> 16 for t < 256
-        a.alias = a.splits == 1 || a.n_pad > 128;
-        if (FUSE) a.s_cols = a.per <= 64 ? std::min(kIMostS, (lora->pool->R + 15) / 16 * 16) : 16;
-        const size_t words = (size_t)(a.alias ? 0 : a.splits * a.per * kIM) + (FUSE ? a.per * (kIM + a.s_cols + 2) : 0) + 2 * a.per + kIM;
-        const size_t tail = words * 4 + kIBars + 1024 + 16;
-        // stages of x (at most 4; of 64 codes for more than 128 tokens), then of w (4, 6 or 8: an even number, as the
-        // workers' halves alternate)
-        a.xk = a.n_pad > 128 ? 1 : 2;
-        const size_t room = 227 * 1024 - tail, x_bytes = (size_t)a.n_pad * 128 * a.xk;
-        a.xstages = a.wstages = 0;
-        for (int x = 4; x >= 2 && !a.wstages && tail < 227 * 1024; --x) {
-            const size_t left = room > x * x_bytes ? room - x * x_bytes : 0;
-            a.xstages = x;
-            a.wstages = (int)std::min<size_t>(left / kIWBytes / 2 * 2, 8);
-            if (a.wstages < (x > 2 && a.xk == 2 ? 6 : 4) || (a.xk == 1 && x < 3)) a.wstages = 0;
+    TilePlan best;
+    long long cost = LLONG_MAX;
+    for (int most = kIN; most >= 64; most /= 2)
+        for (int splits = std::min(8, a.kb_total); splits >= 1; --splits) {
+            TilePlan p;
+            if (!tile_plan(x.rows, m_tiles, a.kb_total, FUSE, FUSE ? lora->pool->R : 0, (x.rows + most - 1) / most, splits, p)) continue;
+            const long long c = tile_cost(p, m_tiles);
+            if (c < cost) cost = c, best = p;
         }
-        a.ring_bytes = (int)std::max<size_t>(a.wstages * kIWBytes + a.xstages * x_bytes,
-                                             a.alias ? (size_t)a.splits * a.per * kIM * 4 : 0);
-        if (a.splits == 1) a.ring_bytes = (int)std::max<size_t>(a.ring_bytes, (size_t)a.n_pad * kIM * 4);
-        smem = a.ring_bytes + tail;
-        if (a.wstages) break;
-    }
-    if (!a.wstages || smem > 227 * 1024 || groups > 65535) return set_error(LORA_EUNSUP, "8-bit product of %d rows", x.rows);
+    if (cost == LLONG_MAX || best.groups > 65535) return set_error(LORA_EUNSUP, "8-bit product of %d rows", x.rows);
+    a.n_pad = best.n_pad;
+    a.splits = best.splits;
+    a.kb_per_split = best.kb_per_split;
+    a.per = best.per;
+    a.per_inv = 65535 / a.per + 1;  // t / per = t * per_inv >> 16 for t < 256
+    a.alias = best.alias;
+    a.xk = best.xk;
+    a.xstages = best.xstages;
+    a.wstages = best.wstages;
+    a.s_cols = best.s_cols;
+    a.ring_bytes = best.ring_bytes;
     if (lora) {
         const PoolView& pv = *lora->pool;
         a.table = pv.table;
@@ -679,15 +735,15 @@ static int launch_tile_t(const I8Rows& x, const I8View& w, void* y, long long ld
     if (rc) return rc;
     static bool attr_set = false;
     if (!attr_set) {
-        LORA_CUDA_TRY(cudaFuncSetAttribute(i8_tile_kernel<T, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024));
+        LORA_CUDA_TRY(cudaFuncSetAttribute(i8_tile_kernel<T, FUSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kISmemMax));
         attr_set = true;
     }
     void* args[] = {(void*)&mW, (void*)&mX, (void*)&a};
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(m_tiles, a.splits, groups);
+    cfg.gridDim = dim3(m_tiles, a.splits, best.groups);
     cfg.blockDim = dim3(kIThreads + (FUSE ? kILora : 0));
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = best.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

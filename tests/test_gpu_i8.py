@@ -411,6 +411,20 @@ def test_linear_many_adapters_in_large_batches(lib, n, slots, r_max):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,h_in,h_out,ranks,r_max", [
+    (130, 1000, 1304, [8] * 100, 8), (257, 2056, 136, [8] * 100, 8), (320, 520, 264, [64, 8, 16], 64), (400, 3000, 2056, [16] * 30, 16),
+    (511, 1032, 520, [32, 24], 32), (512, 520, 4104, [8, 64], 64), (513, 520, 264, [8] * 100, 8)])
+def test_linear_in_several_groups_of_tokens(lib, dtype, n, h_in, h_out, ranks, r_max):
+    check_linear(lib, wl.random_case(n + h_in, n, h_in, h_out, ranks, r_max=r_max, dtype=dtype, p_base=0.1))
+
+
+@pytest.mark.parametrize("n,m,k", [(48, 2056, 2048), (160, 4104, 4096), (256, 2048, 2100), (257, 1000, 1000), (320, 11008, 600), (384, 130, 40000),
+                                   (511, 8, 1500), (512, 3000, 1024)])
+def test_product_in_several_groups_of_tokens(lib, n, m, k):
+    check_product(lib, gauss(n, k, 3), gauss(m, k, 4, scale=0.02), torch.float32, pad=1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", [1, 7, 40, 130, 300, 700])
 def test_adapters_that_are_not_finite_reach_their_own_tokens_only(lib, dtype, n):
     slots = 3 if n < 100 else 4
