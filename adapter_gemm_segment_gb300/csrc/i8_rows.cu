@@ -7,7 +7,9 @@
 // codes (and where a bfloat16 row's largest value is even, one element in 200 lies that close), and with
 // them equal inputs would not give equal bytes on every path.
 //
-// Every kernel here moves its rows once and is bound by memory, below a few MB by the launch.
+// Every kernel here moves its rows once and is bound by memory, below a few MB by the launch.  16384 x 4096
+// bfloat16, us (at the copy rate): quantise 42 (30), read back 32 (30), norm with residual, y and codes 118 (90).  The
+// quantiser's and the norm's instructions fill 64 and 70 % of the issue slots.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -276,7 +278,7 @@ i8_quantize_kernel(const T* x, long long ld, I8View q, RowPlan pl, const int32_t
 // The first n CTAs each take a row of x: quantise it (or turn its stored codes into float16); the others each a
 // token, 8 rows of its adapter's A and a part of K, s[part][t][j] = (alpha / r) x[t] . A[j] over the part.  Both
 // read x, a few KB; bound by latency, which one launch less shortens (one token 4096 x 4096 float16: 25 us for
-// the linear as three launches).
+// the linear as three launches, 8 as two).
 constexpr int kFrontThreads = 256;
 struct FrontArgs {
     PoolView pool;

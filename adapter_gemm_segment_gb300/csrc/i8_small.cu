@@ -2,7 +2,8 @@
 //
 // y[t, o] = sx[t] sw[o] sum_k cx[t, k] cw[o, k] (+ s[t, :] . B_slot(t)[o, :]): the sum in 32-bit integers by
 // four-way dot products, so it is exact in any order.  The weight streams through once per group of NT
-// tokens; a warp takes RW of its rows, 16 bytes a lane, and its lanes' sums meet in one reduction.
+// tokens; a warp takes RW of its rows, 16 bytes a lane, and its lanes' sums meet in one reduction.  Bound by memory
+// and latency: 4096 x 4096 float16 5.3 us with one token (its bytes 2.5), 6.9 with 8; to 11008 features 17.2 with 8.
 #include <algorithm>
 #include <cstring>
 

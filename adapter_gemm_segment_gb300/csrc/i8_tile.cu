@@ -6,7 +6,7 @@
 // partial sums.  Codes go through tcgen05.mma kind::f16; every chunk of so many the accumulator is read into
 // 32-bit integers and started again (usually once, at the end).
 //
-// The weight is the MMA's M side (128 features a tile) and up to 128 tokens its N side.  The weight stays
+// The weight is the MMA's M side (128 features a tile) and up to 256 tokens its N side.  The weight stays
 // in bytes until it is on the SM: TMA brings 128 x 128 codes, sixteen warps turn them into float16 and store
 // them to tensor memory as the MMA's A operand (tcgen05.st), so float16 weights never pass through shared
 // memory.  A warp's turn (waits, loads, conversion, store) takes about 900 clocks for 32 features x 64 codes,
@@ -19,10 +19,10 @@
 // during the main loop for the tokens their CTA will finish.  Tokens come in the order of the segments, so
 // neighbouring tokens share their adapter's rows of B.
 //
-// Measured (launches in a graph, the kernel that makes x's codes included): 16, 64, 256 tokens 4096 x 4096 float16
-// 10.6, 11.3, 22.6 us; 256 x 4096 x 11008 32, of which the MMAs take 17: 86 tiles leave 66 of 152 SMs idle, and a
-// split of K would need 172.  With adapters, 64 tokens over 100 of rank 8 14.7; of rank 64 30 (without their B 18); 200
-// tokens 11008 x 4096 over 6 of rank 64 51, of which the shrink before it 12.  Small batches are a chain of latencies: the
+// Measured (launches in a graph, the kernel that makes x's codes included): 16, 64, 256, 512 tokens 4096 x 4096 float16
+// 10.5, 11.2, 17.9, 24.2 us; 256 x 4096 x 11008 32, of which the MMAs take 17: 86 tiles leave 66 of 152 SMs idle, and a
+// split of K would need 172.  With adapters, 64 tokens over 100 of rank 8 14.6; of rank 64 30 (without their B 18); 200
+// tokens 11008 x 4096 over 6 of rank 64 50, of which the shrink before it 12.  Small batches are a chain of latencies: the
 // kernel ahead, its x through TMA, eight steps, the sums' way through the cluster.
 #include <cuda.h>
 

@@ -191,8 +191,8 @@ struct I8Rows {
     // how many products are sure to stay whole numbers in float32
     const int* peak;
 };
-// On the tensor cores.  Every kernel that could have written w has completed when this grid starts (the kernel
-// ahead waited for it); early_x: so has x.  release: the kernel behind may be released early (never a product by itself, whose y may be
+// On the tensor cores.  Every kernel that could have written w has completed when this grid starts (one ahead waited
+// for it before it released those behind); early_x: so has x.  release: the kernel behind may be released early (never a product by itself, whose y may be
 // a weight that a 16-bit linear streams unwaited).
 int launch_i8_tile(const I8Rows& x, const I8View& w, void* y, int dtype, long long ldy, int32_t* status, bool early_x,
                    bool release, const I8Lora* lora, cudaStream_t st);

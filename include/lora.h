@@ -435,7 +435,7 @@ int lora_fp4_linear_fwd(lora_pool_t pool, const lora_fp4_matrix* w, const void* 
  *   codes   row r at r * pitch, pitch = 16 * ceil(cols / 16) bytes: int8, 0 from cols to pitch
  *   scales  float32, one a row; element (r, k) stands for codes[r][k] * scales[r]
  * Both 256-byte aligned, owned by the caller.  rows >= 0, 1 <= cols <= 131071 (LORA_EUNSUP above: a sum
- * of products has 32 bits). */
+ * of products has 32 bits; and above 2^31 - 256 rows). */
 typedef struct {
     void* codes_dev;
     void* scales_dev;
@@ -464,7 +464,7 @@ int lora_i8_dequantize(const lora_i8_matrix* q, void* out_dev, int dtype, int64_
  * The row's statistics are held to about 2^-44, so out's codes are those of the real v.  A row that holds an
  * infinity or a NaN gets a NaN scale and codes 0.
  *   x, residual (nullable), residual_out (nullable without residual; may be residual or x), y (nullable;
- *   may be x): [rows, cols] of dtype with row strides ldx, ldr, ldro, ldy >= cols; weight [cols];
+ *   may be x, not residual_out): [rows, cols] of dtype with row strides ldx, ldr, ldro, ldy >= cols; weight [cols];
  *   out (nullable): a stored matrix [rows, cols].  y or out is wanted.  eps in [1e-12, 1]. */
 typedef struct {
     const void* x_dev;
@@ -496,11 +496,11 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
  * or, when xq is not NULL, xq (x's stored form from lora_i8_quantize, or lora_i8_rmsnorm's out beside its y
  * as x; projections that read the same x share it); the LoRA term takes x as it is, in the pool's dtype.
  * x_dev, y_dev, seg, errors and the device status word as in lora_linear_fwd.  The LoRA term is computed in
- * float32 and added to the base term in float32; y is rounded once.  (Batches of more than 256 tokens of
+ * float32 and added to the base term in float32; y is rounded once.  (Batches of more than 512 tokens of
  * 16-bit pools take it from the tensor cores, its shrink output s = (alpha / r) x A^T carried in two parts, to
  * 2^-23 of itself.)  An infinity or NaN in one adapter reaches that adapter's tokens only.  The same call gives
  * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 5 kernels.
- * LORA_EUNSUP: batches of more than 256 tokens with x or w of 2^36 codes and more, or of 2^52 products.
+ * LORA_EUNSUP: batches of more than 512 tokens with x or w of 2^36 codes and more, or of 2^52 products.
  * A workspace of lora_i8_linear_workspace_bytes(pool, n) serves every batch of up to n tokens.  The y of a
  * linear, this one included, is not to be w's codes or scales without a wait in between; nor is it, or what
  * lora_i8_rmsnorm wrote, to be the W of a 16-bit linear.  What lora_i8_quantize, lora_i8_dequantize or

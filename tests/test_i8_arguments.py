@@ -30,7 +30,9 @@ def test_bytes():
     assert ags.lora_i8_bytes(3, 17) == (96, 12)
     assert ags.lora_i8_bytes(0, 1) == (0, 0)
     assert ags.lora_i8_bytes(2, 131071) == (2 * 131072, 8)
-    for shape, code in (((-1, 4), ags.LORA_EINVAL), ((4, 0), ags.LORA_EINVAL), ((4, 131072), ags.LORA_EUNSUP)):
+    assert ags.lora_i8_bytes(2 ** 31 - 256, 1) == (16 * (2 ** 31 - 256), 4 * (2 ** 31 - 256))
+    for shape, code in (((-1, 4), ags.LORA_EINVAL), ((4, 0), ags.LORA_EINVAL), ((4, 131072), ags.LORA_EUNSUP),
+                        ((2 ** 31 - 255, 1), ags.LORA_EUNSUP)):
         with pytest.raises(ags.LoraError) as e:
             ags.lora_i8_bytes(*shape)
         assert e.value.code == code
@@ -57,7 +59,8 @@ def test_quantize_and_read_back_refusals():
 def norm_args(**kw):
     out = mat(4, 8)
     a = ags.lora_i8_norm()
-    a.x_dev = a.weight_dev = a.y_dev = a.residual_dev = a.residual_out_dev = P
+    a.x_dev = a.weight_dev = a.residual_dev = a.residual_out_dev = P
+    a.y_dev = 2 * P
     a.ldx = a.ldr = a.ldro = a.ldy = 8
     a.rows, a.cols, a.dtype, a.eps = 4, 8, 0, 1e-5
     a.out = ctypes.pointer(out)
@@ -73,7 +76,7 @@ def norm_args(**kw):
     (dict(eps=0.0), ags.LORA_EINVAL), (dict(eps=float("nan")), ags.LORA_EINVAL), (dict(eps=2.0), ags.LORA_EINVAL),
     (dict(eps=-1e-5), ags.LORA_EINVAL), (dict(rows=-1), ags.LORA_EINVAL), (dict(cols=0), ags.LORA_EINVAL),
     (dict(rows=5), ags.LORA_EINVAL), (dict(cols=131072, ldx=131072), ags.LORA_EUNSUP), (dict(x_dev=P + 2), ags.LORA_EINVAL),
-    (dict(weight_dev=P + 2), ags.LORA_EINVAL), (dict(y_dev=P + 1), ags.LORA_EINVAL)])
+    (dict(weight_dev=P + 2), ags.LORA_EINVAL), (dict(y_dev=P + 1), ags.LORA_EINVAL), (dict(y_dev=P), ags.LORA_EINVAL)])
 def test_norm_refusals(change, code):
     refused(ags.load_library().lora_i8_rmsnorm(ctypes.byref(norm_args(**change)), None), code)
 
