@@ -669,9 +669,119 @@ def test_weights_quantised_right_before_their_product(lib):
         pool.close()
 
 
+FIRST = """
+import torch, sys
+import adapter_gemm_segment_gb300 as lib
+n = int(sys.argv[1])
+g = torch.Generator("cuda").manual_seed(1)
+W, x = torch.randn(264, 512, generator=g, device="cuda").half(), torch.randn(n, 512, generator=g, device="cuda").half()
+w, q, y = lib.I8Matrix(264, 512), lib.I8Matrix(n, 512), torch.zeros(n, 264, device="cuda")
+pool = lib.LoraPool(512, 264, 8, 1, torch.float16, "cuda")
+seg = pool.segment(torch.full((n,), -1, dtype=torch.int32, device="cuda"))
+ws, lws, z = torch.empty(1 << 24, dtype=torch.uint8, device="cuda"), pool.i8_linear_workspace(n), torch.zeros(n, 264, device="cuda").half()
+ones, h = torch.ones(512, device="cuda").half(), torch.empty_like(x)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    lib.lora_i8_quantize(W, w)
+    lib.lora_i8_rmsnorm(x, ones, 1e-5, out=q, y=h)
+    lib.lora_i8_matmul(q, w, y, ws)
+    pool.i8_linear(w, h, seg, xq=q, y=z, ws=lws)
+graph.replay()
+torch.cuda.synchronize()
+first = y.clone(), z.clone()
+assert first[0].abs().sum() > 0 and torch.equal(first[0].half(), first[1])
+lib.lora_i8_matmul(q, w, y, ws)
+pool.i8_linear(w, h, seg, xq=q, y=z, ws=lws)
+torch.cuda.synchronize()
+assert torch.equal(y, first[0]) and torch.equal(z, first[1])
+"""
+
+
+@pytest.mark.parametrize("n", [3, 60, 700])
+def test_the_first_calls_of_a_process_under_capture(n):
+    out = subprocess.run([sys.executable, "-c", FIRST, str(n)], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert out.returncode == 0, out.stderr[-2000:]
+
+
 def test_the_layer_example_runs():
     out = subprocess.run([sys.executable, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "i8_layer.py"),
                           "--tokens", "12", "--prefill", "600", "--adapters", "3", "--hidden", "264", "--ff", "520"],
                          capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, out.stderr[-2000:]
     assert out.stdout.count("relative difference") == 10
+
+
+# ---- offsets past 32 bits ---------------------------------------------------------------------------
+
+def test_stored_matrices_past_32_bits(lib):
+    """Codes past 2^31 bytes: the last rows are those of the last rows alone, through every kernel."""
+    rows, cols = 18000, 121000
+    g = torch.Generator("cuda").manual_seed(1)
+    W = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    last = W[-300:].clone()
+    w, wl_ = lib.lora_i8_quantize(W, lib.I8Matrix(rows, cols)), lib.lora_i8_quantize(last, lib.I8Matrix(300, cols))
+    assert torch.equal(w.codes[-300:], wl_.codes) and torch.equal(w.scales[-300:], wl_.scales)
+    back = lib.lora_i8_dequantize(w, torch.empty_like(W))
+    assert torch.equal(back[-300:], lib.lora_i8_dequantize(wl_, torch.empty_like(last)))
+    gain, q = torch.randn(cols, generator=g, device="cuda").bfloat16(), lib.I8Matrix(rows, cols)
+    lib.lora_i8_rmsnorm(W, gain, 1e-5, out=q, y=back)
+    ql, yl = lib.I8Matrix(300, cols), torch.empty_like(last)
+    lib.lora_i8_rmsnorm(last, gain, 1e-5, out=ql, y=yl)
+    assert torch.equal(q.codes[-300:], ql.codes) and torch.equal(q.scales[-300:], ql.scales) and torch.equal(back[-300:], yl)
+    for n in (3, 40, 600):
+        x = lib.lora_i8_quantize(W[:n], lib.I8Matrix(n, cols))
+        y, z = torch.empty(n, rows, device="cuda"), torch.empty(n, 300, device="cuda")
+        lib.lora_i8_matmul(x, w, y)
+        lib.lora_i8_matmul(x, wl_, z)
+        assert torch.equal(y[:, -300:], z), n
+    # ... as the many tokens of a product
+    y, z = torch.empty(rows, 300, device="cuda"), torch.empty(300, 300, device="cuda")
+    lib.lora_i8_matmul(w, wl_, y)
+    lib.lora_i8_matmul(wl_, wl_, z)
+    assert torch.equal(y[-300:], z)
+
+
+@pytest.mark.parametrize("n,m", [(2, 1200000000), (500, 4500000), (70001, 40008)])
+def test_outputs_past_32_bits(lib, n, m):
+    """y of more than 2^31 elements: its last rows and columns."""
+    g = torch.Generator("cuda").manual_seed(2)
+    x, w = lib.I8Matrix(n, 16), lib.I8Matrix(m, 16)
+    for q in (x, w):
+        q.codes.copy_(torch.randint(-127, 128, q.codes.shape, generator=g, device="cuda", dtype=torch.int8))
+        q.scales.fill_(0.25)
+    y = torch.empty(n, m, device="cuda", dtype=torch.float16)
+    lib.lora_i8_matmul(x, w, y)
+    rows, cols = torch.arange(max(0, n - 200), n, device="cuda"), torch.arange(m - 300, m, device="cuda")
+    ref = (x.codes[rows].double() @ w.codes[cols].double().T) / 16
+    assert torch.equal(y[rows[:, None], cols].double(), ref.half().double())
+    assert y.flatten()[2 ** 31 - 5:2 ** 31 + 5].isfinite().all()
+
+
+@pytest.mark.parametrize("n", [5, 60, 700])
+def test_adapters_past_32_bits(lib, n):
+    """B of more than 2^31 elements: the last features of the last slots."""
+    S, R, h_in, h_out, m = 100, 64, 64, 400000, 256
+    g = torch.Generator("cuda").manual_seed(3)
+    A = [torch.randn(R, h_in, generator=g, device="cuda").bfloat16() * 0.1 for _ in range(S)]
+    Bl = [torch.randn(m, R, generator=g, device="cuda").bfloat16() * 0.1 for _ in range(S)]
+    big, small = lib.LoraPool(h_in, h_out, R, S, torch.bfloat16, "cuda"), lib.LoraPool(h_in, m, R, S, torch.bfloat16, "cuda")
+    B = torch.zeros(h_out, R, device="cuda", dtype=torch.bfloat16)
+    for s in range(S):
+        B[-m:] = Bl[s]
+        big.load_slot(s, A[s], B, 2.0 * R)
+        torch.cuda.synchronize()
+    small.load_slots(range(S), A, Bl, [2.0 * R] * S)
+    torch.cuda.synchronize()
+    W = torch.randn(h_out, h_in, generator=g, device="cuda").bfloat16()
+    x = torch.randn(n, h_in, generator=g, device="cuda").bfloat16()
+    idx = torch.randint(S - 4, S, (n,), generator=g, device="cuda", dtype=torch.int32)
+    y = big.i8_linear(lib.lora_i8_quantize(W, lib.I8Matrix(h_out, h_in)), x, big.segment(idx))
+    z = small.i8_linear(lib.lora_i8_quantize(W[-m:], lib.I8Matrix(m, h_in)), x, small.segment(idx))
+    # the same sums, in another order at most: both rounded to the type, and 160 float32 terms that add up to about 41
+    # in magnitude (2 * 64 * 0.064 of x . A each with 64 * 0.08 of B), 160 * 41 * 2^-24 = 4e-4
+    assert ((y[:, -m:].float() - z.float()).abs() <= 2.0 ** -7 * z.float().abs() + 1e-3).all()
+    assert z.float().abs().mean() > 1
+    big.close()
+    small.close()
