@@ -71,23 +71,27 @@ static I8ProductWs product_ws(int n, int h_out, int h_in) {
     return L;
 }
 
-// Batches of more than 512 tokens that may be spread over many adapters (fewer than 100 tokens a slot; above 2048
-// tokens 16): the product in float32 into the workspace, and a segmented expand after it.  The pair kernel would build
-// blocks of B for every adapter that a tile meets, and the host does not know which.  (4096 x 4096, us, separate /
-// fused: 513 tokens in no order over 6 adapters of rank 64 81 / 149, over 30 of rank 16 55 / 274, in runs of 512 over 6
-// of rank 64 85 / 75; 2048 tokens over 30 of rank 16 114 / 303, in runs of 64 over 30 of rank 8 103 / 106, in runs of
-// 512 over 100 of rank 16 111 / 99; 4096 tokens over 30 of rank 16 200 / 354, in runs over 100 206 / 149.)
-constexpr long long kI8SumElements = 32 << 20;
-constexpr int kI8Spread = 2048;
+// Batches of more than 512 tokens that may be spread over many adapters: the product in float32 into the workspace,
+// the per-token or segmented shrink, and a segmented expand.  The tiles of the tensor-core shrink and of the pair kernel
+// work through every adapter that they meet, and the host does not know which.  So: fewer than 16 tokens a slot; or
+// fewer than 128 where y and the shrink's reads are small.  (us, separate / fused, 4096 x 4096: 513 tokens in no order
+// over 6 adapters of rank 64 81 / 149, over 30 of rank 16 55 / 274, in runs of 512 over 6 of rank 64 85 / 75; 2048 tokens
+// over 30 of rank 16 114 / 303, in runs of 64 over 30 of rank 8 103 / 106, in runs of 512 over 100 of rank 16 111 / 99;
+// 4096 tokens in runs over 100 206 / 149.  8000 tokens 4096 x 256 over 100 of rank 8 93 / 442, in runs 90 / 81; 16384
+// tokens 4096 x 88 in runs over 4 of rank 64 475 / 134.)
+constexpr long long kI8SumElements = 32 << 20, kI8FewElements = 8 << 20, kI8ShrinkProducts = 1 << 29;
 static bool separate(const PoolView& pv, int n) {
-    return pv.dtype != LORA_F32 && n > kI8Tile && n < (n <= kI8Spread ? 100LL : 16LL) * std::min(n, pv.S) &&
-           (long long)n * pv.h_out <= kI8SumElements;
+    const long long slots = std::min(n, pv.S), y = (long long)n * pv.h_out;
+    return pv.dtype != LORA_F32 && n > kI8Tile &&
+           ((n < 16 * slots && y <= kI8SumElements) ||
+            (n < 128 * slots && y <= kI8FewElements && (long long)n * pv.R * pv.h_in <= kI8ShrinkProducts));
 }
 // The largest such batch of at most n tokens (0: none).
 static int most_separate(const PoolView& pv, int n) {
-    const long long all = std::min<long long>(n, kI8SumElements / pv.h_out);
-    const int many = (int)std::min<long long>(all, 16LL * pv.S - 1), few = (int)std::min<long long>({all, kI8Spread, 100LL * pv.S - 1});
-    return many > few && separate(pv, many) ? many : separate(pv, few) ? few : 0;
+    const int a = (int)std::min<long long>({(long long)n, 16LL * pv.S - 1, kI8SumElements / pv.h_out});
+    const int b = (int)std::min<long long>({(long long)n, 128LL * pv.S - 1, kI8FewElements / pv.h_out,
+                                            kI8ShrinkProducts / ((long long)pv.R * pv.h_in)});
+    return std::max(separate(pv, a) ? a : 0, separate(pv, b) ? b : 0);
 }
 
 // Workspace of lora_i8_linear_fwd: the shrink output in its K parts, x's codes (in bytes for a few tokens,
