@@ -148,6 +148,13 @@ template <typename T> __device__ __forceinline__ Raw<T> from8(const float (&f)[8
     return r;
 }
 
+// Not 0 where an element is not.
+template <typename T> __device__ __forceinline__ uint32_t any_bits(const Raw<T>& r) {
+    const uint32_t b = r.v.x | r.v.y | r.v.z | r.v.w;
+    if constexpr (sizeof(T) == 4) return (b | r.w.x | r.w.y | r.w.z | r.w.w) & 0x7fffffffu;
+    return b & 0x7fff7fffu;
+}
+
 // A row's place in a launch: G threads (a warp, several rows a CTA, or the CTA), its vectors, and whether they
 // are kept in shared memory between the two passes over the row (else the second reads them again).  Registers
 // would hold a quarter as many rows on an SM (16384 x 4096 bfloat16 quantised: 102 us).
@@ -446,7 +453,8 @@ i8_dequantize_kernel(I8View q, T* __restrict__ out, long long ld) {
 // have to be those of the real h r w / s, so what a whole row shares is held in two float32 parts: the sum
 // of squares (each square and each addition with its rounding error), r and r / s, to about 2^-44.  An
 // element then costs one product u = h w (exact in two parts) times r / s, and near the border of two codes
-// the second parts decide.
+// the second parts decide.  That wants h^2 and h w well inside float32's range: norm_wide takes the rows where they
+// are not.
 struct NormArgs {
     const void* x;
     const void* residual;  // nullable
@@ -464,67 +472,241 @@ struct Two {
     float hi, lo;
 };
 
-// What a row shares, from its sum of squares and largest |u| (of the row times f).
+// Rows outside these bounds (of sum h^2, max |h w| and the scale) are norm_wide's: inside, r is between 2^-50 and 2^20
+// and the largest |h w| between 2^-77 and 2^100, so that the second parts of all that decides a code are normal numbers.
+constexpr float kMostSquares = 1e30f, kMostProduct = 1.2676506e30f /* 2^100 */, kLeastScale = 5.421011e-20f /* 2^-64 */;
+
+// What a row shares, from its sum of squares and largest |u|.
 struct NormRow {
-    float r, s;  // 1 / sqrt(mean + eps) / f, and the scale
-    float c;     // a power of two that keeps r / s in range
-    Two g;       // r / (s c); 0 where every code is 0
+    float r, s;  // 1 / sqrt(mean + eps), and the scale
+    Two g;       // r / s
 };
-__device__ __forceinline__ NormRow norm_row(Two ss, MaxPair m, int cols, float eps, float f) {
+__device__ __forceinline__ NormRow norm_row(Two ss, MaxPair m, int cols, float eps) {
     NormRow o;
     const float n = static_cast<float>(cols), q0 = __fdiv_rn(ss.hi, n);
     const float q1 = (fmaf(-q0, n, ss.hi) + ss.lo) / n;
     float err;
-    const float hi = two_sum(q0, eps * f * f, err), lo = err + q1;
+    const float hi = two_sum(q0, eps, err), lo = err + q1;
     const float r0 = rsqrtf(hi), p = __fmul_rn(r0, r0);
     float e = fmaf(-hi, p, 1.f);
     e = fmaf(-hi, fmaf(r0, r0, -p), e);
     e = fmaf(-lo, p, e);
-    const Two r = {r0, hi <= kFltMax ? r0 * fmaf(0.375f * e, e, 0.5f * e) : 0.f};
+    const Two r = {r0, r0 * fmaf(0.375f * e, e, 0.5f * e)};
     o.r = r.hi + r.lo;
     // s = max|u| r / 127
     const float t = __fmul_rn(m.hi, r.hi);
     const float tl = fmaf(m.hi, r.hi, -t) + fmaf(m.hi, r.lo, m.lo * r.hi);
     const float s0 = __fdiv_rn(t, 127.f);
     o.s = s0 + (fmaf(-127.f, s0, t) + tl) / 127.f;
-    if (!(m.hi <= kFltMax) || !(o.s <= kFltMax)) o.s = __uint_as_float(0x7fc00000u);
-    o.c = o.s < 1e-20f ? 18446744073709551616.f : 1.f;  // 2^64
-    o.g = Two{0.f, 0.f};
-    if (o.s > 0.f) {
-        const float sc = o.s * o.c;
-        o.g.hi = __fdiv_rn(r.hi, sc);
-        o.g.lo = (fmaf(-o.g.hi, sc, r.hi) + r.lo) / sc;
-    }
+    o.g.hi = __fdiv_rn(r.hi, o.s);
+    o.g.lo = (fmaf(-o.g.hi, o.s, r.hi) + r.lo) / o.s;
     return o;
 }
-// Codes of eight elements h f w, the first four in x: those next to the border of two, or of a row with a tiny
-// scale.  (Out of line: in line its registers cost the common path occupancy, 144 us against 123 for 16384 x 4096.)
-template <typename T> __device__ __noinline__ uint2 norm_codes(Raw<T> hr, Raw<T> wr, float f, NormRow o) {
-    constexpr bool EXACT = sizeof(T) == 2;
+// The code of u + ul (ul: what u's rounding left off) where the quotient is (u + ul) g.
+__device__ __forceinline__ uint32_t norm_code(float u, float ul, Two g) {
+    const float v = __fmul_rn(u, g.hi);
+    // (a tiny scale is rounded coarsely: quotients may pass 127)
+    int k = static_cast<int>(fminf(fmaxf(rintf(v), -127.f), 127.f));
+    if (fabsf(v - static_cast<float>(k)) > 0.4999f) {
+        const float rest = fmaf(u, g.hi, -v) + u * g.lo + ul * g.hi;
+        const int side = v > static_cast<float>(k) ? 1 : -1;
+        const float past = side * ((v - (static_cast<float>(k) + 0.5f * side)) + rest);
+        if (past > 0.f || (past == 0.f && (k & 1) != 0)) k += side;
+    }
+    return static_cast<uint32_t>(min(max(k, -127), 127));
+}
+__device__ __forceinline__ uint2 pack_codes(const uint32_t (&c)[8]) {
+    return make_uint2(i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7]));
+}
+// Codes of eight elements h w, the first four in x: those next to the border of two.  (Out of line: in line its
+// registers cost the common path occupancy, 144 us against 123 for 16384 x 4096.)
+template <typename T> __device__ __noinline__ uint2 norm_codes(Raw<T> hr, Raw<T> wr, Two g) {
     float h[8], w[8];
     to8(hr, h);
     to8(wr, w);
     uint32_t c[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float gh = h[e] * f, u = __fmul_rn(gh, w[e]), uc = u * o.c, v = __fmul_rn(uc, o.g.hi);
-        // (a tiny scale is rounded coarsely: quotients may pass 127)
-        int k = static_cast<int>(fminf(fmaxf(rintf(v), -127.f), 127.f));
-        if (fabsf(v - static_cast<float>(k)) > 0.4999f) {
-            float rest = fmaf(uc, o.g.hi, -v) + uc * o.g.lo;
-            if (!EXACT) rest += fmaf(gh, w[e], -u) * o.c * o.g.hi;  // (16-bit numbers' products are exact)
-            const int side = v > static_cast<float>(k) ? 1 : -1;
-            const float past = side * ((v - (static_cast<float>(k) + 0.5f * side)) + rest);
-            if (past > 0.f || (past == 0.f && (k & 1) != 0)) k += side;
-        }
-        c[e] = static_cast<uint32_t>(min(max(k, -127), 127));
+        const float u = __fmul_rn(h[e], w[e]);
+        c[e] = norm_code(u, sizeof(T) == 2 ? 0.f : fmaf(h[e], w[e], -u), g);  // (16-bit numbers' products are exact)
     }
-    return make_uint2(i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7]));
+    return pack_codes(c);
+}
+
+// A row's threads' sums and maxima together.  red: shared memory of the CTA; again: it may still be read from before.
+template <bool EXACT> __device__ __forceinline__ void norm_reduce(Two& ss, MaxPair& m, int G, float (*red)[4], bool again) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        float err;
+        const float oh = __shfl_xor_sync(0xffffffffu, ss.hi, d), ol = __shfl_xor_sync(0xffffffffu, ss.lo, d);
+        ss.hi = two_sum(ss.hi, oh, err);
+        ss.lo += ol + err;
+        if constexpr (EXACT)
+            m.hi = max_nan(m.hi, __shfl_xor_sync(0xffffffffu, m.hi, d));
+        else
+            m = max_pair(m, MaxPair{__shfl_xor_sync(0xffffffffu, m.hi, d), __shfl_xor_sync(0xffffffffu, m.lo, d)});
+    }
+    if (G > 32) {
+        if (again) __syncthreads();  // (the CTA is one row: all or none come here)
+        if ((threadIdx.x & 31) == 0)
+            *reinterpret_cast<float4*>(red[threadIdx.x >> 5]) = make_float4(ss.hi, ss.lo, m.hi, m.lo);
+        __syncthreads();
+        ss = Two{0.f, 0.f};
+        m = MaxPair{0.f, 0.f};
+#pragma unroll 1
+        for (int k = 0; k < G / 32; ++k) {
+            const float4 o = *reinterpret_cast<const float4*>(red[k]);
+            float err;
+            ss.hi = two_sum(ss.hi, o.x, err);
+            ss.lo += o.y + err;
+            m = max_pair(m, MaxPair{o.z, o.w});
+        }
+    }
+}
+
+// A number as a fraction of at least 1/2 and below 1 either way, and a power of two (0 and what is not finite: themselves).
+struct Frac {
+    float m;
+    int e;
+};
+__device__ __forceinline__ Frac frac(float x) {
+    const uint32_t top = __float_as_uint(x) >> 23 & 255;
+    const float big = top == 0 ? x * 16777216.f : x;  // (subnormal: times 2^24)
+    const uint32_t b = __float_as_uint(big);
+    Frac f;
+    f.e = x == 0.f || top == 255 ? 0 : static_cast<int>(b >> 23 & 255) - (top == 0 ? 150 : 126);
+    f.m = x == 0.f || top == 255 ? x : __uint_as_float((b & 0x807fffffu) | 0x3f000000u);
+    return f;
+}
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+constexpr int kNoProduct = -(1 << 20);
+
+// The rest of a row whose squares or products leave float32's range (elements from about 2^50 on, weights or products
+// at its ends) or that holds an infinity or NaN: fractions and exponents apart, products relative
+// to the largest one's exponent E, squares to the largest element's.  (16384 x 4096
+// bfloat16, y and codes: 547 us where every row comes here, 89 where none does.)
+template <typename T, bool VEC>
+__device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, long long r, int tid, float (*red)[4]) {
+    using Part = RowPart<T, VEC>;
+    const int G = a.pl.G, vecs = a.pl.vecs, cols = a.cols;
+    const T* src = a.h ? static_cast<const T*>(a.h) + r * a.ldh : static_cast<const T*>(a.x) + r * a.ldx;
+    const T* wr = static_cast<const T*>(a.w);
+    auto row = [&](int i, float (&h)[8], float (&w)[8]) {
+        to8(a.pl.keep ? kept[i] : Part::load(src, cols, i, tid, G), h);
+        to8(Part::load(wr, cols, i, tid, G), w);
+    };
+    // the largest |h| and |w| (their bits: a NaN's are the largest), and the products' largest exponent
+    uint32_t hb = 0, wb = 0;
+    int E = kNoProduct;
+#pragma unroll 1
+    for (int i = tid; i < vecs; i += G) {
+        float h[8], w[8];
+        row(i, h, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            hb = max(hb, __float_as_uint(h[e]) & 0x7fffffffu);
+            wb = max(wb, __float_as_uint(w[e]) & 0x7fffffffu);
+            if (h[e] != 0.f && w[e] != 0.f) E = max(E, frac(h[e]).e + frac(w[e]).e);
+        }
+    }
+    hb = __reduce_max_sync(0xffffffffu, hb);
+    wb = __reduce_max_sync(0xffffffffu, wb);
+    E = __reduce_max_sync(0xffffffffu, E);
+    if (G > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+            *reinterpret_cast<int4*>(red[threadIdx.x >> 5]) = make_int4(static_cast<int>(hb), static_cast<int>(wb), E, 0);
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < G / 32; ++k) {
+            const int4 o = *reinterpret_cast<const int4*>(red[k]);
+            hb = max(hb, static_cast<uint32_t>(o.x));
+            wb = max(wb, static_cast<uint32_t>(o.y));
+            E = max(E, o.z);
+        }
+    }
+    constexpr uint32_t kInf = 0x7f800000u;
+    const bool bad = hb >= kInf || wb >= kInf;
+    // squares of h 2^-eh.  (Not of less than 2^-60: eps is at least 2^-40, and has to stay in range times 2^-2eh.)
+    const int eh = max(hb < kInf ? frac(__uint_as_float(hb)).e : 0, -60);
+    Two ss = {0.f, 0.f};
+    MaxPair m = {0.f, 0.f};
+    if (hb < kInf && E != kNoProduct) {  // (else the row's values are 0, or those of an infinity or NaN)
+#pragma unroll 1
+        for (int i = tid; i < vecs; i += G) {
+            float h[8], w[8];
+            row(i, h, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const Frac fh = frac(h[e]), fw = frac(w[e]);
+                const float g = fh.m * pow2(max(fh.e - eh, -126)), sq = __fmul_rn(g, g), p = __fmul_rn(fh.m, fw.m);
+                float err;
+                ss.hi = two_sum(ss.hi, sq, err);
+                ss.lo += err + fmaf(g, g, -sq);
+                const int d = fh.e + fw.e - E;
+                if (p != 0.f && d > -30) {
+                    const float l = fmaf(fh.m, fw.m, -p), x = pow2(d);
+                    m = max_pair(m, MaxPair{fabsf(p) * x, (p < 0.f ? -l : l) * x});
+                }
+            }
+        }
+        norm_reduce<false>(ss, m, G, red, true);
+    }
+    const int k0 = E - eh;
+    const float half = pow2(max(-eh, -126));  // (times 2^-120 and less eps counts for nothing)
+    const NormRow o = norm_row(ss, m, cols, a.eps * half * half);
+    // 1 / sqrt, times 2^eh; of a row with an infinity 0, with a NaN NaN
+    const float rf = hb > kInf ? __uint_as_float(hb) : hb == kInf ? 0.f : o.r;
+    float s = __uint_as_float(0x7fc00000u);
+    Two g = {0.f, 0.f};
+    if (E == kNoProduct && !bad) {
+        s = 0.f;
+    } else if (!bad) {
+        const int es = frac(o.s).e + k0;
+        if (es >= -125 && es <= 128) {
+            s = ldexpf(o.s, k0);
+            g = o.g;
+        } else {
+            // a scale with fewer bits, or 0, or too large for float32 (NaN): rounded once, from float64
+            const double mean = (static_cast<double>(ss.hi) + ss.lo) / cols + ldexp(static_cast<double>(a.eps), -2 * eh);
+            const double rE = ldexp(1.0 / sqrt(mean), k0), sd = (static_cast<double>(m.hi) + m.lo) * rE / 127.0;
+            if (static_cast<float>(sd) <= kFltMax) s = static_cast<float>(sd);
+            if (s > 0.f) {
+                const double q = rE / s;
+                g.hi = static_cast<float>(q);
+                g.lo = static_cast<float>(q - g.hi);
+            }
+        }
+    }
+    if (a.q.codes && tid == 0) a.q.scales[r] = s;
+#pragma unroll 1
+    for (int i = tid; i < vecs; i += G) {
+        float h[8], w[8], y[8];
+        row(i, h, w);
+        uint32_t c[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const Frac fh = frac(h[e]), fw = frac(w[e]);
+            const float p = __fmul_rn(fh.m, fw.m);
+            const int d = fh.e + fw.e - E;
+            c[e] = 0;
+            if (g.hi > 0.f && p != 0.f && d > -30) {
+                const float x = pow2(d);
+                c[e] = norm_code(p * x, fmaf(fh.m, fw.m, -p) * x, g);
+            }
+            // (p rf is between 2^-62 and 2^10, or 0 or not finite: the first factor's product is exact, or is an infinity
+            // that the second would have made)
+            const int k = fh.e + fw.e - eh, k1 = min(max(k, -62), 127);
+            y[e] = p * rf * pow2(k1) * pow2(min(max(k - k1, -126), 127));
+        }
+        if (a.q.codes) Part::store_words(a.q.codes + r * a.q.pitch, (int)a.q.pitch, i, tid, G, pack_codes(c));
+        if (a.y) Part::store(static_cast<T*>(a.y) + r * a.ldy, cols, i, tid, G, from8<T>(y));
+    }
 }
 
 template <typename T, int U, bool VEC>
 __global__ void __launch_bounds__(kRowThreads)
-i8_rmsnorm_kernel(const NormArgs a) {
+i8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) uint8_t row_smem[];
     __shared__ __align__(16) float red[kRowThreads / 32][4];
     pdl_wait();
@@ -544,36 +726,6 @@ i8_rmsnorm_kernel(const NormArgs a) {
         if (a.pl.keep) return kept[i];
         if (hr) return Part::load(hr, cols, i, tid, G);
         return Part::load(xr, cols, i, tid, G);  // (without residual_out there is no residual)
-    };
-    // the row's threads' sums and maxima together
-    auto reduce = [&](Two& ss, MaxPair& m, bool second) {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            float err;
-            const float oh = __shfl_xor_sync(0xffffffffu, ss.hi, d), ol = __shfl_xor_sync(0xffffffffu, ss.lo, d);
-            ss.hi = two_sum(ss.hi, oh, err);
-            ss.lo += ol + err;
-            if constexpr (EXACT)
-                m.hi = max_nan(m.hi, __shfl_xor_sync(0xffffffffu, m.hi, d));
-            else
-                m = max_pair(m, MaxPair{__shfl_xor_sync(0xffffffffu, m.hi, d), __shfl_xor_sync(0xffffffffu, m.lo, d)});
-        }
-        if (G > 32) {
-            if (second) __syncthreads();  // (the CTA is one row: all or none come here)
-            if ((threadIdx.x & 31) == 0)
-                *reinterpret_cast<float4*>(red[threadIdx.x >> 5]) = make_float4(ss.hi, ss.lo, m.hi, m.lo);
-            __syncthreads();
-            ss = Two{0.f, 0.f};
-            m = MaxPair{0.f, 0.f};
-#pragma unroll 1
-            for (int k = 0; k < G / 32; ++k) {
-                const float4 o = *reinterpret_cast<const float4*>(red[k]);
-                float err;
-                ss.hi = two_sum(ss.hi, o.x, err);
-                ss.lo += o.y + err;
-                m = max_pair(m, MaxPair{o.z, o.w});
-            }
-        }
     };
     for (int i0 = tid; i0 < vecs; i0 += U * G) {
         Raw<T> v[U], t[U];
@@ -620,7 +772,6 @@ i8_rmsnorm_kernel(const NormArgs a) {
             sl = add2(sl, err);
         }
     }
-    float f = 1.f;  // the row is taken times f
     Two ss;
     {
         const float2 hi = unpack(sh), lo = unpack(sl);
@@ -628,33 +779,22 @@ i8_rmsnorm_kernel(const NormArgs a) {
         ss.hi = two_sum(hi.x, hi.y, err);
         ss.lo = lo.x + lo.y + err;
     }
-    reduce(ss, m, false);
-    if (!(ss.hi <= 1e30f)) {
-        // squares that overflow float32 (elements from about 2^50 on) are taken of a smaller row
-        f = 7.888609052210118e-31f;  // 2^-100
-        ss = Two{0.f, 0.f};
-        m = MaxPair{0.f, 0.f};
+    norm_reduce<EXACT>(ss, m, G, red, false);
+    NormRow o = norm_row(ss, m, cols, a.eps);
+    if (!(ss.hi <= kMostSquares && m.hi <= kMostProduct && o.s >= kLeastScale)) {
+        // a row of zeros (a silent token) has nothing to take care of but 0 / 0
+        uint32_t any = !(ss.hi == 0.f && m.hi == 0.f);
+        if (!any)
 #pragma unroll 1
-        for (int i = tid; i < vecs; i += G) {
-            float h[8], w[8];
-            to8(again(i), h);
-            to8(Part::load(wr, cols, i, tid, G), w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float g = h[e] * f, sq = __fmul_rn(g, g), u = __fmul_rn(g, w[e]), l = fmaf(g, w[e], -u);
-                float err;
-                ss.hi = two_sum(ss.hi, sq, err);
-                ss.lo += err + fmaf(g, g, -sq);
-                m = max_pair(m, MaxPair{fabsf(u), EXACT ? 0.f : u < 0.f ? -l : l});
-            }
+            for (int i = tid; i < vecs; i += G) any |= any_bits(again(i));
+        if (G > 32 ? __syncthreads_or(any) : __any_sync(0xffffffffu, any)) {
+            norm_wide<T, VEC>(a, kept, r, tid, red);
+            return;
         }
-        reduce(ss, m, true);
+        o.s = o.g.hi = 0.f;
     }
-    const NormRow o = norm_row(ss, m, cols, a.eps, f);
     if (a.q.codes && tid == 0) a.q.scales[r] = o.s;
-    // both factors are 1 but for rows of enormous or of tiny elements
-    const F2 f22 = f2(f, f), g2 = f2(o.g.hi, o.g.hi), c2 = f2(o.c, o.c);
-    const bool plain = o.c == 1.f;
+    const F2 g2 = f2(o.g.hi, o.g.hi);
 #pragma unroll 1
     for (int i = tid; i < vecs; i += G) {
         const Raw<T> hraw = again(i), wraw = Part::load(wr, cols, i, tid, G);
@@ -663,21 +803,18 @@ i8_rmsnorm_kernel(const NormArgs a) {
         to8(wraw, w);
         F2 u[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = mul2(mul2(f2(h[2 * e], h[2 * e + 1]), f22), f2(w[2 * e], w[2 * e + 1]));
+        for (int e = 0; e < 4; ++e) u[e] = mul2(f2(h[2 * e], h[2 * e + 1]), f2(w[2 * e], w[2 * e + 1]));
         if (a.q.codes) {
             uint32_t code[8];
             float far = 0.f;
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-                const F2 q = mul2(mul2(u[e / 2], c2), g2);
+                const F2 q = mul2(u[e / 2], g2);
                 const float2 t = unpack(sub2(q, nearest2(q, code[e], code[e + 1])));
                 far = fmaxf(far, fmaxf(fabsf(t.x), fabsf(t.y)));
             }
-            uint2 words = make_uint2(i8_pack4(code[0], code[1], code[2], code[3]), i8_pack4(code[4], code[5], code[6], code[7]));
-            if (!(o.g.hi > 0.f))
-                words = make_uint2(0, 0);
-            else if (far > 0.4999f || !plain)
-                words = norm_codes<T>(hraw, wraw, f, o);
+            uint2 words = pack_codes(code);
+            if (far > 0.4999f) words = norm_codes<T>(hraw, wraw, o.g);
             Part::store_words(a.q.codes + r * a.q.pitch, (int)a.q.pitch, i, tid, G, words);
         }
         if (a.y) {
