@@ -114,10 +114,13 @@ __device__ __forceinline__ uint2 i8_to_f16x4(uint32_t w) {
     return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// A product's value from its whole-number sum: the scales are applied one after the other, the larger
-// number first in, so that a small scale times a small scale does not underflow on the way.
+// A product's value from its whole-number sum: times the scales, one after the other.  The sum is below 2^31, so times
+// a scale of up to 2^96 it is a float32 number; of a larger one the other comes first, which then is small or makes an
+// infinity that the output is too.  (Downwards nothing is lost: a sum is 0 or at least 1.)
+__device__ __forceinline__ bool i8_large(float sx) { return sx > 7.9228163e28f; }
 __device__ __forceinline__ float i8_scaled(int sum, float sx, float sw) {
-    return __int2float_rn(sum) * sx * sw;
+    const bool swap = i8_large(sx);
+    return __int2float_rn(sum) * (swap ? sw : sx) * (swap ? sx : sw);
 }
 
 // Eight consecutive elements of a row of B (R elements), zeros past R.

@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "fp4_device.cuh"
@@ -51,7 +52,7 @@ constexpr int kJUnits = kJMaxN / 32;  // 16-token units of a drain warp, at most
 // a LoRA block: 8 columns of B for 128 features, then of s in two parts for N / 2 <= 128 tokens
 constexpr int kJBufs = 4;  // blocks ahead of the MMAs: a tile of two adapters of rank 16 takes four
 constexpr int kJLoraB = kJM * 32, kJLoraBytes = kJLoraB + 2 * (kJMaxN / 2) * 32;
-constexpr size_t kJTail = kJMaxN * 12 + 64 * 4 + 256 * 4 + 16 + 512 + 1024;
+constexpr size_t kJTail = kJMaxN * 16 + 64 * 4 + 256 * 4 + 16 + 512 + 1024;
 constexpr size_t kJSmemMax = 227 * 1024;
 
 struct I8PairArgs {
@@ -106,7 +107,8 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     int* row_sm = reinterpret_cast<int*>(lora_sm + (FUSE ? kJBufs * kJLoraBytes : 0));  // [N] row of y of a token of the tile
     int* slot_sm = row_sm + kJMaxN;                              // [N] its adapter
     float* sx_sm = reinterpret_cast<float*>(slot_sm + kJMaxN);   // [N] its scale
-    uint32_t* seen = reinterpret_cast<uint32_t*>(sx_sm + kJMaxN);  // [64] slots the tile's tokens name
+    float* up_sm = sx_sm + kJMaxN;                               // [N] and what its product is multiplied by
+    uint32_t* seen = reinterpret_cast<uint32_t*>(up_sm + kJMaxN);  // [64] slots the tile's tokens name
     int* dlist = reinterpret_cast<int*>(seen + 64);              // [256] in order
     int* distinct = dlist + 256;                                 // [2] their number
     uint64_t* full = reinterpret_cast<uint64_t*>(distinct + 4);  // even CTA: both CTAs' halves landed
@@ -422,13 +424,22 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             named_bar_sync(2, 256);  // the tile before is through with the tokens' rows
             if (lt < N) {
                 row_sm[lt] = next.row;
-                sx_sm[lt] = next.sx;
+                // (a scale that its sum could carry past float32's range is taken down by a power of two, and the product
+                // with sw up again: see i8_scaled.  With the LoRA term that is one instruction, as the addition by itself)
+                const bool large = i8_large(next.sx);
+                sx_sm[lt] = large ? next.sx * 0x1p-64f : next.sx;
+                up_sm[lt] = large ? 0x1p64f : 1.f;
                 if constexpr (FUSE) slot_sm[lt] = next.slot;
             }
             const float sw = o < a.h_out ? __ldg(a.sw + o) : 0.f;
             const bool lora = FUSE && !named_bar_and(2, 256, next.slot < 0);
             if constexpr (!FUSE) named_bar_sync(2, 256);
             if (tile + npairs < total) look_up(tile + npairs);
+            bool large_sx = false;
+            if constexpr (!FUSE) {
+                for (int t = lane; t < N; t += 32) large_sx = large_sx || up_sm[t] != 1.f;
+                large_sx = __any_sync(0xffffffffu, large_sx);
+            }
             int sum[kJUnits][16];
 #pragma unroll
             for (int i = 0; i < kJUnits; ++i)
@@ -471,29 +482,35 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             }
             // values first, which leaves the LoRA accumulator to the next tile's MMAs, then the stores
             const uint32_t laddr = tmem + lbuf * N + (static_cast<uint32_t>(q * 32) << 16);
+            auto values = [&](auto large) {
 #pragma unroll
-            for (int i = 0; i < kJUnits; ++i) {
-                const int u = 2 * i + hv;
-                if (u < units) {
-                    uint32_t r[16];
-                    if (lora) {
-                        __syncwarp();
-                        tmem_ld16(laddr + u * 16, r);
-                        tmem_ld_wait();
-                    }
+                for (int i = 0; i < kJUnits; ++i) {
+                    const int u = 2 * i + hv;
+                    if (u < units) {
+                        uint32_t r[16];
+                        if (lora) {
+                            __syncwarp();
+                            tmem_ld16(laddr + u * 16, r);
+                            tmem_ld_wait();
+                        }
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 sx = *reinterpret_cast<const float4*>(sx_sm + u * 16 + e);
-                        const float s4[4] = {sx.x, sx.y, sx.z, sx.w};
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 sx = *reinterpret_cast<const float4*>(sx_sm + u * 16 + e);
+                            const float4 up = large ? *reinterpret_cast<const float4*>(up_sm + u * 16 + e) : make_float4(1.f, 1.f, 1.f, 1.f);
+                            const float s4[4] = {sx.x, sx.y, sx.z, sx.w}, u4[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            float v = i8_scaled(sum[i][e + k], s4[k], sw);
-                            if (lora) v += __uint_as_float(r[e + k]);
-                            sum[i][e + k] = __float_as_int(v);
+                            for (int k = 0; k < 4; ++k) {
+                                const float v = __int2float_rn(sum[i][e + k]) * s4[k] * sw;
+                                sum[i][e + k] = __float_as_int(lora ? fmaf(v, u4[k], __uint_as_float(r[e + k])) : large ? v * u4[k] : v);
+                            }
                         }
                     }
                 }
-            }
+            };
+            if (FUSE || large_sx)
+                values(std::true_type{});
+            else
+                values(std::false_type{});
             if constexpr (FUSE) {
                 tc_fence_before();
                 __syncwarp();

@@ -1,5 +1,5 @@
 """The 8-bit operators at the ends of float32's range: a norm whose h * weight leaves it while the norm itself does
-not."""
+not, and a product whose sum times one scale does while the output does not."""
 import numpy as np
 import pytest
 import torch
@@ -91,3 +91,57 @@ def test_norm_of_rows_that_are_not_finite_among_large_weights(lib, dtype):
     lib.lora_i8_rmsnorm(x.cuda(), w.cuda(), 1e-6, out=m, y=y)
     assert m.scales.isnan().all() and (m.codes == 0).all()
     assert y[0, 7].isinf() and y[3, 7].isinf() and y[0, :7].isfinite().all() and y[3, 8:].isfinite().all()
+
+
+# ---- products ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 4, 8, 40, 200, 700])
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("xexp,wexp", [(115, -130), (-130, 115), (100, -90), (120, -100)])
+def test_products_of_a_large_and_a_small_scale(lib, n, odd, xexp, wexp):
+    """The sum times x's scale is above float32's range, the output is not."""
+    m, k = (257, 2100) if odd else (256, 2048)
+    rng = np.random.default_rng([n, k])
+    x, w = lib.I8Matrix(n, k), lib.I8Matrix(m, k)
+    cx, cw = rng.integers(1, 128, (n, k)), rng.integers(1, 128, (m, k))  # sums of about 2^23
+    sx = (2.0 ** xexp * (1 + rng.random(n))).astype(np.float32)
+    sw = (2.0 ** wexp * (1 + rng.random(m))).astype(np.float32)
+    sx[::2] = rng.random(len(sx[::2])).astype(np.float32)  # ordinary rows beside them
+    for q, c, s in ((x, cx, sx), (w, cw, sw)):
+        q.codes.zero_()
+        q.codes[:, :k].copy_(torch.from_numpy(c.astype(np.int8)))
+        q.scales.copy_(torch.from_numpy(s))
+    y = torch.empty(n, m, device="cuda")
+    lib.lora_i8_matmul(x, w, y)
+    ref = Q.sums(cx, cw).astype(np.float64) * sx.astype(np.float64)[:, None] * sw.astype(np.float64)
+    with np.errstate(over="ignore"):
+        ref = np.where(np.abs(ref) > np.finfo(np.float32).max, np.inf, ref)
+    got = y.cpu().double().numpy()
+    # the sum, its product with one scale and with the other: three roundings
+    assert np.array_equal(np.isinf(got), np.isinf(ref))
+    ok = np.isfinite(ref)
+    assert (np.abs(got[ok] - ref[ok]) <= 3 * F * np.abs(ref[ok]) + 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("n,slots", [(3, 2), (40, 2), (200, 60), (700, 2), (700, 100)])
+def test_linears_of_large_rows_and_small_weights(lib, dtype, n, slots):
+    """x of 2^115 over weights of 2^-100: sums times x's scale pass 2^128."""
+    h_in, h_out = 1024, 136
+    x = torch.from_numpy(np.abs(spread(n, h_in, 7)) * 2.0 ** 115).to(dtype)
+    W = torch.from_numpy((np.abs(spread(h_out, h_in, 8)) + 0.5) * 2.0 ** -100).to(dtype)
+    x[0] = x[0] * 2.0 ** -115
+    pool = lib.LoraPool(h_in, h_out, 8, slots, dtype, "cuda")
+    # adapters of zeros: the LoRA term's paths, and a term that is 0
+    zeros = [torch.zeros(8, h_in, dtype=dtype, device="cuda"), torch.zeros(h_out, 8, dtype=dtype, device="cuda")]
+    pool.load_slots(range(slots), [zeros[0]] * slots, [zeros[1]] * slots, [8.0] * slots)
+    idx = torch.randint(-1, slots, (n,), generator=torch.Generator().manual_seed(n), dtype=torch.int32)
+    w = lib.lora_i8_quantize(W.cuda(), lib.I8Matrix(h_out, h_in))
+    seg = pool.segment(idx.cuda())
+    y = pool.i8_linear(w, x.cuda(), seg)
+    assert lib.lora_segment_status(seg) == lib.LORA_OK
+    (cx, sx), (cw, sw) = Q.quantise(x), Q.quantise(W)
+    ref = Q.sums(cx, cw).astype(np.float64) * sx.astype(np.float64)[:, None] * sw.astype(np.float64)
+    err = np.abs(y.cpu().double().numpy() - ref)
+    assert (err <= (4 * F + UNIT[dtype]) * np.abs(ref)).all()
+    pool.close()
