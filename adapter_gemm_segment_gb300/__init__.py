@@ -727,7 +727,8 @@ def lora_i8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Opti
                     residual_out: Optional[torch.Tensor] = None, stream=None) -> None:
     """h = x + residual into residual_out (the residual itself where it is not given); the root-mean-square
     norm of h times weight into y and, as 8-bit integers, into out (either may be left out).  x, residual,
-    residual_out, y: [rows, cols] of one dtype, contiguous rows, any row stride; weight [cols]."""
+    residual_out, y: [rows, cols] of one dtype, contiguous rows, any row stride; weight [cols].  residual_out and y may
+    each be x or residual itself, and overlap nothing else."""
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
     if residual is not None and residual_out is None:

@@ -46,6 +46,29 @@ static int check_rows(const void* p, int dtype, int64_t ld, int rows, int cols, 
     return LORA_OK;
 }
 
+// Whether an output [rows, cols] meets another array of the same element size, in elements other than (may: or in) the
+// ones of the same index.  Distances in elements; lda, ldb >= cols.
+static bool meets(const void* out, int64_t lda, const void* other, int64_t ldb, int rows, int cols, size_t elt, bool may) {
+    if (!out || !other) return false;
+    // (both are aligned to their element: the distance is a whole number of them)
+    const int64_t d = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(other)) / (int64_t)elt, last = rows - 1;
+    if (d > last * ldb + cols - 1 || -d > last * lda + cols - 1) return false;
+    if (lda == ldb || rows == 1) {  // every row the same: out's row r is k rows and c columns behind other's
+        if (d == 0) return !may;
+        const int64_t k = d >= 0 ? d / ldb : -((-d + ldb - 1) / ldb), c = d - k * ldb;
+        const int64_t behind = k >= 0 ? k : -k, next = k + 1 >= 0 ? k + 1 : -(k + 1);
+        return (c < cols && behind <= last) || (c > ldb - cols && next <= last);
+    }
+    for (int64_t r = 0; r <= last; ++r) {
+        const int64_t at = d + r * lda;  // of out's row r, from other's first element
+        const int64_t k = at >= 0 ? at / ldb : -1, c = at - k * ldb;
+        if (k >= 0 && k <= last && c < cols && !(may && k == r && c == 0)) return true;
+        if (c > ldb - cols && k + 1 >= 0 && k + 1 <= last) return true;
+        if (k > last) break;
+    }
+    return false;
+}
+
 static I8View view_of(const lora_i8_matrix* m) { return i8_view(m->codes_dev, m->scales_dev, m->rows, m->cols); }
 
 // Up to this many tokens the dot products of i8_small.cu.  (4096 x 4096 float16, us, these / the tile kernel: 1 token
@@ -163,10 +186,26 @@ int lora_i8_rmsnorm(const lora_i8_norm* p, void* stream) {
     if (!rc && p->y_dev) rc = check_rows(p->y_dev, p->dtype, p->ldy, p->rows, p->cols, "y");
     if (!rc && p->out) rc = check_matrix(p->out, "out");
     if (rc) return rc;
+    if (p->rows > 0) {
+        // a row is written while others are still read
+        const size_t elt = dtype_size(p->dtype);
+        const struct {
+            const void *out, *other;
+            int64_t lda, ldb;
+            bool may;
+            const char *what, *over;
+        } pairs[] = {{p->residual_out_dev, p->x_dev, p->ldro, p->ldx, true, "residual_out", "x"},
+                     {p->residual_out_dev, p->residual_dev, p->ldro, p->ldr, true, "residual_out", "residual"},
+                     {p->y_dev, p->x_dev, p->ldy, p->ldx, true, "y", "x"},
+                     {p->y_dev, p->residual_dev, p->ldy, p->ldr, true, "y", "residual"},
+                     {p->y_dev, p->residual_out_dev, p->ldy, p->ldro, false, "y", "residual_out"}};
+        for (const auto& q : pairs)
+            if (meets(q.out, q.lda, q.other, q.ldb, p->rows, p->cols, elt, q.may))
+                return set_error(LORA_EINVAL, "%s overlaps %s%s", q.what, q.over, q.may ? " without being the same array" : "");
+    }
     if (p->out && (p->out->rows != p->rows || p->out->cols != p->cols))
         return set_error(LORA_EINVAL, "out is %d x %d, x %d x %d", p->out->rows, p->out->cols, p->rows, p->cols);
     if (p->rows == 0) return LORA_OK;
-    if (p->y_dev && p->y_dev == p->residual_out_dev) return set_error(LORA_EINVAL, "y and residual_out are the same array");
     return launch_i8_rmsnorm(*p, static_cast<cudaStream_t>(stream));
 }
 

@@ -463,9 +463,10 @@ int lora_i8_dequantize(const lora_i8_matrix* q, void* out_dev, int dtype, int64_
  * residual_out receives h, y receives v rounded once to dtype, out the stored form of v itself (not of y).
  * The row's statistics are held to about 2^-44, so out's codes are those of the real v, also where h * weight leaves
  * float32's range and v does not.  A row that holds an infinity or a NaN gets a NaN scale and codes 0.
- *   x, residual (nullable), residual_out (nullable without residual; may be residual or x), y (nullable;
- *   may be x, not residual_out): [rows, cols] of dtype with row strides ldx, ldr, ldro, ldy >= cols; weight [cols];
- *   out (nullable): a stored matrix [rows, cols].  y or out is wanted.  eps in [1e-12, 1]. */
+ *   x, residual (nullable), residual_out (nullable without residual), y (nullable): [rows, cols] of dtype with row
+ *   strides ldx, ldr, ldro, ldy >= cols; weight [cols]; out (nullable): a stored matrix [rows, cols].  y or out is
+ *   wanted.  residual_out and y may each be x or residual (the same elements in the same places, hence the same stride);
+ *   any other overlap with them or with each other is LORA_EINVAL.  eps in [1e-12, 1]. */
 typedef struct {
     const void* x_dev;
     const void* residual_dev;
