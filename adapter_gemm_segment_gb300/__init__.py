@@ -676,8 +676,16 @@ def lora_fp4_linear_fwd(pool_handle, w: Fp4Matrix, x: torch.Tensor, y: torch.Ten
 
 # ---- 8-bit integer base weights ---------------------------------------------------------------
 
+def _i8_sizes(*sizes) -> None:
+    """The library takes sizes in 32 bits, to which ctypes would cut a larger one without a word."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7fffffff:
+            raise LoraError(LORA_EUNSUP, f"8-bit matrices of {n} rows or columns")
+
+
 def lora_i8_bytes(rows: int, cols: int):
     """(codes bytes, scales bytes) of a stored 8-bit matrix [rows, cols]."""
+    _i8_sizes(rows, cols)
     c, s = ctypes.c_size_t(), ctypes.c_size_t()
     _check(_lib.lora_i8_bytes(rows, cols, ctypes.byref(c), ctypes.byref(s)))
     return c.value, s.value
@@ -735,6 +743,8 @@ def lora_i8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Opti
         residual_out = residual
     shape, dtype = x.shape, x.dtype
     rows, cols = shape
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        _i8_sizes(rows, cols)
     dt, ldx = _rows_of(x, rows, cols, "x")
 
     def like_x(t, name):  # address and row stride
@@ -757,6 +767,7 @@ def lora_i8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, out: Opti
 
 
 def lora_i8_matmul_workspace_bytes(x_rows: int, w_rows: int, cols: int) -> int:
+    _i8_sizes(x_rows, w_rows, cols)
     out = ctypes.c_size_t()
     _check(_lib.lora_i8_matmul_workspace_bytes(x_rows, w_rows, cols, ctypes.byref(out)))
     return out.value
@@ -777,6 +788,7 @@ def lora_i8_matmul(x: I8Matrix, w: I8Matrix, y: torch.Tensor, ws: Optional[torch
 
 
 def lora_i8_linear_workspace_bytes(pool_handle, n_tokens: int) -> int:
+    _i8_sizes(n_tokens)
     out = ctypes.c_size_t()
     _check(_lib.lora_i8_linear_workspace_bytes(pool_handle, n_tokens, ctypes.byref(out)))
     return out.value
