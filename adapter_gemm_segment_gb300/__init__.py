@@ -16,6 +16,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
+import weakref
 from typing import Optional
 
 import torch
@@ -848,10 +850,38 @@ def _capturing() -> bool:
     return torch.cuda.is_current_stream_capturing()
 
 
+class _SharedWorkspace:
+    """The workspace of every pool's 8-bit linears on one stream, as large as the largest call has needed.  Above 512
+    tokens a call's holds its whole weight in float16, more than 8 bits save of it: one for each pool would leave less
+    memory than 16-bit weights do.  Calls on a stream run one after the other; lock keeps the launches of one together
+    where several threads call."""
+
+    __slots__ = ("lock", "memory", "nbytes", "__weakref__")
+    _held = weakref.WeakValueDictionary()  # by (device, stream); the pools that have used one keep it
+    _held_lock = threading.Lock()
+
+    def __init__(self):
+        self.lock, self.memory, self.nbytes = threading.Lock(), None, 0
+
+    @classmethod
+    def of(cls, key) -> "_SharedWorkspace":
+        with cls._held_lock:
+            held = cls._held.get(key)
+            if held is None:
+                held = cls._held[key] = cls()
+            return held
+
+    def grow(self, nbytes: int, device) -> None:
+        """To nbytes, on the current stream; the lock is held."""
+        self.memory, self.nbytes = None, 0
+        self.memory = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.nbytes = nbytes
+
+
 class LoraPool:
     """One adapter pool (one linear layer) in a device buffer this object owns.  Where a call is given no
-    workspace the pool keeps one for each stream, so that calls on several streams do not share one; a call
-    under stream capture gets one of its graph's own."""
+    workspace the pool keeps one for each stream, so that calls on several streams do not share one (the 8-bit
+    linears of all pools share one there); a call under stream capture gets one of its graph's own."""
 
     def __init__(self, h_in: int, h_out: int, r_max: int, n_slots: int, dtype: torch.dtype, device="cuda",
                  stream=None):
@@ -894,8 +924,8 @@ class LoraPool:
         return lora_linear_fwd(self.handle, W, x, y, seg, ws, variant, stream)
 
     def _own_workspace(self, kind: str, n: int, device, stream) -> torch.Tensor:
-        """The workspace of this pool's calls of n tokens on one stream.  The 4-bit and 8-bit linears keep the
-        largest asked for, which serves every smaller batch; the 16-bit linear's may need more for fewer tokens, so
+        """The workspace of this pool's calls of n tokens on one stream.  The 4-bit linear keeps the largest
+        asked for, which serves every smaller batch; the 16-bit linear's may need more for fewer tokens, so
         it keeps one for each n."""
         if stream is not None:
             with _on_stream(stream):
@@ -904,12 +934,11 @@ class LoraPool:
 
     def _stream_workspace(self, kind: str, n: int, device, handle) -> torch.Tensor:
         """_own_workspace on the current stream, whose handle that is."""
-        key = (kind, device, handle, n) if kind == "linear" else (kind, device, handle)
+        key = (kind, device, handle) if kind == "fp4" else (kind, device, handle, n)
         captured = _capturing()
         held, ws = self._ws.get(key, (-1, None))
         if captured or held < n:
-            make = {"fp4": lora_fp4_linear_workspace_bytes, "i8": lora_i8_linear_workspace_bytes,
-                    "linear": lora_linear_workspace_bytes}[kind]
+            make = lora_fp4_linear_workspace_bytes if kind == "fp4" else lora_linear_workspace_bytes
             ws = torch.empty(max(make(self.handle, n), 256), dtype=torch.uint8, device=device)
             if not captured:
                 self._ws[key] = (n, ws)
@@ -934,13 +963,30 @@ class LoraPool:
 
     def i8_linear(self, w: I8Matrix, x: torch.Tensor, seg, xq: Optional[I8Matrix] = None,
                   y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """``linear`` over an 8-bit base weight."""
+        """``linear`` over an 8-bit base weight.  ws not given: one that every pool's calls on the stream share."""
+        if stream is None:
+            return self._i8_linear(w, x, seg, xq, y, ws, None)
+        with _on_stream(stream):
+            return self._i8_linear(w, x, seg, xq, y, ws, stream)
+
+    def _i8_linear(self, w, x, seg, xq, y, ws, stream) -> torch.Tensor:
+        """i8_linear, the current stream being the call's."""
         n = int(seg.n_tokens)
         if y is None:
-            with _on_stream(stream):
-                y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
+            y = torch.empty((n, self.h_out), dtype=self.dtype, device=x.device)
+        if ws is None and not _capturing():
+            handle = _stream(stream).value
+            key = ("i8", x.device, handle)
+            most, need, shared = self._ws.get(key, (-1, 0, None))
+            if most < n:
+                need, shared = max(lora_i8_linear_workspace_bytes(self.handle, n), 256), _SharedWorkspace.of(key)
+                self._ws[key] = (n, need, shared)
+            with shared.lock:
+                if shared.nbytes < need:
+                    shared.grow(need, x.device)
+                return lora_i8_linear_fwd(self.handle, w, x, y, seg, shared.memory, xq, stream)
         if ws is None:
-            ws = self._own_workspace("i8", n, x.device, stream)
+            ws = torch.empty(max(lora_i8_linear_workspace_bytes(self.handle, n), 256), dtype=torch.uint8, device=x.device)
         return lora_i8_linear_fwd(self.handle, w, x, y, seg, ws, xq, stream)
 
     def close(self) -> None:

@@ -89,6 +89,9 @@ def main():
         if ags.lora_segment_status(seg) != ags.LORA_OK:
             raise RuntimeError("the batch was refused")
         print(f"{label}, {n} tokens: {times[False]:.0f} us over bf16 bases, {times[True]:.0f} us over 8 bits")
+        # one serves every projection: the calls of a stream run one after the other
+        room = max(ags.lora_i8_linear_workspace_bytes(p.pool.handle, n) for p in layer.values())
+        print(f"  workspace of the 8-bit projections together: {room / 1e6:.1f} MB")
         for name in layer:
             a, b = out[False][name].float(), out[True][name].float()
             print(f"  {name:10s} relative difference {((a - b).norm() / a.norm()).item():.4f}")

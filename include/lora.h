@@ -502,7 +502,11 @@ int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev
  * 2^-23 of itself.)  An infinity or NaN in one adapter reaches that adapter's tokens only.  The same call gives
  * the same bits, with xq or without; the path is chosen from sizes alone.  2 to 5 kernels.
  * LORA_EUNSUP: batches of more than 512 tokens with x or w of 2^36 codes and more, or of 2^52 products.
- * A workspace of lora_i8_linear_workspace_bytes(pool, n) serves every batch of up to n tokens.  The y of a
+ * A workspace of lora_i8_linear_workspace_bytes(pool, n) serves every batch of up to n tokens, and successive calls on
+ * one stream, of whichever pools, may share the largest.  It holds x's codes (from 9 tokens on 2 bytes each) and the
+ * shrink output (r_max floats a token; for few tokens in up to 4 parts, for float32 24); above 512 tokens also w in
+ * float16 codes, 2 bytes each, and for batches that may name many adapters the float32 product, up to 128 MB.
+ * (4096 x 4096, r_max 16, 100 slots, 16-bit: 4.2 MB for 512 tokens, 46 MB for 513, 203 MB for 16384.)  The y of a
  * linear, this one included, is not to be w's codes or scales without a wait in between; nor is it, or what
  * lora_i8_rmsnorm wrote, to be the W of a 16-bit linear.  What lora_i8_quantize, lora_i8_dequantize or
  * lora_i8_matmul wrote may be used as it is. */
