@@ -460,7 +460,10 @@ int lora_i8_dequantize(const lora_i8_matrix* q, void* out_dev, int dtype, int64_
 /* Residual addition, root-mean-square norm and its output in 8 bits, one kernel on `stream`:
  *     h = x + residual (rounded to dtype; x where residual is NULL)
  *     v = h / sqrt(mean(h^2) + eps) * weight
- * residual_out receives h, y receives v rounded once to dtype, out the stored form of v itself (not of y).
+ * residual_out receives h, out the stored form of v itself (not of y), y receives v from float32 arithmetic, rounded
+ * to dtype: h * weight, 1 / sqrt and their product are each rounded to float32 before, so beside half a step of dtype
+ * y is within 3 * 2^-24 of v (of an element whose h * weight is below float32's normal range, within 2^-149 / sqrt(mean
+ * + eps)).
  * The row's statistics are held to about 2^-44, so out's codes are those of the real v, also where h * weight leaves
  * float32's range and v does not.  A row that holds an infinity or a NaN gets a NaN scale and codes 0.
  *   x, residual (nullable), residual_out (nullable without residual), y (nullable): [rows, cols] of dtype with row
@@ -486,7 +489,9 @@ int lora_i8_rmsnorm(const lora_i8_norm* args, void* stream);
  * w.rows elements, aligned to its element).  A NaN scale makes the outputs of its row NaN and no others.
  * ws_dev: >= lora_i8_matmul_workspace_bytes (which may be 0: ws_dev is then not used), 256-byte aligned;
  * successive calls on one stream may share it.  The same row of x gives the same bits in every batch.  LORA_EUNSUP
- * as for lora_i8_linear_fwd.  1 to 3 kernels. */
+ * as for lora_i8_linear_fwd.  1 to 3 kernels.  Every wait on the device is bounded; the call has no status word, so a
+ * wait that runs out (it does not unless the GPU is stopped for seconds) leaves parts of y unwritten without a report
+ * (the linear reports it in its segments' status). */
 int lora_i8_matmul_workspace_bytes(int x_rows, int w_rows, int cols, size_t* bytes);
 int lora_i8_matmul(const lora_i8_matrix* x, const lora_i8_matrix* w, void* y_dev, int dtype, int64_t ldy, void* ws_dev,
                    size_t ws_bytes, void* stream);
