@@ -8,8 +8,9 @@
 // them equal inputs would not give equal bytes on every path.
 //
 // Every kernel here moves its rows once and is bound by memory, below a few MB by the launch.  16384 x 4096
-// bfloat16, us (at the copy rate): quantise 42 (30), read back 32 (30), norm with residual, y and codes 118 (90).  The
-// quantiser's and the norm's instructions fill 64 and 70 % of the issue slots.
+// bfloat16, us (at the copy rate): quantise 42 (30), read back 32 (30), norm with residual, y and codes 112 (90).  The
+// quantiser's and the norm's instructions fill 66 and 68 % of the issue slots; the float32 quantiser's a third: its
+// vectors are 32 bytes, so that a warp's 16-byte accesses lie 32 apart (8191 x 11008: 101 us, 67 at the copy rate).
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -582,9 +583,9 @@ __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) <
 constexpr int kNoProduct = -(1 << 20);
 
 // The rest of a row whose squares or products leave float32's range (elements from about 2^50 on, weights or products
-// at its ends) or that holds an infinity or NaN: fractions and exponents apart, products relative
-// to the largest one's exponent E, squares to the largest element's.  (16384 x 4096
-// bfloat16, y and codes: 547 us where every row comes here, 89 where none does.)
+// at its ends) or that holds an infinity or NaN: fractions and exponents apart, products relative to the largest one's
+// exponent E, squares to the largest element's.  (16384 x 4096 bfloat16, y and codes: 547 us where every row comes here,
+// 89 where none does.)
 template <typename T, bool VEC>
 __device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, long long r, int tid, float (*red)[4]) {
     using Part = RowPart<T, VEC>;

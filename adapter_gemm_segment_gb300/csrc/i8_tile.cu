@@ -4,7 +4,8 @@
 // is exact in float32, so is a sum of 1024 of them (1024 * 128 * 128 = 2^24), or of more where the tokens' codes
 // are small: the kernel before this one leaves each token's largest sum of |code| over 256, which bounds the
 // partial sums.  Codes go through tcgen05.mma kind::f16; every chunk of so many the accumulator is read into
-// 32-bit integers and started again (usually once, at the end).
+// 32-bit integers and started again (normal data: 24 to 26 steps of 128 codes; with a few loud channels, as activations
+// have them, some hundred).
 //
 // The weight is the MMA's M side (128 features a tile) and up to 256 tokens its N side.  The weight stays
 // in bytes until it is on the SM: TMA brings 128 x 128 codes, sixteen warps turn them into float16 and store
