@@ -474,8 +474,8 @@ struct Two {
 };
 
 // Rows outside these bounds (of sum h^2, max |h w| and the scale) are norm_wide's: inside, r is between 2^-50 and 2^20
-// and the largest |h w| between 2^-77 and 2^100, so that the second parts of all that decides a code are normal numbers.
-constexpr float kMostSquares = 1e30f, kMostProduct = 1.2676506e30f /* 2^100 */, kLeastScale = 5.421011e-20f /* 2^-64 */;
+// and the largest |h w| between 2^-77 and 2^76, so that the second parts of all that decides a code are normal numbers.
+constexpr float kMostSquares = 1e30f, kMostProduct = 0x1p76f, kLeastScale = 0x1p-64f;
 
 // What a row shares, from its sum of squares and largest |u|.
 struct NormRow {
@@ -580,14 +580,37 @@ __device__ __forceinline__ Frac frac(float x) {
     return f;
 }
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }  // -126 <= k <= 127
+constexpr uint32_t kInf = 0x7f800000u;
 constexpr int kNoProduct = -(1 << 20);
 
-// The rest of a row whose squares or products leave float32's range (elements from about 2^50 on, weights or products
-// at its ends) or that holds an infinity or NaN: fractions and exponents apart, products relative to the largest one's
-// exponent E, squares to the largest element's.  (16384 x 4096 bfloat16, y and codes: 547 us where every row comes here,
-// 89 where none does.)
-template <typename T, bool VEC>
-__device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, long long r, int tid, float (*red)[4]) {
+// The largest and least of a row's threads' numbers (red: as norm_reduce's).
+__device__ __forceinline__ void row_extremes(uint32_t (&most)[2], uint32_t (&least)[2], int G, float (*red)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        most[i] = __reduce_max_sync(0xffffffffu, most[i]);
+        least[i] = __reduce_min_sync(0xffffffffu, least[i]);
+    }
+    if (G > 32) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+            *reinterpret_cast<uint4*>(red[threadIdx.x >> 5]) = make_uint4(most[0], most[1], least[0], least[1]);
+        __syncthreads();
+#pragma unroll 1
+        for (int k = 0; k < G / 32; ++k) {
+            const uint4 o = *reinterpret_cast<const uint4*>(red[k]);
+            most[0] = max(most[0], o.x), most[1] = max(most[1], o.y);
+            least[0] = min(least[0], o.z), least[1] = min(least[1], o.w);
+        }
+    }
+}
+
+// A row whose squares or products leave float32's range (elements from about 2^50 on, weights or products at its ends)
+// or that holds an infinity or NaN.  Squares are of h 2^ea, products relative to 2^E.  Mostly one power of
+// two for all of h and one for all of w bring every product between 2^-100 and 2^62; SPREAD: where none do, fractions
+// and exponents apart, E the largest product's exponent.  hb, wb: bits of the largest |h| and |w| (a NaN's are the largest).
+template <typename T, bool VEC, bool SPREAD>
+__device__ __forceinline__ void norm_wide_row(const NormArgs& a, const Raw<T>* kept, long long r, int tid, float (*red)[4],
+                                              uint32_t hb, uint32_t wb, int ea, int eb) {
     using Part = RowPart<T, VEC>;
     const int G = a.pl.G, vecs = a.pl.vecs, cols = a.cols;
     const T* src = a.h ? static_cast<const T*>(a.h) + r * a.ldh : static_cast<const T*>(a.x) + r * a.ldx;
@@ -596,40 +619,42 @@ __device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, lo
         to8(a.pl.keep ? kept[i] : Part::load(src, cols, i, tid, G), h);
         to8(Part::load(wr, cols, i, tid, G), w);
     };
-    // the largest |h| and |w| (their bits: a NaN's are the largest), and the products' largest exponent
-    uint32_t hb = 0, wb = 0;
-    int E = kNoProduct;
-#pragma unroll 1
-    for (int i = tid; i < vecs; i += G) {
-        float h[8], w[8];
-        row(i, h, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            hb = max(hb, __float_as_uint(h[e]) & 0x7fffffffu);
-            wb = max(wb, __float_as_uint(w[e]) & 0x7fffffffu);
-            if (h[e] != 0.f && w[e] != 0.f) E = max(E, frac(h[e]).e + frac(w[e]).e);
-        }
-    }
-    hb = __reduce_max_sync(0xffffffffu, hb);
-    wb = __reduce_max_sync(0xffffffffu, wb);
-    E = __reduce_max_sync(0xffffffffu, E);
-    if (G > 32) {
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0)
-            *reinterpret_cast<int4*>(red[threadIdx.x >> 5]) = make_int4(static_cast<int>(hb), static_cast<int>(wb), E, 0);
-        __syncthreads();
-#pragma unroll 1
-        for (int k = 0; k < G / 32; ++k) {
-            const int4 o = *reinterpret_cast<const int4*>(red[k]);
-            hb = max(hb, static_cast<uint32_t>(o.x));
-            wb = max(wb, static_cast<uint32_t>(o.y));
-            E = max(E, o.z);
-        }
-    }
-    constexpr uint32_t kInf = 0x7f800000u;
+    constexpr bool EXACT = sizeof(T) == 2;  // squares and products of two 16-bit numbers are float32 numbers
     const bool bad = hb >= kInf || wb >= kInf;
-    // squares of h 2^-eh.  (Not of less than 2^-60: eps is at least 2^-40, and has to stay in range times 2^-2eh.)
-    const int eh = max(hb < kInf ? frac(__uint_as_float(hb)).e : 0, -60);
+    int E = -(ea + eb);
+    if constexpr (SPREAD) {
+        uint32_t most[2] = {0, 0}, least[2] = {0, 0};
+#pragma unroll 1
+        for (int i = tid; i < vecs; i += G) {
+            float h[8], w[8];
+            row(i, h, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (h[e] != 0.f && w[e] != 0.f)
+                    most[0] = max(most[0], static_cast<uint32_t>(frac(h[e]).e + frac(w[e]).e - kNoProduct));
+        }
+        row_extremes(most, least, G, red);
+        E = static_cast<int>(most[0]) + kNoProduct;
+    }
+    const float fa = pow2(max(ea, -126)), fb = pow2(max(eb, -126));  // (without SPREAD ea and eb are at least -98)
+    // h's product with w is (p + l) 2^E; g: h 2^ea
+    auto product = [&](float h, float w, float& g, float& p, float& l) {
+        if constexpr (SPREAD) {
+            const Frac fh = frac(h), fw = frac(w);
+            g = fh.m * pow2(max(fh.e + ea, -126));
+            p = __fmul_rn(fh.m, fw.m);
+            l = EXACT ? 0.f : fmaf(fh.m, fw.m, -p);
+            const int d = fh.e + fw.e - E;
+            const float x = d > -30 ? pow2(min(d, 1)) : 0.f;  // (smaller ones are codes of 0; d > 0: of what is not finite)
+            p *= x;
+            l *= x;
+        } else {
+            g = h * fa;
+            const float v = w * fb;
+            p = __fmul_rn(g, v);
+            l = EXACT ? 0.f : fmaf(g, v, -p);
+        }
+    };
     Two ss = {0.f, 0.f};
     MaxPair m = {0.f, 0.f};
     if (hb < kInf && E != kNoProduct) {  // (else the row's values are 0, or those of an infinity or NaN)
@@ -639,37 +664,35 @@ __device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, lo
             row(i, h, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const Frac fh = frac(h[e]), fw = frac(w[e]);
-                const float g = fh.m * pow2(max(fh.e - eh, -126)), sq = __fmul_rn(g, g), p = __fmul_rn(fh.m, fw.m);
-                float err;
+                float g, p, l, err;
+                product(h[e], w[e], g, p, l);
+                const float sq = __fmul_rn(g, g);
                 ss.hi = two_sum(ss.hi, sq, err);
-                ss.lo += err + fmaf(g, g, -sq);
-                const int d = fh.e + fw.e - E;
-                if (p != 0.f && d > -30) {
-                    const float l = fmaf(fh.m, fw.m, -p), x = pow2(d);
-                    m = max_pair(m, MaxPair{fabsf(p) * x, (p < 0.f ? -l : l) * x});
-                }
+                ss.lo += EXACT ? err : err + fmaf(g, g, -sq);
+                if constexpr (EXACT)
+                    m.hi = max_nan(m.hi, fabsf(p));
+                else
+                    m = max_pair(m, MaxPair{fabsf(p), p < 0.f ? -l : l});
             }
         }
-        norm_reduce<false>(ss, m, G, red, true);
+        norm_reduce<EXACT>(ss, m, G, red, true);
     }
-    const int k0 = E - eh;
-    const float half = pow2(max(-eh, -126));  // (times 2^-120 and less eps counts for nothing)
-    const NormRow o = norm_row(ss, m, cols, a.eps * half * half);
-    // 1 / sqrt, times 2^eh; of a row with an infinity 0, with a NaN NaN
+    const int k0 = E + ea;
+    const NormRow o = norm_row(ss, m, cols, a.eps * fa * fa);  // (where fa is cut off, eps counts for nothing)
+    // 1 / sqrt, times 2^-ea; of a row with an infinity 0, with a NaN NaN
     const float rf = hb > kInf ? __uint_as_float(hb) : hb == kInf ? 0.f : o.r;
     float s = __uint_as_float(0x7fc00000u);
     Two g = {0.f, 0.f};
-    if (E == kNoProduct && !bad) {
+    if (!bad && !(m.hi > 0.f)) {
         s = 0.f;
     } else if (!bad) {
         const int es = frac(o.s).e + k0;
-        if (es >= -125 && es <= 128) {
+        if (o.s >= 0x1p-72f && es >= -125 && es <= 128) {
             s = ldexpf(o.s, k0);
             g = o.g;
         } else {
             // a scale with fewer bits, or 0, or too large for float32 (NaN): rounded once, from float64
-            const double mean = (static_cast<double>(ss.hi) + ss.lo) / cols + ldexp(static_cast<double>(a.eps), -2 * eh);
+            const double mean = (static_cast<double>(ss.hi) + ss.lo) / cols + ldexp(static_cast<double>(a.eps), 2 * ea);
             const double rE = ldexp(1.0 / sqrt(mean), k0), sd = (static_cast<double>(m.hi) + m.lo) * rE / 127.0;
             if (static_cast<float>(sd) <= kFltMax) s = static_cast<float>(sd);
             if (s > 0.f) {
@@ -680,6 +703,8 @@ __device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, lo
         }
     }
     if (a.q.codes && tid == 0) a.q.scales[r] = s;
+    // (without SPREAD the 1 / sqrt is between 2^-62 and 2^10, and times a product at most 2^40)
+    const float rup = rf * 0x1p62f, down = SPREAD ? 0.f : pow2(-eb - 62);
 #pragma unroll 1
     for (int i = tid; i < vecs; i += G) {
         float h[8], w[8], y[8];
@@ -687,26 +712,63 @@ __device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, lo
         uint32_t c[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const Frac fh = frac(h[e]), fw = frac(w[e]);
-            const float p = __fmul_rn(fh.m, fw.m);
-            const int d = fh.e + fw.e - E;
-            c[e] = 0;
-            if (g.hi > 0.f && p != 0.f && d > -30) {
-                const float x = pow2(d);
-                c[e] = norm_code(p * x, fmaf(fh.m, fw.m, -p) * x, g);
+            float hg, p, l;
+            product(h[e], w[e], hg, p, l);
+            c[e] = g.hi > 0.f ? norm_code(p, l, g) : 0;
+            if constexpr (SPREAD) {
+                // (the product of fractions times rf is between 2^-62 and 2^10, or 0 or not finite: the first factor's
+                // product is exact, or is an infinity that the second would have made)
+                const Frac fh = frac(h[e]), fw = frac(w[e]);
+                const int k = fh.e + fw.e + ea, k1 = min(max(k, -62), 127);
+                y[e] = __fmul_rn(fh.m, fw.m) * rf * pow2(k1) * pow2(min(max(k - k1, -126), 127));
+            } else {
+                y[e] = p * rup * down;
             }
-            // (p rf is between 2^-62 and 2^10, or 0 or not finite: the first factor's product is exact, or is an infinity
-            // that the second would have made)
-            const int k = fh.e + fw.e - eh, k1 = min(max(k, -62), 127);
-            y[e] = p * rf * pow2(k1) * pow2(min(max(k - k1, -126), 127));
         }
         if (a.q.codes) Part::store_words(a.q.codes + r * a.q.pitch, (int)a.q.pitch, i, tid, G, pack_codes(c));
         if (a.y) Part::store(static_cast<T*>(a.y) + r * a.ldy, cols, i, tid, G, from8<T>(y));
     }
 }
 
+// norm_wide_row, with what brings the row into range.  (Out of line, for the common path's registers.  16384 x 4096 bfloat16, y and codes: 243 us where
+// every row comes here, 599 where it needs SPREAD, 90 where none does.)
+template <typename T, bool VEC>
+__device__ __noinline__ void norm_wide(const NormArgs& a, const Raw<T>* kept, long long r, int tid, float (*red)[4]) {
+    using Part = RowPart<T, VEC>;
+    const int G = a.pl.G, vecs = a.pl.vecs, cols = a.cols;
+    const T* src = a.h ? static_cast<const T*>(a.h) + r * a.ldh : static_cast<const T*>(a.x) + r * a.ldx;
+    // the largest |h| and |w|, and one less than the least that are not 0 (their bits)
+    uint32_t most[2] = {0, 0}, least[2] = {0xffffffffu, 0xffffffffu};
+#pragma unroll 1
+    for (int i = tid; i < vecs; i += G) {
+        float v[2][8];
+        to8(a.pl.keep ? kept[i] : Part::load(src, cols, i, tid, G), v[0]);
+        to8(Part::load(static_cast<const T*>(a.w), cols, i, tid, G), v[1]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const uint32_t b = __float_as_uint(v[e / 8][e % 8]) & 0x7fffffffu;
+            most[e / 8] = max(most[e / 8], b);
+            least[e / 8] = min(least[e / 8], b - 1);
+        }
+    }
+    row_extremes(most, least, G, red);
+    if (most[0] < kInf && most[1] < kInf) {
+        // the largest to 2^31 at most, times 2^60 at most (eps, which is at least 2^-40, has to stay in range times 2^2ea)
+        const int ea = min(31 - frac(__uint_as_float(most[0])).e, 60), eb = min(31 - frac(__uint_as_float(most[1])).e, 60);
+        const int el = ea + (most[0] ? frac(__uint_as_float(least[0] + 1)).e : 0);
+        const int fl = eb + (most[1] ? frac(__uint_as_float(least[1] + 1)).e : 0);
+        // (a fraction is at least 1/2: products from 2^-100 on, no factor below 2^-121)
+        if (el >= -120 && fl >= -120 && el + fl >= -98) {
+            norm_wide_row<T, VEC, false>(a, kept, r, tid, red, most[0], most[1], ea, eb);
+            return;
+        }
+    }
+    const int eh = most[0] < kInf ? frac(__uint_as_float(most[0])).e : 0;
+    norm_wide_row<T, VEC, true>(a, kept, r, tid, red, most[0], most[1], min(-eh, 60), 0);
+}
+
 template <typename T, int U, bool VEC>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __maxnreg__(VEC || U == 1 ? 64 : 80)  // (norm_wide's needs may not cost the common path occupancy)
 i8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
     extern __shared__ __align__(16) uint8_t row_smem[];
     __shared__ __align__(16) float red[kRowThreads / 32][4];
@@ -795,7 +857,9 @@ i8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
         o.s = o.g.hi = 0.f;
     }
     if (a.q.codes && tid == 0) a.q.scales[r] = o.s;
-    const F2 g2 = f2(o.g.hi, o.g.hi);
+    // Products are taken times 2^24: 1 / sqrt is at most 2^20, so a value y that is a normal number comes from a product
+    // that is one too.
+    const F2 up = f2(0x1p24f, 0x1p24f), g2 = f2(o.g.hi * 0x1p-24f, o.g.hi * 0x1p-24f), r2 = f2(o.r * 0x1p-24f, o.r * 0x1p-24f);
 #pragma unroll 1
     for (int i = tid; i < vecs; i += G) {
         const Raw<T> hraw = again(i), wraw = Part::load(wr, cols, i, tid, G);
@@ -804,7 +868,7 @@ i8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
         to8(wraw, w);
         F2 u[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = mul2(f2(h[2 * e], h[2 * e + 1]), f2(w[2 * e], w[2 * e + 1]));
+        for (int e = 0; e < 4; ++e) u[e] = mul2(mul2(f2(h[2 * e], h[2 * e + 1]), up), f2(w[2 * e], w[2 * e + 1]));
         if (a.q.codes) {
             uint32_t code[8];
             float far = 0.f;
@@ -822,7 +886,7 @@ i8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 p = unpack(mul2(u[e], f2(o.r, o.r)));
+                const float2 p = unpack(mul2(u[e], r2));
                 y[2 * e] = p.x, y[2 * e + 1] = p.y;
             }
             Part::store(static_cast<T*>(a.y) + r * a.ldy, cols, i, tid, G, from8<T>(y));

@@ -462,8 +462,7 @@ int lora_i8_dequantize(const lora_i8_matrix* q, void* out_dev, int dtype, int64_
  *     v = h / sqrt(mean(h^2) + eps) * weight
  * residual_out receives h, out the stored form of v itself (not of y), y receives v from float32 arithmetic, rounded
  * to dtype: h * weight, 1 / sqrt and their product are each rounded to float32 before, so beside half a step of dtype
- * y is within 3 * 2^-24 of v (of an element whose h * weight is below float32's normal range, within 2^-149 / sqrt(mean
- * + eps)).
+ * y is within 3 * 2^-24 of v.
  * The row's statistics are held to about 2^-44, so out's codes are those of the real v, also where h * weight leaves
  * float32's range and v does not.  A row that holds an infinity or a NaN gets a NaN scale and codes 0.
  *   x, residual (nullable), residual_out (nullable without residual), y (nullable): [rows, cols] of dtype with row

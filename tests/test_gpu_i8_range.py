@@ -71,6 +71,26 @@ def test_norm_of_rows_that_span_the_range(lib, dtype, cols, shift):
 
 
 @pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("cols,shift", [(200, 1), (2048, 0)])
+@pytest.mark.parametrize("span", [3, 20, 45, 64, 90])
+@pytest.mark.parametrize("hexp,wexp", [(60, 0), (0, 110), (-40, -60), (-100, 30), (30, -120)])
+def test_norm_of_rows_of_every_span(lib, dtype, cols, shift, span, hexp, wexp):
+    """Elements and weights spread over more and more powers of two, each by itself: from rows that one factor brings into
+    range to rows that none does."""
+    rng = np.random.default_rng([cols, span])
+
+    def draw(rows, middle):
+        e = np.clip(middle + rng.integers(-span, span + 1, (rows, cols)), -140, 118).astype(np.float64)
+        return (1 + rng.random((rows, cols))) * np.exp2(e) * rng.choice([-1.0, 1.0], (rows, cols))
+
+    x, w = draw(5, hexp), draw(1, wexp)[0]
+    x[1, ::3] = 0
+    x[2, 1:] = 0
+    w[5] = 0
+    check_norm(lib, torch.from_numpy(x).to(dtype), torch.from_numpy(w).to(dtype), 1e-5, shift)
+
+
+@pytest.mark.parametrize("dtype", WIDE)
 def test_norm_of_rows_that_are_not_finite_among_large_weights(lib, dtype):
     """An infinity in the weight or the row, beside products that overflow: NaN scale, codes 0, and the others' values."""
     x = torch.from_numpy(spread(5, 264, 5)).to(dtype)
